@@ -77,6 +77,7 @@ typedef enum {
 #define QRE_DEV_BAD_SCALE     0x4   /* quantize: a group scale was not finite        */
 #define QRE_DEV_BAD_INDEX     0x8   /* an expert id outside [0, n_experts)           */
 #define QRE_DEV_FP16_RANGE    0x10  /* prefill: an activation or h exceeded fp16     */
+#define QRE_DEV_NO_PAGE       0x20  /* key-value cache: no free page, or a full row  */
 
 /* Layer shape.  H = hidden, I = expert intermediate, E = routed experts,
  * k = experts per token, G = quantization group along the reduction axis. */
@@ -433,6 +434,162 @@ QRE_API qre_status qre_set_host_unit_cost(int32_t cost);
  * use; a CUDA graph keeps the values in force when it was captured.
  */
 QRE_API qre_status qre_debug_wait_test(uint64_t wait_limit_ns, uint64_t stall_ns);
+
+/* ------------------------------------------------------------------------
+ * Attention between the MoE layers: a paged key-value cache, and the attention
+ * that fills and reads it.  The pages this library follows describe only the
+ * MoE layer; everything below is the library's own.
+ *
+ * The conventions at the top hold (device pointers, caller-owned memory, stream
+ * order, host-side argument errors, device conditions in the status word).
+ * Limits: head_dim in {64, 128}; page_size a power of two from 16 to 256;
+ * n_heads a multiple of n_kv_heads, at most 1024; n_kv_heads <= 256; at most
+ * 4096 sequences, requests or forks per call; n_pages and total tokens below
+ * 2^24; strides are in elements, non-negative multiples of 8.
+ */
+typedef enum { QRE_BF16 = 0, QRE_FP16 = 1, QRE_E4M3 = 2 } qre_dtype;
+
+/*
+ * A paged key-value cache.  Position p of sequence s is row p % page_size of
+ * page page_table[s][p / page_size], in every layer.  One page of one head is
+ * contiguous.  ref_count[p] says how many rows of the table hold page p; 0 is a
+ * free page.  A QRE_E4M3 cache stores E4M3 bytes, worth byte * scale of the
+ * layer and KV head.  seq_len[s] counts the reserved positions, so sequence s
+ * holds ceil(seq_len[s] / page_size) pages; table entries beyond are -1.
+ */
+typedef struct {
+  void* k;              /* [n_layers][n_pages][n_kv_heads][page_size][head_dim], device */
+  void* v;              /* the same shape, device                                       */
+  int32_t* page_table;  /* [max_seqs][max_pages], device                                */
+  int32_t* seq_len;     /* [max_seqs], device                                           */
+  int32_t* ref_count;   /* [n_pages], device                                            */
+  const float* k_scale; /* [n_layers][n_kv_heads], device; QRE_E4M3 only, NULL = 1;
+                           read one by one: 4-byte alignment is enough                  */
+  const float* v_scale; /* the same                                                     */
+  int32_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
+  int32_t max_seqs, max_pages;
+  int32_t dtype;        /* qre_dtype of k and v                                         */
+} qre_kv_cache;
+
+/* New key and value rows [token][head][head_dim]: type (QRE_BF16 or QRE_FP16) and strides. */
+typedef struct {
+  int64_t k_token, k_head, v_token, v_head;
+  int32_t dtype;
+  int32_t reserved;     /* must be 0 */
+} qre_kv_rows;
+
+/*
+ * One attention: heads, type of q, k, v and o (QRE_BF16 or QRE_FP16), the scale
+ * of the scores (finite, > 0), and the strides of [token][head][head_dim]
+ * arrays (k_* and v_* are read by qre_attn_prefill only).  Query i of a
+ * sequence with q_len queries and k_len keys stands at position
+ * p = k_len - q_len + i.  It sees key j iff j < k_len, and with causal != 0
+ * j <= p, and with window > 0 (causal only) j > p - window.  A query that sees
+ * nothing gives o = 0 and lse = -infinity; keys and values that a query does
+ * not see do not reach its result, whatever they hold (NaN and infinities
+ * included).
+ */
+typedef struct {
+  int32_t n_heads, n_kv_heads, head_dim, dtype;
+  float scale;
+  int32_t causal;
+  int32_t window;       /* 0 = none */
+  int32_t reserved;     /* must be 0 */
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+} qre_attn;
+
+/* Bytes of workspace that qre_kv_reserve, qre_kv_fork and qre_kv_compact need
+ * on this cache (bytes: host).  Its content need not be initialised. */
+QRE_API qre_status qre_kv_workspace_size(const qre_kv_cache* cache, size_t* bytes);
+
+/*
+ * Reserves n_new[i] positions behind sequence seqs[i]: pages from the free ones,
+ * lowest numbers first, in the order of the list; seq_len grows.  Requests are
+ * served in order until one finds too few free pages; that one, and later ones
+ * that need a page, stay as they were and QRE_DEV_NO_PAGE is set, as for a
+ * request beyond max_pages.  An id outside [0, max_seqs) or a negative n_new is
+ * dropped with QRE_DEV_BAD_INDEX.  The ids of one call are distinct.
+ *   seqs, n_new  [n] int32, device
+ */
+QRE_API qre_status qre_kv_reserve(const qre_kv_cache* cache, int32_t n, const int32_t* seqs, const int32_t* n_new,
+                                  void* workspace, size_t workspace_bytes, qre_stream_t stream);
+
+/*
+ * Writes n_tokens new rows of one layer: row t goes to position token_pos[t] of
+ * sequence token_seq[t], as it is (cache and rows of one type) or, into a
+ * QRE_E4M3 cache, as E4M3(row / scale), to nearest even, clamped to +-448.
+ * A token with token_pos < 0 is skipped (padding); one without a page there, or
+ * with a bad id, is skipped with QRE_DEV_BAD_INDEX.
+ *   token_seq, token_pos  [n_tokens] int32, device
+ *   k, v                  [n_tokens][n_kv_heads][head_dim], device
+ */
+QRE_API qre_status qre_kv_write(const qre_kv_cache* cache, int32_t layer, const qre_kv_rows* rows, int32_t n_tokens,
+                                const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
+                                qre_stream_t stream);
+
+/*
+ * Forks sequence src[i] into the empty sequence dst[i], i = 0 .. n-1: whole
+ * pages are shared (ref_count + 1); a last page that is not full is copied, all
+ * layers, into the lowest free page (in the order of the list).  All requests
+ * see the state before the call; dst ids are distinct and none is a src.  A bad
+ * id, or a dst that holds positions, drops the request with QRE_DEV_BAD_INDEX;
+ * a request that finds no free page is dropped with QRE_DEV_NO_PAGE.
+ */
+QRE_API qre_status qre_kv_fork(const qre_kv_cache* cache, int32_t n, const int32_t* src, const int32_t* dst,
+                               void* workspace, size_t workspace_bytes, qre_stream_t stream);
+
+/*
+ * Frees sequences: every page of seqs[i] loses one reference (pages at 0 are
+ * free), its table row becomes -1 and its length 0.  Freeing an empty sequence
+ * changes nothing; bad ids are dropped with QRE_DEV_BAD_INDEX.
+ */
+QRE_API qre_status qre_kv_free(const qre_kv_cache* cache, int32_t n, const int32_t* seqs, qre_stream_t stream);
+
+/*
+ * Compacts the pool: with L pages live, every live page numbered L or above
+ * moves (all layers) to the free place of the same rank below L, both in
+ * ascending order, so that the live pages become 0 .. L-1.
+ *   page_table_out  [max_seqs][max_pages] int32, device (written): the table with
+ *                   the new numbers; may be the cache's own
+ *   ref_count_out   [n_pages] int32, device (written); may be the cache's own
+ *   n_live          [1] int32, device (written): L
+ */
+QRE_API qre_status qre_kv_compact(const qre_kv_cache* cache, int32_t* page_table_out, int32_t* ref_count_out,
+                                  int32_t* n_live, void* workspace, size_t workspace_bytes, qre_stream_t stream);
+
+/*
+ * Attention over packed prompts: sequence s has the queries cu_q[s] ..
+ * cu_q[s+1]-1 and the keys cu_k[s] .. cu_k[s+1]-1 (prefix sums from 0; more
+ * keys than queries when a prefix stands before them).
+ *   cu_q, cu_k  [n_seqs + 1] int32, device; a sequence whose bounds are not
+ *               ascending inside [0, total] is skipped with QRE_DEV_BAD_INDEX
+ *   q [total_q][n_heads][head_dim], k, v [total_k][n_kv_heads][head_dim], device
+ *   o [total_q][n_heads][head_dim], device (written)
+ *   lse [total_q][n_heads] fp32 or NULL, device (written): natural log of the
+ *               sum of exp(score) over the keys seen
+ */
+QRE_API qre_status qre_attn_prefill(const qre_attn* attn, int32_t n_seqs, int32_t total_q, int32_t total_k,
+                                    const int32_t* cu_q, const int32_t* cu_k, const void* q, const void* k,
+                                    const void* v, void* o, float* lse, qre_stream_t stream);
+
+/* Bytes of workspace qre_attn_decode needs for n sequences (bytes: host). */
+QRE_API qre_status qre_attn_decode_workspace_size(const qre_attn* attn, const qre_kv_cache* cache, int32_t n,
+                                                  size_t* bytes);
+
+/*
+ * Attention of one new token per sequence over the cache: query i belongs to
+ * sequence seqs[i] (NULL: i) and sees its seq_len positions (the new token's own
+ * row, written before, included), or the last `window` of them.
+ *   max_len  host: an upper bound of the lengths, 0 if not known; it chooses how
+ *            the work is split and nothing else
+ *   q, o     [n][n_heads][head_dim], device; lse [n][n_heads] fp32 or NULL
+ * A bad id gives the empty result and QRE_DEV_BAD_INDEX; a position whose page
+ * is missing counts as not seen, with QRE_DEV_BAD_INDEX.  cache and attn have
+ * one type, or the cache is QRE_E4M3.
+ */
+QRE_API qre_status qre_attn_decode(const qre_attn* attn, const qre_kv_cache* cache, int32_t layer, int32_t n,
+                                   const int32_t* seqs, int32_t max_len, const void* q, void* o, float* lse,
+                                   void* workspace, size_t workspace_bytes, qre_stream_t stream);
 
 /*
  * Synchronizes the stream, then writes the current device's status word

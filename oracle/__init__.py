@@ -18,9 +18,14 @@ Modules
     permutation, active list), the SwiGLU expert FFN on dequantized weights, the
     shared expert, and the routing-weighted combine.
 
-Every function cites the passage it follows.  All parts are pinned by tests
+``oracle.attention``
+    Attention over packed prompts and a paged key-value cache, the cache's page
+    bookkeeping and E4M3 rounding (the library's own: the pages describe only the
+    MoE layer), with the error bounds the GPU tests use.
+
+Every function of the MoE layer cites the passage it follows.  All parts are pinned by tests
 against closed forms, hand-derived fixtures, invariants and brute force; none
 says "parity unpinned".
 """
 
-from . import quant, moe  # noqa: F401
+from . import attention, moe, quant  # noqa: F401

@@ -33,6 +33,12 @@ QRE_DEV_NULL_SLOT = 0x2
 QRE_DEV_BAD_SCALE = 0x4
 QRE_DEV_BAD_INDEX = 0x8
 QRE_DEV_FP16_RANGE = 0x10
+QRE_DEV_NO_PAGE = 0x20
+
+# qre_dtype
+QRE_BF16 = 0
+QRE_FP16 = 1
+QRE_E4M3 = 2
 
 # Every symbol include/qre.h declares.
 EXPORTS = (
@@ -43,6 +49,8 @@ EXPORTS = (
     "qre_read_device_status", "qre_clear_device_status", "qre_route_noalloc", "qre_debug_wait_test",
     "qre_expert_ffn_routed", "qre_expert_ffn_shared", "qre_shared_workspace_size", "qre_stage_experts",
     "qre_read_probe", "qre_set_host_unit_cost", "qre_route_dispatch",
+    "qre_kv_workspace_size", "qre_kv_reserve", "qre_kv_write", "qre_kv_fork", "qre_kv_free", "qre_kv_compact",
+    "qre_attn_prefill", "qre_attn_decode_workspace_size", "qre_attn_decode",
 )
 
 
@@ -54,6 +62,25 @@ class qre_layer_shape(ctypes.Structure):
 class qre_slot(ctypes.Structure):
     _fields_ = [("w_gate_up", ctypes.c_void_p), ("s_gate_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("s_down", ctypes.c_void_p), ("tier", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class qre_kv_cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "page_table", "seq_len", "ref_count", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "n_kv_heads", "page_size", "head_dim",
+                                                 "max_seqs", "max_pages", "dtype")])
+
+
+class qre_kv_rows(ctypes.Structure):
+    _fields_ = [("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64), ("v_token", ctypes.c_int64),
+                ("v_head", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class qre_attn(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "dtype")]
+                + [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                   ("reserved", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+                                                 "o_token", "o_head")])
 
 
 class QreError(RuntimeError):
@@ -69,6 +96,7 @@ _lib = None
 
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _SHAPE = ctypes.POINTER(qre_layer_shape)
+_KV, _ATTN, _ROWS = ctypes.POINTER(qre_kv_cache), ctypes.POINTER(qre_attn), ctypes.POINTER(qre_kv_rows)
 _SIGS = {
     "qre_last_error": ([], ctypes.c_char_p),
     "qre_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -97,6 +125,15 @@ _SIGS = {
     "qre_set_host_unit_cost": ([_I32], ctypes.c_int),
     "qre_route_dispatch": ([_SHAPE, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
                            ctypes.c_int),
+    "qre_kv_workspace_size": ([_KV, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "qre_kv_reserve": ([_KV, _I32, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "qre_kv_write": ([_KV, _I32, _ROWS, _I32, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "qre_kv_fork": ([_KV, _I32, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "qre_kv_free": ([_KV, _I32, _VP, _VP], ctypes.c_int),
+    "qre_kv_compact": ([_KV, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "qre_attn_prefill": ([_ATTN, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "qre_attn_decode_workspace_size": ([_ATTN, _KV, _I32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "qre_attn_decode": ([_ATTN, _KV, _I32, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
 }
 
 
@@ -291,6 +328,89 @@ def qre_set_host_unit_cost(cost: int) -> None:
     """Process-wide: cut the decode kernels' work at equal cost with a host-mapped
     unit counted as ``cost`` (0 or 1: equal counts, the default)."""
     _check(load_library().qre_set_host_unit_cost(cost), "qre_set_host_unit_cost")
+
+
+def make_kv_cache(k, v, page_table, seq_len, ref_count, dtype, k_scale=None, v_scale=None) -> qre_kv_cache:
+    """Descriptor of a paged cache from its tensors: k, v [n_layers, n_pages, n_kv_heads, page_size, head_dim]
+    (contiguous), page_table [max_seqs, max_pages], seq_len [max_seqs], ref_count [n_pages] int32.  It holds
+    addresses only: keep the tensors alive."""
+    L, P, H, S, D = k.shape
+    assert v.shape == k.shape and k.is_contiguous() and v.is_contiguous() and page_table.is_contiguous()
+    assert seq_len.numel() == page_table.shape[0] and ref_count.numel() == P
+    return qre_kv_cache(_ptr(k), _ptr(v), _ptr(page_table), _ptr(seq_len), _ptr(ref_count), _ptr(k_scale),
+                        _ptr(v_scale), L, P, H, S, D, page_table.shape[0], page_table.shape[1], dtype)
+
+
+def _strides(t):
+    if t is None:
+        return 0, 0
+    assert t.dim() == 3 and (t.shape[2] == 0 or t.stride(2) == 1), "[tokens, heads, head_dim] with contiguous rows"
+    return t.stride(0), t.stride(1)
+
+
+def make_kv_rows(dtype, k, v) -> qre_kv_rows:
+    """Type and strides of new rows k, v [tokens, n_kv_heads, head_dim]."""
+    return qre_kv_rows(*_strides(k), *_strides(v), dtype, 0)
+
+
+def make_attn(n_heads, n_kv_heads, head_dim, dtype, scale, causal=True, window=0, q=None, k=None, v=None,
+              o=None) -> qre_attn:
+    """Descriptor of an attention; the strides are taken from q, k, v, o [tokens, heads, head_dim] (k and v may be
+    left out for qre_attn_decode)."""
+    return qre_attn(n_heads, n_kv_heads, head_dim, dtype, scale, 1 if causal else 0, window, 0, *_strides(q),
+                    *_strides(k), *_strides(v), *_strides(o))
+
+
+def qre_kv_workspace_size(cache: qre_kv_cache) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().qre_kv_workspace_size(ctypes.byref(cache), ctypes.byref(out)), "qre_kv_workspace_size")
+    return out.value
+
+
+def qre_kv_reserve(cache, n, seqs, n_new, workspace, workspace_bytes=None, stream=None) -> None:
+    _check(load_library().qre_kv_reserve(ctypes.byref(cache), n, _ptr(seqs), _ptr(n_new), _ptr(workspace),
+                                         _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_kv_reserve")
+
+
+def qre_kv_write(cache, layer, rows, n_tokens, token_seq, token_pos, k, v, stream=None) -> None:
+    _check(load_library().qre_kv_write(ctypes.byref(cache), layer, ctypes.byref(rows), n_tokens, _ptr(token_seq),
+                                       _ptr(token_pos), _ptr(k), _ptr(v), _stream(stream)), "qre_kv_write")
+
+
+def qre_kv_fork(cache, n, src, dst, workspace, workspace_bytes=None, stream=None) -> None:
+    _check(load_library().qre_kv_fork(ctypes.byref(cache), n, _ptr(src), _ptr(dst), _ptr(workspace),
+                                      _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_kv_fork")
+
+
+def qre_kv_free(cache, n, seqs, stream=None) -> None:
+    _check(load_library().qre_kv_free(ctypes.byref(cache), n, _ptr(seqs), _stream(stream)), "qre_kv_free")
+
+
+def qre_kv_compact(cache, page_table_out, ref_count_out, n_live, workspace, workspace_bytes=None,
+                   stream=None) -> None:
+    _check(load_library().qre_kv_compact(ctypes.byref(cache), _ptr(page_table_out), _ptr(ref_count_out),
+                                         _ptr(n_live), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                         _stream(stream)), "qre_kv_compact")
+
+
+def qre_attn_prefill(attn, n_seqs, total_q, total_k, cu_q, cu_k, q, k, v, o, lse=None, stream=None) -> None:
+    _check(load_library().qre_attn_prefill(ctypes.byref(attn), n_seqs, total_q, total_k, _ptr(cu_q), _ptr(cu_k),
+                                           _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _stream(stream)),
+           "qre_attn_prefill")
+
+
+def qre_attn_decode_workspace_size(attn: qre_attn, cache: qre_kv_cache, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().qre_attn_decode_workspace_size(ctypes.byref(attn), ctypes.byref(cache), n,
+                                                         ctypes.byref(out)), "qre_attn_decode_workspace_size")
+    return out.value
+
+
+def qre_attn_decode(attn, cache, layer, n, seqs, max_len, q, o, lse, workspace, workspace_bytes=None,
+                    stream=None) -> None:
+    _check(load_library().qre_attn_decode(ctypes.byref(attn), ctypes.byref(cache), layer, n, _ptr(seqs), max_len,
+                                          _ptr(q), _ptr(o), _ptr(lse), _ptr(workspace),
+                                          _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_attn_decode")
 
 
 def qre_read_device_status(stream=None) -> int:

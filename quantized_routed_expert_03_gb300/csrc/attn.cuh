@@ -1,0 +1,35 @@
+// attn.cuh -- what the prefill and the decode attention share.
+#pragma once
+
+#include "common.cuh"
+
+namespace qre {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int DT>
+__device__ __forceinline__ float bits_to_float(uint32_t b) {
+  return DT == QRE_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half((unsigned short)b));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (DT == QRE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Keys [lo, hi) that the query at position p of a sequence with k_len keys sees.
+__device__ __forceinline__ void visible_range(int p, int k_len, int causal, int window, int& lo, int& hi) {
+  lo = 0;
+  hi = k_len;
+  if (causal && p + 1 < hi) hi = p + 1;
+  if (window > 0 && p + 1 - window > 0) lo = p + 1 - window;
+  if (hi < lo) hi = lo;
+}
+
+}  // namespace qre

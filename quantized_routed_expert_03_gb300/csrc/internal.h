@@ -127,6 +127,28 @@ cudaError_t launch_combine(const qre_layer_shape& s, int T, const float* expert_
 // (e.g. a base that is not 16-byte aligned).
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
 
+// Key-value cache (kv_cache.cu) and attention (attn_prefill.cu, attn_decode.cu).
+// The arguments have been checked (api_attn.cu).
+constexpr int kKvMaxRequests = 4096;   // sequences, requests or forks of one call
+size_t kv_ws_bytes(const qre_kv_cache& c);
+cudaError_t launch_kv_reserve(const qre_kv_cache& c, int n, const int32_t* seqs, const int32_t* n_new, void* ws,
+                              int* status, cudaStream_t stream);
+cudaError_t launch_kv_write(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n_tokens,
+                            const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
+                            int* status, cudaStream_t stream);
+cudaError_t launch_kv_fork(const qre_kv_cache& c, int n, const int32_t* src, const int32_t* dst, void* ws, int* status,
+                           cudaStream_t stream);
+cudaError_t launch_kv_free(const qre_kv_cache& c, int n, const int32_t* seqs, int* status, cudaStream_t stream);
+cudaError_t launch_kv_compact(const qre_kv_cache& c, int32_t* table_out, int32_t* ref_out, int32_t* n_live, void* ws,
+                              int* status, cudaStream_t stream);
+cudaError_t launch_attn_prefill(const qre_attn& a, int n_seqs, int total_q, int total_k, const int32_t* cu_q,
+                                const int32_t* cu_k, const void* q, const void* k, const void* v, void* o, float* lse,
+                                int* status, cudaStream_t stream);
+size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n);
+cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
+                               int max_len, const void* q, void* o, float* lse, void* ws, int* status,
+                               cudaStream_t stream);
+
 // Router logits on the tensor cores (long token batches): whether a call of T
 // tokens takes them, the workspace they need beyond the logits (the router
 // weights split into three bf16 parts), and the launch (split, then GEMM).
