@@ -23,6 +23,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 2^x by the hardware's approximation (relative error about 2^-22); 2^-inf = 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Keys [lo, hi) that the query at position p of a sequence with k_len keys sees.
 __device__ __forceinline__ void visible_range(int p, int k_len, int causal, int window, int& lo, int& hi) {
   lo = 0;

@@ -1,8 +1,36 @@
 // attn_decode.cu -- attention of one new token per sequence over the paged cache.
 //
-// One pass over the sequence's positions with a running maximum and sum (base
-// 2, fp32), as in attn_prefill.cu.
+// o = sum_j softmax_j(scale q . k_j) v_j over the positions j that the token
+// sees, for every head, in one pass over K and V: with the running maximum m and
+// sum l (fp32, base 2),
+//   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), o' alike,
+// and the same formula joins parts of a sequence.
+//
+// Bound: every K and V row is read once, 4 g flops per element (g query heads
+// share a KV head), so the memory bounds it, and what counts is how many bytes
+// are in flight.
+//
+// Work split.  A chunk is CK positions of one KV head (K and V, 8 KB together);
+// the chunks of all (sequence, KV head) units in a row are cut into equal
+// contiguous ranges, one per CTA, whatever the lengths are; a CTA's eight warps
+// take the chunks of its range in turn.  The lengths stay on the device: every
+// CTA sums them up for itself.  A unit that lies inside one range is finished
+// there; one that is cut leaves a part (o, m, l in fp32) per CTA in the
+// workspace, and a second, dependent launch joins the parts in the order of the
+// CTAs, so results do not depend on timing.
+//
+// A warp runs on its own between the ends of units: it fills a ring of chunks in
+// shared memory with cp.async (16-byte pieces, rows that are not seen zero-filled,
+// so what they hold never reaches a product) and multiplies with mma.sync
+// (m16n8k16): S = Q K^T with the group's heads as the 16 rows, then O += P V.
+// The 16 rows are mostly padding, but the tensor work of a chunk is far below its
+// load time, and tcgen05 would want 128 rows.  More than 16 heads per KV head run
+// as several units over the same keys, which then come from L2.
+// An E4M3 cache is multiplied as fp16, which holds every E4M3 value; a bf16 query
+// is brought into fp16's range by a power of two per head.
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "attn.cuh"
 #include "internal.h"
@@ -10,106 +38,645 @@
 namespace qre {
 namespace {
 
-// Element e of a row of the cache.
-template <int CT>
-__device__ __forceinline__ float cache_value(const void* base, size_t e) {
-  if (CT == QRE_E4M3) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(base)[e], __NV_E4M3);
-    return __half2float(__half(h));
-  }
-  return bits_to_float<CT>(static_cast<const uint16_t*>(base)[e]);
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk
+constexpr int kRows = 16;             // query heads of a unit at most
+constexpr int kMaxParts = 1024;       // CTAs of the main kernel at most
+
+// What CTA b of the main kernel leaves for the join, in the workspace.
+struct CutInfo {
+  long long u0, u1;   // chunks of the unit that range b begins in; u0 < begin of range b iff the unit is cut there
+  long long total;    // chunks of the call
+  int t, block;       // query and head block of the unit
+  int ctas, valid;
+};
+
+__device__ __forceinline__ long long range_begin(int c, int ctas, long long total) { return total * c / ctas; }
+
+__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
+  const int bytes = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two E4M3 bytes (low half of b) as an fp16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t b) {
+  uint32_t r;
+  asm("{.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(b));
+  return r;
 }
 
-// One warp per (sequence, head); a lane scores one key at a time, then the lanes
-// share the head's dimensions for the values.
-template <int DT, int CT, int D>
-__global__ void __launch_bounds__(256) attn_decode_kernel(const __grid_constant__ qre_attn a,
-                                                          const __grid_constant__ qre_kv_cache c, int layer, int n,
-                                                          const int32_t* __restrict__ seqs,
-                                                          const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
-                                                          float* __restrict__ lse, int* status) {
-  __shared__ float qs[8][D];
+// DT: type of q and o; CT: type of the cache; HI: more than 8 query heads in a unit.
+template <int DT, int CT, int D, bool HI>
+struct Decode {
+  static constexpr bool F8 = CT == QRE_E4M3;
+  static constexpr bool BF = CT == QRE_BF16;      // type of the products
+  static constexpr int RB = D * (F8 ? 1 : 2);     // bytes of a row
+  static constexpr int CK = kTile / RB;           // positions of a chunk
+  static constexpr int PR = RB / 16;              // 16-byte pieces of a row
+  static constexpr int RI = 32 / PR;              // rows that the warp's 32 lanes fetch at once
+  static constexpr int NP = CK / 16;              // runs of 16 positions (each inside one page)
+  static constexpr int NT = CK / 8;
+  static constexpr int KS = D / 16;
+
+  // Byte offset of piece `col` of row `row` in a tile: pieces of a 128-byte line
+  // are permuted by the row, so the eight rows that ldmatrix reads at one column
+  // lie in different banks.
+  static __device__ __forceinline__ uint32_t at(int row, int col) {
+    return (uint32_t)(row * RB + 16 * (PR >= 8 ? col ^ (row & 7) : col ^ ((row >> 1) & 3)));
+  }
+};
+
+struct Seq {
+  int row, len, first;   // table row, length, chunks of the queries before
+};
+
+template <int DT, int CT, int D, bool HI>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
+                       const int32_t* __restrict__ seqs, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
+                       float* __restrict__ lse, CutInfo* __restrict__ cuts, float* __restrict__ parts, int stages,
+                       int buf_rows, int* status) {
+  using K = Decode<DT, CT, D, HI>;
+  constexpr int CK = K::CK, NT = K::NT, KS = K::KS;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* ring = smem + (size_t)(threadIdx.x >> 5) * stages * 2 * kTile;   // this warp's
+  float* buf = reinterpret_cast<float*>(smem + (size_t)kWarps * stages * 2 * kTile);   // [kWarps][buf_rows][D]
+  float2* ml = reinterpret_cast<float2*>(buf + kWarps * buf_rows * D);                 // [kWarps][kRows]
+  Seq* sq = reinterpret_cast<Seq*>(ml + kWarps * kRows);                               // [n + 1]
+  __shared__ int scan_part[kWarps];
+  __shared__ int scan_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.n_heads / a.n_kv_heads;
+  const int blocks = (g + kRows - 1) / kRows;       // head blocks of a KV head
+  const int units = a.n_kv_heads * blocks;          // units of a sequence
+  const int ps_shift = 31 - __clz(c.page_size);
+
   grid_dependency_wait();
   grid_dependents_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 8 + warp;
-  if (unit >= (long long)n * a.n_heads) return;
-  const int t = (int)(unit / a.n_heads), h = (int)(unit % a.n_heads), hk = h / (a.n_heads / a.n_kv_heads);
-  const int s = seqs ? seqs[t] : t;
-  int len = 0;
-  if (s >= 0 && s < c.max_seqs) len = c.seq_len[s];
-  else if (lane == 0) set_status(status, QRE_DEV_BAD_INDEX);
-  if (len < 0 || len > (long long)c.max_pages * c.page_size) {
-    len = 0;
-    if (lane == 0) set_status(status, QRE_DEV_BAD_INDEX);
-  }
-  int lo, hi;
-  visible_range(len - 1, len, 1, a.window, lo, hi);
-  const size_t si = (size_t)layer * c.n_kv_heads + hk;
-  const float ks = CT == QRE_E4M3 && c.k_scale ? c.k_scale[si] : 1.0f;
-  const float vs = CT == QRE_E4M3 && c.v_scale ? c.v_scale[si] : 1.0f;
-  for (int d = lane; d < D; d += 32)
-    qs[warp][d] = bits_to_float<DT>(q[(size_t)t * a.q_token + (size_t)h * a.q_head + d]) * a.scale * kLog2e * ks;
-  __syncwarp();
-  float m = -INFINITY, l = 0.0f, acc[D / 32] = {};
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
-    float x = -INFINITY;
-    int page = -1;
-    if (j < hi) page = c.page_table[(size_t)s * c.max_pages + j / c.page_size];
-    const bool ok = page >= 0 && page < c.n_pages;
-    if (j < hi && !ok) set_status(status, QRE_DEV_BAD_INDEX);
-    const size_t row =
-        ok ? ((((size_t)layer * c.n_pages + page) * c.n_kv_heads + hk) * c.page_size + j % c.page_size) * D : 0;
-    if (ok) {
-      x = 0.0f;
-      for (int d = 0; d < D; ++d) x += qs[warp][d] * cache_value<CT>(c.k, row + d);
+
+  // ---- the plan: chunks of every query, summed up
+  int before = 0;
+  for (int t0 = 0; t0 < n; t0 += kThreads) {
+    const int t = t0 + tid;
+    int row = 0, len = 0, ch = 0;
+    if (t < n) {
+      row = seqs ? seqs[t] : t;
+      bool bad = row < 0 || row >= c.max_seqs;
+      if (!bad) {
+        len = c.seq_len[row];
+        bad = len < 0 || len > (long long)c.max_pages * c.page_size;
+      }
+      if (bad) {
+        if (blockIdx.x == 0) set_status(status, QRE_DEV_BAD_INDEX);
+        len = row = 0;
+      }
+      const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
+      ch = len > 0 ? (len + CK - 1) / CK - lo / CK : 0;
     }
-    float mx = x;
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    const float m2 = fmaxf(m, mx), f = m == -INFINITY ? 0.0f : exp2f(m - m2);
-    const float p = ok ? exp2f(x - m2) : 0.0f;
-    float sum = p;
-    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    l = l * f + sum;
-    m = m2;
+    int inc = ch;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] *= f;
-    for (int i = 0; i < 32 && j0 + i < hi; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      const size_t r = __shfl_sync(0xffffffffu, row, i);
-      if (!__shfl_sync(0xffffffffu, (int)ok, i)) continue;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] += pi * cache_value<CT>(c.v, r + lane + 32 * e);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += u;
     }
+    if (lane == 31) scan_part[warp] = inc;
+    __syncthreads();
+    int base = before;
+    for (int w = 0; w < warp; ++w) base += scan_part[w];
+    if (t < n) {
+      sq[t].row = row;
+      sq[t].len = len;
+      sq[t].first = base + inc - ch;
+    }
+    if (tid == kThreads - 1) scan_total = base + inc;
+    __syncthreads();
+    before = scan_total;
   }
-  const bool empty = l == 0.0f;
-  const float inv = empty ? 0.0f : vs / l;
+  if (tid == 0) sq[n].first = before;
+  __syncthreads();
+  const long long total = (long long)before * units;
+  // ranges of at least one chunk per warp
+  const long long want = (total + kWarps - 1) / kWarps;
+  const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
+
+  // queries that see nothing
+  for (int t = blockIdx.x; t < n; t += gridDim.x) {
+    if (sq[t + 1].first != sq[t].first) continue;
+    for (int i = tid; i < a.n_heads * (D / 8); i += kThreads) {
+      const int h = i / (D / 8), d = (i - h * (D / 8)) * 8;
+      *reinterpret_cast<uint4*>(o + (size_t)t * a.o_token + (size_t)h * a.o_head + d) = make_uint4(0, 0, 0, 0);
+    }
+    if (lse)
+      for (int h = tid; h < a.n_heads; h += kThreads) lse[(size_t)t * a.n_heads + h] = -INFINITY;
+  }
+  if ((int)blockIdx.x >= ctas) {
+    if (tid == 0) cuts[blockIdx.x].valid = 0;
+    return;
+  }
+  const long long c0 = range_begin(blockIdx.x, ctas, total), c1 = range_begin(blockIdx.x + 1, ctas, total);
+
+  // the query that chunk c0 belongs to
+  int t_first;
+  {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((long long)sq[mid].first * units <= c0) lo = mid;
+      else hi = mid - 1;
+    }
+    t_first = lo;   // the last one that begins at or before c0: it has chunks
+  }
+
+  // A place in the flat list of chunks.
+  struct Place {
+    int t, unit, ck, nch;
+  };
+  auto place_of = [&](long long i, int t) {
+    while ((long long)sq[t + 1].first * units <= i) ++t;
+    Place p;
+    p.t = t;
+    p.nch = sq[t + 1].first - sq[t].first;
+    const long long rest = i - (long long)sq[t].first * units;
+    p.unit = (int)(rest / p.nch);
+    p.ck = (int)(rest - (long long)p.unit * p.nch);
+    return p;
+  };
+  auto advance = [&](Place& p, int by) {   // not past the last chunk of the list
+    p.ck += by;
+    while (p.ck >= p.nch) {
+      p.ck -= p.nch;
+      if (++p.unit == units) {
+        p.unit = 0;
+        do {
+          ++p.t;
+          if (p.t >= n) return;
+          p.nch = sq[p.t + 1].first - sq[p.t].first;
+        } while (p.nch == 0);
+      }
+    }
+  };
+
+  // ---- loader: this warp's chunks c0 + warp, c0 + warp + kWarps, ...
+  long long li = c0 + warp;          // next chunk to fetch
+  Place lp = li < c1 ? place_of(li, t_first) : Place{0, 0, 0, 1};
+  int pages = 0;                     // lane j: page of positions 16 j .. 16 j + 15 of that chunk, -1 missing, -2 not seen
+  auto look_up = [&]() {
+    pages = -2;
+    if (li < c1 && lane < K::NP) {
+      const int len = sq[lp.t].len;
+      const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
+      const int pos = (lo / CK + lp.ck) * CK + 16 * lane;
+      if (pos < len && pos + 16 > lo) {
+        pages = c.page_table[(size_t)sq[lp.t].row * c.max_pages + (pos >> ps_shift)];
+        if (pages < 0 || pages >= c.n_pages) {
+          pages = -1;
+          set_status(status, QRE_DEV_BAD_INDEX);
+        }
+      }
+    }
+  };
+  const uint8_t* pool_k = static_cast<const uint8_t*>(c.k);
+  const uint8_t* pool_v = static_cast<const uint8_t*>(c.v);
+  const size_t head_bytes = (size_t)c.page_size * K::RB;
+  uint32_t missing = 0;              // bit NP * slot + j: run j of that ring slot has no page
+  auto fetch = [&](int slot) {       // fetches chunk li into the slot and moves on
+    if (li < c1) {
+      const int len = sq[lp.t].len;
+      const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
+      const int pos0 = (lo / CK + lp.ck) * CK;
+      const int hk = lp.unit / blocks;
+      const uint32_t gone = __ballot_sync(0xffffffffu, pages == -1);
+      missing = (missing & ~(((1u << K::NP) - 1u) << (K::NP * slot))) | (gone << (K::NP * slot));
+      const uint32_t dst = smem_addr(ring + (size_t)slot * 2 * kTile);
+      const int r0 = lane / K::PR, col = lane % K::PR;
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    o[(size_t)t * a.o_token + (size_t)h * a.o_head + lane + 32 * e] = (uint16_t)pack2<DT>(acc[e] * inv, 0.0f);
-  if (lse && lane == 0) lse[(size_t)t * a.n_heads + h] = empty ? -INFINITY : m * kLn2 + logf(l);
+      for (int j = 0; j < K::NP; ++j) {
+        const int page = __shfl_sync(0xffffffffu, pages, j);
+        const size_t base = page < 0 ? 0
+                                     : (((size_t)layer * c.n_pages + page) * c.n_kv_heads + hk) * head_bytes +
+                                           (size_t)((pos0 + 16 * j) & (c.page_size - 1)) * K::RB;
+#pragma unroll
+        for (int r = 0; r < 16; r += K::RI) {
+          const int row = 16 * j + r + r0, pos = pos0 + row;
+          const bool ok = page >= 0 && pos >= lo && pos < len;
+          const size_t off = ok ? base + (size_t)((r + r0) * K::RB + 16 * col) : 0;
+          cp_async_16_zfill(dst + K::at(row, col), pool_k + off, ok);
+          cp_async_16_zfill(dst + kTile + K::at(row, col), pool_v + off, ok);
+        }
+      }
+      li += kWarps;
+      if (li < c1) advance(lp, kWarps);
+      look_up();
+    }
+    cp_async_commit();
+  };
+  look_up();
+  for (int s = 0; s < stages - 1; ++s) fetch(s);
+  int slot_in = stages - 1, slot = 0;
+
+  // ---- the units of this range, one after the other
+  const size_t si = (size_t)layer * c.n_kv_heads;
+  long long s0 = c0;
+  Place cp = place_of(c0, t_first);
+  long long next = c0 + warp;        // this warp's next chunk to compute
+  while (s0 < c1) {
+    const long long u0 = s0 - cp.ck, u1 = u0 + cp.nch;
+    const long long s1 = u1 < c1 ? u1 : c1;
+    const int t = cp.t, hk = cp.unit / blocks, h0 = hk * g + (cp.unit - hk * blocks) * kRows;
+    const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
+    const int len = sq[t].len, lo = a.window > 0 && len > a.window ? len - a.window : 0;
+
+    // the unit's queries as the A operand: rows lane / 4 (and + 8), zero beyond `rows`
+    uint32_t qa[KS][4];
+    float s2[2];                     // score factor of the two rows, base 2
+    const int r0 = lane >> 2, j4 = lane & 3;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = r0 + 8 * hh;
+      s2[hh] = a.scale * kLog2e;
+      if (!HI && hh == 1) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qa[k][1] = qa[k][3] = 0;
+        continue;
+      }
+      const uint16_t* qr = q + (size_t)t * a.q_token + (size_t)(h0 + (r < rows ? r : 0)) * a.q_head;
+      if (!K::F8) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(qr + 16 * k + 2 * j4);
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 + 2 * j4);
+          qa[k][hh] = r < rows ? x : 0;
+          qa[k][2 + hh] = r < rows ? y : 0;
+        }
+      } else {
+        // element order of the E4M3 products: k = 2 j + e is dimension 16 ks + 4 j + e, k = 8 + 2 j + e is 4 j + 2 + e
+        uint2 x[KS];
+        float big = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          x[k] = *reinterpret_cast<const uint2*>(qr + 16 * k + 4 * j4);
+          if (r >= rows) x[k] = make_uint2(0, 0);
+          if (DT == QRE_BF16) {
+            big = fmaxf(big, fmaxf(fmaxf(fabsf(bits_to_float<DT>(x[k].x & 0xffffu)), fabsf(bits_to_float<DT>(x[k].x >> 16))),
+                                   fmaxf(fabsf(bits_to_float<DT>(x[k].y & 0xffffu)), fabsf(bits_to_float<DT>(x[k].y >> 16)))));
+          }
+        }
+        float f = 1.0f;
+        if (DT == QRE_BF16) {
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // largest element to [2^14, 2^15): exact but for elements 2^-29 times smaller, which round to 2^-39 of it
+          const int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
+          const int up = e >= 128 || big == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
+          f = __uint_as_float((uint32_t)(up + 127) << 23);
+          s2[hh] *= __uint_as_float((uint32_t)(127 - up) << 23);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          if (DT == QRE_BF16) {
+            qa[k][hh] = pack2<QRE_FP16>(bits_to_float<DT>(x[k].x & 0xffffu) * f, bits_to_float<DT>(x[k].x >> 16) * f);
+            qa[k][2 + hh] = pack2<QRE_FP16>(bits_to_float<DT>(x[k].y & 0xffffu) * f, bits_to_float<DT>(x[k].y >> 16) * f);
+          } else {
+            qa[k][hh] = x[k].x;
+            qa[k][2 + hh] = x[k].y;
+          }
+        }
+        const float ks = c.k_scale ? c.k_scale[si + hk] : 1.0f;
+        s2[hh] *= ks;
+      }
+    }
+
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    for (; next < s1; next += kWarps) {
+      fetch(slot_in);
+      slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
+      if (stages == 2) cp_async_wait_group<1>();
+      else if (stages == 3) cp_async_wait_group<2>();
+      else cp_async_wait_group<3>();
+      __syncwarp();
+      const uint32_t kt = smem_addr(ring + (size_t)slot * 2 * kTile), vt = kt + kTile;
+
+      float s[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+      const int m8 = lane >> 3, l8 = lane & 7;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int p = 0; p < K::PR / 4; ++p) {
+          uint32_t b[4];
+          ldmatrix_x4(b, kt + K::at(8 * i + l8, 4 * p + m8));
+          if (!K::F8) {
+            mma16816<K::BF>(s[i], qa[2 * p], b[0], b[1]);
+            mma16816<K::BF>(s[i], qa[2 * p + 1], b[2], b[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma16816<false>(s[i], qa[4 * p + e], e4m3x2_to_half2(b[e] & 0xffffu), e4m3x2_to_half2(b[e] >> 16));
+          }
+        }
+      }
+
+      // scores in base 2, with what is not seen at -inf
+      const int pos0 = (lo / CK + (int)(next - u0)) * CK;
+      const uint32_t gone = (missing >> (K::NP * slot)) & ((1u << K::NP) - 1u);
+      const bool edge = pos0 < lo || pos0 + CK > len || gone;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int e = 0; e < (HI ? 4 : 2); ++e) {
+          float x = s[i][e] * s2[e >> 1];
+          if (edge) {
+            const int pos = pos0 + 8 * i + 2 * j4 + (e & 1);
+            if (pos < lo || pos >= len || ((gone >> (i >> 1)) & 1u)) x = -INFINITY;
+          }
+          s[i][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      }
+      bool grow = false;
+      float f[2];
+#pragma unroll
+      for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
+        mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(0xffffffffu, mx[hh], 1));
+        mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(0xffffffffu, mx[hh], 2));
+        const float m2 = fmaxf(m[hh], mx[hh]);
+        f[hh] = m[hh] == m2 ? 1.0f : ex2(m[hh] - m2);   // 2^-inf = 0 for the first keys
+        grow |= m[hh] != m2;
+        m[hh] = m2;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
+          l[hh] *= f[hh];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            acc[i][2 * hh] *= f[hh];
+            acc[i][2 * hh + 1] *= f[hh];
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int e = 0; e < (HI ? 4 : 2); ++e) {
+          const float mm = m[e >> 1];
+          const float p = ex2(s[i][e] - (mm == -INFINITY ? 0.0f : mm));   // nothing seen so far: 2^-inf = 0
+          s[i][e] = p;
+          l[e >> 1] += p;
+        }
+      }
+      // O += P V: the weights are rounded to the products' type (the sum l keeps them in fp32)
+#pragma unroll
+      for (int kk = 0; kk < K::NP; ++kk) {
+        uint32_t pa[4];
+        pa[0] = pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk][0], s[2 * kk][1]);
+        pa[1] = HI ? pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk][2], s[2 * kk][3]) : 0;
+        pa[2] = pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk + 1][0], s[2 * kk + 1][1]);
+        pa[3] = HI ? pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk + 1][2], s[2 * kk + 1][3]) : 0;
+#pragma unroll
+        for (int p = 0; p < K::PR / 2; ++p) {
+          uint32_t b[4];   // pieces 2 p and 2 p + 1, keys 0-7 and 8-15 of each
+          ldmatrix_x4_trans(b, vt + K::at(16 * kk + 8 * (m8 & 1) + l8, 2 * p + (m8 >> 1)));
+          if (!K::F8) {
+            mma16816<K::BF>(acc[2 * p], pa, b[0], b[1]);
+            mma16816<K::BF>(acc[2 * p + 1], pa, b[2], b[3]);
+          } else {
+            // a register holds keys 2 j, 2 j + 1 of dimensions 2 c, 2 c + 1: sort by dimension
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x = __byte_perm(b[2 * e], 0, 0x3120), y = __byte_perm(b[2 * e + 1], 0, 0x3120);
+              mma16816<false>(acc[4 * p + 2 * e], pa, e4m3x2_to_half2(x & 0xffffu), e4m3x2_to_half2(y & 0xffffu));
+              mma16816<false>(acc[4 * p + 2 * e + 1], pa, e4m3x2_to_half2(x >> 16), e4m3x2_to_half2(y >> 16));
+            }
+          }
+        }
+      }
+      slot = slot + 1 == stages ? 0 : slot + 1;
+      __syncwarp();
+    }
+
+    // ---- end of the unit in this range: join the warps
+#pragma unroll
+    for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
+      l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
+      l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
+      if (j4 == 0) ml[warp * kRows + r0 + 8 * hh] = make_float2(m[hh], l[hh]);
+    }
+    const bool whole = s0 == u0 && s1 == u1;
+    float* part = parts + ((size_t)2 * blockIdx.x + (s0 == c0 ? 0 : 1)) * kRows * (D + 2);
+    const float vs = K::F8 && c.v_scale ? c.v_scale[si + hk] : 1.0f;
+#pragma unroll
+    for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
+      if (r0 < buf_rows) {
+        float* b = buf + (size_t)(warp * buf_rows + r0) * D;
+        const int x = (r0 & 3) * 8;   // spreads the rows over the banks
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          if (!K::F8) {
+            *reinterpret_cast<float2*>(b + ((8 * i + 2 * j4) ^ x)) = make_float2(acc[i][2 * hh], acc[i][2 * hh + 1]);
+          } else if (!(i & 1)) {
+            // dimensions 16 p + 4 j .. + 3 (p = i / 2)
+            *reinterpret_cast<float4*>(b + ((8 * i + 4 * j4) ^ x)) =
+                make_float4(acc[i][2 * hh], acc[i + 1][2 * hh], acc[i][2 * hh + 1], acc[i + 1][2 * hh + 1]);
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < buf_rows * (D / 4); i += kThreads) {
+        const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4, r = rr + 8 * hh;
+        if (r >= rows) continue;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+        float L = 0.0f;
+        float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 e = ml[w * kRows + r];
+          // a warp that saw nothing (m = -inf, l = 0) counts nothing; a NaN in l stays one
+          const float f = e.x == -INFINITY && e.y == 0.0f ? 0.0f : ex2(e.x - M);
+          const float4 x = *reinterpret_cast<const float4*>(buf + (size_t)(w * buf_rows + rr) * D + (d ^ ((rr & 3) * 8)));
+          L += e.y * f;
+          sum.x += x.x * f;
+          sum.y += x.y * f;
+          sum.z += x.z * f;
+          sum.w += x.w * f;
+        }
+        if (whole) {
+          const float inv = L == 0.0f ? 0.0f : vs / L;
+          *reinterpret_cast<uint2*>(o + (size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + d) =
+              make_uint2(pack2<DT>(sum.x * inv, sum.y * inv), pack2<DT>(sum.z * inv, sum.w * inv));
+          if (lse && d == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+        } else {
+          *reinterpret_cast<float4*>(part + r * D + d) = sum;
+          if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(M, L);
+        }
+      }
+      __syncthreads();
+    }
+    if (s0 == c0 && tid == 0) {
+      CutInfo ci;
+      ci.u0 = u0;
+      ci.u1 = u1;
+      ci.total = total;
+      ci.t = t;
+      ci.block = cp.unit;
+      ci.ctas = ctas;
+      ci.valid = 1;
+      cuts[blockIdx.x] = ci;
+    }
+    s0 = s1;
+    if (s0 < c1) advance(cp, (int)(s1 - u0) - cp.ck);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
+
+// Joins the parts of the units that were cut: CTA b takes the unit that the begin
+// of range b cuts, if no earlier begin cuts it too.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ qre_attn a,
+                                                        const float* __restrict__ v_scale, uint16_t* __restrict__ o,
+                                                        float* __restrict__ lse, const CutInfo* __restrict__ cuts,
+                                                        const float* __restrict__ parts) {
+  __shared__ float2 ml[kRows];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.x + 1;
+  const CutInfo ci = cuts[b];
+  if (!ci.valid) return;
+  if (ci.u0 >= range_begin(b, ci.ctas, ci.total) || range_begin(b - 1, ci.ctas, ci.total) > ci.u0) return;
+  int e = b;   // last range of the unit
+  while (e + 1 < ci.ctas && range_begin(e + 1, ci.ctas, ci.total) < ci.u1) ++e;
+  const int g = a.n_heads / a.n_kv_heads, blocks = (g + kRows - 1) / kRows;
+  const int hk = ci.block / blocks, h0 = hk * g + (ci.block - hk * blocks) * kRows;
+  const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
+  // part of range c: its first slot when the unit's share begins the range, else its second
+  auto part = [&](int c) {
+    return parts + ((size_t)2 * c + (ci.u0 <= range_begin(c, ci.ctas, ci.total) ? 0 : 1)) * kRows * (D + 2);
+  };
+  const float vs = v_scale ? v_scale[hk] : 1.0f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < rows; r += 8) {
+    float M = -INFINITY, L = 0.0f;
+    for (int c = b - 1 + lane; c <= e; c += 32) M = fmaxf(M, part(c)[kRows * D + 2 * r]);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    for (int c = b - 1 + lane; c <= e; c += 32) {
+      const float2 x = *reinterpret_cast<const float2*>(part(c) + kRows * D + 2 * r);
+      L += x.x == -INFINITY && x.y == 0.0f ? 0.0f : x.y * ex2(x.x - M);
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
+    if (lane == 0) ml[r] = make_float2(M, L);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+    const float M = ml[r].x, L = ml[r].y;
+    float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int c = b - 1; c <= e; ++c) {
+      const float* p = part(c);
+      const float2 x = *reinterpret_cast<const float2*>(p + kRows * D + 2 * r);
+      const float4 y = *reinterpret_cast<const float4*>(p + r * D + d);
+      const float f = x.x == -INFINITY && x.y == 0.0f ? 0.0f : ex2(x.x - M);
+      sum.x += y.x * f;
+      sum.y += y.y * f;
+      sum.z += y.z * f;
+      sum.w += y.w * f;
+    }
+    const float inv = L == 0.0f ? 0.0f : vs / L;
+    *reinterpret_cast<uint2*>(o + (size_t)ci.t * a.o_token + (size_t)(h0 + r) * a.o_head + d) =
+        make_uint2(pack2<DT>(sum.x * inv, sum.y * inv), pack2<DT>(sum.z * inv, sum.w * inv));
+    if (lse && d == 0) lse[(size_t)ci.t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+  }
+}
+
+int decode_grid() {
+  const int sms = device_sm_count();
+  return sms <= 0 ? 152 : (sms < kMaxParts ? sms : kMaxParts);   // one CTA per SM
+}
+
+size_t cut_bytes(int grid) { return ((size_t)grid * sizeof(CutInfo) + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t attn_decode_ws_bytes(const qre_attn&, const qre_kv_cache&, int) { return 256; }
+size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache&, int) {
+  const int grid = decode_grid();
+  return cut_bytes(grid) + (size_t)2 * grid * kRows * (a.head_dim + 2) * sizeof(float);
+}
 
 cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
                                int max_len, const void* q, void* o, float* lse, void* ws, int* status,
                                cudaStream_t stream) {
-  const long long units = (long long)n * a.n_heads;
-  auto go = [&](auto kernel) {
-    return launch_dependent(kernel, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, stream, a, c, layer, n, seqs,
-                            static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, status);
+  const int grid = decode_grid();
+  const int g = a.n_heads / a.n_kv_heads;
+  const int buf_rows = g < 8 ? g : 8;
+  const size_t fixed = (size_t)kWarps * buf_rows * a.head_dim * sizeof(float) + kWarps * kRows * sizeof(float2) +
+                       (size_t)(n + 1) * sizeof(Seq);
+  const long long room = (long long)device_max_smem_optin() - 256 - (long long)fixed;
+  int stages = (int)(room / (kWarps * 2 * kTile));
+  stages = stages < 2 ? 2 : (stages > 3 ? 3 : stages);
+  const size_t smem = (size_t)stages * kWarps * 2 * kTile + fixed;
+  CutInfo* cuts = static_cast<CutInfo*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + cut_bytes(grid));
+  const float* v_scale = c.dtype == QRE_E4M3 && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;
+  auto go = [&](auto kernel, auto join) -> cudaError_t {
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kernel, dim3(grid), dim3(kThreads), smem, stream, a, c, layer, n, seqs,
+                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, cuts, parts, stages,
+                         buf_rows, status);
+    if (e != cudaSuccess || grid < 2) return e;
+    return launch_dependent(join, dim3(grid - 1), dim3(256), 0, stream, a, v_scale, static_cast<uint16_t*>(o), lse,
+                            const_cast<const CutInfo*>(cuts), const_cast<const float*>(parts));
   };
+  auto pick = [&](auto dt, auto ct, auto d) {
+    constexpr int DT = decltype(dt)::value, CT = decltype(ct)::value, D = decltype(d)::value;
+    return g > 8 ? go(attn_decode_kernel<DT, CT, D, true>, attn_join_kernel<DT, D>)
+                 : go(attn_decode_kernel<DT, CT, D, false>, attn_join_kernel<DT, D>);
+  };
+  using B = std::integral_constant<int, QRE_BF16>;
+  using H = std::integral_constant<int, QRE_FP16>;
+  using E = std::integral_constant<int, QRE_E4M3>;
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
   const bool bf = a.dtype == QRE_BF16, d64 = a.head_dim == 64;
   if (c.dtype == QRE_E4M3) {
-    if (bf) return d64 ? go(attn_decode_kernel<QRE_BF16, QRE_E4M3, 64>) : go(attn_decode_kernel<QRE_BF16, QRE_E4M3, 128>);
-    return d64 ? go(attn_decode_kernel<QRE_FP16, QRE_E4M3, 64>) : go(attn_decode_kernel<QRE_FP16, QRE_E4M3, 128>);
+    if (bf) return d64 ? pick(B{}, E{}, D64{}) : pick(B{}, E{}, D128{});
+    return d64 ? pick(H{}, E{}, D64{}) : pick(H{}, E{}, D128{});
   }
-  if (bf) return d64 ? go(attn_decode_kernel<QRE_BF16, QRE_BF16, 64>) : go(attn_decode_kernel<QRE_BF16, QRE_BF16, 128>);
-  return d64 ? go(attn_decode_kernel<QRE_FP16, QRE_FP16, 64>) : go(attn_decode_kernel<QRE_FP16, QRE_FP16, 128>);
+  if (bf) return d64 ? pick(B{}, B{}, D64{}) : pick(B{}, B{}, D128{});
+  return d64 ? pick(H{}, H{}, D64{}) : pick(H{}, H{}, D128{});
 }
 
 }  // namespace qre
