@@ -127,6 +127,12 @@ cudaError_t launch_combine(const qre_layer_shape& s, int T, const float* expert_
 // (e.g. a base that is not 16-byte aligned).
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
 
+// 3-D tensor map of [token][head][cols] rows of 16-bit elements (strides in
+// elements): boxes of 64 columns x box_heads heads x box_tokens tokens, 128-byte
+// swizzle, zero fill outside.  False when the driver refuses it.
+bool make_tmap_rows16(CUtensorMap* m, const void* base, long long tokens, long long token_stride, int heads,
+                      long long head_stride, int cols, int box_heads, int box_tokens);
+
 // Key-value cache (kv_cache.cu) and attention (attn_prefill.cu, attn_decode.cu).
 // The arguments have been checked (api_attn.cu).
 constexpr int kKvMaxRequests = 4096;   // sequences, requests or forks of one call
