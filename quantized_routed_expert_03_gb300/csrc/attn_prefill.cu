@@ -281,68 +281,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         *issued = i;
       }
     } else if (warp == kMmaWarp) {
-      if (lane == 0 && je > jb) {
+      if (je > jb) {   // the whole warp, so that the operands stay in uniform registers
+        const uint32_t lead = elect_lane();
         const uint32_t id_s = DT == QRE_BF16 ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
         const uint32_t id_o = (DT == QRE_BF16 ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
-        const uint32_t q_addr = smem_addr(sq), kv_addr = smem_addr(skv);
-        auto scores = [&](int t, int j) {      // S_t = Q_t K_j^T
-          const uint32_t ka = kv_addr + (uint32_t)((2 * (j - jb)) % P::SLOTS) * P::TILE, qa = q_addr + t * P::TILE;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t qd = umma_desc_sw128(smem_addr(sq)), kd = umma_desc_sw128(smem_addr(skv));
+        const uint64_t vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
+        auto scores = [&](int t, int slot) {      // S_t = Q_t K_j^T
+          const uint64_t k0d = kd + (uint32_t)slot * (P::TILE >> 4), q0d = qd + (uint32_t)t * (P::TILE >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * P::HALF + (k % 4) * 32;
-            umma_f16(tmem + (t ? kS1 : kS0), umma_desc_sw128(qa + off), umma_desc_sw128(ka + off), id_s, k ? 1u : 0u);
+            const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
+            umma_f16_lead(tm + (t ? kS1 : kS0), q0d + off, k0d + off, id_s, k ? 1u : 0u, lead);
           }
-          umma_commit(&s_full[t]);
+          umma_commit_lead(&s_full[t], lead);
         };
-        auto values = [&](int t, int j, bool first) {   // O_t += P_t V_j
-          const uint32_t va = kv_addr + (uint32_t)((2 * (j - jb) + 1) % P::SLOTS) * P::TILE;
+        auto values = [&](int t, int slot, bool first) {   // O_t += P_t V_j
+          const uint64_t v0d = vd + (uint32_t)slot * (P::TILE >> 4);
 #pragma unroll
           for (int k = 0; k < kN / 16; ++k)
-            umma_f16_tmem_a(tmem + (t ? kO1 : kO0), tmem + (t ? kS1 : kS0) + 8 * k,
-                            umma_desc_sw128_mn(va + 2048 * k, P::HALF), id_o, first && k == 0 ? 0u : 1u);
-          umma_commit(&o_done[t]);
+            umma_f16_tmem_a_lead(tm + (t ? kO1 : kO0), tm + (t ? kS1 : kS0) + 8 * k, v0d + k * (2048 >> 4), id_o,
+                                 first && k == 0 ? 0u : 1u, lead);
+          umma_commit_lead(&o_done[t], lead);
         };
-        auto wait_tile = [&](int i) {
-          return mbar_wait_inline(&full[i % P::SLOTS], (i / P::SLOTS) & 1, abort_flag, status, limit_ns);
+        auto wait_for = [&](uint64_t* b, uint32_t parity) {
+          return __all_sync(0xffffffffu, mbar_wait_inline(b, parity, abort_flag, status, limit_ns) ? 1 : 0) != 0;
         };
-        bool ok = mbar_wait_inline(q_full, 0, abort_flag, status, limit_ns) && wait_tile(0);
+        auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], (i / P::SLOTS) & 1); };
+        bool ok = wait_for(q_full, 0) && wait_tile(0);
         tc_fence_after();
         if (ok) {
-          if (active(0, jb)) scores(0, jb);
-          if (active(1, jb)) scores(1, jb);
-          umma_commit(&empty[0]);
+          if (active(0, jb)) scores(0, 0);
+          if (active(1, jb)) scores(1, 0);
+          umma_commit_lead(&empty[0], lead);
         }
         int pn[2] = {0, 0};
         for (int j = jb; ok && j < je; ++j) {
-          const int i = 2 * (j - jb);
+          const int i = 2 * (j - jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
           bool have_next = j + 1 >= je;
-          if (!wait_tile(i + 1) || !mbar_wait_inline(&scanned[(i + 1) % P::SLOTS], ((i + 1) / P::SLOTS) & 1,
-                                                      abort_flag, status, limit_ns))
-            break;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (active(t, j)) {
-              ok = mbar_wait_inline(&p_full[t], pn[t] & 1, abort_flag, status, limit_ns);
-              if (!ok) break;
+          if (!wait_tile(i + 1) || !wait_for(&scanned[sv], ((i + 1) / P::SLOTS) & 1)) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (ok && active(t, j)) {
+              ok = wait_for(&p_full[t], pn[t] & 1);
               tc_fence_after();
-              values(t, j, pn[t] == 0);
+              if (ok) values(t, sv, pn[t] == 0);
               ++pn[t];
             }
             // the scores of the next tile overwrite P: issued behind the product that reads it
-            if (j + 1 < je && active(t, j + 1)) {
+            if (ok && j + 1 < je && active(t, j + 1)) {
               if (!have_next) {
                 ok = wait_tile(i + 2);
-                if (!ok) break;
                 have_next = true;
                 tc_fence_after();
               }
-              scores(t, j + 1);
+              if (ok) scores(t, sk);
             }
           }
           if (!ok) break;
-          umma_commit(&empty[(i + 1) % P::SLOTS]);
+          umma_commit_lead(&empty[sv], lead);
           if (j + 1 < je) {
             if (!have_next && !wait_tile(i + 2)) break;
-            umma_commit(&empty[(i + 2) % P::SLOTS]);
+            umma_commit_lead(&empty[sk], lead);
           }
         }
       }
@@ -426,9 +427,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 128; ++i)
             if (i < a0 || i >= a1) x[i] = 0xff800000u;   // -inf
         }
-        float mx = __uint_as_float(x[0]);
+        float mx8[8];   // independent chains: a single one would be 64 dependent steps
 #pragma unroll
-        for (int i = 1; i < 128; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
+        for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 8]));
+#pragma unroll
+        for (int i = 16; i < 128; i += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx8[e] = max3(mx8[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 8 + e]));
+        const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         // the reference follows the maximum only when it is far behind: weights stay below 2^8
         bool move = false;
         float f = 1.0f;
@@ -455,21 +461,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.0f : m * s2;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t s22 = pair(s2, s2), off2 = pair(-off, -off);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2(fmaf(__uint_as_float(x[32 * b + 2 * i]), s2, -off));
-            const float p1 = ex2(fmaf(__uint_as_float(x[32 * b + 2 * i + 1]), s2, -off));
-            sum[(2 * i) & 3] += p0;
-            sum[(2 * i + 1) & 3] += p1;
+            const float2 y = unpair(fma2(pair(__uint_as_float(x[32 * b + 2 * i]), __uint_as_float(x[32 * b + 2 * i + 1])),
+                                         s22, off2));
+            const float p0 = ex2(y.x), p1 = ex2(y.y);
+            sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
             p[i] = pack2<DT>(p0, p1);    // the weights of the product are rounded; the sum is not
           }
           tmem_st_32x32b_x16(sc + 16 * b, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 total = unpair(add2(sum[0], sum[1]));
+        l += total.x + total.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
