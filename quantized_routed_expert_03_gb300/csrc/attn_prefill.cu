@@ -3,6 +3,8 @@
 // o_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys that query i sees, in
 // one pass: with the running maximum m and sum l (fp32, base 2),
 //   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), o' alike.
+#include <type_traits>
+
 #include "attn.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -88,21 +90,26 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
 
 constexpr int kM = 128;            // rows of a query tile: kM / gp tokens x gp heads of one KV head
 constexpr int kN = 128;            // keys of a tile
+constexpr int kPart = 96;          // keys of a tile's first part (of two): P V of it starts while the rest is weighted
 constexpr int kThreads = 384;
 // warps 0-3: softmax of tile 0, 4-7: of tile 1
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScanWarp = 10, kScanWarps = 2;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScanWarp = 11;   // MMA warps 9 and 10: one per query tile
 // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384;   // tensor-memory columns; P overwrites its S
-constexpr float kLazy = 8.0f;      // the reference maximum follows when it is 2^8 behind
+// A row's weights are taken against a reference that stays while their sum is at
+// most this: fp16 weights must not pass 65504, bf16 ones have fp32's range.
+template <int DT>
+constexpr float kMostWeight = DT == QRE_BF16 ? 1.1529215e18f /* 2^60 */ : 32768.0f;
 
 template <int D>
 struct Plan {
   static constexpr int HALF = kN * 128;              // 64 columns of a 128-row tile, 128-byte rows
   static constexpr int TILE = HALF * (D / 64);
   static constexpr int SLOTS = D == 128 ? 4 : 8;     // K and V tiles in flight
-  static constexpr int BYTES = 1024 + 2 * TILE + SLOTS * TILE + 512;
+  static constexpr int STAGE = 32 * 64;              // output rows of a softmax warp on their way out: 32 columns
+  static constexpr int BYTES = 1024 + 2 * TILE + SLOTS * TILE + 8 * STAGE + 1024;
 };
 
 // mbar_wait_bounded without a call: the register split (setmaxnreg) leaves no room for the calling convention.
@@ -121,14 +128,166 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity,
   return true;
 }
 
-// One query tile's keys: tiles [jb, je) of the sequence.
-struct TileKeys {
-  int jb, je;
+// Of two 16-bit pairs the larger magnitudes, NaN if there is one.
+template <int DT>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  if (DT == QRE_BF16) {
+    const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)), __habs2(*reinterpret_cast<const __half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One piece of work: two query tiles of one sequence and head group.
+struct Work {
+  int q0, q_len, k0, k_len;   // the sequence
+  int tok0;                   // first token, in the sequence
+  int h0;                     // first head
+  int end;                    // no more work
+  int poison;                 // a value that is not finite was taken out of a key tile
+};
+
+// What every warp derives from it.
+struct Range {
+  int jb, je;   // key tiles [jb, je) of the sequence
+};
+struct Job {
+  Range r0, r1;           // of the two query tiles
+  int jb, je;             // of both
+  int lo_last, hi_first;  // first key of the last token, end of the keys of the first
+  __device__ __forceinline__ Job(const qre_attn& a, const Work& w, int tt) {
+    const int shift = w.k_len - w.q_len;   // position of token i is i + shift
+    auto keys_of = [&](int t) {            // both bounds grow with the token
+      Range r{0, 0};
+      const int ta = w.tok0 + t * tt, tb = ta + tt < w.q_len ? ta + tt : w.q_len;
+      if (ta < tb) {
+        int lo, hi, x;
+        visible_range(ta + shift, w.k_len, a.causal, a.window, lo, x);
+        visible_range(tb - 1 + shift, w.k_len, a.causal, a.window, x, hi);
+        if (hi > lo) {
+          r.jb = lo / kN;
+          r.je = (hi + kN - 1) / kN;
+        }
+      }
+      return r;
+    };
+    r0 = keys_of(0);
+    r1 = keys_of(1);
+    const bool has0 = r0.je > r0.jb, has1 = r1.je > r1.jb;
+    jb = has0 ? r0.jb : r1.jb;
+    je = has1 ? r1.je : r0.je;
+    const int last = (w.tok0 + 2 * tt < w.q_len ? w.tok0 + 2 * tt : w.q_len) - 1;
+    int x;
+    visible_range(last + shift, w.k_len, a.causal, a.window, lo_last, x);
+    visible_range(w.tok0 + shift, w.k_len, a.causal, a.window, x, hi_first);
+  }
+  // some token of the work does not see all of key tile j
+  __device__ __forceinline__ bool special(int j) const { return j * kN < lo_last || (j + 1) * kN > hi_first; }
+};
+
+// Finds the piece of work of an index.  The longest come first, so that the last
+// CTAs to finish end together: with at most 128 sequences the tiles of all
+// sequences are ordered by their last key tile, with more (then each is short
+// against the whole) by sequence.
+class Finder {
+ public:
+  __device__ __forceinline__ Finder(int n_seqs, int total_q, int total_k, const int32_t* cu_q, const int32_t* cu_k, int pair)
+      : n_(n_seqs), tq_(total_q), tk_(total_k), cu_q_(cu_q), cu_k_(cu_k), pair_(pair) {
+    lane_ = threadIdx.x & 31;
+    if (n_ <= 128) {
+      int top = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        load(32 * c + lane_, cnt_[c], shift_[c]);
+        if (cnt_[c] > 0) top = max(top, (shift_[c] + cnt_[c] * pair_ - 1) / kN);
+      }
+      top_ = __reduce_max_sync(0xffffffffu, top);
+    }
+  }
+  // False: no work of that index.
+  __device__ __forceinline__ bool find(int b, int& seq, int& tile) {
+    if (n_ <= 128) {
+      if (b >= at_least(0)) return false;
+      int lo = 0, hi = top_;          // the largest level with more than b tiles at or above it
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (at_least(mid) > b) lo = mid;
+        else hi = mid - 1;
+      }
+      int rest = b - at_least(lo + 1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int first = lowest(c, lo), e = cnt_[c] - first - (cnt_[c] - lowest(c, lo + 1));
+        const int sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)e);
+        if (rest < sum) {
+          pick(e, rest, c, first, seq, tile);
+          return true;
+        }
+        rest -= sum;
+      }
+      return false;
+    }
+    if (b < base_) at_ = base_ = 0;   // indices come in ascending order: go on from the last one
+    for (; at_ < n_; at_ += 32) {
+      int cnt, shift;
+      load(at_ + lane_, cnt, shift);
+      const int sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)cnt);
+      if (b < base_ + sum) {
+        pick(cnt, b - base_, at_ / 32, 0, seq, tile);
+        tile = __shfl_sync(0xffffffffu, cnt, seq & 31) - 1 - tile;   // a sequence's longest first
+        return true;
+      }
+      base_ += sum;
+    }
+    return false;
+  }
+
+ private:
+  __device__ __forceinline__ void load(int i, int& cnt, int& shift) const {
+    cnt = shift = 0;
+    if (i < n_) {
+      const int q0 = cu_q_[i], q1 = cu_q_[i + 1], k0 = cu_k_[i], k1 = cu_k_[i + 1];
+      if (q0 >= 0 && q1 >= q0 && q1 <= tq_ && k0 >= 0 && k1 >= k0 && k1 <= tk_) {
+        cnt = (q1 - q0 + pair_ - 1) / pair_;
+        shift = k1 - k0 - (q1 - q0);
+      }
+    }
+  }
+  // first tile of sequence (c, lane) whose last token stands at level * kN or later
+  __device__ __forceinline__ int lowest(int c, int level) const {
+    const int x = level * kN + 1 - shift_[c];
+    const int i = level <= 0 || x <= 0 ? 0 : (x + pair_ - 1) / pair_ - 1;
+    return i < cnt_[c] ? i : cnt_[c];
+  }
+  __device__ __forceinline__ int at_least(int level) const {
+    int s = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s += cnt_[c] - lowest(c, level);
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
+  }
+  // the `rest`-th of the lanes' e items
+  __device__ __forceinline__ void pick(int e, int rest, int c, int first, int& seq, int& tile) const {
+    int inc = e;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane_ >= d) inc += u;
+    }
+    const int w = __ffs(__ballot_sync(0xffffffffu, rest < inc)) - 1;
+    seq = 32 * c + w;
+    tile = __shfl_sync(0xffffffffu, first, w) + rest - __shfl_sync(0xffffffffu, inc - e, w);
+  }
+  int n_, tq_, tk_;
+  const int32_t *cu_q_, *cu_k_;
+  int pair_, lane_, top_ = 0, at_ = 0, base_ = 0;
+  int cnt_[4], shift_[4];
 };
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tc_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q, int total_k, int gp, int groups,
+    attn_tc_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q, int total_k, int gp_shift, int groups,
                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, int q_heads_move, int k_heads_move, int v_heads_move,
@@ -139,400 +298,504 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = smem;                       // two query tiles
   uint8_t* skv = smem + 2 * P::TILE;        // ring of key and value tiles
-  uint64_t* bar = reinterpret_cast<uint64_t*>(skv + P::SLOTS * P::TILE);
-  uint64_t* full = bar;                     // [SLOTS]
+  uint8_t* stage = skv + P::SLOTS * P::TILE;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(stage + 8 * P::STAGE);
+  uint64_t* answer = bar;                   // [2], 16-byte aligned
+  uint64_t* full = answer + 2;              // [SLOTS]
   uint64_t* empty = full + P::SLOTS;        // [SLOTS]
-  uint64_t* q_full = empty + P::SLOTS;
-  uint64_t* s_full = q_full + 1;            // [2]
-  uint64_t* p_full = s_full + 2;            // [2]
-  uint64_t* o_done = p_full + 2;            // [2]
-  uint64_t* scanned = o_done + 2;           // [SLOTS]
-  uint64_t* drain = scanned + P::SLOTS;
-  uint32_t* tmem_p = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* scanned = empty + P::SLOTS;     // [SLOTS]
+  uint64_t* q_full = scanned + P::SLOTS;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;           // [2]
+  uint64_t* p_full = s_full + 2;            // [part][2]: one phase of each per key tile
+  uint64_t* o_done = p_full + 4;            // [part][2]
+  uint64_t* turn = o_done + 4;              // [2]: the MMA warps issue in turn
+  uint64_t* work_full = turn + 2;           // [2]
+  uint64_t* work_empty = work_full + 2;     // [2]
+  uint64_t* answered = work_empty + 2;
+  uint64_t* drain = answered + 1;           // [2]
+  Work* works = reinterpret_cast<Work*>(drain + 2);          // [2]
+  uint32_t* tmem_p = reinterpret_cast<uint32_t*>(works + 2);
   int* misc = reinterpret_cast<int*>(tmem_p + 1);
   volatile int* abort_flag = misc;          // a wait gave up
-  volatile int* poison = misc + 1;          // a value that is not finite was taken out of a tile
-  int* issued = misc + 2;                   // ring tiles whose loads were issued
-  int* where = misc + 3;                    // sequence and tile of this CTA
+  int* issued = misc + 1;                   // ring tiles whose loads were issued
+  int* q_issued = misc + 2;                 // loads of query tiles
+  int* asked = misc + 3;                    // questions for the next piece of work
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int group = blockIdx.x % groups;
-  const int tt = kM / gp;                   // tokens of a query tile
+  const int gp = 1 << gp_shift, tt = kM >> gp_shift;   // heads and tokens of a query tile
 
   if (tid == 0) {
     for (int s = 0; s < P::SLOTS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-      mbar_init(&scanned[s], kScanWarps);
+      mbar_init(&empty[s], 2);
+      mbar_init(&scanned[s], 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
-      mbar_init(&o_done[t], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&p_full[2 * h + t], 4);
+        mbar_init(&o_done[2 * h + t], 1);
+      }
+      mbar_init(&turn[t], 1);
+      mbar_init(&work_full[t], 1);
+      mbar_init(&work_empty[t], kThreads / 32 - 1);
+      mbar_init(&drain[t], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(answered, 1);
     *abort_flag = 0;
-    *poison = 0;
-    *issued = 0;
+    *issued = *q_issued = *asked = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_p, kTmemCols);
     tmem_relinquish();
   }
-  grid_dependency_wait();
-  grid_dependents_launch();
-  // ---- this CTA's sequence: the tile index counts the sequences' pairs of query tiles
-  if (warp == 0) {
-    int rest = blockIdx.x / groups, s = -1;
-    for (int i0 = 0; i0 < n_seqs && s < 0; i0 += 32) {
-      const int i = i0 + lane;
-      int cnt = 0;
-      if (i < n_seqs) {
-        const int q0 = cu_q[i], q1 = cu_q[i + 1], k0 = cu_k[i], k1 = cu_k[i + 1];
-        if (q0 >= 0 && q1 >= q0 && q1 <= total_q && k0 >= 0 && k1 >= k0 && k1 <= total_k)
-          cnt = (q1 - q0 + 2 * tt - 1) / (2 * tt);
-      }
-      int inc = cnt;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += u;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, rest < inc);
-      if (hit) {
-        const int w = __ffs(hit) - 1;
-        s = i0 + w;
-        const int before = __shfl_sync(0xffffffffu, inc - cnt, w), n = __shfl_sync(0xffffffffu, cnt, w);
-        rest = n - 1 - (rest - before);   // a sequence's last tiles, the longest, first
-      } else {
-        rest -= __shfl_sync(0xffffffffu, inc, 31);
-      }
-    }
-    if (lane == 0) {
-      where[0] = s;
-      where[1] = rest;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();
+  grid_dependents_launch();
   const uint32_t tmem = *tmem_p;
-  const int seq = where[0];
   if (blockIdx.x == 0)   // bad bounds are flagged once
     for (int i = tid; i < n_seqs; i += kThreads) {
       const int q0 = cu_q[i], q1 = cu_q[i + 1], k0 = cu_k[i], k1 = cu_k[i + 1];
       if (q0 < 0 || q1 < q0 || q1 > total_q || k0 < 0 || k1 < k0 || k1 > total_k) set_status(status, QRE_DEV_BAD_INDEX);
     }
-  if (seq >= 0) {
-    const int q0 = cu_q[seq], q_len = cu_q[seq + 1] - q0, k0 = cu_k[seq], k_len = cu_k[seq + 1] - k0;
-    const int h0 = group * gp, hk = h0 / (a.n_heads / a.n_kv_heads);
-    const int tok0 = where[1] * 2 * tt;     // first token, in the sequence
-    const int shift = k_len - q_len;        // position of token i is i + shift
-    // key tiles that a query tile's tokens see (both bounds grow with the token)
-    auto keys_of = [&](int t) {
-      TileKeys r{0, 0};
-      const int ta = tok0 + t * tt, tb = ta + tt < q_len ? ta + tt : q_len;
-      if (ta < tb) {
-        int lo, hi, x;
-        visible_range(ta + shift, k_len, a.causal, a.window, lo, x);
-        visible_range(tb - 1 + shift, k_len, a.causal, a.window, x, hi);
-        if (hi > lo) {
-          r.jb = lo / kN;
-          r.je = (hi + kN - 1) / kN;
-        }
-      }
-      return r;
-    };
-    const TileKeys r0 = keys_of(0), r1 = keys_of(1);
-    const bool has0 = r0.je > r0.jb, has1 = r1.je > r1.jb;
-    const int jb = has0 ? r0.jb : r1.jb, je = has1 ? r1.je : r0.je;
-    auto active = [&](int t, int j) { return t == 0 ? j >= r0.jb && j < r0.je : j >= r1.jb && j < r1.je; };
-    // tile j is special when some token of the CTA does not see all of it
-    const int last_tok = (tok0 + 2 * tt < q_len ? tok0 + 2 * tt : q_len) - 1;
-    int lo_last, hi_first;
-    {
-      int x;
-      visible_range(last_tok + shift, k_len, a.causal, a.window, lo_last, x);
-      visible_range(tok0 + shift, k_len, a.causal, a.window, x, hi_first);
-    }
-    auto special = [&](int j) { return j * kN < lo_last || (j + 1) * kN > hi_first; };
+  auto wait_for = [&](uint64_t* b, int n) {   // phase n of b; the same answer in all lanes
+    return __all_sync(0xffffffffu, mbar_wait_inline(b, n & 1, abort_flag, status, limit_ns) ? 1 : 0) != 0;
+  };
+  // The n-th piece of work; false when there is none or a wait gave up.
+  auto take = [&](int n, Work& w) {
+    if (!wait_for(&work_full[n & 1], n >> 1)) return false;
+    w = works[n & 1];
+    return w.end == 0;
+  };
+  auto give_back = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_empty[n & 1]);
+  };
 
-    if (warp >= kTmaWarp) {
+  if (warp >= kTmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
-      if (lane == 0 && je > jb) {
-        const int qh = q_heads_move ? h0 : 0, kh = k_heads_move ? hk : 0, vh = v_heads_move ? hk : 0;
-        mbar_arrive_expect_tx(q_full, 2 * P::TILE);
-        for (int t = 0; t < 2; ++t)
-          for (int x = 0; x < D / 64; ++x)
-            tma_load_3d(sq + t * P::TILE + x * P::HALF, &tq, 64 * x, qh, q0 + tok0 + t * tt, q_full);
-        const int n = 2 * (je - jb);
-        int i = 0;
-        for (; i < n; ++i) {
-          const int s = i % P::SLOTS;
-          if (i >= P::SLOTS && !mbar_wait_inline(&empty[s], ((i / P::SLOTS) - 1) & 1, abort_flag, status, limit_ns)) break;
-          mbar_arrive_expect_tx(&full[s], P::TILE);
-          for (int x = 0; x < D / 64; ++x)
-            tma_load_3d(skv + s * P::TILE + x * P::HALF, (i & 1) ? &tv : &tk, 64 * x, (i & 1) ? vh : kh,
-                        k0 + (jb + i / 2) * kN, &full[s]);
+      // ---- finds the work, fetches its tiles, and asks for the next
+      Finder finder(n_seqs, total_q, total_k, cu_q, cu_k, 2 * tt);
+      int b = blockIdx.x, i0 = 0, nq = 0;
+      for (int n = 0;; ++n) {
+        int seq = 0, tile = 0;
+        const bool have = b >= 0 && finder.find(b / groups, seq, tile);
+        if (n >= 2 && !wait_for(&work_empty[n & 1], (n >> 1) - 1)) break;
+        Work w{};
+        w.end = !have;
+        if (have) {
+          w.q0 = cu_q[seq];
+          w.q_len = cu_q[seq + 1] - w.q0;
+          w.k0 = cu_k[seq];
+          w.k_len = cu_k[seq + 1] - w.k0;
+          w.tok0 = tile * 2 * tt;
+          w.h0 = (b % groups) * gp;
         }
-        *issued = i;
+        if (lane == 0) {
+          works[n & 1] = w;
+          mbar_arrive(&work_full[n & 1]);
+        }
+        __syncwarp();
+        if (!have) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(answered, 16);
+          ask_next_cta(answer, answered);
+          *asked = n + 1;
+        }
+        const Job job(a, w, tt);
+        bool ok = true;
+        if (job.je > job.jb) {
+          const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
+          const int qh = q_heads_move ? w.h0 : 0, kh = k_heads_move ? hk : 0, vh = v_heads_move ? hk : 0;
+          ok = nq == 0 || wait_for(q_empty, nq - 1);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(q_full, 2 * P::TILE);
+            for (int t = 0; t < 2; ++t)
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_3d(sq + t * P::TILE + x * P::HALF, &tq, 64 * x, qh, w.q0 + w.tok0 + t * tt, q_full);
+            *q_issued = nq + 1;
+          }
+          ++nq;
+          const int end = i0 + 2 * (job.je - job.jb);
+          for (int i = i0; ok && i < end; ++i) {
+            const int s = i % P::SLOTS;
+            ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
+            if (ok && lane == 0) {
+              const bool is_v = (i - i0) & 1;
+              mbar_arrive_expect_tx(&full[s], P::TILE);
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_3d(skv + s * P::TILE + x * P::HALF, is_v ? &tv : &tk, 64 * x, is_v ? vh : kh,
+                            w.k0 + (job.jb + (i - i0) / 2) * kN, &full[s]);
+              *issued = i + 1;
+            }
+          }
+          i0 = end;
+        }
+        if (!ok || !wait_for(answered, n)) break;
+        b = next_cta(answer);
+        fence_proxy_async_smem();   // read before the next answer is written
+        __syncwarp();
       }
-    } else if (warp == kMmaWarp) {
-      if (je > jb) {   // the whole warp, so that the operands stay in uniform registers
-        const uint32_t lead = elect_lane();
-        const uint32_t id_s = DT == QRE_BF16 ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
-        const uint32_t id_o = (DT == QRE_BF16 ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t qd = umma_desc_sw128(smem_addr(sq)), kd = umma_desc_sw128(smem_addr(skv));
-        const uint64_t vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
-        auto scores = [&](int t, int slot) {      // S_t = Q_t K_j^T
-          const uint64_t k0d = kd + (uint32_t)slot * (P::TILE >> 4), q0d = qd + (uint32_t)t * (P::TILE >> 4);
+    } else if (warp < kScanWarp) {
+      // ---- MMA: the whole warp, so that the operands stay in uniform registers
+      const int t = warp - kMmaWarp;
+      const uint32_t lead = elect_lane();
+      const uint32_t id_s = DT == QRE_BF16 ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
+      const uint32_t id_o = (DT == QRE_BF16 ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + (t ? kS1 : kS0), to = tm + (t ? kO1 : kO0);
+      const uint64_t qd = umma_desc_sw128(smem_addr(sq + t * P::TILE)), kd = umma_desc_sw128(smem_addr(skv));
+      const uint64_t vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
+      auto scores = [&](int slot) {      // S = Q K_j^T
+        const uint64_t k0d = kd + (uint32_t)slot * (P::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
-            umma_f16_lead(tm + (t ? kS1 : kS0), q0d + off, k0d + off, id_s, k ? 1u : 0u, lead);
-          }
-          umma_commit_lead(&s_full[t], lead);
-        };
-        auto values = [&](int t, int slot, bool first) {   // O_t += P_t V_j
-          const uint64_t v0d = vd + (uint32_t)slot * (P::TILE >> 4);
-#pragma unroll
-          for (int k = 0; k < kN / 16; ++k)
-            umma_f16_tmem_a_lead(tm + (t ? kO1 : kO0), tm + (t ? kS1 : kS0) + 8 * k, v0d + k * (2048 >> 4), id_o,
-                                 first && k == 0 ? 0u : 1u, lead);
-          umma_commit_lead(&o_done[t], lead);
-        };
-        auto wait_for = [&](uint64_t* b, uint32_t parity) {
-          return __all_sync(0xffffffffu, mbar_wait_inline(b, parity, abort_flag, status, limit_ns) ? 1 : 0) != 0;
-        };
-        auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], (i / P::SLOTS) & 1); };
-        bool ok = wait_for(q_full, 0) && wait_tile(0);
-        tc_fence_after();
-        if (ok) {
-          if (active(0, jb)) scores(0, 0);
-          if (active(1, jb)) scores(1, 0);
-          umma_commit_lead(&empty[0], lead);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
+          umma_f16_lead(ts, qd + off, k0d + off, id_s, k ? 1u : 0u, lead);
         }
-        int pn[2] = {0, 0};
-        for (int j = jb; ok && j < je; ++j) {
-          const int i = 2 * (j - jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
-          bool have_next = j + 1 >= je;
-          if (!wait_tile(i + 1) || !wait_for(&scanned[sv], ((i + 1) / P::SLOTS) & 1)) break;
+        umma_commit_lead(&s_full[t], lead);
+      };
+      auto values = [&](int slot, int part, bool first) {   // O += P V_j, one part of the keys
+        const uint64_t v0d = vd + (uint32_t)slot * (P::TILE >> 4);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (ok && active(t, j)) {
-              ok = wait_for(&p_full[t], pn[t] & 1);
-              tc_fence_after();
-              if (ok) values(t, sv, pn[t] == 0);
-              ++pn[t];
-            }
-            // the scores of the next tile overwrite P: issued behind the product that reads it
-            if (ok && j + 1 < je && active(t, j + 1)) {
-              if (!have_next) {
-                ok = wait_tile(i + 2);
-                have_next = true;
-                tc_fence_after();
-              }
-              if (ok) scores(t, sk);
-            }
+        for (int k = 0; k < kN / 16; ++k)
+          if ((k < kPart / 16) == (part == 0))
+            umma_f16_tmem_a_lead(to, ts + 8 * k, v0d + k * (2048 >> 4), id_o, first && k == 0 ? 0u : 1u, lead);
+        umma_commit_lead(&o_done[2 * part + t], lead);
+      };
+      auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
+      // the value tile of step i, through the warp that looks it over
+      auto wait_values = [&](int i) { return wait_for(&scanned[i % P::SLOTS], i / P::SLOTS); };
+      // The tiles' products are issued in turn, each tile's in one go: left to themselves the two
+      // softmaxes fall into step and compete for the same cycles, and the tensor cores wait.
+      auto pass_turn = [&]() {
+        if (lead) mbar_arrive(&turn[t ^ 1]);
+        __syncwarp();
+      };
+      int i0 = 0, nq = 0, n = 0, step = 0;   // ring tiles, query tiles, key tiles of this query tile, turns
+      Work w;
+      bool ok = true;
+      for (int nw = 0; ok && take(nw, w); ++nw) {
+        const Job job(a, w, tt);
+        give_back(nw);
+        const Range r = t ? job.r1 : job.r0;
+        if (job.je <= job.jb) continue;
+        ok = wait_for(q_full, nq);
+        ++nq;
+        if (ok && r.je <= r.jb && lead) mbar_arrive(q_empty);
+        __syncwarp();
+        for (int j = job.jb; ok && j < job.je; ++j, ++step) {
+          const int i = i0 + 2 * (j - job.jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
+          const bool mine = j >= r.jb && j < r.je, more = mine && j + 1 < r.je;
+          if (mine && j == r.jb) {
+            ok = wait_tile(i);
+            if (!ok) break;
+            tc_fence_after();
+            scores(i % P::SLOTS);
+            umma_commit_lead(&empty[i % P::SLOTS], lead);
+            if (!more) umma_commit_lead(q_empty, lead);
           }
+          // The waits for what is long there stand before those for the weights: each costs some
+          // 150 cycles all the same.
+          if (mine) ok = wait_values(i + 1) && (!more || wait_tile(i + 2)) && wait_for(&p_full[t], n);
+          else ok = wait_tile(i) && wait_tile(i + 1);
+          if (t == 1 || step > 0) ok = ok && wait_for(&turn[t], step - 1 + t);
           if (!ok) break;
-          umma_commit_lead(&empty[sv], lead);
-          if (j + 1 < je) {
-            if (!have_next && !wait_tile(i + 2)) break;
-            umma_commit_lead(&empty[sk], lead);
+          if (!mine) {                     // the other query tile's keys only
+            pass_turn();
+            if (lead) {
+              mbar_arrive(&empty[i % P::SLOTS]);
+              mbar_arrive(&empty[sv]);
+            }
+            __syncwarp();
+            continue;
           }
+          tc_fence_after();
+          values(sv, 0, j == r.jb);
+          ok = wait_for(&p_full[2 + t], n);
+          if (!ok) break;
+          tc_fence_after();
+          values(sv, 1, false);
+          ++n;
+          if (more) scores(sk);   // overwrites P: issued behind the product that reads it
+          pass_turn();
+          umma_commit_lead(&empty[sv], lead);
+          if (more) umma_commit_lead(&empty[sk], lead);
+          if (more && j + 2 == r.je) umma_commit_lead(q_empty, lead);
         }
+        i0 += 2 * (job.je - job.jb);
       }
     } else {
       // ---- values that some token does not see: 0 x NaN or 0 x infinity in P V would reach
       // its result.  In the tiles where that can happen, rows behind the sequence's end are
       // zeroed, and elements that are not finite are zeroed and noted; the epilogue adds them
       // back for the tokens that see them.
-      const int w = warp - kScanWarp;
-      for (int j = jb; j < je; ++j) {
-        const int i = 2 * (j - jb) + 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_inline(&full[i % P::SLOTS], (i / P::SLOTS) & 1, abort_flag, status,
-                                                       limit_ns) ? 1 : 0))
-          break;
-        uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
-        const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
-        bool touched = false;
-        for (int e = w * 32 + lane; special(j) && e < P::TILE / 16; e += 32 * kScanWarps) {
-          const int row = (e % (P::HALF / 16)) / 8;   // key of this 16-byte piece
-          if (j * kN + row >= k_len) {
-            tile[e] = make_uint4(0, 0, 0, 0);
-            touched = true;
-            continue;
-          }
-          uint4 x = tile[e];
-          uint32_t u[4] = {x.x, x.y, x.z, x.w};
-          bool bad = false;
+      const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
+      int i0 = 0;
+      Work w;
+      bool ok = true;
+      for (int nw = 0; ok && take(nw, w); ++nw) {
+        const Job job(a, w, tt);
+        for (int j = job.jb; j < job.je; ++j) {
+          const int i = i0 + 2 * (j - job.jb) + 1;
+          ok = wait_for(&full[i % P::SLOTS], i / P::SLOTS);
+          if (!ok) break;
+          if (job.special(j)) {
+            uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
+            const int rows = w.k_len - j * kN;
+            uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
+            bool touched = false;
+#pragma unroll 8
+            for (int e = lane; e < P::TILE / 16; e += 32) {
+              if ((e % (P::HALF / 16)) / 8 < rows) {
+                const uint4 x = tile[e];
+                top = max_abs2<DT>(max_abs2<DT>(top, x.x), max_abs2<DT>(x.y, max_abs2<DT>(x.z, x.w)));
+              } else {
+                tile[e] = make_uint4(0, 0, 0, 0);
+                touched = true;
+              }
+            }
+            if (__any_sync(0xffffffffu, (top & expo) == expo || ((top >> 16) & expo) == expo)) {
+              for (int e = lane; e < P::TILE / 16; e += 32) {
+                if ((e % (P::HALF / 16)) / 8 >= rows) continue;
+                uint4 x = tile[e];
+                uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const bool b0 = (u[y] & expo) == expo, b1 = ((u[y] >> 16) & expo) == expo;
-            bad |= b0 | b1;
-            u[y] &= (b0 ? 0xffff0000u : 0xffffffffu) & (b1 ? 0x0000ffffu : 0xffffffffu);
+                for (int y = 0; y < 4; ++y)
+                  u[y] &= ((u[y] & expo) == expo ? 0xffff0000u : 0xffffffffu) &
+                          (((u[y] >> 16) & expo) == expo ? 0x0000ffffu : 0xffffffffu);
+                tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
+              }
+              touched = true;
+              *reinterpret_cast<volatile int*>(&works[nw & 1].poison) = 1;
+            }
+            if (touched) fence_proxy_async_smem();
+            __syncwarp();
           }
-          if (bad) {
-            tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
-            *poison = 1;
-            touched = true;
-          }
+          if (lane == 0) mbar_arrive(&scanned[i % P::SLOTS]);
         }
-        if (touched) fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&scanned[i % P::SLOTS]);
+        i0 += 2 * (job.je - job.jb);
+        give_back(nw);
       }
     }
-    } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-      // ---- softmax: thread r of the four warps owns row r of its query tile
-      const int t = warp >> 2, row = 32 * (warp & 3) + lane;
-      const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-      const uint32_t sc = lanes + (t ? kS1 : kS0), oc = lanes + (t ? kO1 : kO0);
-      const int tok = tok0 + t * tt + row / gp, head = h0 + row % gp;
-      const bool valid = tok < q_len;
-      const int tok_c = valid ? tok : q_len - 1;
-      int lo, hi;
-      visible_range(tok_c + shift, k_len, a.causal, a.window, lo, hi);
-      const TileKeys r = t ? r1 : r0;
-      // the tile's own tokens: the last one's first key, the first one's last
-      int lo_max, hi_min;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ---- softmax: thread r of the four warps owns row r of its query tile
+    const int t = warp >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t sc = lanes + (t ? kS1 : kS0), oc = lanes + (t ? kO1 : kO0);
+    const float s2 = a.scale * kLog2e;
+    const uint64_t s22 = pair(s2, s2);
+    uint8_t* out_stage = stage + warp * P::STAGE;
+    int cnt = 0;   // key tiles of this query tile so far
+    bool ok = true;
+    for (int nw = 0; ok; ++nw) {
+      Range r;
+      int lo, hi, lo_max, hi_min;
       {
+        Work w;
+        if (!take(nw, w)) break;
+        const Job job(a, w, tt);
+        r = t ? job.r1 : job.r0;
+        const int shift = w.k_len - w.q_len, tile0 = w.tok0 + t * tt;   // the query tile's first token
         int x;
-        const int ta = tok0 + t * tt < q_len ? tok0 + t * tt : q_len - 1;
-        const int tb = (tok0 + (t + 1) * tt < q_len ? tok0 + (t + 1) * tt : q_len) - 1;
-        visible_range(tb + shift, k_len, a.causal, a.window, lo_max, x);
-        visible_range(ta + shift, k_len, a.causal, a.window, x, hi_min);
+        const int tok = min(tile0 + (row >> gp_shift), w.q_len - 1);
+        visible_range(tok + shift, w.k_len, a.causal, a.window, lo, hi);
+        // the tile's own tokens: the last one's first key, the first one's last
+        visible_range(min(tile0 + tt, w.q_len) - 1 + shift, w.k_len, a.causal, a.window, lo_max, x);
+        visible_range(min(tile0, w.q_len - 1) + shift, w.k_len, a.causal, a.window, x, hi_min);
       }
-      const float s2 = a.scale * kLog2e;
       float m = -INFINITY, l = 0.0f;       // reference maximum (of the raw scores) and sum
-      bool ok = true;
-      for (int j = r.jb; j < r.je; ++j) {
-        const int it = j - r.jb;
-        ok = __all_sync(0xffffffffu, mbar_wait_inline(&s_full[t], it & 1, abort_flag, status, limit_ns) ? 1 : 0);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t x[128];
+      auto weights = [&](const uint32_t (&x)[32], uint32_t* p, uint64_t off2, uint64_t (&sum)[2]) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(sc + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
-        tmem_ld_wait();
-        if (j * kN < lo_max || (j + 1) * kN > hi_min) {
-          const int a0 = lo - j * kN, a1 = hi - j * kN;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < a0 || i >= a1) x[i] = 0xff800000u;   // -inf
+        for (int i = 0; i < 16; ++i) {
+          const float2 z = unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), s22, off2));
+          const float p0 = ex2(z.x), p1 = ex2(z.y);
+          sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+          p[i] = pack2<DT>(p0, p1);    // the weights of the product are rounded; the sum is not
         }
-        float mx8[8];   // independent chains: a single one would be 64 dependent steps
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 8]));
-#pragma unroll
-        for (int i = 16; i < 128; i += 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx8[e] = max3(mx8[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 8 + e]));
-        const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        // the reference follows the maximum only when it is far behind: weights stay below 2^8
-        bool move = false;
-        float f = 1.0f;
-        if (mx > m && (m == -INFINITY || (mx - m) * s2 > kLazy)) {
-          move = true;
-          f = m == -INFINITY ? 0.0f : ex2((m - mx) * s2);
-          m = mx;
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          l *= f;
-          if (it > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_inline(&o_done[t], (it - 1) & 1, abort_flag, status, limit_ns) ? 1 : 0);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) {
-              uint32_t y[16];
-              tmem_ld_32x32b_x16(oc + 16 * b, y);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              tmem_st_32x32b_x16(oc + 16 * b, y);
-            }
-          }
-        }
-        const float off = m == -INFINITY ? 0.0f : m * s2;
-        const uint64_t s22 = pair(s2, s2), off2 = pair(-off, -off);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 y = unpair(fma2(pair(__uint_as_float(x[32 * b + 2 * i]), __uint_as_float(x[32 * b + 2 * i + 1])),
-                                         s22, off2));
-            const float p0 = ex2(y.x), p1 = ex2(y.y);
-            sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
-            p[i] = pack2<DT>(p0, p1);    // the weights of the product are rounded; the sum is not
-          }
-          tmem_st_32x32b_x16(sc + 16 * b, p);
-        }
-        const float2 total = unpair(add2(sum[0], sum[1]));
-        l += total.x + total.y;
+      };
+      auto offset = [&]() {
+        const float off = m == -INFINITY ? 0.0f : -m * s2;
+        return pair(off, off);
+      };
+      auto add_sum = [&](const uint64_t (&sum)[2]) {
+        const float2 u = unpair(add2(sum[0], sum[1]));
+        l += u.x + u.y;
+      };
+      auto publish = [&](int part) {
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (lane == 0) mbar_arrive(&p_full[2 * part + t]);
+      };
+      // The 32-key pieces [b0, b1) of a tile by the book: the maximum first, the reference moved to it
+      // (O and l brought along) where it is far behind, then the weights.  P of piece b lies where
+      // scores of pieces up to b were, which have been read.
+      auto careful = [&](bool masked, bool first, int part, int b0, int b1, int key0) {
+        uint32_t y[32];
+        auto piece = [&](int b) {
+          tmem_ld_32x32b_x32(sc + 32 * b, y);
+          tmem_ld_wait();
+          if (masked) {
+            const int a0 = lo - key0 - 32 * b, a1 = hi - key0 - 32 * b;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < a0 || i >= a1) y[i] = 0xff800000u;   // -inf
+          }
+        };
+        float mx = m;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+          piece(b);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+        }
+        const bool move = mx > m && (m == -INFINITY || (mx - m) * s2 > 8.0f);
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mx) * s2);
+          if (move) m = mx;
+          l *= f;
+          if (!first) {                  // behind the product of the part before
+            ok = wait_for(&o_done[2 * (part ^ 1) + t], cnt + part - 1);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < D / 32; ++b) {
+              tmem_ld_32x32b_x32(oc + 32 * b, y);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              tmem_st_32x32b_x32(oc + 32 * b, y);
+            }
+          }
+        }
+        const uint64_t off2 = offset();
+        uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+          uint32_t p[16];
+          piece(b);
+          weights(y, p, off2, sum);
+          tmem_st_32x32b_x16(sc + 16 * b, p);
+        }
+        add_sum(sum);
+        publish(part);
+      };
+      // Keys that every token of the tile sees: the weights against the reference of before, with no
+      // maximum looked for.  Rounding does not depend on the reference, so it may stay far behind;
+      // only when the weights' sum is too large for their type, the keys go by the book.
+      auto fast = [&](auto& x, int part, int b0, int key0) {
+        constexpr int N = sizeof(x) / 4;
+        uint32_t p[N / 2];
+        const uint64_t off2 = offset();
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int b = 0; b < N / 32; ++b) weights(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * b), p + 16 * b, off2, sum);
+        const float2 u = unpair(add2(sum[0], sum[1]));
+        const float total = u.x + u.y;
+        if (__any_sync(0xffffffffu, m == -INFINITY || total > kMostWeight<DT>)) {
+          careful(false, false, part, b0, b0 + N / 32, key0);
+          return;
+        }
+        l += total;
+#pragma unroll
+        for (int b = 0; b < N / 32; ++b)
+          tmem_st_32x32b_x16(sc + 16 * (b0 + b), *reinterpret_cast<uint32_t(*)[16]>(p + 16 * b));
+        publish(part);
+      };
+      for (int j = r.jb; j < r.je; ++j, ++cnt) {
+        ok = wait_for(&s_full[t], cnt);
+        if (!ok) break;
+        tc_fence_after();
+        const bool masked = j * kN < lo_max || (j + 1) * kN > hi_min;
+        if (masked || j == r.jb) {
+#pragma unroll 1
+          for (int part = 0; ok && part < 2; ++part)
+            careful(masked, j == r.jb && part == 0, part, part ? kPart / 32 : 0, part ? kN / 32 : kPart / 32, j * kN);
+        } else {
+          uint32_t xa[kPart], xb[kN - kPart];
+#pragma unroll
+          for (int b = 0; b < kPart / 32; ++b)
+            tmem_ld_32x32b_x32(sc + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(xa + 32 * b));
+          tmem_ld_wait();
+#pragma unroll
+          for (int b = 0; b < (kN - kPart) / 32; ++b)
+            tmem_ld_32x32b_x32(sc + kPart + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(xb + 32 * b));
+          fast(xa, 0, 0, j * kN);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kN - kPart; ++i) asm volatile("" : "+r"(xb[i]));   // not before the wait
+          if (ok) fast(xb, 1, kPart / 32, j * kN);
+        }
+        if (!ok) break;
       }
       // ---- epilogue
-      const int n = r.je - r.jb;
-      if (ok && n > 0)
-        ok = __all_sync(0xffffffffu, mbar_wait_inline(&o_done[t], (n - 1) & 1, abort_flag, status, limit_ns) ? 1 : 0);
+      const bool any = r.je > r.jb;
+      if (ok && any) ok = wait_for(&o_done[2 + t], cnt - 1);
+      if (!ok) break;
       tc_fence_after();
-      if (ok) {
-        const bool empty_row = hi <= lo;
-        const float inv = empty_row ? 0.0f : 1.0f / l;
-        uint16_t* out = o + (size_t)(q0 + tok_c) * a.o_token + (size_t)head * a.o_head;
+      const Work w = works[nw & 1];   // read again: its registers are better used above
+      const int tile0 = w.tok0 + t * tt;
+      const bool empty_row = hi <= lo;
+      const float inv = empty_row ? 0.0f : 1.0f / l;
+      const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
+#pragma unroll 1
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t y[32];
+        __syncwarp();
+        if (any) {
+          tmem_ld_32x32b_x32(oc + 32 * b, y);
+          tmem_ld_wait();
+        }
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
-          uint32_t y[32];
-          __syncwarp();
-          if (n > 0) {
-            tmem_ld_32x32b_x32(oc + 32 * b, y);
-            tmem_ld_wait();
-          }
-          if (!valid) continue;
-          if (empty_row) {
+        for (int i = 0; i < 32; ++i) y[i] = empty_row ? 0u : __float_as_uint(__uint_as_float(y[i]) * inv);
+        if (w.poison && !empty_row) {
+          const Job job(a, w, tt);
+          for (int j = job.jb; j < job.je; ++j) {
+            if (!job.special(j)) continue;
+            const int ka = j * kN > lo ? j * kN : lo, kb = (j + 1) * kN < hi ? (j + 1) * kN : hi;
+            for (int key = ka; key < kb; ++key) {
+              const uint16_t* vr = v + (size_t)(w.k0 + key) * a.v_token + (size_t)hk * a.v_head + 32 * b;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = 0;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * inv);
-            if (*poison) {
-              for (int j = jb; j < je; ++j) {
-                if (!special(j)) continue;
-                const int ka = j * kN > lo ? j * kN : lo, kb = (j + 1) * kN < hi ? (j + 1) * kN : hi;
-                for (int key = ka; key < kb; ++key) {
-                  const uint16_t* vr = v + (size_t)(k0 + key) * a.v_token + (size_t)hk * a.v_head + 32 * b;
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    const float z = bits_to_float<DT>(vr[i]);
-                    if (!isfinite(z)) y[i] = __float_as_uint(__uint_as_float(y[i]) + z);
-                  }
-                }
+              for (int i = 0; i < 32; ++i) {
+                const float z = bits_to_float<DT>(vr[i]);
+                if (!isfinite(z)) y[i] = __float_as_uint(__uint_as_float(y[i]) + z);
               }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(out + 32 * b + i) =
-                make_uint4(pack2<DT>(__uint_as_float(y[i]), __uint_as_float(y[i + 1])),
-                           pack2<DT>(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])),
-                           pack2<DT>(__uint_as_float(y[i + 4]), __uint_as_float(y[i + 5])),
-                           pack2<DT>(__uint_as_float(y[i + 6]), __uint_as_float(y[i + 7])));
         }
-        if (lse && valid)
-          lse[(size_t)(q0 + tok) * a.n_heads + head] = empty_row ? -INFINITY : m * s2 * kLn2 + logf(l);
+        // through shared memory, so that four lanes store 64 bytes of one row (a thread's own row
+        // would touch 32 lines with every store)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(out_stage + 64 * lane + 16 * (i ^ ((lane >> 1) & 3))) =
+              make_uint4(pack2<DT>(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
+                         pack2<DT>(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
+                         pack2<DT>(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
+                         pack2<DT>(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 8 * i + (lane >> 2), gr = 32 * (warp & 3) + rr;   // row of the warp, of the tile
+          const int tok = tile0 + (gr >> gp_shift), head = w.h0 + (gr & (gp - 1));
+          if (tok < w.q_len)
+            *reinterpret_cast<uint4*>(o + (size_t)(w.q0 + tok) * a.o_token + (size_t)head * a.o_head + 32 * b +
+                                      8 * (lane & 3)) =
+                *reinterpret_cast<const uint4*>(out_stage + 64 * rr + 16 * ((lane & 3) ^ ((rr >> 1) & 3)));
+        }
       }
+      const int tok = tile0 + (row >> gp_shift);
+      if (lse && tok < w.q_len)
+        lse[(size_t)(w.q0 + tok) * a.n_heads + w.h0 + (row & (gp - 1))] = empty_row ? -INFINITY : m * s2 * kLn2 + logf(l);
+      tc_fence_before();
+      give_back(nw);
     }
   }
 
@@ -540,14 +803,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag && tid == 0) {
     // a wait gave up: the loads and tensor-core work already issued complete before the CTA exits
+    if (*q_issued > 0) mbar_wait_drain(q_full, (*q_issued - 1) & 1, status);
     const int n = *issued;
-    if (n > 0) mbar_wait_drain(q_full, 0, status);
     for (int i = n - P::SLOTS > 0 ? n - P::SLOTS : 0; i < n; ++i)
       mbar_wait_drain(&full[i % P::SLOTS], (i / P::SLOTS) & 1, status);
+    if (*asked > 0) mbar_wait_drain(answered, (*asked - 1) & 1, status);
   }
-  if (*abort_flag && warp == kMmaWarp && lane == 0) {
-    umma_commit(drain);
-    mbar_wait_drain(drain, 0, status);
+  if (*abort_flag && (warp == kMmaWarp || warp == kMmaWarp + 1) && lane == 0) {
+    uint64_t* d = drain + (warp - kMmaWarp);
+    umma_commit(d);
+    mbar_wait_drain(d, 0, status);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -574,12 +839,14 @@ bool launch_tc(const qre_attn& a, int n_seqs, int total_q, int total_k, const in
       !make_tmap_rows16(&tv, v, total_k, stride(a.v_token, total_k), vm ? a.n_kv_heads : 1, stride(a.v_head, vm ? a.n_kv_heads : 1), D, 1, kN))
     return false;
   const int groups = a.n_heads / gp, pair = 2 * kM / gp;
+  int gp_shift = 0;
+  while ((1 << gp_shift) < gp) ++gp_shift;
   const long long blocks = ((long long)total_q / pair + (n_seqs < total_q ? n_seqs : total_q)) * groups;
   auto kernel = attn_tc_kernel<DT, D>;
   *err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), Plan<D>::BYTES);
   if (*err != cudaSuccess) return true;
   *err = launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), (size_t)Plan<D>::BYTES, stream, a, n_seqs,
-                          total_q, total_k, gp, groups, cu_q, cu_k, tq, tk, tv, qm, km, vm,
+                          total_q, total_k, gp_shift, groups, cu_q, cu_k, tq, tk, tv, qm, km, vm,
                           static_cast<const uint16_t*>(v), static_cast<uint16_t*>(o), lse, wait_limit_ns(), status);
   return true;
 }

@@ -229,4 +229,31 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- work of CTAs not yet launched
+
+// Asks for the work of a CTA of this grid that has not been launched: a 16-byte
+// answer is written to dst and counted on `bar`.
+__device__ __forceinline__ void ask_next_cta(void* dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_addr(dst)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The answer: the x index of the CTA that will not be launched, or -1.
+__device__ __forceinline__ int next_cta(const void* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return got ? (int)x : -1;
+}
+
 }  // namespace qre
