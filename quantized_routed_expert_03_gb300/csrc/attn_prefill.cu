@@ -91,11 +91,12 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
 constexpr int kM = 128;            // rows of a query tile: kM / gp tokens x gp heads of one KV head
 constexpr int kN = 128;            // keys of a tile
 constexpr int kPart = 96;          // keys of a tile's first part (of two): P V of it starts while the rest is weighted
-constexpr int kThreads = 384;
-// warps 0-3: softmax of tile 0, 4-7: of tile 1
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScanWarp = 11;   // MMA warps 9 and 10: one per query tile
-// Registers: 384 x 168 at launch = 256 x 208 + 128 x 88.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kThreads = 512;
+// warps 0-3: softmax of tile 0, 4-7: of tile 1, 8-11: output of both
+constexpr int kStoreWarp = 8;
+constexpr int kTmaWarp = 12, kMmaWarp = 13;   // MMA warps 13 and 14: one per query tile; 15 fills the warpgroup
+// Registers: 512 x 128 at launch = 256 x 160 + 128 x 112 + 128 x 80.
+constexpr int kSoftmaxRegs = 160, kStoreRegs = 112, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384;   // tensor-memory columns; P overwrites its S
 // A row's weights are taken against a reference that stays while their sum is at
@@ -108,8 +109,7 @@ struct Plan {
   static constexpr int HALF = kN * 128;              // 64 columns of a 128-row tile, 128-byte rows
   static constexpr int TILE = HALF * (D / 64);
   static constexpr int SLOTS = D == 128 ? 4 : 8;     // K and V tiles in flight
-  static constexpr int STAGE = 32 * 64;              // output rows of a softmax warp on their way out: 32 columns
-  static constexpr int BYTES = 1024 + 2 * TILE + SLOTS * TILE + 8 * STAGE + 1024;
+  static constexpr int BYTES = 2 * TILE + SLOTS * TILE + 2 * HALF + 2048 + 768;   // stage; sums; barriers
 };
 
 // mbar_wait_bounded without a call: the register split (setmaxnreg) leaves no room for the calling convention.
@@ -290,32 +290,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q, int total_k, int gp_shift, int groups,
                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, int q_heads_move, int k_heads_move, int v_heads_move,
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                   int store_o, int q_heads_move, int k_heads_move, int v_heads_move,
                    const uint16_t* __restrict__ v, uint16_t* __restrict__ o, float* __restrict__ lse,
                    uint64_t limit_ns, int* status) {
   using P = Plan<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle goes by addresses; no static shared memory beside it
   uint8_t* sq = smem;                       // two query tiles
   uint8_t* skv = smem + 2 * P::TILE;        // ring of key and value tiles
-  uint8_t* stage = skv + P::SLOTS * P::TILE;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(stage + 8 * P::STAGE);
+  uint8_t* stage = skv + P::SLOTS * P::TILE;   // [2]: 64 columns of a query tile's output on their way out
+  uint64_t* bar = reinterpret_cast<uint64_t*>(stage + 2 * P::HALF);
   uint64_t* answer = bar;                   // [2], 16-byte aligned
   uint64_t* full = answer + 2;              // [SLOTS]
   uint64_t* empty = full + P::SLOTS;        // [SLOTS]
-  uint64_t* scanned = empty + P::SLOTS;     // [SLOTS]
-  uint64_t* q_full = scanned + P::SLOTS;
+  uint64_t* q_full = empty + P::SLOTS;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;           // [2]
   uint64_t* p_full = s_full + 2;            // [part][2]: one phase of each per key tile
   uint64_t* o_done = p_full + 4;            // [part][2]
-  uint64_t* turn = o_done + 4;              // [2]: the MMA warps issue in turn
-  uint64_t* work_full = turn + 2;           // [2]
+  uint64_t* work_full = o_done + 4;         // [2]
   uint64_t* work_empty = work_full + 2;     // [2]
-  uint64_t* answered = work_empty + 2;
+  uint64_t* sums_full = work_empty + 2;     // [2]: a query tile's sums and maxima are there
+  uint64_t* o_free = sums_full + 2;         // [2]: its output (and they) have been read
+  uint64_t* stage_ready = o_free + 2;       // [2], of the two halves of the stage in turn: a warp comes back to one
+  uint64_t* stage_free = stage_ready + 2;   // only behind stage_free, so it cannot count twice for a round
+  uint64_t* answered = stage_free + 1;
   uint64_t* drain = answered + 1;           // [2]
   Work* works = reinterpret_cast<Work*>(drain + 2);          // [2]
-  uint32_t* tmem_p = reinterpret_cast<uint32_t*>(works + 2);
+  float2* sums = reinterpret_cast<float2*>(works + 2);       // [2][kM]: (l, m in base 2) of the rows
+  uint32_t* tmem_p = reinterpret_cast<uint32_t*>(sums + 2 * kM);
   int* misc = reinterpret_cast<int*>(tmem_p + 1);
   volatile int* abort_flag = misc;          // a wait gave up
   int* issued = misc + 1;                   // ring tiles whose loads were issued
@@ -329,21 +332,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < P::SLOTS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 2);
-      mbar_init(&scanned[s], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(&p_full[2 * h + t], 4);
+        mbar_init(&p_full[2 * h + t], h ? 4 : 5);   // four warps, and the other tile's MMA warp
         mbar_init(&o_done[2 * h + t], 1);
       }
-      mbar_init(&turn[t], 1);
+      mbar_init(&sums_full[t], 4);
+      mbar_init(&o_free[t], 4);
       mbar_init(&work_full[t], 1);
-      mbar_init(&work_empty[t], kThreads / 32 - 1);
+      mbar_init(&work_empty[t], kMmaWarp + 2 - 1);   // all warps but the one that finds the work and the last
       mbar_init(&drain[t], 1);
     }
+    mbar_init(&stage_ready[0], 4);
+    mbar_init(&stage_ready[1], 4);
+    mbar_init(stage_free, 1);
     mbar_init(answered, 1);
     *abort_flag = 0;
     *issued = *q_issued = *asked = 0;
@@ -443,13 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();   // read before the next answer is written
         __syncwarp();
       }
-    } else if (warp < kScanWarp) {
+    } else if (warp < kMmaWarp + 2) {
       // ---- MMA: the whole warp, so that the operands stay in uniform registers
       const int t = warp - kMmaWarp;
       const uint32_t lead = elect_lane();
       const uint32_t id_s = DT == QRE_BF16 ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
       const uint32_t id_o = (DT == QRE_BF16 ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + (t ? kS1 : kS0), to = tm + (t ? kO1 : kO0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + (t ? kS1 : kS0), td = tm + (t ? kO1 : kO0);
       const uint64_t qd = umma_desc_sw128(smem_addr(sq + t * P::TILE)), kd = umma_desc_sw128(smem_addr(skv));
       const uint64_t vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
       auto scores = [&](int slot) {      // S = Q K_j^T
@@ -466,33 +472,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kN / 16; ++k)
           if ((k < kPart / 16) == (part == 0))
-            umma_f16_tmem_a_lead(to, ts + 8 * k, v0d + k * (2048 >> 4), id_o, first && k == 0 ? 0u : 1u, lead);
+            umma_f16_tmem_a_lead(td, ts + 8 * k, v0d + k * (2048 >> 4), id_o, first && k == 0 ? 0u : 1u, lead);
         umma_commit_lead(&o_done[2 * part + t], lead);
       };
       auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
-      // the value tile of step i, through the warp that looks it over
-      auto wait_values = [&](int i) { return wait_for(&scanned[i % P::SLOTS], i / P::SLOTS); };
       // The tiles' products are issued in turn, each tile's in one go: left to themselves the two
-      // softmaxes fall into step and compete for the same cycles, and the tensor cores wait.
-      auto pass_turn = [&]() {
-        if (lead) mbar_arrive(&turn[t ^ 1]);
+      // softmaxes fall into step and compete for the same cycles, and the tensor cores wait.  The
+      // turn is one more arrival on the barrier of the first weights: a wait of its own would
+      // cost some 200 cycles, as every wait here does, next to the tensor cores' reads.
+      auto turn_to = [&](int tile) {
+        if (lead) mbar_arrive(&p_full[tile]);
         __syncwarp();
       };
-      int i0 = 0, nq = 0, n = 0, step = 0;   // ring tiles, query tiles, key tiles of this query tile, turns
+      // ring tiles, query tiles, key tiles of this query tile, pieces with keys for this query tile
+      int i0 = 0, nq = 0, n = 0, no = 0;
       Work w;
       bool ok = true;
       for (int nw = 0; ok && take(nw, w); ++nw) {
         const Job job(a, w, tt);
         give_back(nw);
-        const Range r = t ? job.r1 : job.r0;
+        const Range r = t ? job.r1 : job.r0, other = t ? job.r0 : job.r1;
         if (job.je <= job.jb) continue;
         ok = wait_for(q_full, nq);
         ++nq;
         if (ok && r.je <= r.jb && lead) mbar_arrive(q_empty);
         __syncwarp();
-        for (int j = job.jb; ok && j < job.je; ++j, ++step) {
+        for (int j = job.jb; ok && j < job.je; ++j) {
           const int i = i0 + 2 * (j - job.jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
           const bool mine = j >= r.jb && j < r.je, more = mine && j + 1 < r.je;
+          // turns go tile 0, tile 1, tile 0, ... by key tile; with no step of the other tile before
+          // it, a step has its turn of itself
+          const int next = j + t, last = j - 1 + t;
+          const bool pass = next >= other.jb && next < other.je;
+          const bool own = last < other.jb || last >= other.je;
           if (mine && j == r.jb) {
             ok = wait_tile(i);
             if (!ok) break;
@@ -501,14 +513,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit_lead(&empty[i % P::SLOTS], lead);
             if (!more) umma_commit_lead(q_empty, lead);
           }
-          // The waits for what is long there stand before those for the weights: each costs some
-          // 150 cycles all the same.
-          if (mine) ok = wait_values(i + 1) && (!more || wait_tile(i + 2)) && wait_for(&p_full[t], n);
-          else ok = wait_tile(i) && wait_tile(i + 1);
-          if (t == 1 || step > 0) ok = ok && wait_for(&turn[t], step - 1 + t);
+          // The waits for what is long there stand before the one for the weights.
+          ok = mine ? wait_tile(i + 1) && (!more || wait_tile(i + 2)) : wait_tile(i) && wait_tile(i + 1);
+          if (ok && mine && j == r.jb) {   // the output of the piece before has been read
+            ok = no == 0 || wait_for(&o_free[t], no - 1);
+            ++no;
+          }
+          if (ok && mine && own) turn_to(t);
+          if (ok && mine) ok = wait_for(&p_full[t], n);
           if (!ok) break;
           if (!mine) {                     // the other query tile's keys only
-            pass_turn();
             if (lead) {
               mbar_arrive(&empty[i % P::SLOTS]);
               mbar_arrive(&empty[sv]);
@@ -524,66 +538,127 @@ __global__ void __launch_bounds__(kThreads, 1)
           values(sv, 1, false);
           ++n;
           if (more) scores(sk);   // overwrites P: issued behind the product that reads it
-          pass_turn();
+          if (pass) turn_to(t ^ 1);
           umma_commit_lead(&empty[sv], lead);
           if (more) umma_commit_lead(&empty[sk], lead);
           if (more && j + 2 == r.je) umma_commit_lead(q_empty, lead);
         }
         i0 += 2 * (job.je - job.jb);
       }
-    } else {
-      // ---- values that some token does not see: 0 x NaN or 0 x infinity in P V would reach
-      // its result.  In the tiles where that can happen, rows behind the sequence's end are
-      // zeroed, and elements that are not finite are zeroed and noted; the epilogue adds them
-      // back for the tokens that see them.
-      const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
-      int i0 = 0;
-      Work w;
-      bool ok = true;
-      for (int nw = 0; ok && take(nw, w); ++nw) {
-        const Job job(a, w, tt);
-        for (int j = job.jb; j < job.je; ++j) {
-          const int i = i0 + 2 * (j - job.jb) + 1;
-          ok = wait_for(&full[i % P::SLOTS], i / P::SLOTS);
-          if (!ok) break;
-          if (job.special(j)) {
-            uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
-            const int rows = w.k_len - j * kN;
-            uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
-            bool touched = false;
-#pragma unroll 8
-            for (int e = lane; e < P::TILE / 16; e += 32) {
-              if ((e % (P::HALF / 16)) / 8 < rows) {
-                const uint4 x = tile[e];
-                top = max_abs2<DT>(max_abs2<DT>(top, x.x), max_abs2<DT>(x.y, max_abs2<DT>(x.z, x.w)));
-              } else {
-                tile[e] = make_uint4(0, 0, 0, 0);
-                touched = true;
-              }
-            }
-            if (__any_sync(0xffffffffu, (top & expo) == expo || ((top >> 16) & expo) == expo)) {
-              for (int e = lane; e < P::TILE / 16; e += 32) {
-                if ((e % (P::HALF / 16)) / 8 >= rows) continue;
-                uint4 x = tile[e];
-                uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  u[y] &= ((u[y] & expo) == expo ? 0xffff0000u : 0xffffffffu) &
-                          (((u[y] >> 16) & expo) == expo ? 0x0000ffffu : 0xffffffffu);
-                tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
-              }
-              touched = true;
-              *reinterpret_cast<volatile int*>(&works[nw & 1].poison) = 1;
-            }
-            if (touched) fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(&scanned[i % P::SLOTS]);
-        }
-        i0 += 2 * (job.je - job.jb);
-        give_back(nw);
-      }
     }
+  } else if (warp >= kStoreWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kStoreRegs));
+    // ---- output: o = O / l.  Warps of their own, because what leaves an SM leaves slowly: the softmax
+    // goes on with the next piece of work meanwhile.  A full tile goes through shared memory by
+    // TMA, 64 columns at a time; the last tile of a sequence by stores of each row's own thread.
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const bool issuer = warp == kStoreWarp && lane == 0;
+    int cnt[2] = {0, 0}, no[2] = {0, 0}, rounds = 0;
+    bool ok = true;
+    Work w;
+    for (int nw = 0; ok && take(nw, w); ++nw) {
+      const Job job(a, w, tt);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const Range r = t ? job.r1 : job.r0;
+        const int tile0 = w.tok0 + t * tt;
+        if (!ok || tile0 >= w.q_len) continue;
+        const bool any = r.je > r.jb;
+        float2 sum = make_float2(0.0f, 0.0f);
+        if (any) {
+          cnt[t] += r.je - r.jb;
+          ok = wait_for(&sums_full[t], no[t]) && wait_for(&o_done[2 + t], cnt[t] - 1);
+          if (!ok) continue;
+          tc_fence_after();
+          sum = sums[t * kM + row];
+        }
+        const int tok = tile0 + (row >> gp_shift), head = w.h0 + (row & (gp - 1));
+        const bool valid = tok < w.q_len;
+        int lo, hi;
+        visible_range(min(tok, w.q_len - 1) + w.k_len - w.q_len, w.k_len, a.causal, a.window, lo, hi);
+        const bool empty_row = hi <= lo;
+        const float inv = empty_row ? 0.0f : 1.0f / sum.x;
+        if (lse && valid)
+          lse[(size_t)(w.q0 + tok) * a.n_heads + head] = empty_row ? -INFINITY : sum.y * kLn2 + logf(sum.x);
+        const bool full_tile = store_o && tile0 + tt <= w.q_len;
+        const bool poison = *reinterpret_cast<volatile int*>(&works[nw & 1].poison) != 0;
+        uint16_t* out = o + (size_t)(w.q0 + tok) * a.o_token + (size_t)head * a.o_head;
+        const uint32_t oc = lanes + (t ? kO1 : kO0);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t y[64];
+          if (any) {
+            tmem_ld_32x32b_x32(oc + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(y));
+            tmem_ld_32x32b_x32(oc + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(y + 32));
+            tmem_ld_wait();
+            if (c == D / 64 - 1) {       // the next piece may overwrite O and the sums
+              ++no[t];
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&o_free[t]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 64; ++i) y[i] = empty_row ? 0u : __float_as_uint(__uint_as_float(y[i]) * inv);
+          if (poison && !empty_row) {
+            const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
+            for (int j = job.jb; j < job.je; ++j) {
+              if (!job.special(j)) continue;
+              const int ka = j * kN > lo ? j * kN : lo, kb = (j + 1) * kN < hi ? (j + 1) * kN : hi;
+              for (int key = ka; key < kb; ++key) {
+                const uint16_t* vr = v + (size_t)(w.k0 + key) * a.v_token + (size_t)hk * a.v_head + 64 * c;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                  const float z = bits_to_float<DT>(vr[i]);
+                  if (!isfinite(z)) y[i] = __float_as_uint(__uint_as_float(y[i]) + z);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = pack2<DT>(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+          __syncwarp();
+          if (full_tile) {
+            // the store two rounds before has read its half of the stage
+            if (rounds >= 2) {
+              if (issuer) {
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                mbar_arrive(stage_free);
+              }
+              __syncwarp();
+              ok = wait_for(stage_free, rounds - 2);
+              if (!ok) break;
+            }
+            uint8_t* half = stage + (rounds & 1) * P::HALF;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(half + row * 128 + 16 * (i ^ (row & 7))) =
+                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&stage_ready[rounds & 1]);
+            if (warp == kStoreWarp) {
+              ok = wait_for(&stage_ready[rounds & 1], rounds >> 1);
+              if (!ok) break;
+              if (issuer) {
+                tma_store_3d(&to, half, 64 * c, w.h0, w.q0 + tile0);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              }
+              __syncwarp();
+            }
+            ++rounds;
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(out + 64 * c + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          }
+          __syncwarp();
+        }
+      }
+      give_back(nw);
+    }
+    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax: thread r of the four warps owns row r of its query tile
@@ -592,26 +667,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sc = lanes + (t ? kS1 : kS0), oc = lanes + (t ? kO1 : kO0);
     const float s2 = a.scale * kLog2e;
     const uint64_t s22 = pair(s2, s2);
-    uint8_t* out_stage = stage + warp * P::STAGE;
-    int cnt = 0;   // key tiles of this query tile so far
+    int cnt = 0, no = 0;   // key tiles of this query tile so far, pieces of work with any
+    int i0 = 0;            // ring tiles so far
     bool ok = true;
     for (int nw = 0; ok; ++nw) {
       Range r;
-      int lo, hi, lo_max, hi_min;
+      int lo, hi, lo_max, hi_min, k_len, iv;   // iv: ring index of key tile 0's values
       {
         Work w;
         if (!take(nw, w)) break;
         const Job job(a, w, tt);
+        give_back(nw);
         r = t ? job.r1 : job.r0;
+        iv = i0 + 1 - 2 * job.jb;
+        i0 += 2 * (job.je - job.jb);
+        if (r.je <= r.jb) continue;
+        k_len = w.k_len;
         const int shift = w.k_len - w.q_len, tile0 = w.tok0 + t * tt;   // the query tile's first token
         int x;
         const int tok = min(tile0 + (row >> gp_shift), w.q_len - 1);
         visible_range(tok + shift, w.k_len, a.causal, a.window, lo, hi);
         // the tile's own tokens: the last one's first key, the first one's last
         visible_range(min(tile0 + tt, w.q_len) - 1 + shift, w.k_len, a.causal, a.window, lo_max, x);
-        visible_range(min(tile0, w.q_len - 1) + shift, w.k_len, a.causal, a.window, x, hi_min);
+        visible_range(tile0 + shift, w.k_len, a.causal, a.window, x, hi_min);
       }
       float m = -INFINITY, l = 0.0f;       // reference maximum (of the raw scores) and sum
+      bool started = false;                // a key tile has been through
       auto weights = [&](const uint32_t (&x)[32], uint32_t* p, uint64_t off2, uint64_t (&sum)[2]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -620,6 +701,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
           p[i] = pack2<DT>(p0, p1);    // the weights of the product are rounded; the sum is not
         }
+      };
+      // -inf for the keys of a piece (from key k0) that the row does not see
+      auto mask = [&](uint32_t (&x)[32], int k0) {
+        const int a0 = min(max(lo - k0, 0), 32), a1 = min(max(hi - k0, 0), 32);
+        // bits a0 .. a1 - 1 (64-bit shifts: a bound may be 32)
+        const uint32_t seen = (uint32_t)((1ull << a1) - 1) & ~(uint32_t)((1ull << a0) - 1);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(seen & (1u << i))) x[i] = 0xff800000u;
       };
       auto offset = [&]() {
         const float off = m == -INFINITY ? 0.0f : -m * s2;
@@ -638,17 +728,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The 32-key pieces [b0, b1) of a tile by the book: the maximum first, the reference moved to it
       // (O and l brought along) where it is far behind, then the weights.  P of piece b lies where
       // scores of pieces up to b were, which have been read.
-      auto careful = [&](bool masked, bool first, int part, int b0, int b1, int key0) {
+      auto careful = [&](bool masked, int part, int b0, int b1, int key0) {
         uint32_t y[32];
         auto piece = [&](int b) {
           tmem_ld_32x32b_x32(sc + 32 * b, y);
           tmem_ld_wait();
-          if (masked) {
-            const int a0 = lo - key0 - 32 * b, a1 = hi - key0 - 32 * b;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < a0 || i >= a1) y[i] = 0xff800000u;   // -inf
-          }
+          if (masked) mask(y, key0 + 32 * b);
         };
         float mx = m;
 #pragma unroll 1
@@ -662,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mx) * s2);
           if (move) m = mx;
           l *= f;
-          if (!first) {                  // behind the product of the part before
+          if (part || started) {         // behind the product of the part before
             ok = wait_for(&o_done[2 * (part ^ 1) + t], cnt + part - 1);
             if (!ok) return;
             tc_fence_after();
@@ -688,114 +773,153 @@ __global__ void __launch_bounds__(kThreads, 1)
         add_sum(sum);
         publish(part);
       };
-      // Keys that every token of the tile sees: the weights against the reference of before, with no
-      // maximum looked for.  Rounding does not depend on the reference, so it may stay far behind;
-      // only when the weights' sum is too large for their type, the keys go by the book.
-      auto fast = [&](auto& x, int part, int b0, int key0) {
+      // The weights are taken against the reference of before, with no maximum looked for (the row's
+      // first keys set it).  Rounding does not depend on the reference, so it may stay far behind;
+      // only when the weights' sum is too large for their type, or a row has seen no key yet, the
+      // keys go by the book.  False: they have to.
+      auto fits = [&](const uint64_t (&sum)[2], bool unset) {
+        const float2 u = unpair(add2(sum[0], sum[1]));
+        const float total = u.x + u.y;
+        if (__any_sync(0xffffffffu, unset || total > kMostWeight<DT>)) return false;
+        l += total;
+        return true;
+      };
+      // Keys that every token of the tile sees, loaded before.
+      auto whole = [&](auto& x, int part, int b0, int key0) {
         constexpr int N = sizeof(x) / 4;
         uint32_t p[N / 2];
         const uint64_t off2 = offset();
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int b = 0; b < N / 32; ++b) weights(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * b), p + 16 * b, off2, sum);
-        const float2 u = unpair(add2(sum[0], sum[1]));
-        const float total = u.x + u.y;
-        if (__any_sync(0xffffffffu, m == -INFINITY || total > kMostWeight<DT>)) {
-          careful(false, false, part, b0, b0 + N / 32, key0);
+        if (!fits(sum, m == -INFINITY)) {
+          careful(false, part, b0, b0 + N / 32, key0);
           return;
         }
-        l += total;
 #pragma unroll
         for (int b = 0; b < N / 32; ++b)
           tmem_st_32x32b_x16(sc + 16 * (b0 + b), *reinterpret_cast<uint32_t(*)[16]>(p + 16 * b));
         publish(part);
       };
+      // A first tile, or one that a mask cuts, piece by piece, the next one on its way.
+      auto edge = [&](auto pieces, bool masked, int part, int b0, int key0) {
+        constexpr int NB = decltype(pieces)::value;
+        uint32_t y[2][32], p[16 * NB];
+        auto fetch = [&](int b) { tmem_ld_32x32b_x32(sc + 32 * (b0 + b), y[b & 1]); };
+        auto arrived = [&](int b) {
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(y[b & 1][i]));   // not before the wait
+          if (b + 1 < NB) fetch(b + 1);
+          if (masked) mask(y[b & 1], key0 + 32 * (b0 + b));
+        };
+        if (!started && part == 0) {
+          float mx[2] = {-INFINITY, -INFINITY};
+          fetch(0);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            arrived(b);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                mx[e] = max3(mx[e], __uint_as_float(y[b & 1][i + e]), __uint_as_float(y[b & 1][i + 2 + e]));
+          }
+          m = fmaxf(mx[0], mx[1]);
+        }
+        const uint64_t off2 = offset();
+        uint64_t sum[2] = {0, 0};
+        fetch(0);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          arrived(b);
+          weights(y[b & 1], p + 16 * b, off2, sum);
+        }
+        if (!fits(sum, m == -INFINITY && (started || part))) {
+          careful(masked, part, b0, b0 + NB, key0);
+          return;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          tmem_st_32x32b_x16(sc + 16 * (b0 + b), *reinterpret_cast<uint32_t(*)[16]>(p + 16 * b));
+        publish(part);
+      };
+      // Values that some token does not see: 0 x NaN or 0 x infinity in P V would reach its result.
+      // In the key tiles that a mask cuts, rows behind the sequence's end are zeroed, and elements
+      // that are not finite are zeroed and noted; the output adds them back for the tokens that see
+      // them.  The softmax warps do it, before the scores are there: a warp of its own took 8500
+      // cycles a tile next to the tensor cores' reads, and their arrival with the weights is the
+      // only one needed.
+      auto look_over = [&](int j) {
+        const int i = iv + 2 * j;
+        ok = wait_for(&full[i % P::SLOTS], i / P::SLOTS);
+        if (!ok) return;
+        const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
+        uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
+        const int rows = k_len - j * kN;
+        uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
+        bool touched = false;
+#pragma unroll 8
+        for (int e = row; e < P::TILE / 16; e += kM) {
+          if ((e % (P::HALF / 16)) / 8 < rows) {
+            const uint4 x = tile[e];
+            top = max_abs2<DT>(max_abs2<DT>(top, x.x), max_abs2<DT>(x.y, max_abs2<DT>(x.z, x.w)));
+          } else {
+            tile[e] = make_uint4(0, 0, 0, 0);
+            touched = true;
+          }
+        }
+        if ((top & expo) == expo || ((top >> 16) & expo) == expo) {
+          for (int e = row; e < P::TILE / 16; e += kM) {
+            if ((e % (P::HALF / 16)) / 8 >= rows) continue;
+            uint4 x = tile[e];
+            uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              u[y] &= ((u[y] & expo) == expo ? 0xffff0000u : 0xffffffffu) &
+                      (((u[y] >> 16) & expo) == expo ? 0x0000ffffu : 0xffffffffu);
+            tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          touched = true;
+          *reinterpret_cast<volatile int*>(&works[nw & 1].poison) = 1;
+        }
+        if (touched) fence_proxy_async_smem();
+        __syncwarp();
+      };
       for (int j = r.jb; j < r.je; ++j, ++cnt) {
-        ok = wait_for(&s_full[t], cnt);
+        const bool masked = j * kN < lo_max || (j + 1) * kN > hi_min;
+        if (masked) look_over(j);
+        if (ok) ok = wait_for(&s_full[t], cnt);
         if (!ok) break;
         tc_fence_after();
-        const bool masked = j * kN < lo_max || (j + 1) * kN > hi_min;
-        if (masked || j == r.jb) {
-#pragma unroll 1
-          for (int part = 0; ok && part < 2; ++part)
-            careful(masked, j == r.jb && part == 0, part, part ? kPart / 32 : 0, part ? kN / 32 : kPart / 32, j * kN);
+        if (masked || !started) {
+          edge(std::integral_constant<int, kPart / 32>{}, masked, 0, 0, j * kN);
+          if (ok) edge(std::integral_constant<int, (kN - kPart) / 32>{}, masked, 1, kPart / 32, j * kN);
+          started = true;
         } else {
           uint32_t xa[kPart], xb[kN - kPart];
 #pragma unroll
           for (int b = 0; b < kPart / 32; ++b)
             tmem_ld_32x32b_x32(sc + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(xa + 32 * b));
           tmem_ld_wait();
+          whole(xa, 0, 0, j * kN);
+          if (!ok) break;
 #pragma unroll
           for (int b = 0; b < (kN - kPart) / 32; ++b)
             tmem_ld_32x32b_x32(sc + kPart + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(xb + 32 * b));
-          fast(xa, 0, 0, j * kN);
           tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < kN - kPart; ++i) asm volatile("" : "+r"(xb[i]));   // not before the wait
-          if (ok) fast(xb, 1, kPart / 32, j * kN);
+          whole(xb, 1, kPart / 32, j * kN);
         }
         if (!ok) break;
       }
-      // ---- epilogue
-      const bool any = r.je > r.jb;
-      if (ok && any) ok = wait_for(&o_done[2 + t], cnt - 1);
       if (!ok) break;
-      tc_fence_after();
-      const Work w = works[nw & 1];   // read again: its registers are better used above
-      const int tile0 = w.tok0 + t * tt;
-      const bool empty_row = hi <= lo;
-      const float inv = empty_row ? 0.0f : 1.0f / l;
-      const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
-#pragma unroll 1
-      for (int b = 0; b < D / 32; ++b) {
-        uint32_t y[32];
-        __syncwarp();
-        if (any) {
-          tmem_ld_32x32b_x32(oc + 32 * b, y);
-          tmem_ld_wait();
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = empty_row ? 0u : __float_as_uint(__uint_as_float(y[i]) * inv);
-        if (w.poison && !empty_row) {
-          const Job job(a, w, tt);
-          for (int j = job.jb; j < job.je; ++j) {
-            if (!job.special(j)) continue;
-            const int ka = j * kN > lo ? j * kN : lo, kb = (j + 1) * kN < hi ? (j + 1) * kN : hi;
-            for (int key = ka; key < kb; ++key) {
-              const uint16_t* vr = v + (size_t)(w.k0 + key) * a.v_token + (size_t)hk * a.v_head + 32 * b;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float z = bits_to_float<DT>(vr[i]);
-                if (!isfinite(z)) y[i] = __float_as_uint(__uint_as_float(y[i]) + z);
-              }
-            }
-          }
-        }
-        // through shared memory, so that four lanes store 64 bytes of one row (a thread's own row
-        // would touch 32 lines with every store)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(out_stage + 64 * lane + 16 * (i ^ ((lane >> 1) & 3))) =
-              make_uint4(pack2<DT>(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
-                         pack2<DT>(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
-                         pack2<DT>(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
-                         pack2<DT>(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = 8 * i + (lane >> 2), gr = 32 * (warp & 3) + rr;   // row of the warp, of the tile
-          const int tok = tile0 + (gr >> gp_shift), head = w.h0 + (gr & (gp - 1));
-          if (tok < w.q_len)
-            *reinterpret_cast<uint4*>(o + (size_t)(w.q0 + tok) * a.o_token + (size_t)head * a.o_head + 32 * b +
-                                      8 * (lane & 3)) =
-                *reinterpret_cast<const uint4*>(out_stage + 64 * rr + 16 * ((lane & 3) ^ ((rr >> 1) & 3)));
-        }
-      }
-      const int tok = tile0 + (row >> gp_shift);
-      if (lse && tok < w.q_len)
-        lse[(size_t)(w.q0 + tok) * a.n_heads + w.h0 + (row & (gp - 1))] = empty_row ? -INFINITY : m * s2 * kLn2 + logf(l);
-      tc_fence_before();
-      give_back(nw);
+      // what the output needs: for the warps that write it, once they have read the last ones
+      if (no > 0) ok = wait_for(&o_free[t], no - 1);
+      if (!ok) break;
+      sums[t * kM + row] = make_float2(l, m * s2);
+      ++no;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums_full[t]);
     }
   }
 
@@ -838,6 +962,10 @@ bool launch_tc(const qre_attn& a, int n_seqs, int total_q, int total_k, const in
       !make_tmap_rows16(&tk, k, total_k, stride(a.k_token, total_k), km ? a.n_kv_heads : 1, stride(a.k_head, km ? a.n_kv_heads : 1), D, 1, kN) ||
       !make_tmap_rows16(&tv, v, total_k, stride(a.v_token, total_k), vm ? a.n_kv_heads : 1, stride(a.v_head, vm ? a.n_kv_heads : 1), D, 1, kN))
     return false;
+  CUtensorMap to = tq;   // not used without store_o
+  const int store_o = (total_q == 1 || a.o_token > 0) && (a.n_heads == 1 || a.o_head > 0) &&
+                      make_tmap_rows16(&to, o, total_q, stride(a.o_token, total_q), a.n_heads,
+                                       stride(a.o_head, a.n_heads), D, gp, kM / gp);
   const int groups = a.n_heads / gp, pair = 2 * kM / gp;
   int gp_shift = 0;
   while ((1 << gp_shift) < gp) ++gp_shift;
@@ -846,7 +974,7 @@ bool launch_tc(const qre_attn& a, int n_seqs, int total_q, int total_k, const in
   *err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), Plan<D>::BYTES);
   if (*err != cudaSuccess) return true;
   *err = launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), (size_t)Plan<D>::BYTES, stream, a, n_seqs,
-                          total_q, total_k, gp_shift, groups, cu_q, cu_k, tq, tk, tv, qm, km, vm,
+                          total_q, total_k, gp_shift, groups, cu_q, cu_k, tq, tk, tv, to, store_o, qm, km, vm,
                           static_cast<const uint16_t*>(v), static_cast<uint16_t*>(o), lse, wait_limit_ns(), status);
   return true;
 }
