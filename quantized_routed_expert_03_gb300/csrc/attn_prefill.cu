@@ -108,8 +108,8 @@ template <int D>
 struct Plan {
   static constexpr int HALF = kN * 128;              // 64 columns of a 128-row tile, 128-byte rows
   static constexpr int TILE = HALF * (D / 64);
-  static constexpr int SLOTS = D == 128 ? 4 : 8;     // K and V tiles in flight
-  static constexpr int BYTES = 2 * TILE + SLOTS * TILE + 2 * HALF + 2048 + 768;   // stage; sums; barriers
+  static constexpr int SLOTS = D == 128 ? 5 : 10;    // K and V tiles in flight
+  static constexpr int BYTES = 2 * TILE + SLOTS * TILE + 2048 + 768;   // tiles; sums; barriers
 };
 
 // mbar_wait_bounded without a call: the register split (setmaxnreg) leaves no room for the calling convention.
@@ -138,6 +138,12 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   }
   const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)), __habs2(*reinterpret_cast<const __half2*>(&b)));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* z) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]),
+               "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+               : "memory");
 }
 
 // One piece of work: two query tiles of one sequence and head group.
@@ -290,16 +296,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q, int total_k, int gp_shift, int groups,
                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-                   int store_o, int q_heads_move, int k_heads_move, int v_heads_move,
+                   const __grid_constant__ CUtensorMap tv, int wide_o, int q_heads_move, int k_heads_move, int v_heads_move,
                    const uint16_t* __restrict__ v, uint16_t* __restrict__ o, float* __restrict__ lse,
                    uint64_t limit_ns, int* status) {
   using P = Plan<D>;
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle goes by addresses; no static shared memory beside it
   uint8_t* sq = smem;                       // two query tiles
   uint8_t* skv = smem + 2 * P::TILE;        // ring of key and value tiles
-  uint8_t* stage = skv + P::SLOTS * P::TILE;   // [2]: 64 columns of a query tile's output on their way out
-  uint64_t* bar = reinterpret_cast<uint64_t*>(stage + 2 * P::HALF);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(skv + P::SLOTS * P::TILE);
   uint64_t* answer = bar;                   // [2], 16-byte aligned
   uint64_t* full = answer + 2;              // [SLOTS]
   uint64_t* empty = full + P::SLOTS;        // [SLOTS]
@@ -312,9 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* work_empty = work_full + 2;     // [2]
   uint64_t* sums_full = work_empty + 2;     // [2]: a query tile's sums and maxima are there
   uint64_t* o_free = sums_full + 2;         // [2]: its output (and they) have been read
-  uint64_t* stage_ready = o_free + 2;       // [2], of the two halves of the stage in turn: a warp comes back to one
-  uint64_t* stage_free = stage_ready + 2;   // only behind stage_free, so it cannot count twice for a round
-  uint64_t* answered = stage_free + 1;
+  uint64_t* answered = o_free + 2;
   uint64_t* drain = answered + 1;           // [2]
   Work* works = reinterpret_cast<Work*>(drain + 2);          // [2]
   float2* sums = reinterpret_cast<float2*>(works + 2);       // [2][kM]: (l, m in base 2) of the rows
@@ -347,9 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&work_empty[t], kMmaWarp + 2 - 1);   // all warps but the one that finds the work and the last
       mbar_init(&drain[t], 1);
     }
-    mbar_init(&stage_ready[0], 4);
-    mbar_init(&stage_ready[1], 4);
-    mbar_init(stage_free, 1);
     mbar_init(answered, 1);
     *abort_flag = 0;
     *issued = *q_issued = *asked = 0;
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!more) umma_commit_lead(q_empty, lead);
           }
           // The waits for what is long there stand before the one for the weights.
-          ok = mine ? wait_tile(i + 1) && (!more || wait_tile(i + 2)) : wait_tile(i) && wait_tile(i + 1);
+          ok = wait_tile(i + 1) && (mine || wait_tile(i));
           if (ok && mine && j == r.jb) {   // the output of the piece before has been read
             ok = no == 0 || wait_for(&o_free[t], no - 1);
             ++no;
@@ -536,10 +535,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           values(sv, 1, false);
-          ++n;
-          if (more) scores(sk);   // overwrites P: issued behind the product that reads it
-          if (pass) turn_to(t ^ 1);
           umma_commit_lead(&empty[sv], lead);
+          ++n;
+          if (more) {
+            ok = wait_tile(i + 2);
+            if (!ok) break;
+            tc_fence_after();
+            scores(sk);   // overwrites P: issued behind the product that reads it
+          }
+          if (pass) turn_to(t ^ 1);
           if (more) umma_commit_lead(&empty[sk], lead);
           if (more && j + 2 == r.je) umma_commit_lead(q_empty, lead);
         }
@@ -548,13 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kStoreWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kStoreRegs));
-    // ---- output: o = O / l.  Warps of their own, because what leaves an SM leaves slowly: the softmax
-    // goes on with the next piece of work meanwhile.  A full tile goes through shared memory by
-    // TMA, 64 columns at a time; the last tile of a sequence by stores of each row's own thread.
+    // ---- output: o = O / l.  Warps of their own, because what leaves an SM leaves slowly (two tiles in
+    // some 8000 cycles, by TMA through shared memory as by stores of each row's own thread): the
+    // softmax goes on with the next piece of work meanwhile.
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const bool issuer = warp == kStoreWarp && lane == 0;
-    int cnt[2] = {0, 0}, no[2] = {0, 0}, rounds = 0;
+    int cnt[2] = {0, 0}, no[2] = {0, 0};
     bool ok = true;
     Work w;
     for (int nw = 0; ok && take(nw, w); ++nw) {
@@ -581,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = empty_row ? 0.0f : 1.0f / sum.x;
         if (lse && valid)
           lse[(size_t)(w.q0 + tok) * a.n_heads + head] = empty_row ? -INFINITY : sum.y * kLn2 + logf(sum.x);
-        const bool full_tile = store_o && tile0 + tt <= w.q_len;
         const bool poison = *reinterpret_cast<volatile int*>(&works[nw & 1].poison) != 0;
         uint16_t* out = o + (size_t)(w.q0 + tok) * a.o_token + (size_t)head * a.o_head;
         const uint32_t oc = lanes + (t ? kO1 : kO0);
@@ -619,46 +621,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = pack2<DT>(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
           __syncwarp();
-          if (full_tile) {
-            // the store two rounds before has read its half of the stage
-            if (rounds >= 2) {
-              if (issuer) {
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                mbar_arrive(stage_free);
-              }
-              __syncwarp();
-              ok = wait_for(stage_free, rounds - 2);
-              if (!ok) break;
-            }
-            uint8_t* half = stage + (rounds & 1) * P::HALF;
+          if (valid) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(half + row * 128 + 16 * (i ^ (row & 7))) =
-                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&stage_ready[rounds & 1]);
-            if (warp == kStoreWarp) {
-              ok = wait_for(&stage_ready[rounds & 1], rounds >> 1);
-              if (!ok) break;
-              if (issuer) {
-                tma_store_3d(&to, half, 64 * c, w.h0, w.q0 + tile0);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            for (int i = 0; i < 32; i += 8) {
+              if (wide_o) {
+                st_global_32(out + 64 * c + 2 * i, y + i);
+              } else {
+                *reinterpret_cast<uint4*>(out + 64 * c + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                *reinterpret_cast<uint4*>(out + 64 * c + 2 * i + 8) = make_uint4(y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
               }
-              __syncwarp();
             }
-            ++rounds;
-          } else if (valid) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(out + 64 * c + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
           }
           __syncwarp();
         }
       }
       give_back(nw);
     }
-    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax: thread r of the four warps owns row r of its query tile
@@ -719,7 +697,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 u = unpair(add2(sum[0], sum[1]));
         l += u.x + u.y;
       };
+      int unseen = -1;   // a tile whose values have yet to be looked over
+      // Values that some token does not see: 0 x NaN or 0 x infinity in P V would reach its result.
+      // In the key tiles that a mask cuts, rows behind the sequence's end are zeroed, and elements
+      // that are not finite are zeroed and noted; the output adds them back for the tokens that see
+      // them.  The softmax warps do it: a warp of its own took 8500 cycles a tile next to the tensor
+      // cores' reads, and their arrival with the weights is the only one needed.
+      auto look_over = [&](int j) {
+        const int i = iv + 2 * j;
+        const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
+        uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
+        const int rows = k_len - j * kN;
+        uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
+        bool touched = false;
+#pragma unroll 8
+        for (int e = row; e < P::TILE / 16; e += kM) {
+          if ((e % (P::HALF / 16)) / 8 < rows) {
+            const uint4 x = tile[e];
+            top = max_abs2<DT>(max_abs2<DT>(top, x.x), max_abs2<DT>(x.y, max_abs2<DT>(x.z, x.w)));
+          } else {
+            tile[e] = make_uint4(0, 0, 0, 0);
+            touched = true;
+          }
+        }
+        if ((top & expo) == expo || ((top >> 16) & expo) == expo) {
+          for (int e = row; e < P::TILE / 16; e += kM) {
+            if ((e % (P::HALF / 16)) / 8 >= rows) continue;
+            uint4 x = tile[e];
+            uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              u[y] &= ((u[y] & expo) == expo ? 0xffff0000u : 0xffffffffu) &
+                      (((u[y] >> 16) & expo) == expo ? 0x0000ffffu : 0xffffffffu);
+            tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          touched = true;
+          *reinterpret_cast<volatile int*>(&works[nw & 1].poison) = 1;
+        }
+        if (touched) fence_proxy_async_smem();
+        __syncwarp();
+      };
       auto publish = [&](int part) {
+        if (part == 0 && unseen >= 0) {
+          const int i = iv + 2 * unseen;
+          ok = wait_for(&full[i % P::SLOTS], i / P::SLOTS);
+          if (!ok) return;
+          look_over(unseen);
+          unseen = -1;
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -844,52 +869,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_32x32b_x16(sc + 16 * (b0 + b), *reinterpret_cast<uint32_t(*)[16]>(p + 16 * b));
         publish(part);
       };
-      // Values that some token does not see: 0 x NaN or 0 x infinity in P V would reach its result.
-      // In the key tiles that a mask cuts, rows behind the sequence's end are zeroed, and elements
-      // that are not finite are zeroed and noted; the output adds them back for the tokens that see
-      // them.  The softmax warps do it, before the scores are there: a warp of its own took 8500
-      // cycles a tile next to the tensor cores' reads, and their arrival with the weights is the
-      // only one needed.
-      auto look_over = [&](int j) {
-        const int i = iv + 2 * j;
-        ok = wait_for(&full[i % P::SLOTS], i / P::SLOTS);
-        if (!ok) return;
-        const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
-        uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
-        const int rows = k_len - j * kN;
-        uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
-        bool touched = false;
-#pragma unroll 8
-        for (int e = row; e < P::TILE / 16; e += kM) {
-          if ((e % (P::HALF / 16)) / 8 < rows) {
-            const uint4 x = tile[e];
-            top = max_abs2<DT>(max_abs2<DT>(top, x.x), max_abs2<DT>(x.y, max_abs2<DT>(x.z, x.w)));
-          } else {
-            tile[e] = make_uint4(0, 0, 0, 0);
-            touched = true;
-          }
-        }
-        if ((top & expo) == expo || ((top >> 16) & expo) == expo) {
-          for (int e = row; e < P::TILE / 16; e += kM) {
-            if ((e % (P::HALF / 16)) / 8 >= rows) continue;
-            uint4 x = tile[e];
-            uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              u[y] &= ((u[y] & expo) == expo ? 0xffff0000u : 0xffffffffu) &
-                      (((u[y] >> 16) & expo) == expo ? 0x0000ffffu : 0xffffffffu);
-            tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-          touched = true;
-          *reinterpret_cast<volatile int*>(&works[nw & 1].poison) = 1;
-        }
-        if (touched) fence_proxy_async_smem();
-        __syncwarp();
-      };
       for (int j = r.jb; j < r.je; ++j, ++cnt) {
         const bool masked = j * kN < lo_max || (j + 1) * kN > hi_min;
-        if (masked) look_over(j);
-        if (ok) ok = wait_for(&s_full[t], cnt);
+        // the values of a cut tile: before the scores are there if they have come, else before the
+        // weights are published
+        if (masked) {
+          const int i = iv + 2 * j;
+          if (__all_sync(0xffffffffu, mbar_try_wait(&full[i % P::SLOTS], (i / P::SLOTS) & 1))) look_over(j);
+          else unseen = j;
+        }
+        ok = wait_for(&s_full[t], cnt);
         if (!ok) break;
         tc_fence_after();
         if (masked || !started) {
@@ -962,10 +951,7 @@ bool launch_tc(const qre_attn& a, int n_seqs, int total_q, int total_k, const in
       !make_tmap_rows16(&tk, k, total_k, stride(a.k_token, total_k), km ? a.n_kv_heads : 1, stride(a.k_head, km ? a.n_kv_heads : 1), D, 1, kN) ||
       !make_tmap_rows16(&tv, v, total_k, stride(a.v_token, total_k), vm ? a.n_kv_heads : 1, stride(a.v_head, vm ? a.n_kv_heads : 1), D, 1, kN))
     return false;
-  CUtensorMap to = tq;   // not used without store_o
-  const int store_o = (total_q == 1 || a.o_token > 0) && (a.n_heads == 1 || a.o_head > 0) &&
-                      make_tmap_rows16(&to, o, total_q, stride(a.o_token, total_q), a.n_heads,
-                                       stride(a.o_head, a.n_heads), D, gp, kM / gp);
+  const int wide_o = reinterpret_cast<uintptr_t>(o) % 32 == 0 && a.o_token % 16 == 0 && a.o_head % 16 == 0;
   const int groups = a.n_heads / gp, pair = 2 * kM / gp;
   int gp_shift = 0;
   while ((1 << gp_shift) < gp) ++gp_shift;
@@ -974,7 +960,7 @@ bool launch_tc(const qre_attn& a, int n_seqs, int total_q, int total_k, const in
   *err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), Plan<D>::BYTES);
   if (*err != cudaSuccess) return true;
   *err = launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), (size_t)Plan<D>::BYTES, stream, a, n_seqs,
-                          total_q, total_k, gp_shift, groups, cu_q, cu_k, tq, tk, tv, to, store_o, qm, km, vm,
+                          total_q, total_k, gp_shift, groups, cu_q, cu_k, tq, tk, tv, wide_o, qm, km, vm,
                           static_cast<const uint16_t*>(v), static_cast<uint16_t*>(o), lse, wait_limit_ns(), status);
   return true;
 }
