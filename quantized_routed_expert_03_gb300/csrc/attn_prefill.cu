@@ -94,7 +94,8 @@ constexpr int kPart = 96;          // keys of a tile's first part (of two): P V 
 constexpr int kThreads = 512;
 // warps 0-3: softmax of tile 0, 4-7: of tile 1, 8-11: output of both
 constexpr int kStoreWarp = 8;
-constexpr int kTmaWarp = 12, kMmaWarp = 13;   // MMA warps 13 and 14: one per query tile; 15 fills the warpgroup
+constexpr int kTmaWarp = 12, kMmaWarp = 13, kFindWarp = 15;   // MMA warps 13 and 14: one per query tile
+constexpr int kWorks = 3;          // pieces of work known at a time: being stored, computed, fetched
 // Registers: 512 x 128 at launch = 256 x 160 + 128 x 112 + 128 x 80.
 constexpr int kSoftmaxRegs = 160, kStoreRegs = 112, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512;
@@ -199,8 +200,8 @@ struct Job {
 // against the whole) by sequence.
 class Finder {
  public:
-  __device__ __forceinline__ Finder(int n_seqs, int total_q, int total_k, const int32_t* cu_q, const int32_t* cu_k, int pair)
-      : n_(n_seqs), tq_(total_q), tk_(total_k), cu_q_(cu_q), cu_k_(cu_k), pair_(pair) {
+  __device__ __forceinline__ Finder(int n_seqs, int total_q, int total_k, const int32_t* cu_q, const int32_t* cu_k, int pair_shift)
+      : n_(n_seqs), tq_(total_q), tk_(total_k), cu_q_(cu_q), cu_k_(cu_k), shift_by_(pair_shift), pair_(1 << pair_shift) {
     lane_ = threadIdx.x & 31;
     if (n_ <= 128) {
       int top = 0;
@@ -256,7 +257,7 @@ class Finder {
     if (i < n_) {
       const int q0 = cu_q_[i], q1 = cu_q_[i + 1], k0 = cu_k_[i], k1 = cu_k_[i + 1];
       if (q0 >= 0 && q1 >= q0 && q1 <= tq_ && k0 >= 0 && k1 >= k0 && k1 <= tk_) {
-        cnt = (q1 - q0 + pair_ - 1) / pair_;
+        cnt = (q1 - q0 + pair_ - 1) >> shift_by_;
         shift = k1 - k0 - (q1 - q0);
       }
     }
@@ -264,7 +265,7 @@ class Finder {
   // first tile of sequence (c, lane) whose last token stands at level * kN or later
   __device__ __forceinline__ int lowest(int c, int level) const {
     const int x = level * kN + 1 - shift_[c];
-    const int i = level <= 0 || x <= 0 ? 0 : (x + pair_ - 1) / pair_ - 1;
+    const int i = level <= 0 || x <= 0 ? 0 : ((x + pair_ - 1) >> shift_by_) - 1;
     return i < cnt_[c] ? i : cnt_[c];
   }
   __device__ __forceinline__ int at_least(int level) const {
@@ -287,7 +288,8 @@ class Finder {
   }
   int n_, tq_, tk_;
   const int32_t *cu_q_, *cu_k_;
-  int pair_, lane_, top_ = 0, at_ = 0, base_ = 0;
+  int shift_by_, pair_;   // tokens of a piece of work: 1 << shift_by_
+  int lane_, top_ = 0, at_ = 0, base_ = 0;
   int cnt_[4], shift_[4];
 };
 
@@ -312,14 +314,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_empty + 1;           // [2]
   uint64_t* p_full = s_full + 2;            // [part][2]: one phase of each per key tile
   uint64_t* o_done = p_full + 4;            // [part][2]
-  uint64_t* work_full = o_done + 4;         // [2]
-  uint64_t* work_empty = work_full + 2;     // [2]
-  uint64_t* sums_full = work_empty + 2;     // [2]: a query tile's sums and maxima are there
+  uint64_t* work_full = o_done + 4;         // [kWorks]
+  uint64_t* work_empty = work_full + kWorks;   // [kWorks]
+  uint64_t* sums_full = work_empty + kWorks;     // [2]: a query tile's sums and maxima are there
   uint64_t* o_free = sums_full + 2;         // [2]: its output (and they) have been read
   uint64_t* answered = o_free + 2;
   uint64_t* drain = answered + 1;           // [2]
-  Work* works = reinterpret_cast<Work*>(drain + 2);          // [2]
-  float2* sums = reinterpret_cast<float2*>(works + 2);       // [2][kM]: (l, m in base 2) of the rows
+  Work* works = reinterpret_cast<Work*>(drain + 2);          // [kWorks]
+  float2* sums = reinterpret_cast<float2*>(works + kWorks);       // [2][kM]: (l, m in base 2) of the rows
   uint32_t* tmem_p = reinterpret_cast<uint32_t*>(sums + 2 * kM);
   int* misc = reinterpret_cast<int*>(tmem_p + 1);
   volatile int* abort_flag = misc;          // a wait gave up
@@ -345,9 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(&sums_full[t], 4);
       mbar_init(&o_free[t], 4);
-      mbar_init(&work_full[t], 1);
-      mbar_init(&work_empty[t], kMmaWarp + 2 - 1);   // all warps but the one that finds the work and the last
       mbar_init(&drain[t], 1);
+    }
+    for (int i = 0; i < kWorks; ++i) {
+      mbar_init(&work_full[i], 1);
+      mbar_init(&work_empty[i], kFindWarp);   // all warps but the one that finds the work
     }
     mbar_init(answered, 1);
     *abort_flag = 0;
@@ -374,26 +378,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // The n-th piece of work; false when there is none or a wait gave up.
   auto take = [&](int n, Work& w) {
-    if (!wait_for(&work_full[n & 1], n >> 1)) return false;
-    w = works[n & 1];
+    if (!wait_for(&work_full[n % kWorks], n / kWorks)) return false;
+    w = works[n % kWorks];
     return w.end == 0;
   };
   auto give_back = [&](int n) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&work_empty[n & 1]);
+    if (lane == 0) mbar_arrive(&work_empty[n % kWorks]);
   };
 
   if (warp >= kTmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kTmaWarp) {
-      // ---- finds the work, fetches its tiles, and asks for the next
-      Finder finder(n_seqs, total_q, total_k, cu_q, cu_k, 2 * tt);
-      int b = blockIdx.x, i0 = 0, nq = 0;
+    if (warp == kFindWarp) {
+      // ---- finds the work, and asks for the next
+      Finder finder(n_seqs, total_q, total_k, cu_q, cu_k, 8 - gp_shift);
+      int b = blockIdx.x;
       for (int n = 0;; ++n) {
         int seq = 0, tile = 0;
-        const bool have = b >= 0 && finder.find(b / groups, seq, tile);
-        if (n >= 2 && !wait_for(&work_empty[n & 1], (n >> 1) - 1)) break;
         Work w{};
+        const bool have = b >= 0 && finder.find(b / groups, seq, tile);
         w.end = !have;
         if (have) {
           w.q0 = cu_q[seq];
@@ -403,9 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.tok0 = tile * 2 * tt;
           w.h0 = (b % groups) * gp;
         }
+        if (n >= kWorks && !wait_for(&work_empty[n % kWorks], n / kWorks - 1)) break;
         if (lane == 0) {
-          works[n & 1] = w;
-          mbar_arrive(&work_full[n & 1]);
+          works[n % kWorks] = w;
+          mbar_arrive(&work_full[n % kWorks]);
         }
         __syncwarp();
         if (!have) break;
@@ -414,41 +418,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           ask_next_cta(answer, answered);
           *asked = n + 1;
         }
-        const Job job(a, w, tt);
-        bool ok = true;
-        if (job.je > job.jb) {
-          const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
-          const int qh = q_heads_move ? w.h0 : 0, kh = k_heads_move ? hk : 0, vh = v_heads_move ? hk : 0;
-          ok = nq == 0 || wait_for(q_empty, nq - 1);
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(q_full, 2 * P::TILE);
-            for (int t = 0; t < 2; ++t)
-              for (int x = 0; x < D / 64; ++x)
-                tma_load_3d(sq + t * P::TILE + x * P::HALF, &tq, 64 * x, qh, w.q0 + w.tok0 + t * tt, q_full);
-            *q_issued = nq + 1;
-          }
-          ++nq;
-          const int end = i0 + 2 * (job.je - job.jb);
-          for (int i = i0; ok && i < end; ++i) {
-            const int s = i % P::SLOTS;
-            ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
-            if (ok && lane == 0) {
-              const bool is_v = (i - i0) & 1;
-              mbar_arrive_expect_tx(&full[s], P::TILE);
-              for (int x = 0; x < D / 64; ++x)
-                tma_load_3d(skv + s * P::TILE + x * P::HALF, is_v ? &tv : &tk, 64 * x, is_v ? vh : kh,
-                            w.k0 + (job.jb + (i - i0) / 2) * kN, &full[s]);
-              *issued = i + 1;
-            }
-          }
-          i0 = end;
-        }
-        if (!ok || !wait_for(answered, n)) break;
+        if (!wait_for(answered, n)) break;
         b = next_cta(answer);
         fence_proxy_async_smem();   // read before the next answer is written
         __syncwarp();
       }
-    } else if (warp < kMmaWarp + 2) {
+    } else if (warp == kTmaWarp) {
+      // ---- fetches the tiles
+      int i0 = 0, nq = 0;
+      bool ok = true;
+      Work w;
+      for (int n = 0; ok && take(n, w); ++n) {
+        const Job job(a, w, tt);
+        give_back(n);
+        if (job.je <= job.jb) continue;
+        const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
+        const int qh = q_heads_move ? w.h0 : 0, kh = k_heads_move ? hk : 0, vh = v_heads_move ? hk : 0;
+        ok = nq == 0 || wait_for(q_empty, nq - 1);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(q_full, 2 * P::TILE);
+          for (int t = 0; t < 2; ++t)
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_3d(sq + t * P::TILE + x * P::HALF, &tq, 64 * x, qh, w.q0 + w.tok0 + t * tt, q_full);
+          *q_issued = nq + 1;
+        }
+        ++nq;
+        const int end = i0 + 2 * (job.je - job.jb);
+        for (int i = i0; ok && i < end; ++i) {
+          const int s = i % P::SLOTS;
+          ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
+          if (ok && lane == 0) {
+            const bool is_v = (i - i0) & 1;
+            mbar_arrive_expect_tx(&full[s], P::TILE);
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_3d(skv + s * P::TILE + x * P::HALF, is_v ? &tv : &tk, 64 * x, is_v ? vh : kh,
+                          w.k0 + (job.jb + (i - i0) / 2) * kN, &full[s]);
+            *issued = i + 1;
+          }
+        }
+        i0 = end;
+      }
+    } else {
       // ---- MMA: the whole warp, so that the operands stay in uniform registers
       const int t = warp - kMmaWarp;
       const uint32_t lead = elect_lane();
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = empty_row ? 0.0f : 1.0f / sum.x;
         if (lse && valid)
           lse[(size_t)(w.q0 + tok) * a.n_heads + head] = empty_row ? -INFINITY : sum.y * kLn2 + logf(sum.x);
-        const bool poison = *reinterpret_cast<volatile int*>(&works[nw & 1].poison) != 0;
+        const bool poison = *reinterpret_cast<volatile int*>(&works[nw % kWorks].poison) != 0;
         uint16_t* out = o + (size_t)(w.q0 + tok) * a.o_token + (size_t)head * a.o_head;
         const uint32_t oc = lanes + (t ? kO1 : kO0);
 #pragma unroll
@@ -708,21 +718,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t expo = DT == QRE_BF16 ? 0x7f80u : 0x7c00u;
         uint4* tile = reinterpret_cast<uint4*>(skv + (i % P::SLOTS) * P::TILE);
         const int rows = k_len - j * kN;
-        uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
+        constexpr int kMine = P::TILE / 16 / kM;   // 16-byte pieces of a thread: row (e % 1024) / 8 of the tile
         bool touched = false;
-#pragma unroll 8
-        for (int e = row; e < P::TILE / 16; e += kM) {
-          if ((e % (P::HALF / 16)) / 8 < rows) {
-            const uint4 x = tile[e];
-            top = max_abs2<DT>(max_abs2<DT>(top, x.x), max_abs2<DT>(x.y, max_abs2<DT>(x.z, x.w)));
-          } else {
-            tile[e] = make_uint4(0, 0, 0, 0);
-            touched = true;
-          }
+        if (rows < kN) {
+#pragma unroll 1
+          for (int e = row; e < P::TILE / 16; e += kM)
+            if ((e % (P::HALF / 16)) / 8 >= rows) {
+              tile[e] = make_uint4(0, 0, 0, 0);
+              touched = true;
+            }
+        }
+        uint32_t top = 0;   // largest magnitudes of the two halves of a word: not finite iff one element is
+#pragma unroll
+        for (int g = 0; g < kMine; g += 8) {
+          uint4 x[8];       // several loads in flight
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = tile[row + (g + i) * kM];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            top = max_abs2<DT>(max_abs2<DT>(top, x[i].x), max_abs2<DT>(x[i].y, max_abs2<DT>(x[i].z, x[i].w)));
         }
         if ((top & expo) == expo || ((top >> 16) & expo) == expo) {
           for (int e = row; e < P::TILE / 16; e += kM) {
-            if ((e % (P::HALF / 16)) / 8 >= rows) continue;
             uint4 x = tile[e];
             uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -732,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
           }
           touched = true;
-          *reinterpret_cast<volatile int*>(&works[nw & 1].poison) = 1;
+          *reinterpret_cast<volatile int*>(&works[nw % kWorks].poison) = 1;
         }
         if (touched) fence_proxy_async_smem();
         __syncwarp();
