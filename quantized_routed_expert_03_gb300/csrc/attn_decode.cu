@@ -22,10 +22,15 @@
 // A warp runs on its own between the ends of units: it fills a ring of chunks in
 // shared memory with cp.async (16-byte pieces, rows that are not seen zero-filled,
 // so what they hold never reaches a product) and multiplies with mma.sync
-// (m16n8k16): S = Q K^T with the group's heads as the 16 rows, then O += P V.
-// The 16 rows are mostly padding, but the tensor work of a chunk is far below its
-// load time, and tcgen05 would want 128 rows.  More than 16 heads per KV head run
-// as several units over the same keys, which then come from L2.
+// (m16n8k16), keys and dimensions on the 16 side, heads on the 8 side:
+//   S^T = K Q^T (16 keys x 8 heads), O^T += V^T P^T (16 dimensions x 8 heads);
+// P turns from the first product's layout into the second's by one 8 x 8
+// transpose (movmatrix).  Nothing is padding with 8 heads per KV head; tcgen05
+// would want 128 rows.  More than 16 heads per KV head run as several units over
+// the same keys, which then come from L2.  Two CTAs share an SM, so that one
+// streams while the other joins its warps at the end of a unit.
+// A unit's first chunk sets the reference of its weights; later ones look for no
+// maximum (and shuffle nothing) unless a sum of weights grows too large.
 // An E4M3 cache is multiplied as fp16, which holds every E4M3 value; a bf16 query
 // is brought into fp16's range by a power of two per head.
 #include <cuda_fp8.h>
@@ -38,7 +43,8 @@
 namespace qre {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 2;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk
 constexpr int kRows = 16;             // query heads of a unit at most
@@ -70,16 +76,23 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "r"(addr)
                : "memory");
 }
+// 8 x 8 transpose of 16-bit elements held as ldmatrix leaves them.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 template <bool BF>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         const uint32_t (&b)[2]) {
   if (BF)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
 }
 // Two E4M3 bytes (low half of b) as an fp16 pair.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t b) {
@@ -88,8 +101,8 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t b) {
   return r;
 }
 
-// DT: type of q and o; CT: type of the cache; HI: more than 8 query heads in a unit.
-template <int DT, int CT, int D, bool HI>
+// DT: type of q and o; CT: type of the cache; NH: query heads of a unit in eights.
+template <int DT, int CT, int D, int NH>
 struct Decode {
   static constexpr bool F8 = CT == QRE_E4M3;
   static constexpr bool BF = CT == QRE_BF16;      // type of the products
@@ -98,8 +111,10 @@ struct Decode {
   static constexpr int PR = RB / 16;              // 16-byte pieces of a row
   static constexpr int RI = 32 / PR;              // rows that the warp's 32 lanes fetch at once
   static constexpr int NP = CK / 16;              // runs of 16 positions (each inside one page)
-  static constexpr int NT = CK / 8;
   static constexpr int KS = D / 16;
+  static constexpr int PT = BF ? QRE_BF16 : QRE_FP16;
+  // largest sum of a chunk's weights against a standing reference (fp16 weights end at 65504)
+  static constexpr float kMost = BF ? 1.1529215e18f /* 2^60 */ : 32768.0f;
 
   // Byte offset of piece `col` of row `row` in a tile: pieces of a 128-byte line
   // are permuted by the row, so the eight rows that ldmatrix reads at one column
@@ -113,18 +128,18 @@ struct Seq {
   int row, len, first;   // table row, length, chunks of the queries before
 };
 
-template <int DT, int CT, int D, bool HI>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DT, int CT, int D, int NH>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
                        const int32_t* __restrict__ seqs, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
                        float* __restrict__ lse, CutInfo* __restrict__ cuts, float* __restrict__ parts, int stages,
-                       int buf_rows, int* status) {
-  using K = Decode<DT, CT, D, HI>;
-  constexpr int CK = K::CK, NT = K::NT, KS = K::KS;
+                       int* status) {
+  using K = Decode<DT, CT, D, NH>;
+  constexpr int CK = K::CK, KS = K::KS;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + (size_t)(threadIdx.x >> 5) * stages * 2 * kTile;   // this warp's
-  float* buf = reinterpret_cast<float*>(smem + (size_t)kWarps * stages * 2 * kTile);   // [kWarps][buf_rows][D]
-  float2* ml = reinterpret_cast<float2*>(buf + kWarps * buf_rows * D);                 // [kWarps][kRows]
+  float* buf = reinterpret_cast<float*>(smem + (size_t)kWarps * stages * 2 * kTile);   // [kWarps][8][64]
+  float2* ml = reinterpret_cast<float2*>(buf + kWarps * 8 * 64);                       // [kWarps][kRows]
   Seq* sq = reinterpret_cast<Seq*>(ml + kWarps * kRows);                               // [n + 1]
   __shared__ int scan_part[kWarps];
   __shared__ int scan_total;
@@ -299,246 +314,286 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the units of this range, one after the other
   const size_t si = (size_t)layer * c.n_kv_heads;
+  const int r4 = lane >> 2, j4 = lane & 3;
+  // A unit's queries as the B operand: head 8 nh + lane / 4, zero beyond the unit's heads.  The words
+  // are asked for one unit ahead.
+  uint32_t qw[KS][NH][2];
+  auto heads_of = [&](const Place& p, int& hk, int& h0) {
+    hk = p.unit / blocks;
+    h0 = hk * g + (p.unit - hk * blocks) * kRows;
+    return (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
+  };
+  auto ask_queries = [&](const Place& p) {
+    int hk, h0;
+    const int rows = heads_of(p, hk, h0);
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const int r = 8 * nh + r4;
+      const uint16_t* qr = q + (size_t)p.t * a.q_token + (size_t)(h0 + (r < rows ? r : 0)) * a.q_head;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if (K::F8) {   // element order of the E4M3 products: k = 2 j + e is dimension 4 j + e, 8 + 2 j + e is 4 j + 2 + e
+          const uint2 x = *reinterpret_cast<const uint2*>(qr + 16 * k + 4 * j4);
+          qw[k][nh][0] = r < rows ? x.x : 0;
+          qw[k][nh][1] = r < rows ? x.y : 0;
+        } else {
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(qr + 16 * k + 2 * j4);
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 + 2 * j4);
+          qw[k][nh][0] = r < rows ? x : 0;
+          qw[k][nh][1] = r < rows ? y : 0;
+        }
+      }
+    }
+  };
   long long s0 = c0;
   Place cp = place_of(c0, t_first);
+  ask_queries(cp);
   long long next = c0 + warp;        // this warp's next chunk to compute
   while (s0 < c1) {
     const long long u0 = s0 - cp.ck, u1 = u0 + cp.nch;
     const long long s1 = u1 < c1 ? u1 : c1;
-    const int t = cp.t, hk = cp.unit / blocks, h0 = hk * g + (cp.unit - hk * blocks) * kRows;
-    const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
+    const int t = cp.t;
+    int hk, h0;
+    const int rows = heads_of(cp, hk, h0);
     const int len = sq[t].len, lo = a.window > 0 && len > a.window ? len - a.window : 0;
+    const float ks = K::F8 && c.k_scale ? c.k_scale[si + hk] : 1.0f;
+    const float vs = K::F8 && c.v_scale ? c.v_scale[si + hk] : 1.0f;
 
-    // the unit's queries as the A operand: rows lane / 4 (and + 8), zero beyond `rows`
-    uint32_t qa[KS][4];
-    float s2[2];                     // score factor of the two rows, base 2
-    const int r0 = lane >> 2, j4 = lane & 3;
+    uint32_t qb[KS][NH][2];
+    float s2[NH][2];                 // score factor of heads 2 j and 2 j + 1, base 2
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int r = r0 + 8 * hh;
-      s2[hh] = a.scale * kLog2e;
-      if (!HI && hh == 1) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) qa[k][1] = qa[k][3] = 0;
-        continue;
-      }
-      const uint16_t* qr = q + (size_t)t * a.q_token + (size_t)(h0 + (r < rows ? r : 0)) * a.q_head;
-      if (!K::F8) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(qr + 16 * k + 2 * j4);
-          const uint32_t y = *reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 + 2 * j4);
-          qa[k][hh] = r < rows ? x : 0;
-          qa[k][2 + hh] = r < rows ? y : 0;
-        }
-      } else {
-        // element order of the E4M3 products: k = 2 j + e is dimension 16 ks + 4 j + e, k = 8 + 2 j + e is 4 j + 2 + e
-        uint2 x[KS];
+    for (int nh = 0; nh < NH; ++nh) {
+      float own = a.scale * kLog2e * ks;   // of head lane / 4
+      float f = 1.0f;
+      if (K::F8 && DT == QRE_BF16) {
         float big = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          x[k] = *reinterpret_cast<const uint2*>(qr + 16 * k + 4 * j4);
-          if (r >= rows) x[k] = make_uint2(0, 0);
-          if (DT == QRE_BF16) {
-            big = fmaxf(big, fmaxf(fmaxf(fabsf(bits_to_float<DT>(x[k].x & 0xffffu)), fabsf(bits_to_float<DT>(x[k].x >> 16))),
-                                   fmaxf(fabsf(bits_to_float<DT>(x[k].y & 0xffffu)), fabsf(bits_to_float<DT>(x[k].y >> 16)))));
-          }
-        }
-        float f = 1.0f;
-        if (DT == QRE_BF16) {
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // largest element to [2^14, 2^15): exact but for elements 2^-29 times smaller, which round to 2^-39 of it
-          const int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
-          const int up = e >= 128 || big == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
-          f = __uint_as_float((uint32_t)(up + 127) << 23);
-          s2[hh] *= __uint_as_float((uint32_t)(127 - up) << 23);
-        }
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          if (DT == QRE_BF16) {
-            qa[k][hh] = pack2<QRE_FP16>(bits_to_float<DT>(x[k].x & 0xffffu) * f, bits_to_float<DT>(x[k].x >> 16) * f);
-            qa[k][2 + hh] = pack2<QRE_FP16>(bits_to_float<DT>(x[k].y & 0xffffu) * f, bits_to_float<DT>(x[k].y >> 16) * f);
-          } else {
-            qa[k][hh] = x[k].x;
-            qa[k][2 + hh] = x[k].y;
-          }
-        }
-        const float ks = c.k_scale ? c.k_scale[si + hk] : 1.0f;
-        s2[hh] *= ks;
+          for (int e = 0; e < 2; ++e)
+            big = fmaxf(big, fmaxf(fabsf(bits_to_float<DT>(qw[k][nh][e] & 0xffffu)), fabsf(bits_to_float<DT>(qw[k][nh][e] >> 16))));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // largest element to [2^14, 2^15): exact but for elements 2^-29 times smaller, which round to 2^-39 of it
+        const int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
+        const int up = e >= 128 || big == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
+        f = __uint_as_float((uint32_t)(up + 127) << 23);
+        own *= __uint_as_float((uint32_t)(127 - up) << 23);
       }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qb[k][nh][e] = K::F8 && DT == QRE_BF16
+                             ? pack2<QRE_FP16>(bits_to_float<DT>(qw[k][nh][e] & 0xffffu) * f, bits_to_float<DT>(qw[k][nh][e] >> 16) * f)
+                             : qw[k][nh][e];
+      s2[nh][0] = __shfl_sync(0xffffffffu, own, 8 * j4);
+      s2[nh][1] = __shfl_sync(0xffffffffu, own, 8 * j4 + 4);
     }
 
-    float acc[D / 8][4];
+    float acc[D / 16][NH][4];        // O^T: dimensions by heads 2 j, 2 j + 1
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) acc[i][nh][0] = acc[i][nh][1] = acc[i][nh][2] = acc[i][nh][3] = 0.0f;
+    float m[NH][2], l[NH][2];        // reference (base 2) and this lane's share of the sum
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      m[nh][0] = m[nh][1] = -INFINITY;
+      l[nh][0] = l[nh][1] = 0.0f;
+    }
 
     for (; next < s1; next += kWarps) {
       fetch(slot_in);
       slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
       if (stages == 2) cp_async_wait_group<1>();
-      else if (stages == 3) cp_async_wait_group<2>();
-      else cp_async_wait_group<3>();
+      else cp_async_wait_group<2>();
       __syncwarp();
       const uint32_t kt = smem_addr(ring + (size_t)slot * 2 * kTile), vt = kt + kTile;
-
-      float s[NT][4];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
       const int m8 = lane >> 3, l8 = lane & 7;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-#pragma unroll
-        for (int p = 0; p < K::PR / 4; ++p) {
-          uint32_t b[4];
-          ldmatrix_x4(b, kt + K::at(8 * i + l8, 4 * p + m8));
-          if (!K::F8) {
-            mma16816<K::BF>(s[i], qa[2 * p], b[0], b[1]);
-            mma16816<K::BF>(s[i], qa[2 * p + 1], b[2], b[3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma16816<false>(s[i], qa[4 * p + e], e4m3x2_to_half2(b[e] & 0xffffu), e4m3x2_to_half2(b[e] >> 16));
-          }
-        }
-      }
 
-      // scores in base 2, with what is not seen at -inf
-      const int pos0 = (lo / CK + (int)(next - u0)) * CK;
-      const uint32_t gone = (missing >> (K::NP * slot)) & ((1u << K::NP) - 1u);
-      const bool edge = pos0 < lo || pos0 + CK > len || gone;
-      float mx[2] = {-INFINITY, -INFINITY};
+      float s[K::NP][NH][4];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int i = 0; i < K::NP; ++i) {
 #pragma unroll
-        for (int e = 0; e < (HI ? 4 : 2); ++e) {
-          float x = s[i][e] * s2[e >> 1];
-          if (edge) {
-            const int pos = pos0 + 8 * i + 2 * j4 + (e & 1);
-            if (pos < lo || pos >= len || ((gone >> (i >> 1)) & 1u)) x = -INFINITY;
-          }
-          s[i][e] = x;
-          mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
-      }
-      bool grow = false;
-      float f[2];
+        for (int nh = 0; nh < NH; ++nh) s[i][nh][0] = s[i][nh][1] = s[i][nh][2] = s[i][nh][3] = 0.0f;
+        // pieces p and p + 1 of 16 keys: keys 0-7 and 8-15 of each
 #pragma unroll
-      for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
-        mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(0xffffffffu, mx[hh], 1));
-        mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(0xffffffffu, mx[hh], 2));
-        const float m2 = fmaxf(m[hh], mx[hh]);
-        f[hh] = m[hh] == m2 ? 1.0f : ex2(m[hh] - m2);   // 2^-inf = 0 for the first keys
-        grow |= m[hh] != m2;
-        m[hh] = m2;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
+        for (int p = 0; p < K::PR; p += 2) {
+          uint32_t x[4];
+          ldmatrix_x4(x, kt + K::at(16 * i + 8 * (m8 & 1) + l8, p + (m8 >> 1)));
 #pragma unroll
-        for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
-          l[hh] *= f[hh];
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            acc[i][2 * hh] *= f[hh];
-            acc[i][2 * hh + 1] *= f[hh];
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-#pragma unroll
-        for (int e = 0; e < (HI ? 4 : 2); ++e) {
-          const float mm = m[e >> 1];
-          const float p = ex2(s[i][e] - (mm == -INFINITY ? 0.0f : mm));   // nothing seen so far: 2^-inf = 0
-          s[i][e] = p;
-          l[e >> 1] += p;
-        }
-      }
-      // O += P V: the weights are rounded to the products' type (the sum l keeps them in fp32)
-#pragma unroll
-      for (int kk = 0; kk < K::NP; ++kk) {
-        uint32_t pa[4];
-        pa[0] = pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk][0], s[2 * kk][1]);
-        pa[1] = HI ? pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk][2], s[2 * kk][3]) : 0;
-        pa[2] = pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk + 1][0], s[2 * kk + 1][1]);
-        pa[3] = HI ? pack2<K::BF ? QRE_BF16 : QRE_FP16>(s[2 * kk + 1][2], s[2 * kk + 1][3]) : 0;
-#pragma unroll
-        for (int p = 0; p < K::PR / 2; ++p) {
-          uint32_t b[4];   // pieces 2 p and 2 p + 1, keys 0-7 and 8-15 of each
-          ldmatrix_x4_trans(b, vt + K::at(16 * kk + 8 * (m8 & 1) + l8, 2 * p + (m8 >> 1)));
-          if (!K::F8) {
-            mma16816<K::BF>(acc[2 * p], pa, b[0], b[1]);
-            mma16816<K::BF>(acc[2 * p + 1], pa, b[2], b[3]);
-          } else {
-            // a register holds keys 2 j, 2 j + 1 of dimensions 2 c, 2 c + 1: sort by dimension
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = __byte_perm(b[2 * e], 0, 0x3120), y = __byte_perm(b[2 * e + 1], 0, 0x3120);
-              mma16816<false>(acc[4 * p + 2 * e], pa, e4m3x2_to_half2(x & 0xffffu), e4m3x2_to_half2(y & 0xffffu));
-              mma16816<false>(acc[4 * p + 2 * e + 1], pa, e4m3x2_to_half2(x >> 16), e4m3x2_to_half2(y >> 16));
+          for (int nh = 0; nh < NH; ++nh) {
+            if (!K::F8) {
+              mma16816<K::BF>(s[i][nh], x[0], x[1], x[2], x[3], qb[p / 2][nh]);
+            } else {
+              mma16816<false>(s[i][nh], e4m3x2_to_half2(x[0] & 0xffffu), e4m3x2_to_half2(x[1] & 0xffffu),
+                              e4m3x2_to_half2(x[0] >> 16), e4m3x2_to_half2(x[1] >> 16), qb[p][nh]);
+              mma16816<false>(s[i][nh], e4m3x2_to_half2(x[2] & 0xffffu), e4m3x2_to_half2(x[3] & 0xffffu),
+                              e4m3x2_to_half2(x[2] >> 16), e4m3x2_to_half2(x[3] >> 16), qb[p + 1][nh]);
             }
           }
         }
+      }
+
+      const int pos0 = (lo / CK + (int)(next - u0)) * CK;
+      const uint32_t gone = (missing >> (K::NP * slot)) & ((1u << K::NP) - 1u);
+      if (pos0 < lo || pos0 + CK > len || gone) {   // what is not seen: -inf
+#pragma unroll
+        for (int i = 0; i < K::NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int pos = pos0 + 16 * i + 4 * e + r4;
+            if (pos < lo || pos >= len || ((gone >> i) & 1u)) {
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) s[i][nh][e] = s[i][nh][e + 1] = -INFINITY;
+            }
+          }
+      }
+      float p[K::NP][NH][4], sum[NH][2];
+      auto weights = [&]() {
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+          sum[nh][0] = sum[nh][1] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < K::NP; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float mm = m[nh][e & 1];
+              p[i][nh][e] = ex2(fmaf(s[i][nh][e], s2[nh][e & 1], mm == -INFINITY ? 0.0f : -mm));
+              sum[nh][e & 1] += p[i][nh][e];
+            }
+        }
+      };
+      weights();
+      bool redo = false;
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) redo |= m[nh][e] == -INFINITY || sum[nh][e] > K::kMost;
+      if (__any_sync(0xffffffffu, redo)) {   // the reference moves to the maximum so far
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < K::NP; ++i) mx = fmaxf(mx, fmaxf(s[i][nh][e], s[i][nh][e + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float to = fmaxf(m[nh][e], mx * s2[nh][e]);
+            const float f = m[nh][e] == to ? 1.0f : ex2(m[nh][e] - to);   // 2^-inf = 0 for the first keys
+            m[nh][e] = to;
+            l[nh][e] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              acc[i][nh][e] *= f;
+              acc[i][nh][e + 2] *= f;
+            }
+          }
+        weights();
+      }
+      // O^T += V^T P^T: the weights are rounded to the products' type (the sum l keeps them in fp32)
+#pragma unroll
+      for (int i = 0; i < K::NP; ++i) {
+        uint32_t pb[NH][2];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+          pb[nh][0] = movmatrix(pack2<K::PT>(p[i][nh][0], p[i][nh][1]));
+          pb[nh][1] = movmatrix(pack2<K::PT>(p[i][nh][2], p[i][nh][3]));
+        }
+#pragma unroll
+        for (int d = 0; d < K::PR; d += 2) {
+          uint32_t x[4];
+          if (!K::F8) {
+            // 16 dimensions: pieces d and d + 1 of keys 0-7, then of keys 8-15
+            ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 >> 1) + l8, d + (m8 & 1)));
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) mma16816<K::BF>(acc[d / 2][nh], x[0], x[1], x[2], x[3], pb[nh]);
+          } else {
+            // piece d of keys 0-7 and 8-15, then piece d + 1; a register holds keys 2 j, 2 j + 1 of dimensions
+            // 2 r, 2 r + 1: row r of the product is dimension 2 r, row r + 8 dimension 2 r + 1
+            ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 & 1) + l8, d + (m8 >> 1)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t y0 = __byte_perm(x[2 * e], 0, 0x3120), y1 = __byte_perm(x[2 * e + 1], 0, 0x3120);
+              const uint32_t a0 = e4m3x2_to_half2(y0 & 0xffffu), a1 = e4m3x2_to_half2(y0 >> 16);
+              const uint32_t a2 = e4m3x2_to_half2(y1 & 0xffffu), a3 = e4m3x2_to_half2(y1 >> 16);
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma16816<false>(acc[d + e][nh], a0, a1, a2, a3, pb[nh]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+        l[nh][0] += sum[nh][0];
+        l[nh][1] += sum[nh][1];
       }
       slot = slot + 1 == stages ? 0 : slot + 1;
       __syncwarp();
     }
 
-    // ---- end of the unit in this range: join the warps
-#pragma unroll
-    for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
-      l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
-      l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-      if (j4 == 0) ml[warp * kRows + r0 + 8 * hh] = make_float2(m[hh], l[hh]);
+    // ---- end of the unit in this range: join the warps (the next unit's queries come meanwhile)
+    Place np = cp;
+    if (s1 < c1) {
+      advance(np, (int)(s1 - s0));
+      ask_queries(np);
     }
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nh][e] += __shfl_xor_sync(0xffffffffu, l[nh][e], d);
+        if (r4 == 0) ml[warp * kRows + 8 * nh + 2 * j4 + e] = make_float2(m[nh][e], l[nh][e]);
+      }
     const bool whole = s0 == u0 && s1 == u1;
     float* part = parts + ((size_t)2 * blockIdx.x + (s0 == c0 ? 0 : 1)) * kRows * (D + 2);
-    const float vs = K::F8 && c.v_scale ? c.v_scale[si + hk] : 1.0f;
+    // eight heads by 64 dimensions at a time
 #pragma unroll
-    for (int hh = 0; hh < (HI ? 2 : 1); ++hh) {
-      if (r0 < buf_rows) {
-        float* b = buf + (size_t)(warp * buf_rows + r0) * D;
-        const int x = (r0 & 3) * 8;   // spreads the rows over the banks
+    for (int pass = 0; pass < NH * (D / 64); ++pass) {
+      const int nh = pass / (D / 64), half = pass % (D / 64);
+      float* b = buf + (size_t)warp * 8 * 64;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          if (!K::F8) {
-            *reinterpret_cast<float2*>(b + ((8 * i + 2 * j4) ^ x)) = make_float2(acc[i][2 * hh], acc[i][2 * hh + 1]);
-          } else if (!(i & 1)) {
-            // dimensions 16 p + 4 j .. + 3 (p = i / 2)
-            *reinterpret_cast<float4*>(b + ((8 * i + 4 * j4) ^ x)) =
-                make_float4(acc[i][2 * hh], acc[i + 1][2 * hh], acc[i][2 * hh + 1], acc[i + 1][2 * hh + 1]);
-          }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // heads are spread over the banks by permuting eights of dimensions
+          const int d0 = 16 * i + (K::F8 ? 2 * r4 : r4), d1 = 16 * i + (K::F8 ? 2 * r4 + 1 : r4 + 8), x = 8 * j4;
+          b[(2 * j4 + e) * 64 + (d0 ^ x)] = acc[4 * half + i][nh][e];
+          b[(2 * j4 + e) * 64 + (d1 ^ x)] = acc[4 * half + i][nh][e + 2];
         }
-      }
       __syncthreads();
-      for (int i = tid; i < buf_rows * (D / 4); i += kThreads) {
-        const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4, r = rr + 8 * hh;
-        if (r >= rows) continue;
-        float M = -INFINITY;
+      {
+        const int rr = tid >> 4, d = (tid & 15) * 4, r = rr + 8 * nh, dd = 64 * half + d;
+        if (r < rows) {
+          float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
-        float L = 0.0f;
-        float4 sum = make_float4(0, 0, 0, 0);
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+          float L = 0.0f;
+          float4 sum = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 e = ml[w * kRows + r];
-          // a warp that saw nothing (m = -inf, l = 0) counts nothing; a NaN in l stays one
-          const float f = e.x == -INFINITY && e.y == 0.0f ? 0.0f : ex2(e.x - M);
-          const float4 x = *reinterpret_cast<const float4*>(buf + (size_t)(w * buf_rows + rr) * D + (d ^ ((rr & 3) * 8)));
-          L += e.y * f;
-          sum.x += x.x * f;
-          sum.y += x.y * f;
-          sum.z += x.z * f;
-          sum.w += x.w * f;
-        }
-        if (whole) {
-          const float inv = L == 0.0f ? 0.0f : vs / L;
-          *reinterpret_cast<uint2*>(o + (size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + d) =
-              make_uint2(pack2<DT>(sum.x * inv, sum.y * inv), pack2<DT>(sum.z * inv, sum.w * inv));
-          if (lse && d == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
-        } else {
-          *reinterpret_cast<float4*>(part + r * D + d) = sum;
-          if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(M, L);
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 e = ml[w * kRows + r];
+            // a warp that saw nothing (m = -inf, l = 0) counts nothing; a NaN in l stays one
+            const float f = e.x == -INFINITY && e.y == 0.0f ? 0.0f : ex2(e.x - M);
+            const float4 x = *reinterpret_cast<const float4*>(buf + (size_t)(w * 8 + rr) * 64 + (d ^ (8 * (rr >> 1))));
+            L += e.y * f;
+            sum.x += x.x * f;
+            sum.y += x.y * f;
+            sum.z += x.z * f;
+            sum.w += x.w * f;
+          }
+          if (whole) {
+            const float inv = L == 0.0f ? 0.0f : vs / L;
+            *reinterpret_cast<uint2*>(o + (size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + dd) =
+                make_uint2(pack2<DT>(sum.x * inv, sum.y * inv), pack2<DT>(sum.z * inv, sum.w * inv));
+            if (lse && dd == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+          } else {
+            *reinterpret_cast<float4*>(part + r * D + dd) = sum;
+            if (dd == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(M, L);
+          }
         }
       }
       __syncthreads();
@@ -555,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cuts[blockIdx.x] = ci;
     }
     s0 = s1;
-    if (s0 < c1) advance(cp, (int)(s1 - u0) - cp.ck);
+    cp = np;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -623,7 +678,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 
 int decode_grid() {
   const int sms = device_sm_count();
-  return sms <= 0 ? 152 : (sms < kMaxParts ? sms : kMaxParts);   // one CTA per SM
+  const int n = (sms <= 0 ? 152 : sms) * kCtasPerSm;
+  return n < kMaxParts ? n : kMaxParts;
 }
 
 size_t cut_bytes(int grid) { return ((size_t)grid * sizeof(CutInfo) + 255) & ~(size_t)255; }
@@ -640,12 +696,12 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
                                cudaStream_t stream) {
   const int grid = decode_grid();
   const int g = a.n_heads / a.n_kv_heads;
-  const int buf_rows = g < 8 ? g : 8;
-  const size_t fixed = (size_t)kWarps * buf_rows * a.head_dim * sizeof(float) + kWarps * kRows * sizeof(float2) +
+  const size_t fixed = (size_t)kWarps * 8 * 64 * sizeof(float) + kWarps * kRows * sizeof(float2) +
                        (size_t)(n + 1) * sizeof(Seq);
-  const long long room = (long long)device_max_smem_optin() - 256 - (long long)fixed;
+  // what the CTAs of an SM share (1 KB of each is the system's, and the kernel's static arrays)
+  const long long room = ((long long)device_max_smem_optin() + 1024) / kCtasPerSm - 1024 - 128 - (long long)fixed;
   int stages = (int)(room / (kWarps * 2 * kTile));
-  stages = stages < 2 ? 2 : (stages > 3 ? 3 : stages);
+  stages = stages < 2 ? 2 : (stages > 3 ? 3 : stages);   // a long list takes room: then one CTA has the SM
   const size_t smem = (size_t)stages * kWarps * 2 * kTile + fixed;
   CutInfo* cuts = static_cast<CutInfo*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + cut_bytes(grid));
@@ -654,16 +710,15 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3(grid), dim3(kThreads), smem, stream, a, c, layer, n, seqs,
-                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, cuts, parts, stages,
-                         buf_rows, status);
+                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, cuts, parts, stages, status);
     if (e != cudaSuccess || grid < 2) return e;
     return launch_dependent(join, dim3(grid - 1), dim3(256), 0, stream, a, v_scale, static_cast<uint16_t*>(o), lse,
                             const_cast<const CutInfo*>(cuts), const_cast<const float*>(parts));
   };
   auto pick = [&](auto dt, auto ct, auto d) {
     constexpr int DT = decltype(dt)::value, CT = decltype(ct)::value, D = decltype(d)::value;
-    return g > 8 ? go(attn_decode_kernel<DT, CT, D, true>, attn_join_kernel<DT, D>)
-                 : go(attn_decode_kernel<DT, CT, D, false>, attn_join_kernel<DT, D>);
+    return g > 8 ? go(attn_decode_kernel<DT, CT, D, 2>, attn_join_kernel<DT, D>)
+                 : go(attn_decode_kernel<DT, CT, D, 1>, attn_join_kernel<DT, D>);
   };
   using B = std::integral_constant<int, QRE_BF16>;
   using H = std::integral_constant<int, QRE_FP16>;
