@@ -12,23 +12,22 @@
 //
 // Work split.  A chunk is CK positions of one KV head (K and V, 8 KB together);
 // the chunks of all (sequence, KV head) units in a row are cut into equal
-// contiguous ranges, one per CTA, whatever the lengths are; a CTA's eight warps
-// take the chunks of its range in turn.  The lengths stay on the device: every
-// CTA sums them up for itself.  A unit that lies inside one range is finished
-// there; one that is cut leaves a part (o, m, l in fp32) per CTA in the
-// workspace, and a second, dependent launch joins the parts in the order of the
-// CTAs, so results do not depend on timing.
+// contiguous ranges, one per warp of the grid, whatever the lengths are.  The
+// lengths stay on the device: every CTA sums them up for itself.  A unit that lies
+// inside one range is finished there; one that is cut leaves a part (o, m, l in
+// fp32) per range in the workspace, and a second, dependent launch joins the
+// parts in the order of the ranges, so results do not depend on timing.
 //
-// A warp runs on its own between the ends of units: it fills a ring of chunks in
-// shared memory with cp.async (16-byte pieces, rows that are not seen zero-filled,
+// A warp runs on its own, with no barrier (with ranges of CTAs, whose warps met at
+// the end of every unit, 256 sequences of up to 1500 positions took 57 us instead
+// of 53): it fills a ring of chunks in shared memory with cp.async (16-byte pieces, rows that are not seen zero-filled,
 // so what they hold never reaches a product) and multiplies with mma.sync
 // (m16n8k16), keys and dimensions on the 16 side, heads on the 8 side:
 //   S^T = K Q^T (16 keys x 8 heads), O^T += V^T P^T (16 dimensions x 8 heads);
 // P turns from the first product's layout into the second's by one 8 x 8
 // transpose (movmatrix).  Nothing is padding with 8 heads per KV head; tcgen05
 // would want 128 rows.  More than 16 heads per KV head run as several units over
-// the same keys, which then come from L2.  Two CTAs share an SM, so that one
-// streams while the other joins its warps at the end of a unit.
+// the same keys, which then come from L2.
 // A unit's first chunk sets the reference of its weights; later ones look for no
 // maximum (and shuffle nothing) unless a sum of weights grows too large.
 // An E4M3 cache is multiplied as fp16, which holds every E4M3 value; a bf16 query
@@ -48,17 +47,21 @@ constexpr int kCtasPerSm = 2;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk
 constexpr int kRows = 16;             // query heads of a unit at most
-constexpr int kMaxParts = 1024;       // CTAs of the main kernel at most
+constexpr int kMaxCtas = 1024;        // of the main kernel
+constexpr int kMinChunks = 2;         // of a range: fewer would save nothing and leave more parts to join
 
-// What CTA b of the main kernel leaves for the join, in the workspace.
-struct CutInfo {
-  long long u0, u1;   // chunks of the unit that range b begins in; u0 < begin of range b iff the unit is cut there
+// What the main kernel leaves for the join, in the workspace.
+struct Header {
   long long total;    // chunks of the call
-  int t, block;       // query and head block of the unit
-  int ctas, valid;
-};
+  int ranges, pad;
+};                    // followed at kFirstsAt by the chunks before each query, n + 1 int32
+constexpr int kFirstsAt = 256;
 
-__device__ __forceinline__ long long range_begin(int c, int ctas, long long total) { return total * c / ctas; }
+__device__ __forceinline__ long long range_begin(int b, int ranges, long long total) { return total * b / ranges; }
+// The range that chunk i lies in: the last b with total b / ranges < i + 1.
+__device__ __forceinline__ int range_of(long long i, int ranges, long long total) {
+  return (int)(((i + 1) * ranges - 1) / total);
+}
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
   const int bytes = valid ? 16 : 0;
@@ -124,6 +127,12 @@ struct Decode {
   }
 };
 
+// Floats of a part: eight heads at a time by D, and (m, l) of each head.
+template <int D, int NH>
+constexpr int part_floats() {
+  return 8 * NH * (D + 2);
+}
+
 struct Seq {
   int row, len, first;   // table row, length, chunks of the queries before
 };
@@ -132,15 +141,13 @@ template <int DT, int CT, int D, int NH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
                        const int32_t* __restrict__ seqs, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
-                       float* __restrict__ lse, CutInfo* __restrict__ cuts, float* __restrict__ parts, int stages,
+                       float* __restrict__ lse, Header* __restrict__ header, float* __restrict__ parts, int stages,
                        int* status) {
   using K = Decode<DT, CT, D, NH>;
   constexpr int CK = K::CK, KS = K::KS;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + (size_t)(threadIdx.x >> 5) * stages * 2 * kTile;   // this warp's
-  float* buf = reinterpret_cast<float*>(smem + (size_t)kWarps * stages * 2 * kTile);   // [kWarps][8][64]
-  float2* ml = reinterpret_cast<float2*>(buf + kWarps * 8 * 64);                       // [kWarps][kRows]
-  Seq* sq = reinterpret_cast<Seq*>(ml + kWarps * kRows);                               // [n + 1]
+  Seq* sq = reinterpret_cast<Seq*>(smem + (size_t)kWarps * stages * 2 * kTile);   // [n + 1]
   __shared__ int scan_part[kWarps];
   __shared__ int scan_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -153,25 +160,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   grid_dependents_launch();
 
   // ---- the plan: chunks of every query, summed up
+  constexpr int kEach = 4;   // queries of a thread at a time: their loads are in flight together
   int before = 0;
-  for (int t0 = 0; t0 < n; t0 += kThreads) {
-    const int t = t0 + tid;
-    int row = 0, len = 0, ch = 0;
-    if (t < n) {
-      row = seqs ? seqs[t] : t;
-      bool bad = row < 0 || row >= c.max_seqs;
-      if (!bad) {
-        len = c.seq_len[row];
-        bad = len < 0 || len > (long long)c.max_pages * c.page_size;
-      }
-      if (bad) {
-        if (blockIdx.x == 0) set_status(status, QRE_DEV_BAD_INDEX);
-        len = row = 0;
-      }
-      const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
-      ch = len > 0 ? (len + CK - 1) / CK - lo / CK : 0;
+  for (int t0 = 0; t0 < n; t0 += kEach * kThreads) {
+    int row[kEach], len[kEach], ch[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = t0 + kEach * tid + i;
+      row[i] = t < n ? (seqs ? seqs[t] : t) : -1;
     }
-    int inc = ch;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) len[i] = row[i] >= 0 && row[i] < c.max_seqs ? c.seq_len[row[i]] : -1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (len[i] < 0 || len[i] > (long long)c.max_pages * c.page_size) {
+        if (blockIdx.x == 0 && t0 + kEach * tid + i < n) set_status(status, QRE_DEV_BAD_INDEX);
+        len[i] = row[i] = 0;
+      }
+      const int lo = a.window > 0 && len[i] > a.window ? len[i] - a.window : 0;
+      ch[i] = len[i] > 0 ? (len[i] + CK - 1) / CK - lo / CK : 0;
+      mine += ch[i];
+    }
+    int inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, inc, d);
@@ -179,23 +189,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     if (lane == 31) scan_part[warp] = inc;
     __syncthreads();
-    int base = before;
-    for (int w = 0; w < warp; ++w) base += scan_part[w];
-    if (t < n) {
-      sq[t].row = row;
-      sq[t].len = len;
-      sq[t].first = base + inc - ch;
+    int first = before + inc - mine;
+    for (int w = 0; w < warp; ++w) first += scan_part[w];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = t0 + kEach * tid + i;
+      if (t < n) sq[t] = Seq{row[i], len[i], first};
+      first += ch[i];
     }
-    if (tid == kThreads - 1) scan_total = base + inc;
+    if (tid == kThreads - 1) scan_total = first;
     __syncthreads();
     before = scan_total;
   }
   if (tid == 0) sq[n].first = before;
   __syncthreads();
   const long long total = (long long)before * units;
-  // ranges of at least one chunk per warp
-  const long long want = (total + kWarps - 1) / kWarps;
-  const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
+  const long long want = (total + kMinChunks - 1) / kMinChunks, all = (long long)gridDim.x * kWarps;
+  const int ranges = (int)(want < all ? want : all);
+  const int me = warp * (int)gridDim.x + blockIdx.x;   // this warp's range: few ranges spread over the SMs
 
   // queries that see nothing
   for (int t = blockIdx.x; t < n; t += gridDim.x) {
@@ -207,11 +218,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (lse)
       for (int h = tid; h < a.n_heads; h += kThreads) lse[(size_t)t * a.n_heads + h] = -INFINITY;
   }
-  if ((int)blockIdx.x >= ctas) {
-    if (tid == 0) cuts[blockIdx.x].valid = 0;
-    return;
+  if (blockIdx.x == 0) {
+    if (tid == 0) *header = Header{total, ranges, 0};
+    int32_t* firsts = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(header) + kFirstsAt);
+    for (int t = tid; t <= n; t += kThreads) firsts[t] = sq[t].first;
   }
-  const long long c0 = range_begin(blockIdx.x, ctas, total), c1 = range_begin(blockIdx.x + 1, ctas, total);
+  if (me >= ranges) return;
+  const long long c0 = range_begin(me, ranges, total), c1 = range_begin(me + 1, ranges, total);
 
   // the query that chunk c0 belongs to
   int t_first;
@@ -254,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   };
 
-  // ---- loader: this warp's chunks c0 + warp, c0 + warp + kWarps, ...
-  long long li = c0 + warp;          // next chunk to fetch
+  // ---- loader
+  long long li = c0;                 // next chunk to fetch
   Place lp = li < c1 ? place_of(li, t_first) : Place{0, 0, 0, 1};
   int pages = 0;                     // lane j: page of positions 16 j .. 16 j + 15 of that chunk, -1 missing, -2 not seen
   auto look_up = [&]() {
@@ -302,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           cp_async_16_zfill(dst + kTile + K::at(row, col), pool_v + off, ok);
         }
       }
-      li += kWarps;
-      if (li < c1) advance(lp, kWarps);
+      ++li;
+      if (li < c1) advance(lp, 1);
       look_up();
     }
     cp_async_commit();
@@ -348,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   long long s0 = c0;
   Place cp = place_of(c0, t_first);
   ask_queries(cp);
-  long long next = c0 + warp;        // this warp's next chunk to compute
   while (s0 < c1) {
     const long long u0 = s0 - cp.ck, u1 = u0 + cp.nch;
     const long long s1 = u1 < c1 ? u1 : c1;
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       l[nh][0] = l[nh][1] = 0.0f;
     }
 
-    for (; next < s1; next += kWarps) {
+    for (long long next = s0; next < s1; ++next) {
       fetch(slot_in);
       slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
       if (stages == 2) cp_async_wait_group<1>();
@@ -534,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       __syncwarp();
     }
 
-    // ---- end of the unit in this range: join the warps (the next unit's queries come meanwhile)
+    // ---- end of the unit in this range (the next unit's queries come meanwhile)
     Place np = cp;
     if (s1 < c1) {
       advance(np, (int)(s1 - s0));
@@ -543,71 +555,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nh][e] += __shfl_xor_sync(0xffffffffu, l[nh][e], d);
-        if (r4 == 0) ml[warp * kRows + 8 * nh + 2 * j4 + e] = make_float2(m[nh][e], l[nh][e]);
-      }
-    const bool whole = s0 == u0 && s1 == u1;
-    float* part = parts + ((size_t)2 * blockIdx.x + (s0 == c0 ? 0 : 1)) * kRows * (D + 2);
-    // eight heads by 64 dimensions at a time
+    if (s0 == u0 && s1 == u1) {   // whole: o = O / l, transposed so that a lane has neighbouring dimensions of head lane / 4
 #pragma unroll
-    for (int pass = 0; pass < NH * (D / 64); ++pass) {
-      const int nh = pass / (D / 64), half = pass % (D / 64);
-      float* b = buf + (size_t)warp * 8 * 64;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int nh = 0; nh < NH; ++nh) {
+        float inv[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // heads are spread over the banks by permuting eights of dimensions
-          const int d0 = 16 * i + (K::F8 ? 2 * r4 : r4), d1 = 16 * i + (K::F8 ? 2 * r4 + 1 : r4 + 8), x = 8 * j4;
-          b[(2 * j4 + e) * 64 + (d0 ^ x)] = acc[4 * half + i][nh][e];
-          b[(2 * j4 + e) * 64 + (d1 ^ x)] = acc[4 * half + i][nh][e + 2];
+          inv[e] = l[nh][e] == 0.0f ? 0.0f : vs / l[nh][e];
+          const int r = 8 * nh + 2 * j4 + e;
+          if (lse && r4 == 0 && r < rows)
+            lse[(size_t)t * a.n_heads + h0 + r] = l[nh][e] == 0.0f ? -INFINITY : m[nh][e] * kLn2 + logf(l[nh][e]);
         }
-      __syncthreads();
-      {
-        const int rr = tid >> 4, d = (tid & 15) * 4, r = rr + 8 * nh, dd = 64 * half + d;
-        if (r < rows) {
-          float M = -INFINITY;
+        const int r = 8 * nh + r4;
+        uint16_t* out = o + (size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
-          float L = 0.0f;
-          float4 sum = make_float4(0, 0, 0, 0);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 e = ml[w * kRows + r];
-            // a warp that saw nothing (m = -inf, l = 0) counts nothing; a NaN in l stays one
-            const float f = e.x == -INFINITY && e.y == 0.0f ? 0.0f : ex2(e.x - M);
-            const float4 x = *reinterpret_cast<const float4*>(buf + (size_t)(w * 8 + rr) * 64 + (d ^ (8 * (rr >> 1))));
-            L += e.y * f;
-            sum.x += x.x * f;
-            sum.y += x.y * f;
-            sum.z += x.z * f;
-            sum.w += x.w * f;
-          }
-          if (whole) {
-            const float inv = L == 0.0f ? 0.0f : vs / L;
-            *reinterpret_cast<uint2*>(o + (size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + dd) =
-                make_uint2(pack2<DT>(sum.x * inv, sum.y * inv), pack2<DT>(sum.z * inv, sum.w * inv));
-            if (lse && dd == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
-          } else {
-            *reinterpret_cast<float4*>(part + r * D + dd) = sum;
-            if (dd == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(M, L);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t x = movmatrix(pack2<DT>(acc[i][nh][0] * inv[0], acc[i][nh][1] * inv[1]));
+          const uint32_t y = movmatrix(pack2<DT>(acc[i][nh][2] * inv[0], acc[i][nh][3] * inv[1]));
+          if (r < rows) {
+            if (K::F8) {   // x: dimensions 4 j, 4 j + 2; y: 4 j + 1, 4 j + 3
+              *reinterpret_cast<uint2*>(out + 16 * i + 4 * j4) = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+            } else {
+              *reinterpret_cast<uint32_t*>(out + 16 * i + 2 * j4) = x;
+              *reinterpret_cast<uint32_t*>(out + 16 * i + 8 + 2 * j4) = y;
+            }
           }
         }
       }
-      __syncthreads();
-    }
-    if (s0 == c0 && tid == 0) {
-      CutInfo ci;
-      ci.u0 = u0;
-      ci.u1 = u1;
-      ci.total = total;
-      ci.t = t;
-      ci.block = cp.unit;
-      ci.ctas = ctas;
-      ci.valid = 1;
-      cuts[blockIdx.x] = ci;
+    } else {                      // a part, as it lies in the registers
+      float* part = parts + ((size_t)2 * me + (s0 == c0 ? 0 : 1)) * part_floats<D, NH>();
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[((i * NH + nh) * 4 + e) * 32 + lane] = acc[i][nh][e];
+      float2* ml = reinterpret_cast<float2*>(part + 8 * NH * D);
+      if (r4 == 0)
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ml[8 * nh + 2 * j4 + e] = make_float2(m[nh][e], l[nh][e]);
     }
     s0 = s1;
     cp = np;
@@ -615,80 +606,130 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Joins the parts of the units that were cut: CTA b takes the unit that the begin
-// of range b cuts, if no earlier begin cuts it too.
-template <int DT, int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ qre_attn a,
+// Joins the parts of a unit that was cut, with a running maximum and sum.  A thread
+// has four outputs of the unit, the heads 8 nh + odd + 2 j of one dimension, as the
+// parts lie in memory.  SPLIT: a CTA has 32 such groups and its warps take the
+// parts in turn and meet in shared memory (few units, many parts each); else a
+// thread goes through all parts.  blockIdx.x is the unit (by_cut == 0), or the begin
+// of a range: then the unit that it cuts, if no earlier begin cuts it too.
+template <int DT, bool F8, int D, int NH, bool SPLIT>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ qre_attn a, int n, int by_cut,
                                                         const float* __restrict__ v_scale, uint16_t* __restrict__ o,
-                                                        float* __restrict__ lse, const CutInfo* __restrict__ cuts,
+                                                        float* __restrict__ lse, const Header* __restrict__ header,
                                                         const float* __restrict__ parts) {
-  __shared__ float2 ml[kRows];
+  constexpr int PF = part_floats<D, NH>();
   grid_dependency_wait();
   grid_dependents_launch();
-  const int b = blockIdx.x + 1;
-  const CutInfo ci = cuts[b];
-  if (!ci.valid) return;
-  if (ci.u0 >= range_begin(b, ci.ctas, ci.total) || range_begin(b - 1, ci.ctas, ci.total) > ci.u0) return;
-  int e = b;   // last range of the unit
-  while (e + 1 < ci.ctas && range_begin(e + 1, ci.ctas, ci.total) < ci.u1) ++e;
-  const int g = a.n_heads / a.n_kv_heads, blocks = (g + kRows - 1) / kRows;
-  const int hk = ci.block / blocks, h0 = hk * g + (ci.block - hk * blocks) * kRows;
-  const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
-  // part of range c: its first slot when the unit's share begins the range, else its second
-  auto part = [&](int c) {
-    return parts + ((size_t)2 * c + (ci.u0 <= range_begin(c, ci.ctas, ci.total) ? 0 : 1)) * kRows * (D + 2);
-  };
-  const float vs = v_scale ? v_scale[hk] : 1.0f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < rows; r += 8) {
-    float M = -INFINITY, L = 0.0f;
-    for (int c = b - 1 + lane; c <= e; c += 32) M = fmaxf(M, part(c)[kRows * D + 2 * r]);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    for (int c = b - 1 + lane; c <= e; c += 32) {
-      const float2 x = *reinterpret_cast<const float2*>(part(c) + kRows * D + 2 * r);
-      L += x.x == -INFINITY && x.y == 0.0f ? 0.0f : x.y * ex2(x.x - M);
+  const Header h = *header;
+  if (h.total == 0) return;
+  const int32_t* firsts = reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(header) + kFirstsAt);
+  const int g = a.n_heads / a.n_kv_heads, blocks = (g + kRows - 1) / kRows, units = a.n_kv_heads * blocks;
+  int t, unit;
+  long long u0;
+  int nch;
+  if (!by_cut) {
+    t = blockIdx.x / units;
+    unit = blockIdx.x - t * units;
+    nch = firsts[t + 1] - firsts[t];
+    u0 = (long long)firsts[t] * units + (long long)unit * nch;
+    if (nch == 0) return;
+  } else {
+    const int b = blockIdx.x + 1;
+    if (b >= h.ranges) return;
+    const long long x = range_begin(b, h.ranges, h.total);
+    int lo = 0, hi = n - 1;   // the last query that begins at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((long long)firsts[mid] * units <= x) lo = mid;
+      else hi = mid - 1;
     }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
-    if (lane == 0) ml[r] = make_float2(M, L);
+    t = lo;
+    nch = firsts[t + 1] - firsts[t];
+    const long long rest = x - (long long)firsts[t] * units;
+    unit = (int)(rest / nch);
+    u0 = x - (rest - (long long)unit * nch);
+    if (u0 == x || range_begin(b - 1, h.ranges, h.total) > u0) return;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
-    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-    const float M = ml[r].x, L = ml[r].y;
-    float4 sum = make_float4(0, 0, 0, 0);
+  const int b0 = range_of(u0, h.ranges, h.total), np = range_of(u0 + nch - 1, h.ranges, h.total) - b0 + 1;
+  if (np < 2) return;
+  // the first part lies in its range's first place when the unit begins there too; the others begin theirs
+  const float* first = parts + ((size_t)2 * b0 + (u0 == range_begin(b0, h.ranges, h.total) ? 0 : 1)) * PF;
+  const int hk = unit / blocks, h0 = hk * g + (unit - hk * blocks) * kRows;
+  const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slot = SPLIT ? 32 * blockIdx.y + lane : (int)blockDim.x * blockIdx.y + tid, reg = slot >> 3, r0 = 8 * ((reg >> 2) % NH) + (reg & 1);
+  float m[4], l[4], x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = -INFINITY;
+    l[j] = x[j] = 0.0f;
+  }
 #pragma unroll 4
-    for (int c = b - 1; c <= e; ++c) {
-      const float* p = part(c);
-      const float2 x = *reinterpret_cast<const float2*>(p + kRows * D + 2 * r);
-      const float4 y = *reinterpret_cast<const float4*>(p + r * D + d);
-      const float f = x.x == -INFINITY && x.y == 0.0f ? 0.0f : ex2(x.x - M);
-      sum.x += y.x * f;
-      sum.y += y.y * f;
-      sum.z += y.z * f;
-      sum.w += y.w * f;
+  for (int i = SPLIT ? warp : 0; i < np; i += SPLIT ? 8 : 1) {
+    const float* part = i == 0 ? first : parts + (size_t)2 * (b0 + i) * PF;
+    const float4 y4 = *reinterpret_cast<const float4*>(part + 4 * slot);
+    const float y[4] = {y4.x, y4.y, y4.z, y4.w};
+    const float2* ml = reinterpret_cast<const float2*>(part + 8 * NH * D);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 e = ml[r0 + 2 * j];
+      const float to = fmaxf(m[j], e.x);
+      // what saw nothing (m = -inf) counts nothing; a NaN in l stays one
+      const float f = m[j] == to ? 1.0f : ex2(m[j] - to), fe = e.x == to ? 1.0f : ex2(e.x - to);
+      m[j] = to;
+      l[j] = l[j] * f + e.y * fe;
+      x[j] = x[j] * f + y[j] * fe;
     }
-    const float inv = L == 0.0f ? 0.0f : vs / L;
-    *reinterpret_cast<uint2*>(o + (size_t)ci.t * a.o_token + (size_t)(h0 + r) * a.o_head + d) =
-        make_uint2(pack2<DT>(sum.x * inv, sum.y * inv), pack2<DT>(sum.z * inv, sum.w * inv));
-    if (lse && d == 0) lse[(size_t)ci.t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+  }
+  const float vs = v_scale ? v_scale[hk] : 1.0f;
+  auto write = [&](int sl, int j, float M, float L, float X) {
+    const int rg = sl >> 3, i = (rg >> 2) / NH, high = (rg >> 1) & 1;
+    const int r = 8 * ((rg >> 2) % NH) + (rg & 1) + 2 * j, d = 16 * i + (F8 ? 2 * (sl & 7) + high : (sl & 7) + 8 * high);
+    if (r >= rows) return;
+    o[(size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + d] =
+        (uint16_t)pack2<DT>(L == 0.0f ? 0.0f : X * (vs / L), 0.0f);
+    if (lse && d == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+  };
+  if constexpr (SPLIT) {
+    __shared__ float ms[8][32][4], ls[8][32][4], xs[8][32][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ms[warp][lane][j] = m[j];
+      ls[warp][lane][j] = l[j];
+      xs[warp][lane][j] = x[j];
+    }
+    __syncthreads();
+    if (tid >= 128) return;
+    const int k = tid >> 2, j = tid & 3;   // slot of the CTA, head
+    float M = -INFINITY, L = 0.0f, X = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, ms[w][k][j]);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float f = ms[w][k][j] == M ? 1.0f : ex2(ms[w][k][j] - M);
+      L += ls[w][k][j] * f;
+      X += xs[w][k][j] * f;
+    }
+    write(32 * blockIdx.y + k, j, M, L, X);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) write(slot, j, m[j], l[j], x[j]);
   }
 }
 
 int decode_grid() {
   const int sms = device_sm_count();
   const int n = (sms <= 0 ? 152 : sms) * kCtasPerSm;
-  return n < kMaxParts ? n : kMaxParts;
+  return n < kMaxCtas ? n : kMaxCtas;
 }
 
-size_t cut_bytes(int grid) { return ((size_t)grid * sizeof(CutInfo) + 255) & ~(size_t)255; }
+size_t header_bytes(int n) { return (kFirstsAt + (size_t)(n + 1) * sizeof(int32_t) + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache&, int) {
+size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache&, int n) {
   const int grid = decode_grid();
-  return cut_bytes(grid) + (size_t)2 * grid * kRows * (a.head_dim + 2) * sizeof(float);
+  return header_bytes(n) + (size_t)2 * grid * kWarps * kRows * (a.head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
@@ -696,29 +737,39 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
                                cudaStream_t stream) {
   const int grid = decode_grid();
   const int g = a.n_heads / a.n_kv_heads;
-  const size_t fixed = (size_t)kWarps * 8 * 64 * sizeof(float) + kWarps * kRows * sizeof(float2) +
-                       (size_t)(n + 1) * sizeof(Seq);
+  const size_t fixed = (size_t)(n + 1) * sizeof(Seq);
   // what the CTAs of an SM share (1 KB of each is the system's, and the kernel's static arrays)
   const long long room = ((long long)device_max_smem_optin() + 1024) / kCtasPerSm - 1024 - 128 - (long long)fixed;
-  int stages = (int)(room / (kWarps * 2 * kTile));
-  stages = stages < 2 ? 2 : (stages > 3 ? 3 : stages);   // a long list takes room: then one CTA has the SM
+  const int stages = room >= 3ll * kWarps * 2 * kTile ? 3 : 2;
   const size_t smem = (size_t)stages * kWarps * 2 * kTile + fixed;
-  CutInfo* cuts = static_cast<CutInfo*>(ws);
-  float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + cut_bytes(grid));
+  Header* header = static_cast<Header*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + header_bytes(n));
+  const long long all_units = (long long)n * a.n_kv_heads * ((g + kRows - 1) / kRows);
+  const int cuts = grid * kWarps - 1;   // at most as many units are cut
+  const int by_cut = all_units > cuts;
   const float* v_scale = c.dtype == QRE_E4M3 && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;
-  auto go = [&](auto kernel, auto join) -> cudaError_t {
+  // parts by warps where units are few (8 units of 49 chunks each: 7.4 us by threads, 6.3 us by warps;
+  // 512 units of two or three parts: 16.7 us by warps, 9 us by threads)
+  const bool split = all_units <= 64;
+  auto go = [&](auto kernel, auto join, int slots) -> cudaError_t {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3(grid), dim3(kThreads), smem, stream, a, c, layer, n, seqs,
-                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, cuts, parts, stages, status);
-    if (e != cudaSuccess || grid < 2) return e;
-    return launch_dependent(join, dim3(grid - 1), dim3(256), 0, stream, a, v_scale, static_cast<uint16_t*>(o), lse,
-                            const_cast<const CutInfo*>(cuts), const_cast<const float*>(parts));
+                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, header, parts, stages, status);
+    if (e != cudaSuccess) return e;
+    const int threads = split || slots > 256 ? 256 : slots;
+    return launch_dependent(join, dim3((unsigned)(by_cut ? cuts : all_units), slots / (split ? 32 : threads)),
+                            dim3(threads), 0, stream, a, n, by_cut, v_scale, static_cast<uint16_t*>(o), lse,
+                            const_cast<const Header*>(header), const_cast<const float*>(parts));
   };
   auto pick = [&](auto dt, auto ct, auto d) {
     constexpr int DT = decltype(dt)::value, CT = decltype(ct)::value, D = decltype(d)::value;
-    return g > 8 ? go(attn_decode_kernel<DT, CT, D, 2>, attn_join_kernel<DT, D>)
-                 : go(attn_decode_kernel<DT, CT, D, 1>, attn_join_kernel<DT, D>);
+    constexpr bool F8 = CT == QRE_E4M3;
+    if (g > 8)
+      return split ? go(attn_decode_kernel<DT, CT, D, 2>, attn_join_kernel<DT, F8, D, 2, true>, 4 * D)
+                   : go(attn_decode_kernel<DT, CT, D, 2>, attn_join_kernel<DT, F8, D, 2, false>, 4 * D);
+    return split ? go(attn_decode_kernel<DT, CT, D, 1>, attn_join_kernel<DT, F8, D, 1, true>, 2 * D)
+                 : go(attn_decode_kernel<DT, CT, D, 1>, attn_join_kernel<DT, F8, D, 1, false>, 2 * D);
   };
   using B = std::integral_constant<int, QRE_BF16>;
   using H = std::integral_constant<int, QRE_FP16>;
