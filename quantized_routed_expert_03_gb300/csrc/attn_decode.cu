@@ -12,7 +12,10 @@
 //
 // Work split.  A chunk is CK positions of one KV head (K and V, 8 KB together);
 // the chunks of all (sequence, KV head) units in a row are cut into equal
-// contiguous ranges, one per warp of the grid, whatever the lengths are.  The
+// contiguous ranges, one per warp of the grid, whatever the lengths are; a unit
+// counts kUnitCost chunks more than it has, its queries, first maximum and result
+// (without that, ranges of many short units end last: SMs were idle for 28 % of a
+// call with 256 sequences of 1 to 2000 positions).  The
 // lengths stay on the device: every CTA sums them up for itself.  A unit that lies
 // inside one range is finished there; one that is cut leaves a part (o, m, l in
 // fp32) per range in the workspace, and a second, dependent launch joins the
@@ -48,13 +51,14 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk
 constexpr int kRows = 16;             // query heads of a unit at most
 constexpr int kMaxCtas = 1024;        // of the main kernel
+constexpr int kUnitCost = 2;          // chunks that the begin and the end of a unit are worth (see below)
 constexpr int kMinChunks = 2;         // of a range: fewer would save nothing and leave more parts to join
 
 // What the main kernel leaves for the join, in the workspace.
 struct Header {
-  long long total;    // chunks of the call
+  long long total;    // places of the call: chunks, and kUnitCost in front of each unit's
   int ranges, pad;
-};                    // followed at kFirstsAt by the chunks before each query, n + 1 int32
+};                    // followed at kFirstsAt by the places before each query's first unit, n + 1 int32
 constexpr int kFirstsAt = 256;
 
 __device__ __forceinline__ long long range_begin(int b, int ranges, long long total) { return total * b / ranges; }
@@ -134,7 +138,7 @@ constexpr int part_floats() {
 }
 
 struct Seq {
-  int row, len, first;   // table row, length, chunks of the queries before
+  int row, len, first;   // table row, length, places of the queries before (for one unit each)
 };
 
 template <int DT, int CT, int D, int NH>
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         len[i] = row[i] = 0;
       }
       const int lo = a.window > 0 && len[i] > a.window ? len[i] - a.window : 0;
-      ch[i] = len[i] > 0 ? (len[i] + CK - 1) / CK - lo / CK : 0;
+      ch[i] = len[i] > 0 ? (len[i] + CK - 1) / CK - lo / CK + kUnitCost : 0;
       mine += ch[i];
     }
     int inc = mine;
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     t_first = lo;   // the last one that begins at or before c0: it has chunks
   }
 
-  // A place in the flat list of chunks.
+  // A place in the list: place ck of nch of the unit; its chunks begin at place kUnitCost.
   struct Place {
     int t, unit, ck, nch;
   };
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     p.ck = (int)(rest - (long long)p.unit * p.nch);
     return p;
   };
-  auto advance = [&](Place& p, int by) {   // not past the last chunk of the list
+  auto advance = [&](Place& p, int by) {   // not past the end of the list
     p.ck += by;
     while (p.ck >= p.nch) {
       p.ck -= p.nch;
@@ -268,15 +272,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   };
 
   // ---- loader
-  long long li = c0;                 // next chunk to fetch
-  Place lp = li < c1 ? place_of(li, t_first) : Place{0, 0, 0, 1};
+  long long li = c0;                 // place of the next chunk to fetch
+  Place lp = place_of(li, t_first);
+  auto to_chunk = [&]() {
+    if (lp.ck < kUnitCost) {
+      li += kUnitCost - lp.ck;
+      lp.ck = kUnitCost;
+    }
+  };
+  to_chunk();
   int pages = 0;                     // lane j: page of positions 16 j .. 16 j + 15 of that chunk, -1 missing, -2 not seen
   auto look_up = [&]() {
     pages = -2;
     if (li < c1 && lane < K::NP) {
       const int len = sq[lp.t].len;
       const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
-      const int pos = (lo / CK + lp.ck) * CK + 16 * lane;
+      const int pos = (lo / CK + lp.ck - kUnitCost) * CK + 16 * lane;
       if (pos < len && pos + 16 > lo) {
         pages = c.page_table[(size_t)sq[lp.t].row * c.max_pages + (pos >> ps_shift)];
         if (pages < 0 || pages >= c.n_pages) {
@@ -294,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (li < c1) {
       const int len = sq[lp.t].len;
       const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
-      const int pos0 = (lo / CK + lp.ck) * CK;
+      const int pos0 = (lo / CK + lp.ck - kUnitCost) * CK;
       const int hk = lp.unit / blocks;
       const uint32_t gone = __ballot_sync(0xffffffffu, pages == -1);
       missing = (missing & ~(((1u << K::NP) - 1u) << (K::NP * slot))) | (gone << (K::NP * slot));
@@ -316,7 +327,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
       ++li;
-      if (li < c1) advance(lp, 1);
+      if (li < c1) {
+        advance(lp, 1);
+        to_chunk();
+      }
       look_up();
     }
     cp_async_commit();
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   Place cp = place_of(c0, t_first);
   ask_queries(cp);
   while (s0 < c1) {
-    const long long u0 = s0 - cp.ck, u1 = u0 + cp.nch;
+    const long long u0 = s0 - cp.ck, u1 = u0 + cp.nch, k0 = u0 + kUnitCost;   // k0: its first chunk
     const long long s1 = u1 < c1 ? u1 : c1;
     const int t = cp.t;
     int hk, h0;
@@ -403,6 +417,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       s2[nh][1] = __shfl_sync(0xffffffffu, own, 8 * j4 + 4);
     }
 
+    Place np = cp;                   // the next unit: its queries come meanwhile
+    if (s1 < c1) {
+      advance(np, (int)(s1 - s0));
+      ask_queries(np);
+    }
+
     float acc[D / 16][NH][4];        // O^T: dimensions by heads 2 j, 2 j + 1
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -415,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       l[nh][0] = l[nh][1] = 0.0f;
     }
 
-    for (long long next = s0; next < s1; ++next) {
+    for (long long next = s0 < k0 ? k0 : s0; next < s1; ++next) {
       fetch(slot_in);
       slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
       if (stages == 2) cp_async_wait_group<1>();
@@ -448,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
 
-      const int pos0 = (lo / CK + (int)(next - u0)) * CK;
+      const int pos0 = (lo / CK + (int)(next - k0)) * CK;
       const uint32_t gone = (missing >> (K::NP * slot)) & ((1u << K::NP) - 1u);
       if (pos0 < lo || pos0 + CK > len || gone) {   // what is not seen: -inf
 #pragma unroll
@@ -546,19 +566,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       __syncwarp();
     }
 
-    // ---- end of the unit in this range (the next unit's queries come meanwhile)
-    Place np = cp;
-    if (s1 < c1) {
-      advance(np, (int)(s1 - s0));
-      ask_queries(np);
-    }
+    // ---- end of the unit in this range
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nh][e] += __shfl_xor_sync(0xffffffffu, l[nh][e], d);
-    if (s0 == u0 && s1 == u1) {   // whole: o = O / l, transposed so that a lane has neighbouring dimensions of head lane / 4
+    if (s1 <= k0) {               // none of its chunks
+    } else if (s0 <= k0 && s1 == u1) {   // whole: o = O / l, transposed so that a lane has neighbouring dimensions of head lane / 4
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
         float inv[2];
@@ -648,12 +664,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const long long rest = x - (long long)firsts[t] * units;
     unit = (int)(rest / nch);
     u0 = x - (rest - (long long)unit * nch);
-    if (u0 == x || range_begin(b - 1, h.ranges, h.total) > u0) return;
+    // only the begin of the second range that has chunks of the unit
+    if (x <= u0 + kUnitCost || range_begin(b - 1, h.ranges, h.total) > u0 + kUnitCost) return;
   }
-  const int b0 = range_of(u0, h.ranges, h.total), np = range_of(u0 + nch - 1, h.ranges, h.total) - b0 + 1;
+  const int b0 = range_of(u0 + kUnitCost, h.ranges, h.total), np = range_of(u0 + nch - 1, h.ranges, h.total) - b0 + 1;
   if (np < 2) return;
   // the first part lies in its range's first place when the unit begins there too; the others begin theirs
-  const float* first = parts + ((size_t)2 * b0 + (u0 == range_begin(b0, h.ranges, h.total) ? 0 : 1)) * PF;
+  const float* first = parts + ((size_t)2 * b0 + (range_begin(b0, h.ranges, h.total) >= u0 ? 0 : 1)) * PF;
   const int hk = unit / blocks, h0 = hk * g + (unit - hk * blocks) * kRows;
   const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
