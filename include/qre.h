@@ -517,7 +517,8 @@ QRE_API qre_status qre_kv_reserve(const qre_kv_cache* cache, int32_t n, const in
 /*
  * Writes n_tokens new rows of one layer: row t goes to position token_pos[t] of
  * sequence token_seq[t], as it is (cache and rows of one type) or, into a
- * QRE_E4M3 cache, as E4M3(row / scale), to nearest even, clamped to +-448.
+ * QRE_E4M3 cache, as E4M3(row * (1 / scale)), reciprocal and product rounded to
+ * fp32, then to nearest even, clamped to +-448.
  * A token with token_pos < 0 is skipped (padding); one without a page there, or
  * with a bad id, is skipped with QRE_DEV_BAD_INDEX.
  *   token_seq, token_pos  [n_tokens] int32, device

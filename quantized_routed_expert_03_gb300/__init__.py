@@ -162,10 +162,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = _current_device = None
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object: 0.3 us instead of 3 us of every call
+        global _raw_stream, _current_device
+        if _raw_stream is None:
+            import torch
+            _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        return _raw_stream(_current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

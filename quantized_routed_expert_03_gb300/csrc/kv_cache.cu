@@ -81,11 +81,12 @@ __device__ __forceinline__ int4 page_counts(const int32_t* ref, int n_pages, int
 }
 
 // Writes the first `want` free pages, ascending, to list; returns how many there are (at most want).
-__device__ int find_free_pages(const int32_t* ref, int n_pages, int want, int32_t* list, int* part) {
+// first4: this thread's page_counts of the first step, asked for early.
+__device__ int find_free_pages(const int32_t* ref, int n_pages, int want, int32_t* list, int* part, int4 first4) {
   int found = 0;
   for (int p0 = 0; p0 < n_pages && found < want; p0 += kScan) {
     const int p = p0 + 4 * (int)threadIdx.x;
-    const int4 r = page_counts(ref, n_pages, p);
+    const int4 r = p0 == 0 ? first4 : page_counts(ref, n_pages, p);
     const int f[4] = {r.x <= 0, r.y <= 0, r.z <= 0, r.w <= 0};
     int total;
     int rank = found + block_scan(f[0] + f[1] + f[2] + f[3], part, &total);
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const __grid_const
   __shared__ int first[kKvMaxRequests + 1];
   grid_dependency_wait();
   grid_dependents_launch();
+  const int4 first4 = page_counts(c.ref_count, c.n_pages, 4 * (int)threadIdx.x);
   long long sum = 0;
   for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + (int)threadIdx.x;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const __grid_const
   if (threadIdx.x == 0) first[n] = (int)sum;
   __syncthreads();
   const int want = first[n] < c.n_pages ? first[n] : c.n_pages;
-  const int found = find_free_pages(c.ref_count, c.n_pages, want, ws.a, part);
+  const int found = find_free_pages(c.ref_count, c.n_pages, want, ws.a, part, first4);
   // the pages, spread over the threads: page number r belongs to the last request with first <= r
   for (int r = threadIdx.x; r < found; r += kThreads) {
     int lo = 0, hi = n - 1;
@@ -209,48 +211,52 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
                                                                 const int32_t* __restrict__ dst, KvWs ws,
                                                                 int32_t* fresh, int* status) {
   __shared__ int part[33];
-  __shared__ int rank_of[kKvMaxRequests];   // rank of the fresh page, -1 none needed, -2 dropped
+  __shared__ int list[kKvMaxRequests];
+  constexpr int kEach = kKvMaxRequests / kThreads;
+  int rank[kEach], old[kEach];   // rank of the fresh page (-1: none needed, -2: dropped), the page to copy
   grid_dependency_wait();
   grid_dependents_launch();
+  const int4 first4 = page_counts(c.ref_count, c.n_pages, 4 * (int)threadIdx.x);
   int sum = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    int need = 0, state = -2;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * kThreads + (int)threadIdx.x;
+    rank[e] = -2;
+    old[e] = -1;
+    if (e * kThreads >= n) continue;   // the same for all threads
+    int need = 0;
     if (i < n) {
       const int s = src[i], d = dst[i];
-      if (s < 0 || s >= c.max_seqs || d < 0 || d >= c.max_seqs || s == d || c.seq_len[d] != 0 || c.seq_len[s] < 0 ||
-          c.seq_len[s] > (long long)c.max_pages * c.page_size) {
-        set_status(status, QRE_DEV_BAD_INDEX);
-      } else {
-        state = -1;
-        const int len = c.seq_len[s];
-        if (len % c.page_size) {
-          if (page_ok(c, c.page_table[(size_t)s * c.max_pages + len / c.page_size])) need = 1;
-          else {
-            state = -2;
-            set_status(status, QRE_DEV_BAD_INDEX);
-          }
-        }
+      const bool ids = s >= 0 && s < c.max_seqs && d >= 0 && d < c.max_seqs && s != d;
+      const int len = ids ? c.seq_len[s] : -1, there = ids ? c.seq_len[d] : -1;
+      bool ok = there == 0 && len >= 0 && len <= (long long)c.max_pages * c.page_size;
+      if (ok && len % c.page_size) {
+        old[e] = c.page_table[(size_t)s * c.max_pages + len / c.page_size];
+        ok = page_ok(c, old[e]);
+        need = ok;
       }
+      if (ok) rank[e] = -1;
+      else set_status(status, QRE_DEV_BAD_INDEX);
     }
     int total;
     const int before = block_scan(need, part, &total);
-    if (i < n) rank_of[i] = need ? sum + before : state;
+    if (need) rank[e] = sum + before;
     sum += total;
   }
-  __syncthreads();
   const int want = sum < c.n_pages ? sum : c.n_pages;
-  const int found = find_free_pages(c.ref_count, c.n_pages, want, ws.b, part);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int r = rank_of[i];
+  const int found = find_free_pages(c.ref_count, c.n_pages, want, list, part, first4);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * kThreads + (int)threadIdx.x, r = rank[e];
+    if (i >= n) continue;
     int f = r;
     if (r >= found) {
       f = -2;
       set_status(status, QRE_DEV_NO_PAGE);
     } else if (r >= 0) {
-      const int s = src[i];
-      f = ws.b[r];
-      ws.a[r] = c.page_table[(size_t)s * c.max_pages + c.seq_len[s] / c.page_size];
+      f = list[r];
+      ws.a[r] = old[e];
+      ws.b[r] = f;
       c.ref_count[f] = 1;
     }
     fresh[i] = f;
@@ -388,58 +394,89 @@ __device__ __forceinline__ float to_float(uint16_t b) {
   return RT == QRE_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half(b));
 }
 
-// One thread moves 8 elements of one row of K or V.
+// Memory bound: each row is read and written once.  A CTA has a few tokens: where
+// their rows go is looked up once per token, while the rows' 16-byte pieces are on
+// their way into registers; no index needs a division of more than a multiply (the
+// first form, which divided 64-bit indices for every piece, took 33 us for 11,300
+// rows of K and V into an E4M3 cache instead of 16).
+constexpr int kWriteThreads = 256;
+constexpr int kWriteEach = 2;        // pieces of a thread
+constexpr int kWriteTokens = 64;     // of a CTA at most
+
 template <int RT, bool FP8>
-__global__ void __launch_bounds__(256) kv_write_kernel(const __grid_constant__ qre_kv_cache c, int layer,
-                                                       const __grid_constant__ qre_kv_rows r, int n_tokens,
-                                                       const int32_t* __restrict__ token_seq,
-                                                       const int32_t* __restrict__ token_pos,
-                                                       const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                                                       int* status) {
+__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(
+    const __grid_constant__ qre_kv_cache c, int layer, const __grid_constant__ qre_kv_rows r, int n_tokens, int tokens,
+    uint32_t magic, const int32_t* __restrict__ token_seq, const int32_t* __restrict__ token_pos,
+    const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int* status) {
+  __shared__ long long to[kWriteTokens];   // element of the token's row of head 0, -1: skipped
   grid_dependency_wait();
   grid_dependents_launch();
-  const int per_head = c.head_dim / 8, per_row = c.n_kv_heads * per_head;
-  const long long total = 2ll * n_tokens * per_row;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (long long)gridDim.x * blockDim.x) {
-    const int t = (int)(i / (2 * per_row)), rest = (int)(i - (long long)t * 2 * per_row);
-    const bool is_v = rest >= per_row;
-    const int w = is_v ? rest - per_row : rest, h = w / per_head, d = (w - h * per_head) * 8;
-    const int pos = token_pos[t], s = token_seq[t];
-    if (pos < 0) continue;
-    int p = -1;
-    if (s >= 0 && s < c.max_seqs && pos / c.page_size < c.max_pages)
-      p = c.page_table[(size_t)s * c.max_pages + pos / c.page_size];
-    if (!page_ok(c, p)) {
-      set_status(status, QRE_DEV_BAD_INDEX);
-      continue;
+  const int per_head_shift = c.head_dim == 64 ? 3 : 4, per_row = c.n_kv_heads << per_head_shift, per_token = 2 * per_row;
+  const int t0 = blockIdx.x * tokens, mine = n_tokens - t0 < tokens ? n_tokens - t0 : tokens;
+  const int pieces = mine * per_token, ps_shift = 31 - __clz(c.page_size);
+  for (int i0 = 0; i0 < pieces; i0 += kWriteThreads * kWriteEach) {   // once, unless a token has more pieces
+    uint4 x[kWriteEach];
+    int at_token[kWriteEach], at_rest[kWriteEach];
+#pragma unroll
+    for (int e = 0; e < kWriteEach; ++e) {
+      const int i = i0 + e * kWriteThreads + (int)threadIdx.x;
+      if (i >= pieces) continue;
+      const int t = (int)__umulhi((uint32_t)i, magic), rest = i - t * per_token;
+      const bool is_v = rest >= per_row;
+      const int w = is_v ? rest - per_row : rest, h = w >> per_head_shift, d = (w & ((1 << per_head_shift) - 1)) * 8;
+      const uint16_t* src = is_v ? v + (size_t)(t0 + t) * r.v_token + (size_t)h * r.v_head
+                                 : k + (size_t)(t0 + t) * r.k_token + (size_t)h * r.k_head;
+      x[e] = *reinterpret_cast<const uint4*>(src + d);
+      at_token[e] = t;
+      at_rest[e] = rest;
     }
-    const uint16_t* src = is_v ? v + (size_t)t * r.v_token + (size_t)h * r.v_head
-                               : k + (size_t)t * r.k_token + (size_t)h * r.k_head;
-    const uint4 x = *reinterpret_cast<const uint4*>(src + d);
-    const size_t at =
-        ((((size_t)layer * c.n_pages + p) * c.n_kv_heads + h) * c.page_size + pos % c.page_size) * c.head_dim + d;
-    if (!FP8) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? c.v : c.k) + at) = x;
-    } else {
-      // the quotient is IEEE, so a row divided elsewhere in fp32 gives the same byte; one rounding to 8 bits
-      const float* scales = is_v ? c.v_scale : c.k_scale;
-      const float sc = scales ? scales[(size_t)layer * c.n_kv_heads + h] : 1.0f;
-      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-      uint32_t out[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t b = 0;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint32_t u = in[2 * j + m];
-          const float2 f = make_float2(__fdiv_rn(to_float<RT>((uint16_t)u), sc),
-                                       __fdiv_rn(to_float<RT>((uint16_t)(u >> 16)), sc));
-          b |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (16 * m);
+    if (i0 == 0) {
+      if ((int)threadIdx.x < mine) {
+        const int pos = token_pos[t0 + threadIdx.x], s = token_seq[t0 + threadIdx.x];
+        long long at = -1;
+        if (pos >= 0) {
+          int p = -1;
+          if (s >= 0 && s < c.max_seqs && (pos >> ps_shift) < c.max_pages)
+            p = c.page_table[(size_t)s * c.max_pages + (pos >> ps_shift)];
+          if (page_ok(c, p))
+            at = ((((long long)layer * c.n_pages + p) * c.n_kv_heads << ps_shift) + (pos & (c.page_size - 1))) * c.head_dim;
+          else
+            set_status(status, QRE_DEV_BAD_INDEX);
         }
-        out[j] = b;
+        to[threadIdx.x] = at;
       }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at) = make_uint2(out[0], out[1]);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < kWriteEach; ++e) {
+      const int i = i0 + e * kWriteThreads + (int)threadIdx.x;
+      if (i >= pieces || to[at_token[e]] < 0) continue;
+      const bool is_v = at_rest[e] >= per_row;
+      const int w = is_v ? at_rest[e] - per_row : at_rest[e], h = w >> per_head_shift;
+      const size_t at = (size_t)to[at_token[e]] + ((size_t)h << ps_shift) * c.head_dim +
+                        (w & ((1 << per_head_shift) - 1)) * 8;
+      if (!FP8) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? c.v : c.k) + at) = x[e];
+      } else {
+        // times the correctly rounded reciprocal, in fp32, then one rounding to 8 bits (a division for
+        // every element took 6 us more of the 15)
+        const float* scales = is_v ? c.v_scale : c.k_scale;
+        const float inv = scales ? __frcp_rn(scales[(size_t)layer * c.n_kv_heads + h]) : 1.0f;
+        const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+        uint32_t out[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t b = 0;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t u = in[2 * j + m];
+            const float2 f = make_float2(to_float<RT>((uint16_t)u) * inv, to_float<RT>((uint16_t)(u >> 16)) * inv);
+            b |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (16 * m);
+          }
+          out[j] = b;
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at) = make_uint2(out[0], out[1]);
+      }
     }
   }
 }
@@ -486,12 +523,16 @@ cudaError_t launch_kv_compact(const qre_kv_cache& c, int32_t* table_out, int32_t
 cudaError_t launch_kv_write(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n_tokens,
                             const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
                             int* status, cudaStream_t stream) {
-  const long long total = 2ll * n_tokens * c.n_kv_heads * (c.head_dim / 8);
-  const long long blocks = (total + 255) / 256, most = wide_grid() * 4ll;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
+  const int per_token = 2 * c.n_kv_heads * (c.head_dim / 8);   // 16-byte pieces: at most 8192
+  int tokens = kWriteThreads * kWriteEach / per_token;
+  tokens = tokens < 1 ? 1 : (tokens > kWriteTokens ? kWriteTokens : tokens);
+  while (tokens > 1 && (n_tokens + tokens - 1) / tokens < 2 * device_sm_count()) tokens /= 2;   // few tokens: more CTAs
+  // floor(i / per_token) = umulhi(i, magic) for the indices of a CTA (below 2^16): per_token is at most 2^13
+  const uint32_t magic = (uint32_t)((0x100000000ull + per_token - 1) / per_token);
+  const dim3 grid((unsigned)((n_tokens + tokens - 1) / tokens));
   auto go = [&](auto kernel) {
-    return launch_dependent(kernel, grid, dim3(256), 0, stream, c, layer, r, n_tokens, token_seq, token_pos,
-                            static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), status);
+    return launch_dependent(kernel, grid, dim3(kWriteThreads), 0, stream, c, layer, r, n_tokens, tokens, magic, token_seq,
+                            token_pos, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), status);
   };
   if (c.dtype != QRE_E4M3) return go(kv_write_kernel<QRE_BF16, false>);   // the bits as they are, either type
   return r.dtype == QRE_BF16 ? go(kv_write_kernel<QRE_BF16, true>) : go(kv_write_kernel<QRE_FP16, true>);

@@ -187,9 +187,8 @@ def test_write(row, kind, dim, heads, page, fused):
                 continue
             r = new[t]
             if kind == "e4m3":
-                # the quotient in fp32 is the definition's input; rounding by the oracle
-                quo = (r.float() / sc[1][:, None]).cpu().numpy()
-                vals = torch.from_numpy(oatt.e4m3_round(quo)).float()
+                # the product with the reciprocal, in fp32, is what is rounded; rounding by the oracle
+                vals = torch.from_numpy(oatt.e4m3_round((r.float() * (1.0 / sc[1])[:, None]).cpu().numpy())).float()
                 r = vals.to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
             want[1, page_of[t], :, pos[t] % page] = r
         if kind == "e4m3":
