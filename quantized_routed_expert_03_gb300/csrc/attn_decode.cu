@@ -20,6 +20,11 @@
 // inside one range is finished there; one that is cut leaves a part (o, m, l in
 // fp32) per range in the workspace, and a second, dependent launch joins the
 // parts in the order of the ranges, so results do not depend on timing.
+// Where max_len or the window says that no unit has more than kWholeChunks chunks,
+// ranges begin at units and there is no join.  32 heads on 8, D = 128, one length
+// for all, cut / whole: 4 chunks (64 positions) 8.6 / 7.1 us for 1 sequence, 10.5 /
+// 8.3 for 64, 20.0 / 13.7 for 256; 8 chunks 8.8 / 10.1, 11.9 / 11.7, 23.8 / 20.5;
+// 16 chunks 9.5 / 15.9, 13.2 / 18.3, 36.7 / 36.8.
 //
 // A warp runs on its own, with no barrier (with ranges of CTAs, whose warps met at
 // the end of every unit, 256 sequences of up to 1500 positions took 57 us instead
@@ -52,6 +57,7 @@ constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk
 constexpr int kRows = 16;             // query heads of a unit at most
 constexpr int kMaxCtas = 1024;        // of the main kernel
 constexpr int kUnitCost = 2;          // chunks that the begin and the end of a unit are worth (see below)
+constexpr int kWholeChunks = 4;       // units of so many chunks are not cut (see below)
 constexpr int kMinChunks = 2;         // of a range: fewer would save nothing and leave more parts to join
 
 // What the main kernel leaves for the join, in the workspace.
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
                        const int32_t* __restrict__ seqs, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
                        float* __restrict__ lse, Header* __restrict__ header, float* __restrict__ parts, int stages,
-                       int* status) {
+                       int by_unit, int* status) {
   using K = Decode<DT, CT, D, NH>;
   constexpr int CK = K::CK, KS = K::KS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -208,9 +214,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (tid == 0) sq[n].first = before;
   __syncthreads();
   const long long total = (long long)before * units;
-  const long long want = (total + kMinChunks - 1) / kMinChunks, all = (long long)gridDim.x * kWarps;
+  const long long want = by_unit ? (long long)n * units : (total + kMinChunks - 1) / kMinChunks;
+  const long long all = (long long)gridDim.x * kWarps;
   const int ranges = (int)(want < all ? want : all);
   const int me = warp * (int)gridDim.x + blockIdx.x;   // this warp's range: few ranges spread over the SMs
+  // the place at which range b begins: any, or (by_unit) a unit's first
+  auto begin = [&](int b) {
+    if (!by_unit) return range_begin(b, ranges, total);
+    const long long u = (long long)n * units * b / ranges;
+    const int t = (int)(u / units);
+    return t >= n ? total : (long long)sq[t].first * units + (u - (long long)t * units) * (sq[t + 1].first - sq[t].first);
+  };
 
   // queries that see nothing
   for (int t = blockIdx.x; t < n; t += gridDim.x) {
@@ -222,13 +236,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (lse)
       for (int h = tid; h < a.n_heads; h += kThreads) lse[(size_t)t * a.n_heads + h] = -INFINITY;
   }
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0 && !by_unit) {
     if (tid == 0) *header = Header{total, ranges, 0};
     int32_t* firsts = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(header) + kFirstsAt);
     for (int t = tid; t <= n; t += kThreads) firsts[t] = sq[t].first;
   }
   if (me >= ranges) return;
-  const long long c0 = range_begin(me, ranges, total), c1 = range_begin(me + 1, ranges, total);
+  const long long c0 = begin(me), c1 = begin(me + 1);
+  if (c0 >= c1) return;
 
   // the query that chunk c0 belongs to
   int t_first;
@@ -768,12 +783,15 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
   // parts by warps where units are few (8 units of 49 chunks each: 7.4 us by threads, 6.3 us by warps;
   // 512 units of two or three parts: 16.7 us by warps, 9 us by threads)
   const bool split = all_units <= 64;
+  // Whole units for the warps, and no join, where the caller's bound or the window says that all are short
+  const int most = a.window > 0 && (max_len == 0 || a.window < max_len) ? a.window : max_len;
+  const int by_unit = most > 0 && most <= kWholeChunks * (kTile / (a.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)));
   auto go = [&](auto kernel, auto join, int slots) -> cudaError_t {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3(grid), dim3(kThreads), smem, stream, a, c, layer, n, seqs,
-                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, header, parts, stages, status);
-    if (e != cudaSuccess) return e;
+                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, header, parts, stages, by_unit, status);
+    if (e != cudaSuccess || by_unit) return e;
     const int threads = split || slots > 256 ? 256 : slots;
     return launch_dependent(join, dim3((unsigned)(by_cut ? cuts : all_units), slots / (split ? 32 : threads)),
                             dim3(threads), 0, stream, a, n, by_cut, v_scale, static_cast<uint16_t*>(o), lse,
