@@ -3,6 +3,31 @@
 // o_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys that query i sees, in
 // one pass: with the running maximum m and sum l (fp32, base 2),
 //   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), o' alike.
+//
+// Bound: 4 D flops for each (query head, key seen).  A tile of 128 queries x 128
+// keys is 1024 cycles of an SM's tensor cores at D = 128 (S and P V, 512 each) and
+// 16384 exponentials, 512 cycles at the 32 a cycle that were measured: the tensor
+// cores bound it if the rest runs beside them.  At D = 64 both need 512.
+//
+// A CTA (one per SM, 512 threads) takes pieces of work: two query tiles of one
+// sequence and one group of heads, tile rows = tokens x heads of one KV head, so
+// that few tokens still fill a tile and K and V are fetched once for the group.
+// Warps have one job each: one finds the work (clusterlaunchcontrol hands out the
+// grid's indices, so CTAs that finish early take more; three pieces ahead), one
+// fetches tiles by TMA (5 x 32 KB ring), two issue the products (tcgen05, S in
+// tensor memory, P over it in 16 bits, O beside it), eight weight the scores, one
+// thread per row, and four bring O out while the next piece goes on.
+//
+// What it measured (32 heads on 8, D = 128, bf16; of the 1901 TFLOP/s measured for
+// cuBLAS): one causal prompt of 8192 tokens 359 us, 1.53 PFLOP/s (81 %); 8 prompts of 7 to 4000 tokens, 106
+// Gflop, 124 us (45 % of it: short prompts are mostly tiles that a mask cuts).
+// A pair of query tiles takes some 2600 cycles per key tile of the 2048 that its
+// products need.  Steps on the prompt of 8192: one MMA thread and plain softmax
+// 522 us; MMA issued by a converged warp, three-operand maximum, paired fp32 414;
+// persistent, weights against a standing reference, P V begun on the first 96
+// keys, tiles in turn 384; output and work finding on warps of their own 358.
+// Slower: two threads a row (497), first parts of 64 keys (397).
+#include <climits>
 #include <type_traits>
 
 #include "attn.cuh"
@@ -12,8 +37,9 @@
 namespace qre {
 namespace {
 
-// One warp per (query token, head); a lane scores one key at a time, then the
-// lanes share the head's dimensions for the values.
+// For what TMA cannot address (rows that repeat: a token stride of 0) and calls
+// without any key: one warp per (query token, head); a lane scores one key at a
+// time, then the lanes share the head's dimensions for the values.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q,
                                                         int total_k, const int32_t* __restrict__ cu_q,
@@ -182,9 +208,9 @@ struct Job {
     };
     r0 = keys_of(0);
     r1 = keys_of(1);
-    const bool has0 = r0.je > r0.jb, has1 = r1.je > r1.jb;
-    jb = has0 ? r0.jb : r1.jb;
-    je = has1 ? r1.je : r0.je;
+    if (r0.je <= r0.jb) r0 = r1;   // tokens that see nothing go along, so that tile 0 has keys if the work has
+    jb = r0.jb;
+    je = r1.je > r1.jb ? r1.je : r0.je;
     const int last = (w.tok0 + 2 * tt < w.q_len ? w.tok0 + 2 * tt : w.q_len) - 1;
     int x;
     visible_range(last + shift, w.k_len, a.causal, a.window, lo_last, x);
@@ -488,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The tiles' products are issued in turn, each tile's in one go: left to themselves the two
       // softmaxes fall into step and compete for the same cycles, and the tensor cores wait.  The
       // turn is one more arrival on the barrier of the first weights: a wait of its own would
-      // cost some 200 cycles, as every wait here does, next to the tensor cores' reads.
+      // cost some 200 cycles, as every wait here does, next to the tensor cores' reads.  There is
+      // one turn: each step hands it to the next one in the order of work, key tile, query tile,
+      // so that a barrier never gets it while the phase before is open.
       auto turn_to = [&](int tile) {
         if (lead) mbar_arrive(&p_full[tile]);
         __syncwarp();
@@ -497,10 +525,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       int i0 = 0, nq = 0, n = 0, no = 0;
       Work w;
       bool ok = true;
+      if (t == 0) turn_to(0);
       for (int nw = 0; ok && take(nw, w); ++nw) {
         const Job job(a, w, tt);
         give_back(nw);
-        const Range r = t ? job.r1 : job.r0, other = t ? job.r0 : job.r1;
+        const Range r = t ? job.r1 : job.r0;
+        // a step of key tile j hands the turn to the other query tile if j is in [give_b, give_e) or is
+        // the last (of tile 0: if tile 1 has keys), else to this one; a piece begins with tile 0
+        const bool two = job.r1.je > job.r1.jb;
+        const int give_b = t ? 0 : two ? job.r1.jb : INT_MAX, give_e = t ? job.r0.je - 1 : INT_MAX;
+        const int last = two ? r.je - 1 : INT_MAX;
         if (job.je <= job.jb) continue;
         ok = wait_for(q_full, nq);
         ++nq;
@@ -509,11 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = job.jb; ok && j < job.je; ++j) {
           const int i = i0 + 2 * (j - job.jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
           const bool mine = j >= r.jb && j < r.je, more = mine && j + 1 < r.je;
-          // turns go tile 0, tile 1, tile 0, ... by key tile; with no step of the other tile before
-          // it, a step has its turn of itself
-          const int next = j + t, last = j - 1 + t;
-          const bool pass = next >= other.jb && next < other.je;
-          const bool own = last < other.jb || last >= other.je;
+          const bool pass = (j >= give_b && j < give_e) || j == last;
           if (mine && j == r.jb) {
             ok = wait_tile(i);
             if (!ok) break;
@@ -528,7 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = no == 0 || wait_for(&o_free[t], no - 1);
             ++no;
           }
-          if (ok && mine && own) turn_to(t);
           if (ok && mine) ok = wait_for(&p_full[t], n);
           if (!ok) break;
           if (!mine) {                     // the other query tile's keys only
@@ -554,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             scores(sk);   // overwrites P: issued behind the product that reads it
           }
           if (pass) turn_to(t ^ 1);
+          else turn_to(t);
           if (more) umma_commit_lead(&empty[sk], lead);
           if (more && j + 2 == r.je) umma_commit_lead(q_empty, lead);
         }
@@ -681,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.0f;       // reference maximum (of the raw scores) and sum
       bool started = false;                // a key tile has been through
+      bool unset = true;                   // a row of the warp has no reference
       auto weights = [&](const uint32_t (&x)[32], uint32_t* p, uint64_t off2, uint64_t (&sum)[2]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -816,13 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish(part);
       };
       // The weights are taken against the reference of before, with no maximum looked for (the row's
-      // first keys set it).  Rounding does not depend on the reference, so it may stay far behind;
-      // only when the weights' sum is too large for their type, or a row has seen no key yet, the
-      // keys go by the book.  False: they have to.
-      auto fits = [&](const uint64_t (&sum)[2], bool unset) {
+      // first keys set it).  Rounding does not depend on the reference, so it may stay far behind; only
+      // when the weights' sum is too large for their type the keys go by the book.  False: they have to.
+      auto fits = [&](const uint64_t (&sum)[2]) {
         const float2 u = unpair(add2(sum[0], sum[1]));
         const float total = u.x + u.y;
-        if (__any_sync(0xffffffffu, unset || total > kMostWeight<DT>)) return false;
+        if (__any_sync(0xffffffffu, total > kMostWeight<DT>)) return false;
         l += total;
         return true;
       };
@@ -834,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int b = 0; b < N / 32; ++b) weights(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * b), p + 16 * b, off2, sum);
-        if (!fits(sum, m == -INFINITY)) {
+        if (!fits(sum)) {
           careful(false, part, b0, b0 + N / 32, key0);
           return;
         }
@@ -843,7 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_32x32b_x16(sc + 16 * (b0 + b), *reinterpret_cast<uint32_t(*)[16]>(p + 16 * b));
         publish(part);
       };
-      // A first tile, or one that a mask cuts, piece by piece, the next one on its way.
+      // A tile that a mask cuts, or with rows that have no reference yet, piece by piece, the next one
+      // on its way.
       auto edge = [&](auto pieces, bool masked, int part, int b0, int key0) {
         constexpr int NB = decltype(pieces)::value;
         uint32_t y[2][32], p[16 * NB];
@@ -855,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b + 1 < NB) fetch(b + 1);
           if (masked) mask(y[b & 1], key0 + 32 * (b0 + b));
         };
-        if (!started && part == 0) {
+        if (unset) {                       // rows that have seen no key: these set their references
           float mx[2] = {-INFINITY, -INFINITY};
           fetch(0);
 #pragma unroll
@@ -867,7 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 2; ++e)
                 mx[e] = max3(mx[e], __uint_as_float(y[b & 1][i + e]), __uint_as_float(y[b & 1][i + 2 + e]));
           }
-          m = fmaxf(mx[0], mx[1]);
+          if (m == -INFINITY) m = fmaxf(mx[0], mx[1]);
+          unset = __any_sync(0xffffffffu, m == -INFINITY);
         }
         const uint64_t off2 = offset();
         uint64_t sum[2] = {0, 0};
@@ -877,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           arrived(b);
           weights(y[b & 1], p + 16 * b, off2, sum);
         }
-        if (!fits(sum, m == -INFINITY && (started || part))) {
+        if (!fits(sum)) {
           careful(masked, part, b0, b0 + NB, key0);
           return;
         }
@@ -898,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_for(&s_full[t], cnt);
         if (!ok) break;
         tc_fence_after();
-        if (masked || !started) {
+        if (masked || unset) {
           edge(std::integral_constant<int, kPart / 32>{}, masked, 0, 0, j * kN);
           if (ok) edge(std::integral_constant<int, (kN - kPart) / 32>{}, masked, 1, kPart / 32, j * kN);
           started = true;
@@ -939,10 +971,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(&full[i % P::SLOTS], (i / P::SLOTS) & 1, status);
     if (*asked > 0) mbar_wait_drain(answered, (*asked - 1) & 1, status);
   }
-  if (*abort_flag && (warp == kMmaWarp || warp == kMmaWarp + 1) && lane == 0) {
+  if (*abort_flag && (warp == kMmaWarp || warp == kMmaWarp + 1)) {
     uint64_t* d = drain + (warp - kMmaWarp);
-    umma_commit(d);
-    mbar_wait_drain(d, 0, status);
+    if (elect_lane()) {   // the lane that issued them: an election of the same lanes has the same outcome
+      umma_commit(d);
+      mbar_wait_drain(d, 0, status);
+    }
+    __syncwarp();
   }
   __syncthreads();
   if (warp == kMmaWarp) {

@@ -116,6 +116,24 @@ def test_prefill_large_scores_and_scale():
     check(o, l, ref, "bf16", n, float(v.abs().max()))
 
 
+def test_prefill_query_tiles_at_their_own_pace():
+    """Several hundred short pieces of work whose later tokens see scores that grow sharply, so that of a piece's two
+    query tiles one is held up again and again while the other could go on; some first tokens see nothing."""
+    rng = np.random.default_rng(5)
+    q_lens = [int(x) for x in rng.integers(20, 65, 300)]
+    k_lens = [int(n + x) for n, x in zip(q_lens, rng.integers(-30, 200, 300))]
+    k_lens = [max(x, 0) for x in k_lens]
+    H, Hk, D = 8, 2, 64
+    q, k, v = (randn((sum(n), h, D), 1 + i, "bf16") for i, (n, h) in enumerate(((q_lens, H), (k_lens, Hk), (k_lens, Hk))))
+    grow = torch.cat([torch.linspace(0.05, 6, 300)[:n].flip(0) if i % 3 == 0 else torch.logspace(-1, 1, max(n, 1))[:n]
+                      for i, n in enumerate(k_lens)]).to(DEV)
+    k = (k.float() * grow[:, None, None]).to(torch.bfloat16)
+    ref = oatt.prefill(npy(q), npy(k), npy(v), q_lens, k_lens, 0.5)
+    o, l = run_prefill(q, k, v, q_lens, k_lens, "bf16", scale=0.5)
+    assert qre.qre_read_device_status() == 0
+    check(o, l, ref, "bf16", max(k_lens), float(v.abs().max()))
+
+
 def test_prefill_equal_keys_average_the_values():
     n, D = 300, 64
     q, v = randn((n, 2, D), 1, "fp16"), randn((n, 1, D), 2, "fp16")
@@ -368,6 +386,22 @@ def test_decode_result_does_not_depend_on_the_other_sequences():
     pg.k[:, free], pg.v[:, free] = float("nan"), float("nan")
     o2, l2 = run_decode(pg, q, "bf16")
     assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("kind,cache,D", [("bf16", "bf16", 128), ("fp16", "fp16", 64), ("bf16", "e4m3", 64)])
+def test_decode_short_sequences_left_whole(kind, cache, D, window):
+    """A bound of the lengths (or a window) under which units are not cut, true or not; and with more units than warps."""
+    rng = np.random.default_rng(D + window)
+    lens = [0, 1, 7, 64, 700] + [int(x) for x in rng.integers(1, 60, 395)]
+    pg = Paged(lens, 8, D, 16, cache)
+    q = randn((len(lens), 16, D), 4, kind)
+    cut, lc = run_decode(pg, q, kind, window=window)
+    whole, lw = run_decode(pg, q, kind, window=window, max_len=60)
+    assert qre.qre_read_device_status() == 0
+    ref = decode_ref(pg, q, window=window)
+    check(cut, lc, ref, kind, 700, float(pg.v.float().abs().max()))
+    check(whole, lw, ref, kind, 700, float(pg.v.float().abs().max()))
 
 
 @pytest.mark.parametrize("cache,kind", [("bf16", "bf16"), ("e4m3", "fp16")])
