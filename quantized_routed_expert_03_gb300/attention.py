@@ -1,0 +1,96 @@
+"""Device plumbing for attention: the paged key-value cache and the two attention calls over it.
+
+Like ``layer``, PyTorch only allocates memory and supplies streams here; every
+computation is a call into libqre.so through the binding in ``__init__``.
+
+* :class:`KVCache` owns the pages of all layers and the device state (page table,
+  lengths, reference counts): reserve, write, fork, free, compact.
+* :class:`Attention` is one layer's attention on such a cache: ``prefill`` over
+  packed prompts (keys and values as they come from the projections), ``decode``
+  of one new token per sequence over the pages.
+
+Both keep a workspace: calls on one object belong on one stream at a time.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import (QRE_BF16, QRE_E4M3, QRE_FP16, make_attn, make_kv_cache, make_kv_rows, qre_attn_decode,
+               qre_attn_decode_workspace_size, qre_attn_prefill, qre_kv_compact, qre_kv_fork, qre_kv_free,
+               qre_kv_reserve, qre_kv_workspace_size, qre_kv_write)
+
+DTYPES = {torch.bfloat16: QRE_BF16, torch.float16: QRE_FP16, torch.float8_e4m3fn: QRE_E4M3}
+
+
+class KVCache:
+    """``n_pages`` pages of ``page_size`` positions for all layers, and up to ``max_seqs`` sequences on them.
+
+    k_scale, v_scale: [n_layers, n_kv_heads] fp32, for an E4M3 cache only (None: 1).
+    Sequence ids, counts and positions are int32 tensors on the device that begin at a 16-byte boundary
+    (clone a slice that does not); nothing here synchronizes.
+    """
+
+    def __init__(self, n_layers, n_pages, n_kv_heads, page_size, head_dim, max_seqs, max_pages,
+                 dtype=torch.bfloat16, k_scale=None, v_scale=None, device="cuda"):
+        self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        shape = (n_layers, n_pages, n_kv_heads, page_size, head_dim)
+        self.k = torch.empty(shape, dtype=dtype, device=self.device)
+        self.v = torch.empty(shape, dtype=dtype, device=self.device)
+        self.page_table = torch.full((max_seqs, max_pages), -1, **i32)
+        self.seq_len = torch.zeros(max_seqs, **i32)
+        self.ref_count = torch.zeros(n_pages, **i32)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.desc = make_kv_cache(self.k, self.v, self.page_table, self.seq_len, self.ref_count, DTYPES[dtype],
+                                  k_scale, v_scale)
+        self.workspace = torch.empty(qre_kv_workspace_size(self.desc), dtype=torch.uint8, device=self.device)
+        self.n_live = torch.zeros(1, **i32)
+
+    def reserve(self, seqs, n_new, stream=None):
+        qre_kv_reserve(self.desc, seqs.numel(), seqs, n_new, self.workspace, stream=stream)
+
+    def write(self, layer, token_seq, token_pos, k, v, stream=None):
+        """k, v: [tokens, n_kv_heads, head_dim], any token and head strides (views of one projection's output)."""
+        qre_kv_write(self.desc, layer, make_kv_rows(DTYPES[k.dtype], k, v), token_seq.numel(), token_seq, token_pos,
+                     k, v, stream)
+
+    def fork(self, src, dst, stream=None):
+        qre_kv_fork(self.desc, src.numel(), src, dst, self.workspace, stream=stream)
+
+    def free(self, seqs, stream=None):
+        qre_kv_free(self.desc, seqs.numel(), seqs, stream)
+
+    def compact(self, stream=None):
+        """Returns the device tensor that will hold the number of live pages."""
+        qre_kv_compact(self.desc, self.page_table, self.ref_count, self.n_live, self.workspace, stream=stream)
+        return self.n_live
+
+
+class Attention:
+    """Layer ``layer``'s attention with ``n_heads`` query heads on ``cache``; up to ``max_batch`` sequences a decode."""
+
+    def __init__(self, cache, layer, n_heads, max_batch, dtype=torch.bfloat16, scale=None, window=0):
+        self.cache, self.layer, self.dtype, self.window = cache, layer, DTYPES[dtype], window
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, cache.k.shape[2], cache.k.shape[4]
+        self.scale = self.head_dim ** -0.5 if scale is None else scale
+        n = qre_attn_decode_workspace_size(self._desc(), cache.desc, max_batch)
+        self.workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=cache.device)
+
+    def _desc(self, q=None, k=None, v=None, o=None):
+        return make_attn(self.n_heads, self.n_kv_heads, self.head_dim, self.dtype, self.scale, True, self.window,
+                         q, k, v, o)
+
+    def prefill(self, q, k, v, cu_q, cu_k, o=None, lse=None, stream=None):
+        """q [tokens, n_heads, head_dim], k, v [keys, n_kv_heads, head_dim], cu_q, cu_k [sequences + 1]."""
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        qre_attn_prefill(self._desc(q, k, v, o), cu_q.numel() - 1, q.shape[0], k.shape[0], cu_q, cu_k, q, k, v, o,
+                         lse, stream)
+        return o
+
+    def decode(self, q, seqs, o=None, lse=None, max_len=0, stream=None):
+        """q [sequences, n_heads, head_dim]: the newest token of each sequence, its row reserved and written before."""
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        qre_attn_decode(self._desc(q, o=o), self.cache.desc, self.layer, q.shape[0], seqs, max_len, q, o, lse,
+                        self.workspace, stream=stream)
+        return o

@@ -241,8 +241,8 @@ def staged_prefill(layers, inputs, areas, copy_stream, T, stream=None):
     experts staged into HBM one layer ahead on ``copy_stream``.
 
     layers: MoELayer objects; inputs: (x, w_router, bias) per layer (the layers are
-    independent here: between MoE layers a model has attention, which is not this
-    library's); areas: two StagingArea objects used alternately.  Ordering: layer l
+    independent here: what a model has between them, attention and projections, does
+    not run in this call); areas: two StagingArea objects used alternately.  Ordering: layer l
     waits for its area's copies; the copies into an area wait until the layer that
     last read it has finished its expert FFN.  Works inside CUDA graph capture.
     """
