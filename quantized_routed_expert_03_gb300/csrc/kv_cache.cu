@@ -270,15 +270,25 @@ __device__ void copy_pages(const qre_kv_cache& c, const int32_t* from, const int
                            int ctas) {
   const size_t page = (size_t)c.n_kv_heads * c.page_size * c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2);
   const int vecs = (int)(page / 16);
-  const long long items = (long long)copies * c.n_layers * 2;
+  constexpr int kEach = 8;              // 16-byte pieces of a thread on their way
+  const int slices = (vecs + kEach * 256 - 1) / (kEach * 256);
+  const int per_copy = 2 * c.n_layers * slices;
+  const long long items = (long long)copies * per_copy;
   for (long long it = first_cta; it < items; it += ctas) {
-    const int j = (int)(it / (2 * c.n_layers)), l = (int)(it % (2 * c.n_layers)) >> 1;
+    const int j = (int)(it / per_copy), rest = (int)(it - (long long)j * per_copy);
+    const int run = rest / slices, i0 = (rest - run * slices) * kEach * 256 + (int)threadIdx.x;
     const int a = from[j], b = to[j];
     if (!page_ok(c, a) || !page_ok(c, b)) continue;
-    char* base = static_cast<char*>((it & 1) ? c.v : c.k) + (size_t)l * c.n_pages * page;
+    char* base = static_cast<char*>((run & 1) ? c.v : c.k) + (size_t)(run >> 1) * c.n_pages * page;
     const uint4* s = reinterpret_cast<const uint4*>(base + (size_t)a * page);
     uint4* d = reinterpret_cast<uint4*>(base + (size_t)b * page);
-    for (int i = threadIdx.x; i < vecs; i += blockDim.x) d[i] = s[i];
+    uint4 x[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (i0 + e * 256 < vecs) x[e] = s[i0 + e * 256];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (i0 + e * 256 < vecs) d[i0 + e * 256] = x[e];
   }
 }
 
