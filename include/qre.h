@@ -581,8 +581,8 @@ QRE_API qre_status qre_attn_decode_workspace_size(const qre_attn* attn, const qr
  * Attention of one new token per sequence over the cache: query i belongs to
  * sequence seqs[i] (NULL: i) and sees its seq_len positions (the new token's own
  * row, written before, included), or the last `window` of them.
- *   max_len  host: an upper bound of the lengths, 0 if not known; a small one (or
- *            a small window) has short sequences left whole, which saves a launch;
+ *   max_len  host: an upper bound of the lengths, 0 if not known.  It chooses how
+ *            the work is split (short sequences are not cut, which saves a launch);
  *            a wrong one costs time and nothing else
  *   q, o     [n][n_heads][head_dim], device; lse [n][n_heads] fp32 or NULL
  * A bad id gives the empty result and QRE_DEV_BAD_INDEX; a position whose page

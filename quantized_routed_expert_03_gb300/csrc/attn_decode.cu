@@ -20,11 +20,19 @@
 // inside one range is finished there; one that is cut leaves a part (o, m, l in
 // fp32) per range in the workspace, and a second, dependent launch joins the
 // parts in the order of the ranges, so results do not depend on timing.
-// Where max_len or the window says that no unit has more than kWholeChunks chunks,
-// ranges begin at units and there is no join.  32 heads on 8, D = 128, one length
-// for all, cut / whole: 4 chunks (64 positions) 8.6 / 7.1 us for 1 sequence, 10.5 /
-// 8.3 for 64, 20.0 / 13.7 for 256; 8 chunks 8.8 / 10.1, 11.9 / 11.7, 23.8 / 20.5;
-// 16 chunks 9.5 / 15.9, 13.2 / 18.3, 36.7 / 36.8.
+// Where max_len or the window says that all units are short, none is cut and there
+// is no join launch.  Units of up to two chunks (four when there are more units than
+// CTAs) are left whole, each to one warp.  When a unit can have a CTA or a cluster of
+// 2, 4 or 8 to itself, its warps share its chunks, up to eight each, and meet in
+// shared memory.  The ways that lengths of one size took, 32 heads on 8, D = 128, us:
+//   sequences x positions   cut    whole   shared by (warps)
+//         1 x   64          9.0     7.4      7.3 (4)
+//         1 x  777         10.9    42.4     16.6 (4)  10.4 (16)   9.1 (32)
+//         1 x 4096         14.8   202       31.8 (8)  19.8 (16)  14.2 (32)
+//         9 x  777         16.3    42.7     12.7 (8)  11.2 (16)  23.5 (32: two waves)
+//        16 x 2048         20.1   104       21.3 (8)
+//        38 x  256         12.4    17.5     11.0 (4)
+//        76 x   64         11.6     8.8     15.3 (4: two waves)
 //
 // A warp runs on its own, with no barrier (with ranges of CTAs, whose warps met at
 // the end of every unit, 256 sequences of up to 1500 positions took 57 us instead
@@ -57,7 +65,8 @@ constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk
 constexpr int kRows = 16;             // query heads of a unit at most
 constexpr int kMaxCtas = 1024;        // of the main kernel
 constexpr int kUnitCost = 2;          // chunks that the begin and the end of a unit are worth (see below)
-constexpr int kWholeChunks = 4;       // units of so many chunks are not cut (see below)
+constexpr int kMostWays = 32;         // warps of a cluster of 8 CTAs
+constexpr int kMostShare = 8;         // chunks of a warp that shares a unit
 constexpr int kMinChunks = 2;         // of a range: fewer would save nothing and leave more parts to join
 
 // What the main kernel leaves for the join, in the workspace.
@@ -147,12 +156,69 @@ struct Seq {
   int row, len, first;   // table row, length, places of the queries before (for one unit each)
 };
 
+// Parts of four outputs of a unit, with a running maximum and sum: the heads r0 + 2 j of one dimension,
+// as they lie in a part (slot: 16 bytes of it).
+struct Joined {
+  float m[4], l[4], x[4];
+  __device__ __forceinline__ Joined() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m[j] = -INFINITY;
+      l[j] = x[j] = 0.0f;
+    }
+  }
+  __device__ __forceinline__ void add(const float4& y4, const float2 (&e)[4]) {
+    const float y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float to = fmaxf(m[j], e[j].x);
+      // what saw nothing (m = -inf) counts nothing; a NaN in l stays one
+      const float f = m[j] == to ? 1.0f : ex2(m[j] - to), fe = e[j].x == to ? 1.0f : ex2(e[j].x - to);
+      m[j] = to;
+      l[j] = l[j] * f + e[j].y * fe;
+      x[j] = x[j] * f + y[j] * fe;
+    }
+  }
+  // o = x / l of the j-th head of a slot (and lse, with the head's first dimension)
+  template <int DT, bool F8, int NH>
+  static __device__ __forceinline__ void write(const qre_attn& a, int slot, int j, int t, int h0, int rows, float vs, float M,
+                                               float L, float X, uint16_t* o, float* lse) {
+    const int reg = slot >> 3, i = (reg >> 2) / NH, high = (reg >> 1) & 1;
+    const int r = 8 * ((reg >> 2) % NH) + (reg & 1) + 2 * j;
+    const int d = 16 * i + (F8 ? 2 * (slot & 7) + high : (slot & 7) + 8 * high);
+    if (r >= rows) return;
+    o[(size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + d] =
+        (uint16_t)pack2<DT>(L == 0.0f ? 0.0f : X * (vs / L), 0.0f);
+    if (lse && d == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+  }
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// What lies at a shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 peer_float4(uint32_t addr, int rank) {
+  float4 r;
+  asm volatile("{.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n\t}"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ float2 peer_float2(uint32_t addr, int rank) {
+  float2 r;
+  asm volatile("{.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [p];\n\t}"
+               : "=f"(r.x), "=f"(r.y)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return r;
+}
+
 template <int DT, int CT, int D, int NH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
                        const int32_t* __restrict__ seqs, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
                        float* __restrict__ lse, Header* __restrict__ header, float* __restrict__ parts, int stages,
-                       int by_unit, int* status) {
+                       int ways, int* status) {
   using K = Decode<DT, CT, D, NH>;
   constexpr int CK = K::CK, KS = K::KS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -160,6 +226,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   Seq* sq = reinterpret_cast<Seq*>(smem + (size_t)kWarps * stages * 2 * kTile);   // [n + 1]
   __shared__ int scan_part[kWarps];
   __shared__ int scan_total;
+  __shared__ int has_part[kWarps];
+  __shared__ float2 joined[8 * NH];   // (m, l) of the heads
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.n_heads / a.n_kv_heads;
   const int blocks = (g + kRows - 1) / kRows;       // head blocks of a KV head
@@ -214,16 +282,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (tid == 0) sq[n].first = before;
   __syncthreads();
   const long long total = (long long)before * units;
-  const long long want = by_unit ? (long long)n * units : (total + kMinChunks - 1) / kMinChunks;
+  const bool together = ways > 1;   // a cluster has one unit, `ways` warps share its chunks
+  const long long want = ways ? (long long)n * units : (total + kMinChunks - 1) / kMinChunks;
   const long long all = (long long)gridDim.x * kWarps;
-  const int ranges = (int)(want < all ? want : all);
-  const int me = warp * (int)gridDim.x + blockIdx.x;   // this warp's range: few ranges spread over the SMs
-  // the place at which range b begins: any, or (by_unit) a unit's first
+  const int ranges = (int)(together ? all : want < all ? want : all);
+  // this warp's range: few ranges spread over the SMs
+  const int me = together ? (int)blockIdx.x * kWarps + warp : warp * (int)gridDim.x + (int)blockIdx.x;
+  // the place at which range b begins: any, or a unit's first, or one of `ways` shares of a unit
   auto begin = [&](int b) {
-    if (!by_unit) return range_begin(b, ranges, total);
-    const long long u = (long long)n * units * b / ranges;
+    if (!ways) return range_begin(b, ranges, total);
+    const long long u = together ? b / ways : (long long)n * units * b / ranges;
     const int t = (int)(u / units);
-    return t >= n ? total : (long long)sq[t].first * units + (u - (long long)t * units) * (sq[t + 1].first - sq[t].first);
+    if (t >= n) return total;
+    const int nch = sq[t + 1].first - sq[t].first, i = together ? b % ways : 0;
+    return (long long)sq[t].first * units + (u - (long long)t * units) * nch +
+           (i && nch ? kUnitCost + (long long)(nch - kUnitCost) * i / ways : 0);
   };
 
   // queries that see nothing
@@ -236,15 +309,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (lse)
       for (int h = tid; h < a.n_heads; h += kThreads) lse[(size_t)t * a.n_heads + h] = -INFINITY;
   }
-  if (blockIdx.x == 0 && !by_unit) {
+  if (blockIdx.x == 0 && !ways) {
     if (tid == 0) *header = Header{total, ranges, 0};
     int32_t* firsts = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(header) + kFirstsAt);
     for (int t = tid; t <= n; t += kThreads) firsts[t] = sq[t].first;
   }
   if (me >= ranges) return;
   const long long c0 = begin(me), c1 = begin(me + 1);
-  if (c0 >= c1) return;
+  if (c0 >= c1 && !together) return;
 
+  if (together && lane == 0) has_part[warp] = 0;
+  __syncwarp();
+  if (c0 < c1) {   // (always, unless together)
   // the query that chunk c0 belongs to
   int t_first;
   {
@@ -589,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nh][e] += __shfl_xor_sync(0xffffffffu, l[nh][e], d);
     if (s1 <= k0) {               // none of its chunks
-    } else if (s0 <= k0 && s1 == u1) {   // whole: o = O / l, transposed so that a lane has neighbouring dimensions of head lane / 4
+    } else if (!together && s0 <= k0 && s1 == u1) {   // whole: o = O / l, transposed so that a lane has neighbouring dimensions of head lane / 4
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
         float inv[2];
@@ -617,7 +693,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
     } else {                      // a part, as it lies in the registers
-      float* part = parts + ((size_t)2 * me + (s0 == c0 ? 0 : 1)) * part_floats<D, NH>();
+      float* part = together ? reinterpret_cast<float*>(ring) : parts + ((size_t)2 * me + (s0 == c0 ? 0 : 1)) * part_floats<D, NH>();
+      if (together) {            // over the ring, from which nothing more is read
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) has_part[warp] = 1;
+      }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -635,6 +716,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     cp = np;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  if (!together) return;
+  // ---- the shares of the unit meet: those of a CTA in its first warp's ring, then those of the CTAs,
+  // each of which finishes some of the outputs
+  constexpr int kSlots = 2 * NH * D;   // four outputs each, see Joined
+  const int ctas = ways / kWarps, rank = (int)blockIdx.x % ctas, u = (int)blockIdx.x / ctas;
+  uint8_t* rings = ring - (size_t)warp * stages * 2 * kTile;
+  __syncthreads();
+  for (int slot = tid; slot < kSlots; slot += kThreads) {
+    const int reg = slot >> 3, r0 = 8 * ((reg >> 2) % NH) + (reg & 1);
+    Joined x;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (!has_part[w]) continue;
+      const float* part = reinterpret_cast<const float*>(rings + (size_t)w * stages * 2 * kTile);
+      const float2* ml = reinterpret_cast<const float2*>(part + 8 * NH * D) + r0;
+      const float2 e[4] = {ml[0], ml[2], ml[4], ml[6]};
+      x.add(*reinterpret_cast<const float4*>(part + 4 * slot), e);
+    }
+    *reinterpret_cast<float4*>(rings + 16 * slot) = make_float4(x.x[0], x.x[1], x.x[2], x.x[3]);
+    if ((reg >> 2) < NH && !(reg & 2) && !(slot & 7))
+#pragma unroll
+      for (int j = 0; j < 4; ++j) joined[r0 + 2 * j] = make_float2(x.m[j], x.l[j]);
+  }
+  cluster_arrive();
+  cluster_wait();
+  const int t = u / units, unit = u - t * units, hk = unit / blocks, h0 = hk * g + (unit - hk * blocks) * kRows;
+  const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
+  const float vs = K::F8 && c.v_scale ? c.v_scale[(size_t)layer * c.n_kv_heads + hk] : 1.0f;
+  for (int i = tid; i < kSlots / ctas; i += kThreads) {
+    const int slot = rank * (kSlots / ctas) + i, reg = slot >> 3, r0 = 8 * ((reg >> 2) % NH) + (reg & 1);
+    Joined x;
+    const uint32_t at = smem_addr(rings + 16 * slot), ml = smem_addr(joined + r0);
+#pragma unroll 4
+    for (int b = 0; b < ctas; ++b) {
+      float2 e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = peer_float2(ml + 16 * j, b);
+      x.add(peer_float4(at, b), e);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      Joined::write<DT, K::F8, NH>(a, slot, j, t, h0, rows, vs, x.m[j], x.l[j], x.x[j], o, lse);
+  }
+  cluster_arrive();   // nobody leaves while its memory is read
+  cluster_wait();
 }
 
 // Joins the parts of a unit that was cut, with a running maximum and sum.  A thread
@@ -690,45 +817,25 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const int rows = (hk + 1) * g - h0 < kRows ? (hk + 1) * g - h0 : kRows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slot = SPLIT ? 32 * blockIdx.y + lane : (int)blockDim.x * blockIdx.y + tid, reg = slot >> 3, r0 = 8 * ((reg >> 2) % NH) + (reg & 1);
-  float m[4], l[4], x[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    m[j] = -INFINITY;
-    l[j] = x[j] = 0.0f;
-  }
+  Joined x;
 #pragma unroll 4
   for (int i = SPLIT ? warp : 0; i < np; i += SPLIT ? 8 : 1) {
     const float* part = i == 0 ? first : parts + (size_t)2 * (b0 + i) * PF;
-    const float4 y4 = *reinterpret_cast<const float4*>(part + 4 * slot);
-    const float y[4] = {y4.x, y4.y, y4.z, y4.w};
-    const float2* ml = reinterpret_cast<const float2*>(part + 8 * NH * D);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 e = ml[r0 + 2 * j];
-      const float to = fmaxf(m[j], e.x);
-      // what saw nothing (m = -inf) counts nothing; a NaN in l stays one
-      const float f = m[j] == to ? 1.0f : ex2(m[j] - to), fe = e.x == to ? 1.0f : ex2(e.x - to);
-      m[j] = to;
-      l[j] = l[j] * f + e.y * fe;
-      x[j] = x[j] * f + y[j] * fe;
-    }
+    const float2* ml = reinterpret_cast<const float2*>(part + 8 * NH * D) + r0;
+    const float2 e[4] = {ml[0], ml[2], ml[4], ml[6]};
+    x.add(*reinterpret_cast<const float4*>(part + 4 * slot), e);
   }
   const float vs = v_scale ? v_scale[hk] : 1.0f;
   auto write = [&](int sl, int j, float M, float L, float X) {
-    const int rg = sl >> 3, i = (rg >> 2) / NH, high = (rg >> 1) & 1;
-    const int r = 8 * ((rg >> 2) % NH) + (rg & 1) + 2 * j, d = 16 * i + (F8 ? 2 * (sl & 7) + high : (sl & 7) + 8 * high);
-    if (r >= rows) return;
-    o[(size_t)t * a.o_token + (size_t)(h0 + r) * a.o_head + d] =
-        (uint16_t)pack2<DT>(L == 0.0f ? 0.0f : X * (vs / L), 0.0f);
-    if (lse && d == 0) lse[(size_t)t * a.n_heads + h0 + r] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+    Joined::write<DT, F8, NH>(a, sl, j, t, h0, rows, vs, M, L, X, o, lse);
   };
   if constexpr (SPLIT) {
     __shared__ float ms[8][32][4], ls[8][32][4], xs[8][32][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      ms[warp][lane][j] = m[j];
-      ls[warp][lane][j] = l[j];
-      xs[warp][lane][j] = x[j];
+      ms[warp][lane][j] = x.m[j];
+      ls[warp][lane][j] = x.l[j];
+      xs[warp][lane][j] = x.x[j];
     }
     __syncthreads();
     if (tid >= 128) return;
@@ -745,7 +852,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     write(32 * blockIdx.y + k, j, M, L, X);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) write(slot, j, m[j], l[j], x[j]);
+    for (int j = 0; j < 4; ++j) write(slot, j, x.m[j], x.l[j], x.x[j]);
   }
 }
 
@@ -771,7 +878,7 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
   const int g = a.n_heads / a.n_kv_heads;
   const size_t fixed = (size_t)(n + 1) * sizeof(Seq);
   // what the CTAs of an SM share (1 KB of each is the system's, and the kernel's static arrays)
-  const long long room = ((long long)device_max_smem_optin() + 1024) / kCtasPerSm - 1024 - 128 - (long long)fixed;
+  const long long room = ((long long)device_max_smem_optin() + 1024) / kCtasPerSm - 1024 - 256 - (long long)fixed;
   const int stages = room >= 3ll * kWarps * 2 * kTile ? 3 : 2;
   const size_t smem = (size_t)stages * kWarps * 2 * kTile + fixed;
   Header* header = static_cast<Header*>(ws);
@@ -783,15 +890,26 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
   // parts by warps where units are few (8 units of 49 chunks each: 7.4 us by threads, 6.3 us by warps;
   // 512 units of two or three parts: 16.7 us by warps, 9 us by threads)
   const bool split = all_units <= 64;
-  // Whole units for the warps, and no join, where the caller's bound or the window says that all are short
+  // Units are not cut at the warps' convenience where the caller's bound or the window says that all
+  // are short: left whole, or shared by the warps of a cluster (see above)
   const int most = a.window > 0 && (max_len == 0 || a.window < max_len) ? a.window : max_len;
-  const int by_unit = most > 0 && most <= kWholeChunks * (kTile / (a.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)));
+  const int chunk = kTile / (a.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)), chunks = (int)(((long long)most + chunk - 1) / chunk);
+  int ways = 0;
+  if (chunks > 0 && chunks <= (all_units > grid ? 4 : 2)) {
+    ways = 1;
+  } else if (chunks > 0 && all_units <= grid) {
+    ways = kWarps;
+    while (2 * chunks > 3 * ways && ways < kMostWays && all_units * (2 * ways / kWarps) <= grid) ways *= 2;
+    if (chunks > kMostShare * ways) ways = 0;
+  }
   auto go = [&](auto kernel, auto join, int slots) -> cudaError_t {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kernel, dim3(grid), dim3(kThreads), smem, stream, a, c, layer, n, seqs,
-                         static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), lse, header, parts, stages, by_unit, status);
-    if (e != cudaSuccess || by_unit) return e;
+    const int ctas = ways / kWarps;
+    e = launch_dependent_cluster(kernel, dim3(ctas ? (unsigned)all_units * ctas : grid), dim3(kThreads), ctas ? ctas : 1,
+                                 smem, stream, a, c, layer, n, seqs, static_cast<const uint16_t*>(q),
+                                 static_cast<uint16_t*>(o), lse, header, parts, stages, ways, status);
+    if (e != cudaSuccess || ways) return e;
     const int threads = split || slots > 256 ? 256 : slots;
     return launch_dependent(join, dim3((unsigned)(by_cut ? cuts : all_units), slots / (split ? 32 : threads)),
                             dim3(threads), 0, stream, a, n, by_cut, v_scale, static_cast<uint16_t*>(o), lse,

@@ -53,20 +53,28 @@ cudaError_t ensure_smem_limit(const void* kernel, int bytes);
 // (griddepcontrol.launch_dependents) only after that wait, so a dependent's
 // early part never overlaps anything but its direct predecessor.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                             Args... args) {
+cudaError_t launch_dependent_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, size_t smem,
+                                     cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
   return err != cudaSuccess ? err : cudaGetLastError();
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+  return launch_dependent_cluster(kernel, grid, block, 1, smem, stream, args...);
 }
 
 // Kernel launchers (return the launch error, cudaSuccess otherwise).

@@ -467,6 +467,40 @@ def test_decode_bad_ids_lengths_and_missing_pages():
     assert torch.equal(o[[0, 1, 3]], want[[0, 1, 3]])
 
 
+@pytest.mark.parametrize("H,Hk,D,kind,cache", [(32, 8, 128, "bf16", "bf16"), (40, 2, 64, "fp16", "fp16"), (6, 2, 128, "fp16", "e4m3")])
+@pytest.mark.parametrize("bound", [40, 150, 400, 900, 2000])
+def test_decode_shared_by_a_cluster(H, Hk, D, kind, cache, bound):
+    """Few units under a bound: 4 to 32 warps share each.  Lengths of 0 and 1, the bound itself and (a wrong bound) far
+    more, a page that is missing, a bad id, another stream."""
+    lens = [bound, 0, 1, bound // 2, 3 * bound, 97]
+    pg = Paged(lens, Hk, D, 16, cache)
+    q = randn((len(lens), H, D), 7, kind)
+    v_max = float(pg.v.float().abs().max())
+    ref = decode_ref(pg, q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    o, l = run_decode(pg, q, kind, max_len=bound, stream=stream)
+    stream.synchronize()
+    assert qre.qre_read_device_status() == 0
+    check(o, l, ref, kind, 3 * bound, v_max)
+    again, _ = run_decode(pg, q, kind, max_len=bound)
+    assert torch.equal(o, again)
+    one, l1 = run_decode(pg, q, kind, max_len=bound, window=1)      # the last position's values themselves
+    check(one, l1, decode_ref(pg, q, window=1), kind, 1, v_max)
+
+    pg.table[int(pg.seqs[5]), 2] = -1                               # positions 32 .. 47 of 97 missing
+    pg.seqs[0] = 10 ** 6
+    o, l = run_decode(pg, q, kind, max_len=bound)
+    assert qre.qre_read_device_status() == qre.QRE_DEV_BAD_INDEX
+    assert (o[0] == 0).all() and torch.isneginf(l[0]).all()
+    assert torch.equal(o[1:5], again[1:5])
+    k, v = pg.rows(5, 1)
+    seen = np.r_[0:32, 48:97]
+    for h in range(H):
+        r = oatt.attend(npy(q)[5, h:h + 1], k[seen, h // (H // Hk)], v[seen, h // (H // Hk)], D ** -0.5, [0], [len(seen)])
+        check(o[5, h:h + 1], l[5, h:h + 1], r, kind, 97, v_max)
+
+
 def test_decode_pool_beyond_32_bits():
     heads, page, dim, n_pages = 8, 64, 128, 40000             # 2.6e9 elements
     k = torch.empty((1, n_pages, heads, page, dim), dtype=torch.bfloat16, device=DEV)
