@@ -173,48 +173,41 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* z) {
                : "memory");
 }
 
-// One piece of work: two query tiles of one sequence and head group.
-struct Work {
+// One piece of work: two query tiles of one sequence and head group, with what every warp wants to
+// know of it (worked out once, by the warp that finds it: between two pieces every warp's way is
+// on the critical path, and cold code takes long).
+struct Range {
+  int jb, je;   // key tiles [jb, je) of the sequence
+};
+struct alignas(16) Work {
   int q0, q_len, k0, k_len;   // the sequence
   int tok0;                   // first token, in the sequence
   int h0;                     // first head
   int end;                    // no more work
   int poison;                 // a value that is not finite was taken out of a key tile
-};
-
-// What every warp derives from it.
-struct Range {
-  int jb, je;   // key tiles [jb, je) of the sequence
-};
-struct Job {
-  Range r0, r1;           // of the two query tiles
-  int jb, je;             // of both
-  int lo_last, hi_first;  // first key of the last token, end of the keys of the first
-  __device__ __forceinline__ Job(const qre_attn& a, const Work& w, int tt) {
-    const int shift = w.k_len - w.q_len;   // position of token i is i + shift
-    auto keys_of = [&](int t) {            // both bounds grow with the token
-      Range r{0, 0};
-      const int ta = w.tok0 + t * tt, tb = ta + tt < w.q_len ? ta + tt : w.q_len;
-      if (ta < tb) {
-        int lo, hi, x;
-        visible_range(ta + shift, w.k_len, a.causal, a.window, lo, x);
-        visible_range(tb - 1 + shift, w.k_len, a.causal, a.window, x, hi);
-        if (hi > lo) {
-          r.jb = lo / kN;
-          r.je = (hi + kN - 1) / kN;
-        }
+  Range r[2];                 // key tiles of the two query tiles
+  int jb, je;                 // of both
+  int lo_last, hi_first;      // first key of the last token, end of the keys of the first
+  int lo_max[2], hi_min[2];   // the same of each query tile
+  __device__ __forceinline__ void plan(const qre_attn& a, int tt) {
+    const int shift = k_len - q_len;   // position of token i is i + shift
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {      // both bounds grow with the token
+      const int ta = tok0 + t * tt, tb = ta + tt < q_len ? ta + tt : q_len;
+      int lo, hi;
+      r[t] = Range{0, 0};
+      visible_range(ta + shift, k_len, a.causal, a.window, lo, hi_min[t]);
+      visible_range(tb - 1 + shift, k_len, a.causal, a.window, lo_max[t], hi);
+      if (ta < tb && hi > lo) {
+        r[t].jb = lo / kN;
+        r[t].je = (hi + kN - 1) / kN;
       }
-      return r;
-    };
-    r0 = keys_of(0);
-    r1 = keys_of(1);
-    if (r0.je <= r0.jb) r0 = r1;   // tokens that see nothing go along, so that tile 0 has keys if the work has
-    jb = r0.jb;
-    je = r1.je > r1.jb ? r1.je : r0.je;
-    const int last = (w.tok0 + 2 * tt < w.q_len ? w.tok0 + 2 * tt : w.q_len) - 1;
-    int x;
-    visible_range(last + shift, w.k_len, a.causal, a.window, lo_last, x);
-    visible_range(w.tok0 + shift, w.k_len, a.causal, a.window, x, hi_first);
+    }
+    if (r[0].je <= r[0].jb) r[0] = r[1];   // tokens that see nothing go along, so that tile 0 has keys if the work has
+    jb = r[0].jb;
+    je = r[1].je > r[1].jb ? r[1].je : r[0].je;
+    hi_first = hi_min[0];
+    lo_last = tok0 + tt < q_len ? lo_max[1] : lo_max[0];
   }
   // some token of the work does not see all of key tile j
   __device__ __forceinline__ bool special(int j) const { return j * kN < lo_last || (j + 1) * kN > hi_first; }
@@ -345,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sums_full = work_empty + kWorks;     // [2]: a query tile's sums and maxima are there
   uint64_t* o_free = sums_full + 2;         // [2]: its output (and they) have been read
   uint64_t* answered = o_free + 2;
-  uint64_t* drain = answered + 1;           // [2]
-  Work* works = reinterpret_cast<Work*>(drain + 2);          // [kWorks]
+  uint64_t* drain = answered + 1;           // [2], and one that is not used: 28 + 2 SLOTS of 8 bytes, so
+  Work* works = reinterpret_cast<Work*>(drain + 3);          // [kWorks] begin at a multiple of 16
   float2* sums = reinterpret_cast<float2*>(works + kWorks);       // [2][kM]: (l, m in base 2) of the rows
   uint32_t* tmem_p = reinterpret_cast<uint32_t*>(sums + 2 * kM);
   int* misc = reinterpret_cast<int*>(tmem_p + 1);
@@ -431,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.k_len = cu_k[seq + 1] - w.k0;
           w.tok0 = tile * 2 * tt;
           w.h0 = (b % groups) * gp;
+          w.plan(a, tt);
         }
         if (n >= kWorks && !wait_for(&work_empty[n % kWorks], n / kWorks - 1)) break;
         if (lane == 0) {
@@ -455,9 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Work w;
       for (int n = 0; ok && take(n, w); ++n) {
-        const Job job(a, w, tt);
         give_back(n);
-        if (job.je <= job.jb) continue;
+        if (w.je <= w.jb) continue;
         const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
         const int qh = q_heads_move ? w.h0 : 0, kh = k_heads_move ? hk : 0, vh = v_heads_move ? hk : 0;
         ok = nq == 0 || wait_for(q_empty, nq - 1);
@@ -469,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *q_issued = nq + 1;
         }
         ++nq;
-        const int end = i0 + 2 * (job.je - job.jb);
+        const int end = i0 + 2 * (w.je - w.jb);
         for (int i = i0; ok && i < end; ++i) {
           const int s = i % P::SLOTS;
           ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
@@ -478,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&full[s], P::TILE);
             for (int x = 0; x < D / 64; ++x)
               tma_load_3d(skv + s * P::TILE + x * P::HALF, is_v ? &tv : &tk, 64 * x, is_v ? vh : kh,
-                          w.k0 + (job.jb + (i - i0) / 2) * kN, &full[s]);
+                          w.k0 + (w.jb + (i - i0) / 2) * kN, &full[s]);
             *issued = i + 1;
           }
         }
@@ -527,21 +520,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       if (t == 0) turn_to(0);
       for (int nw = 0; ok && take(nw, w); ++nw) {
-        const Job job(a, w, tt);
         give_back(nw);
-        const Range r = t ? job.r1 : job.r0;
+        const Range r = t ? w.r[1] : w.r[0];
         // a step of key tile j hands the turn to the other query tile if j is in [give_b, give_e) or is
         // the last (of tile 0: if tile 1 has keys), else to this one; a piece begins with tile 0
-        const bool two = job.r1.je > job.r1.jb;
-        const int give_b = t ? 0 : two ? job.r1.jb : INT_MAX, give_e = t ? job.r0.je - 1 : INT_MAX;
+        const bool two = w.r[1].je > w.r[1].jb;
+        const int give_b = t ? 0 : two ? w.r[1].jb : INT_MAX, give_e = t ? w.r[0].je - 1 : INT_MAX;
         const int last = two ? r.je - 1 : INT_MAX;
-        if (job.je <= job.jb) continue;
+        if (w.je <= w.jb) continue;
         ok = wait_for(q_full, nq);
         ++nq;
         if (ok && r.je <= r.jb && lead) mbar_arrive(q_empty);
         __syncwarp();
-        for (int j = job.jb; ok && j < job.je; ++j) {
-          const int i = i0 + 2 * (j - job.jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
+        for (int j = w.jb; ok && j < w.je; ++j) {
+          const int i = i0 + 2 * (j - w.jb), sv = (i + 1) % P::SLOTS, sk = (i + 2) % P::SLOTS;
           const bool mine = j >= r.jb && j < r.je, more = mine && j + 1 < r.je;
           const bool pass = (j >= give_b && j < give_e) || j == last;
           if (mine && j == r.jb) {
@@ -587,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) umma_commit_lead(&empty[sk], lead);
           if (more && j + 2 == r.je) umma_commit_lead(q_empty, lead);
         }
-        i0 += 2 * (job.je - job.jb);
+        i0 += 2 * (w.je - w.jb);
       }
     }
   } else if (warp >= kStoreWarp) {
@@ -601,10 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Work w;
     for (int nw = 0; ok && take(nw, w); ++nw) {
-      const Job job(a, w, tt);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const Range r = t ? job.r1 : job.r0;
+        const Range r = t ? w.r[1] : w.r[0];
         const int tile0 = w.tok0 + t * tt;
         if (!ok || tile0 >= w.q_len) continue;
         const bool any = r.je > r.jb;
@@ -645,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 64; ++i) y[i] = empty_row ? 0u : __float_as_uint(__uint_as_float(y[i]) * inv);
           if (poison && !empty_row) {
             const int hk = w.h0 / (a.n_heads / a.n_kv_heads);
-            for (int j = job.jb; j < job.je; ++j) {
-              if (!job.special(j)) continue;
+            for (int j = w.jb; j < w.je; ++j) {
+              if (!w.special(j)) continue;
               const int ka = j * kN > lo ? j * kN : lo, kb = (j + 1) * kN < hi ? (j + 1) * kN : hi;
               for (int key = ka; key < kb; ++key) {
                 const uint16_t* vr = v + (size_t)(w.k0 + key) * a.v_token + (size_t)hk * a.v_head + 64 * c;
@@ -694,20 +685,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         Work w;
         if (!take(nw, w)) break;
-        const Job job(a, w, tt);
         give_back(nw);
-        r = t ? job.r1 : job.r0;
-        iv = i0 + 1 - 2 * job.jb;
-        i0 += 2 * (job.je - job.jb);
+        r = t ? w.r[1] : w.r[0];
+        iv = i0 + 1 - 2 * w.jb;
+        i0 += 2 * (w.je - w.jb);
         if (r.je <= r.jb) continue;
         k_len = w.k_len;
-        const int shift = w.k_len - w.q_len, tile0 = w.tok0 + t * tt;   // the query tile's first token
-        int x;
-        const int tok = min(tile0 + (row >> gp_shift), w.q_len - 1);
-        visible_range(tok + shift, w.k_len, a.causal, a.window, lo, hi);
-        // the tile's own tokens: the last one's first key, the first one's last
-        visible_range(min(tile0 + tt, w.q_len) - 1 + shift, w.k_len, a.causal, a.window, lo_max, x);
-        visible_range(tile0 + shift, w.k_len, a.causal, a.window, x, hi_min);
+        const int tok = min(w.tok0 + t * tt + (row >> gp_shift), w.q_len - 1);
+        visible_range(tok + w.k_len - w.q_len, w.k_len, a.causal, a.window, lo, hi);
+        lo_max = t ? w.lo_max[1] : w.lo_max[0];
+        hi_min = t ? w.hi_min[1] : w.hi_min[0];
       }
       float m = -INFINITY, l = 0.0f;       // reference maximum (of the raw scores) and sum
       bool started = false;                // a key tile has been through
@@ -873,42 +860,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_32x32b_x16(sc + 16 * (b0 + b), *reinterpret_cast<uint32_t(*)[16]>(p + 16 * b));
         publish(part);
       };
-      // A tile that a mask cuts, or with rows that have no reference yet, piece by piece, the next one
-      // on its way.
+      // The same for a tile that a mask cuts, or with rows that have no reference yet.  (Code of its
+      // own: with both branches in the loop's usual way a prompt of 8192 tokens took 392 us, not 359.)
       auto edge = [&](auto pieces, bool masked, int part, int b0, int key0) {
         constexpr int NB = decltype(pieces)::value;
-        uint32_t y[2][32], p[16 * NB];
-        auto fetch = [&](int b) { tmem_ld_32x32b_x32(sc + 32 * (b0 + b), y[b & 1]); };
-        auto arrived = [&](int b) {
-          tmem_ld_wait();
+        uint32_t x[32 * NB], p[16 * NB];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(y[b & 1][i]));   // not before the wait
-          if (b + 1 < NB) fetch(b + 1);
-          if (masked) mask(y[b & 1], key0 + 32 * (b0 + b));
-        };
-        if (unset) {                       // rows that have seen no key: these set their references
+        for (int b = 0; b < NB; ++b) tmem_ld_32x32b_x32(sc + 32 * (b0 + b), *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
+        tmem_ld_wait();
+        if (masked)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mask(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * b), key0 + 32 * (b0 + b));
+        if (unset) {                         // rows that have seen no key: these set their references
           float mx[2] = {-INFINITY, -INFINITY};
-          fetch(0);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            arrived(b);
+          for (int i = 0; i < 32 * NB; i += 4)
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                mx[e] = max3(mx[e], __uint_as_float(y[b & 1][i + e]), __uint_as_float(y[b & 1][i + 2 + e]));
-          }
+            for (int e = 0; e < 2; ++e) mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 2 + e]));
           if (m == -INFINITY) m = fmaxf(mx[0], mx[1]);
           unset = __any_sync(0xffffffffu, m == -INFINITY);
         }
         const uint64_t off2 = offset();
         uint64_t sum[2] = {0, 0};
-        fetch(0);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          arrived(b);
-          weights(y[b & 1], p + 16 * b, off2, sum);
-        }
+        for (int b = 0; b < NB; ++b) weights(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * b), p + 16 * b, off2, sum);
         if (!fits(sum)) {
           careful(masked, part, b0, b0 + NB, key0);
           return;
