@@ -18,15 +18,17 @@
 // tensor memory, P over it in 16 bits, O beside it), eight weight the scores, one
 // thread per row, and four bring O out while the next piece goes on.
 //
-// What it measured (32 heads on 8, D = 128, bf16; of the 1901 TFLOP/s measured for
-// cuBLAS): one causal prompt of 8192 tokens 359 us, 1.53 PFLOP/s (81 %); 8 prompts of 7 to 4000 tokens, 106
-// Gflop, 124 us (45 % of it: short prompts are mostly tiles that a mask cuts).
-// A pair of query tiles takes some 2600 cycles per key tile of the 2048 that its
-// products need.  Steps on the prompt of 8192: one MMA thread and plain softmax
-// 522 us; MMA issued by a converged warp, three-operand maximum, paired fp32 414;
-// persistent, weights against a standing reference, P V begun on the first 96
-// keys, tiles in turn 384; output and work finding on warps of their own 358.
-// Slower: two threads a row (497), first parts of 64 keys (397).
+// What it measured (32 heads on 8, D = 128, bf16; cuBLAS: 1901 TFLOP/s): one causal
+// prompt of 8192 tokens 356 us, 1.54 PFLOP/s (81 %); 16 prompts of up to 2048, 106
+// Gflop, 116 us (48 %).  A pair of query tiles takes 2620 cycles per key tile of the
+// 2048 that its products need.  What short prompts lose is lost between two pieces
+// of work (some 6000 cycles): the first and the last key tile of a piece, cut by the
+// mask, run code that is not in the instruction cache, and O is handed over.
+// Steps on the prompt of 8192: one MMA thread and plain softmax 522 us; MMA issued
+// by a converged warp, three-operand maximum, paired fp32 414; persistent, weights
+// against a standing reference, P V begun on the first 96 keys, tiles in turn 384;
+// output and work finding on warps of their own 358.  Slower: two threads a row
+// (497), first parts of 64 keys (397), a query buffer released tile by tile (380).
 #include <climits>
 #include <type_traits>
 
@@ -587,13 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- output: o = O / l.  Warps of their own, because what leaves an SM leaves slowly (two tiles in
     // some 8000 cycles, by TMA through shared memory as by stores of each row's own thread): the
     // softmax goes on with the next piece of work meanwhile.
+    // Loops and not unrolled: what these warps execute pushes the softmax's code out of the instruction
+    // cache (unrolled, 16 prompts of up to 2048 tokens took 119.9 us, not 116.2).
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    int cnt[2] = {0, 0}, no[2] = {0, 0};
+    int cnt0 = 0, cnt1 = 0, no0 = 0, no1 = 0;
     bool ok = true;
     Work w;
     for (int nw = 0; ok && take(nw, w); ++nw) {
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const Range r = t ? w.r[1] : w.r[0];
         const int tile0 = w.tok0 + t * tt;
@@ -601,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool any = r.je > r.jb;
         float2 sum = make_float2(0.0f, 0.0f);
         if (any) {
-          cnt[t] += r.je - r.jb;
-          ok = wait_for(&sums_full[t], no[t]) && wait_for(&o_done[2 + t], cnt[t] - 1);
+          (t ? cnt1 : cnt0) += r.je - r.jb;
+          ok = wait_for(&sums_full[t], t ? no1 : no0) && wait_for(&o_done[2 + t], (t ? cnt1 : cnt0) - 1);
           if (!ok) continue;
           tc_fence_after();
           sum = sums[t * kM + row];
@@ -618,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool poison = *reinterpret_cast<volatile int*>(&works[nw % kWorks].poison) != 0;
         uint16_t* out = o + (size_t)(w.q0 + tok) * a.o_token + (size_t)head * a.o_head;
         const uint32_t oc = lanes + (t ? kO1 : kO0);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t y[64];
           if (any) {
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_32x32b_x32(oc + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(y + 32));
             tmem_ld_wait();
             if (c == D / 64 - 1) {       // the next piece may overwrite O and the sums
-              ++no[t];
+              ++(t ? no1 : no0);
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&o_free[t]);
