@@ -157,6 +157,10 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+__device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Of two 16-bit pairs the larger magnitudes, NaN if there is one.
 template <int DT>
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
@@ -383,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_p, kTmemCols);
     tmem_relinquish();
   }
+  if (warp == kTmaWarp && lane < 3) prefetch_tmap(lane == 0 ? &tq : lane == 1 ? &tk : &tv);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
