@@ -42,7 +42,7 @@ qre_status check_cache(const qre_kv_cache* c, bool scales) {
   if (!head_dim_ok(c->head_dim)) QRE_FAIL(QRE_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", c->head_dim);
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     QRE_FAIL(QRE_ERR_UNSUPPORTED, "page_size %d is not a power of two from 16 to 256", c->page_size);
-  if (c->n_kv_heads > 256) QRE_FAIL(QRE_ERR_UNSUPPORTED, "n_kv_heads %d > 256", c->n_kv_heads);
+  if (c->n_kv_heads > qre::kKvMaxHeads) QRE_FAIL(QRE_ERR_UNSUPPORTED, "n_kv_heads %d > %d", c->n_kv_heads, qre::kKvMaxHeads);
   if (c->n_pages >= kMaxCount || c->max_seqs >= kMaxCount || c->max_pages >= kMaxCount || c->n_layers >= kMaxCount)
     QRE_FAIL(QRE_ERR_UNSUPPORTED, "cache sizes must be below 2^24");
   if ((long long)c->max_pages * c->page_size > 0x7fffffffll)

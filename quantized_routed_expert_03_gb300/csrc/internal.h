@@ -144,6 +144,7 @@ bool make_tmap_rows16(CUtensorMap* m, const void* base, long long tokens, long l
 // Key-value cache (kv_cache.cu) and attention (attn_prefill.cu, attn_decode.cu).
 // The arguments have been checked (api_attn.cu).
 constexpr int kKvMaxRequests = 4096;   // sequences, requests or forks of one call
+constexpr int kKvMaxHeads = 256;       // KV heads
 size_t kv_ws_bytes(const qre_kv_cache& c);
 cudaError_t launch_kv_reserve(const qre_kv_cache& c, int n, const int32_t* seqs, const int32_t* n_new, void* ws,
                               int* status, cudaStream_t stream);

@@ -404,27 +404,32 @@ __device__ __forceinline__ float to_float(uint16_t b) {
   return RT == QRE_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half(b));
 }
 
-// Memory bound: each row is read and written once.  A CTA has a few tokens: where
-// their rows go is looked up once per token, while the rows' 16-byte pieces are on
-// their way into registers; no index needs a division of more than a multiply (the
-// first form, which divided 64-bit indices for every piece, took 33 us for 11,300
-// rows of K and V into an E4M3 cache instead of 16).
+// Memory bound: each row is read and written once.  A CTA has as many neighbouring
+// tokens as let all CTAs run at once; where their rows go, and the scales'
+// reciprocals, it looks up once, while the first rows' 16-byte pieces are on their
+// way into registers.  No index needs a division of more than a multiply.  11,278
+// tokens of 8 heads into E4M3 pages, with the free and the reservation before them:
+// 22.8 us; 25.3 with CTAs of two tokens (most of their time was those look-ups), 24.3
+// with four pieces of a thread on their way (fewer CTAs fit), 31 with a division for
+// every element.
 constexpr int kWriteThreads = 256;
-constexpr int kWriteEach = 2;        // pieces of a thread
+constexpr int kWriteEach = 2;        // pieces of a thread on their way
+constexpr int kWriteCtas = 8;        // of an SM
 constexpr int kWriteTokens = 64;     // of a CTA at most
 
 template <int RT, bool FP8>
-__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(
+__global__ void __launch_bounds__(kWriteThreads, kWriteCtas) kv_write_kernel(
     const __grid_constant__ qre_kv_cache c, int layer, const __grid_constant__ qre_kv_rows r, int n_tokens, int tokens,
     uint32_t magic, const int32_t* __restrict__ token_seq, const int32_t* __restrict__ token_pos,
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int* status) {
   __shared__ long long to[kWriteTokens];   // element of the token's row of head 0, -1: skipped
+  __shared__ float by[FP8 ? 2 : 1][FP8 ? kKvMaxHeads : 1];   // 1 / scale of K and of V
   grid_dependency_wait();
   grid_dependents_launch();
   const int per_head_shift = c.head_dim == 64 ? 3 : 4, per_row = c.n_kv_heads << per_head_shift, per_token = 2 * per_row;
   const int t0 = blockIdx.x * tokens, mine = n_tokens - t0 < tokens ? n_tokens - t0 : tokens;
   const int pieces = mine * per_token, ps_shift = 31 - __clz(c.page_size);
-  for (int i0 = 0; i0 < pieces; i0 += kWriteThreads * kWriteEach) {   // once, unless a token has more pieces
+  for (int i0 = 0; i0 < pieces; i0 += kWriteThreads * kWriteEach) {
     uint4 x[kWriteEach];
     int at_token[kWriteEach], at_rest[kWriteEach];
 #pragma unroll
@@ -441,6 +446,12 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(
       at_rest[e] = rest;
     }
     if (i0 == 0) {
+      if (FP8)
+        for (int i = threadIdx.x; i < 2 * c.n_kv_heads; i += kWriteThreads) {
+          const int is_v = i >= c.n_kv_heads, h = is_v ? i - c.n_kv_heads : i;
+          const float* scales = is_v ? c.v_scale : c.k_scale;
+          by[is_v][h] = scales ? __frcp_rn(scales[(size_t)layer * c.n_kv_heads + h]) : 1.0f;
+        }
       if ((int)threadIdx.x < mine) {
         const int pos = token_pos[t0 + threadIdx.x], s = token_seq[t0 + threadIdx.x];
         long long at = -1;
@@ -468,10 +479,8 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(
       if (!FP8) {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? c.v : c.k) + at) = x[e];
       } else {
-        // times the correctly rounded reciprocal, in fp32, then one rounding to 8 bits (a division for
-        // every element took 6 us more of the 15)
-        const float* scales = is_v ? c.v_scale : c.k_scale;
-        const float inv = scales ? __frcp_rn(scales[(size_t)layer * c.n_kv_heads + h]) : 1.0f;
+        // times the correctly rounded reciprocal, in fp32, then one rounding to 8 bits
+        const float inv = by[is_v][h];
         const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
         uint32_t out[2];
 #pragma unroll
@@ -534,10 +543,11 @@ cudaError_t launch_kv_write(const qre_kv_cache& c, int layer, const qre_kv_rows&
                             const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
                             int* status, cudaStream_t stream) {
   const int per_token = 2 * c.n_kv_heads * (c.head_dim / 8);   // 16-byte pieces: at most 8192
-  int tokens = kWriteThreads * kWriteEach / per_token;
-  tokens = tokens < 1 ? 1 : (tokens > kWriteTokens ? kWriteTokens : tokens);
-  while (tokens > 1 && (n_tokens + tokens - 1) / tokens < 2 * device_sm_count()) tokens /= 2;   // few tokens: more CTAs
-  // floor(i / per_token) = umulhi(i, magic) for the indices of a CTA (below 2^16): per_token is at most 2^13
+  const int ctas = device_sm_count() * kWriteCtas;
+  int tokens = ctas > 0 ? (n_tokens + ctas - 1) / ctas : 1;
+  const int most = (1 << 18) / per_token < kWriteTokens ? (1 << 18) / per_token : kWriteTokens;
+  tokens = tokens > most ? most : tokens < 1 ? 1 : tokens;
+  // floor(i / per_token) = umulhi(i, magic) for the indices of a CTA (below 2^18): per_token is at most 2^13
   const uint32_t magic = (uint32_t)((0x100000000ull + per_token - 1) / per_token);
   const dim3 grid((unsigned)((n_tokens + tokens - 1) / tokens));
   auto go = [&](auto kernel) {

@@ -199,6 +199,34 @@ def test_write(row, kind, dim, heads, page, fused):
         assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
 
 
+@pytest.mark.parametrize("heads,dim,n,kind", [(3, 64, 100003, "bf16"), (64, 128, 40000, "e4m3"), (256, 64, 2501, "bf16")])
+def test_write_many_tokens(heads, dim, n, kind):
+    """Several tokens for each CTA, up to the most that one takes; an odd number of tokens."""
+    page, cols = 64, 500
+    g = torch.Generator(device=DEV).manual_seed(2)
+    n_pages = -(-n // page) + 7
+    S = -(-n_pages // cols)
+    k, v = (torch.randn((n, heads, dim), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    pool_k, pool_v = (torch.zeros((2, n_pages, heads, page, dim), dtype=torch.uint8 if kind == "e4m3" else torch.bfloat16,
+                                  device=DEV).view(DT[kind][1]) for _ in range(2))
+    table = torch.full((S, cols), -1, dtype=torch.int32, device=DEV)
+    table.view(-1)[:n_pages] = torch.randperm(n_pages, generator=g, device=DEV).int()
+    at = torch.randperm(n_pages * page, generator=g, device=DEV)[:n]
+    seq, pos = (at // (cols * page)).int(), (at % (cols * page)).int()
+    scales = torch.rand((2, 2, heads), generator=g, device=DEV) + 0.25 if kind == "e4m3" else (None, None)
+    cache = qre.make_kv_cache(pool_k, pool_v, table, i32([0] * S), i32([1] * n_pages), DT[kind][0],
+                              *(s if s is None else s.contiguous() for s in scales))
+    qre.qre_kv_write(cache, 1, qre.make_kv_rows(qre.QRE_BF16, k, v), n, seq, pos, k, v)
+    assert qre.qre_read_device_status() == 0
+    bits = torch.uint8 if kind == "e4m3" else torch.int16
+    where = table.view(-1)[at // page].long(), (at % page)
+    for pool, new, sc in ((pool_k, k, scales[0]), (pool_v, v, scales[1])):
+        r = new if kind == "bf16" else (new.float() * (1.0 / sc[1])[:, None]).to(torch.float8_e4m3fn)
+        assert torch.equal(pool.view(bits)[1][where[0], :, where[1]], r.view(bits))
+        pool.view(bits)[1][where[0], :, where[1]] = 0
+        assert int(torch.count_nonzero(pool.view(bits))) == 0       # and nowhere else
+
+
 def test_write_without_a_page():
     pool = torch.zeros((1, 4, 1, 16, 64), dtype=torch.bfloat16, device=DEV)
     table = i32([0, -1, 9, 1]).view(2, 2)
