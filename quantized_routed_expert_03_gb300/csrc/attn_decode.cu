@@ -193,7 +193,10 @@ struct Joined {
   }
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();   // the aligned form wants the whole warp
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // What lies at a shared address in CTA `rank` of the cluster.
 __device__ __forceinline__ float4 peer_float4(uint32_t addr, int rank) {
