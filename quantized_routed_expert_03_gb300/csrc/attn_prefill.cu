@@ -39,9 +39,12 @@
 namespace qre {
 namespace {
 
-// For what TMA cannot address (rows that repeat: a token stride of 0) and calls
-// without any key: one warp per (query token, head); a lane scores one key at a
-// time, then the lanes share the head's dimensions for the values.
+constexpr int kFewKeys = 128, kFewWork = 1 << 23;   // see launch_attn_prefill
+
+// For a handful of keys, for what TMA cannot address (rows that repeat: a token
+// stride of 0) and for calls without any key: one warp per (query token, head); a
+// lane scores one key at a time, then has two neighbouring dimensions of each 64 for
+// the values.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q,
                                                         int total_k, const int32_t* __restrict__ cu_q,
@@ -49,68 +52,103 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
                                                         const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v, uint16_t* __restrict__ o,
                                                         float* __restrict__ lse, int* status) {
-  __shared__ float qs[8][D];
+  constexpr int W = D / 64;     // 32-bit words of a row for a lane
+  constexpr int kAhead = 8;     // keys whose values are on their way together
+  __shared__ __align__(16) float qs[8][D];
   grid_dependency_wait();
   grid_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + warp;
   if (unit >= (long long)total_q * a.n_heads) return;
   const int t = (int)(unit / a.n_heads), h = (int)(unit % a.n_heads), hk = h / (a.n_heads / a.n_kv_heads);
-  int s = -1;
-  for (int i = 0; i < n_seqs; ++i)
-    if (cu_q[i] <= t && t < cu_q[i + 1]) {
-      s = i;
-      break;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(q + (size_t)t * a.q_token + (size_t)h * a.q_head + 64 * w + 2 * lane);
+    qs[warp][64 * w + 2 * lane] = bits_to_float<DT>(x & 0xffffu) * a.scale * kLog2e;
+    qs[warp][64 * w + 2 * lane + 1] = bits_to_float<DT>(x >> 16) * a.scale * kLog2e;
+  }
+  int q0 = 0, q1 = 0, k0 = 0, k1 = 0, s = -1;   // the first sequence that has the token
+  for (int i0 = 0; i0 < n_seqs && s < 0; i0 += 32) {
+    const int i = i0 + lane;
+    if (i < n_seqs) {
+      q0 = cu_q[i];
+      q1 = cu_q[i + 1];
+      k0 = cu_k[i];
+      k1 = cu_k[i + 1];
     }
+    const unsigned has = __ballot_sync(0xffffffffu, i < n_seqs && q0 <= t && t < q1);
+    if (has) s = __ffs(has) - 1;
+  }
   if (s < 0) return;
-  const int q0 = cu_q[s], q1 = cu_q[s + 1], k0 = cu_k[s], k1 = cu_k[s + 1];
+  q0 = __shfl_sync(0xffffffffu, q0, s);
+  q1 = __shfl_sync(0xffffffffu, q1, s);
+  k0 = __shfl_sync(0xffffffffu, k0, s);
+  k1 = __shfl_sync(0xffffffffu, k1, s);
   if (q0 < 0 || q1 > total_q || k0 < 0 || k1 < k0 || k1 > total_k) {
     if (lane == 0) set_status(status, QRE_DEV_BAD_INDEX);
     return;
   }
   int lo, hi;
   visible_range(k1 - k0 - (q1 - q0) + t - q0, k1 - k0, a.causal, a.window, lo, hi);
-  for (int d = lane; d < D; d += 32)
-    qs[warp][d] = bits_to_float<DT>(q[(size_t)t * a.q_token + (size_t)h * a.q_head + d]) * a.scale * kLog2e;
   __syncwarp();
-  float m = -INFINITY, l = 0.0f, acc[D / 32] = {};
+  float m = -INFINITY, l = 0.0f, acc[2 * W] = {};
   for (int j0 = lo; j0 < hi; j0 += 32) {
     const int j = j0 + lane;
     float x = -INFINITY;
     if (j < hi) {
       const uint16_t* kr = k + (size_t)(k0 + j) * a.k_token + (size_t)hk * a.k_head;
-      x = 0.0f;
+      float part[2] = {0.0f, 0.0f};
+#pragma unroll
       for (int d = 0; d < D; d += 8) {
         const uint4 w = *reinterpret_cast<const uint4*>(kr + d);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x += qs[warp][d + 2 * e] * bits_to_float<DT>(u[e] & 0xffffu) +
-               qs[warp][d + 2 * e + 1] * bits_to_float<DT>(u[e] >> 16);
+        for (int e = 0; e < 4; ++e) {
+          part[0] = fmaf(qs[warp][d + 2 * e], bits_to_float<DT>(u[e] & 0xffffu), part[0]);
+          part[1] = fmaf(qs[warp][d + 2 * e + 1], bits_to_float<DT>(u[e] >> 16), part[1]);
+        }
       }
+      x = part[0] + part[1];
     }
     float mx = x;
+#pragma unroll
     for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
     const float m2 = fmaxf(m, mx), f = m == -INFINITY ? 0.0f : exp2f(m - m2);
     const float p = j < hi ? exp2f(x - m2) : 0.0f;
     float sum = p;
+#pragma unroll
     for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
     l = l * f + sum;
     m = m2;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] *= f;
-    for (int i = 0; i < 32 && j0 + i < hi; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      const uint16_t* vr = v + (size_t)(k0 + j0 + i) * a.v_token + (size_t)hk * a.v_head;
+    for (int i = 0; i < 2 * W; ++i) acc[i] *= f;
+    const int keys = hi - j0 < 32 ? hi - j0 : 32;
+    for (int i0 = 0; i0 < keys; i0 += kAhead) {
+      uint32_t y[kAhead][W];
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] += pi * bits_to_float<DT>(vr[lane + 32 * e]);
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int w = 0; w < W; ++w)   // rows that are not seen are not read
+          y[i][w] = i0 + i < keys ? *reinterpret_cast<const uint32_t*>(v + (size_t)(k0 + j0 + i0 + i) * a.v_token +
+                                                                       (size_t)hk * a.v_head + 64 * w + 2 * lane)
+                                  : 0u;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float pi = __shfl_sync(0xffffffffu, p, i0 + i);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          acc[2 * w] = fmaf(pi, bits_to_float<DT>(y[i][w] & 0xffffu), acc[2 * w]);
+          acc[2 * w + 1] = fmaf(pi, bits_to_float<DT>(y[i][w] >> 16), acc[2 * w + 1]);
+        }
+      }
     }
   }
   const bool empty = hi <= lo;
   const float inv = empty ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    o[(size_t)t * a.o_token + (size_t)h * a.o_head + lane + 32 * e] = (uint16_t)pack2<DT>(acc[e] * inv, 0.0f);
+  for (int w = 0; w < W; ++w)
+    *reinterpret_cast<uint32_t*>(o + (size_t)t * a.o_token + (size_t)h * a.o_head + 64 * w + 2 * lane) =
+        pack2<DT>(acc[2 * w] * inv, acc[2 * w + 1] * inv);
   if (lse && lane == 0) lse[(size_t)t * a.n_heads + h] = empty ? -INFINITY : m * kLn2 + logf(l);
 }
 
@@ -1009,7 +1047,13 @@ cudaError_t launch_attn_prefill(const qre_attn& a, int n_seqs, int total_q, int 
   // A tensor map wants a distance between tokens; without keys there is nothing to multiply.
   const bool maps = total_k > 0 && (total_q == 1 || a.q_token > 0) &&
                     (total_k == 1 || (a.k_token > 0 && a.v_token > 0));
-  if (maps) {
+  // A handful of keys is done before tensor memory and barriers are set up (one prompt of 16 tokens: 3.4
+  // us by rows, 6.8 by tiles at 8 heads of 64; 4.1, 7.5 at 32 of 128; one of 64: 7.7, 8.3 and 13.9, 9.8;
+  // 3 of 40: 6.0, 7.7 and 16.9, 9.5): what counts is the rows' work, by the sequences' mean length, and
+  // no more than some 14 us if one sequence has it all.
+  const long long work = (long long)total_q * a.n_heads * a.head_dim * total_k;
+  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys && work <= kFewWork && work / (n_seqs > 0 ? n_seqs : 1) <= kFewWork / 4;
+  if (maps && !few) {
     cudaError_t err = cudaSuccess;
     const bool d64 = a.head_dim == 64;
     const bool made =

@@ -106,6 +106,31 @@ def test_prefill(case, how):
     check(o, l, ref, kind, max(k_lens), float(v.abs().max()) if v.numel() else 0.0)
 
 
+@pytest.mark.parametrize("H,Hk,D,kind", [(8, 2, 64, "bf16"), (32, 8, 128, "fp16"), (3, 1, 128, "bf16")])
+@pytest.mark.parametrize("q_lens,k_lens", [([1], [1]), ([16], [16]), ([17], [17]), ([1, 0, 3], [33, 5, 40]), ([30, 9, 24], [30, 9, 24]),
+                                           ([0, 7, 0, 12], [4, 2, 0, 50]), ([64], [64]), ([65], [65]), ([1] * 40, [3] * 40)])
+def test_prefill_a_handful_of_keys(H, Hk, D, kind, q_lens, k_lens):
+    """Around the sizes at which the work goes by rows, not by tiles; what is not seen is NaN."""
+    q = randn((sum(q_lens), H, D), 1, kind, 1.5)
+    k, v = (randn((sum(k_lens), Hk, D), 2 + i, kind) for i in range(2))
+    for window in (0, 5):
+        ref = oatt.prefill(npy(q), npy(k), npy(v), q_lens, k_lens, 1.0 / math.sqrt(D), True, window)
+        kk, vv = k.clone(), v.clone()
+        y = 0
+        for nq, nk in zip(q_lens, k_lens):
+            lo, hi = oatt.visible(nq, nk, True, window)
+            seen = np.zeros(nk, bool)
+            for a, b in zip(lo, hi):
+                seen[a:b] = True
+            for j in np.flatnonzero(~seen):
+                kk[y + j] = vv[y + j] = float("nan")
+            y += nk
+        o, l = run_prefill(layout(q, "padded"), layout(kk, "padded"), layout(vv, "head_major"), q_lens, k_lens, kind,
+                           window=window, how="padded")
+        assert qre.qre_read_device_status() == 0
+        check(o, l, ref, kind, max(k_lens), float(v.abs().max()))
+
+
 def test_prefill_large_scores_and_scale():
     """Scores of hundreds, growing along the keys, so the running maximum moves again and again."""
     n, D = 700, 128
