@@ -19,8 +19,8 @@
 // thread per row, and four bring O out while the next piece goes on.
 //
 // What it measured (32 heads on 8, D = 128, bf16; cuBLAS: 1901 TFLOP/s): one causal
-// prompt of 8192 tokens 356 us, 1.54 PFLOP/s (81 %); 16 prompts of up to 2048, 106
-// Gflop, 116 us (48 %).  A pair of query tiles takes 2620 cycles per key tile of the
+// prompt of 8192 tokens 354 us, 1.55 PFLOP/s (82 %); 16 prompts of up to 2048, 106
+// Gflop, 115 us (48 %).  A pair of query tiles takes 2620 cycles per key tile of the
 // 2048 that its products need.  What short prompts lose is lost between two pieces
 // of work (some 6000 cycles): the first and the last key tile of a piece, cut by the
 // mask, run code that is not in the instruction cache, and O is handed over.
@@ -39,21 +39,21 @@
 namespace qre {
 namespace {
 
-constexpr int kFewKeys = 128, kFewWork = 1 << 23;   // see launch_attn_prefill
+constexpr int kFewKeys = 512, kFewWork = 1 << 22;   // see launch_attn_prefill
 
 // For a handful of keys, for what TMA cannot address (rows that repeat: a token
 // stride of 0) and for calls without any key: one warp per (query token, head); a
 // lane scores one key at a time, then has two neighbouring dimensions of each 64 for
 // the values.
 template <int DT, int D>
-__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q,
+__global__ void __launch_bounds__(256, 2) attn_rows_kernel(const __grid_constant__ qre_attn a, int n_seqs, int total_q,
                                                         int total_k, const int32_t* __restrict__ cu_q,
                                                         const int32_t* __restrict__ cu_k,
                                                         const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v, uint16_t* __restrict__ o,
                                                         float* __restrict__ lse, int* status) {
   constexpr int W = D / 64;     // 32-bit words of a row for a lane
-  constexpr int kAhead = 8;     // keys whose values are on their way together
+  constexpr int kAhead = 32 / W;   // keys whose values are on their way together, the first beside the keys
   __shared__ __align__(16) float qs[8][D];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -67,23 +67,34 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     qs[warp][64 * w + 2 * lane] = bits_to_float<DT>(x & 0xffffu) * a.scale * kLog2e;
     qs[warp][64 * w + 2 * lane + 1] = bits_to_float<DT>(x >> 16) * a.scale * kLog2e;
   }
-  int q0 = 0, q1 = 0, k0 = 0, k1 = 0, s = -1;   // the first sequence that has the token
-  for (int i0 = 0; i0 < n_seqs && s < 0; i0 += 32) {
-    const int i = i0 + lane;
-    if (i < n_seqs) {
-      q0 = cu_q[i];
-      q1 = cu_q[i + 1];
-      k0 = cu_k[i];
-      k1 = cu_k[i + 1];
+  int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+  bool found = false;           // the first sequence that has the token
+  for (int i0 = 0; i0 < n_seqs && !found; i0 += 128) {
+    int b[4][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int i = i0 + 32 * c + lane;
+      b[c][0] = b[c][1] = 0;    // has no token
+      if (i < n_seqs) {
+        b[c][0] = cu_q[i];
+        b[c][1] = cu_q[i + 1];
+        b[c][2] = cu_k[i];
+        b[c][3] = cu_k[i + 1];
+      }
     }
-    const unsigned has = __ballot_sync(0xffffffffu, i < n_seqs && q0 <= t && t < q1);
-    if (has) s = __ffs(has) - 1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const unsigned has = __ballot_sync(0xffffffffu, b[c][0] <= t && t < b[c][1]);
+      if (!has || found) continue;
+      const int at = __ffs(has) - 1;
+      q0 = __shfl_sync(0xffffffffu, b[c][0], at);
+      q1 = __shfl_sync(0xffffffffu, b[c][1], at);
+      k0 = __shfl_sync(0xffffffffu, b[c][2], at);
+      k1 = __shfl_sync(0xffffffffu, b[c][3], at);
+      found = true;
+    }
   }
-  if (s < 0) return;
-  q0 = __shfl_sync(0xffffffffu, q0, s);
-  q1 = __shfl_sync(0xffffffffu, q1, s);
-  k0 = __shfl_sync(0xffffffffu, k0, s);
-  k1 = __shfl_sync(0xffffffffu, k1, s);
+  if (!found) return;
   if (q0 < 0 || q1 > total_q || k0 < 0 || k1 < k0 || k1 > total_k) {
     if (lane == 0) set_status(status, QRE_DEV_BAD_INDEX);
     return;
@@ -93,7 +104,18 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   __syncwarp();
   float m = -INFINITY, l = 0.0f, acc[2 * W] = {};
   for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
+    const int j = j0 + lane, keys = hi - j0 < 32 ? hi - j0 : 32;
+    uint32_t y[kAhead][W];
+    auto fetch = [&](int i0) {   // rows that are not seen are not read
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          y[i][w] = i0 + i < keys ? *reinterpret_cast<const uint32_t*>(v + (size_t)(k0 + j0 + i0 + i) * a.v_token +
+                                                                       (size_t)hk * a.v_head + 64 * w + 2 * lane)
+                                  : 0u;
+    };
+    fetch(0);                    // beside the keys
     float x = -INFINITY;
     if (j < hi) {
       const uint16_t* kr = k + (size_t)(k0 + j) * a.k_token + (size_t)hk * a.k_head;
@@ -122,16 +144,8 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     m = m2;
 #pragma unroll
     for (int i = 0; i < 2 * W; ++i) acc[i] *= f;
-    const int keys = hi - j0 < 32 ? hi - j0 : 32;
     for (int i0 = 0; i0 < keys; i0 += kAhead) {
-      uint32_t y[kAhead][W];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-        for (int w = 0; w < W; ++w)   // rows that are not seen are not read
-          y[i][w] = i0 + i < keys ? *reinterpret_cast<const uint32_t*>(v + (size_t)(k0 + j0 + i0 + i) * a.v_token +
-                                                                       (size_t)hk * a.v_head + 64 * w + 2 * lane)
-                                  : 0u;
+      if (i0) fetch(i0);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const float pi = __shfl_sync(0xffffffffu, p, i0 + i);
@@ -1047,12 +1061,13 @@ cudaError_t launch_attn_prefill(const qre_attn& a, int n_seqs, int total_q, int 
   // A tensor map wants a distance between tokens; without keys there is nothing to multiply.
   const bool maps = total_k > 0 && (total_q == 1 || a.q_token > 0) &&
                     (total_k == 1 || (a.k_token > 0 && a.v_token > 0));
-  // A handful of keys is done before tensor memory and barriers are set up (one prompt of 16 tokens: 3.4
-  // us by rows, 6.8 by tiles at 8 heads of 64; 4.1, 7.5 at 32 of 128; one of 64: 7.7, 8.3 and 13.9, 9.8;
-  // 3 of 40: 6.0, 7.7 and 16.9, 9.5): what counts is the rows' work, by the sequences' mean length, and
-  // no more than some 14 us if one sequence has it all.
-  const long long work = (long long)total_q * a.n_heads * a.head_dim * total_k;
-  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys && work <= kFewWork && work / (n_seqs > 0 ? n_seqs : 1) <= kFewWork / 4;
+  // A handful of keys is done by rows before tensor memory and barriers are set up, and a tile holds
+  // one sequence's rows only.  By rows / by tiles, us: one prompt of 16 tokens 3.5 / 6.6 at 8 heads of
+  // 64, 3.9 / 7.3 at 32 of 128; one of 32: 4.1 / 6.9 and 5.6 / 7.8; of 48: 5.6 / 8.1 and 11.6 / 9.3; of
+  // 128: 10.7 / 7.9 and 38 / 9.8; 128 of one token: 3.9 / 11.1 and 8.3 / 37.  What counts is the rows'
+  // work, by the sequences' mean length.
+  const long long work = (long long)total_q * a.n_heads * a.head_dim * total_k / (n_seqs > 0 ? n_seqs : 1);
+  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys && work <= kFewWork;
   if (maps && !few) {
     cudaError_t err = cudaSuccess;
     const bool d64 = a.head_dim == 64;

@@ -108,7 +108,8 @@ def test_prefill(case, how):
 
 @pytest.mark.parametrize("H,Hk,D,kind", [(8, 2, 64, "bf16"), (32, 8, 128, "fp16"), (3, 1, 128, "bf16")])
 @pytest.mark.parametrize("q_lens,k_lens", [([1], [1]), ([16], [16]), ([17], [17]), ([1, 0, 3], [33, 5, 40]), ([30, 9, 24], [30, 9, 24]),
-                                           ([0, 7, 0, 12], [4, 2, 0, 50]), ([64], [64]), ([65], [65]), ([1] * 40, [3] * 40)])
+                                           ([0, 7, 0, 12], [4, 2, 0, 50]), ([64], [64]), ([65], [65]), ([1] * 40, [3] * 40),
+                                           ([1, 0, 2] * 140, [1, 0, 2] * 140), ([1] * 256, [2] * 256), ([1] * 257, [2] * 257)])
 def test_prefill_a_handful_of_keys(H, Hk, D, kind, q_lens, k_lens):
     """Around the sizes at which the work goes by rows, not by tiles; what is not seen is NaN."""
     q = randn((sum(q_lens), H, D), 1, kind, 1.5)
