@@ -57,6 +57,13 @@ __global__ void __launch_bounds__(256, 2) attn_rows_kernel(const __grid_constant
   __shared__ __align__(16) float qs[8][D];
   grid_dependency_wait();
   grid_dependents_launch();
+  if (blockIdx.x == gridDim.x - 1) {   // the last block has no rows: it looks over the bounds
+    for (int i = threadIdx.x; i < n_seqs; i += 256) {
+      const int q0 = cu_q[i], q1 = cu_q[i + 1], k0 = cu_k[i], k1 = cu_k[i + 1];
+      if (q0 < 0 || q1 < q0 || q1 > total_q || k0 < 0 || k1 < k0 || k1 > total_k) set_status(status, QRE_DEV_BAD_INDEX);
+    }
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + warp;
   if (unit >= (long long)total_q * a.n_heads) return;
@@ -95,10 +102,7 @@ __global__ void __launch_bounds__(256, 2) attn_rows_kernel(const __grid_constant
     }
   }
   if (!found) return;
-  if (q0 < 0 || q1 > total_q || k0 < 0 || k1 < k0 || k1 > total_k) {
-    if (lane == 0) set_status(status, QRE_DEV_BAD_INDEX);
-    return;
-  }
+  if (q0 < 0 || q1 > total_q || k0 < 0 || k1 < k0 || k1 > total_k) return;
   int lo, hi;
   visible_range(k1 - k0 - (q1 - q0) + t - q0, k1 - k0, a.causal, a.window, lo, hi);
   __syncwarp();
@@ -1081,7 +1085,7 @@ cudaError_t launch_attn_prefill(const qre_attn& a, int n_seqs, int total_q, int 
   }
   const long long units = (long long)total_q * a.n_heads;
   auto go = [&](auto kernel) {
-    return launch_dependent(kernel, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, stream, a, n_seqs, total_q,
+    return launch_dependent(kernel, dim3((unsigned)((units + 7) / 8 + 1)), dim3(256), 0, stream, a, n_seqs, total_q,
                             total_k, cu_q, cu_k, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                             static_cast<const uint16_t*>(v), static_cast<uint16_t*>(o), lse, status);
   };

