@@ -1070,8 +1070,8 @@ cudaError_t launch_attn_prefill(const qre_attn& a, int n_seqs, int total_q, int 
   // 64, 3.9 / 7.3 at 32 of 128; one of 32: 4.1 / 6.9 and 5.6 / 7.8; of 48: 5.6 / 8.1 and 11.6 / 9.3; of
   // 128: 10.7 / 7.9 and 38 / 9.8; 128 of one token: 3.9 / 11.1 and 8.3 / 37.  What counts is the rows'
   // work, by the sequences' mean length.
-  const long long work = (long long)total_q * a.n_heads * a.head_dim * total_k / (n_seqs > 0 ? n_seqs : 1);
-  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys && work <= kFewWork;
+  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys &&
+                   (long long)total_q * a.n_heads * a.head_dim * total_k / (n_seqs > 0 ? n_seqs : 1) <= kFewWork;
   if (maps && !few) {
     cudaError_t err = cudaSuccess;
     const bool d64 = a.head_dim == 64;
