@@ -213,6 +213,16 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+// A count in shared memory that one thread writes and others read beside its barriers.
+__device__ __forceinline__ void store_release(int* p, int n) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(p)), "r"(n) : "memory");
+}
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int n;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(n) : "r"(smem_addr(p)) : "memory");
+  return n;
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -535,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < D / 64; ++x)
               tma_load_3d(skv + s * P::TILE + x * P::HALF, is_v ? &tv : &tk, 64 * x, is_v ? vh : kh,
                           w.k0 + (w.jb + (i - i0) / 2) * kN, &full[s]);
-            *issued = i + 1;
+            store_release(issued, i + 1);
           }
         }
         i0 = end;
@@ -961,10 +971,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = r.jb; j < r.je; ++j, ++cnt) {
         const bool masked = j * kN < lo_max || (j + 1) * kN > hi_min;
         // the values of a cut tile: before the scores are there if they have come, else before the
-        // weights are published
+        // weights are published.  A parity says whether they have come only once their load is issued
+        // (then the slot's tile of a lap before has come and gone): this query tile may be laps ahead of
+        // the ring, because it passes by pieces that have no keys for it.
         if (masked) {
           const int i = iv + 2 * j;
-          if (__all_sync(0xffffffffu, mbar_try_wait(&full[i % P::SLOTS], (i / P::SLOTS) & 1))) look_over(j);
+          if (__all_sync(0xffffffffu, load_acquire(issued) > i && mbar_try_wait(&full[i % P::SLOTS], (i / P::SLOTS) & 1)))
+            look_over(j);
           else unseen = j;
         }
         ok = wait_for(&s_full[t], cnt);

@@ -1,0 +1,99 @@
+"""Prefill and decode attention where calls mix what is usually apart, or lie at the end of a range; against fp64."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_routed_expert_03_gb300 as qre
+from oracle import attention as oatt
+from test_gpu_attention import DEV, check, clean_status, npy, randn, run_prefill  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def prefill_ref(q, k, v, q_lens, k_lens, scale, window=0):
+    """oracle.attention.prefill's four results (causal), a sequence and a KV head at a time in torch's fp64."""
+    T, H, D = q.shape
+    g = H // k.shape[1]
+    f64 = dict(dtype=torch.float64, device=DEV)
+    o, a = torch.zeros(q.shape, **f64), torch.zeros(q.shape, **f64)
+    lse, big = torch.full((T, H), -math.inf, **f64), torch.zeros((T, H), **f64)
+    x = y = 0
+    for nq, nk in zip(q_lens, k_lens):
+        lo, hi = (torch.tensor(b, device=DEV)[None, :, None] for b in oatt.visible(nq, nk, True, window))
+        j = torch.arange(nk, device=DEV)[None, None]
+        seen = (j >= lo) & (j < hi)                                             # [1, nq, nk]
+        used = seen.any(1)[0]
+        for hk in range(k.shape[1]):
+            heads = slice(hk * g, hk * g + g)
+            qq = q[x:x + nq, heads].double().transpose(0, 1)                      # [g, nq, D]
+            kk, vv = (torch.where(used[:, None], t[y:y + nk, hk].double(), 0.0) for t in (k, v))
+            s = torch.where(seen, qq @ kk.T * scale, -math.inf)
+            l = torch.logsumexp(s, -1)
+            p = torch.where(seen, torch.exp(s - torch.where(l.isinf(), 0.0, l)[..., None]), 0.0)
+            lse[x:x + nq, heads] = l.T
+            o[x:x + nq, heads], a[x:x + nq, heads] = (p @ vv).transpose(0, 1), (p @ vv.abs()).transpose(0, 1)
+            b = torch.where(seen, qq.abs() @ kk.abs().T * scale, 0.0)
+            big[x:x + nq, heads] = (b.amax(-1) if nk else torch.zeros((g, nq), **f64)).T
+        x, y = x + nq, y + nk
+    return tuple(t.cpu().numpy() for t in (o, lse, a, big))
+
+
+def hide_unseen(k, v, q_lens, k_lens, window):
+    """NaN in every key and value that no query sees."""
+    k, v = k.clone(), v.clone()
+    y = 0
+    for nq, nk in zip(q_lens, k_lens):
+        lo, hi = oatt.visible(nq, nk, True, window)
+        seen = np.zeros(nk + 1, int)
+        for a, b in zip(lo, hi):
+            seen[a] += 1
+            seen[b] -= 1
+        gone = torch.from_numpy(y + np.flatnonzero(np.cumsum(seen)[:nk] == 0)).to(DEV)
+        k[gone], v[gone] = float("nan"), float("nan")
+        y += nk
+    return k, v
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("H,Hk", [(8, 8), (32, 8), (32, 4)])           # 128, 32 and 16 tokens to a query tile
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_few_new_tokens_on_long_contexts_beside_short_prompts(D, H, Hk, many, window):
+    """Pieces of work without a second query tile and with many key tiles, in front of short prompts with two: the second
+    tile's softmax is pieces ahead of the keys and values that are being fetched.  More pieces than SMs, and at most and more than 128 sequences
+    (two orders of the work).  What is not seen is NaN."""
+    rng = np.random.default_rng(D + H + Hk + many)
+    tile = 128 // (H // Hk)
+    n_long, n_short = (80, 60) if many else (44, 30)
+    long = [(int(a), int(b)) for a, b in zip(rng.integers(1, tile + 1, n_long), rng.integers(300, 4001 if not many else 1200, n_long))]
+    if tile == 128:   # two query tiles and a cut first key tile: more queries than keys
+        short = [(int(a), int(b)) for a, b in zip(rng.integers(130, 250, n_short), rng.integers(20, 128, n_short))]
+    else:
+        short = [(int(a), int(a)) for a in rng.integers(tile + 1, 128, n_short)]
+    lens = [(long + short)[i] for i in rng.permutation(n_long + n_short)]
+    q_lens, k_lens = [a for a, _ in lens], [b for _, b in lens]
+    kind = "bf16" if D == 128 else "fp16"
+    q = randn((sum(q_lens), H, D), 1, kind, 1.5)
+    k, v = (randn((sum(k_lens), Hk, D), 2 + i, kind) for i in range(2))
+    ref = prefill_ref(q, k, v, q_lens, k_lens, D ** -0.5, window)
+    v_max = float(v.abs().max())
+    k, v = hide_unseen(k, v, q_lens, k_lens, window)
+    o, l = run_prefill(q, k, v, q_lens, k_lens, kind, window=window)
+    assert qre.qre_read_device_status() == 0
+    check(o, l, ref, kind, max(k_lens), v_max)
+    for _ in range(10):
+        o2, l2 = run_prefill(q, k, v, q_lens, k_lens, kind, window=window)
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+def test_the_fp64_reference_of_this_file():
+    q_lens, k_lens = [5, 9, 3, 0], [30, 4, 3, 7]
+    q, k, v = (randn((sum(n), h, 64), i, "bf16") for i, (n, h) in enumerate(((q_lens, 4), (k_lens, 2), (k_lens, 2))))
+    for window in (0, 3):
+        mine = prefill_ref(q, k, v, q_lens, k_lens, 0.125, window)
+        for a, b in zip(mine, oatt.prefill(npy(q), npy(k), npy(v), q_lens, k_lens, 0.125, True, window)):
+            assert np.array_equal(np.isneginf(a), np.isneginf(b))
+            assert np.allclose(np.where(np.isneginf(a), 0, a), np.where(np.isneginf(b), 0, b), rtol=1e-12, atol=1e-12)
