@@ -832,6 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             top = max_abs2<DT>(max_abs2<DT>(top, x[i].x), max_abs2<DT>(x[i].y, max_abs2<DT>(x[i].z, x[i].w)));
         }
         if ((top & expo) == expo || ((top >> 16) & expo) == expo) {
+          // The note first: the other query tile may see the element, multiply the zero, and look for the note.
+          *reinterpret_cast<volatile int*>(&works[nw % kWorks].poison) = 1;
+          __threadfence_block();
           for (int e = row; e < P::TILE / 16; e += kM) {
             uint4 x = tile[e];
             uint32_t u[4] = {x.x, x.y, x.z, x.w};
@@ -842,7 +845,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
           }
           touched = true;
-          *reinterpret_cast<volatile int*>(&works[nw % kWorks].poison) = 1;
         }
         if (touched) fence_proxy_async_smem();
         __syncwarp();

@@ -97,3 +97,26 @@ def test_the_fp64_reference_of_this_file():
         for a, b in zip(mine, oatt.prefill(npy(q), npy(k), npy(v), q_lens, k_lens, 0.125, True, window)):
             assert np.array_equal(np.isneginf(a), np.isneginf(b))
             assert np.allclose(np.where(np.isneginf(a), 0, a), np.where(np.isneginf(b), 0, b), rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_infinities_that_one_query_tile_sees_whole_and_the_other_cut(D):
+    """The value tile is one for both query tiles of a piece: what is taken out of it for the one that a window cuts has to
+    reach the result of the one that sees all of it, whichever of the two is ahead."""
+    n, seqs, H, Hk, window = 400, 60, 8, 2, 170             # 32 tokens to a query tile
+    lens = [n] * seqs
+    q, k, v = (randn((n * seqs, h, D), i, "bf16") for i, h in ((1, H), (2, Hk), (3, Hk)))
+    scale = 0.02                                             # no weight is so small that it is rounded to zero
+    want, _ = run_prefill(q, k, v, lens, lens, "bf16", window=window, scale=scale)
+    bad = v.clone()
+    at = torch.arange(seqs, device=DEV) * n + torch.arange(seqs, device=DEV) * 6 % n
+    bad[at, 1, 3] = float("inf")
+    token = torch.arange(n * seqs, device=DEV).view(seqs, n)
+    sees = ((token >= at[:, None]) & (token < at[:, None] + window)).view(-1)
+    for _ in range(10):
+        o, _ = run_prefill(q, k, bad, lens, lens, "bf16", window=window, scale=scale)
+        hit = o[:, 4:, 3]
+        assert torch.isposinf(hit[sees]).all() and torch.isfinite(hit[~sees]).all()
+        rest = torch.ones_like(o, dtype=torch.bool)
+        rest[:, 4:, 3] = ~sees[:, None]
+        assert torch.equal(o[rest], want[rest])
