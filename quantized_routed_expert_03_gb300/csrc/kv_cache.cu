@@ -195,9 +195,11 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const __grid_const
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int s = seqs[i], add = n_new[i];
     if (s < 0 || s >= c.max_seqs || add < 0) continue;
-    const long long len = c.seq_len[s] > 0 ? c.seq_len[s] : 0;
-    if (len + add > (long long)c.max_pages * c.page_size) continue;
-    if (first[i + 1] > first[i] && first[i + 1] > found) set_status(status, QRE_DEV_NO_PAGE);
+    const long long len = c.seq_len[s] > 0 ? c.seq_len[s] : 0, ps = c.page_size;
+    if (len + add > c.max_pages * ps) continue;
+    // (the request's own need: sums that saturate do not differ)
+    const bool needs = (len + add + ps - 1) / ps > (len + ps - 1) / ps;
+    if (needs && first[i + 1] > found) set_status(status, QRE_DEV_NO_PAGE);
     else c.seq_len[s] = (int)(len + add);
   }
 }
