@@ -41,30 +41,31 @@ KvWs kv_ws(const qre_kv_cache& c, void* ws) {
 }
 
 // Exclusive prefix sum of one value per thread over a CTA of kThreads; *total is
-// the sum.  `part` is shared memory for 33 ints; the call ends with a barrier.
-__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+// the sum.  `part` is shared memory for 33 values; the call ends with a barrier.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* part, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  T inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    const T u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
   if (lane == 31) part[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int w = part[lane];
-    const int own = w;
+    T w = part[lane];
+    const T own = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      const T u = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += u;
     }
     part[lane] = w - own;
     if (lane == 31) part[32] = w;
   }
   __syncthreads();
-  const int base = part[warp];
+  const T base = part[warp];
   *total = part[32];
   __syncthreads();
   return base + inc - v;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const __grid_const
                                                               const int32_t* __restrict__ n_new, KvWs ws,
                                                               int* status) {
   __shared__ int part[33];
+  __shared__ long long part64[33];
   __shared__ int first[kKvMaxRequests + 1];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const __grid_const
   long long sum = 0;
   for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + (int)threadIdx.x;
-    int need = 0;
+    long long need = 0;   // below 2^24, but 1024 of them are summed at a time
     if (i < n) {
       const int s = seqs[i], add = n_new[i];
       if (s < 0 || s >= c.max_seqs || add < 0) {
@@ -160,11 +162,11 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const __grid_const
         const long long len = c.seq_len[s] > 0 ? c.seq_len[s] : 0, ps = c.page_size;
         const long long have = (len + ps - 1) / ps, to = (len + add + ps - 1) / ps;
         if (to > c.max_pages) set_status(status, QRE_DEV_NO_PAGE);
-        else need = (int)(to - have);
+        else need = to - have;
       }
     }
-    int total;
-    const int before = block_scan(need, part, &total);
+    long long total;
+    const long long before = block_scan(need, part64, &total);
     // sums beyond the pool saturate: such requests are not served
     const long long at = sum + before;
     if (i < n) first[i] = (int)(at < c.n_pages + 1 ? at : c.n_pages + 1);

@@ -1,10 +1,11 @@
-"""The paged cache's bookkeeping where a call asks for more than the pool has."""
+"""The paged cache's bookkeeping where a call asks for more than the pool has, or sums pass 32 bits."""
 
 import numpy as np
 import pytest
+import torch
 
 import quantized_routed_expert_03_gb300 as qre
-from test_gpu_kv_cache import Cache, clean_status  # noqa: F401
+from test_gpu_kv_cache import DEV, Cache, clean_status, i32  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,20 @@ def test_random_life_of_a_cache_that_runs_out(n_pages, page, max_pages):
         c.check()
     assert passed >= 5                                       # calls whose wants pass the whole pool
     assert qre.qre_read_device_status() & ~qre.QRE_DEV_NO_PAGE == 0
+
+
+@pytest.mark.parametrize("small", [0, 3])
+def test_reserve_whose_needs_pass_32_bits(small):
+    """1024 requests of 2^21 pages each (2^31 in all), behind a few that fit a pool of 50."""
+    S, max_pages, page, n_pages = 1024 + small, 1 << 21, 16, 50
+    pool = torch.empty((1, n_pages, 1, page, 64), dtype=torch.bfloat16, device=DEV)
+    table = torch.full((S, max_pages), -1, dtype=torch.int32, device=DEV)
+    ln, ref = torch.zeros(S, dtype=torch.int32, device=DEV), torch.zeros(n_pages, dtype=torch.int32, device=DEV)
+    c = qre.make_kv_cache(pool, pool, table, ln, ref, qre.QRE_BF16)
+    ws = torch.full((qre.qre_kv_workspace_size(c),), 0xA5, dtype=torch.uint8, device=DEV)
+    qre.qre_kv_reserve(c, S, i32(range(S)), i32([page * 2] * small + [page * max_pages] * 1024), ws)
+    assert qre.qre_read_device_status() == qre.QRE_DEV_NO_PAGE
+    assert ln.tolist() == [page * 2] * small + [0] * 1024
+    assert ref.tolist() == [1] * (2 * small) + [0] * (n_pages - 2 * small)
+    assert table[:small, :2].flatten().tolist() == list(range(2 * small))
+    assert int((table >= 0).sum()) == 2 * small
