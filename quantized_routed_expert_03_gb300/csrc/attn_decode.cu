@@ -219,7 +219,7 @@ __device__ __forceinline__ float2 peer_float2(uint32_t addr, int rank) {
 template <int DT, int CT, int D, int NH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
-                       const int32_t* __restrict__ seqs, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
+                       const int32_t* __restrict__ seqs, int row0, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
                        float* __restrict__ lse, Header* __restrict__ header, float* __restrict__ parts, int stages,
                        int ways, int* status) {
   using K = Decode<DT, CT, D, NH>;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int t = t0 + kEach * tid + i;
-      row[i] = t < n ? (seqs ? seqs[t] : t) : -1;
+      row[i] = t < n ? (seqs ? seqs[t] : row0 + t) : -1;
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) len[i] = row[i] >= 0 && row[i] < c.max_seqs ? c.seq_len[row[i]] : -1;
@@ -874,9 +874,11 @@ size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache&, int n) {
   return header_bytes(n) + (size_t)2 * grid * kWarps * kRows * (a.head_dim + 2) * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
-                               int max_len, const void* q, void* o, float* lse, void* ws, int* status,
-                               cudaStream_t stream) {
+namespace {
+
+// One launch (and its join): n queries whose places sum up below 2^31; without ids, of the rows from row0 on.
+cudaError_t launch_part(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs, int row0,
+                        int max_len, const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream) {
   const int grid = decode_grid();
   const int g = a.n_heads / a.n_kv_heads;
   const size_t fixed = (size_t)(n + 1) * sizeof(Seq);
@@ -910,7 +912,7 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
     if (e != cudaSuccess) return e;
     const int ctas = ways / kWarps;
     e = launch_dependent_cluster(kernel, dim3(ctas ? (unsigned)all_units * ctas : grid), dim3(kThreads), ctas ? ctas : 1,
-                                 smem, stream, a, c, layer, n, seqs, static_cast<const uint16_t*>(q),
+                                 smem, stream, a, c, layer, n, seqs, row0, static_cast<const uint16_t*>(q),
                                  static_cast<uint16_t*>(o), lse, header, parts, stages, ways, status);
     if (e != cudaSuccess || ways) return e;
     const int threads = split || slots > 256 ? 256 : slots;
@@ -939,6 +941,27 @@ cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int lay
   }
   if (bf) return d64 ? pick(B{}, B{}, D64{}) : pick(B{}, B{}, D128{});
   return d64 ? pick(H{}, H{}, D64{}) : pick(H{}, H{}, D128{});
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
+                               int max_len, const void* q, void* o, float* lse, void* ws, int* status,
+                               cudaStream_t stream) {
+  // The kernel counts the places of a launch in 32 bits.  A sequence has at most as many as its table row (or the
+  // window) allows, 2^27 and a few, so a launch takes at least 15; a call is split only where rows hold millions
+  // of positions.
+  const long long chunk = kTile / (a.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)), held = (long long)c.max_pages * c.page_size;
+  const long long places = (a.window > 0 && a.window < held ? a.window : held) / chunk + 2 + kUnitCost;
+  const int most = 0x7fffffffll / places < n ? (int)(0x7fffffffll / places) : n;
+  for (int i = 0; i < n; i += most) {
+    const int m = n - i < most ? n - i : most;
+    const cudaError_t e =
+        launch_part(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
+                    static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, ws, status, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace qre

@@ -8,7 +8,8 @@ import torch
 
 import quantized_routed_expert_03_gb300 as qre
 from oracle import attention as oatt
-from test_gpu_attention import DEV, check, clean_status, npy, randn, run_prefill  # noqa: F401
+from test_gpu_attention import (DEV, Paged, check, clean_status, decode_ref, i32, npy, randn, run_decode,  # noqa: F401
+                                run_prefill)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +121,41 @@ def test_prefill_infinities_that_one_query_tile_sees_whole_and_the_other_cut(D):
         rest = torch.ones_like(o, dtype=torch.bool)
         rest[:, 4:, 3] = ~sees[:, None]
         assert torch.equal(o[rest], want[rest])
+
+
+# ---------------------------------------------------------------- decode
+
+@pytest.mark.parametrize("seqs", ["list", None])
+def test_decode_rows_of_a_billion_positions(seqs):
+    """Table rows so long that a call's chunks are counted apart for some of its sequences; the sequences are short."""
+    lens = [0, 1, 700, 33] + [int(x) for x in np.random.default_rng(1).integers(1, 300, 33)]
+    pg = Paged(lens, 2, 128, 256, "bf16", rows=len(lens) - 1)
+    if seqs is None:
+        pg.seqs = np.arange(len(lens))
+        pg.lens = [int(x) for x in pg.len.cpu()[:len(lens)]]
+    wide = torch.full((pg.table.shape[0], 1 << 22), -1, dtype=torch.int32, device=DEV)
+    wide[:, :pg.table.shape[1]] = pg.table
+    pg.c = qre.make_kv_cache(pg.k, pg.v, wide, pg.len, pg.ref, qre.QRE_BF16)
+    q = randn((len(lens), 8, 128), 3, "bf16")
+    for hint, window in ((0, 0), (700, 0), (0, 50)):
+        o, l = run_decode(pg, q, "bf16", max_len=hint, window=window, seqs=seqs, how="padded")
+        assert qre.qre_read_device_status() == 0
+        check(o, l, decode_ref(pg, q, window=window), "bf16", 700, float(pg.v.float().abs().max()))
+
+
+def test_decode_more_chunks_than_32_bits_count():
+    """33 sequences of 2^30 positions, every page of them the same one: 2^31 and more chunks of 16.  Keys are zero, so all
+    weights are 1, and values of -1, 0 and 1 add up exactly."""
+    n, cols, page, D = 33, 1 << 22, 256, 128
+    k = torch.zeros((1, 1, 1, page, D), dtype=torch.bfloat16, device=DEV)
+    v = (torch.arange(D, device=DEV) % 3 - 1).to(torch.bfloat16).expand(k.shape).contiguous()
+    table, ln, ref = torch.zeros((n, cols), dtype=torch.int32, device=DEV), i32([cols * page] * n), i32([1])
+    c = qre.make_kv_cache(k, v, table, ln, ref, qre.QRE_BF16)
+    q = randn((n, 2, D), 1, "bf16")
+    o, lse = torch.empty_like(q), torch.empty((n, 2), dtype=torch.float32, device=DEV)
+    a = qre.make_attn(2, 1, D, qre.QRE_BF16, 0.1, q=q, o=o)
+    ws = torch.empty(qre.qre_attn_decode_workspace_size(a, c, n), dtype=torch.uint8, device=DEV)
+    qre.qre_attn_decode(a, c, 0, n, None, 0, q, o, lse, ws)
+    assert qre.qre_read_device_status() == 0
+    assert torch.equal(o, v[0, 0, 0, :1].expand(o.shape))
+    assert (lse - 30 * math.log(2)).abs().max() < 2.0 ** -17
