@@ -135,8 +135,9 @@ struct Decode {
   static constexpr int NP = CK / 16;              // runs of 16 positions (each inside one page)
   static constexpr int KS = D / 16;
   static constexpr int PT = BF ? QRE_BF16 : QRE_FP16;
-  // largest sum of a chunk's weights against a standing reference (fp16 weights end at 65504)
-  static constexpr float kMost = BF ? 1.1529215e18f /* 2^60 */ : 32768.0f;
+  // Largest sum of a chunk's weights against a standing reference: fp16 weights end at 65504, and values enter
+  // the accumulators times weights of up to this, so that finite ones must not overflow there.
+  static constexpr float kMost = 32768.0f;
 
   // Byte offset of piece `col` of row `row` in a tile: pieces of a 128-byte line
   // are permuted by the row, so the eight rows that ldmatrix reads at one column

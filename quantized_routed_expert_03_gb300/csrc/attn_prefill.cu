@@ -185,9 +185,9 @@ constexpr int kSoftmaxRegs = 160, kStoreRegs = 112, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384;   // tensor-memory columns; P overwrites its S
 // A row's weights are taken against a reference that stays while their sum is at
-// most this: fp16 weights must not pass 65504, bf16 ones have fp32's range.
-template <int DT>
-constexpr float kMostWeight = DT == QRE_BF16 ? 1.1529215e18f /* 2^60 */ : 32768.0f;
+// most this: fp16 weights must not pass 65504; and values enter the accumulators
+// times weights of up to this, so that finite ones must not overflow there.
+constexpr float kMostWeight = 32768.0f;
 
 template <int D>
 struct Plan {
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fits = [&](const uint64_t (&sum)[2]) {
         const float2 u = unpair(add2(sum[0], sum[1]));
         const float total = u.x + u.y;
-        if (__any_sync(0xffffffffu, total > kMostWeight<DT>)) return false;
+        if (__any_sync(0xffffffffu, total > kMostWeight)) return false;
         l += total;
         return true;
       };

@@ -123,6 +123,30 @@ def test_prefill_infinities_that_one_query_tile_sees_whole_and_the_other_cut(D):
         assert torch.equal(o[rest], want[rest])
 
 
+def rising(n, heads, D, seed):
+    """Queries and keys whose scores (base 2, for scale = ln 2) are some 0 for 130 keys and then rise by 50."""
+    rise = torch.cat([torch.zeros(130, device=DEV), torch.linspace(20, 50, n - 130, device=DEV)])
+    k = torch.randn((n, heads, D), generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV) * 0.1
+    k[:, :, 0] = rise[:, None] / 8
+    return k.to(torch.bfloat16)
+
+
+def queries(n, heads, D, seed):
+    q = torch.randn((n, heads, D), generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV) * 0.1
+    q[:, :, 0] = 8.0
+    return q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_large_finite_values_under_scores_that_rise(D):
+    """Values of 2^100, and weights that would be 2^50 against the row's first keys: the product has to stay finite."""
+    n, scale = 600, math.log(2)
+    q, k = queries(n, 4, D, 1), rising(n, 2, D, 2)
+    v = (randn((n, 2, D), 3, "bf16").float() * 2.0 ** 100).to(torch.bfloat16)
+    o, l = run_prefill(q, k, v, [n], [n], "bf16", scale=scale)
+    check(o, l, prefill_ref(q, k, v, [n], [n], scale), "bf16", n, float(v.abs().max()))
+
+
 # ---------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("seqs", ["list", None])
@@ -159,3 +183,18 @@ def test_decode_more_chunks_than_32_bits_count():
     assert qre.qre_read_device_status() == 0
     assert torch.equal(o, v[0, 0, 0, :1].expand(o.shape))
     assert (lse - 30 * math.log(2)).abs().max() < 2.0 ** -17
+
+
+@pytest.mark.parametrize("hint", [0, 1, 900])                     # cut; one warp goes through a whole sequence; a cluster shares it
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_large_finite_values_under_scores_that_rise(D, hint):
+    pg = Paged([900, 500, 3000], 2, D, 16, "bf16")
+    pg.v.copy_((pg.v.float() * 2.0 ** 100).to(torch.bfloat16))
+    for i, n in enumerate(pg.lens):
+        k = rising(n, 2, D, i)
+        for p in range(-(-n // 16)):
+            rows = k[16 * p:16 * p + 16].transpose(0, 1)
+            pg.k[1, pg.tab[pg.seqs[i], p], :, :rows.shape[1]] = rows
+    q = queries(3, 8, D, 9)
+    o, l = run_decode(pg, q, "bf16", scale=math.log(2), max_len=hint)
+    check(o, l, decode_ref(pg, q, scale=math.log(2)), "bf16", 3000, float(pg.v.float().abs().max()))
