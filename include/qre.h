@@ -487,7 +487,7 @@ typedef struct {
  * j <= p, and with window > 0 (causal only) j > p - window.  A query that sees
  * nothing gives o = 0 and lse = -infinity; keys and values that a query does
  * not see do not reach its result, whatever they hold (NaN and infinities
- * included).  Values are summed up in fp32 times weights of up to 2^15 and
+ * included).  Values are summed up in fp32 times weights of up to 2^16 and
  * divided by the weights' sum at the end: the largest finite |v| times the
  * number of keys seen has to stay below 2^112.
  */

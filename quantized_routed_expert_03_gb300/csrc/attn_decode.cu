@@ -138,6 +138,10 @@ struct Decode {
   // Largest sum of a chunk's weights against a standing reference: fp16 weights end at 65504, and values enter
   // the accumulators times weights of up to this, so that finite ones must not overflow there.
   static constexpr float kMost = 32768.0f;
+  // The reference lies this far (base 2) below the maximum that sets it.  fp16 ends at 2^-24 below: with the
+  // maximum itself, keys whose weights are under 2^-25 of it would count in the sum and not in O, and in a long
+  // sequence they weigh something.  A lane's eight weights of 2^kUp stay under kMost with room for a maximum that grows.
+  static constexpr float kUp = BF ? 0.0f : 10.0f;
 
   // Byte offset of piece `col` of row `row` in a tile: pieces of a 128-byte line
   // are permuted by the row, so the eight rows that ldmatrix reads at one column
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
         for (int e = 0; e < 2; ++e) redo |= m[nh][e] == -INFINITY || sum[nh][e] > K::kMost;
-      if (__any_sync(0xffffffffu, redo)) {   // the reference moves to the maximum so far
+      if (__any_sync(0xffffffffu, redo)) {   // the reference moves with the maximum so far
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int i = 0; i < K::NP; ++i) mx = fmaxf(mx, fmaxf(s[i][nh][e], s[i][nh][e + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float to = fmaxf(m[nh][e], mx * s2[nh][e]);
+            const float to = fmaxf(m[nh][e], mx * s2[nh][e] - K::kUp);
             const float f = m[nh][e] == to ? 1.0f : ex2(m[nh][e] - to);   // 2^-inf = 0 for the first keys
             m[nh][e] = to;
             l[nh][e] *= f;

@@ -184,10 +184,19 @@ constexpr int kWorks = 3;          // pieces of work known at a time: being stor
 constexpr int kSoftmaxRegs = 160, kStoreRegs = 112, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384;   // tensor-memory columns; P overwrites its S
-// A row's weights are taken against a reference that stays while their sum is at
-// most this: fp16 weights must not pass 65504; and values enter the accumulators
-// times weights of up to this, so that finite ones must not overflow there.
-constexpr float kMostWeight = 32768.0f;
+// A row's weights are taken against a reference that stays while the sum of a part's weights is at most this:
+// fp16 weights end here; and values enter the accumulators times weights of up to this, so that finite ones must
+// not overflow there.
+constexpr float kMostWeight = 65504.0f;
+// The weight, in base 2, of the maximum that sets a row's reference.  fp16 ends at 2^-24 below: with 0, keys under
+// 2^-25 of the maximum count in the sum and not in O, and many of them weigh something (60,000 keys behind one that
+// is 26 ahead of them in base 2: all of their 2^-10).  With 6 prefill_chunk takes 41.4 us, not 37.2: rows that see
+// few keys in their first tile set a low reference, and their sums pass kMostWeight often.  bf16 has fp32's range.
+// kMove: how far ahead of the reference a maximum is when it is moved; a sum of 96 above kMostWeight has one that is.
+template <int DT>
+constexpr float kUp = DT == QRE_FP16 ? 4.0f : 0.0f;
+template <int DT>
+constexpr float kMove = DT == QRE_FP16 ? 5.0f : 8.0f;
 
 template <int D>
 struct Plan {
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* answered = o_free + 2;
   uint64_t* drain = answered + 1;           // [2], and one that is not used: 28 + 2 SLOTS of 8 bytes, so
   Work* works = reinterpret_cast<Work*>(drain + 3);          // [kWorks] begin at a multiple of 16
-  float2* sums = reinterpret_cast<float2*>(works + kWorks);       // [2][kM]: (l, m in base 2) of the rows
+  float2* sums = reinterpret_cast<float2*>(works + kWorks);       // [2][kM]: (l, its reference in base 2) of the rows
   uint32_t* tmem_p = reinterpret_cast<uint32_t*>(sums + 2 * kM);
   int* misc = reinterpret_cast<int*>(tmem_p + 1);
   volatile int* abort_flag = misc;          // a wait gave up
@@ -793,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(seen & (1u << i))) x[i] = 0xff800000u;
       };
       auto offset = [&]() {
-        const float off = m == -INFINITY ? 0.0f : -m * s2;
+        const float off = m == -INFINITY ? 0.0f : kUp<DT> - m * s2;
         return pair(off, off);
       };
       auto add_sum = [&](const uint64_t (&sum)[2]) {
@@ -879,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
         }
-        const bool move = mx > m && (m == -INFINITY || (mx - m) * s2 > 8.0f);
+        const bool move = mx > m && (m == -INFINITY || (mx - m) * s2 > kMove<DT>);
         if (__any_sync(0xffffffffu, move)) {
           const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mx) * s2);
           if (move) m = mx;
@@ -1009,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what the output needs: for the warps that write it, once they have read the last ones
       if (no > 0) ok = wait_for(&o_free[t], no - 1);
       if (!ok) break;
-      sums[t * kM + row] = make_float2(l, m * s2);
+      sums[t * kM + row] = make_float2(l, m * s2 - kUp<DT>);
       ++no;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sums_full[t]);

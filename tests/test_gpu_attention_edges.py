@@ -8,8 +8,8 @@ import torch
 
 import quantized_routed_expert_03_gb300 as qre
 from oracle import attention as oatt
-from test_gpu_attention import (DEV, Paged, check, clean_status, decode_ref, i32, npy, randn, run_decode,  # noqa: F401
-                                run_prefill)  # noqa: F401
+from test_gpu_attention import (DEV, DT, UNIT, Paged, check, clean_status, decode_ref, i32, npy, randn,  # noqa: F401
+                                run_decode, run_prefill)
 
 pytestmark = pytest.mark.gpu
 
@@ -147,6 +147,46 @@ def test_prefill_large_finite_values_under_scores_that_rise(D):
     check(o, l, prefill_ref(q, k, v, [n], [n], scale), "bf16", n, float(v.abs().max()))
 
 
+def one_far_ahead(n, heads, D, kind, seed):
+    """Keys and values: the key at 5 scores 26 (base 2, scale ln 2, queries of `ahead_queries`) and its value is zero, the
+    others score 0 to 1 and together still decide the result."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    k = torch.zeros((n, heads, D), device=DEV)
+    k[:, :, 0] = torch.randint(0, 5, (n, heads), generator=g, device=DEV) / 4
+    k[5, :, 0] = 26.0
+    v = torch.randn((n, heads, D), generator=g, device=DEV) * 4 + 64
+    v[5] = 0.0
+    return tuple(x.to(DT[kind][1]) for x in (k, v))
+
+
+def ahead_queries(n, heads, D, kind):
+    q = torch.zeros((n, heads, D), device=DEV)
+    q[:, :, 0] = 1.0
+    return q.to(DT[kind][1])
+
+
+def check_small_weights(o, lse, ref, kind, n_keys, v_max, lost):
+    """check(), but weights are rounded to fp16's steps (2^-24) `lost` powers of two lower than against the row's maximum."""
+    ro, rl, ra, rb = ref
+    D = ro.shape[-1]
+    tol = oatt.tolerance(ro, ra, rb, n_keys, D, UNIT[kind], 0.0) + n_keys * 2.0 ** (-25 - lost) * v_max
+    assert (np.abs(npy(o) - ro) <= tol).all(), (np.abs(npy(o) - ro) - tol).max()
+    assert (np.abs(npy(lse) - rl) <= oatt.lse_tolerance(rl, rb, n_keys, D)).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_fp16_many_small_weights_behind_one_key(D):
+    """Each weight is below fp16's smallest against the row's maximum; 60,000 of them weigh 2^-10."""
+    q_lens, k_lens, scale = [3, 40], [60000, 20000], math.log(2)
+    k, v = (torch.cat(x) for x in zip(*(one_far_ahead(n, 1, D, "fp16", n) for n in k_lens)))
+    q = ahead_queries(43, 2, D, "fp16")
+    ref = prefill_ref(q, k, v, q_lens, k_lens, scale)
+    o, l = run_prefill(q, k, v, q_lens, k_lens, "fp16", scale=scale)
+    check_small_weights(o, l, ref, "fp16", 60000, float(v.abs().max()), 4)
+    # the oracle's bound tells them apart: the keys behind the first weigh far more than it allows
+    assert (np.abs(ref[0][:3]) > 4 * 60000 * 2.0 ** -29 * float(v.abs().max())).all()
+
+
 # ---------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("seqs", ["list", None])
@@ -198,3 +238,27 @@ def test_decode_large_finite_values_under_scores_that_rise(D, hint):
     q = queries(3, 8, D, 9)
     o, l = run_decode(pg, q, "bf16", scale=math.log(2), max_len=hint)
     check(o, l, decode_ref(pg, q, scale=math.log(2)), "bf16", 3000, float(pg.v.float().abs().max()))
+
+
+@pytest.mark.parametrize("hint", [0, 1])                                # cut; one warp goes through a whole sequence
+@pytest.mark.parametrize("kind,cache,D", [("fp16", "fp16", 64), ("fp16", "fp16", 128), ("bf16", "e4m3", 64), ("fp16", "e4m3", 128)])
+def test_decode_fp16_products_many_small_weights_behind_one_key(kind, cache, D, hint):
+    n, scale = 60000, math.log(2)
+    pg = Paged([n, 300], 1, D, 64, cache)
+    if cache == "e4m3":
+        pg.scales.fill_(1.0)
+        for s in pg.sc:
+            s.fill_(1.0)
+    k, v = one_far_ahead(n, 1, D, cache, 1)
+    for pool, x in ((pg.k, k), (pg.v, v)):
+        raw = (lambda t: t.view(torch.uint8)) if cache == "e4m3" else (lambda t: t)
+        pages = torch.from_numpy(pg.tab[pg.seqs[0], :-(-n // 64)]).long().to(DEV)
+        pad = torch.zeros((pages.numel() * 64, D), device=DEV).to(x.dtype)
+        raw(pad)[:n] = raw(x)[:, 0]
+        raw(pool)[1, pages, 0] = raw(pad).view(-1, 64, D)
+    q = ahead_queries(2, 4, D, kind)
+    ref = decode_ref(pg, q, scale=scale)
+    o, l = run_decode(pg, q, kind, scale=scale, max_len=hint)
+    v_max = float(v.float().abs().max())
+    check_small_weights(o[:1], l[:1], [r[:1] for r in ref], kind, n, v_max, 10)
+    assert (np.abs(ref[0][0]) > 100 * n * 2.0 ** -35 * v_max).all()
