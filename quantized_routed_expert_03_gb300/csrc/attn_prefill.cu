@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256, 2) attn_rows_kernel(const __grid_constant
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
     const float m2 = fmaxf(m, mx), f = m == -INFINITY ? 0.0f : exp2f(m - m2);
-    const float p = j < hi ? exp2f(x - m2) : 0.0f;
+    const float p = j < hi ? exp2f(x - (m2 == -INFINITY ? 0.0f : m2)) : 0.0f;   // (keys that score -infinity count 0)
     float sum = p;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);

@@ -123,6 +123,17 @@ def test_prefill_infinities_that_one_query_tile_sees_whole_and_the_other_cut(D):
         assert torch.equal(o[rest], want[rest])
 
 
+@pytest.mark.parametrize("n,gone", [(48, 40), (700, 300)])              # by rows, by tiles
+def test_prefill_keys_that_score_minus_infinity_first(n, gone):
+    """A row's first keys, more than one step of the kernel, score -infinity: they count nothing."""
+    q, k, v = (randn((n, h, 64), i, "bf16") for i, h in ((1, 2), (2, 1), (3, 1)))
+    q[:, :, 0] = q[:, :, 0].abs() + 0.1
+    ref = [r.copy() for r in prefill_ref(q[gone:], k[gone:], v[gone:], [n - gone], [n - gone], 0.125)]
+    k[:gone, :, 0] = -float("inf")
+    o, l = run_prefill(q, k, v, [n], [n], "bf16", scale=0.125)
+    check(o[gone:], l[gone:], ref, "bf16", n, float(v.abs().max()))
+
+
 def rising(n, heads, D, seed):
     """Queries and keys whose scores (base 2, for scale = ln 2) are some 0 for 130 keys and then rise by 50."""
     rise = torch.cat([torch.zeros(130, device=DEV), torch.linspace(20, 50, n - 130, device=DEV)])
