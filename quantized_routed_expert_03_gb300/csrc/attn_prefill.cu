@@ -39,7 +39,8 @@
 namespace qre {
 namespace {
 
-constexpr int kFewKeys = 512, kFewWork = 1 << 22;   // see launch_attn_prefill
+// See launch_attn_prefill.
+constexpr int kFewKeys = 512, kFewLong = 256, kFewWork = 1 << 22, kFewTotal = 1 << 26;
 
 // For a handful of keys, for what TMA cannot address (rows that repeat: a token
 // stride of 0) and for calls without any key: one warp per (query token, head); a
@@ -1093,9 +1094,13 @@ cudaError_t launch_attn_prefill(const qre_attn& a, int n_seqs, int total_q, int 
   // one sequence's rows only.  By rows / by tiles, us: one prompt of 16 tokens 3.5 / 6.6 at 8 heads of
   // 64, 3.9 / 7.3 at 32 of 128; one of 32: 4.1 / 6.9 and 5.6 / 7.8; of 48: 5.6 / 8.1 and 11.6 / 9.3; of
   // 128: 10.7 / 7.9 and 38 / 9.8; 128 of one token: 3.9 / 11.1 and 8.3 / 37.  What counts is the rows'
-  // work, by the sequences' mean length.
-  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys &&
-                   (long long)total_q * a.n_heads * a.head_dim * total_k / (n_seqs > 0 ? n_seqs : 1) <= kFewWork;
+  // work, by the sequences' mean length.  The host does not know the longest, so two bounds keep an uneven
+  // call from rows: on the longest if none is empty (60 of one token and one of 300: 39 / 10.8 at 8 heads of
+  // 64), and on the work if it were all one sequence's (512 tokens and 399 empty sequences: 375 / 81 at 32 of
+  // 128).  What they cost is less: 128 of four tokens 7.3 / 11.1, 256 of one 13.5 / 68.
+  const long long work = (long long)total_q * a.n_heads * a.head_dim * total_k;
+  const bool few = total_k <= kFewKeys && n_seqs <= kFewKeys && total_k - n_seqs < kFewLong &&
+                   work / (n_seqs > 0 ? n_seqs : 1) <= kFewWork && work <= kFewTotal;
   if (maps && !few) {
     cudaError_t err = cudaSuccess;
     const bool d64 = a.head_dim == 64;

@@ -134,6 +134,23 @@ def test_prefill_keys_that_score_minus_infinity_first(n, gone):
     check(o[gone:], l[gone:], ref, "bf16", n, float(v.abs().max()))
 
 
+@pytest.mark.parametrize("lens,H,Hk,D,rows", [
+    ([16], 8, 2, 64, True), ([8, 5, 30], 32, 8, 128, True), ([2] * 64, 32, 8, 128, True), ([2] * 128, 8, 2, 64, True),
+    ([5] * 40, 8, 2, 64, True), ([128], 32, 8, 128, False), ([1] * 99 + [400], 8, 2, 64, False),
+    ([1] * 60 + [300], 8, 2, 64, False), ([512] + [0] * 399, 32, 8, 128, False), ([0] * 255 + [300], 32, 8, 128, False)])
+def test_prefill_which_way_a_handful_of_keys_goes(lens, H, Hk, D, rows):
+    """By rows only where no sequence of an uneven or padded call can be long.  Rows keep their weights in fp32, tiles round
+    them to bf16: of two keys with weights 1 and 0.999 and values 1 and -1 the one leaves 0.0005, the other nothing."""
+    n = sum(lens)
+    q, k, v = (torch.zeros((n, h, D), dtype=torch.bfloat16, device=DEV) for h in (H, Hk, Hk))
+    q[:, :, 0], v[:] = 1.0, 1.0
+    first = int(np.cumsum([0] + lens)[int(np.argmax(lens))])
+    k[first + 1, :, 0], v[first + 1] = -0.001, -1.0
+    o, l = run_prefill(q, k, v, lens, lens, "bf16", scale=1.0)
+    check(o, l, prefill_ref(q, k, v, lens, lens, 1.0), "bf16", max(lens), 1.0)
+    assert bool((o[first + 1] != 0).all()) == rows and bool((o[first + 1] == 0).all()) == (not rows)
+
+
 def rising(n, heads, D, seed):
     """Queries and keys whose scores (base 2, for scale = ln 2) are some 0 for 130 keys and then rise by 50."""
     rise = torch.cat([torch.zeros(130, device=DEV), torch.linspace(20, 50, n - 130, device=DEV)])
