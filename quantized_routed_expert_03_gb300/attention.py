@@ -9,7 +9,10 @@ computation is a call into libqre.so through the binding in ``__init__``.
   packed prompts (keys and values as they come from the projections), ``decode``
   of one new token per sequence over the pages.
 
-Both keep a workspace: calls on one object belong on one stream at a time.
+Both keep a workspace: calls on one object belong on one stream at a time.  A
+result allocated here belongs to the stream that the call was given, like any
+tensor made there: a program that uses it on another stream waits for the call
+and, before it lets go of the tensor, tells the allocator (``record_stream``).
 """
 
 from __future__ import annotations
@@ -21,6 +24,18 @@ from . import (QRE_BF16, QRE_E4M3, QRE_FP16, make_attn, make_kv_cache, make_kv_r
                qre_kv_reserve, qre_kv_workspace_size, qre_kv_write)
 
 DTYPES = {torch.bfloat16: QRE_BF16, torch.float16: QRE_FP16, torch.float8_e4m3fn: QRE_E4M3}
+
+
+def _empty_like(q, stream):
+    """An output for a call on ``stream``: memory of that stream's pool, so that nothing that another stream still does
+    with a block it was given before can meet the call."""
+    if stream is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if not isinstance(stream, torch.cuda.Stream):        # a raw handle, 0: the default stream
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle, device=q.device) if handle else torch.cuda.default_stream(q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
 
 
 class KVCache:
@@ -83,14 +98,14 @@ class Attention:
 
     def prefill(self, q, k, v, cu_q, cu_k, o=None, lse=None, stream=None):
         """q [tokens, n_heads, head_dim], k, v [keys, n_kv_heads, head_dim], cu_q, cu_k [sequences + 1]."""
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        o = _empty_like(q, stream) if o is None else o
         qre_attn_prefill(self._desc(q, k, v, o), cu_q.numel() - 1, q.shape[0], k.shape[0], cu_q, cu_k, q, k, v, o,
                          lse, stream)
         return o
 
     def decode(self, q, seqs, o=None, lse=None, max_len=0, stream=None):
         """q [sequences, n_heads, head_dim]: the newest token of each sequence, its row reserved and written before."""
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        o = _empty_like(q, stream) if o is None else o
         qre_attn_decode(self._desc(q, o=o), self.cache.desc, self.layer, q.shape[0], seqs, max_len, q, o, lse,
                         self.workspace, stream=stream)
         return o

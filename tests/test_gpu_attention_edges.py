@@ -8,6 +8,7 @@ import torch
 
 import quantized_routed_expert_03_gb300 as qre
 from oracle import attention as oatt
+from quantized_routed_expert_03_gb300.attention import Attention, KVCache
 from test_gpu_attention import (DEV, DT, UNIT, Paged, check, clean_status, decode_ref, i32, npy, randn,  # noqa: F401
                                 run_decode, run_prefill)
 
@@ -290,3 +291,34 @@ def test_decode_fp16_products_many_small_weights_behind_one_key(kind, cache, D, 
     v_max = float(v.float().abs().max())
     check_small_weights(o[:1], l[:1], [r[:1] for r in ref], kind, n, v_max, 10)
     assert (np.abs(ref[0][0]) > 100 * n * 2.0 ** -35 * v_max).all()
+
+
+# ---------------------------------------------------------------- the Python classes
+
+@pytest.mark.parametrize("on", ["stream", "handle", "default", "0"])
+@pytest.mark.parametrize("what", ["prefill", "decode"])
+def test_an_output_made_for_another_stream(what, on):
+    """The current stream has work before it on memory that was given back to the allocator; the call on the other stream
+    must not be given that memory."""
+    n, H, Hk, D = 300, 8, 2, 128
+    cache = KVCache(1, 40, Hk, 16, D, 4, 40)
+    att = Attention(cache, 0, H, 4)
+    q, k, v = (randn((n, h, D), i, "bf16") for i, h in ((1, H), (2, Hk), (3, Hk)))
+    cu, seqs = i32([0, n]), i32([0])
+    cache.reserve(seqs, i32([n]))
+    cache.write(0, i32([0] * n), torch.arange(n, dtype=torch.int32, device=DEV), k, v)
+    x = q if what == "prefill" else q[-1:].clone()
+    call = (lambda **kw: att.prefill(x, k, v, cu, cu, **kw)) if what == "prefill" else (lambda **kw: att.decode(x, seqs, **kw))
+    want = call()
+    side = torch.cuda.Stream()
+    here, there = (side, torch.cuda.default_stream()) if on in ("default", "0") else (torch.cuda.current_stream(), side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        for _ in range(3):
+            old = torch.empty_like(x)
+            torch.cuda._sleep(20_000_000)    # some 10 ms
+            old.fill_(float("nan"))          # pending on this stream
+            del old
+            o = call(stream=there if on in ("stream", "default") else there.cuda_stream)
+            torch.cuda.synchronize()
+            assert torch.equal(o, want)
