@@ -487,9 +487,12 @@ typedef struct {
  * j <= p, and with window > 0 (causal only) j > p - window.  A query that sees
  * nothing gives o = 0 and lse = -infinity; keys and values that a query does
  * not see do not reach its result, whatever they hold (NaN and infinities
- * included).  Values are summed up in fp32 times weights of up to 2^16 and
- * divided by the weights' sum at the end: the largest finite |v| times the
- * number of keys seen has to stay below 2^112.
+ * included).  Scores, the sum of the weights and the results are kept in fp32;
+ * for the product with V the weights are rounded to 16 bits: to the type of q,
+ * to fp16 for a QRE_E4M3 cache (a prefill call of a handful of keys keeps
+ * fp32).  Values are summed up in fp32 times weights of up to 2^16 and divided
+ * by the weights' sum at the end: the largest finite |v| times the number of
+ * keys seen has to stay below 2^112.
  */
 typedef struct {
   int32_t n_heads, n_kv_heads, head_dim, dtype;
@@ -520,7 +523,8 @@ QRE_API qre_status qre_kv_reserve(const qre_kv_cache* cache, int32_t n, const in
  * Writes n_tokens new rows of one layer: row t goes to position token_pos[t] of
  * sequence token_seq[t], as it is (cache and rows of one type) or, into a
  * QRE_E4M3 cache, as E4M3(row * (1 / scale)), reciprocal and product rounded to
- * fp32, then to nearest even, clamped to +-448.
+ * fp32, then to nearest even, clamped to +-448. (Next to a tie this can be one
+ * E4M3 step from E4M3(row / scale): 2 of 10 million elements.)
  * A token with token_pos < 0 is skipped (padding); one without a page there, or
  * with a bad id, is skipped with QRE_DEV_BAD_INDEX.
  *   token_seq, token_pos  [n_tokens] int32, device

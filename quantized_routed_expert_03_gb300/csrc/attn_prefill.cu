@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish(part);
       };
       // The weights are taken against the reference of before, with no maximum looked for (the row's
-      // first keys set it).  Rounding does not depend on the reference, so it may stay far behind; only
+      // first keys set it).  Rounding does not depend on the reference, so it may stay behind; only
       // when the weights' sum is too large for their type the keys go by the book.  False: they have to.
       auto fits = [&](const uint64_t (&sum)[2]) {
         const float2 u = unpair(add2(sum[0], sum[1]));
