@@ -10,10 +10,13 @@ Shows the paged cache, prefill and decode attention and the MoE layer as a serve
   * all but the best sample of each prompt are freed, the pages are compacted, and the rest
     goes on.
 
-Weights are random (there is no tokenizer either: tokens are numbers).  Norms, projections and
-the residual stream are plain PyTorch.
+With --rotary the heads of queries and keys are normed and turned by their positions on the way
+into the pages; with --shared the samples of a prompt read the pages that they share together.
 
-    python examples/generate.py [--cache e4m3] [--steps 24]
+Weights are random (there is no tokenizer either: tokens are numbers).  The norms of the residual
+stream, the projections and the residual stream itself are plain PyTorch.
+
+    python examples/generate.py [--cache e4m3 | e2m1] [--rotary] [--shared] [--steps 24]
 """
 
 from __future__ import annotations
@@ -28,14 +31,14 @@ import torch.nn.functional as F
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import quantized_routed_expert_03_gb300 as qre                                    # noqa: E402
-from quantized_routed_expert_03_gb300.attention import Attention, KVCache         # noqa: E402
+from quantized_routed_expert_03_gb300.attention import Attention, KVCache, Rotary # noqa: E402
 from quantized_routed_expert_03_gb300.layer import ExpertArena, MoELayer          # noqa: E402
 
 
 class Decoder:
     def __init__(self, hidden=256, inter=128, experts=16, top_k=4, group=32, heads=4, kv_heads=2, head_dim=64,
                  layers=2, vocab=500, page=16, n_pages=200, max_seqs=16, max_pages=32, t_max=512,
-                 cache_dtype=torch.bfloat16, seed=0, device="cuda:0"):
+                 cache_dtype=torch.bfloat16, seed=0, device="cuda:0", rotary=False, shared=False):
         dev = torch.device(device)
         g = torch.Generator(device=dev).manual_seed(seed)
 
@@ -46,6 +49,11 @@ class Decoder:
         scales = None
         if cache_dtype == torch.float8_e4m3fn:   # E4M3 holds values up to 448; keys here are a few units large
             scales = torch.full((layers, kv_heads), 1 / 32, device=dev)
+        self.shared = shared
+        self.rotary = None
+        if rotary:
+            self.rotary = Rotary(heads, kv_heads, head_dim, q_norm=torch.ones(head_dim, device=dev),
+                                 k_norm=torch.ones(head_dim, device=dev), device=dev)
         self.cache = KVCache(layers, n_pages, kv_heads, page, head_dim, max_seqs, max_pages, cache_dtype, scales,
                              scales, dev)
         self.embed = rand(vocab, hidden).bfloat16()
@@ -62,17 +70,24 @@ class Decoder:
                 w_qkv=rand(hidden, (heads + 2 * kv_heads) * head_dim, scale=hidden ** -0.5).bfloat16(),
                 w_o=rand(heads * head_dim, hidden, scale=(heads * head_dim) ** -0.5).bfloat16(),
                 w_router=rand(experts, hidden, scale=hidden ** -0.5), arena=arena, moe=moe,
-                attention=Attention(self.cache, l, heads, max_seqs)))
+                attention=Attention(self.cache, l, heads, max_seqs, max_groups=max_seqs if shared else 0)))
         self.trace = None    # a list: gets (layer, q, k, v, o) of every attention
 
+    def _write(self, layer, token_seq, token_pos, q, k, v):
+        """Keys and values into the pages; the queries and keys that attention takes."""
+        if self.rotary is not None:
+            return self.cache.write_rope(layer, self.rotary, token_seq, token_pos, q, k, v)
+        self.cache.write(layer, token_seq, token_pos, k, v)
+        return q, k
+
     def _forward(self, tokens, attend):
-        """attend(layer's Attention, q, k, v) -> o writes the cache and attends."""
+        """attend(layer's Attention, q, k, v) -> q, k, o writes the cache and attends."""
         x = self.embed[tokens]
         T, split = x.shape[0], (self.heads, self.kv_heads, self.kv_heads)
         for l, p in enumerate(self.layers):
             qkv = F.rms_norm(x, x.shape[1:]) @ p["w_qkv"]
             q, k, v = qkv.view(T, -1, self.head_dim).split(split, 1)     # strided views: nothing is copied
-            o = attend(p["attention"], q, k, v)
+            q, k, o = attend(p["attention"], q, k, v)
             if self.trace is not None:
                 self.trace.append((l, q.clone(), k.clone(), v.clone(), o.clone()))
             x = x + o.view(T, -1) @ p["w_o"]
@@ -94,19 +109,21 @@ class Decoder:
         self.cache.reserve(seqs, lens)
 
         def attend(att, q, k, v):
-            self.cache.write(att.layer, token_seq, token_pos, k, v)
-            return att.prefill(q, k, v, cu, cu)
+            q, k = self._write(att.layer, token_seq, token_pos, q, k, v)
+            return q, k, att.prefill(q, k, v, cu, cu)
 
         return self._logits(self._forward(tokens, attend)[cu[1:] - 1])
 
-    def step(self, tokens, seqs, ones):
-        """One new token for each of ``seqs`` (ones: as many int32 ones); the logits after it."""
+    def step(self, tokens, seqs, ones, cu_group=None):
+        """One new token for each of ``seqs`` (ones: as many int32 ones); the logits after it.  cu_group: groups of
+        neighbours in ``seqs`` that share pages."""
         pos = self.cache.seq_len[seqs]
         self.cache.reserve(seqs, ones)
+        common = None if cu_group is None else self.cache.common_len(seqs, cu_group)
 
         def attend(att, q, k, v):
-            self.cache.write(att.layer, seqs, pos, k, v)
-            return att.decode(q, seqs)
+            q, k = self._write(att.layer, seqs, pos, q, k, v)
+            return q, k, att.decode(q, seqs) if common is None else att.decode_shared(q, seqs, cu_group, common)
 
         return self._logits(self._forward(tokens, attend))
 
@@ -114,14 +131,14 @@ class Decoder:
 class Sampler:
     """Greedy continuation of a set of sequences: tokens so far and their log-probability."""
 
-    def __init__(self, model, seqs, tokens, score, graph=True):
-        self.model, self.seqs, self.use_graph = model, seqs, graph
+    def __init__(self, model, seqs, tokens, score, graph=True, cu_group=None):
+        self.model, self.seqs, self.use_graph, self.cu_group = model, seqs, graph, cu_group
         self.tokens, self.score = tokens.to(torch.int32).clone(), score.clone()
         self.ones = torch.ones_like(seqs)
         self.graph = None
 
     def _step(self):
-        logp = F.log_softmax(self.model.step(self.tokens, self.seqs, self.ones), -1)
+        logp = F.log_softmax(self.model.step(self.tokens, self.seqs, self.ones, self.cu_group), -1)
         best = logp.max(-1)
         self.score += best.values
         self.tokens.copy_(best.indices)
@@ -151,18 +168,25 @@ def generate(model, prompts, samples=3, steps=24, graph=True):
     first = logp.topk(samples, -1)
     for s in range(1, samples):
         cache.fork(seqs[:n], seqs[s * n:(s + 1) * n].clone())    # arrays begin at 16-byte boundaries
-    run = Sampler(model, seqs, first.indices.t().reshape(-1), first.values.t().reshape(-1), graph)
-    begin = run.tokens.clone()
-    part1 = run.run(steps)
+    # the order of the batch: with shared pages read together, a prompt's samples side by side
+    order, cu_group = torch.arange(n * samples, device=dev), None
+    if model.shared:
+        order = order.view(samples, n).t().reshape(-1)
+        cu_group = torch.arange(0, n * samples + 1, samples, dtype=torch.int32, device=dev)
+    back = torch.argsort(order)
+    run = Sampler(model, seqs[order], first.indices.t().reshape(-1)[order], first.values.t().reshape(-1)[order], graph,
+                  cu_group)
+    begin = run.tokens[back].clone()
+    part1 = run.run(steps)[:, back]
     live1 = cache.compact().clone()
 
-    best = run.score.view(samples, n).argmax(0)
+    best = run.score[back].view(samples, n).argmax(0)
     keep = (best * n + torch.arange(n, device=dev)).to(torch.int32)
     drop = torch.ones(n * samples, dtype=torch.bool, device=dev)
     drop[keep.long()] = False
     cache.free(seqs[drop])
     live2 = cache.compact().clone()
-    rest = Sampler(model, keep, run.tokens[keep.long()], run.score[keep.long()], graph)
+    rest = Sampler(model, keep, run.tokens[back][keep.long()], run.score[back][keep.long()], graph)
     part2 = rest.run(steps)
     tokens = torch.cat([begin[None], part1])[:, keep.long()]
     return torch.cat([tokens, part2]).t().cpu(), int(live1), int(live2)
@@ -170,10 +194,13 @@ def generate(model, prompts, samples=3, steps=24, graph=True):
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
-    ap.add_argument("--cache", choices=["bf16", "e4m3"], default="bf16")
+    ap.add_argument("--cache", choices=["bf16", "e4m3", "e2m1"], default="bf16")
+    ap.add_argument("--rotary", action="store_true")
+    ap.add_argument("--shared", action="store_true")
     ap.add_argument("--steps", type=int, default=24)
     args = ap.parse_args()
-    model = Decoder(cache_dtype=torch.float8_e4m3fn if args.cache == "e4m3" else torch.bfloat16)
+    kinds = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "e2m1": torch.float4_e2m1fn_x2}
+    model = Decoder(cache_dtype=kinds[args.cache], rotary=args.rotary, shared=args.shared)
     prompts = [[(7 * i + 3 * j) % 500 for j in range(n)] for i, n in enumerate((5, 33, 70, 16))]
     tokens, live1, live2 = generate(model, prompts, steps=args.steps)
     status = qre.qre_read_device_status()

@@ -447,7 +447,7 @@ QRE_API qre_status qre_debug_wait_test(uint64_t wait_limit_ns, uint64_t stall_ns
  * 4096 sequences, requests or forks per call; n_pages and total tokens below
  * 2^24; strides are in elements, non-negative multiples of 8.
  */
-typedef enum { QRE_BF16 = 0, QRE_FP16 = 1, QRE_E4M3 = 2 } qre_dtype;
+typedef enum { QRE_BF16 = 0, QRE_FP16 = 1, QRE_E4M3 = 2, QRE_E2M1 = 4 } qre_dtype;
 
 /*
  * A paged key-value cache.  Position p of sequence s is row p % page_size of
@@ -456,15 +456,23 @@ typedef enum { QRE_BF16 = 0, QRE_FP16 = 1, QRE_E4M3 = 2 } qre_dtype;
  * free page.  A QRE_E4M3 cache stores E4M3 bytes, worth byte * scale of the
  * layer and KV head.  seq_len[s] counts the reserved positions, so sequence s
  * holds ceil(seq_len[s] / page_size) pages; table entries beyond are -1.
+ *
+ * A QRE_E2M1 cache stores 4-bit codes, and a scale for every 16 elements of a
+ * row.  One page of one head is page_size * head_dim * 9 / 16 bytes: the rows'
+ * codes, [page_size][head_dim / 2] bytes with element 2 i in the low half of
+ * byte i, then the rows' scales, [page_size][head_dim / 16] E4M3 bytes.  A code
+ * is a sign (bit 3) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6; an element is worth
+ * code * scale of its 16 * scale of the layer and KV head.
  */
 typedef struct {
-  void* k;              /* [n_layers][n_pages][n_kv_heads][page_size][head_dim], device */
+  void* k;              /* [n_layers][n_pages][n_kv_heads][page_size][head_dim], device
+                           (QRE_E2M1: bytes as above in place of the last two)          */
   void* v;              /* the same shape, device                                       */
   int32_t* page_table;  /* [max_seqs][max_pages], device                                */
   int32_t* seq_len;     /* [max_seqs], device                                           */
   int32_t* ref_count;   /* [n_pages], device                                            */
-  const float* k_scale; /* [n_layers][n_kv_heads], device; QRE_E4M3 only, NULL = 1;
-                           read one by one: 4-byte alignment is enough                  */
+  const float* k_scale; /* [n_layers][n_kv_heads], device; QRE_E4M3 and QRE_E2M1 only,
+                           NULL = 1; read one by one: 4-byte alignment is enough        */
   const float* v_scale; /* the same                                                     */
   int32_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
   int32_t max_seqs, max_pages;
@@ -489,8 +497,8 @@ typedef struct {
  * not see do not reach its result, whatever they hold (NaN and infinities
  * included).  Scores, the sum of the weights and the results are kept in fp32;
  * for the product with V the weights are rounded to 16 bits: to the type of q,
- * to fp16 for a QRE_E4M3 cache (a prefill call of a handful of keys keeps
- * fp32).  Values are summed up in fp32 times weights of up to 2^16 and divided
+ * to fp16 for a QRE_E4M3 or QRE_E2M1 cache (a prefill call of a handful of keys
+ * keeps fp32).  Values are summed up in fp32 times weights of up to 2^16 and divided
  * by the weights' sum at the end: the largest finite |v| times the number of
  * keys seen has to stay below 2^112.
  */
@@ -524,7 +532,11 @@ QRE_API qre_status qre_kv_reserve(const qre_kv_cache* cache, int32_t n, const in
  * sequence token_seq[t], as it is (cache and rows of one type) or, into a
  * QRE_E4M3 cache, as E4M3(row * (1 / scale)), reciprocal and product rounded to
  * fp32, then to nearest even, clamped to +-448. (Next to a tie this can be one
- * E4M3 step from E4M3(row / scale): 2 of 10 million elements.)
+ * E4M3 step from E4M3(row / scale): 2 of 10 million elements.)  Into a QRE_E2M1
+ * cache: x = row * (1 / scale) as above; each 16 neighbours get the scale
+ * s = E4M3(max |x| / 6) (to nearest even, at most 448) and the codes nearest to
+ * x / s (to nearest even, at most 6; 0 where s is 0).  With a NaN among them s is
+ * NaN, and so are all 16.
  * A token with token_pos < 0 is skipped (padding); one without a page there, or
  * with a bad id, is skipped with QRE_DEV_BAD_INDEX.
  *   token_seq, token_pos  [n_tokens] int32, device
@@ -533,6 +545,74 @@ QRE_API qre_status qre_kv_reserve(const qre_kv_cache* cache, int32_t n, const in
 QRE_API qre_status qre_kv_write(const qre_kv_cache* cache, int32_t layer, const qre_kv_rows* rows, int32_t n_tokens,
                                 const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
                                 qre_stream_t stream);
+
+/*
+ * Reads rows of one layer back: the positions first[i] .. first[i] + m_i - 1 of
+ * sequence seqs[i] become the rows cu[i] .. cu[i+1]-1 of k and v, m_i of them
+ * (prefix sums from 0, as in qre_attn_prefill).  So a prompt that goes on behind
+ * a cached prefix has that prefix for qre_attn_prefill.  A cache of the rows' type
+ * gives its bits; a QRE_E4M3 or QRE_E2M1 cache what its elements are worth, their
+ * product with the scale in fp32 rounded once to the rows' type.
+ * A row whose position is behind seq_len or has no page becomes 0 with
+ * QRE_DEV_BAD_INDEX, as does every row of a bad id or a negative first; a sequence
+ * whose bounds are not ascending inside [0, total] is skipped with
+ * QRE_DEV_BAD_INDEX.  Rows that no sequence has stay as they were.
+ *   seqs   [n] int32, device (NULL: 0, 1, ...); first [n] int32, device (NULL: 0)
+ *   cu     [n + 1] int32, device
+ *   k, v   [total][n_kv_heads][head_dim], device (written); type and strides: rows
+ */
+QRE_API qre_status qre_kv_read(const qre_kv_cache* cache, int32_t layer, const qre_kv_rows* rows, int32_t n,
+                               const int32_t* seqs, const int32_t* first, const int32_t* cu, int32_t total, void* k,
+                               void* v, qre_stream_t stream);
+
+/*
+ * Norm and position rotation of query and key heads.  Each head's row x with a
+ * norm is first x * w / sqrt(mean(x^2) + eps) (a norm over the head's head_dim
+ * elements); then the pairs (a, b) of its first rot_dim elements turn by the angle
+ * token_pos * inv_freq[i]: a' = a cos - b sin, b' = b cos + a sin.  Pair i is the
+ * elements i and i + rot_dim / 2, or with interleaved != 0 the elements 2 i and
+ * 2 i + 1.  All in fp32 (the angle modulo a whole turn in 64 bits, so that far
+ * positions keep theirs), rounded once.
+ * rot_dim is a multiple of 16, at most head_dim; 0: no rotation.
+ */
+typedef struct {
+  const float* inv_freq; /* [rot_dim / 2], device (NULL if rot_dim is 0)              */
+  const float* q_norm;   /* [head_dim] weights w of the queries' norm, device;
+                            NULL: queries are not normed                              */
+  const float* k_norm;   /* the same for the keys                                     */
+  int32_t n_heads, n_kv_heads, head_dim;
+  int32_t dtype;         /* QRE_BF16 or QRE_FP16: all arrays                          */
+  int32_t rot_dim;
+  int32_t interleaved;
+  float eps;             /* finite, >= 0                                              */
+  int32_t reserved;      /* must be 0                                                 */
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;   /* strides of the inputs  */
+  int64_t qo_token, qo_head, ko_token, ko_head;                /* and of q_out and k_out */
+} qre_rope;
+
+/*
+ * Norms and turns n_tokens tokens' queries and keys.  A token with token_pos < 0
+ * (padding) is skipped: its rows of q_out and k_out stay as they were.
+ *   token_pos  [n_tokens] int32, device
+ *   q, q_out   [n_tokens][n_heads][head_dim], device; q_out may be q itself
+ *   k, k_out   [n_tokens][n_kv_heads][head_dim], device; k_out may be k itself
+ * Outputs that overlap an input in another way are not defined.
+ */
+QRE_API qre_status qre_qk_norm_rope(const qre_rope* rope, int32_t n_tokens, const int32_t* token_pos, const void* q,
+                                    const void* k, void* q_out, void* k_out, qre_stream_t stream);
+
+/*
+ * The same on the way into the cache: q_out gets the queries, and the turned keys
+ * and the values go to position token_pos[t] of sequence token_seq[t], as
+ * qre_kv_write puts rows there (what a QRE_E4M3 or QRE_E2M1 cache rounds is the
+ * fp32 result, and the turned keys are rounded once).  k_out (NULL: not wanted)
+ * gets the turned keys too.  Padding is skipped; a token without a page at its
+ * position, or with a bad id, has its queries and its row of k_out written and is
+ * flagged with QRE_DEV_BAD_INDEX.
+ */
+QRE_API qre_status qre_kv_write_rope(const qre_kv_cache* cache, int32_t layer, const qre_rope* rope, int32_t n_tokens,
+                                     const int32_t* token_seq, const int32_t* token_pos, const void* q, const void* k,
+                                     const void* v, void* q_out, void* k_out, qre_stream_t stream);
 
 /*
  * Forks sequence src[i] into the empty sequence dst[i], i = 0 .. n-1: whole
@@ -593,11 +673,51 @@ QRE_API qre_status qre_attn_decode_workspace_size(const qre_attn* attn, const qr
  *   q, o     [n][n_heads][head_dim], device; lse [n][n_heads] fp32 or NULL
  * A bad id gives the empty result and QRE_DEV_BAD_INDEX; a position whose page
  * is missing counts as not seen, with QRE_DEV_BAD_INDEX.  cache and attn have
- * one type, or the cache is QRE_E4M3.
+ * one type, or the cache is QRE_E4M3 or QRE_E2M1.
  */
 QRE_API qre_status qre_attn_decode(const qre_attn* attn, const qre_kv_cache* cache, int32_t layer, int32_t n,
                                    const int32_t* seqs, int32_t max_len, const void* q, void* o, float* lse,
                                    void* workspace, size_t workspace_bytes, qre_stream_t stream);
+
+/*
+ * How much groups of sequences have in common: group i is the sequences seqs[j],
+ * cu_group[i] <= j < cu_group[i+1] (prefix sums from 0 to n), and common_len[i] is
+ * the number of leading positions whose pages are the same in all of them, at most
+ * the shortest's length; 0 for a group of fewer than two.  Forks of a prompt have
+ * its full pages in common.
+ * A group with a bad id, and one whose bounds are not ascending inside [0, n], has
+ * nothing in common, with QRE_DEV_BAD_INDEX.
+ *   seqs        [n] int32, device (NULL: 0, 1, ...)
+ *   cu_group    [n_groups + 1] int32, device
+ *   common_len  [n_groups] int32, device (written); good for the attention of all
+ *               layers, and of later steps while the sequences live and only grow
+ */
+QRE_API qre_status qre_kv_common_len(const qre_kv_cache* cache, int32_t n, const int32_t* seqs, int32_t n_groups,
+                                     const int32_t* cu_group, int32_t* common_len, qre_stream_t stream);
+
+/* Bytes of workspace qre_attn_decode_shared needs for n sequences in n_groups groups (bytes: host). */
+QRE_API qre_status qre_attn_decode_shared_workspace_size(const qre_attn* attn, const qre_kv_cache* cache, int32_t n,
+                                                         int32_t n_groups, size_t* bytes);
+
+/*
+ * qre_attn_decode for sequences that share the pages of a long prefix: the keys
+ * and values of a group's common positions are read once for all of its queries,
+ * each sequence's own positions for itself, and the two parts of a query's softmax
+ * are joined in fp32.  Arguments, results and limits are those of qre_attn_decode;
+ * groups and common_len as qre_kv_common_len takes and gives them (a queries' group
+ * is that of its place in the list, every query is in one group).  How much of a
+ * common prefix is read together is the library's choice.  A common_len that is
+ * negative or beyond a sequence's length counts as 0 for its group, and a query that
+ * is in no group, or whose group's bounds are bad, is computed by itself, both with
+ * QRE_DEV_BAD_INDEX; one that claims more than the sequences have in common gives
+ * the attention to the first sequence's pages.
+ *   max_len  host: an upper bound of the lengths, 0 if not known; a wrong one costs
+ *            time and nothing else
+ */
+QRE_API qre_status qre_attn_decode_shared(const qre_attn* attn, const qre_kv_cache* cache, int32_t layer, int32_t n,
+                                          const int32_t* seqs, int32_t n_groups, const int32_t* cu_group,
+                                          const int32_t* common_len, int32_t max_len, const void* q, void* o, float* lse,
+                                          void* workspace, size_t workspace_bytes, qre_stream_t stream);
 
 /*
  * Synchronizes the stream, then writes the current device's status word

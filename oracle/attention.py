@@ -152,3 +152,78 @@ class Pages:
             self.ref[b], self.ref[a] = self.ref[a], 0
             self.content[b] = self.content[a]
         return live
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_code(x):
+    """Code (0 .. 15) of the E2M1 value nearest to x, ties to the even code, at most 6 in size."""
+    m = np.abs(np.asarray(x, np.float64))
+    d = np.abs(m[..., None] - E2M1)
+    near = d == d.min(-1, keepdims=True)
+    first = near.argmax(-1)
+    tie = near.sum(-1) > 1
+    code = np.where(tie & (first % 2 == 1), first + 1, first)
+    code = np.where(m >= 6, 7, code)
+    return np.where(np.signbit(x), code | 8, code).astype(np.uint8)
+
+
+def e2m1_blocks(x, scale=None):
+    """Rows x [..., heads, D] as a 4-bit cache keeps them: codes [..., D], block scales [..., D / 16] as values (NaN
+    where a block has one), and what they are worth before the head's factor.  scale [heads]: the head's factor, whose
+    reciprocal and the product with it are rounded to fp32."""
+    x = np.asarray(x, np.float64)
+    if scale is not None:
+        with np.errstate(over="ignore", invalid="ignore"):
+            inv = (np.float32(1) / np.asarray(scale, np.float32)).astype(np.float64)
+            x = (x * inv[:, None]).astype(np.float32).astype(np.float64)
+    b = x.reshape(x.shape[:-1] + (-1, 16))
+    most = np.abs(b).max(-1)                              # NaN if there is one
+    s = e4m3_round(np.where(np.isnan(most), np.nan, np.minimum(most, 1e300)) / 6)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = np.where(s[..., None] > 0, b / s[..., None], 0.0)
+    code = np.where(s[..., None] > 0, e2m1_code(np.where(np.isnan(q), 0.0, q)), 0).astype(np.uint8)
+    worth = np.where(code & 8, -1.0, 1.0) * E2M1[code & 7] * s[..., None]
+    return code.reshape(x.shape), s, worth.reshape(x.shape)
+
+
+def e4m3_bytes(v):
+    """E4M3 bytes of non-negative values that E4M3 holds (NaN: 0x7f)."""
+    v = np.asarray(v, np.float64)
+    e = np.maximum(np.floor(np.log2(np.where(v > 0, v, 1.0))), -6)
+    f = np.where(np.isnan(v), 0, v) / np.exp2(e)          # 1 <= f < 2, below for subnormals
+    byte = np.where(f >= 1, (e + 7) * 8 + (f - 1) * 8, f * 8)
+    return np.where(np.isnan(v), 0x7f, byte).astype(np.uint8)
+
+
+def turn(x, pos, inv_freq, interleaved, weight=None, eps=0.0):
+    """Norm (if weight) and rotation of x [tokens, heads, D] at positions pos; also what an error bound needs: for every
+    element the sum of the magnitudes that it is made of, and its token's and pair's angle."""
+    x = np.asarray(x, np.float64)
+    if weight is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    y, size, angle = x.copy(), np.abs(x), np.zeros(x.shape)
+    n = len(inv_freq)
+    for i in range(n):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+        w = np.asarray(pos, np.float64) * float(inv_freq[i])
+        c, s = np.cos(w)[:, None], np.sin(w)[:, None]
+        y[..., a] = x[..., a] * c - x[..., b] * s
+        y[..., b] = x[..., b] * c + x[..., a] * s
+        size[..., a] = size[..., b] = np.abs(x[..., a]) + np.abs(x[..., b])
+        angle[..., a] = angle[..., b] = np.abs(w)[:, None]
+    return y, size, angle
+
+
+def turn_tolerance(y, size, angle, unit, head_dim):
+    """Largest error of `turn` in fp32 with one rounding to an output of unit roundoff `unit`.
+
+    With u = 2^-24: the sum of head_dim squares, the mean, eps, the root and the quotient put at most (head_dim / 2 + 6) u
+    on the norm's factor, the weight and the product with x two more.  A cosine is of an angle whose turns are a product
+    of three numbers in 64 bits (3 roundings of 2^-53 of it), rounded to fp32 as at most half a turn (pi 2^-25 of an angle
+    at most, twice), and good to 2 units in the last place (2^-23).  Two products and a sum are 3 u of their size.
+    """
+    u = 2.0 ** -24
+    e = (head_dim / 2 + 11) * u + 2.0 ** -23 + np.pi * 2.0 ** -24 + angle * 2.0 ** -51
+    return unit * np.abs(y) + (1 + unit) * e * size + 2.0 ** -25

@@ -39,6 +39,7 @@ QRE_DEV_NO_PAGE = 0x20
 QRE_BF16 = 0
 QRE_FP16 = 1
 QRE_E4M3 = 2
+QRE_E2M1 = 4
 
 # Every symbol include/qre.h declares.
 EXPORTS = (
@@ -51,6 +52,8 @@ EXPORTS = (
     "qre_read_probe", "qre_set_host_unit_cost", "qre_route_dispatch",
     "qre_kv_workspace_size", "qre_kv_reserve", "qre_kv_write", "qre_kv_fork", "qre_kv_free", "qre_kv_compact",
     "qre_attn_prefill", "qre_attn_decode_workspace_size", "qre_attn_decode",
+    "qre_kv_read", "qre_qk_norm_rope", "qre_kv_write_rope", "qre_kv_common_len",
+    "qre_attn_decode_shared_workspace_size", "qre_attn_decode_shared",
 )
 
 
@@ -83,6 +86,14 @@ class qre_attn(ctypes.Structure):
                                                  "o_token", "o_head")])
 
 
+class qre_rope(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("inv_freq", "q_norm", "k_norm")]
+                + [(n, ctypes.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "dtype", "rot_dim", "interleaved")]
+                + [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+                                                 "qo_token", "qo_head", "ko_token", "ko_head")])
+
+
 class QreError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         self.status = status
@@ -97,6 +108,7 @@ _lib = None
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _SHAPE = ctypes.POINTER(qre_layer_shape)
 _KV, _ATTN, _ROWS = ctypes.POINTER(qre_kv_cache), ctypes.POINTER(qre_attn), ctypes.POINTER(qre_kv_rows)
+_ROPE = ctypes.POINTER(qre_rope)
 _SIGS = {
     "qre_last_error": ([], ctypes.c_char_p),
     "qre_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -134,6 +146,13 @@ _SIGS = {
     "qre_attn_prefill": ([_ATTN, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "qre_attn_decode_workspace_size": ([_ATTN, _KV, _I32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "qre_attn_decode": ([_ATTN, _KV, _I32, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "qre_kv_read": ([_KV, _I32, _ROWS, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP], ctypes.c_int),
+    "qre_qk_norm_rope": ([_ROPE, _I32, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "qre_kv_write_rope": ([_KV, _I32, _ROPE, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "qre_kv_common_len": ([_KV, _I32, _VP, _I32, _VP, _VP, _VP], ctypes.c_int),
+    "qre_attn_decode_shared_workspace_size": ([_ATTN, _KV, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "qre_attn_decode_shared": ([_ATTN, _KV, _I32, _I32, _VP, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _SZ, _VP],
+                               ctypes.c_int),
 }
 
 
@@ -341,8 +360,12 @@ def qre_set_host_unit_cost(cost: int) -> None:
 def make_kv_cache(k, v, page_table, seq_len, ref_count, dtype, k_scale=None, v_scale=None) -> qre_kv_cache:
     """Descriptor of a paged cache from its tensors: k, v [n_layers, n_pages, n_kv_heads, page_size, head_dim]
     (contiguous), page_table [max_seqs, max_pages], seq_len [max_seqs], ref_count [n_pages] int32.  It holds
-    addresses only: keep the tensors alive."""
+    addresses only: keep the tensors alive.  The pages of a QRE_E2M1 cache are bytes, [..., page_size,
+    head_dim * 9 / 16] in all."""
     L, P, H, S, D = k.shape
+    if dtype == QRE_E2M1:
+        assert D % 9 == 0 and k.element_size() == 1, "a QRE_E2M1 page has 9 bytes for every 16 elements"
+        D = D // 9 * 16
     assert v.shape == k.shape and k.is_contiguous() and v.is_contiguous() and page_table.is_contiguous()
     assert seq_len.numel() == page_table.shape[0] and ref_count.numel() == P
     return qre_kv_cache(_ptr(k), _ptr(v), _ptr(page_table), _ptr(seq_len), _ptr(ref_count), _ptr(k_scale),
@@ -419,6 +442,57 @@ def qre_attn_decode(attn, cache, layer, n, seqs, max_len, q, o, lse, workspace, 
     _check(load_library().qre_attn_decode(ctypes.byref(attn), ctypes.byref(cache), layer, n, _ptr(seqs), max_len,
                                           _ptr(q), _ptr(o), _ptr(lse), _ptr(workspace),
                                           _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_attn_decode")
+
+
+def make_rope(n_heads, n_kv_heads, head_dim, dtype, inv_freq, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
+              q=None, k=None, v=None, q_out=None, k_out=None) -> qre_rope:
+    """Descriptor of norms and rotation; inv_freq, fp32, has one entry per turned pair (None: nothing turns); the
+    strides are taken from the arrays [tokens, heads, head_dim].  It holds addresses only: keep inv_freq and the
+    norms alive."""
+    for t in (inv_freq, q_norm, k_norm):
+        assert t is None or (t.is_contiguous() and t.element_size() == 4)
+    assert all(t is None or t.numel() == head_dim for t in (q_norm, k_norm)), "a norm has head_dim weights"
+    return qre_rope(_ptr(inv_freq), _ptr(q_norm), _ptr(k_norm), n_heads, n_kv_heads, head_dim, dtype,
+                    0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0, eps, 0, *_strides(q),
+                    *_strides(k), *_strides(v), *_strides(q_out), *_strides(k_out))
+
+
+def qre_kv_read(cache, layer, rows, n, seqs, first, cu, total, k, v, stream=None) -> None:
+    _check(load_library().qre_kv_read(ctypes.byref(cache), layer, ctypes.byref(rows), n, _ptr(seqs), _ptr(first),
+                                      _ptr(cu), total, _ptr(k), _ptr(v), _stream(stream)), "qre_kv_read")
+
+
+def qre_qk_norm_rope(rope, n_tokens, token_pos, q, k, q_out, k_out, stream=None) -> None:
+    _check(load_library().qre_qk_norm_rope(ctypes.byref(rope), n_tokens, _ptr(token_pos), _ptr(q), _ptr(k),
+                                           _ptr(q_out), _ptr(k_out), _stream(stream)), "qre_qk_norm_rope")
+
+
+def qre_kv_write_rope(cache, layer, rope, n_tokens, token_seq, token_pos, q, k, v, q_out, k_out=None,
+                      stream=None) -> None:
+    _check(load_library().qre_kv_write_rope(ctypes.byref(cache), layer, ctypes.byref(rope), n_tokens, _ptr(token_seq),
+                                            _ptr(token_pos), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out),
+                                            _stream(stream)), "qre_kv_write_rope")
+
+
+def qre_kv_common_len(cache, n, seqs, n_groups, cu_group, common_len, stream=None) -> None:
+    _check(load_library().qre_kv_common_len(ctypes.byref(cache), n, _ptr(seqs), n_groups, _ptr(cu_group),
+                                            _ptr(common_len), _stream(stream)), "qre_kv_common_len")
+
+
+def qre_attn_decode_shared_workspace_size(attn: qre_attn, cache: qre_kv_cache, n: int, n_groups: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().qre_attn_decode_shared_workspace_size(ctypes.byref(attn), ctypes.byref(cache), n, n_groups,
+                                                                ctypes.byref(out)),
+           "qre_attn_decode_shared_workspace_size")
+    return out.value
+
+
+def qre_attn_decode_shared(attn, cache, layer, n, seqs, n_groups, cu_group, common_len, max_len, q, o, lse, workspace,
+                           workspace_bytes=None, stream=None) -> None:
+    _check(load_library().qre_attn_decode_shared(ctypes.byref(attn), ctypes.byref(cache), layer, n, _ptr(seqs),
+                                                 n_groups, _ptr(cu_group), _ptr(common_len), max_len, _ptr(q), _ptr(o),
+                                                 _ptr(lse), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                                 _stream(stream)), "qre_attn_decode_shared")
 
 
 def qre_read_device_status(stream=None) -> int:

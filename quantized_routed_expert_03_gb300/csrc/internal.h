@@ -151,8 +151,21 @@ cudaError_t launch_kv_reserve(const qre_kv_cache& c, int n, const int32_t* seqs,
 cudaError_t launch_kv_write(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n_tokens,
                             const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
                             int* status, cudaStream_t stream);
+// Into a QRE_E2M1 cache, and back out of any (kv_rows.cu).
+cudaError_t launch_kv_write4(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n_tokens,
+                             const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
+                             int* status, cudaStream_t stream);
+cudaError_t launch_kv_read(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n, const int32_t* seqs,
+                           const int32_t* first, const int32_t* cu, int total, void* k, void* v, int* status,
+                           cudaStream_t stream);
+// Norm and rotation of queries and keys (qk_rope.cu); c: on the way into the cache, NULL: on arrays.
+cudaError_t launch_qk_rope(const qre_rope& r, const qre_kv_cache* c, int layer, int n_tokens, const int32_t* token_seq,
+                           const int32_t* token_pos, const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                           int* status, cudaStream_t stream);
 cudaError_t launch_kv_fork(const qre_kv_cache& c, int n, const int32_t* src, const int32_t* dst, void* ws, int* status,
                            cudaStream_t stream);
+cudaError_t launch_kv_common_len(const qre_kv_cache& c, int n, const int32_t* seqs, int n_groups, const int32_t* cu_group,
+                                 int32_t* common_len, int* status, cudaStream_t stream);
 cudaError_t launch_kv_free(const qre_kv_cache& c, int n, const int32_t* seqs, int* status, cudaStream_t stream);
 cudaError_t launch_kv_compact(const qre_kv_cache& c, int32_t* table_out, int32_t* ref_out, int32_t* n_live, void* ws,
                               int* status, cudaStream_t stream);
@@ -163,6 +176,12 @@ size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n);
 cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
                                int max_len, const void* q, void* o, float* lse, void* ws, int* status,
                                cudaStream_t stream);
+
+// Decode attention with common prefixes read once (attn_shared.cu).
+size_t attn_shared_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups);
+cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
+                                      int n_groups, const int32_t* cu_group, const int32_t* common_len, int max_len,
+                                      const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream);
 
 // Router logits on the tensor cores (long token batches): whether a call of T
 // tokens takes them, the workspace they need beyond the logits (the router

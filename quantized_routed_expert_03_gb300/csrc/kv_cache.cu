@@ -15,8 +15,8 @@
 // over all SMs.
 #include <cuda_fp8.h>
 
-#include "common.cuh"
 #include "internal.h"
+#include "kv_rows.cuh"
 
 namespace qre {
 namespace {
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
 // (33 MB copied) took 20.6 us and a compaction of 1024 pages 49.6, now 14.7 and 46.9.
 __device__ void copy_pages(const qre_kv_cache& c, const int32_t* from, const int32_t* to, int copies, int first_cta,
                            int ctas) {
-  const size_t page = (size_t)c.n_kv_heads * c.page_size * c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2);
+  const size_t page = (size_t)c.n_kv_heads * kv_head_bytes(c);
   const int vecs = (int)(page / 16);
   constexpr int kEach = 8;              // 16-byte pieces of a thread on their way
   const int slices = (vecs + kEach * 256 - 1) / (kEach * 256);
@@ -403,6 +403,84 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
   copy_pages(c, ws.a, ws.b, ws.head[0], blockIdx.x, gridDim.x);
 }
 
+// ---------------------------------------------------------------- common prefix
+
+// One CTA per group: the first column in which the rows of its sequences' tables differ.  Bound by latency (ids and
+// lengths, then entries): a thread has one of 256 columns and a quarter of the sequences, eight loads on their way.
+__global__ void __launch_bounds__(kThreads) kv_common_len_kernel(const __grid_constant__ qre_kv_cache c, int n,
+                                                                 const int32_t* __restrict__ seqs,
+                                                                 const int32_t* __restrict__ cu_group,
+                                                                 int32_t* __restrict__ common_len, int* status) {
+  constexpr int kCols = 256, kParts = kThreads / kCols, kAhead = 8;
+  __shared__ int ids[kKvMaxRequests];
+  __shared__ int part[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int a = cu_group[blockIdx.x], b = cu_group[blockIdx.x + 1];
+  if (a < 0 || b < a || b > n) {
+    if (threadIdx.x == 0) {
+      common_len[blockIdx.x] = 0;
+      set_status(status, QRE_DEV_BAD_INDEX);
+    }
+    return;
+  }
+  if (b - a < 2) {
+    if (threadIdx.x == 0) common_len[blockIdx.x] = 0;
+    return;
+  }
+  int least = 0x7fffffff, bad = 0;
+  for (int i = threadIdx.x; i < b - a; i += kThreads) {
+    const int s = seqs ? seqs[a + i] : a + i;
+    ids[i] = s;
+    if (s < 0 || s >= c.max_seqs) bad = 1;
+    else least = min(least, max(c.seq_len[s], 0));
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      common_len[blockIdx.x] = 0;
+      set_status(status, QRE_DEV_BAD_INDEX);
+    }
+    return;
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = least;
+  __syncthreads();
+  least = __reduce_min_sync(0xffffffffu, part[threadIdx.x & 31]);
+  const long long held = ((long long)least + c.page_size - 1) / c.page_size;
+  const int cols = held < c.max_pages ? (int)held : c.max_pages;
+  int same = cols;
+  for (int c0 = 0; c0 < cols; c0 += kCols) {
+    const int col = c0 + (int)threadIdx.x % kCols, p = (int)threadIdx.x / kCols;
+    int differ = 0x7fffffff;
+    if (col < cols) {
+      const int page = c.page_table[(size_t)ids[0] * c.max_pages + col];
+      bool ok = page_ok(c, page);
+      for (int i0 = p; i0 < b - a; i0 += kParts * kAhead) {
+        int x[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          x[e] = i0 + e * kParts < b - a ? c.page_table[(size_t)ids[i0 + e * kParts] * c.max_pages + col] : page;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) ok = ok && x[e] == page;
+      }
+      if (!ok) differ = col;
+    }
+    differ = __reduce_min_sync(0xffffffffu, differ);
+    __syncthreads();   // the last step's values have been read
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = differ;
+    __syncthreads();
+    differ = __reduce_min_sync(0xffffffffu, part[threadIdx.x & 31]);
+    if (differ < cols) {   // the same in all threads
+      same = differ;
+      break;
+    }
+  }
+  if (threadIdx.x == 0) {
+    const long long positions = (long long)same * c.page_size;
+    common_len[blockIdx.x] = positions < least ? (int)positions : least;
+  }
+}
+
 // ---------------------------------------------------------------- write
 
 template <int RT>
@@ -515,6 +593,12 @@ int wide_grid() {
 
 size_t kv_ws_bytes(const qre_kv_cache& c) { return 256 + 3 * list_bytes(c); }
 
+cudaError_t launch_kv_common_len(const qre_kv_cache& c, int n, const int32_t* seqs, int n_groups, const int32_t* cu_group,
+                                 int32_t* common_len, int* status, cudaStream_t stream) {
+  return launch_dependent(kv_common_len_kernel, dim3(n_groups), dim3(kThreads), 0, stream, c, n, seqs, cu_group,
+                          common_len, status);
+}
+
 cudaError_t launch_kv_free(const qre_kv_cache& c, int n, const int32_t* seqs, int* status, cudaStream_t stream) {
   return launch_dependent(kv_free_kernel, dim3(n), dim3(128), 0, stream, c, seqs, status);
 }
@@ -548,6 +632,7 @@ cudaError_t launch_kv_compact(const qre_kv_cache& c, int32_t* table_out, int32_t
 cudaError_t launch_kv_write(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n_tokens,
                             const int32_t* token_seq, const int32_t* token_pos, const void* k, const void* v,
                             int* status, cudaStream_t stream) {
+  if (c.dtype == QRE_E2M1) return launch_kv_write4(c, layer, r, n_tokens, token_seq, token_pos, k, v, status, stream);
   const int per_token = 2 * c.n_kv_heads * (c.head_dim / 8);   // 16-byte pieces: at most 8192
   const int ctas = device_sm_count() * kWriteCtas;
   int tokens = ctas > 0 ? (n_tokens + ctas - 1) / ctas : 1;
