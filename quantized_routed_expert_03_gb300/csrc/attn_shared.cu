@@ -1,16 +1,873 @@
 // attn_shared.cu -- attention of one new token for sequences that share the pages of a prefix.
-#include "internal.h"
+//
+// The softmax of a query over [0, len) is joined from two parts, the group's common positions (its hole) and its own:
+//   m = max m_i, l = sum l_i 2^(m_i - m), o = sum o_i 2^(m_i - m) / l   (base 2, in fp32).
+//
+// Bound: the prefix is read once for a group, and each sequence's own positions once; 4 flops an element for each query
+// head.  The rows of a group that share a KV head, members x heads, are multiplied with a tile of keys together: at 128
+// rows a tile of 128 keys (64 KB in 16 bits at D = 128) takes the tensor cores 1024 cycles and the memory 2800.
+//
+// Steps: a plan (one CTA: what each group shares, in tiles of 128 keys); the prefixes (below); the decode kernel over
+// what lies outside the holes; the join.
+//
+// Prefixes: units are (group, KV head, 256 rows); their tiles in a row are cut into equal ranges, one per CTA (one on an
+// SM), as the decode kernel cuts its chunks.  A CTA multiplies with tcgen05, S and P in tensor memory, O beside it, in
+// two chains, each with a softmax of 128 threads, one row each: with more than 128 rows a chain has 128 of them, with
+// less both have the same rows and take the tiles in turn, so that one's products run beside the other's softmax.  K and
+// V come through a ring by TMA out of the pages; rows of 8 and 4 bits come as bytes and are widened to fp16 in shared
+// memory by four warps of their own.  No row needs a mask: a hole begins where all of the group's windows have, at a
+// whole tile, and ends with a common page, behind which the last tile's rows are zeroed.
+#include <type_traits>
+
+#include "attn_decode.cuh"
+#include "tc.cuh"
 
 namespace qre {
+namespace {
 
-size_t attn_shared_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups) {
-  return attn_decode_ws_bytes(a, c, n);
+constexpr int kM = 128;              // rows of a chain
+constexpr int kUnitRows = 2 * kM;
+constexpr int kN = 128;              // keys of a tile
+constexpr int kTileCost = 2;         // tiles that the begin and the end of a unit are worth
+constexpr int kMinTiles = 3;         // places of a range, at least
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kS = 0, kO = 256, kChain = 128;   // tensor-memory columns, from one chain to the other; P overwrites its S
+// A row's weights are taken against a reference that stays while the sum of a tile's weights is at most this (fp16
+// weights end at 65504, and values enter the accumulators times weights of up to this).
+constexpr float kMostSum = 65504.0f;
+// The weight, in base 2, of the maximum that sets the reference: fp16 ends at 2^-24, so weights below 2^-33 of the
+// largest are lost; 128 weights of it stay below kMostSum with room for a maximum that doubles.
+template <bool BF>
+constexpr float kLift = BF ? 0.0f : 8.0f;
+
+struct Group {
+  int c0, m;             // queries
+  int ha, hb;            // positions [ha, hb): ha a whole tile
+  int before;            // queries of the groups before that share something
+  int tiles;
+  int pad[2];
+};
+struct PlanHead {
+  long long total;       // places
+  int ranges, pad;
+};
+// The workspace.
+struct Space {
+  PlanHead* head;
+  long long* first;      // [n_groups + 1] places of the groups before
+  Group* groups;         // [n_groups]
+  int2* hole;            // [n]
+  int32_t* group_of;     // [n]
+  float* own_o;          // [n][n_heads][D]
+  float2* own_ml;        // [n][n_heads]
+  float* part_o;         // [rows][D]
+  float2* part_ml;       // [rows]
+  void* decode;
+  size_t bytes;
+};
+
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+int shared_grid() {
+  const int sms = device_sm_count();
+  return sms <= 0 ? 152 : sms;
+}
+
+constexpr int kPartQueries = 1024;   // of a launch of the decode kernel: it keeps 24 bytes of each in shared memory
+
+Space space_of(const qre_attn& a, int n, int n_groups, void* ws) {
+  Space s;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = static_cast<char*>(ws) + at;
+    at += up256(bytes);
+    return p;
+  };
+  const size_t heads = (size_t)n * a.n_heads;
+  // pieces of units: rows once or twice, and 256 for each range's end
+  const size_t rows = 2 * heads + (size_t)kUnitRows * shared_grid();
+  s.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
+  s.first = reinterpret_cast<long long*>(take(((size_t)n_groups + 1) * sizeof(long long)));
+  s.groups = reinterpret_cast<Group*>(take((size_t)n_groups * sizeof(Group)));
+  s.hole = reinterpret_cast<int2*>(take((size_t)n * sizeof(int2)));
+  s.group_of = reinterpret_cast<int32_t*>(take((size_t)n * sizeof(int32_t)));
+  s.own_o = reinterpret_cast<float*>(take(heads * a.head_dim * sizeof(float)));
+  s.own_ml = reinterpret_cast<float2*>(take(heads * sizeof(float2)));
+  s.part_o = reinterpret_cast<float*>(take(rows * a.head_dim * sizeof(float)));
+  s.part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
+  s.decode = take(decode_ws_bytes(a, n < kPartQueries ? n : kPartQueries));
+  s.bytes = at;
+  return s;
+}
+
+// ---------------------------------------------------------------- the plan
+
+// One CTA, a warp per group: the positions that it shares, [ha, hb): hb the common length in whole runs of 16 whose
+// pages are there, ha a whole tile at or behind the first position that every member sees.
+__global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant__ qre_kv_cache c, int n,
+                                                           const int32_t* __restrict__ seqs, int n_groups,
+                                                           const int32_t* __restrict__ cu_group,
+                                                           const int32_t* __restrict__ common_len, int window, int g,
+                                                           int n_kv_heads, int min_positions, int grid, Space s,
+                                                           int* status) {
+  __shared__ long long scan[33];
+  __shared__ int scan_m[33];
+  __shared__ long long places_of[32];
+  __shared__ int shared_of[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  int bad = 0;
+  for (int i = tid; i < n_groups; i += 1024) {
+    const int a = cu_group[i], b = cu_group[i + 1];
+    bad |= a < 0 || b < a || b > n || (i == 0 && a != 0) || (i == n_groups - 1 && b != n);
+  }
+  for (int i = tid; i < n; i += 1024) s.hole[i] = make_int2(0, 0);
+  bad = __syncthreads_or(bad || (n_groups == 0 && n > 0));
+  if (bad) {   // nothing is shared
+    if (tid == 0) {
+      set_status(status, QRE_DEV_BAD_INDEX);
+      *s.head = PlanHead{0, 0, 0};
+    }
+    return;
+  }
+  const int ps_shift = 31 - __clz(c.page_size);
+  long long total = 0;
+  int before = 0;
+  for (int g0 = 0; g0 < n_groups; g0 += 32) {
+    const int gi = g0 + warp;
+    Group x = {};
+    if (gi < n_groups) {
+      x.c0 = cu_group[gi];
+      x.m = cu_group[gi + 1] - x.c0;
+      const int common = common_len[gi];
+      int least = 0x7fffffff, most = 0, row = -1;
+      for (int i = lane; i < x.m; i += 32) {
+        const int id = seqs ? seqs[x.c0 + i] : x.c0 + i;
+        const int len = id >= 0 && id < c.max_seqs ? c.seq_len[id] : -1;
+        if (i == 0) row = id;
+        least = min(least, len);
+        most = max(most, len);
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      row = __shfl_sync(0xffffffffu, row, 0);
+      const bool ok = least >= 0 && common >= 0 && common <= least && (long long)most <= (long long)c.max_pages * c.page_size;
+      if (x.m > 0 && least >= 0 && !ok && lane == 0) set_status(status, QRE_DEV_BAD_INDEX);
+      int hb = ok && x.m > 1 ? common & ~15 : 0;
+      const int lo = window > 0 && most > window ? most - window : 0;
+      x.ha = (int)min(((long long)lo + kN - 1) / kN * kN, (long long)hb);
+      // up to the first page that is missing: what lies behind counts as not seen, each sequence for itself
+      const int col0 = x.ha >> ps_shift, cols = (hb + c.page_size - 1) >> ps_shift;
+      int gone = cols;
+      for (int k0 = col0; k0 < cols && gone == cols; k0 += 32 * 8) {
+        int p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = k0 + 32 * e + lane < cols ? c.page_table[(size_t)row * c.max_pages + k0 + 32 * e + lane] : 0;
+        int first = cols;
+#pragma unroll
+        for (int e = 7; e >= 0; --e)
+          if (p[e] < 0 || p[e] >= c.n_pages) first = k0 + 32 * e + lane;
+        gone = __reduce_min_sync(0xffffffffu, first);
+      }
+      if (gone < cols) hb = gone << ps_shift;
+      if (hb - x.ha < min_positions) hb = x.ha = 0;
+      x.hb = hb;
+      x.tiles = (hb - x.ha + kN - 1) / kN;
+      if (x.tiles)
+        for (int i = lane; i < x.m; i += 32) {
+          s.hole[x.c0 + i] = make_int2(x.ha, x.hb);
+          s.group_of[x.c0 + i] = gi;
+        }
+    }
+    const int blocks = (x.m * g + kUnitRows - 1) / kUnitRows;
+    if (lane == 0) {
+      places_of[warp] = x.tiles ? (long long)n_kv_heads * blocks * (x.tiles + kTileCost) : 0;
+      shared_of[warp] = x.tiles ? x.m : 0;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      long long p = places_of[lane];
+      int q = shared_of[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, p, d);
+        const int v = __shfl_up_sync(0xffffffffu, q, d);
+        if (lane >= d) {
+          p += u;
+          q += v;
+        }
+      }
+      scan[lane + 1] = p;
+      scan_m[lane + 1] = q;
+      if (lane == 0) scan[0] = scan_m[0] = 0;
+    }
+    __syncthreads();
+    if (gi < n_groups && lane == 0) {
+      x.before = before + scan_m[warp];
+      s.groups[gi] = x;
+      s.first[gi] = total + scan[warp];
+    }
+    total += scan[32];
+    before += scan_m[32];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    s.first[n_groups] = total;
+    const long long want = (total + kMinTiles - 1) / kMinTiles;
+    *s.head = PlanHead{total, (int)(want < grid ? want : grid), 0};
+  }
+}
+
+// ---------------------------------------------------------------- the prefixes
+
+template <int DT, int CT, int D>
+struct Shape {
+  static constexpr bool F8 = CT == QRE_E4M3, F4 = CT == QRE_E2M1, LOW = F8 || F4;
+  static constexpr bool BF = CT == QRE_BF16;         // type of the products
+  static constexpr int PT = BF ? QRE_BF16 : QRE_FP16;
+  static constexpr int HALF = kN * 128;              // 64 columns of a 128-row tile, 128-byte rows
+  static constexpr int TILE = HALF * (D / 64);
+  static constexpr int RB = F4 ? D / 2 : F8 ? D : 2 * D;   // bytes of a stored row, without scales
+  static constexpr int SB = F4 ? D / kBlock4 : 0;
+  static constexpr int RAW = kN * (RB + SB);         // bytes of a stored tile
+  static constexpr int SLOTS = D == 128 ? (LOW ? 3 : 5) : (LOW ? 6 : 10);
+  static constexpr int STAGES = !LOW ? 0 : F8 ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
+  static constexpr int THREADS = LOW ? 512 : 384;
+  static constexpr int BYTES = 2 * TILE + SLOTS * TILE + STAGES * RAW + 2048;
+  // warps 0-7: the two chains' softmax; then
+  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kWiden = 12;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, status, limit_ns) ? 1 : 0) != 0;
+}
+
+// A piece of work: some tiles of a unit.
+struct Piece {
+  int c0, rows0, rows;     // first query of the group; rows [rows0, rows0 + rows) of the KV head's
+  int hk;
+  int pos0, hb;            // first position, end of the group's common positions
+  int tiles;
+  long long out;           // first row of its parts
+  __device__ __forceinline__ bool both() const { return rows > kM; }   // each chain has rows of its own
+  // the tiles of chain t: begin, step, number
+  __device__ __forceinline__ int first(int t) const { return both() ? 0 : t; }
+  __device__ __forceinline__ int step() const { return both() ? 1 : 2; }
+  __device__ __forceinline__ int count(int t) const { return both() ? tiles : (tiles + 1 - t) / 2; }
+  __device__ __forceinline__ int valid(int t) const { return both() ? (t ? rows - kM : kM) : rows; }
+};
+
+// The pieces of one range, in order.  Every warp goes through them for itself.
+class Pieces {
+ public:
+  __device__ __forceinline__ Pieces(const Space& s, int n_groups, int g, int n_heads) : s_(s), g_(g), heads_(n_heads), gi_(-1) {
+    const PlanHead h = *s.head;
+    b_ = blockIdx.x;
+    if (b_ >= h.ranges) {
+      at_ = end_ = 0;
+      return;
+    }
+    at_ = range_begin(b_, h.ranges, h.total);
+    end_ = range_begin(b_ + 1, h.ranges, h.total);
+    int lo = 0, hi = n_groups - 1;   // the last group that begins at or before at_
+    while (lo < hi) {                // 32 at a time
+      const int lane = threadIdx.x & 31, step = (hi - lo + 31) / 32;
+      const int i = lo + (lane + 1) * step;
+      const unsigned le = __ballot_sync(0xffffffffu, i <= hi && s.first[i <= hi ? i : hi] <= at_);
+      const int k = __popc(le);      // first[] ascends: the lanes with a bit come first
+      lo += k * step;
+      if (lo + step - 1 < hi) hi = lo + step - 1;
+    }
+    gi_ = lo;
+    load();
+  }
+  __device__ __forceinline__ bool next(Piece& p) {
+    while (at_ < end_) {
+      while (at_ >= next_) {         // (groups that share nothing have no place)
+        ++gi_;
+        load();
+      }
+      const int per = x_.tiles + kTileCost;
+      const int unit = (int)((at_ - first_) / per), in = (int)(at_ - first_ - (long long)unit * per);
+      const long long left = end_ - at_;
+      const int to = left < per - in ? in + (int)left : per;
+      const int t0 = in > kTileCost ? in - kTileCost : 0, t1 = to - kTileCost;
+      at_ += to - in;
+      if (t1 <= t0) continue;
+      const int rows = x_.m * g_, blocks = (rows + kUnitRows - 1) / kUnitRows, block = unit % blocks;
+      p.hk = unit / blocks;
+      p.c0 = x_.c0;
+      p.rows0 = block * kUnitRows;
+      p.rows = rows - p.rows0 < kUnitRows ? rows - p.rows0 : kUnitRows;
+      p.pos0 = x_.ha + t0 * kN;
+      p.hb = x_.hb;
+      p.tiles = t1 - t0;
+      p.out = 2 * ((long long)x_.before * heads_ + (long long)p.hk * rows + p.rows0) + (long long)kUnitRows * b_;
+      return true;
+    }
+    return false;
+  }
+
+ private:
+  __device__ __forceinline__ void load() {
+    x_ = s_.groups[gi_];
+    first_ = s_.first[gi_];
+    next_ = s_.first[gi_ + 1];
+  }
+  const Space& s_;
+  int g_, heads_, gi_, b_;
+  long long at_, end_, first_ = 0, next_ = 0;
+  Group x_;
+};
+
+template <int DT, int CT, int D>
+__global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
+    shared_prefix_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer,
+                         const int32_t* __restrict__ seqs, int n_groups, const uint16_t* __restrict__ q,
+                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                         const __grid_constant__ CUtensorMap tk16, const __grid_constant__ CUtensorMap tv16, int box_rows,
+                         const __grid_constant__ Space space, uint64_t limit_ns, int* status) {
+  using P = Shape<DT, CT, D>;
+  extern __shared__ __align__(1024) uint8_t tiles_smem[];   // the swizzle goes by addresses; no static shared memory beside it
+  uint8_t* sq = tiles_smem;                   // two query tiles
+  uint8_t* skv = tiles_smem + 2 * P::TILE;         // ring of key and value tiles
+  uint8_t* sraw = skv + P::SLOTS * P::TILE;  // ring of stored tiles
+  uint64_t* full = reinterpret_cast<uint64_t*>(sraw + P::STAGES * P::RAW);   // [SLOTS]
+  uint64_t* empty = full + P::SLOTS;         // [SLOTS]
+  uint64_t* raw_full = empty + P::SLOTS;     // [STAGES]
+  uint64_t* raw_empty = raw_full + P::STAGES;
+  uint64_t* q_full = raw_empty + P::STAGES;
+  uint64_t* q_free = q_full + 1;
+  uint64_t* s_full = q_free + 1;             // [2]
+  uint64_t* p_full = s_full + 2;             // [2]
+  uint64_t* o_done = p_full + 2;             // [2]
+  uint64_t* drain = o_done + 2;              // [2]
+  float* row_scale = reinterpret_cast<float*>(drain + 2);   // [2][kM]: factor of a row's scores
+  uint32_t* tmem_p = reinterpret_cast<uint32_t*>(row_scale + 2 * kM);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_p + 1);   // a wait gave up
+  int* issued = const_cast<int*>(reinterpret_cast<volatile int*>(tmem_p + 2));   // tiles whose loads were issued
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.n_heads / a.n_kv_heads;
+
+  if (tid == 0) {
+    for (int s = 0; s < P::SLOTS; ++s) {
+      mbar_init(&full[s], P::LOW ? 4 : 1);
+      mbar_init(&empty[s], 2);
+    }
+    for (int s = 0; s < P::STAGES; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(q_free, 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_done[t], 1);
+      mbar_init(&drain[t], 1);
+    }
+    *abort_flag = 0;
+    *issued = 0;
+    fence_barrier_init();
+  }
+  if (warp == P::kMma) {
+    tmem_alloc(tmem_p, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const uint32_t tmem = *tmem_p;
+  auto wait_for = [&](uint64_t* b, int n) { return wait_bounded(b, n & 1, abort_flag, status, limit_ns); };   // phase n
+  Pieces pieces(space, n_groups, g, a.n_heads);
+  Piece w;
+  const int ps_shift = 31 - __clz(c.page_size);
+
+  if (warp == P::kTma) {
+    // ---- fetches the tiles: a lane has one run of rows of one page
+    int i = 0;                       // tiles so far, K and V in turn
+    bool ok = true;
+    const size_t head_bytes = (size_t)c.page_size * (P::RB + P::SB);
+    while (ok && pieces.next(w)) {
+      const int id = seqs ? seqs[w.c0] : w.c0;
+      const int32_t* table = c.page_table + (size_t)id * c.max_pages;
+      for (int j = 0; ok && j < w.tiles; ++j) {
+        const int pos0 = w.pos0 + j * kN, rows = w.hb - pos0 < kN ? w.hb - pos0 : kN;
+        const bool whole = rows == kN;
+        const int run = whole || P::LOW ? box_rows : 16, runs = (rows + run - 1) / run;
+        int page = 0;
+        if (lane < runs) page = table[(pos0 + lane * run) >> ps_shift];
+        const int off = (pos0 + lane * run) & (c.page_size - 1);
+        for (int x = 0; ok && x < 2; ++x, ++i) {
+          const bool is_v = x == 1;
+          if constexpr (!P::LOW) {
+            const int s = i % P::SLOTS;
+            ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
+            if (!ok) break;
+            uint8_t* tile = skv + s * P::TILE;
+            if (is_v && !whole) {    // what lies behind the end is multiplied by weights of 0
+              for (int e = lane; e < (kN - rows) * 8 * (D / 64); e += 32) {
+                const int half = e / ((kN - rows) * 8), r = e - half * (kN - rows) * 8;
+                reinterpret_cast<uint4*>(tile + half * P::HALF + rows * 128)[r] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&full[s], (uint32_t)(rows * 2 * D));
+              *issued = i + 1;
+            }
+            __syncwarp();
+            if (lane < runs) {
+              const CUtensorMap* map = whole ? (is_v ? &tv : &tk) : (is_v ? &tv16 : &tk16);
+              const int row = (page * c.n_kv_heads + w.hk) * c.page_size + off;
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_2d(tile + h * P::HALF + lane * run * 128, map, 64 * h, row, &full[s]);
+            }
+          } else {
+            const int s = i % P::STAGES;
+            ok = i < P::STAGES || wait_for(&raw_empty[s], i / P::STAGES - 1);
+            if (!ok) break;
+            uint8_t* raw = sraw + s * P::RAW;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(rows * (P::RB + P::SB)));
+              *issued = i + 1;
+            }
+            __syncwarp();
+            if (lane < runs) {
+              const int mine = rows - lane * run < run ? rows - lane * run : run;
+              const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) +
+                                    (((size_t)layer * c.n_pages + page) * c.n_kv_heads + w.hk) * head_bytes;
+              bulk_copy_g2s(raw + lane * run * P::RB, base + (size_t)off * P::RB, (uint32_t)(mine * P::RB), &raw_full[s]);
+              if constexpr (P::F4)
+                bulk_copy_g2s(raw + kN * P::RB + lane * run * P::SB, base + (size_t)c.page_size * P::RB + (size_t)off * P::SB,
+                              (uint32_t)(mine * P::SB), &raw_full[s]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp == P::kMma || warp == P::kMma + 1) {
+    // ---- products: the whole warp, so that the operands stay in uniform registers; a chain each
+    const int t = warp - P::kMma;
+    const uint32_t lead = elect_lane();
+    const uint32_t id_s = P::BF ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
+    const uint32_t id_o = (P::BF ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + kS + t * kChain, td = tm + kO + t * kChain;
+    const uint64_t kd = umma_desc_sw128(smem_addr(skv)), vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
+    int i0 = 0, np = 0, n = 0;       // ring tiles, pieces, key tiles of this chain so far
+    bool ok = true;
+    auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
+    while (ok && pieces.next(w)) {
+      const bool both = w.both();
+      const uint64_t qd = umma_desc_sw128(smem_addr(sq + (both ? t : 0) * P::TILE));
+      auto scores = [&](int i) {     // S = Q K_j^T
+        const uint64_t k0 = kd + (uint32_t)(i % P::SLOTS) * (P::TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
+          umma_f16_lead(ts, qd + off, k0 + off, id_s, k ? 1u : 0u, lead);
+        }
+        umma_commit_lead(&s_full[t], lead);
+        umma_commit_lead(&empty[i % P::SLOTS], lead);
+      };
+      ok = wait_for(q_full, np);
+      ++np;
+      bool begun = false;
+      for (int j = 0; ok && j < w.tiles; ++j) {
+        const int ik = i0 + 2 * j, iv = ik + 1;
+        if (!both && (j & 1) != t) {   // the other chain's
+          ok = wait_tile(ik) && wait_tile(iv);
+          if (ok && lead) {
+            mbar_arrive(&empty[ik % P::SLOTS]);
+            mbar_arrive(&empty[iv % P::SLOTS]);
+          }
+          __syncwarp();
+          continue;
+        }
+        ok = wait_tile(ik);
+        if (!ok) break;
+        tc_fence_after();
+        scores(ik);                  // over P of the tile before: issued behind the product that reads it
+        ok = wait_tile(iv) && wait_for(&p_full[t], n);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v0 = vd + (uint32_t)(iv % P::SLOTS) * (P::TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < kN / 16; ++k)   // O += P V_j
+          umma_f16_tmem_a_lead(td, ts + 8 * k, v0 + k * (2048 >> 4), id_o, begun || k ? 1u : 0u, lead);
+        umma_commit_lead(&o_done[t], lead);
+        umma_commit_lead(&empty[iv % P::SLOTS], lead);
+        begun = true;
+        ++n;
+      }
+      i0 += 2 * w.tiles;
+    }
+  } else if (P::LOW && warp >= P::kWiden) {
+    // ---- stored tiles to fp16: a thread has 16 elements of a row at a time
+    if constexpr (P::LOW) {
+      constexpr int PR = D / 16;
+      const int me = tid - 32 * P::kWiden;
+      int i = 0;
+      bool ok = true;
+      while (ok && pieces.next(w)) {
+        for (int j = 0; ok && j < w.tiles; ++j) {
+          const int rows = w.hb - (w.pos0 + j * kN) < kN ? w.hb - (w.pos0 + j * kN) : kN;
+          for (int x = 0; ok && x < 2; ++x, ++i) {
+            const int st = i % P::STAGES, sl = i % P::SLOTS;
+            ok = wait_for(&raw_full[st], i / P::STAGES) && (i < P::SLOTS || wait_for(&empty[sl], i / P::SLOTS - 1));
+            if (!ok) break;
+            const uint8_t* raw = sraw + st * P::RAW;
+            uint8_t* tile = skv + sl * P::TILE;
+#pragma unroll 4
+            for (int e = me; e < kN * PR; e += 128) {
+              const int row = e / PR, p = e % PR;
+              uint32_t y[8] = {};
+              if (row < rows) {
+                if constexpr (P::F8) {
+                  const uint4 u = *reinterpret_cast<const uint4*>(raw + row * P::RB + 16 * p);
+                  const uint32_t b[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) y[k] = e4m3x2_to_half2((b[k / 2] >> (16 * (k & 1))) & 0xffffu);
+                } else {
+                  const uint2 u = *reinterpret_cast<const uint2*>(raw + row * P::RB + 8 * p);
+                  const uint32_t sc = raw[kN * P::RB + row * P::SB + p];
+                  const uint32_t s2 = e4m3x2_to_half2(sc | sc << 8);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) y[k] = mul_half2(e2m1x2_to_half2((k < 4 ? u.x : u.y) >> (8 * (k & 3))), s2);
+                }
+              }
+              uint8_t* line = tile + (p / 4) * P::HALF + row * 128;
+              const int c0 = 2 * (p % 4);
+              *reinterpret_cast<uint4*>(line + 16 * (c0 ^ (row & 7))) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(line + 16 * ((c0 + 1) ^ (row & 7))) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&full[sl]);
+              mbar_arrive(&raw_empty[st]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ---- softmax: thread r of four warps owns row r of its chain
+    const int t = warp >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t sc = lanes + kS + t * kChain, oc = lanes + kO + t * kChain;
+    const float base = a.scale * kLog2e;
+    int np = 0, cnt = 0;             // pieces, key tiles of this chain so far
+    bool ok = true;
+    while (ok && pieces.next(w)) {
+      // the queries: 16 or 8 lanes a row, all eight warps both tiles
+      if (np > 0) ok = wait_for(q_free, np - 1);   // all rows of the piece before have seen their last scores
+      if (!ok) break;
+      {
+        constexpr int LR = D / 8;
+        const float ks = base * (P::LOW && c.k_scale ? c.k_scale[(size_t)layer * c.n_kv_heads + w.hk] : 1.0f);
+        const int tiles = w.both() ? 2 : 1, p = lane % LR;
+        for (int r = warp * (32 / LR) + lane / LR; r < tiles * kM; r += 8 * (32 / LR)) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < w.rows) {
+            const int i = (w.rows0 + r) / g, h = (w.rows0 + r) - i * g;
+            x = *reinterpret_cast<const uint4*>(q + (size_t)(w.c0 + i) * a.q_token + (size_t)(w.hk * g + h) * a.q_head + 8 * p);
+          }
+          float own = ks;
+          if (P::LOW && DT == QRE_BF16) {
+            // the largest element to [2^14, 2^15): exact but for elements 2^-29 times smaller, which round to 2^-39 of it
+            float y[8];
+            unpack8<DT>(x, y);
+            float big = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(y[e]));
+#pragma unroll
+            for (int d = LR / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+            const int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
+            const int up = e >= 128 || big == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
+            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+            own *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+            for (int e2 = 0; e2 < 8; ++e2) y[e2] *= f;
+            x = pack8<QRE_FP16>(y);
+          }
+          const int tt = r / kM, rr = r % kM;
+          *reinterpret_cast<uint4*>(sq + tt * P::TILE + (p / 8) * P::HALF + rr * 128 + 16 * ((p % 8) ^ (rr & 7))) = x;
+          if (p == 0) row_scale[r] = own;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      ok = wait_for(q_full, np);     // all rows' factors are there
+      ++np;
+      if (!ok) break;
+      const int valid = w.valid(t);
+      const float s2 = row_scale[(w.both() ? t * kM : 0) + row];
+      const bool idle = 32 * (warp & 3) >= valid;   // rows that do not exist: whatever P holds stays in their own O
+      float m = -INFINITY, l = 0.0f;                // reference (base 2) and sum
+      const int tiles = w.count(t);
+      for (int jj = 0; jj < tiles; ++jj, ++cnt) {
+        const int j = w.first(t) + jj * w.step();
+        const int seen = w.hb - (w.pos0 + j * kN);   // keys of the tile
+        ok = wait_for(&s_full[t], cnt);
+        if (!ok) break;
+        if (!idle) {
+          tc_fence_after();
+          uint32_t p[64];
+          float sum = 0.0f;
+          auto weights = [&]() {
+            const float off = m == -INFINITY ? 0.0f : -m;
+            const uint64_t s22 = pair(s2, s2), off2 = pair(off, off);
+            uint64_t part[2] = {0, 0};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(sc + 32 * b, x);
+              tmem_ld_wait();
+              if (seen < 32 * (b + 1)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (32 * b + e >= seen) x[e] = 0xff800000u;
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 z = unpair(fma2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), s22, off2));
+                const float p0 = ex2(z.x), p1 = ex2(z.y);
+                part[e & 1] = add2(part[e & 1], pair(p0, p1));
+                p[16 * b + e] = pack2<P::PT>(p0, p1);   // the weights of the product are rounded; the sum is not
+              }
+            }
+            const float2 u = unpair(add2(part[0], part[1]));
+            sum = u.x + u.y;
+          };
+          weights();
+          if (__any_sync(0xffffffffu, m == -INFINITY || sum > kMostSum)) {   // the reference moves with the maximum so far
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(sc + 32 * b, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * b + e < seen) mx = fmaxf(mx, __uint_as_float(x[e]));
+            }
+            const float to = fmaxf(m, mx * s2 - kLift<P::BF>);
+            const float f = m == to ? 1.0f : ex2(m - to);   // 2^-inf = 0 for the first keys
+            m = to;
+            l *= f;
+            if (jj > 0) {            // behind the product of the tile before
+              ok = wait_for(&o_done[t], cnt - 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int b = 0; b < D / 32; ++b) {
+                uint32_t x[32];
+                tmem_ld_32x32b_x32(oc + 32 * b, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tmem_st_32x32b_x32(oc + 32 * b, x);
+              }
+            }
+            weights();
+          }
+          l += sum;
+          tmem_st_32x32b_x32(sc, *reinterpret_cast<uint32_t(*)[32]>(p));
+          tmem_st_32x32b_x32(sc + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_free);
+      // the part: O, reference and sum
+      if (tiles > 0) ok = wait_for(&o_done[t], cnt - 1);
+      if (!ok) break;
+      if (!idle) {
+        const long long at = w.out + (w.both() ? t * kM : t * w.rows) + row;
+        if (tiles > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int b = 0; b < D / 32; ++b) {
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(oc + 32 * b, x);
+            tmem_ld_wait();
+            if (row < valid) {
+              uint4* out = reinterpret_cast<uint4*>(space.part_o + (size_t)at * D + 32 * b);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) out[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+          }
+          tc_fence_before();
+        }
+        if (row < valid) space.part_ml[at] = make_float2(m, l);   // without tiles: -inf, and O is not read
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // a wait gave up: the loads and tensor-core work already issued complete before the CTA exits
+    if (tid == 0) {
+      const int n = *issued, ring = P::LOW ? P::STAGES : P::SLOTS;
+      uint64_t* bars = P::LOW ? raw_full : full;
+      for (int i = n - ring > 0 ? n - ring : 0; i < n; ++i) mbar_wait_drain(&bars[i % ring], (i / ring) & 1, status);
+    }
+    if (warp == P::kMma || warp == P::kMma + 1) {
+      uint64_t* d = drain + (warp - P::kMma);
+      if (elect_lane()) {
+        umma_commit(d);
+        mbar_wait_drain(d, 0, status);
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  if (warp == P::kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- the join
+
+// A warp per query head: its own part, then those of the prefix in the order of the ranges.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ qre_attn a, int n,
+                                                          const float* __restrict__ v_scale, uint16_t* __restrict__ o,
+                                                          float* __restrict__ lse, const __grid_constant__ Space s) {
+  constexpr int E = D / 32;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (id >= (long long)n * a.n_heads) return;
+  const int t = (int)(id / a.n_heads), h = (int)(id - (long long)t * a.n_heads);
+  const int2 hole = s.hole[t];
+  if (hole.y <= hole.x) return;      // complete already
+  const int g = a.n_heads / a.n_kv_heads, hk = h / g;
+  const PlanHead head = *s.head;
+  const int gi = s.group_of[t];
+  const Group x = s.groups[gi];
+  const int rows = x.m * g, r = (t - x.c0) * g + h - hk * g, blocks = (rows + kUnitRows - 1) / kUnitRows, block = r / kUnitRows;
+  const int per = x.tiles + kTileCost, in_block = rows - block * kUnitRows < kUnitRows ? rows - block * kUnitRows : kUnitRows;
+  const long long u0 = s.first[gi] + (long long)(hk * blocks + block) * per;
+  const int b0 = range_of(u0 + kTileCost, head.ranges, head.total), b1 = range_of(u0 + per - 1, head.ranges, head.total);
+  const long long base = 2 * ((long long)x.before * a.n_heads + (long long)hk * rows + block * kUnitRows) + r - block * kUnitRows;
+  const float vs = v_scale ? v_scale[hk] : 1.0f;
+  float M, L, X[E];
+  {
+    const float2 ml = s.own_ml[id];
+    M = ml.x;
+    L = ml.y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : s.own_o[(size_t)id * D + E * lane + e];
+  }
+  const int parts = in_block > kM ? 1 : 2;
+#pragma unroll 2
+  for (int b = b0; b <= b1; ++b)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k >= parts) continue;
+      const long long at = base + (long long)kUnitRows * b + (long long)k * in_block;
+      const float2 ml = s.part_ml[at];
+      if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // saw nothing: its O was not written
+      const float to = fmaxf(M, ml.x);
+      const float f = M == to ? 1.0f : ex2(M - to), fe = ml.x == to ? 1.0f : ex2(ml.x - to);
+      M = to;
+      L = L * f + ml.y * fe;
+#pragma unroll
+      for (int e = 0; e < E; ++e) X[e] = X[e] * f + s.part_o[(size_t)at * D + E * lane + e] * (fe * vs);
+    }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint16_t* out = o + (size_t)t * a.o_token + (size_t)h * a.o_head + E * lane;
+  if (E == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2<DT>(X[0] * inv, X[1] * inv), pack2<DT>(X[E - 2] * inv, X[E - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack2<DT>(X[0] * inv, X[1] * inv);
+  if (lse && lane == 0) lse[id] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+}
+
+}  // namespace
+
+size_t attn_shared_ws_bytes(const qre_attn& a, const qre_kv_cache&, int n, int n_groups) {
+  return space_of(a, n, n_groups, nullptr).bytes;
 }
 
 cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
                                       int n_groups, const int32_t* cu_group, const int32_t* common_len, int max_len,
                                       const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream) {
-  return launch_attn_decode(a, c, layer, n, seqs, max_len, q, o, lse, ws, status, stream);
+  const Space s = space_of(a, n, n_groups, ws);
+  const int g = a.n_heads / a.n_kv_heads, box = c.page_size < kN ? c.page_size : kN, grid = shared_grid();
+  const bool low = c.dtype == QRE_E4M3 || c.dtype == QRE_E2M1;
+  CUtensorMap tk = {}, tv = {}, tk16 = {}, tv16 = {};
+  if (!low) {
+    const long long rows = (long long)c.n_pages * c.n_kv_heads * c.page_size;
+    const size_t skip = (size_t)layer * rows * c.head_dim * 2;
+    const char *k = static_cast<const char*>(c.k) + skip, *v = static_cast<const char*>(c.v) + skip;
+    // (rows beyond 31 bits, which only a pool that is larger than the memory has, cannot be addressed)
+    if (rows > 0x7fffffffll || !make_tmap_bf16(&tk, k, rows, c.head_dim, box) || !make_tmap_bf16(&tv, v, rows, c.head_dim, box) ||
+        !make_tmap_bf16(&tk16, k, rows, c.head_dim, 16) || !make_tmap_bf16(&tv16, v, rows, c.head_dim, 16))
+      return launch_attn_decode(a, c, layer, n, seqs, max_len, q, o, lse, s.decode, status, stream);
+  }
+  cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(1024), 0, stream, c, n, seqs, n_groups, cu_group,
+                                   common_len, a.window, g, a.n_kv_heads, kN, grid, s, status);
+  if (e != cudaSuccess) return e;
+  auto prefix = [&](auto dt, auto ct, auto d) -> cudaError_t {
+    constexpr int DT = decltype(dt)::value, CT = decltype(ct)::value, D = decltype(d)::value;
+    using P = Shape<DT, CT, D>;
+    auto kernel = shared_prefix_kernel<DT, CT, D>;
+    const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), P::BYTES);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(kernel, dim3(grid), dim3(P::THREADS), (size_t)P::BYTES, stream, a, c, layer, seqs, n_groups,
+                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, wait_limit_ns(), status);
+  };
+  using B = std::integral_constant<int, QRE_BF16>;
+  using H = std::integral_constant<int, QRE_FP16>;
+  using E8 = std::integral_constant<int, QRE_E4M3>;
+  using E4 = std::integral_constant<int, QRE_E2M1>;
+  auto by_dim = [&](auto dt, auto ct) {
+    return a.head_dim == 64 ? prefix(dt, ct, std::integral_constant<int, 64>{}) : prefix(dt, ct, std::integral_constant<int, 128>{});
+  };
+  const bool bf = a.dtype == QRE_BF16;
+  if (c.dtype == QRE_E4M3) e = bf ? by_dim(B{}, E8{}) : by_dim(H{}, E8{});
+  else if (c.dtype == QRE_E2M1) e = bf ? by_dim(B{}, E4{}) : by_dim(H{}, E4{});
+  else e = bf ? by_dim(B{}, B{}) : by_dim(H{}, H{});
+  if (e != cudaSuccess) return e;
+
+  // The sequences' own positions; chunks are counted in 32 bits (see launch_attn_decode; a hole makes one more)
+  const long long chunk = chunk_of(c), held = (long long)c.max_pages * c.page_size;
+  const long long places = (a.window > 0 && a.window < held ? a.window : held) / chunk + 3 + kUnitCost;
+  int most = 0x7fffffffll / places < n ? (int)(0x7fffffffll / places) : n;
+  most = most < kPartQueries ? most : kPartQueries;
+  for (int i = 0; i < n; i += most) {
+    const int m = n - i < most ? n - i : most;
+    const Own own{s.hole + i, s.own_o + (size_t)i * a.n_heads * a.head_dim, s.own_ml + (size_t)i * a.n_heads};
+    e = launch_part<true>(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
+                          static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, own, s.decode,
+                          status, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const float* v_scale = low && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;
+  const dim3 warps((unsigned)(((long long)n * a.n_heads + 7) / 8));
+  auto join = [&](auto kernel) {
+    return launch_dependent(kernel, warps, dim3(256), 0, stream, a, n, v_scale, static_cast<uint16_t*>(o), lse, s);
+  };
+  if (bf) return a.head_dim == 64 ? join(shared_join_kernel<QRE_BF16, 64>) : join(shared_join_kernel<QRE_BF16, 128>);
+  return a.head_dim == 64 ? join(shared_join_kernel<QRE_FP16, 64>) : join(shared_join_kernel<QRE_FP16, 128>);
 }
 
 }  // namespace qre
