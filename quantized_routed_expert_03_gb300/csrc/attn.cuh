@@ -58,6 +58,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* z) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]),
+               "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+               : "memory");
+}
+
 // Keys [lo, hi) that the query at position p of a sequence with k_len keys sees.
 __device__ __forceinline__ void visible_range(int p, int k_len, int causal, int window, int& lo, int& hi) {
   lo = 0;

@@ -207,22 +207,6 @@ struct Plan {
   static constexpr int BYTES = 2 * TILE + SLOTS * TILE + 2048 + 768;   // tiles; sums; barriers
 };
 
-// mbar_wait_bounded without a call: the register split (setmaxnreg) leaves no room for the calling convention.
-__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
-                                                 uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t deadline = global_timer_ns() + limit_ns;
-  while (!mbar_try_wait_1us(bar, parity)) {
-    if (*abort) return false;
-    if (global_timer_ns() > deadline) {
-      *abort = 1;
-      set_status(status, QRE_DEV_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
 // A count in shared memory that one thread writes and others read beside its barriers.
 __device__ __forceinline__ void store_release(int* p, int n) {
   asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(p)), "r"(n) : "memory");
@@ -247,12 +231,6 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   }
   const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)), __habs2(*reinterpret_cast<const __half2*>(&b)));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* z) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]),
-               "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
-               : "memory");
 }
 
 // One piece of work: two query tiles of one sequence and head group, with what every warp wants to

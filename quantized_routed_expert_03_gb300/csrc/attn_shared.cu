@@ -47,17 +47,35 @@ struct Group {
   int tiles;
   int pad[2];
 };
+// Places are counted in 31 bits (a call with more shares nothing): 64-bit divisions take long, most of all in
+// code that is not in the instruction cache yet.
 struct PlanHead {
-  long long total;       // places
-  int ranges, pad;
+  int total;             // places
+  int ranges;
+  int each, rest;        // total / ranges, total % ranges
+  __device__ __forceinline__ int begin(int b) const { return each * b + (int)((unsigned)rest * (unsigned)b / (unsigned)ranges); }
+  // the range that place i lies in
+  __device__ __forceinline__ int range_of(int i) const {
+    int b = (int)((float)i * ((float)ranges / (float)total));
+    b = b < ranges ? b : ranges - 1;
+    while (begin(b) > i) --b;
+    while (begin(b + 1) <= i) ++b;
+    return b;
+  }
+};
+// What the join wants to know of a query, in one place: its loads are a chain as it is.
+struct alignas(16) Query {
+  int c0, m, before, tiles;   // of its group; no tiles: it is complete already
+  int first;                  // places before the group's
+  int pad[3];
 };
 // The workspace.
 struct Space {
   PlanHead* head;
-  long long* first;      // [n_groups + 1] places of the groups before
+  int32_t* first;        // [n_groups + 1] places of the groups before
   Group* groups;         // [n_groups]
   int2* hole;            // [n]
-  int32_t* group_of;     // [n]
+  Query* query;          // [n]
   float* own_o;          // [n][n_heads][D]
   float2* own_ml;        // [n][n_heads]
   float* part_o;         // [rows][D]
@@ -87,10 +105,10 @@ Space space_of(const qre_attn& a, int n, int n_groups, void* ws) {
   // pieces of units: rows once or twice, and 256 for each range's end
   const size_t rows = 2 * heads + (size_t)kUnitRows * shared_grid();
   s.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
-  s.first = reinterpret_cast<long long*>(take(((size_t)n_groups + 1) * sizeof(long long)));
+  s.first = reinterpret_cast<int32_t*>(take(((size_t)n_groups + 1) * sizeof(int32_t)));
   s.groups = reinterpret_cast<Group*>(take((size_t)n_groups * sizeof(Group)));
   s.hole = reinterpret_cast<int2*>(take((size_t)n * sizeof(int2)));
-  s.group_of = reinterpret_cast<int32_t*>(take((size_t)n * sizeof(int32_t)));
+  s.query = reinterpret_cast<Query*>(take((size_t)n * sizeof(Query)));
   s.own_o = reinterpret_cast<float*>(take(heads * a.head_dim * sizeof(float)));
   s.own_ml = reinterpret_cast<float2*>(take(heads * sizeof(float2)));
   s.part_o = reinterpret_cast<float*>(take(rows * a.head_dim * sizeof(float)));
@@ -122,12 +140,15 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
     const int a = cu_group[i], b = cu_group[i + 1];
     bad |= a < 0 || b < a || b > n || (i == 0 && a != 0) || (i == n_groups - 1 && b != n);
   }
-  for (int i = tid; i < n; i += 1024) s.hole[i] = make_int2(0, 0);
+  for (int i = tid; i < n; i += 1024) {
+    s.hole[i] = make_int2(0, 0);
+    s.query[i].tiles = 0;
+  }
   bad = __syncthreads_or(bad || (n_groups == 0 && n > 0));
   if (bad) {   // nothing is shared
     if (tid == 0) {
       set_status(status, QRE_DEV_BAD_INDEX);
-      *s.head = PlanHead{0, 0, 0};
+      *s.head = PlanHead{0, 0, 0, 0};
     }
     return;
   }
@@ -174,11 +195,6 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       if (hb - x.ha < min_positions) hb = x.ha = 0;
       x.hb = hb;
       x.tiles = (hb - x.ha + kN - 1) / kN;
-      if (x.tiles)
-        for (int i = lane; i < x.m; i += 32) {
-          s.hole[x.c0 + i] = make_int2(x.ha, x.hb);
-          s.group_of[x.c0 + i] = gi;
-        }
     }
     const int blocks = (x.m * g + kUnitRows - 1) / kUnitRows;
     if (lane == 0) {
@@ -203,19 +219,33 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       if (lane == 0) scan[0] = scan_m[0] = 0;
     }
     __syncthreads();
+    x.before = before + scan_m[warp];
+    const int first = (int)(total + scan[warp]);
     if (gi < n_groups && lane == 0) {
-      x.before = before + scan_m[warp];
       s.groups[gi] = x;
-      s.first[gi] = total + scan[warp];
+      s.first[gi] = first;
     }
+    if (x.tiles)
+      for (int i = lane; i < x.m; i += 32) {
+        s.hole[x.c0 + i] = make_int2(x.ha, x.hb);
+        s.query[x.c0 + i] = Query{x.c0, x.m, x.before, x.tiles, first, {}};
+      }
     total += scan[32];
     before += scan_m[32];
     __syncthreads();
   }
+  if (total > 0x7fffffff - 1024) {   // (the same in all threads)
+    for (int i = tid; i < n; i += 1024) {
+      s.hole[i] = make_int2(0, 0);
+      s.query[i].tiles = 0;
+    }
+    if (tid == 0) *s.head = PlanHead{0, 0, 0, 0};
+    return;
+  }
   if (tid == 0) {
-    s.first[n_groups] = total;
-    const long long want = (total + kMinTiles - 1) / kMinTiles;
-    *s.head = PlanHead{total, (int)(want < grid ? want : grid), 0};
+    s.first[n_groups] = (int)total;
+    const int most = (int)((total + kMinTiles - 1) / kMinTiles), ranges = most < grid ? most : grid;
+    *s.head = PlanHead{(int)total, ranges, ranges ? (int)total / ranges : 0, ranges ? (int)total % ranges : 0};
   }
 }
 
@@ -234,13 +264,15 @@ struct Shape {
   static constexpr int SLOTS = D == 128 ? (LOW ? 3 : 5) : (LOW ? 6 : 10);
   static constexpr int STAGES = !LOW ? 0 : F8 ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
   static constexpr int THREADS = LOW ? 512 : 384;
+  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88, 512 x 128 = 256 x 160 + 256 x 96.
+  static constexpr int SOFT_REGS = LOW ? 160 : 208, OTHER_REGS = LOW ? 96 : 88;
   static constexpr int BYTES = 2 * TILE + SLOTS * TILE + STAGES * RAW + 2048;
   // warps 0-7: the two chains' softmax; then
   static constexpr int kTma = 8, kMma = 9 /* and 10 */, kWiden = 12;
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, status, limit_ns) ? 1 : 0) != 0;
+  return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort, status, limit_ns) ? 1 : 0) != 0;
 }
 
 // A piece of work: some tiles of a unit.
@@ -261,15 +293,16 @@ struct Piece {
 // The pieces of one range, in order.  Every warp goes through them for itself.
 class Pieces {
  public:
-  __device__ __forceinline__ Pieces(const Space& s, int n_groups, int g, int n_heads) : s_(s), g_(g), heads_(n_heads), gi_(-1) {
+  __device__ __forceinline__ Pieces(const Space& s, int g, int n_heads) : s_(s), g_(g), heads_(n_heads), gi_(-1) {}
+  // Reads the plan.
+  __device__ __forceinline__ void begin(int n_groups) {
+    const Space& s = s_;
     const PlanHead h = *s.head;
     b_ = blockIdx.x;
-    if (b_ >= h.ranges) {
-      at_ = end_ = 0;
-      return;
-    }
-    at_ = range_begin(b_, h.ranges, h.total);
-    end_ = range_begin(b_ + 1, h.ranges, h.total);
+    at_ = end_ = 0;
+    if (b_ >= h.ranges) return;
+    at_ = h.begin(b_);
+    end_ = h.begin(b_ + 1);
     int lo = 0, hi = n_groups - 1;   // the last group that begins at or before at_
     while (lo < hi) {                // 32 at a time
       const int lane = threadIdx.x & 31, step = (hi - lo + 31) / 32;
@@ -289,9 +322,8 @@ class Pieces {
         load();
       }
       const int per = x_.tiles + kTileCost;
-      const int unit = (int)((at_ - first_) / per), in = (int)(at_ - first_ - (long long)unit * per);
-      const long long left = end_ - at_;
-      const int to = left < per - in ? in + (int)left : per;
+      const int unit = (at_ - first_) / per, in = at_ - first_ - unit * per, left = end_ - at_;
+      const int to = left < per - in ? in + left : per;
       const int t0 = in > kTileCost ? in - kTileCost : 0, t1 = to - kTileCost;
       at_ += to - in;
       if (t1 <= t0) continue;
@@ -317,7 +349,7 @@ class Pieces {
   }
   const Space& s_;
   int g_, heads_, gi_, b_;
-  long long at_, end_, first_ = 0, next_ = 0;
+  int at_ = 0, end_ = 0, first_ = 0, next_ = 0;
   Group x_;
 };
 
@@ -378,140 +410,161 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_dependency_wait();
-  grid_dependents_launch();
   const uint32_t tmem = *tmem_p;
   auto wait_for = [&](uint64_t* b, int n) { return wait_bounded(b, n & 1, abort_flag, status, limit_ns); };   // phase n
-  Pieces pieces(space, n_groups, g, a.n_heads);
   Piece w;
+  Pieces pieces(space, g, a.n_heads);
+  auto begin = [&]() {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    pieces.begin(n_groups);
+  };
   const int ps_shift = 31 - __clz(c.page_size);
-
-  if (warp == P::kTma) {
-    // ---- fetches the tiles: a lane has one run of rows of one page
-    int i = 0;                       // tiles so far, K and V in turn
-    bool ok = true;
-    const size_t head_bytes = (size_t)c.page_size * (P::RB + P::SB);
-    while (ok && pieces.next(w)) {
-      const int id = seqs ? seqs[w.c0] : w.c0;
-      const int32_t* table = c.page_table + (size_t)id * c.max_pages;
-      for (int j = 0; ok && j < w.tiles; ++j) {
-        const int pos0 = w.pos0 + j * kN, rows = w.hb - pos0 < kN ? w.hb - pos0 : kN;
-        const bool whole = rows == kN;
-        const int run = whole || P::LOW ? box_rows : 16, runs = (rows + run - 1) / run;
-        int page = 0;
-        if (lane < runs) page = table[(pos0 + lane * run) >> ps_shift];
-        const int off = (pos0 + lane * run) & (c.page_size - 1);
-        for (int x = 0; ok && x < 2; ++x, ++i) {
-          const bool is_v = x == 1;
-          if constexpr (!P::LOW) {
-            const int s = i % P::SLOTS;
-            ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
-            if (!ok) break;
-            uint8_t* tile = skv + s * P::TILE;
-            if (is_v && !whole) {    // what lies behind the end is multiplied by weights of 0
-              for (int e = lane; e < (kN - rows) * 8 * (D / 64); e += 32) {
-                const int half = e / ((kN - rows) * 8), r = e - half * (kN - rows) * 8;
-                reinterpret_cast<uint4*>(tile + half * P::HALF + rows * 128)[r] = make_uint4(0, 0, 0, 0);
+  if (warp >= 8 && warp < P::kWiden) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::OTHER_REGS));
+    if (warp == P::kTma) {
+      // ---- fetches the tiles: a lane has one run of rows of one page
+      begin();
+      int i = 0;                       // tiles so far, K and V in turn
+      bool ok = true;
+      const size_t head_bytes = (size_t)c.page_size * (P::RB + P::SB);
+      while (ok && pieces.next(w)) {
+        const int id = seqs ? seqs[w.c0] : w.c0;
+        const int32_t* table = c.page_table + (size_t)id * c.max_pages;
+        for (int j = 0; ok && j < w.tiles; ++j) {
+          const int pos0 = w.pos0 + j * kN, rows = w.hb - pos0 < kN ? w.hb - pos0 : kN;
+          const bool whole = rows == kN;
+          const int run = whole || P::LOW ? box_rows : 16, runs = (rows + run - 1) / run;
+          int page = 0;
+          if (lane < runs) page = table[(pos0 + lane * run) >> ps_shift];
+          const int off = (pos0 + lane * run) & (c.page_size - 1);
+          for (int x = 0; ok && x < 2; ++x, ++i) {
+            const bool is_v = x == 1;
+            if constexpr (!P::LOW) {
+              const int s = i % P::SLOTS;
+              ok = i < P::SLOTS || wait_for(&empty[s], i / P::SLOTS - 1);
+              if (!ok) break;
+              uint8_t* tile = skv + s * P::TILE;
+              if (is_v && !whole) {    // what lies behind the end is multiplied by weights of 0
+                for (int e = lane; e < (kN - rows) * 8 * (D / 64); e += 32) {
+                  const int half = e / ((kN - rows) * 8), r = e - half * (kN - rows) * 8;
+                  reinterpret_cast<uint4*>(tile + half * P::HALF + rows * 128)[r] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
               }
-              fence_proxy_async_smem();
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&full[s], (uint32_t)(rows * 2 * D));
+                *issued = i + 1;
+              }
               __syncwarp();
-            }
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&full[s], (uint32_t)(rows * 2 * D));
-              *issued = i + 1;
+              if (lane < runs) {
+                const CUtensorMap* map = whole ? (is_v ? &tv : &tk) : (is_v ? &tv16 : &tk16);
+                const int row = (page * c.n_kv_heads + w.hk) * c.page_size + off;
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_2d(tile + h * P::HALF + lane * run * 128, map, 64 * h, row, &full[s]);
+              }
+            } else {
+              const int s = i % P::STAGES;
+              ok = i < P::STAGES || wait_for(&raw_empty[s], i / P::STAGES - 1);
+              if (!ok) break;
+              uint8_t* raw = sraw + s * P::RAW;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(rows * (P::RB + P::SB)));
+                *issued = i + 1;
+              }
+              __syncwarp();
+              if (lane < runs) {
+                const int mine = rows - lane * run < run ? rows - lane * run : run;
+                const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) +
+                                      (((size_t)layer * c.n_pages + page) * c.n_kv_heads + w.hk) * head_bytes;
+                bulk_copy_g2s(raw + lane * run * P::RB, base + (size_t)off * P::RB, (uint32_t)(mine * P::RB), &raw_full[s]);
+                if constexpr (P::F4)
+                  bulk_copy_g2s(raw + kN * P::RB + lane * run * P::SB, base + (size_t)c.page_size * P::RB + (size_t)off * P::SB,
+                                (uint32_t)(mine * P::SB), &raw_full[s]);
+              }
             }
             __syncwarp();
-            if (lane < runs) {
-              const CUtensorMap* map = whole ? (is_v ? &tv : &tk) : (is_v ? &tv16 : &tk16);
-              const int row = (page * c.n_kv_heads + w.hk) * c.page_size + off;
-              for (int h = 0; h < D / 64; ++h)
-                tma_load_2d(tile + h * P::HALF + lane * run * 128, map, 64 * h, row, &full[s]);
-            }
-          } else {
-            const int s = i % P::STAGES;
-            ok = i < P::STAGES || wait_for(&raw_empty[s], i / P::STAGES - 1);
-            if (!ok) break;
-            uint8_t* raw = sraw + s * P::RAW;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(rows * (P::RB + P::SB)));
-              *issued = i + 1;
+          }
+        }
+      }
+    } else if (warp == P::kMma || warp == P::kMma + 1) {
+      // ---- products: the whole warp, so that the operands stay in uniform registers; a chain each
+      const int t = warp - P::kMma;
+      const uint32_t elected = elect_lane();
+      uint32_t lead = 0;               // the first round is for the instruction cache: nobody issues anything
+      const uint32_t id_s = P::BF ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
+      const uint32_t id_o = (P::BF ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + kS + t * kChain, td = tm + kO + t * kChain;
+      const uint64_t kd = umma_desc_sw128(smem_addr(skv)), vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
+      int i0 = 0, np = 0, n = 0;       // ring tiles, pieces, key tiles of this chain so far
+      bool ok = true;
+      auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
+      for (bool dry = true; ok; dry = false) {
+        if (dry) {
+          w.rows = 2 * kM;
+          w.tiles = 1;
+        } else {
+          if (np == 0) {
+            begin();
+            lead = elected;
+          }
+          if (!pieces.next(w)) break;
+        }
+        const bool both = w.both();
+        const uint64_t qd = umma_desc_sw128(smem_addr(sq + (both ? t : 0) * P::TILE));
+        auto scores = [&](int i) {     // S = Q K_j^T
+          const uint64_t k0 = kd + (uint32_t)(i % P::SLOTS) * (P::TILE >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
+            umma_f16_lead(ts, qd + off, k0 + off, id_s, k ? 1u : 0u, lead);
+          }
+          umma_commit_lead(&s_full[t], lead);
+          umma_commit_lead(&empty[i % P::SLOTS], lead);
+        };
+        if (!dry) {
+          ok = wait_for(q_full, np);
+          ++np;
+        }
+        bool begun = false;
+        for (int j = 0; ok && j < w.tiles; ++j) {
+          const int ik = i0 + 2 * j, iv = ik + 1;
+          if (!both && (j & 1) != t) {   // the other chain's
+            ok = wait_tile(ik) && wait_tile(iv);
+            if (ok && lead) {
+              mbar_arrive(&empty[ik % P::SLOTS]);
+              mbar_arrive(&empty[iv % P::SLOTS]);
             }
             __syncwarp();
-            if (lane < runs) {
-              const int mine = rows - lane * run < run ? rows - lane * run : run;
-              const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) +
-                                    (((size_t)layer * c.n_pages + page) * c.n_kv_heads + w.hk) * head_bytes;
-              bulk_copy_g2s(raw + lane * run * P::RB, base + (size_t)off * P::RB, (uint32_t)(mine * P::RB), &raw_full[s]);
-              if constexpr (P::F4)
-                bulk_copy_g2s(raw + kN * P::RB + lane * run * P::SB, base + (size_t)c.page_size * P::RB + (size_t)off * P::SB,
-                              (uint32_t)(mine * P::SB), &raw_full[s]);
-            }
+            continue;
           }
-          __syncwarp();
+          ok = dry || wait_tile(ik);
+          if (!ok) break;
+          tc_fence_after();
+          scores(ik);                  // over P of the tile before: issued behind the product that reads it
+          ok = dry || (wait_tile(iv) && wait_for(&p_full[t], n));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v0 = vd + (uint32_t)(iv % P::SLOTS) * (P::TILE >> 4);
+#pragma unroll
+          for (int k = 0; k < kN / 16; ++k)   // O += P V_j
+            umma_f16_tmem_a_lead(td, ts + 8 * k, v0 + k * (2048 >> 4), id_o, begun || k ? 1u : 0u, lead);
+          umma_commit_lead(&o_done[t], lead);
+          umma_commit_lead(&empty[iv % P::SLOTS], lead);
+          begun = true;
+          n += !dry;
         }
+        if (!dry) i0 += 2 * w.tiles;
       }
     }
-  } else if (warp == P::kMma || warp == P::kMma + 1) {
-    // ---- products: the whole warp, so that the operands stay in uniform registers; a chain each
-    const int t = warp - P::kMma;
-    const uint32_t lead = elect_lane();
-    const uint32_t id_s = P::BF ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
-    const uint32_t id_o = (P::BF ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + kS + t * kChain, td = tm + kO + t * kChain;
-    const uint64_t kd = umma_desc_sw128(smem_addr(skv)), vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
-    int i0 = 0, np = 0, n = 0;       // ring tiles, pieces, key tiles of this chain so far
-    bool ok = true;
-    auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
-    while (ok && pieces.next(w)) {
-      const bool both = w.both();
-      const uint64_t qd = umma_desc_sw128(smem_addr(sq + (both ? t : 0) * P::TILE));
-      auto scores = [&](int i) {     // S = Q K_j^T
-        const uint64_t k0 = kd + (uint32_t)(i % P::SLOTS) * (P::TILE >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
-          umma_f16_lead(ts, qd + off, k0 + off, id_s, k ? 1u : 0u, lead);
-        }
-        umma_commit_lead(&s_full[t], lead);
-        umma_commit_lead(&empty[i % P::SLOTS], lead);
-      };
-      ok = wait_for(q_full, np);
-      ++np;
-      bool begun = false;
-      for (int j = 0; ok && j < w.tiles; ++j) {
-        const int ik = i0 + 2 * j, iv = ik + 1;
-        if (!both && (j & 1) != t) {   // the other chain's
-          ok = wait_tile(ik) && wait_tile(iv);
-          if (ok && lead) {
-            mbar_arrive(&empty[ik % P::SLOTS]);
-            mbar_arrive(&empty[iv % P::SLOTS]);
-          }
-          __syncwarp();
-          continue;
-        }
-        ok = wait_tile(ik);
-        if (!ok) break;
-        tc_fence_after();
-        scores(ik);                  // over P of the tile before: issued behind the product that reads it
-        ok = wait_tile(iv) && wait_for(&p_full[t], n);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t v0 = vd + (uint32_t)(iv % P::SLOTS) * (P::TILE >> 4);
-#pragma unroll
-        for (int k = 0; k < kN / 16; ++k)   // O += P V_j
-          umma_f16_tmem_a_lead(td, ts + 8 * k, v0 + k * (2048 >> 4), id_o, begun || k ? 1u : 0u, lead);
-        umma_commit_lead(&o_done[t], lead);
-        umma_commit_lead(&empty[iv % P::SLOTS], lead);
-        begun = true;
-        ++n;
-      }
-      i0 += 2 * w.tiles;
-    }
-  } else if (P::LOW && warp >= P::kWiden) {
+  } else if (warp >= P::kWiden) {
     // ---- stored tiles to fp16: a thread has 16 elements of a row at a time
     if constexpr (P::LOW) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::OTHER_REGS));
+      begin();
       constexpr int PR = D / 16;
-      const int me = tid - 32 * P::kWiden;
+      const int me = tid - 32 * P::kWiden, p = me % PR, swap = (p / 4) & 1, c0 = 2 * (p % 4) + swap;
       int i = 0;
       bool ok = true;
       while (ok && pieces.next(w)) {
@@ -522,29 +575,39 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             ok = wait_for(&raw_full[st], i / P::STAGES) && (i < P::SLOTS || wait_for(&empty[sl], i / P::SLOTS - 1));
             if (!ok) break;
             const uint8_t* raw = sraw + st * P::RAW;
-            uint8_t* tile = skv + sl * P::TILE;
-#pragma unroll 4
-            for (int e = me; e < kN * PR; e += 128) {
-              const int row = e / PR, p = e % PR;
-              uint32_t y[8] = {};
-              if (row < rows) {
+            uint8_t* to = skv + sl * P::TILE + (p / 4) * P::HALF;
+            constexpr int kRowsAt = 128 / PR, kAhead = PR;   // rows at a time; blocks of a thread: all of a tile
+#pragma unroll 1
+            for (int r0 = me / PR; r0 < kN; r0 += kAhead * kRowsAt) {
+              uint4 u[kAhead];       // E2M1: codes and the scale
+#pragma unroll
+              for (int k = 0; k < kAhead; ++k) {
+                const int row = r0 + k * kRowsAt;
                 if constexpr (P::F8) {
-                  const uint4 u = *reinterpret_cast<const uint4*>(raw + row * P::RB + 16 * p);
-                  const uint32_t b[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) y[k] = e4m3x2_to_half2((b[k / 2] >> (16 * (k & 1))) & 0xffffu);
+                  u[k] = *reinterpret_cast<const uint4*>(raw + row * P::RB + 16 * p);
                 } else {
-                  const uint2 u = *reinterpret_cast<const uint2*>(raw + row * P::RB + 8 * p);
-                  const uint32_t sc = raw[kN * P::RB + row * P::SB + p];
-                  const uint32_t s2 = e4m3x2_to_half2(sc | sc << 8);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) y[k] = mul_half2(e2m1x2_to_half2((k < 4 ? u.x : u.y) >> (8 * (k & 3))), s2);
+                  const uint2 x2 = *reinterpret_cast<const uint2*>(raw + row * P::RB + 8 * p);
+                  u[k] = make_uint4(x2.x, x2.y, raw[kN * P::RB + row * P::SB + p], 0);
                 }
               }
-              uint8_t* line = tile + (p / 4) * P::HALF + row * 128;
-              const int c0 = 2 * (p % 4);
-              *reinterpret_cast<uint4*>(line + 16 * (c0 ^ (row & 7))) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(line + 16 * ((c0 + 1) ^ (row & 7))) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+              for (int k = 0; k < kAhead; ++k) {
+                const int row = r0 + k * kRowsAt;
+                uint32_t y[8];
+                const uint32_t b4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                const uint32_t s2 = P::F4 ? e4m3x2_to_half2(u[k].z | u[k].z << 8) : 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  y[e] = P::F8 ? e4m3x2_to_half2((b4[e / 2] >> (16 * (e & 1))) & 0xffffu)
+                               : mul_half2(e2m1x2_to_half2(b4[e / 4] >> (8 * (e & 3))), s2);
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                const uint4 z0 = row < rows ? make_uint4(y[0], y[1], y[2], y[3]) : zero;
+                const uint4 z1 = row < rows ? make_uint4(y[4], y[5], y[6], y[7]) : zero;
+                // (lanes of the second 64 columns store their second piece first: other banks than the first 64's)
+                uint8_t* line = to + row * 128;
+                *reinterpret_cast<uint4*>(line + 16 * (c0 ^ (row & 7))) = swap ? z1 : z0;
+                *reinterpret_cast<uint4*>(line + 16 * (c0 ^ 1 ^ (row & 7))) = swap ? z0 : z1;
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -557,7 +620,8 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
         }
       }
     }
-  } else if (warp < 8) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::SOFT_REGS));
     // ---- softmax: thread r of four warps owns row r of its chain
     const int t = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -565,25 +629,51 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
     const float base = a.scale * kLog2e;
     int np = 0, cnt = 0;             // pieces, key tiles of this chain so far
     bool ok = true;
-    while (ok && pieces.next(w)) {
-      // the queries: 16 or 8 lanes a row, all eight warps both tiles
-      if (np > 0) ok = wait_for(q_free, np - 1);   // all rows of the piece before have seen their last scores
-      if (!ok) break;
-      {
+    // The first round is for the instruction cache: it does a tile on what lies in tensor memory while the kernels before
+    // this one end (cold, the first tile took 8700 cycles, not 1500), and leaves nothing.
+    for (bool dry = true; ok; dry = false) {
+      if (dry) {
+        w.rows = 2 * kM;
+        w.tiles = 1;
+        w.pos0 = 0;
+        w.hb = kN;
+      } else {
+        if (np == 0) begin();
+        if (!pieces.next(w)) break;
+        // the queries: 16 or 8 lanes a row, all eight warps both tiles
+        if (np > 0) ok = wait_for(q_free, np - 1);   // all rows of the piece before have seen their last scores
+        if (!ok) break;
         constexpr int LR = D / 8;
         const float ks = base * (P::LOW && c.k_scale ? c.k_scale[(size_t)layer * c.n_kv_heads + w.hk] : 1.0f);
-        const int tiles = w.both() ? 2 : 1, p = lane % LR;
-        for (int r = warp * (32 / LR) + lane / LR; r < tiles * kM; r += 8 * (32 / LR)) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < w.rows) {
-            const int i = (w.rows0 + r) / g, h = (w.rows0 + r) - i * g;
-            x = *reinterpret_cast<const uint4*>(q + (size_t)(w.c0 + i) * a.q_token + (size_t)(w.hk * g + h) * a.q_head + 8 * p);
+        const int rows = w.both() ? 2 * kM : kM, p = lane % LR;
+        const uint32_t at = smem_addr(sq) + (p / 8) * P::HALF;
+        // (loops that are not unrolled: this code is cold, and fetching it took 26,000 cycles)
+        constexpr int kStep = 8 * (32 / LR);
+        const int r_first = warp * (32 / LR) + lane / LR, di = kStep / g, dh = kStep - di * g;
+        int i = (w.rows0 + r_first) / g, h = w.rows0 + r_first - i * g;
+#pragma unroll 1
+        for (int r = r_first; r < rows; r += kStep) {
+          const bool there = r < w.rows;
+          const uint16_t* from = q + (there ? (size_t)(w.c0 + i) * a.q_token + (size_t)(w.hk * g + h) * a.q_head + 8 * p : 0);
+          cp_async_16_zfill(at + r / kM * P::TILE + r % kM * 128 + 16 * ((p % 8) ^ (r & 7)), from, there);
+          if (p == 0 && !(P::LOW && DT == QRE_BF16)) row_scale[r] = ks;
+          i += di;
+          h += dh;
+          if (h >= g) {
+            h -= g;
+            ++i;
           }
-          float own = ks;
-          if (P::LOW && DT == QRE_BF16) {
-            // the largest element to [2^14, 2^15): exact but for elements 2^-29 times smaller, which round to 2^-39 of it
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (P::LOW && DT == QRE_BF16) {
+          // to fp16: the largest element of a row to [2^14, 2^15): exact but for elements 2^-29 times smaller, which
+          // round to 2^-39 of it
+          __syncwarp();
+#pragma unroll 1
+          for (int r = r_first; r < rows; r += kStep) {
+            uint4* word = reinterpret_cast<uint4*>(sq + (p / 8) * P::HALF + r / kM * P::TILE + r % kM * 128 + 16 * ((p % 8) ^ (r & 7)));
             float y[8];
-            unpack8<DT>(x, y);
+            unpack8<DT>(*word, y);
             float big = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(y[e]));
@@ -592,50 +682,59 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             const int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
             const int up = e >= 128 || big == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
             const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-            own *= __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int e2 = 0; e2 < 8; ++e2) y[e2] *= f;
-            x = pack8<QRE_FP16>(y);
+            *word = pack8<QRE_FP16>(y);
+            if (p == 0) row_scale[r] = ks * __uint_as_float((uint32_t)(127 - up) << 23);
           }
-          const int tt = r / kM, rr = r % kM;
-          *reinterpret_cast<uint4*>(sq + tt * P::TILE + (p / 8) * P::HALF + rr * 128 + 16 * ((p % 8) ^ (rr & 7))) = x;
-          if (p == 0) row_scale[r] = own;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        ok = wait_for(q_full, np);   // all rows' factors are there
+        ++np;
+        if (!ok) break;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      ok = wait_for(q_full, np);     // all rows' factors are there
-      ++np;
-      if (!ok) break;
       const int valid = w.valid(t);
       const float s2 = row_scale[(w.both() ? t * kM : 0) + row];
       const bool idle = 32 * (warp & 3) >= valid;   // rows that do not exist: whatever P holds stays in their own O
       float m = -INFINITY, l = 0.0f;                // reference (base 2) and sum
       const int tiles = w.count(t);
-      for (int jj = 0; jj < tiles; ++jj, ++cnt) {
+      for (int jj = 0; jj < tiles; ++jj, cnt += !dry) {
         const int j = w.first(t) + jj * w.step();
         const int seen = w.hb - (w.pos0 + j * kN);   // keys of the tile
-        ok = wait_for(&s_full[t], cnt);
+        ok = dry || wait_for(&s_full[t], cnt);
         if (!ok) break;
         if (!idle) {
           tc_fence_after();
-          uint32_t p[64];
-          float sum = 0.0f;
-          auto weights = [&]() {
-            const float off = m == -INFINITY ? 0.0f : -m;
-            const uint64_t s22 = pair(s2, s2), off2 = pair(off, off);
-            uint64_t part[2] = {0, 0};
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+          if (seen < kN) {           // the last tile: what is behind the end scores -infinity
+#pragma unroll 1
+            for (int b = seen / 32; b < 4; ++b) {
               uint32_t x[32];
               tmem_ld_32x32b_x32(sc + 32 * b, x);
               tmem_ld_wait();
-              if (seen < 32 * (b + 1)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (32 * b + e >= seen) x[e] = 0xff800000u;
-              }
+              for (int e = 0; e < 32; ++e)
+                if (32 * b + e >= seen) x[e] = 0xff800000u;
+              tmem_st_32x32b_x32(sc + 32 * b, x);
+            }
+            tmem_st_wait();
+          }
+          uint32_t p[64];
+          float sum;
+          // Once, or again with the reference moved (one copy of the code: it is cold at the first tile)
+#pragma unroll 1
+          for (bool moved = false;; moved = true) {
+            const float off = m == -INFINITY ? 0.0f : -m;
+            const uint64_t s22 = pair(s2, s2), off2 = pair(off, off);
+            uint64_t part[2] = {0, 0};
+            uint32_t xs[2][32];      // the next 32 scores come meanwhile
+            tmem_ld_32x32b_x32(sc, xs[0]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              tmem_ld_wait();
+              if (b < 3) tmem_ld_32x32b_x32(sc + 32 * (b + 1), xs[(b + 1) & 1]);
+              uint32_t(&x)[32] = xs[b & 1];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const float2 z = unpair(fma2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), s22, off2));
@@ -646,9 +745,8 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             }
             const float2 u = unpair(add2(part[0], part[1]));
             sum = u.x + u.y;
-          };
-          weights();
-          if (__any_sync(0xffffffffu, m == -INFINITY || sum > kMostSum)) {   // the reference moves with the maximum so far
+            if (moved || !__any_sync(0xffffffffu, m == -INFINITY || sum > kMostSum)) break;
+            // the reference moves with the maximum so far
             float mx = -INFINITY;
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
@@ -656,8 +754,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
               tmem_ld_32x32b_x32(sc + 32 * b, x);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * b + e < seen) mx = fmaxf(mx, __uint_as_float(x[e]));
+              for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             }
             const float to = fmaxf(m, mx * s2 - kLift<P::BF>);
             const float f = m == to ? 1.0f : ex2(m - to);   // 2^-inf = 0 for the first keys
@@ -677,8 +774,8 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
                 tmem_st_32x32b_x32(oc + 32 * b, x);
               }
             }
-            weights();
           }
+          if (!ok) break;
           l += sum;
           tmem_st_32x32b_x32(sc, *reinterpret_cast<uint32_t(*)[32]>(p));
           tmem_st_32x32b_x32(sc + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
@@ -686,16 +783,16 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (lane == 0 && !dry) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_free);
+      if (lane == 0 && !dry) mbar_arrive(q_free);
       // the part: O, reference and sum
-      if (tiles > 0) ok = wait_for(&o_done[t], cnt - 1);
+      if (tiles > 0 && !dry) ok = wait_for(&o_done[t], cnt - 1);
       if (!ok) break;
       if (!idle) {
-        const long long at = w.out + (w.both() ? t * kM : t * w.rows) + row;
+        const long long at = (dry ? 0 : w.out) + (w.both() ? t * kM : t * w.rows) + row;
         if (tiles > 0) {
           tc_fence_after();
 #pragma unroll 1
@@ -703,15 +800,15 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             uint32_t x[32];
             tmem_ld_32x32b_x32(oc + 32 * b, x);
             tmem_ld_wait();
-            if (row < valid) {
-              uint4* out = reinterpret_cast<uint4*>(space.part_o + (size_t)at * D + 32 * b);
+            if (row < valid && !dry) {
+              float* out = space.part_o + (size_t)at * D + 32 * b;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) out[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+              for (int e = 0; e < 32; e += 8) st_global_32(out + e, x + e);
             }
           }
           tc_fence_before();
         }
-        if (row < valid) space.part_ml[at] = make_float2(m, l);   // without tiles: -inf, and O is not read
+        if (row < valid && !dry) space.part_ml[at] = make_float2(m, l);   // without tiles: -inf, and O is not read
       }
       __syncwarp();
     }
@@ -756,42 +853,78 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31;
   if (id >= (long long)n * a.n_heads) return;
   const int t = (int)(id / a.n_heads), h = (int)(id - (long long)t * a.n_heads);
-  const int2 hole = s.hole[t];
-  if (hole.y <= hole.x) return;      // complete already
-  const int g = a.n_heads / a.n_kv_heads, hk = h / g;
+  // what does not depend on the plan's answer is on its way beside it
+  const Query x = s.query[t];
   const PlanHead head = *s.head;
-  const int gi = s.group_of[t];
-  const Group x = s.groups[gi];
+  const float2 own_ml = s.own_ml[id];
+  float own[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) own[e] = s.own_o[(size_t)id * D + E * lane + e];
+  if (x.tiles == 0) return;          // complete already
+  const int g = a.n_heads / a.n_kv_heads, hk = h / g;
   const int rows = x.m * g, r = (t - x.c0) * g + h - hk * g, blocks = (rows + kUnitRows - 1) / kUnitRows, block = r / kUnitRows;
   const int per = x.tiles + kTileCost, in_block = rows - block * kUnitRows < kUnitRows ? rows - block * kUnitRows : kUnitRows;
-  const long long u0 = s.first[gi] + (long long)(hk * blocks + block) * per;
-  const int b0 = range_of(u0 + kTileCost, head.ranges, head.total), b1 = range_of(u0 + per - 1, head.ranges, head.total);
+  const int u0 = x.first + (hk * blocks + block) * per;
+  const int b0 = head.range_of(u0 + kTileCost), b1 = head.range_of(u0 + per - 1);
   const long long base = 2 * ((long long)x.before * a.n_heads + (long long)hk * rows + block * kUnitRows) + r - block * kUnitRows;
   const float vs = v_scale ? v_scale[hk] : 1.0f;
+  const int copies = in_block > kM ? 1 : 2, parts = (b1 - b0 + 1) * copies;
+  auto row_of = [&](int i) {         // part i of the prefix
+    const int b = b0 + i / copies, k = i - i / copies * copies;
+    return base + (long long)kUnitRows * b + (long long)k * in_block;
+  };
   float M, L, X[E];
   {
-    const float2 ml = s.own_ml[id];
-    M = ml.x;
-    L = ml.y;
+    M = own_ml.x;
+    L = own_ml.y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : s.own_o[(size_t)id * D + E * lane + e];
+    for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : own[e];
   }
-  const int parts = in_block > kM ? 1 : 2;
-#pragma unroll 2
-  for (int b = b0; b <= b1; ++b)
+  for (int i0 = 0; i0 < parts; i0 += 32) {   // a lane has a part's reference and sum
+    const int mine = parts - i0 < 32 ? parts - i0 : 32;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < mine) ml = s.part_ml[row_of(i0 + lane)];
+    const bool empty = ml.x == -INFINITY && ml.y == 0.0f;   // saw nothing: its O was not written
+    float to = ml.x;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= parts) continue;
-      const long long at = base + (long long)kUnitRows * b + (long long)k * in_block;
-      const float2 ml = s.part_ml[at];
-      if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // saw nothing: its O was not written
-      const float to = fmaxf(M, ml.x);
-      const float f = M == to ? 1.0f : ex2(M - to), fe = ml.x == to ? 1.0f : ex2(ml.x - to);
-      M = to;
-      L = L * f + ml.y * fe;
+    for (int d = 16; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+    to = fmaxf(M, to);
+    const float f = M == to ? 1.0f : ex2(M - to), fe = empty ? 0.0f : ml.x == to ? 1.0f : ex2(ml.x - to);
+    float sum = empty ? 0.0f : ml.y * fe;
 #pragma unroll
-      for (int e = 0; e < E; ++e) X[e] = X[e] * f + s.part_o[(size_t)at * D + E * lane + e] * (fe * vs);
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    M = to;
+    L = L * f + sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) X[e] *= f;
+    const uint32_t there = __ballot_sync(0xffffffffu, lane < mine && !empty);
+    constexpr int kAhead = 8;
+    for (int k0 = 0; k0 < mine; k0 += kAhead) {
+      float y[kAhead][E];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
+        if (k0 + u < mine && ((there >> (k0 + u)) & 1u)) {
+          const float* from = s.part_o + (size_t)row_of(i0 + k0 + u) * D + E * lane;
+          if (E == 4) {
+            const float4 z = *reinterpret_cast<const float4*>(from);
+            y[u][0] = z.x, y[u][1] = z.y, y[u][E - 2] = z.z, y[u][E - 1] = z.w;
+          } else {
+            const float2 z = *reinterpret_cast<const float2*>(from);
+            y[u][0] = z.x, y[u][1] = z.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float w = __shfl_sync(0xffffffffu, fe, (k0 + u) & 31) * vs;
+        if (k0 + u < mine && ((there >> (k0 + u)) & 1u))
+#pragma unroll
+          for (int e = 0; e < E; ++e) X[e] = fmaf(y[u][e], w, X[e]);
+      }
     }
+  }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   uint16_t* out = o + (size_t)t * a.o_token + (size_t)h * a.o_head + E * lane;
   if (E == 4)

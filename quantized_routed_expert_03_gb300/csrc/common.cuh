@@ -106,6 +106,22 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, abort, status, limit_ns);
 }
+// mbar_wait_bounded without a call: the register split (setmaxnreg) leaves no room for the calling convention.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                                 uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t deadline = global_timer_ns() + limit_ns;
+  while (!mbar_try_wait_1us(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() > deadline) {
+      *abort = 1;
+      set_status(status, QRE_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // The wait before tensor memory is freed or a kernel exits with copies in
 // flight: not cut short by the abort flag, and always the full kWaitLimitNs
 // (what it waits for, issued tensor-core work or bulk copies, completes on its
