@@ -4,7 +4,7 @@
 
 namespace qre {
 
-size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache&, int n) { return decode_ws_bytes(a, n); }
+size_t attn_decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n) { return decode_ws_bytes(a, c, n); }
 
 cudaError_t launch_attn_decode(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
                                int max_len, const void* q, void* o, float* lse, void* ws, int* status,

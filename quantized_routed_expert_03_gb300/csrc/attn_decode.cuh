@@ -64,7 +64,9 @@ namespace qre {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 2;
+// (a 4-bit cache is bound by its conversions' latency more than by the memory: three CTAs where registers last for it)
+constexpr int ctas_per_sm(int cache_type, int head_dim, bool wide) { return cache_type == QRE_E2M1 && !(head_dim == 128 && wide) ? 3 : 2; }
+constexpr int kChunk4 = 32;           // positions of a chunk of a 4-bit cache
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk (see Decode)
 constexpr int kRows = 16;             // query heads of a unit at most
@@ -121,6 +123,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
 }
+__device__ __forceinline__ void cp_async_16_to(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_8_zfill(uint32_t dst, const void* src, bool valid) {
   const int bytes = valid ? 8 : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -160,7 +165,7 @@ struct Decode {
   static constexpr bool BF = CT == QRE_BF16;      // type of the products
   static constexpr int RB = F4 ? D / 2 : F8 ? D : 2 * D;   // bytes of a row (of codes)
   static constexpr int SB = F4 ? D / kBlock4 : 0; // bytes of a row's scales, behind the codes of the tile
-  static constexpr int CK = F4 ? 64 : kTile / RB; // positions of a chunk
+  static constexpr int CK = F4 ? kChunk4 : kTile / RB; // positions of a chunk
   static constexpr int CODES = CK * RB;           // bytes of a tile's rows
   static constexpr int TILE = CODES + CK * SB;
   static constexpr int PR = RB / 16;              // 16-byte pieces of a row
@@ -307,7 +312,7 @@ __device__ __forceinline__ float2 peer_float2(uint32_t addr, int rank) {
 }
 
 template <int DT, int CT, int D, int NH, bool SH>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
     attn_decode_kernel(const __grid_constant__ qre_attn a, const __grid_constant__ qre_kv_cache c, int layer, int n,
                        const int32_t* __restrict__ seqs, int row0, const uint16_t* __restrict__ q, uint16_t* __restrict__ o,
                        float* __restrict__ lse, Header* __restrict__ header, float* __restrict__ parts, int stages,
@@ -486,7 +491,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   };
   to_chunk();
+  long long code_at = 0;             // lane j, E2M1: byte of that run's codes in the pool
+  int load_unit = -1, load_hk = 0;   // KV head of the unit that is fetched
   int pages = 0;                     // lane j: page of positions 16 j .. 16 j + 15 of that chunk, -1 missing, -2 not seen
+  const size_t head_bytes = (size_t)c.page_size * (K::RB + K::SB);
   auto look_up = [&]() {
     pages = -2;
     if (li < c1 && lane < K::NP) {
@@ -499,43 +507,68 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           set_status(status, QRE_DEV_BAD_INDEX);
         }
       }
+      if constexpr (K::F4) {
+        if (lp.unit != load_unit) {
+          load_unit = lp.unit;
+          load_hk = lp.unit / blocks;
+        }
+        code_at = (((long long)layer * c.n_pages + pages) * c.n_kv_heads + load_hk) * (long long)head_bytes +
+                  (pos & (c.page_size - 1)) * K::RB;
+      }
     }
   };
   const uint8_t* pool_k = static_cast<const uint8_t*>(c.k);
   const uint8_t* pool_v = static_cast<const uint8_t*>(c.v);
-  const size_t head_bytes = (size_t)c.page_size * (K::RB + K::SB);
   uint32_t missing = 0;              // bit NP * slot + j: run j of that ring slot has no page
   auto fetch = [&](int slot) {       // fetches chunk li into the slot and moves on
     if (li < c1) {
       const Span sp = Seen<CK, SH>(sq[lp.t], a.window).span(lp.ck - kUnitCost);
       const int pos0 = sp.pos0, lo = sp.lo, len = sp.hi;
-      const int hk = lp.unit / blocks;
       const uint32_t gone = __ballot_sync(0xffffffffu, pages == -1);
       missing = (missing & ~(((1u << K::NP) - 1u) << (K::NP * slot))) | (gone << (K::NP * slot));
       const uint32_t dst = smem_addr(ring + (size_t)slot * 2 * K::TILE);
       const int r0 = lane / K::PR, col = lane % K::PR;
+      if (K::F4 && !gone && pos0 >= lo && pos0 + CK <= len) {   // all of it is seen: the loader's arithmetic counts here
 #pragma unroll
-      for (int j = 0; j < K::NP; ++j) {
-        const int page = __shfl_sync(0xffffffffu, pages, j);
-        const int row0 = (pos0 + 16 * j) & (c.page_size - 1);
-        const size_t head = page < 0 ? 0 : (((size_t)layer * c.n_pages + page) * c.n_kv_heads + hk) * head_bytes;
-        const size_t base = page < 0 ? 0 : head + (size_t)row0 * K::RB;
+        for (int j = 0; j < K::NP; ++j) {
+          const long long at = __shfl_sync(0xffffffffu, code_at, j);
+          const int row0 = (pos0 + 16 * j) & (c.page_size - 1);
+          const uint8_t *ck = pool_k + at + (r0 * K::RB + 16 * col), *cv = pool_v + at + (r0 * K::RB + 16 * col);
 #pragma unroll
-        for (int r = 0; r < 16; r += K::RI) {
-          const int row = 16 * j + r + r0, pos = pos0 + row;
-          const bool ok = page >= 0 && pos >= lo && pos < len;
-          const size_t off = ok ? base + (size_t)((r + r0) * K::RB + 16 * col) : 0;
-          cp_async_16_zfill(dst + K::at(row, col), pool_k + off, ok);
-          cp_async_16_zfill(dst + K::TILE + K::at(row, col), pool_v + off, ok);
+          for (int r = 0; r < 16; r += K::RI) {
+            cp_async_16_to(dst + K::at(16 * j + r + r0, col), ck + r * K::RB);
+            cp_async_16_to(dst + K::TILE + K::at(16 * j + r + r0, col), cv + r * K::RB);
+          }
+          const uint8_t* sc = (lane < 16 ? pool_k : pool_v) + at + (c.page_size * K::RB - row0 * (K::RB - K::SB) + (lane & 15) * K::SB);
+          const uint32_t to = dst + (lane < 16 ? 0 : K::TILE) + K::CODES + (16 * j + (lane & 15)) * K::SB;
+          if (K::SB == 8) cp_async_8_zfill(to, sc, true);
+          else cp_async_4_zfill(to, sc, true);
         }
-        if constexpr (K::F4) {   // the scales: a row a lane, 16 of K and 16 of V
-          const int r = lane & 15, pos = pos0 + 16 * j + r;
-          const bool ok = page >= 0 && pos >= lo && pos < len;
-          const size_t off = ok ? head + (size_t)c.page_size * K::RB + (size_t)(row0 + r) * K::SB : 0;
-          const uint32_t to = dst + (lane < 16 ? 0 : K::TILE) + K::CODES + (16 * j + r) * K::SB;
-          const uint8_t* pool = lane < 16 ? pool_k : pool_v;
-          if (K::SB == 8) cp_async_8_zfill(to, pool + off, ok);
-          else cp_async_4_zfill(to, pool + off, ok);
+      } else {
+        const int hk = lp.unit / blocks;
+#pragma unroll
+        for (int j = 0; j < K::NP; ++j) {
+          const int page = __shfl_sync(0xffffffffu, pages, j);
+          const int row0 = (pos0 + 16 * j) & (c.page_size - 1);
+          const size_t head = page < 0 ? 0 : (((size_t)layer * c.n_pages + page) * c.n_kv_heads + hk) * head_bytes;
+          const size_t base = page < 0 ? 0 : head + (size_t)row0 * K::RB;
+#pragma unroll
+          for (int r = 0; r < 16; r += K::RI) {
+            const int row = 16 * j + r + r0, pos = pos0 + row;
+            const bool ok = page >= 0 && pos >= lo && pos < len;
+            const size_t off = ok ? base + (size_t)((r + r0) * K::RB + 16 * col) : 0;
+            cp_async_16_zfill(dst + K::at(row, col), pool_k + off, ok);
+            cp_async_16_zfill(dst + K::TILE + K::at(row, col), pool_v + off, ok);
+          }
+          if constexpr (K::F4) {   // the scales: a row a lane, 16 of K and 16 of V
+            const int r = lane & 15, pos = pos0 + 16 * j + r;
+            const bool ok = page >= 0 && pos >= lo && pos < len;
+            const size_t off = ok ? head + (size_t)c.page_size * K::RB + (size_t)(row0 + r) * K::SB : 0;
+            const uint32_t to = dst + (lane < 16 ? 0 : K::TILE) + K::CODES + (16 * j + r) * K::SB;
+            const uint8_t* pool = lane < 16 ? pool_k : pool_v;
+            if (K::SB == 8) cp_async_8_zfill(to, pool + off, ok);
+            else cp_async_4_zfill(to, pool + off, ok);
+          }
         }
       }
       ++li;
@@ -692,11 +725,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const uint32_t sa = scale_of(ksc[i][0], p + b), sb = scale_of(ksc[i][1], p + b);
+              uint32_t ya[4], yb[4];
+              e2m1x8_to_half2(x[2 * b], ya);
+              e2m1x8_to_half2(x[2 * b + 1], yb);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t ya = x[2 * b] >> (16 * e), yb = x[2 * b + 1] >> (16 * e);
-                const uint32_t a0 = mul_half2(e2m1x2_to_half2(ya), sa), a1 = mul_half2(e2m1x2_to_half2(yb), sb);
-                const uint32_t a2 = mul_half2(e2m1x2_to_half2(ya >> 8), sa), a3 = mul_half2(e2m1x2_to_half2(yb >> 8), sb);
+                const uint32_t a0 = mul_half2(ya[2 * e], sa), a1 = mul_half2(yb[2 * e], sb);
+                const uint32_t a2 = mul_half2(ya[2 * e + 1], sa), a3 = mul_half2(yb[2 * e + 1], sb);
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh) mma16816<false>(s[i][nh], a0, a1, a2, a3, qb[2 * (p + b) + e][nh]);
               }
@@ -814,12 +849,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               uint32_t y[2][2][2];   // keys 0-7 or 8-15, product, row r or r + 8
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                const uint32_t sc = pair_scale(vsc[b], d + e), w = x[2 * e + b];
+                const uint32_t sc = pair_scale(vsc[b], d + e);
+                uint32_t u[4];       // dimensions 4 r, 4 r + 1 and 4 r + 2, 4 r + 3 of key 2 j, then of key 2 j + 1
+                e2m1x8_to_half2(x[2 * e + b], u);
 #pragma unroll
                 for (int m2 = 0; m2 < 2; ++m2) {
-                  const uint32_t u = e2m1x2_to_half2(w >> (8 * m2)), z = e2m1x2_to_half2(w >> (16 + 8 * m2));
-                  y[b][m2][0] = mul_half2(__byte_perm(u, z, 0x5410), sc);
-                  y[b][m2][1] = mul_half2(__byte_perm(u, z, 0x7632), sc);
+                  y[b][m2][0] = mul_half2(__byte_perm(u[m2], u[m2 + 2], 0x5410), sc);
+                  y[b][m2][1] = mul_half2(__byte_perm(u[m2], u[m2 + 2], 0x7632), sc);
                 }
               }
 #pragma unroll
@@ -1099,20 +1135,20 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-int decode_grid() {
+int decode_grid(const qre_attn& a, const qre_kv_cache& c) {
   const int sms = device_sm_count();
-  const int n = (sms <= 0 ? 152 : sms) * kCtasPerSm;
+  const int n = (sms <= 0 ? 152 : sms) * ctas_per_sm(c.dtype, a.head_dim, a.n_heads / a.n_kv_heads > 8);
   return n < kMaxCtas ? n : kMaxCtas;
 }
 
 size_t header_bytes(int n) { return (kFirstsAt + (size_t)(n + 1) * sizeof(int32_t) + 255) & ~(size_t)255; }
 
 // Positions of a chunk of a cache, and bytes of its tile of K (or of V).
-int chunk_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? 64 : kTile / (c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)); }
-int tile_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? 64 * (c.head_dim / 2 + c.head_dim / kBlock4) : kTile; }
+int chunk_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? kChunk4 : kTile / (c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)); }
+int tile_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? kChunk4 * (c.head_dim / 2 + c.head_dim / kBlock4) : kTile; }
 
-size_t decode_ws_bytes(const qre_attn& a, int n) {
-  const int grid = decode_grid();
+size_t decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n) {
+  const int grid = decode_grid(a, c);
   return header_bytes(n) + (size_t)2 * grid * kWarps * kRows * (a.head_dim + 2) * sizeof(float);
 }
 
@@ -1121,12 +1157,11 @@ template <bool SH>
 cudaError_t launch_part(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs, int row0,
                         int max_len, const void* q, void* o, float* lse, const Own& own, void* ws, int* status,
                         cudaStream_t stream) {
-  const int grid = decode_grid();
-  const int g = a.n_heads / a.n_kv_heads;
+  const int grid = decode_grid(a, c), g = a.n_heads / a.n_kv_heads, ctas_sm = ctas_per_sm(c.dtype, a.head_dim, g > 8);
   const size_t fixed = (size_t)(n + 1) * sizeof(Seq<SH>);
   const int tile = tile_of(c);
   // what the CTAs of an SM share (1 KB of each is the system's, and the kernel's static arrays)
-  const long long room = ((long long)device_max_smem_optin() + 1024) / kCtasPerSm - 1024 - 256 - (long long)fixed;
+  const long long room = ((long long)device_max_smem_optin() + 1024) / ctas_sm - 1024 - 256 - (long long)fixed;
   const int stages = room >= 3ll * kWarps * 2 * tile ? 3 : 2;
   const size_t smem = (size_t)stages * kWarps * 2 * tile + fixed;
   Header* header = static_cast<Header*>(ws);

@@ -93,7 +93,7 @@ int shared_grid() {
 
 constexpr int kPartQueries = 1024;   // of a launch of the decode kernel: it keeps 24 bytes of each in shared memory
 
-Space space_of(const qre_attn& a, int n, int n_groups, void* ws) {
+Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, void* ws) {
   Space s;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -113,7 +113,7 @@ Space space_of(const qre_attn& a, int n, int n_groups, void* ws) {
   s.own_ml = reinterpret_cast<float2*>(take(heads * sizeof(float2)));
   s.part_o = reinterpret_cast<float*>(take(rows * a.head_dim * sizeof(float)));
   s.part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
-  s.decode = take(decode_ws_bytes(a, n < kPartQueries ? n : kPartQueries));
+  s.decode = take(decode_ws_bytes(a, c, n < kPartQueries ? n : kPartQueries));
   s.bytes = at;
   return s;
 }
@@ -594,12 +594,17 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
               for (int k = 0; k < kAhead; ++k) {
                 const int row = r0 + k * kRowsAt;
                 uint32_t y[8];
-                const uint32_t b4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                const uint32_t s2 = P::F4 ? e4m3x2_to_half2(u[k].z | u[k].z << 8) : 0;
+                if constexpr (P::F8) {
+                  const uint32_t b4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  y[e] = P::F8 ? e4m3x2_to_half2((b4[e / 2] >> (16 * (e & 1))) & 0xffffu)
-                               : mul_half2(e2m1x2_to_half2(b4[e / 4] >> (8 * (e & 3))), s2);
+                  for (int e = 0; e < 8; ++e) y[e] = e4m3x2_to_half2((b4[e / 2] >> (16 * (e & 1))) & 0xffffu);
+                } else {
+                  const uint32_t s2 = e4m3x2_to_half2(__byte_perm(u[k].z, 0, 0x4400) & 0xffffu);
+                  e2m1x8_to_half2(u[k].x, *reinterpret_cast<uint32_t(*)[4]>(y));
+                  e2m1x8_to_half2(u[k].y, *reinterpret_cast<uint32_t(*)[4]>(y + 4));
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] = mul_half2(y[e], s2);
+                }
                 const uint4 zero = make_uint4(0, 0, 0, 0);
                 const uint4 z0 = row < rows ? make_uint4(y[0], y[1], y[2], y[3]) : zero;
                 const uint4 z1 = row < rows ? make_uint4(y[4], y[5], y[6], y[7]) : zero;
@@ -936,14 +941,14 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
 
 }  // namespace
 
-size_t attn_shared_ws_bytes(const qre_attn& a, const qre_kv_cache&, int n, int n_groups) {
-  return space_of(a, n, n_groups, nullptr).bytes;
+size_t attn_shared_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups) {
+  return space_of(a, c, n, n_groups, nullptr).bytes;
 }
 
 cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs,
                                       int n_groups, const int32_t* cu_group, const int32_t* common_len, int max_len,
                                       const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream) {
-  const Space s = space_of(a, n, n_groups, ws);
+  const Space s = space_of(a, c, n, n_groups, ws);
   const int g = a.n_heads / a.n_kv_heads, box = c.page_size < kN ? c.page_size : kN, grid = shared_grid();
   const bool low = c.dtype == QRE_E4M3 || c.dtype == QRE_E2M1;
   CUtensorMap tk = {}, tv = {}, tk16 = {}, tv16 = {};

@@ -103,9 +103,11 @@ __device__ __forceinline__ void load16(const uint8_t* base, int row, int b, int 
     const uint2 u = *reinterpret_cast<const uint2*>(base + (size_t)row * (D / 2) + 8 * b);
     const uint8_t byte = base[(size_t)page_size * (D / 2) + (size_t)row * (D / kBlock4) + b];
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+    e2m1x8_to_half2(u.x, *reinterpret_cast<uint32_t(*)[4]>(y));
+    e2m1x8_to_half2(u.y, *reinterpret_cast<uint32_t(*)[4]>(y + 4));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const __half2 h = u32_as_h2(e2m1x2_to_half2((i < 4 ? u.x : u.y) >> (8 * (i & 3))));
+      const __half2 h = u32_as_h2(y[i]);
       // code * s is exact in fp32 (2 + 4 bits), then one product with the head's scale, then one rounding
       y[i] = pack2<RT>(__low2float(h) * s * scale, __high2float(h) * s * scale);
     }
@@ -116,7 +118,7 @@ __device__ __forceinline__ void load16(const uint8_t* base, int row, int b, int 
 template <int RT, int CT>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(
     const __grid_constant__ qre_kv_cache c, int layer, const __grid_constant__ qre_kv_rows r, int n, int total, int tokens,
-    uint32_t magic, const int32_t* __restrict__ seqs, const int32_t* __restrict__ first, const int32_t* __restrict__ cu,
+    uint32_t magic, int wide, const int32_t* __restrict__ seqs, const int32_t* __restrict__ first, const int32_t* __restrict__ cu,
     uint16_t* __restrict__ k, uint16_t* __restrict__ v, int* status) {
   __shared__ long long page_of[kTokens];   // -1: zeros, -2: nobody's row
   __shared__ int pos_of[kTokens];
@@ -154,23 +156,42 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(
   const int per_head_shift = D == 64 ? 2 : 3, per_row = c.n_kv_heads << per_head_shift, per_token = 2 * per_row;
   const int blocks = mine * per_token;
   const size_t head = kv_head_bytes(c);
-  for (int i = threadIdx.x; i < blocks; i += kThreads) {
-    const int t = (int)__umulhi((uint32_t)i, magic), rest = i - t * per_token;
-    const bool is_v = rest >= per_row;
-    const int x = is_v ? rest - per_row : rest, h = x >> per_head_shift, b = x & ((1 << per_head_shift) - 1);
-    const long long page = page_of[t];
-    if (page == -2) continue;
-    uint32_t y[8] = {};
-    if (page >= 0) {
-      const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) + page + (size_t)h * head;
-      const float* scales = is_v ? c.v_scale : c.k_scale;
-      load16<RT, CT>(base, pos_of[t] & (c.page_size - 1), b, D, c.page_size,
-                     CT != QRE_BF16 && scales ? scales[(size_t)layer * c.n_kv_heads + h] : 1.0f, y);
+  constexpr int kEach = 2;           // blocks of a thread on their way
+  for (int i0 = threadIdx.x; i0 < blocks; i0 += kEach * kThreads) {
+    uint32_t y[kEach][8];
+    uint16_t* dst[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int i = i0 + u * kThreads;
+      dst[u] = nullptr;
+      if (i >= blocks) continue;
+      const int t = (int)__umulhi((uint32_t)i, magic), rest = i - t * per_token;
+      const bool is_v = rest >= per_row;
+      const int x = is_v ? rest - per_row : rest, h = x >> per_head_shift, b = x & ((1 << per_head_shift) - 1);
+      const long long page = page_of[t];
+      if (page == -2) continue;
+      dst[u] = (is_v ? v + (size_t)(t0 + t) * r.v_token + (size_t)h * r.v_head
+                     : k + (size_t)(t0 + t) * r.k_token + (size_t)h * r.k_head) + kBlock4 * b;
+      if (page >= 0) {
+        const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) + page + (size_t)h * head;
+        const float* scales = is_v ? c.v_scale : c.k_scale;
+        load16<RT, CT>(base, pos_of[t] & (c.page_size - 1), b, D, c.page_size,
+                       CT != QRE_BF16 && scales ? scales[(size_t)layer * c.n_kv_heads + h] : 1.0f, y[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[u][e] = 0;
+      }
     }
-    uint16_t* dst = (is_v ? v + (size_t)(t0 + t) * r.v_token + (size_t)h * r.v_head
-                          : k + (size_t)(t0 + t) * r.k_token + (size_t)h * r.k_head) + kBlock4 * b;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      if (!dst[u]) continue;
+      if (wide) {
+        st_global_32(dst[u], y[u]);
+      } else {
+        *reinterpret_cast<uint4*>(dst[u]) = make_uint4(y[u][0], y[u][1], y[u][2], y[u][3]);
+        *reinterpret_cast<uint4*>(dst[u] + 8) = make_uint4(y[u][4], y[u][5], y[u][6], y[u][7]);
+      }
+    }
   }
 }
 
@@ -206,9 +227,11 @@ cudaError_t launch_kv_read(const qre_kv_cache& c, int layer, const qre_kv_rows& 
                            const int32_t* first, const int32_t* cu, int total, void* k, void* v, int* status,
                            cudaStream_t stream) {
   const Cut cut(c, total, 8);
+  auto fits = [](const void* p, int64_t token, int64_t head) { return reinterpret_cast<uintptr_t>(p) % 32 == 0 && token % 16 == 0 && head % 16 == 0; };
+  const int wide = fits(k, r.k_token, r.k_head) && fits(v, r.v_token, r.v_head);   // whole 32-byte sectors
   auto go = [&](auto kernel) {
-    return launch_dependent(kernel, cut.grid, dim3(kThreads), 0, stream, c, layer, r, n, total, cut.tokens, cut.magic, seqs,
-                            first, cu, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), status);
+    return launch_dependent(kernel, cut.grid, dim3(kThreads), 0, stream, c, layer, r, n, total, cut.tokens, cut.magic, wide,
+                            seqs, first, cu, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), status);
   };
   if (c.dtype == QRE_E4M3) return r.dtype == QRE_BF16 ? go(kv_read_kernel<QRE_BF16, QRE_E4M3>) : go(kv_read_kernel<QRE_FP16, QRE_E4M3>);
   if (c.dtype == QRE_E2M1) return r.dtype == QRE_BF16 ? go(kv_read_kernel<QRE_BF16, QRE_E2M1>) : go(kv_read_kernel<QRE_FP16, QRE_E2M1>);

@@ -48,11 +48,23 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
   return r;
 }
 
-// Two E2M1 codes, the low byte of b, as an fp16 pair (the low four bits first).
-__device__ __forceinline__ uint32_t e2m1x2_to_half2(uint32_t b) {
+// Two E2M1 codes, byte B of w, as an fp16 pair (the low four bits first).  The conversion takes any byte of a register;
+// a shift in front of it would be an instruction more.
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_to_half2(uint32_t w) {
   uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(b));
+  if constexpr (B == 0) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+  if constexpr (B == 1) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+  if constexpr (B == 2) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+  if constexpr (B == 3) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
   return r;
+}
+// Eight codes as four pairs.
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&y)[4]) {
+  y[0] = e2m1x2_to_half2<0>(w);
+  y[1] = e2m1x2_to_half2<1>(w);
+  y[2] = e2m1x2_to_half2<2>(w);
+  y[3] = e2m1x2_to_half2<3>(w);
 }
 
 // The scale of a block whose largest magnitude is `most` (NaN if it has one).  The quotient is correctly

@@ -13,7 +13,10 @@
 // rotation needs no exchange between lanes; the norm's sum takes three or two
 // shuffles.  A CTA has a few neighbouring tokens; their cosines and sines, the same
 // for all heads, are worked out once into shared memory while the first rows are on
-// their way, and each thread asks for its next row before it works on this one.
+// their way, and each thread asks for its next row before it works on this one.  The
+// queries' rows come first, then the keys', then the values', so that a lane keeps its
+// weights of the norm in registers; they and its angles lie in shared memory as it reads
+// them, neighbouring lanes side by side.
 #include <type_traits>
 
 #include "internal.h"
@@ -23,7 +26,7 @@ namespace qre {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;    // of a CTA at most
+constexpr int kTokens = 4;     // of a CTA at most
 
 // Cosine and sine of pos * f, f radians per position.  The angle in whole turns is taken modulo 1 in
 // 64 bits: at position 2^31 it is still good to 2^-22 of a turn for f = 1 (in fp32 nothing would be left).
@@ -39,61 +42,51 @@ enum To { kArrays = -1 };   // else the qre_dtype of the cache
 template <int DT, int D, int CT>
 __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
     const __grid_constant__ qre_rope r, const __grid_constant__ qre_kv_cache c, int layer, int n_tokens, int tokens,
-    uint32_t magic, const int32_t* __restrict__ token_seq, const int32_t* __restrict__ token_pos, const uint16_t* q,
-    const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, int* status) {
+    uint32_t q_magic, uint32_t k_magic, const int32_t* __restrict__ token_seq, const int32_t* __restrict__ token_pos,
+    const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, int* status) {
   constexpr int LR = D / 16;             // lanes of a row
   constexpr int kRowsAt = kThreads / LR; // rows of a CTA at a time
   constexpr bool kCache = CT != kArrays;
   constexpr bool kQuant = CT == QRE_E4M3 || CT == QRE_E2M1;
-  __shared__ __align__(16) float2 turn[kTokens][D / 2];
+  __shared__ __align__(16) float2 turn[kTokens][D / 2];   // a lane's angles two by two, lane beside lane
+  __shared__ __align__(16) float weights[2][D];
   __shared__ int pos_of[kTokens];
   __shared__ long long page_of[kCache ? kTokens : 1];
   const int lane = threadIdx.x & 31, j = threadIdx.x % LR;
   const uint32_t mates = ((1u << LR) - 1u) << (lane & ~(LR - 1));
-  const int rows_of = r.n_heads + r.n_kv_heads * (kCache ? 2 : 1);   // of a token: q, k, v
   const int t0 = blockIdx.x * tokens, mine = n_tokens - t0 < tokens ? n_tokens - t0 : tokens;
-  const int rows = mine * rows_of, half = r.rot_dim / 2, step = r.rot_dim / 16;
+  const int half = r.rot_dim / 2, step = r.rot_dim / 16;
   const int ps_shift = kCache ? 31 - __clz(c.page_size) : 0;
-
-  // Pieces of a lane: a rotated pair, or two neighbours behind what is rotated; of a value row two neighbours.
   const bool turns = j < step;
-  const int p0 = turns ? j : 2 * step + 2 * (j - step), p1 = turns ? j + step : p0 + 1;
+  const int i0 = threadIdx.x / LR;
 
+  // The CTA's rows: all queries', then all keys', then all values'.
+  const int q_rows = mine * r.n_heads, k_rows = mine * r.n_kv_heads, rows = q_rows + k_rows * (kCache ? 2 : 1);
   struct Row {
-    int t, h, kind;   // kind 0 q, 1 k, 2 v; -1 none
+    int kind, t, h;   // kind 0 q, 1 k, 2 v
     uint4 x[2];
   };
-  auto ask = [&](int i) {
-    Row w;
-    w.kind = -1;
-    w.t = w.h = 0;
-    if (i >= rows) return w;
-    w.t = (int)__umulhi((uint32_t)i, magic);
-    w.h = i - w.t * rows_of;
-    const uint16_t* src;
+  // Pieces of a lane: a rotated pair, or two neighbours behind what is rotated; of a value row two neighbours.
+  const int own0 = turns ? j : 2 * step + 2 * (j - step), own1 = turns ? j + step : own0 + 1;
+  auto ask = [&](int i, Row& w) {
+    if (i >= rows) return;
+    w.kind = i < q_rows ? 0 : !kCache || i < q_rows + k_rows ? 1 : 2;
+    const int n = w.kind == 0 ? i : w.kind == 1 ? i - q_rows : i - q_rows - k_rows;
+    const int heads = w.kind == 0 ? r.n_heads : r.n_kv_heads;
+    w.t = heads == 1 ? n : (int)__umulhi((uint32_t)n, w.kind == 0 ? q_magic : k_magic);
+    w.h = n - w.t * heads;
     const size_t t = (size_t)(t0 + w.t);
-    if (w.h < r.n_heads) {
-      w.kind = 0;
-      src = q + t * r.q_token + (size_t)w.h * r.q_head;
-    } else if (!kCache || w.h < r.n_heads + r.n_kv_heads) {
-      w.kind = 1;
-      w.h -= r.n_heads;
-      src = k + t * r.k_token + (size_t)w.h * r.k_head;
-    } else {
-      w.kind = 2;
-      w.h -= r.n_heads + r.n_kv_heads;
-      src = v + t * r.v_token + (size_t)w.h * r.v_head;
-    }
+    const uint16_t* row = w.kind == 0   ? q + t * r.q_token + (size_t)w.h * r.q_head
+                          : w.kind == 1 ? k + t * r.k_token + (size_t)w.h * r.k_head
+                                        : v + t * r.v_token + (size_t)w.h * r.v_head;
     const bool is_v = kCache && w.kind == 2;
-    w.x[0] = *reinterpret_cast<const uint4*>(src + 8 * (is_v ? 2 * j : p0));
-    w.x[1] = *reinterpret_cast<const uint4*>(src + 8 * (is_v ? 2 * j + 1 : p1));
-    return w;
+    w.x[0] = *reinterpret_cast<const uint4*>(row + 8 * (is_v ? 2 * j : own0));
+    w.x[1] = *reinterpret_cast<const uint4*>(row + 8 * (is_v ? 2 * j + 1 : own1));
   };
-
   grid_dependency_wait();
   grid_dependents_launch();
-  const int i0 = threadIdx.x / LR;
-  Row next = ask(i0);
+  Row next;
+  ask(i0, next);
   if ((int)threadIdx.x < mine) {
     const int pos = token_pos[t0 + threadIdx.x];
     pos_of[threadIdx.x] = pos;
@@ -108,21 +101,56 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
   }
   for (int i = threadIdx.x; i < mine * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
-    turn[t][f] = turn_by(token_pos[t0 + t], r.inv_freq[f]);
+    // angle f is number e of its lane: of the pairs 8 j + e, or of the pieces j and j + step with four each
+    int of, e;
+    if (r.interleaved) {
+      const int piece = f >> 2, second = piece >= step;
+      of = piece - second * step;
+      e = 4 * second + (f & 3);
+    } else {
+      of = f >> 3;
+      e = f & 7;
+    }
+    turn[t][2 * ((e >> 1) * step + of) + (e & 1)] = turn_by(token_pos[t0 + t], r.inv_freq[f]);
+  }
+  // the norms' weights, a lane's 16 in a row: 1 without a norm
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const int kind = i / D, at = i % D, piece = at >> 3;
+    const float* norm = kind ? r.k_norm : r.q_norm;
+    const int of = piece < step ? piece : piece < 2 * step ? piece - step : step + ((piece - 2 * step) >> 1);
+    const int second = piece < step ? 0 : piece < 2 * step ? 1 : (piece - 2 * step) & 1;
+    weights[kind][((second * 2 + ((at >> 2) & 1)) * LR + of) * 4 + (at & 3)] = norm ? norm[at] : 1.0f;
   }
   __syncthreads();
 
+  int have = -1;                     // whose weights the registers hold
+  float weight[2][8];
   for (int i = i0; i < rows; i += kRowsAt) {   // (the lanes of a row go together)
-    const Row w = next;
-    next = ask(i + kRowsAt);
-    const int pos = pos_of[w.t];
+    const int kind = next.kind, t = next.t, h = next.h;
+    const uint4 w0 = next.x[0], w1 = next.x[1];
+    ask(i + kRowsAt, next);
+    const bool is_v = kCache && kind == 2;
+    const int p0 = is_v ? 2 * j : own0, p1 = is_v ? 2 * j + 1 : own1;
+    const bool norm = kind == 0 ? r.q_norm != nullptr : !is_v && r.k_norm != nullptr;
+    if (norm && kind != have) {
+      have = kind;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 z = *reinterpret_cast<const float4*>(&weights[kind][(e * LR + j) * 4]);
+        float* to = weight[e >> 1] + 4 * (e & 1);
+        to[0] = z.x, to[1] = z.y, to[2] = z.z, to[3] = z.w;
+      }
+    }
+    const int pos = pos_of[t];
     if (pos < 0) continue;
     float x[2][8];
-    unpack8<DT>(w.x[0], x[0]);
-    unpack8<DT>(w.x[1], x[1]);
-    if (!kCache || w.kind < 2) {
-      const float* weight = w.kind == 0 ? r.q_norm : r.k_norm;
-      if (weight) {
+    uint4 y0 = w0, y1 = w1;
+    if (!is_v || kQuant) {
+      unpack8<DT>(w0, x[0]);
+      unpack8<DT>(w1, x[1]);
+    }
+    if (!is_v) {
+      if (norm) {
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(x[0][e], x[0][e], fmaf(x[1][e], x[1][e], sum));
@@ -130,55 +158,51 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
         for (int d = LR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(mates, sum, d);
         const float inv = 1.0f / sqrtf(sum * (1.0f / D) + r.eps);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float* wp = weight + 8 * (b ? p1 : p0);
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[b][e] *= inv * wp[e];
-        }
+          for (int e = 0; e < 8; ++e) x[b][e] *= inv * weight[b][e];
       }
       if (turns) {
-        if (r.interleaved) {
+        const float4* cs = reinterpret_cast<const float4*>(turn[t]) + j;
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float2* cs = &turn[w.t][4 * (b ? p1 : p0)];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 z = cs[e];
-              const float a = x[b][2 * e], y = x[b][2 * e + 1];
-              x[b][2 * e] = a * z.x - y * z.y;
-              x[b][2 * e + 1] = y * z.x + a * z.y;
-            }
-          }
-        } else {
-          const float2* cs = &turn[w.t][8 * p0];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 z = cs[e];
-            const float a = x[0][e], y = x[1][e];
-            x[0][e] = a * z.x - y * z.y;
-            x[1][e] = y * z.x + a * z.y;
+        for (int e = 0; e < 4; ++e) {
+          const float4 z = cs[e * step];   // angles 2 e and 2 e + 1
+          if (r.interleaved) {
+            float(&u)[8] = x[e >> 1];
+            const int at = 4 * (e & 1);
+            const float a = u[at], b = u[at + 1], d = u[at + 2], f = u[at + 3];
+            u[at] = a * z.x - b * z.y;
+            u[at + 1] = b * z.x + a * z.y;
+            u[at + 2] = d * z.z - f * z.w;
+            u[at + 3] = f * z.z + d * z.w;
+          } else {
+            const float a = x[0][2 * e], b = x[1][2 * e], d = x[0][2 * e + 1], f = x[1][2 * e + 1];
+            x[0][2 * e] = a * z.x - b * z.y;
+            x[1][2 * e] = b * z.x + a * z.y;
+            x[0][2 * e + 1] = d * z.z - f * z.w;
+            x[1][2 * e + 1] = f * z.z + d * z.w;
           }
         }
       }
-    }
-    const bool is_v = kCache && w.kind == 2;
-    const int a0 = is_v ? 2 * j : p0, a1 = is_v ? 2 * j + 1 : p1;
-    const uint4 y0 = is_v ? w.x[0] : pack8<DT>(x[0]), y1 = is_v ? w.x[1] : pack8<DT>(x[1]);
-    const size_t t = (size_t)(t0 + w.t);
-    if (w.kind == 0 || (w.kind == 1 && (!kCache || k_out))) {
-      uint16_t* dst = w.kind == 0 ? q_out + t * r.qo_token + (size_t)w.h * r.qo_head : k_out + t * r.ko_token + (size_t)w.h * r.ko_head;
-      *reinterpret_cast<uint4*>(dst + 8 * a0) = y0;
-      *reinterpret_cast<uint4*>(dst + 8 * a1) = y1;
+      y0 = pack8<DT>(x[0]);
+      y1 = pack8<DT>(x[1]);
+      uint16_t* dst = kind == 0 ? q_out + (size_t)(t0 + t) * r.qo_token + (size_t)h * r.qo_head
+                      : k_out   ? k_out + (size_t)(t0 + t) * r.ko_token + (size_t)h * r.ko_head
+                                : nullptr;
+      if (dst) {
+        *reinterpret_cast<uint4*>(dst + 8 * p0) = y0;
+        *reinterpret_cast<uint4*>(dst + 8 * p1) = y1;
+      }
     }
     if constexpr (kCache) {
-      if (w.kind == 0) continue;
-      const long long page = page_of[w.t];
+      if (kind == 0) continue;
+      const long long page = page_of[t];
       if (page < 0) continue;
       const size_t head = kv_head_bytes(c);
-      uint8_t* base = static_cast<uint8_t*>(is_v ? c.v : c.k) + page + (size_t)w.h * head;
+      uint8_t* base = static_cast<uint8_t*>(is_v ? c.v : c.k) + page + (size_t)h * head;
       const int row = pos & (c.page_size - 1);
       if constexpr (kQuant) {
-        const float inv = kv_inverse(is_v ? c.v_scale : c.k_scale, (size_t)layer * c.n_kv_heads + w.h);
+        const float inv = kv_inverse(is_v ? c.v_scale : c.k_scale, (size_t)layer * c.n_kv_heads + h);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -187,14 +211,14 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
       if constexpr (CT == QRE_E4M3) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          *reinterpret_cast<uint2*>(base + (size_t)row * D + 8 * (b ? a1 : a0)) =
+          *reinterpret_cast<uint2*>(base + (size_t)row * D + 8 * (b ? p1 : p0)) =
               make_uint2(to_e4m3x4(x[b][0], x[b][1], x[b][2], x[b][3]), to_e4m3x4(x[b][4], x[b][5], x[b][6], x[b][7]));
       } else if constexpr (CT == QRE_E2M1) {
         // pieces 2 i and 2 i + 1 are a block: the other piece's largest magnitude comes from the lane that has it
         const float m0 = max_magnitude8(x[0]), m1 = max_magnitude8(x[1]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int other = (b ? a1 : a0) ^ 1;
+          const int at = b ? p1 : p0, other = at ^ 1;
           int from, second;
           if (is_v) {
             from = other >> 1;
@@ -208,14 +232,13 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
           }
           const float o0 = __shfl_sync(mates, m0, from, LR), o1 = __shfl_sync(mates, m1, from, LR);
           const Scale4 s(max_magnitude(b ? m1 : m0, second ? o1 : o0));
-          const int at = b ? a1 : a0;
           *reinterpret_cast<uint32_t*>(base + (size_t)row * (D / 2) + 4 * at) = quantize4(x[b], s);
           if (!(at & 1)) base[(size_t)c.page_size * (D / 2) + (size_t)row * (D / 16) + at / 2] = (uint8_t)s.byte;
         }
       } else {
         uint16_t* dst = reinterpret_cast<uint16_t*>(base) + (size_t)row * D;
-        *reinterpret_cast<uint4*>(dst + 8 * a0) = y0;
-        *reinterpret_cast<uint4*>(dst + 8 * a1) = y1;
+        *reinterpret_cast<uint4*>(dst + 8 * p0) = y0;
+        *reinterpret_cast<uint4*>(dst + 8 * p1) = y1;
       }
     }
   }
@@ -226,16 +249,18 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
 cudaError_t launch_qk_rope(const qre_rope& r, const qre_kv_cache* c, int layer, int n_tokens, const int32_t* token_seq,
                            const int32_t* token_pos, const void* q, const void* k, const void* v, void* q_out, void* k_out,
                            int* status, cudaStream_t stream) {
-  const int rows_of = r.n_heads + r.n_kv_heads * (c ? 2 : 1);
-  // tokens of a CTA: two rounds of rows if there are enough of them to fill the GPU several times over
-  int tokens = 1;
-  // floor(i / rows_of) = umulhi(i, magic) for the rows of a CTA (below 2^15)
-  const uint32_t magic = (uint32_t)((0x100000000ull + rows_of - 1) / rows_of);
+  // Tokens of a CTA: as many as leave every SM a few CTAs (a CTA's first rows wait for its angles; 11,278 tokens of 32
+  // and 8 heads: 91.8 us with one, see above for more).
+  const int sms = device_sm_count();
+  int tokens = sms > 0 ? n_tokens / (8 * sms) : 1;
+  tokens = tokens > kTokens ? kTokens : tokens < 1 ? 1 : tokens;
+  // floor(i / heads) = umulhi(i, magic) for the rows of a CTA (below 2^13)
+  auto magic = [](int heads) { return (uint32_t)((0x100000000ull + heads - 1) / heads); };
   const dim3 grid((unsigned)((n_tokens + tokens - 1) / tokens));
   const qre_kv_cache none = {};
   auto go = [&](auto kernel) {
-    return launch_dependent(kernel, grid, dim3(kThreads), 0, stream, r, c ? *c : none, layer, n_tokens, tokens, magic,
-                            token_seq, token_pos, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+    return launch_dependent(kernel, grid, dim3(kThreads), 0, stream, r, c ? *c : none, layer, n_tokens, tokens,
+                            magic(r.n_heads), magic(r.n_kv_heads), token_seq, token_pos, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                             static_cast<const uint16_t*>(v), static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out),
                             status);
   };
