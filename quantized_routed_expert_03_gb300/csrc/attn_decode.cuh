@@ -66,7 +66,7 @@ namespace {
 constexpr int kWarps = 4;
 // (a 4-bit cache is bound by its conversions' latency more than by the memory: three CTAs where registers last for it)
 constexpr int ctas_per_sm(int cache_type, int head_dim, bool wide) { return cache_type == QRE_E2M1 && !(head_dim == 128 && wide) ? 3 : 2; }
-constexpr int kChunk4 = 32;           // positions of a chunk of a 4-bit cache
+constexpr int kChunk4 = 64;           // positions of a chunk of a 4-bit cache
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk (see Decode)
 constexpr int kRows = 16;             // query heads of a unit at most
@@ -149,6 +149,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t low_half2(uint32_t a) { return h2_as_u32(__low2half2(u32_as_h2(a))); }
+__device__ __forceinline__ uint32_t high_half2(uint32_t a) { return h2_as_u32(__high2half2(u32_as_h2(a))); }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) { return h2_as_u32(__hmul2(u32_as_h2(a), u32_as_h2(b))); }
 // Two E4M3 bytes (low half of b) as an fp16 pair.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t b) {
@@ -171,6 +173,13 @@ struct Decode {
   static constexpr int PR = RB / 16;              // 16-byte pieces of a row
   static constexpr int RI = 32 / PR;              // rows that the warp's 32 lanes fetch at once
   static constexpr int NP = CK / 16;              // runs of 16 positions (each inside one page)
+  static constexpr int SUBS = F4 ? 2 : 1;         // parts of a chunk that are multiplied one after the other (registers)
+  static constexpr int NS = NP / SUBS;
+  // How V of an E2M1 cache is multiplied.  A conversion gives two dimensions of one key; the product wants two keys of
+  // one dimension.  With one block of heads the weights are spread instead, a zero between two: then the two halves are
+  // two steps of the product, and even and odd dimensions are products of their own, twice as many (a quarter of the
+  // conversions' instructions less).  With two blocks the products would bound it; the halves are exchanged.
+  static constexpr bool SPREAD = F4 && NH == 1;
   static constexpr int KS = D / 16;
   static constexpr int PT = BF ? QRE_BF16 : QRE_FP16;
   // Largest sum of a chunk's weights against a standing reference: fp16 weights end at 65504, and values enter
@@ -274,7 +283,7 @@ struct Joined {
                                                float L, float X, uint16_t* o, float* lse, const Own* own) {
     const int reg = slot >> 3, i = (reg >> 2) / NH, high = (reg >> 1) & 1;
     const int r = 8 * ((reg >> 2) % NH) + (reg & 1) + 2 * j;
-    const int d = CT == QRE_E2M1 ? 32 * (i >> 1) + 4 * (slot & 7) + 2 * (i & 1) + high
+    const int d = CT == QRE_E2M1 ? 32 * (i >> 1) + 4 * (slot & 7) + (NH == 1 ? (i & 1) + 2 * high : 2 * (i & 1) + high)
                                  : 16 * i + (CT == QRE_E4M3 ? 2 * (slot & 7) + high : (slot & 7) + 8 * high);
     if (r >= rows) return;
     if (own) {
@@ -491,30 +500,37 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
     }
   };
   to_chunk();
-  long long code_at = 0;             // lane j, E2M1: byte of that run's codes in the pool
-  int load_unit = -1, load_hk = 0;   // KV head of the unit that is fetched
-  int pages = 0;                     // lane j: page of positions 16 j .. 16 j + 15 of that chunk, -1 missing, -2 not seen
+  // E2M1, where the loader's arithmetic counts: what holds for the unit that is fetched
+  long long code_at = 0;             // lane j: byte of run j's codes in the pool
+  Span load_span = {};               // of chunk li
+  int load_jump = -1;                // the chunk behind the hole
+  const int32_t* load_row = nullptr;
+  long long load_head = 0;           // byte of the KV head in page 0
   const size_t head_bytes = (size_t)c.page_size * (K::RB + K::SB);
+  const long long page_bytes = (long long)c.n_kv_heads * (long long)head_bytes;
+  auto enter = [&]() {
+    const Seen<CK, SH> se(sq[lp.t], a.window);
+    load_span = se.span(lp.ck - kUnitCost);
+    if (SH) load_jump = se.before > 0 ? se.before + kUnitCost : -1;
+    load_row = c.page_table + (size_t)sq[lp.t].row * c.max_pages;
+    load_head = (long long)layer * c.n_pages * page_bytes + (long long)(lp.unit / blocks) * (long long)head_bytes;
+  };
+  if constexpr (K::F4)
+    if (li < c1) enter();
+  int pages = 0;                     // lane j: page of positions 16 j .. 16 j + 15 of that chunk, -1 missing, -2 not seen
   auto look_up = [&]() {
     pages = -2;
     if (li < c1 && lane < K::NP) {
-      const Span sp = Seen<CK, SH>(sq[lp.t], a.window).span(lp.ck - kUnitCost);
+      const Span sp = K::F4 ? load_span : Seen<CK, SH>(sq[lp.t], a.window).span(lp.ck - kUnitCost);
       const int pos = sp.pos0 + 16 * lane;
       if (pos < sp.hi && pos + 16 > sp.lo) {
-        pages = c.page_table[(size_t)sq[lp.t].row * c.max_pages + (pos >> ps_shift)];
+        pages = K::F4 ? load_row[pos >> ps_shift] : c.page_table[(size_t)sq[lp.t].row * c.max_pages + (pos >> ps_shift)];
         if (pages < 0 || pages >= c.n_pages) {
           pages = -1;
           set_status(status, QRE_DEV_BAD_INDEX);
         }
       }
-      if constexpr (K::F4) {
-        if (lp.unit != load_unit) {
-          load_unit = lp.unit;
-          load_hk = lp.unit / blocks;
-        }
-        code_at = (((long long)layer * c.n_pages + pages) * c.n_kv_heads + load_hk) * (long long)head_bytes +
-                  (pos & (c.page_size - 1)) * K::RB;
-      }
+      if constexpr (K::F4) code_at = load_head + pages * page_bytes + (pos & (c.page_size - 1)) * K::RB;
     }
   };
   const uint8_t* pool_k = static_cast<const uint8_t*>(c.k);
@@ -522,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   uint32_t missing = 0;              // bit NP * slot + j: run j of that ring slot has no page
   auto fetch = [&](int slot) {       // fetches chunk li into the slot and moves on
     if (li < c1) {
-      const Span sp = Seen<CK, SH>(sq[lp.t], a.window).span(lp.ck - kUnitCost);
+      const Span sp = K::F4 ? load_span : Seen<CK, SH>(sq[lp.t], a.window).span(lp.ck - kUnitCost);
       const int pos0 = sp.pos0, lo = sp.lo, len = sp.hi;
       const uint32_t gone = __ballot_sync(0xffffffffu, pages == -1);
       missing = (missing & ~(((1u << K::NP) - 1u) << (K::NP * slot))) | (gone << (K::NP * slot));
@@ -573,8 +589,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
       }
       ++li;
       if (li < c1) {
-        advance(lp, 1);
-        to_chunk();
+        if (K::F4 && lp.ck + 1 < lp.nch) {
+          if (++lp.ck == load_jump) enter();
+          else load_span.pos0 += CK;
+        } else {
+          advance(lp, 1);
+          to_chunk();
+          if constexpr (K::F4) enter();
+        }
       }
       look_up();
     }
@@ -690,204 +712,233 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
       if (stages == 2) cp_async_wait_group<1>();
       else cp_async_wait_group<2>();
       __syncwarp();
-      const uint32_t kt = smem_addr(ring + (size_t)slot * 2 * K::TILE), vt = kt + K::TILE;
+      const uint32_t tile = smem_addr(ring + (size_t)slot * 2 * K::TILE);
       const int m8 = lane >> 3, l8 = lane & 7;
-
-      // E2M1: the scales of a key's row, shifted so that byte 2 p is that of piece p for this lane's dimensions
-      uint2 ksc[K::F4 ? K::NP : 1][2];
-      auto scale_of = [](const uint2& row, int p) {
-        const uint32_t w = p < 2 ? row.x : row.y;
-        return e4m3x2_to_half2(__byte_perm(w, 0, p & 1 ? 0x4422 : 0x4400) & 0xffffu);
-      };
-      if constexpr (K::F4) {
-#pragma unroll
-        for (int i = 0; i < K::NP; ++i)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const uint32_t at = kt + K::CODES + (16 * i + 8 * b + r4) * K::SB;
-            const uint2 w = K::SB == 8 ? lds64(at) : make_uint2(lds32(at), 0);
-            ksc[i][b] = make_uint2(w.x >> (8 * (j4 >> 1)), w.y >> (8 * (j4 >> 1)));
-          }
-      }
-
-      float s[K::NP][NH][4];
-#pragma unroll
-      for (int i = 0; i < K::NP; ++i) {
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh) s[i][nh][0] = s[i][nh][1] = s[i][nh][2] = s[i][nh][3] = 0.0f;
-        // pieces p and p + 1 of 16 keys: keys 0-7 and 8-15 of each
-#pragma unroll
-        for (int p = 0; p < K::PR; p += 2) {
-          uint32_t x[4];
-          ldmatrix_x4(x, kt + K::at(16 * i + 8 * (m8 & 1) + l8, p + (m8 >> 1)));
-          if constexpr (K::F4) {
-            // a register has 8 codes of key lane / 4 (or 8 more), dimensions 32 p + 8 j and on: two steps of the product
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const uint32_t sa = scale_of(ksc[i][0], p + b), sb = scale_of(ksc[i][1], p + b);
-              uint32_t ya[4], yb[4];
-              e2m1x8_to_half2(x[2 * b], ya);
-              e2m1x8_to_half2(x[2 * b + 1], yb);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t a0 = mul_half2(ya[2 * e], sa), a1 = mul_half2(yb[2 * e], sb);
-                const uint32_t a2 = mul_half2(ya[2 * e + 1], sa), a3 = mul_half2(yb[2 * e + 1], sb);
-#pragma unroll
-                for (int nh = 0; nh < NH; ++nh) mma16816<false>(s[i][nh], a0, a1, a2, a3, qb[2 * (p + b) + e][nh]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh) {
-              if (!K::F8) {
-                mma16816<K::BF>(s[i][nh], x[0], x[1], x[2], x[3], qb[p / 2][nh]);
-              } else {
-                mma16816<false>(s[i][nh], e4m3x2_to_half2(x[0] & 0xffffu), e4m3x2_to_half2(x[1] & 0xffffu),
-                                e4m3x2_to_half2(x[0] >> 16), e4m3x2_to_half2(x[1] >> 16), qb[p][nh]);
-                mma16816<false>(s[i][nh], e4m3x2_to_half2(x[2] & 0xffffu), e4m3x2_to_half2(x[3] & 0xffffu),
-                                e4m3x2_to_half2(x[2] >> 16), e4m3x2_to_half2(x[3] >> 16), qb[p + 1][nh]);
-              }
-            }
-          }
-        }
-      }
-
       const Span sp = seen.span((int)(next - k0));
-      const int pos0 = sp.pos0, lo = sp.lo, len = sp.hi;
       const uint32_t gone = (missing >> (K::NP * slot)) & ((1u << K::NP) - 1u);
-      if (pos0 < lo || pos0 + CK > len || gone) {   // what is not seen: -inf
-#pragma unroll
-        for (int i = 0; i < K::NP; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const int pos = pos0 + 16 * i + 4 * e + r4;
-            if (pos < lo || pos >= len || ((gone >> i) & 1u)) {
-#pragma unroll
-              for (int nh = 0; nh < NH; ++nh) s[i][nh][e] = s[i][nh][e + 1] = -INFINITY;
-            }
-          }
-      }
-      float p[K::NP][NH][4], sum[NH][2];
-      auto weights = [&]() {
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh) {
-          sum[nh][0] = sum[nh][1] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < K::NP; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float mm = m[nh][e & 1];
-              p[i][nh][e] = ex2(fmaf(s[i][nh][e], s2[nh][e & 1], mm == -INFINITY ? 0.0f : -mm));
-              sum[nh][e & 1] += p[i][nh][e];
-            }
-        }
-      };
-      weights();
-      bool redo = false;
-#pragma unroll
-      for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) redo |= m[nh][e] == -INFINITY || sum[nh][e] > K::kMost;
-      if (__any_sync(0xffffffffu, redo)) {   // the reference moves with the maximum so far
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < K::NP; ++i) mx = fmaxf(mx, fmaxf(s[i][nh][e], s[i][nh][e + 2]));
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float to = fmaxf(m[nh][e], mx * s2[nh][e] - K::kUp);
-            const float f = m[nh][e] == to ? 1.0f : ex2(m[nh][e] - to);   // 2^-inf = 0 for the first keys
-            m[nh][e] = to;
-            l[nh][e] *= f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              acc[i][nh][e] *= f;
-              acc[i][nh][e + 2] *= f;
-            }
-          }
-        weights();
-      }
-      // O^T += V^T P^T: the weights are rounded to the products' type (the sum l keeps them in fp32)
-#pragma unroll
-      for (int i = 0; i < K::NP; ++i) {
-        uint32_t pb[NH][2];
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh) {
-          pb[nh][0] = movmatrix(pack2<K::PT>(p[i][nh][0], p[i][nh][1]));
-          pb[nh][1] = movmatrix(pack2<K::PT>(p[i][nh][2], p[i][nh][3]));
-        }
-        // E2M1: the scales of keys 2 j and 2 j + 1 (and of 8 further), a row each
-        uint4 vsc[K::F4 ? 2 : 1];
-        auto pair_scale = [&](const uint4& w, int p) {   // of the piece's dimensions 4 r .. 4 r + 3
-          const uint32_t sel = (uint32_t)(r4 >> 2) * 0x11u + 0x40u + (p & 1 ? 0x22u : 0u);
-          return e4m3x2_to_half2(__byte_perm(p < 2 ? w.x : w.y, p < 2 ? w.z : w.w, sel) & 0xffffu);
+      const bool cut = sp.pos0 < sp.lo || sp.pos0 + CK > sp.hi || gone;
+
+#pragma unroll 1
+      for (int sub = 0; sub < K::SUBS; ++sub) {
+        const uint32_t kt = tile + sub * 16 * K::NS * K::RB, vt = kt + K::TILE;
+        const uint32_t kst = tile + K::CODES + sub * 16 * K::NS * K::SB, vst = kst + K::TILE;
+        // E2M1: the scales of a key's row.  Bytes 2 p and 2 p + 1 are of piece p; a lane's dimensions have one of them
+        uint2 ksc[K::F4 ? K::NS : 1][2];
+        const uint32_t ksel = (uint32_t)(j4 >> 1) * 0x11u + 0x20u;
+        auto scales_of = [&](const uint2& row, int p) {   // of pieces p and p + 1
+          return e4m3x2_to_half2(__byte_perm(p < 2 ? row.x : row.y, 0, ksel) & 0xffffu);
         };
         if constexpr (K::F4) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const uint32_t at = vt + K::CODES + (16 * i + 8 * b + 2 * j4) * K::SB;
-            if (K::SB == 8) {
-              vsc[b] = lds128(at);
-            } else {
-              const uint2 w = lds64(at);
-              vsc[b] = make_uint4(w.x, 0, w.y, 0);
+          for (int i = 0; i < K::NS; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t at = kst + (16 * i + 8 * b + r4) * K::SB;
+              ksc[i][b] = K::SB == 8 ? lds64(at) : make_uint2(lds32(at), 0);
             }
-          }
         }
+
+        float s[K::NS][NH][4];
 #pragma unroll
-        for (int d = 0; d < K::PR; d += 2) {
-          uint32_t x[4];
-          if constexpr (K::F4) {
-            // as for E4M3, with four codes for two values: a register has keys 2 j, 2 j + 1 of dimensions 4 r .. 4 r + 3
-            // of the piece's 32; row r of the first product is dimension 4 r, row r + 8 the next, of the second 4 r + 2, 4 r + 3
-            ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 & 1) + l8, d + (m8 >> 1)));
+        for (int i = 0; i < K::NS; ++i) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t y[2][2][2];   // keys 0-7 or 8-15, product, row r or r + 8
+          for (int nh = 0; nh < NH; ++nh) s[i][nh][0] = s[i][nh][1] = s[i][nh][2] = s[i][nh][3] = 0.0f;
+          // pieces p and p + 1 of 16 keys: keys 0-7 and 8-15 of each
+#pragma unroll
+          for (int p = 0; p < K::PR; p += 2) {
+            uint32_t x[4];
+            ldmatrix_x4(x, kt + K::at(16 * i + 8 * (m8 & 1) + l8, p + (m8 >> 1)));
+            if constexpr (K::F4) {
+              // a register has 8 codes of key lane / 4 (or 8 more), dimensions 32 p + 8 j and on: two steps of the product
+              const uint32_t s0 = scales_of(ksc[i][0], p), s1 = scales_of(ksc[i][1], p);
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                const uint32_t sc = pair_scale(vsc[b], d + e);
-                uint32_t u[4];       // dimensions 4 r, 4 r + 1 and 4 r + 2, 4 r + 3 of key 2 j, then of key 2 j + 1
-                e2m1x8_to_half2(x[2 * e + b], u);
+                // (one half for both: the multiplication takes it so)
+                const uint32_t sa = b ? high_half2(s0) : low_half2(s0), sb = b ? high_half2(s1) : low_half2(s1);
+                uint32_t ya[4], yb[4];
+                e2m1x8_to_half2(x[2 * b], ya);
+                e2m1x8_to_half2(x[2 * b + 1], yb);
 #pragma unroll
-                for (int m2 = 0; m2 < 2; ++m2) {
-                  y[b][m2][0] = mul_half2(__byte_perm(u[m2], u[m2 + 2], 0x5410), sc);
-                  y[b][m2][1] = mul_half2(__byte_perm(u[m2], u[m2 + 2], 0x7632), sc);
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t a0 = mul_half2(ya[2 * e], sa), a1 = mul_half2(yb[2 * e], sb);
+                  const uint32_t a2 = mul_half2(ya[2 * e + 1], sa), a3 = mul_half2(yb[2 * e + 1], sb);
+#pragma unroll
+                  for (int nh = 0; nh < NH; ++nh) mma16816<false>(s[i][nh], a0, a1, a2, a3, qb[2 * (p + b) + e][nh]);
                 }
               }
+            } else {
 #pragma unroll
-              for (int m2 = 0; m2 < 2; ++m2)
-#pragma unroll
-                for (int nh = 0; nh < NH; ++nh)
-                  mma16816<false>(acc[2 * (d + e) + m2][nh], y[0][m2][0], y[0][m2][1], y[1][m2][0], y[1][m2][1], pb[nh]);
-            }
-          } else if (!K::F8) {
-            // 16 dimensions: pieces d and d + 1 of keys 0-7, then of keys 8-15
-            ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 >> 1) + l8, d + (m8 & 1)));
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh) mma16816<K::BF>(acc[d / 2][nh], x[0], x[1], x[2], x[3], pb[nh]);
-          } else {
-            // piece d of keys 0-7 and 8-15, then piece d + 1; a register holds keys 2 j, 2 j + 1 of dimensions
-            // 2 r, 2 r + 1: row r of the product is dimension 2 r, row r + 8 dimension 2 r + 1
-            ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 & 1) + l8, d + (m8 >> 1)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t y0 = __byte_perm(x[2 * e], 0, 0x3120), y1 = __byte_perm(x[2 * e + 1], 0, 0x3120);
-              const uint32_t a0 = e4m3x2_to_half2(y0 & 0xffffu), a1 = e4m3x2_to_half2(y0 >> 16);
-              const uint32_t a2 = e4m3x2_to_half2(y1 & 0xffffu), a3 = e4m3x2_to_half2(y1 >> 16);
-#pragma unroll
-              for (int nh = 0; nh < NH; ++nh) mma16816<false>(acc[d + e][nh], a0, a1, a2, a3, pb[nh]);
+              for (int nh = 0; nh < NH; ++nh) {
+                if (!K::F8) {
+                  mma16816<K::BF>(s[i][nh], x[0], x[1], x[2], x[3], qb[p / 2][nh]);
+                } else {
+                  mma16816<false>(s[i][nh], e4m3x2_to_half2(x[0] & 0xffffu), e4m3x2_to_half2(x[1] & 0xffffu),
+                                  e4m3x2_to_half2(x[0] >> 16), e4m3x2_to_half2(x[1] >> 16), qb[p][nh]);
+                  mma16816<false>(s[i][nh], e4m3x2_to_half2(x[2] & 0xffffu), e4m3x2_to_half2(x[3] & 0xffffu),
+                                  e4m3x2_to_half2(x[2] >> 16), e4m3x2_to_half2(x[3] >> 16), qb[p + 1][nh]);
+                }
+              }
             }
           }
         }
-      }
+
+        if (cut) {                     // what is not seen: -inf
 #pragma unroll
-      for (int nh = 0; nh < NH; ++nh) {
-        l[nh][0] += sum[nh][0];
-        l[nh][1] += sum[nh][1];
+          for (int i = 0; i < K::NS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const int run = sub * K::NS + i, pos = sp.pos0 + 16 * run + 4 * e + r4;
+              if (pos < sp.lo || pos >= sp.hi || ((gone >> run) & 1u)) {
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh) s[i][nh][e] = s[i][nh][e + 1] = -INFINITY;
+              }
+            }
+        }
+        float p[K::NS][NH][4], sum[NH][2];
+        auto weights = [&]() {
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            sum[nh][0] = sum[nh][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < K::NS; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float mm = m[nh][e & 1];
+                p[i][nh][e] = ex2(fmaf(s[i][nh][e], s2[nh][e & 1], mm == -INFINITY ? 0.0f : -mm));
+                sum[nh][e & 1] += p[i][nh][e];
+              }
+          }
+        };
+        weights();
+        bool redo = false;
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) redo |= m[nh][e] == -INFINITY || sum[nh][e] > K::kMost;
+        if (__any_sync(0xffffffffu, redo)) {   // the reference moves with the maximum so far
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < K::NS; ++i) mx = fmaxf(mx, fmaxf(s[i][nh][e], s[i][nh][e + 2]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              const float to = fmaxf(m[nh][e], mx * s2[nh][e] - K::kUp);
+              const float f = m[nh][e] == to ? 1.0f : ex2(m[nh][e] - to);   // 2^-inf = 0 for the first keys
+              m[nh][e] = to;
+              l[nh][e] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                acc[i][nh][e] *= f;
+                acc[i][nh][e + 2] *= f;
+              }
+            }
+          weights();
+        }
+        // O^T += V^T P^T: the weights are rounded to the products' type (the sum l keeps them in fp32)
+#pragma unroll
+        for (int i = 0; i < K::NS; ++i) {
+          uint32_t pb[NH][2];
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            pb[nh][0] = movmatrix(pack2<K::PT>(p[i][nh][0], p[i][nh][1]));
+            pb[nh][1] = movmatrix(pack2<K::PT>(p[i][nh][2], p[i][nh][3]));
+          }
+          uint32_t spread[K::SPREAD ? 2 : 1][2][2];   // [keys 0-7, 8-15][even, odd dimensions]: step 2 j is key 2 j, 2 j + 8 key 2 j + 1
+          if constexpr (K::SPREAD) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              spread[b][0][0] = pb[0][b] & 0xffffu;
+              spread[b][0][1] = pb[0][b] >> 16;
+              spread[b][1][0] = pb[0][b] << 16;
+              spread[b][1][1] = pb[0][b] & 0xffff0000u;
+            }
+          }
+          // E2M1: the scales of keys 2 j and 2 j + 1 (and of 8 further), a row each
+          uint4 vsc[K::F4 ? 2 : 1];
+          auto pair_scale = [&](const uint4& w, int p) {   // of the piece's dimensions 4 r .. 4 r + 3
+            const uint32_t sel = (uint32_t)(r4 >> 2) * 0x11u + 0x40u + (p & 1 ? 0x22u : 0u);
+            return e4m3x2_to_half2(__byte_perm(p < 2 ? w.x : w.y, p < 2 ? w.z : w.w, sel) & 0xffffu);
+          };
+          if constexpr (K::F4) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t at = vst + (16 * i + 8 * b + 2 * j4) * K::SB;
+              if (K::SB == 8) {
+                vsc[b] = lds128(at);
+              } else {
+                const uint2 w = lds64(at);
+                vsc[b] = make_uint4(w.x, 0, w.y, 0);
+              }
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < K::PR; d += 2) {
+            uint32_t x[4];
+            if constexpr (K::F4) {
+              // as for E4M3, with four codes for two values: a register has keys 2 j, 2 j + 1 of dimensions 4 r .. 4 r + 3
+              // of the piece's 32.  Row r of the first product is dimension 4 r, row r + 8 the next, of the second 4 r + 2,
+              // 4 r + 3; with the weights spread 4 r and 4 r + 2 of the first, 4 r + 1 and 4 r + 3 of the second
+              ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 & 1) + l8, d + (m8 >> 1)));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if constexpr (K::SPREAD) {
+#pragma unroll
+                  for (int b = 0; b < 2; ++b) {   // keys 0-7 or 8-15
+                    const uint32_t sc = pair_scale(vsc[b], d + e), s0 = low_half2(sc), s1 = high_half2(sc);
+                    uint32_t u[4];     // dimensions 4 r, 4 r + 1 and 4 r + 2, 4 r + 3 of key 2 j, then of key 2 j + 1
+                    e2m1x8_to_half2(x[2 * e + b], u);
+                    const uint32_t a0 = mul_half2(u[0], s0), a1 = mul_half2(u[1], s0), a2 = mul_half2(u[2], s1), a3 = mul_half2(u[3], s1);
+                    mma16816<false>(acc[2 * (d + e)][0], a0, a1, a2, a3, spread[b][0]);
+                    mma16816<false>(acc[2 * (d + e) + 1][0], a0, a1, a2, a3, spread[b][1]);
+                  }
+                } else {
+                  uint32_t y[2][2][2];   // keys 0-7 or 8-15, product, row r or r + 8
+#pragma unroll
+                  for (int b = 0; b < 2; ++b) {
+                    const uint32_t sc = pair_scale(vsc[b], d + e);
+                    uint32_t u[4];       // dimensions 4 r, 4 r + 1 and 4 r + 2, 4 r + 3 of key 2 j, then of key 2 j + 1
+                    e2m1x8_to_half2(x[2 * e + b], u);
+#pragma unroll
+                    for (int m2 = 0; m2 < 2; ++m2) {
+                      y[b][m2][0] = mul_half2(__byte_perm(u[m2], u[m2 + 2], 0x5410), sc);
+                      y[b][m2][1] = mul_half2(__byte_perm(u[m2], u[m2 + 2], 0x7632), sc);
+                    }
+                  }
+#pragma unroll
+                  for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh)
+                      mma16816<false>(acc[2 * (d + e) + m2][nh], y[0][m2][0], y[0][m2][1], y[1][m2][0], y[1][m2][1], pb[nh]);
+                }
+              }
+            } else if (!K::F8) {
+              // 16 dimensions: pieces d and d + 1 of keys 0-7, then of keys 8-15
+              ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 >> 1) + l8, d + (m8 & 1)));
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma16816<K::BF>(acc[d / 2][nh], x[0], x[1], x[2], x[3], pb[nh]);
+            } else {
+              // piece d of keys 0-7 and 8-15, then piece d + 1; a register holds keys 2 j, 2 j + 1 of dimensions
+              // 2 r, 2 r + 1: row r of the product is dimension 2 r, row r + 8 dimension 2 r + 1
+              ldmatrix_x4_trans(x, vt + K::at(16 * i + 8 * (m8 & 1) + l8, d + (m8 >> 1)));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t y0 = __byte_perm(x[2 * e], 0, 0x3120), y1 = __byte_perm(x[2 * e + 1], 0, 0x3120);
+                const uint32_t a0 = e4m3x2_to_half2(y0 & 0xffffu), a1 = e4m3x2_to_half2(y0 >> 16);
+                const uint32_t a2 = e4m3x2_to_half2(y1 & 0xffffu), a3 = e4m3x2_to_half2(y1 >> 16);
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh) mma16816<false>(acc[d + e][nh], a0, a1, a2, a3, pb[nh]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+          l[nh][0] += sum[nh][0];
+          l[nh][1] += sum[nh][1];
+        }
       }
       slot = slot + 1 == stages ? 0 : slot + 1;
       __syncwarp();
@@ -915,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
           for (int i = 0; i < D / 16; ++i)
 #pragma unroll
             for (int high = 0; high < 2; ++high) {
-              const int d = K::F4 ? 32 * (i >> 1) + 4 * r4 + 2 * (i & 1) + high : 16 * i + (K::F8 ? 2 * r4 + high : r4 + 8 * high);
+              const int d = K::F4 ? 32 * (i >> 1) + 4 * r4 + (K::SPREAD ? (i & 1) + 2 * high : 2 * (i & 1) + high) : 16 * i + (K::F8 ? 2 * r4 + high : r4 + 8 * high);
               out[d] = acc[i][nh][e + 2 * high] * vs;
             }
           if (r4 == 0) own.ml[(size_t)t * a.n_heads + h0 + r] = make_float2(m[nh][e], l[nh][e]);
@@ -942,6 +993,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
               const float(&y)[4] = acc[2 * d + b][nh];
               z[b][0] = movmatrix(pack2<DT>(y[0] * inv[0], y[1] * inv[1]));
               z[b][1] = movmatrix(pack2<DT>(y[2] * inv[0], y[3] * inv[1]));
+            }
+            if (K::SPREAD) {         // b: odd dimensions, the second of each two further: as the others lie
+              const uint32_t w = z[0][1];
+              z[0][1] = z[1][0];
+              z[1][0] = w;
             }
             if (r < rows)
               *reinterpret_cast<uint4*>(out + 32 * d + 8 * j4) =
@@ -1135,9 +1191,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-int decode_grid(const qre_attn& a, const qre_kv_cache& c) {
+int decode_grid(int ctas_sm) {
   const int sms = device_sm_count();
-  const int n = (sms <= 0 ? 152 : sms) * ctas_per_sm(c.dtype, a.head_dim, a.n_heads / a.n_kv_heads > 8);
+  const int n = (sms <= 0 ? 152 : sms) * ctas_sm;
   return n < kMaxCtas ? n : kMaxCtas;
 }
 
@@ -1148,7 +1204,7 @@ int chunk_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? kChunk4 : kTi
 int tile_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? kChunk4 * (c.head_dim / 2 + c.head_dim / kBlock4) : kTile; }
 
 size_t decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n) {
-  const int grid = decode_grid(a, c);
+  const int grid = decode_grid(ctas_per_sm(c.dtype, a.head_dim, a.n_heads / a.n_kv_heads > 8));
   return header_bytes(n) + (size_t)2 * grid * kWarps * kRows * (a.head_dim + 2) * sizeof(float);
 }
 
@@ -1157,12 +1213,15 @@ template <bool SH>
 cudaError_t launch_part(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs, int row0,
                         int max_len, const void* q, void* o, float* lse, const Own& own, void* ws, int* status,
                         cudaStream_t stream) {
-  const int grid = decode_grid(a, c), g = a.n_heads / a.n_kv_heads, ctas_sm = ctas_per_sm(c.dtype, a.head_dim, g > 8);
+  const int g = a.n_heads / a.n_kv_heads;
   const size_t fixed = (size_t)(n + 1) * sizeof(Seq<SH>);
   const int tile = tile_of(c);
   // what the CTAs of an SM share (1 KB of each is the system's, and the kernel's static arrays)
-  const long long room = ((long long)device_max_smem_optin() + 1024) / ctas_sm - 1024 - 256 - (long long)fixed;
-  const int stages = room >= 3ll * kWarps * 2 * tile ? 3 : 2;
+  auto room = [&](int ctas) { return ((long long)device_max_smem_optin() + 1024) / ctas - 1024 - 256 - (long long)fixed; };
+  int ctas_sm = ctas_per_sm(c.dtype, a.head_dim, g > 8);
+  if (room(ctas_sm) < 2ll * kWarps * 2 * tile) ctas_sm = 2;   // calls of many queries
+  const int grid = decode_grid(ctas_sm);
+  const int stages = room(ctas_sm) >= 3ll * kWarps * 2 * tile ? 3 : 2;
   const size_t smem = (size_t)stages * kWarps * 2 * tile + fixed;
   Header* header = static_cast<Header*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + header_bytes(n));
