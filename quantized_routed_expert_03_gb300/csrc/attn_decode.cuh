@@ -210,6 +210,10 @@ struct Own {
   const int2* hole;   // [n]
   float* o;           // [n][n_heads][D]
   float2* ml;         // [n][n_heads]
+  // The launch before this one in the stream computes the holes' positions; this one needs nothing of it, only of the
+  // ones before.  So it begins where SMs are free already, and its first CTA waits for that launch at its end: then
+  // what comes behind this launch comes behind both.
+  int late;
 };
 
 template <bool SH>
@@ -342,8 +346,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   const int units = a.n_kv_heads * blocks;          // units of a sequence
   const int ps_shift = 31 - __clz(c.page_size);
 
-  grid_dependency_wait();
+  // (late: see Own)
+  const bool late = SH && own.late;
+  if (!late) grid_dependency_wait();
   grid_dependents_launch();
+  auto leave = [&]() {
+    if (SH && late && blockIdx.x == 0) grid_dependency_wait();
+  };
 
   // ---- the plan: chunks of every query, summed up
   constexpr int kEach = 4;   // queries of a thread at a time: their loads are in flight together
@@ -442,9 +451,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
     int32_t* firsts = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(header) + kFirstsAt);
     for (int t = tid; t <= n; t += kThreads) firsts[t] = sq[t].first;
   }
-  if (me >= ranges) return;
+  if (me >= ranges) {
+    leave();
+    return;
+  }
   const long long c0 = begin(me), c1 = begin(me + 1);
-  if (c0 >= c1 && !together) return;
+  if (c0 >= c1 && !together) {
+    leave();
+    return;
+  }
 
   if (together && lane == 0) has_part[warp] = 0;
   __syncwarp();
@@ -1045,7 +1060,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  if (!together) return;
+  if (!together) {
+    leave();
+    return;
+  }
   // ---- the shares of the unit meet: those of a CTA in its first warp's ring, then those of the CTAs,
   // each of which finishes some of the outputs
   constexpr int kSlots = 2 * NH * D;   // four outputs each, see Joined
@@ -1092,6 +1110,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   }
   cluster_arrive();   // nobody leaves while its memory is read
   cluster_wait();
+  leave();
 }
 
 // Joins the parts of a unit that was cut, with a running maximum and sum.  A thread

@@ -406,12 +406,13 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
 // ---------------------------------------------------------------- common prefix
 
 // One CTA per group: the first column in which the rows of its sequences' tables differ.  Bound by latency (ids and
-// lengths, then entries): a thread has one of 256 columns and a quarter of the sequences, eight loads on their way.
+// lengths, then entries): a thread has one of 256 columns and a quarter of the sequences, 16 loads on their way; the
+// first columns' entries are asked for beside the lengths.
 __global__ void __launch_bounds__(kThreads) kv_common_len_kernel(const __grid_constant__ qre_kv_cache c, int n,
                                                                  const int32_t* __restrict__ seqs,
                                                                  const int32_t* __restrict__ cu_group,
                                                                  int32_t* __restrict__ common_len, int* status) {
-  constexpr int kCols = 256, kParts = kThreads / kCols, kAhead = 8;
+  constexpr int kCols = 256, kParts = kThreads / kCols, kAhead = 16;
   __shared__ int ids[kKvMaxRequests];
   __shared__ int part[32];
   grid_dependency_wait();
@@ -428,12 +429,11 @@ __global__ void __launch_bounds__(kThreads) kv_common_len_kernel(const __grid_co
     if (threadIdx.x == 0) common_len[blockIdx.x] = 0;
     return;
   }
-  int least = 0x7fffffff, bad = 0;
+  int bad = 0;
   for (int i = threadIdx.x; i < b - a; i += kThreads) {
     const int s = seqs ? seqs[a + i] : a + i;
     ids[i] = s;
-    if (s < 0 || s >= c.max_seqs) bad = 1;
-    else least = min(least, max(c.seq_len[s], 0));
+    bad |= s < 0 || s >= c.max_seqs;
   }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
@@ -442,6 +442,25 @@ __global__ void __launch_bounds__(kThreads) kv_common_len_kernel(const __grid_co
     }
     return;
   }
+  // of column col: whether the first row's page is one, and this thread's rows have it too
+  const int p0 = (int)threadIdx.x / kCols;
+  auto agree = [&](int col) {
+    const int page = c.page_table[(size_t)ids[0] * c.max_pages + col];
+    bool ok = true;
+    for (int i0 = p0; i0 < b - a; i0 += kParts * kAhead) {
+      int x[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        x[e] = i0 + e * kParts < b - a ? c.page_table[(size_t)ids[i0 + e * kParts] * c.max_pages + col] : page;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) ok = ok && x[e] == page;
+    }
+    return ok && page_ok(c, page);
+  };
+  int least = 0x7fffffff;
+  for (int i = threadIdx.x; i < b - a; i += kThreads) least = min(least, max(c.seq_len[ids[i]], 0));
+  const int mine = (int)threadIdx.x % kCols;
+  bool ok = mine < c.max_pages ? agree(mine) : false;
   least = __reduce_min_sync(0xffffffffu, least);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = least;
   __syncthreads();
@@ -450,28 +469,15 @@ __global__ void __launch_bounds__(kThreads) kv_common_len_kernel(const __grid_co
   const int cols = held < c.max_pages ? (int)held : c.max_pages;
   int same = cols;
   for (int c0 = 0; c0 < cols; c0 += kCols) {
-    const int col = c0 + (int)threadIdx.x % kCols, p = (int)threadIdx.x / kCols;
-    int differ = 0x7fffffff;
-    if (col < cols) {
-      const int page = c.page_table[(size_t)ids[0] * c.max_pages + col];
-      bool ok = page_ok(c, page);
-      for (int i0 = p; i0 < b - a; i0 += kParts * kAhead) {
-        int x[kAhead];
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-          x[e] = i0 + e * kParts < b - a ? c.page_table[(size_t)ids[i0 + e * kParts] * c.max_pages + col] : page;
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) ok = ok && x[e] == page;
-      }
-      if (!ok) differ = col;
-    }
-    differ = __reduce_min_sync(0xffffffffu, differ);
+    const int col = c0 + mine;
+    if (c0 > 0) ok = col < cols ? agree(col) : true;
+    const int differ = __reduce_min_sync(0xffffffffu, !ok && col < cols ? col : 0x7fffffff);
     __syncthreads();   // the last step's values have been read
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = differ;
     __syncthreads();
-    differ = __reduce_min_sync(0xffffffffu, part[threadIdx.x & 31]);
-    if (differ < cols) {   // the same in all threads
-      same = differ;
+    const int first = __reduce_min_sync(0xffffffffu, part[threadIdx.x & 31]);
+    if (first < cols) {   // the same in all threads
+      same = first;
       break;
     }
   }

@@ -17,7 +17,7 @@ namespace qre {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 64;    // of a CTA at most
+constexpr int kTokens = 128;   // of a CTA at most: the CTAs of 150,000 rows run at once
 
 template <int RT>
 __global__ void __launch_bounds__(kThreads) kv_write4_kernel(
@@ -204,7 +204,7 @@ struct Cut {
     const int per_token = 2 * c.n_kv_heads * (c.head_dim / kBlock4);   // at most 4096
     const int ctas = device_sm_count() * ctas_per_sm;
     tokens = ctas > 0 ? (n_tokens + ctas - 1) / ctas : 1;
-    tokens = tokens > kTokens ? kTokens : tokens < 1 ? 1 : tokens;     // below 2^18 blocks of a CTA
+    tokens = tokens > kTokens ? kTokens : tokens < 1 ? 1 : tokens;     // at most 2^19 blocks of a CTA: the reciprocal is good to 2^20
     magic = (uint32_t)((0x100000000ull + per_token - 1) / per_token);
     grid = dim3((unsigned)((n_tokens + tokens - 1) / tokens));
   }
