@@ -66,7 +66,7 @@ namespace {
 constexpr int kWarps = 4;
 // (a 4-bit cache is bound by its conversions' latency more than by the memory: three CTAs where registers last for it)
 constexpr int ctas_per_sm(int cache_type, int head_dim, bool wide) { return cache_type == QRE_E2M1 && !(head_dim == 128 && wide) ? 3 : 2; }
-constexpr int kChunk4 = 64;           // positions of a chunk of a 4-bit cache
+constexpr int chunk4(int head_dim) { return head_dim == 64 ? 32 : 64; }   // positions of a chunk of a 4-bit cache
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 4096;           // bytes of K (and of V) in a chunk (see Decode)
 constexpr int kRows = 16;             // query heads of a unit at most
@@ -167,13 +167,13 @@ struct Decode {
   static constexpr bool BF = CT == QRE_BF16;      // type of the products
   static constexpr int RB = F4 ? D / 2 : F8 ? D : 2 * D;   // bytes of a row (of codes)
   static constexpr int SB = F4 ? D / kBlock4 : 0; // bytes of a row's scales, behind the codes of the tile
-  static constexpr int CK = F4 ? kChunk4 : kTile / RB; // positions of a chunk
+  static constexpr int CK = F4 ? chunk4(D) : kTile / RB; // positions of a chunk
   static constexpr int CODES = CK * RB;           // bytes of a tile's rows
   static constexpr int TILE = CODES + CK * SB;
   static constexpr int PR = RB / 16;              // 16-byte pieces of a row
   static constexpr int RI = 32 / PR;              // rows that the warp's 32 lanes fetch at once
   static constexpr int NP = CK / 16;              // runs of 16 positions (each inside one page)
-  static constexpr int SUBS = F4 ? 2 : 1;         // parts of a chunk that are multiplied one after the other (registers)
+  static constexpr int SUBS = F4 ? CK / 32 : 1;        // parts of a chunk that are multiplied one after the other (registers)
   static constexpr int NS = NP / SUBS;
   // How V of an E2M1 cache is multiplied.  A conversion gives two dimensions of one key; the product wants two keys of
   // one dimension.  With one block of heads the weights are spread instead, a zero between two: then the two halves are
@@ -1219,8 +1219,8 @@ int decode_grid(int ctas_sm) {
 size_t header_bytes(int n) { return (kFirstsAt + (size_t)(n + 1) * sizeof(int32_t) + 255) & ~(size_t)255; }
 
 // Positions of a chunk of a cache, and bytes of its tile of K (or of V).
-int chunk_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? kChunk4 : kTile / (c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)); }
-int tile_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? kChunk4 * (c.head_dim / 2 + c.head_dim / kBlock4) : kTile; }
+int chunk_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? chunk4(c.head_dim) : kTile / (c.head_dim * (c.dtype == QRE_E4M3 ? 1 : 2)); }
+int tile_of(const qre_kv_cache& c) { return c.dtype == QRE_E2M1 ? chunk4(c.head_dim) * (c.head_dim / 2 + c.head_dim / kBlock4) : kTile; }
 
 size_t decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n) {
   const int grid = decode_grid(ctas_per_sm(c.dtype, a.head_dim, a.n_heads / a.n_kv_heads > 8));
