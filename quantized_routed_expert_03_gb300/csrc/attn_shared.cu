@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
   uint64_t* s_full = q_free + 1;             // [2]
   uint64_t* p_full = s_full + 2;             // [2]
   uint64_t* o_done = p_full + 2;             // [2]
-  uint64_t* drain = o_done + 2;              // [2]
+  uint64_t* turn = o_done + 2;               // [2]
+  uint64_t* drain = turn + 2;                // [2]
   float* row_scale = reinterpret_cast<float*>(drain + 2);   // [2][kM]: factor of a row's scores
   uint32_t* tmem_p = reinterpret_cast<uint32_t*>(row_scale + 2 * kM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_p + 1);   // a wait gave up
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
+      mbar_init(&turn[t], 1);
       mbar_init(&drain[t], 1);
     }
     *abort_flag = 0;
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
       const uint32_t id_o = (P::BF ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + kS + t * kChain, td = tm + kO + t * kChain;
       const uint64_t kd = umma_desc_sw128(smem_addr(skv)), vd = umma_desc_sw128_mn(smem_addr(skv), P::HALF);
-      int i0 = 0, np = 0, n = 0;       // ring tiles, pieces, key tiles of this chain so far
+      int i0 = 0, np = 0, n = 0, turns = 0;   // ring tiles, pieces, key tiles and turns of this chain so far
       bool ok = true;
       auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
       for (bool dry = true; ok; dry = false) {
@@ -527,33 +529,52 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           ok = wait_for(q_full, np);
           ++np;
         }
-        bool begun = false;
-        for (int j = 0; ok && j < w.tiles; ++j) {
-          const int ik = i0 + 2 * j, iv = ik + 1;
-          if (!both && (j & 1) != t) {   // the other chain's
-            ok = wait_tile(ik) && wait_tile(iv);
-            if (ok && lead) {
-              mbar_arrive(&empty[ik % P::SLOTS]);
-              mbar_arrive(&empty[iv % P::SLOTS]);
-            }
-            __syncwarp();
-            continue;
+        // Steps of a chain: P V of a tile and the scores of its next one.  The chains take them in turn, 0 first: left to
+        // themselves they fall into step, both softmaxes run at once, and the tensor cores wait (3600 cycles a tile).  The
+        // turn is handed over where the other chain has a step next; it has as many as this one, or chain 1 one less.
+        const int first = dry ? 0 : w.first(t), step = dry ? 1 : w.step(), count = dry ? 1 : w.count(t), other = dry ? 0 : w.count(t ^ 1);
+        auto pass_by = [&](int j) {      // the other chain's tile: not read here
+          ok = wait_tile(i0 + 2 * j) && wait_tile(i0 + 2 * j + 1);
+          if (ok && lead) {
+            mbar_arrive(&empty[(i0 + 2 * j) % P::SLOTS]);
+            mbar_arrive(&empty[(i0 + 2 * j + 1) % P::SLOTS]);
           }
-          ok = dry || wait_tile(ik);
-          if (!ok) break;
-          tc_fence_after();
-          scores(ik);                  // over P of the tile before: issued behind the product that reads it
+          __syncwarp();
+        };
+        if (!both)
+          for (int j = 0; ok && j < first && j < w.tiles; ++j) pass_by(j);
+        if (ok && count > 0) {
+          ok = dry || wait_tile(i0 + 2 * first);
+          if (ok) {
+            tc_fence_after();
+            scores(i0 + 2 * first);
+          }
+        }
+        for (int k = 0; ok && k < count; ++k) {
+          const int j = first + k * step, iv = i0 + 2 * j + 1;
           ok = dry || (wait_tile(iv) && wait_for(&p_full[t], n));
+          if (ok && !dry && (t ? true : k > 0)) {   // (chain 1 has had a step before each of chain 0's but the first)
+            ok = wait_for(&turn[t], turns);
+            ++turns;
+          }
           if (!ok) break;
           tc_fence_after();
           const uint64_t v0 = vd + (uint32_t)(iv % P::SLOTS) * (P::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < kN / 16; ++k)   // O += P V_j
-            umma_f16_tmem_a_lead(td, ts + 8 * k, v0 + k * (2048 >> 4), id_o, begun || k ? 1u : 0u, lead);
+          for (int e = 0; e < kN / 16; ++e)   // O += P V_j
+            umma_f16_tmem_a_lead(td, ts + 8 * e, v0 + e * (2048 >> 4), id_o, k || e ? 1u : 0u, lead);
           umma_commit_lead(&o_done[t], lead);
           umma_commit_lead(&empty[iv % P::SLOTS], lead);
-          begun = true;
           n += !dry;
+          if (!both && j + 1 < w.tiles) pass_by(j + 1);
+          if (ok && k + 1 < count) {     // over P: issued behind the product that reads it
+            ok = wait_tile(i0 + 2 * (j + step));
+            if (!ok) break;
+            tc_fence_after();
+            scores(i0 + 2 * (j + step));
+          }
+          if (ok && lead && (t ? k + 1 < other : k < other)) mbar_arrive(&turn[t ^ 1]);
+          __syncwarp();
         }
         if (!dry) i0 += 2 * w.tiles;
       }
@@ -652,21 +673,25 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
         const float ks = base * (P::LOW && c.k_scale ? c.k_scale[(size_t)layer * c.n_kv_heads + w.hk] : 1.0f);
         const int rows = w.both() ? 2 * kM : kM, p = lane % LR;
         const uint32_t at = smem_addr(sq) + (p / 8) * P::HALF;
-        // (loops that are not unrolled: this code is cold, and fetching it took 26,000 cycles)
-        constexpr int kStep = 8 * (32 / LR);
+        // (loops that are hardly unrolled: this code is cold, and fetching it took 26,000 cycles)
+        constexpr int kStep = 8 * (32 / LR);   // rows of all warps at a time
         const int r_first = warp * (32 / LR) + lane / LR, di = kStep / g, dh = kStep - di * g;
-        int i = (w.rows0 + r_first) / g, h = w.rows0 + r_first - i * g;
-#pragma unroll 1
+        const int i_first = (w.rows0 + r_first) / g;
+        int h = w.rows0 + r_first - i_first * g;
+        const long long by = di * a.q_token + dh * a.q_head, carry = a.q_token - g * a.q_head;
+        const uint16_t* from = q + (w.c0 + i_first) * a.q_token + (w.hk * g + h) * a.q_head + 8 * p;
+        uint32_t to = at + r_first * 128 + 16 * ((p % 8) ^ (r_first & 7));   // (kStep is a multiple of 8)
+#pragma unroll 2
         for (int r = r_first; r < rows; r += kStep) {
-          const bool there = r < w.rows;
-          const uint16_t* from = q + (there ? (size_t)(w.c0 + i) * a.q_token + (size_t)(w.hk * g + h) * a.q_head + 8 * p : 0);
-          cp_async_16_zfill(at + r / kM * P::TILE + r % kM * 128 + 16 * ((p % 8) ^ (r & 7)), from, there);
+          if (r - kM >= 0 && r - kM < kStep) to += P::TILE - P::HALF;   // into the second tile (its rows follow on the first's)
+          cp_async_16_zfill(to, r < w.rows ? from : q, r < w.rows);
           if (p == 0 && !(P::LOW && DT == QRE_BF16)) row_scale[r] = ks;
-          i += di;
+          to += kStep * 128;
+          from += by;
           h += dh;
           if (h >= g) {
             h -= g;
-            ++i;
+            from += carry;
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -674,7 +699,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           // to fp16: the largest element of a row to [2^14, 2^15): exact but for elements 2^-29 times smaller, which
           // round to 2^-39 of it
           __syncwarp();
-#pragma unroll 1
+#pragma unroll 4
           for (int r = r_first; r < rows; r += kStep) {
             uint4* word = reinterpret_cast<uint4*>(sq + (p / 8) * P::HALF + r / kM * P::TILE + r % kM * 128 + 16 * ((p % 8) ^ (r & 7)));
             float y[8];
