@@ -706,11 +706,12 @@ QRE_API qre_status qre_attn_decode_shared_workspace_size(const qre_attn* attn, c
  * are joined in fp32.  Arguments, results and limits are those of qre_attn_decode;
  * groups and common_len as qre_kv_common_len takes and gives them (a queries' group
  * is that of its place in the list, every query is in one group).  How much of a
- * common prefix is read together is the library's choice.  A common_len that is
- * negative or beyond a sequence's length counts as 0 for its group, and a query that
- * is in no group, or whose group's bounds are bad, is computed by itself, both with
- * QRE_DEV_BAD_INDEX; one that claims more than the sequences have in common gives
- * the attention to the first sequence's pages.
+ * common prefix is read together is the library's choice; where max_len says that
+ * all sequences are short, nothing is, and the groups are not looked at.  Else a
+ * common_len that is negative or beyond a sequence's length counts as 0 for its
+ * group, and with bounds that are not ascending from 0 to n each query is computed by
+ * itself, both with QRE_DEV_BAD_INDEX.  A common_len that claims more than the
+ * sequences have in common gives the attention to the first sequence's pages.
  *   max_len  host: an upper bound of the lengths, 0 if not known; a wrong one costs
  *            time and nothing else
  */

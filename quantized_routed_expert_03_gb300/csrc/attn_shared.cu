@@ -91,6 +91,7 @@ int shared_grid() {
   return sms <= 0 ? 152 : sms;
 }
 
+constexpr long long kWorthBytes = 200000000;   // see launch_attn_decode_shared
 constexpr int kPartQueries = 1024;   // of a launch of the decode kernel: it keeps 24 bytes of each in shared memory
 
 Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, void* ws) {
@@ -113,7 +114,7 @@ Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, vo
   s.own_ml = reinterpret_cast<float2*>(take(heads * sizeof(float2)));
   s.part_o = reinterpret_cast<float*>(take(rows * a.head_dim * sizeof(float)));
   s.part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
-  s.decode = take(decode_ws_bytes(a, c, n < kPartQueries ? n : kPartQueries));
+  s.decode = take(decode_ws_bytes(a, c, n));
   s.bytes = at;
   return s;
 }
@@ -492,9 +493,11 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
       }
     } else if (warp == P::kMma || warp == P::kMma + 1) {
       // ---- products: the whole warp, so that the operands stay in uniform registers; a chain each
-      const int t = warp - P::kMma;
-      const uint32_t elected = elect_lane();
-      uint32_t lead = 0;               // the first round is for the instruction cache: nobody issues anything
+      // (what an MMA takes comes out of a shuffle from lane 0, so that the compiler knows it is the warp's: as each lane's
+      // own it moves to the uniform registers anew for every MMA, and one takes some 110 cycles to issue, not 64)
+      auto of_warp = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const int t = of_warp(warp - P::kMma);
+      const uint32_t lead = elect_lane();
       const uint32_t id_s = P::BF ? umma_idesc_bf16(kM, kN) : umma_idesc_f16(kM, kN);
       const uint32_t id_o = (P::BF ? umma_idesc_bf16(kM, D) : umma_idesc_f16(kM, D)) | kUmmaBMnMajor;
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + kS + t * kChain, td = tm + kO + t * kChain;
@@ -502,37 +505,27 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
       int i0 = 0, np = 0, n = 0, turns = 0;   // ring tiles, pieces, key tiles and turns of this chain so far
       bool ok = true;
       auto wait_tile = [&](int i) { return wait_for(&full[i % P::SLOTS], i / P::SLOTS); };
-      for (bool dry = true; ok; dry = false) {
-        if (dry) {
-          w.rows = 2 * kM;
-          w.tiles = 1;
-        } else {
-          if (np == 0) {
-            begin();
-            lead = elected;
-          }
-          if (!pieces.next(w)) break;
-        }
+      begin();
+      while (ok && pieces.next(w)) {
         const bool both = w.both();
-        const uint64_t qd = umma_desc_sw128(smem_addr(sq + (both ? t : 0) * P::TILE));
+        const uint64_t qd = umma_desc_sw128(smem_addr(sq) + (uint32_t)of_warp(both ? t : 0) * P::TILE);
         auto scores = [&](int i) {     // S = Q K_j^T
-          const uint64_t k0 = kd + (uint32_t)(i % P::SLOTS) * (P::TILE >> 4);
+          const int slot = of_warp(i % P::SLOTS);
+          const uint64_t k0 = kd + (uint32_t)slot * (P::TILE >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k / 4) * P::HALF + (k % 4) * 32) >> 4;
             umma_f16_lead(ts, qd + off, k0 + off, id_s, k ? 1u : 0u, lead);
           }
           umma_commit_lead(&s_full[t], lead);
-          umma_commit_lead(&empty[i % P::SLOTS], lead);
+          umma_commit_lead(&empty[slot], lead);
         };
-        if (!dry) {
-          ok = wait_for(q_full, np);
-          ++np;
-        }
+        ok = wait_for(q_full, np);
+        ++np;
         // Steps of a chain: P V of a tile and the scores of its next one.  The chains take them in turn, 0 first: left to
         // themselves they fall into step, both softmaxes run at once, and the tensor cores wait (3600 cycles a tile).  The
         // turn is handed over where the other chain has a step next; it has as many as this one, or chain 1 one less.
-        const int first = dry ? 0 : w.first(t), step = dry ? 1 : w.step(), count = dry ? 1 : w.count(t), other = dry ? 0 : w.count(t ^ 1);
+        const int first = w.first(t), step = w.step(), count = w.count(t), other = w.count(t ^ 1);
         auto pass_by = [&](int j) {      // the other chain's tile: not read here
           ok = wait_tile(i0 + 2 * j) && wait_tile(i0 + 2 * j + 1);
           if (ok && lead) {
@@ -544,7 +537,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
         if (!both)
           for (int j = 0; ok && j < first && j < w.tiles; ++j) pass_by(j);
         if (ok && count > 0) {
-          ok = dry || wait_tile(i0 + 2 * first);
+          ok = wait_tile(i0 + 2 * first);
           if (ok) {
             tc_fence_after();
             scores(i0 + 2 * first);
@@ -552,20 +545,23 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
         }
         for (int k = 0; ok && k < count; ++k) {
           const int j = first + k * step, iv = i0 + 2 * j + 1;
-          ok = dry || (wait_tile(iv) && wait_for(&p_full[t], n));
-          if (ok && !dry && (t ? true : k > 0)) {   // (chain 1 has had a step before each of chain 0's but the first)
+          ok = wait_tile(iv) && wait_for(&p_full[t], n);
+          if (ok && (t || k > 0)) {   // (chain 1 has had a step before each of chain 0's but the first)
             ok = wait_for(&turn[t], turns);
             ++turns;
           }
           if (!ok) break;
           tc_fence_after();
-          const uint64_t v0 = vd + (uint32_t)(iv % P::SLOTS) * (P::TILE >> 4);
+          const int slot = of_warp(iv % P::SLOTS);
+          const uint64_t v0 = vd + (uint32_t)slot * (P::TILE >> 4);
 #pragma unroll
           for (int e = 0; e < kN / 16; ++e)   // O += P V_j
             umma_f16_tmem_a_lead(td, ts + 8 * e, v0 + e * (2048 >> 4), id_o, k || e ? 1u : 0u, lead);
           umma_commit_lead(&o_done[t], lead);
-          umma_commit_lead(&empty[iv % P::SLOTS], lead);
-          n += !dry;
+          umma_commit_lead(&empty[slot], lead);
+          ++n;
+          if (lead && (t ? k + 1 < other : k < other)) mbar_arrive(&turn[t ^ 1]);
+          __syncwarp();
           if (!both && j + 1 < w.tiles) pass_by(j + 1);
           if (ok && k + 1 < count) {     // over P: issued behind the product that reads it
             ok = wait_tile(i0 + 2 * (j + step));
@@ -573,10 +569,8 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             tc_fence_after();
             scores(i0 + 2 * (j + step));
           }
-          if (ok && lead && (t ? k + 1 < other : k < other)) mbar_arrive(&turn[t ^ 1]);
-          __syncwarp();
         }
-        if (!dry) i0 += 2 * w.tiles;
+        i0 += 2 * w.tiles;
       }
     }
   } else if (warp >= P::kWiden) {
@@ -655,17 +649,9 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
     const float base = a.scale * kLog2e;
     int np = 0, cnt = 0;             // pieces, key tiles of this chain so far
     bool ok = true;
-    // The first round is for the instruction cache: it does a tile on what lies in tensor memory while the kernels before
-    // this one end (cold, the first tile took 8700 cycles, not 1500), and leaves nothing.
-    for (bool dry = true; ok; dry = false) {
-      if (dry) {
-        w.rows = 2 * kM;
-        w.tiles = 1;
-        w.pos0 = 0;
-        w.hb = kN;
-      } else {
-        if (np == 0) begin();
-        if (!pieces.next(w)) break;
+    begin();
+    while (ok && pieces.next(w)) {
+      {
         // the queries: 16 or 8 lanes a row, all eight warps both tiles
         if (np > 0) ok = wait_for(q_free, np - 1);   // all rows of the piece before have seen their last scores
         if (!ok) break;
@@ -699,23 +685,43 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           // to fp16: the largest element of a row to [2^14, 2^15): exact but for elements 2^-29 times smaller, which
           // round to 2^-39 of it
           __syncwarp();
-#pragma unroll 4
-          for (int r = r_first; r < rows; r += kStep) {
-            uint4* word = reinterpret_cast<uint4*>(sq + (p / 8) * P::HALF + r / kM * P::TILE + r % kM * 128 + 16 * ((p % 8) ^ (r & 7)));
-            float y[8];
-            unpack8<DT>(*word, y);
-            float big = 0.0f;
+          constexpr int kAhead = 4;  // rows of a lane at a time (rows is a multiple of kAhead * kStep)
+          uint8_t* line = sq + (p / 8) * P::HALF + 16 * ((p % 8) ^ (r_first & 7));
+#pragma unroll 1
+          for (int r0 = r_first; r0 < rows; r0 += kAhead * kStep) {
+            uint4* word[kAhead];
+            uint4 x[kAhead];
+            float big[kAhead];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(y[e]));
+            for (int u = 0; u < kAhead; ++u) {
+              const int r = r0 + u * kStep;
+              word[u] = reinterpret_cast<uint4*>(line + r / kM * P::TILE + r % kM * 128);
+              x[u] = *word[u];
+            }
 #pragma unroll
-            for (int d = LR / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-            const int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
-            const int up = e >= 128 || big == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
-            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+            for (int u = 0; u < kAhead; ++u) {
+              float y[8];
+              unpack8<DT>(x[u], y);
+              big[u] = 0.0f;
 #pragma unroll
-            for (int e2 = 0; e2 < 8; ++e2) y[e2] *= f;
-            *word = pack8<QRE_FP16>(y);
-            if (p == 0) row_scale[r] = ks * __uint_as_float((uint32_t)(127 - up) << 23);
+              for (int e = 0; e < 8; ++e) big[u] = fmaxf(big[u], fabsf(y[e]));
+            }
+#pragma unroll
+            for (int d = LR / 2; d > 0; d >>= 1)
+#pragma unroll
+              for (int u = 0; u < kAhead; ++u) big[u] = fmaxf(big[u], __shfl_xor_sync(0xffffffffu, big[u], d));
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+              const int e = (int)((__float_as_uint(big[u]) >> 23) & 255) - 127;
+              const int up = e >= 128 || big[u] == 0.0f ? 0 : (14 - e < 126 ? 14 - e : 126);
+              const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+              float y[8];
+              unpack8<DT>(x[u], y);
+#pragma unroll
+              for (int e2 = 0; e2 < 8; ++e2) y[e2] *= f;
+              *word[u] = pack8<QRE_FP16>(y);
+              if (p == 0) row_scale[r0 + u * kStep] = ks * __uint_as_float((uint32_t)(127 - up) << 23);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -730,10 +736,10 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
       const bool idle = 32 * (warp & 3) >= valid;   // rows that do not exist: whatever P holds stays in their own O
       float m = -INFINITY, l = 0.0f;                // reference (base 2) and sum
       const int tiles = w.count(t);
-      for (int jj = 0; jj < tiles; ++jj, cnt += !dry) {
+      for (int jj = 0; jj < tiles; ++jj, ++cnt) {
         const int j = w.first(t) + jj * w.step();
         const int seen = w.hb - (w.pos0 + j * kN);   // keys of the tile
-        ok = dry || wait_for(&s_full[t], cnt);
+        ok = wait_for(&s_full[t], cnt);
         if (!ok) break;
         if (!idle) {
           tc_fence_after();
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           }
           uint32_t p[64];
           float sum;
-          // Once, or again with the reference moved (one copy of the code: it is cold at the first tile)
+          // Once, or again with the reference moved
 #pragma unroll 1
           for (bool moved = false;; moved = true) {
             const float off = m == -INFINITY ? 0.0f : -m;
@@ -813,16 +819,16 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0 && !dry) mbar_arrive(&p_full[t]);
+        if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0 && !dry) mbar_arrive(q_free);
+      if (lane == 0) mbar_arrive(q_free);
       // the part: O, reference and sum
-      if (tiles > 0 && !dry) ok = wait_for(&o_done[t], cnt - 1);
+      if (tiles > 0) ok = wait_for(&o_done[t], cnt - 1);
       if (!ok) break;
       if (!idle) {
-        const long long at = (dry ? 0 : w.out) + (w.both() ? t * kM : t * w.rows) + row;
+        const long long at = w.out + (w.both() ? t * kM : t * w.rows) + row;
         if (tiles > 0) {
           tc_fence_after();
 #pragma unroll 1
@@ -830,7 +836,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             uint32_t x[32];
             tmem_ld_32x32b_x32(oc + 32 * b, x);
             tmem_ld_wait();
-            if (row < valid && !dry) {
+            if (row < valid) {
               float* out = space.part_o + (size_t)at * D + 32 * b;
 #pragma unroll
               for (int e = 0; e < 32; e += 8) st_global_32(out + e, x + e);
@@ -838,7 +844,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           }
           tc_fence_before();
         }
-        if (row < valid && !dry) space.part_ml[at] = make_float2(m, l);   // without tiles: -inf, and O is not read
+        if (row < valid) space.part_ml[at] = make_float2(m, l);   // without tiles: -inf, and O is not read
       }
       __syncwarp();
     }
@@ -910,10 +916,27 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
 #pragma unroll
     for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : own[e];
   }
-  for (int i0 = 0; i0 < parts; i0 += 32) {   // a lane has a part's reference and sum
-    const int mine = parts - i0 < 32 ? parts - i0 : 32;
+  constexpr int kAhead = 16;         // parts whose O is on its way together
+  for (int i0 = 0; i0 < parts; i0 += kAhead) {   // a lane has a part's reference and sum
+    const int mine = parts - i0 < kAhead ? parts - i0 : kAhead;
     float2 ml = make_float2(-INFINITY, 0.0f);
     if (lane < mine) ml = s.part_ml[row_of(i0 + lane)];
+    float y[kAhead][E];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
+      if (u < mine) {
+        const float* from = s.part_o + (size_t)row_of(i0 + u) * D + E * lane;
+        if (E == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(from);
+          y[u][0] = z.x, y[u][1] = z.y, y[u][E - 2] = z.z, y[u][E - 1] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(from);
+          y[u][0] = z.x, y[u][1] = z.y;
+        }
+      }
+    }
     const bool empty = ml.x == -INFINITY && ml.y == 0.0f;   // saw nothing: its O was not written
     float to = ml.x;
 #pragma unroll
@@ -925,34 +948,15 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     M = to;
     L = L * f + sum;
+    const uint32_t there = __ballot_sync(0xffffffffu, !empty);
 #pragma unroll
     for (int e = 0; e < E; ++e) X[e] *= f;
-    const uint32_t there = __ballot_sync(0xffffffffu, lane < mine && !empty);
-    constexpr int kAhead = 8;
-    for (int k0 = 0; k0 < mine; k0 += kAhead) {
-      float y[kAhead][E];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
+      const float w = __shfl_sync(0xffffffffu, fe, u) * vs;
+      if ((there >> u) & 1u)
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
-        if (k0 + u < mine && ((there >> (k0 + u)) & 1u)) {
-          const float* from = s.part_o + (size_t)row_of(i0 + k0 + u) * D + E * lane;
-          if (E == 4) {
-            const float4 z = *reinterpret_cast<const float4*>(from);
-            y[u][0] = z.x, y[u][1] = z.y, y[u][E - 2] = z.z, y[u][E - 1] = z.w;
-          } else {
-            const float2 z = *reinterpret_cast<const float2*>(from);
-            y[u][0] = z.x, y[u][1] = z.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const float w = __shfl_sync(0xffffffffu, fe, (k0 + u) & 31) * vs;
-        if (k0 + u < mine && ((there >> (k0 + u)) & 1u))
-#pragma unroll
-          for (int e = 0; e < E; ++e) X[e] = fmaf(y[u][e], w, X[e]);
-      }
+        for (int e = 0; e < E; ++e) X[e] = fmaf(y[u][e], w, X[e]);
     }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -974,6 +978,14 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
                                       int n_groups, const int32_t* cu_group, const int32_t* common_len, int max_len,
                                       const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream) {
   const Space s = space_of(a, c, n, n_groups, ws);
+  // A prefix that is read again and again comes from L2, at some 11 TB/s; sharing costs launches, a join and the plan.  By
+  // themselves / shared, us, for one group (8 KV heads of 128, 16 bits): 64 sequences of 612 positions 25 / 31, of 2148
+  // 61 / 32; 16 of 2148 25 / 29, of 8292 63 / 43; 4 of 8292 26 / 35, of 32,868 62 / 54; 2 of 32,868 41 / 52.  In 4 bits: 16
+  // of 2148 25 / 26, of 8292 46 / 40; 64 of 612 24 / 34, of 2148 44 / 35.  So it goes by the bytes that sharing can save;
+  // those of 4 bits take longer.
+  const long long all = 2ll * c.n_kv_heads * (long long)(kv_head_bytes(c) / c.page_size) * max_len;
+  const long long saved = (c.dtype == QRE_E2M1 ? all * 3 / 2 : all) * (n > n_groups ? n - n_groups : 0);
+  if (max_len > 0 && saved < kWorthBytes) return launch_attn_decode(a, c, layer, n, seqs, max_len, q, o, lse, s.decode, status, stream);
   const int g = a.n_heads / a.n_kv_heads, box = c.page_size < kN ? c.page_size : kN, grid = shared_grid();
   const bool low = c.dtype == QRE_E4M3 || c.dtype == QRE_E2M1;
   CUtensorMap tk = {}, tv = {}, tk16 = {}, tv16 = {};
