@@ -107,8 +107,9 @@ _lib = None
 
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _SHAPE = ctypes.POINTER(qre_layer_shape)
-_KV, _ATTN, _ROWS = ctypes.POINTER(qre_kv_cache), ctypes.POINTER(qre_attn), ctypes.POINTER(qre_kv_rows)
-_ROPE = ctypes.POINTER(qre_rope)
+# The descriptors of the cache and attention calls go by address (_at): a call of the smallest sizes is bound by what the
+# binding does, and a typed pointer costs it 0.5 us.
+_KV = _ATTN = _ROWS = _ROPE = ctypes.c_void_p
 _SIGS = {
     "qre_last_error": ([], ctypes.c_char_p),
     "qre_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -174,11 +175,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    # (most are tensors, and a call has seven or more: asking for the type first would take as long as the address)
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
 
 
 _current_stream = None
@@ -198,8 +201,15 @@ def _stream(s):
     return s.cuda_stream
 
 
+def _at(desc, kind):
+    """Address of a descriptor of the cache and attention calls."""
+    if type(desc) is not kind:
+        raise TypeError(f"expected a {kind.__name__}, not {type(desc).__name__}")
+    return ctypes.addressof(desc)
+
+
 def _check(status: int, where: str) -> None:
-    if status != QRE_OK:
+    if status:
         raise QreError(status, where, load_library().qre_last_error().decode())
 
 
@@ -394,52 +404,52 @@ def make_attn(n_heads, n_kv_heads, head_dim, dtype, scale, causal=True, window=0
 
 def qre_kv_workspace_size(cache: qre_kv_cache) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().qre_kv_workspace_size(ctypes.byref(cache), ctypes.byref(out)), "qre_kv_workspace_size")
+    _check(load_library().qre_kv_workspace_size(_at(cache, qre_kv_cache), ctypes.byref(out)), "qre_kv_workspace_size")
     return out.value
 
 
 def qre_kv_reserve(cache, n, seqs, n_new, workspace, workspace_bytes=None, stream=None) -> None:
-    _check(load_library().qre_kv_reserve(ctypes.byref(cache), n, _ptr(seqs), _ptr(n_new), _ptr(workspace),
+    _check(load_library().qre_kv_reserve(_at(cache, qre_kv_cache), n, _ptr(seqs), _ptr(n_new), _ptr(workspace),
                                          _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_kv_reserve")
 
 
 def qre_kv_write(cache, layer, rows, n_tokens, token_seq, token_pos, k, v, stream=None) -> None:
-    _check(load_library().qre_kv_write(ctypes.byref(cache), layer, ctypes.byref(rows), n_tokens, _ptr(token_seq),
+    _check(load_library().qre_kv_write(_at(cache, qre_kv_cache), layer, _at(rows, qre_kv_rows), n_tokens, _ptr(token_seq),
                                        _ptr(token_pos), _ptr(k), _ptr(v), _stream(stream)), "qre_kv_write")
 
 
 def qre_kv_fork(cache, n, src, dst, workspace, workspace_bytes=None, stream=None) -> None:
-    _check(load_library().qre_kv_fork(ctypes.byref(cache), n, _ptr(src), _ptr(dst), _ptr(workspace),
+    _check(load_library().qre_kv_fork(_at(cache, qre_kv_cache), n, _ptr(src), _ptr(dst), _ptr(workspace),
                                       _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_kv_fork")
 
 
 def qre_kv_free(cache, n, seqs, stream=None) -> None:
-    _check(load_library().qre_kv_free(ctypes.byref(cache), n, _ptr(seqs), _stream(stream)), "qre_kv_free")
+    _check(load_library().qre_kv_free(_at(cache, qre_kv_cache), n, _ptr(seqs), _stream(stream)), "qre_kv_free")
 
 
 def qre_kv_compact(cache, page_table_out, ref_count_out, n_live, workspace, workspace_bytes=None,
                    stream=None) -> None:
-    _check(load_library().qre_kv_compact(ctypes.byref(cache), _ptr(page_table_out), _ptr(ref_count_out),
+    _check(load_library().qre_kv_compact(_at(cache, qre_kv_cache), _ptr(page_table_out), _ptr(ref_count_out),
                                          _ptr(n_live), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                          _stream(stream)), "qre_kv_compact")
 
 
 def qre_attn_prefill(attn, n_seqs, total_q, total_k, cu_q, cu_k, q, k, v, o, lse=None, stream=None) -> None:
-    _check(load_library().qre_attn_prefill(ctypes.byref(attn), n_seqs, total_q, total_k, _ptr(cu_q), _ptr(cu_k),
+    _check(load_library().qre_attn_prefill(_at(attn, qre_attn), n_seqs, total_q, total_k, _ptr(cu_q), _ptr(cu_k),
                                            _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _stream(stream)),
            "qre_attn_prefill")
 
 
 def qre_attn_decode_workspace_size(attn: qre_attn, cache: qre_kv_cache, n: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().qre_attn_decode_workspace_size(ctypes.byref(attn), ctypes.byref(cache), n,
+    _check(load_library().qre_attn_decode_workspace_size(_at(attn, qre_attn), _at(cache, qre_kv_cache), n,
                                                          ctypes.byref(out)), "qre_attn_decode_workspace_size")
     return out.value
 
 
 def qre_attn_decode(attn, cache, layer, n, seqs, max_len, q, o, lse, workspace, workspace_bytes=None,
                     stream=None) -> None:
-    _check(load_library().qre_attn_decode(ctypes.byref(attn), ctypes.byref(cache), layer, n, _ptr(seqs), max_len,
+    _check(load_library().qre_attn_decode(_at(attn, qre_attn), _at(cache, qre_kv_cache), layer, n, _ptr(seqs), max_len,
                                           _ptr(q), _ptr(o), _ptr(lse), _ptr(workspace),
                                           _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_attn_decode")
 
@@ -458,30 +468,30 @@ def make_rope(n_heads, n_kv_heads, head_dim, dtype, inv_freq, interleaved=False,
 
 
 def qre_kv_read(cache, layer, rows, n, seqs, first, cu, total, k, v, stream=None) -> None:
-    _check(load_library().qre_kv_read(ctypes.byref(cache), layer, ctypes.byref(rows), n, _ptr(seqs), _ptr(first),
+    _check(load_library().qre_kv_read(_at(cache, qre_kv_cache), layer, _at(rows, qre_kv_rows), n, _ptr(seqs), _ptr(first),
                                       _ptr(cu), total, _ptr(k), _ptr(v), _stream(stream)), "qre_kv_read")
 
 
 def qre_qk_norm_rope(rope, n_tokens, token_pos, q, k, q_out, k_out, stream=None) -> None:
-    _check(load_library().qre_qk_norm_rope(ctypes.byref(rope), n_tokens, _ptr(token_pos), _ptr(q), _ptr(k),
+    _check(load_library().qre_qk_norm_rope(_at(rope, qre_rope), n_tokens, _ptr(token_pos), _ptr(q), _ptr(k),
                                            _ptr(q_out), _ptr(k_out), _stream(stream)), "qre_qk_norm_rope")
 
 
 def qre_kv_write_rope(cache, layer, rope, n_tokens, token_seq, token_pos, q, k, v, q_out, k_out=None,
                       stream=None) -> None:
-    _check(load_library().qre_kv_write_rope(ctypes.byref(cache), layer, ctypes.byref(rope), n_tokens, _ptr(token_seq),
+    _check(load_library().qre_kv_write_rope(_at(cache, qre_kv_cache), layer, _at(rope, qre_rope), n_tokens, _ptr(token_seq),
                                             _ptr(token_pos), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out),
                                             _stream(stream)), "qre_kv_write_rope")
 
 
 def qre_kv_common_len(cache, n, seqs, n_groups, cu_group, common_len, stream=None) -> None:
-    _check(load_library().qre_kv_common_len(ctypes.byref(cache), n, _ptr(seqs), n_groups, _ptr(cu_group),
+    _check(load_library().qre_kv_common_len(_at(cache, qre_kv_cache), n, _ptr(seqs), n_groups, _ptr(cu_group),
                                             _ptr(common_len), _stream(stream)), "qre_kv_common_len")
 
 
 def qre_attn_decode_shared_workspace_size(attn: qre_attn, cache: qre_kv_cache, n: int, n_groups: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().qre_attn_decode_shared_workspace_size(ctypes.byref(attn), ctypes.byref(cache), n, n_groups,
+    _check(load_library().qre_attn_decode_shared_workspace_size(_at(attn, qre_attn), _at(cache, qre_kv_cache), n, n_groups,
                                                                 ctypes.byref(out)),
            "qre_attn_decode_shared_workspace_size")
     return out.value
@@ -489,7 +499,7 @@ def qre_attn_decode_shared_workspace_size(attn: qre_attn, cache: qre_kv_cache, n
 
 def qre_attn_decode_shared(attn, cache, layer, n, seqs, n_groups, cu_group, common_len, max_len, q, o, lse, workspace,
                            workspace_bytes=None, stream=None) -> None:
-    _check(load_library().qre_attn_decode_shared(ctypes.byref(attn), ctypes.byref(cache), layer, n, _ptr(seqs),
+    _check(load_library().qre_attn_decode_shared(_at(attn, qre_attn), _at(cache, qre_kv_cache), layer, n, _ptr(seqs),
                                                  n_groups, _ptr(cu_group), _ptr(common_len), max_len, _ptr(q), _ptr(o),
                                                  _ptr(lse), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                                  _stream(stream)), "qre_attn_decode_shared")

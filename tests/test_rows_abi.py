@@ -1,6 +1,8 @@
 """Refusals of the calls that norm, turn, write and read rows, and of shared prefixes: every bad argument is named on the
 host, before any launch (no GPU needed); the formulas' oracle against plain restatements."""
 
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -55,8 +57,11 @@ def test_bad_rope_calls():
 
 def test_bad_reads():
     f = qre.qre_kv_read
-    refused(INV, "rows is NULL", lambda *a, **k: qre._check(qre.load_library().qre_kv_read(cache(), 0, None, 1, A, None, A, 1, A, A, 0),
-                                                            "qre_kv_read"))
+    raw, c = qre.load_library().qre_kv_read, cache()
+    refused(INV, "rows is NULL", lambda **k: qre._check(raw(ctypes.addressof(c), 0, None, 1, A, None, A, 1, A, A, 0), "qre_kv_read"))
+    for bad in (None, attn(), A):
+        with pytest.raises(TypeError, match="qre_kv_rows"):
+            f(cache(), 0, bad, 1, A, None, A, 1, A, A, stream=0)
     refused(INV, "rows dtype", f, cache(), 0, rows(dtype=qre.QRE_E2M1), 1, A, None, A, 1, A, A)
     refused(UNS, "cache of dtype", f, cache(), 0, rows(dtype=qre.QRE_FP16), 1, A, None, A, 1, A, A)
     refused(INV, "n = -1", f, cache(), 0, rows(), -1, A, None, A, 1, A, A)
