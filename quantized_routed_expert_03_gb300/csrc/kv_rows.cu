@@ -204,6 +204,8 @@ struct Cut {
     const int per_token = 2 * c.n_kv_heads * (c.head_dim / kBlock4);   // at most 4096
     const int ctas = device_sm_count() * ctas_per_sm;
     tokens = ctas > 0 ? (n_tokens + ctas - 1) / ctas : 1;
+    const int fill = (kThreads + per_token - 1) / per_token;           // a block for every thread
+    tokens = tokens < fill ? fill : tokens;
     tokens = tokens > kTokens ? kTokens : tokens < 1 ? 1 : tokens;     // at most 2^19 blocks of a CTA: the reciprocal is good to 2^20
     magic = (uint32_t)((0x100000000ull + per_token - 1) / per_token);
     grid = dim3((unsigned)((n_tokens + tokens - 1) / tokens));
