@@ -1227,11 +1227,17 @@ size_t decode_ws_bytes(const qre_attn& a, const qre_kv_cache& c, int n) {
   return header_bytes(n) + (size_t)2 * grid * kWarps * kRows * (a.head_dim + 2) * sizeof(float);
 }
 
-// One launch (and its join): n queries whose places sum up below 2^31; without ids, of the rows from row0 on.
+// What the join of a launch reads: the cut of its work, and the parts.
+struct Cuts {
+  const Header* header;   // NULL: no unit was cut
+  const float* parts;
+};
+
+// One launch (and its join; with `left` the join is left to the caller, if there is one): n queries whose places sum up below 2^31; without ids, of the rows from row0 on.
 template <bool SH>
 cudaError_t launch_part(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs, int row0,
                         int max_len, const void* q, void* o, float* lse, const Own& own, void* ws, int* status,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, Cuts* left = nullptr) {
   const int g = a.n_heads / a.n_kv_heads;
   const size_t fixed = (size_t)(n + 1) * sizeof(Seq<SH>);
   const int tile = tile_of(c);
@@ -1270,7 +1276,8 @@ cudaError_t launch_part(const qre_attn& a, const qre_kv_cache& c, int layer, int
     e = launch_dependent_cluster(kernel, dim3(ctas ? (unsigned)all_units * ctas : grid), dim3(kThreads), ctas ? ctas : 1,
                                  smem, stream, a, c, layer, n, seqs, row0, static_cast<const uint16_t*>(q),
                                  static_cast<uint16_t*>(o), lse, header, parts, stages, ways, own, status);
-    if (e != cudaSuccess || ways) return e;
+    if (left) *left = ways ? Cuts{nullptr, nullptr} : Cuts{header, parts};
+    if (e != cudaSuccess || ways || left) return e;
     const int threads = split || slots > 256 ? 256 : slots;
     return launch_dependent(join, dim3((unsigned)(by_cut ? cuts : all_units), slots / (split ? 32 : threads)),
                             dim3(threads), 0, stream, a, n, by_cut, v_scale, static_cast<uint16_t*>(o), lse,

@@ -877,11 +877,32 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
 
 // ---------------------------------------------------------------- the join
 
-// A warp per query head: its own part, then those of the prefix in the order of the ranges.
+// Where dimension d of head r of a unit lies in a part that the decode kernel left (floats; see Joined::write).
+__device__ __forceinline__ int part_index(int cache_type, bool wide, int r, int d) {
+  int i, row, high;
+  if (cache_type == QRE_E2M1) {
+    const int m = d & 3;
+    row = (d & 31) >> 2;
+    i = 2 * (d >> 5) + (wide ? m >> 1 : m & 1);
+    high = wide ? m & 1 : m >> 1;
+  } else if (cache_type == QRE_E4M3) {
+    i = d >> 4;
+    row = (d & 15) >> 1;
+    high = d & 1;
+  } else {
+    i = d >> 4;
+    row = d & 7;
+    high = (d >> 3) & 1;
+  }
+  return (((wide ? 2 * i + (r >> 3) : i) * 4 + (r & 1) + 2 * high) << 5) + 4 * row + ((r & 7) >> 1);
+}
+
+// A warp per query head: its own part (or parts, where the decode kernel's ranges cut its positions and the join is left
+// to this kernel: a launch of its own took 5 us), then those of the prefix, all in the order of the ranges.
 template <int DT, int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ qre_attn a, int n,
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ qre_attn a, int n, int cache_type,
                                                           const float* __restrict__ v_scale, uint16_t* __restrict__ o,
-                                                          float* __restrict__ lse, const __grid_constant__ Space s) {
+                                                          float* __restrict__ lse, const __grid_constant__ Space s, Cuts cuts) {
   constexpr int E = D / 32;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -896,67 +917,107 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   float own[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) own[e] = s.own_o[(size_t)id * D + E * lane + e];
-  if (x.tiles == 0) return;          // complete already
-  const int g = a.n_heads / a.n_kv_heads, hk = h / g;
-  const int rows = x.m * g, r = (t - x.c0) * g + h - hk * g, blocks = (rows + kUnitRows - 1) / kUnitRows, block = r / kUnitRows;
-  const int per = x.tiles + kTileCost, in_block = rows - block * kUnitRows < kUnitRows ? rows - block * kUnitRows : kUnitRows;
-  const int u0 = x.first + (hk * blocks + block) * per;
-  const int b0 = head.range_of(u0 + kTileCost), b1 = head.range_of(u0 + per - 1);
-  const long long base = 2 * ((long long)x.before * a.n_heads + (long long)hk * rows + block * kUnitRows) + r - block * kUnitRows;
-  const float vs = v_scale ? v_scale[hk] : 1.0f;
-  const int copies = in_block > kM ? 1 : 2, parts = (b1 - b0 + 1) * copies;
-  auto row_of = [&](int i) {         // part i of the prefix
-    const int b = b0 + i / copies, k = i - i / copies * copies;
-    return base + (long long)kUnitRows * b + (long long)k * in_block;
-  };
-  float M, L, X[E];
-  {
-    M = own_ml.x;
-    L = own_ml.y;
-#pragma unroll
-    for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : own[e];
+  Header cut = {};
+  int f0 = 0, f1 = 0;
+  if (cuts.header) {
+    const int32_t* firsts = reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(cuts.header) + kFirstsAt);
+    cut = *cuts.header;
+    f0 = firsts[t];
+    f1 = firsts[t + 1];
   }
-  constexpr int kAhead = 16;         // parts whose O is on its way together
-  for (int i0 = 0; i0 < parts; i0 += kAhead) {   // a lane has a part's reference and sum
-    const int mine = parts - i0 < kAhead ? parts - i0 : kAhead;
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (lane < mine) ml = s.part_ml[row_of(i0 + lane)];
-    float y[kAhead][E];
+  const int g = a.n_heads / a.n_kv_heads, hk = h / g;
+  const float vs = v_scale ? v_scale[hk] : 1.0f;
+  float M = own_ml.x, L = own_ml.y, X[E];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+  for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : own[e];
+  bool joined = false;               // of parts, all of its result if it has no hole
+  if (f1 > f0) {
+    const int blocks = (g + kRows - 1) / kRows, in_kv = h - hk * g, unit = hk * blocks + in_kv / kRows, r = in_kv % kRows;
+    const int nch = f1 - f0, u0 = f0 * a.n_kv_heads * blocks + unit * nch;
+    const PlanHead by{(int)cut.total, cut.ranges, (int)cut.total / cut.ranges, (int)cut.total % cut.ranges};
+    const int b0 = by.range_of(u0 + kUnitCost), b1 = by.range_of(u0 + nch - 1);
+    if (b1 > b0) {                   // cut: what lies in own was not written
+      const bool wide = g > 8;
+      const size_t floats = (size_t)(wide ? 16 : 8) * (D + 2);
+      joined = true;
+      M = -INFINITY;
+      L = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
-      if (u < mine) {
-        const float* from = s.part_o + (size_t)row_of(i0 + u) * D + E * lane;
-        if (E == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(from);
-          y[u][0] = z.x, y[u][1] = z.y, y[u][E - 2] = z.z, y[u][E - 1] = z.w;
-        } else {
-          const float2 z = *reinterpret_cast<const float2*>(from);
-          y[u][0] = z.x, y[u][1] = z.y;
-        }
+      for (int e = 0; e < E; ++e) X[e] = 0.0f;
+      int at[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) at[e] = part_index(cache_type, wide, r, E * lane + e);
+#pragma unroll 4
+      for (int b = b0; b <= b1; ++b) {
+        // the first part lies in its range's first place when the unit begins there too; the others begin theirs
+        const float* part = cuts.parts + ((size_t)2 * b + (b == b0 && by.begin(b0) < u0 ? 1 : 0)) * floats;
+        const float2 ml = reinterpret_cast<const float2*>(part + (wide ? 16 : 8) * D)[r];
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = part[at[e]];
+        const float to = fmaxf(M, ml.x);
+        const float f = M == to ? 1.0f : ex2(M - to), fe = ml.x == to ? 1.0f : ex2(ml.x - to);
+        M = to;
+        L = L * f + ml.y * fe;
+#pragma unroll
+        for (int e = 0; e < E; ++e) X[e] = X[e] * f + y[e] * (fe * vs);
       }
     }
-    const bool empty = ml.x == -INFINITY && ml.y == 0.0f;   // saw nothing: its O was not written
-    float to = ml.x;
+  }
+  if (x.tiles == 0 && !joined) return;   // complete already
+  if (x.tiles > 0) {
+    const int rows = x.m * g, r = (t - x.c0) * g + h - hk * g, blocks = (rows + kUnitRows - 1) / kUnitRows, block = r / kUnitRows;
+    const int per = x.tiles + kTileCost, in_block = rows - block * kUnitRows < kUnitRows ? rows - block * kUnitRows : kUnitRows;
+    const int u0 = x.first + (hk * blocks + block) * per;
+    const int b0 = head.range_of(u0 + kTileCost), b1 = head.range_of(u0 + per - 1);
+    const long long base = 2 * ((long long)x.before * a.n_heads + (long long)hk * rows + block * kUnitRows) + r - block * kUnitRows;
+    const int copies = in_block > kM ? 1 : 2, parts = (b1 - b0 + 1) * copies;
+    auto row_of = [&](int i) {         // part i of the prefix
+      const int b = b0 + i / copies, k = i - i / copies * copies;
+      return base + (long long)kUnitRows * b + (long long)k * in_block;
+    };
+    constexpr int kAhead = 16;         // parts whose O is on its way together
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {   // a lane has a part's reference and sum
+      const int mine = parts - i0 < kAhead ? parts - i0 : kAhead;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (lane < mine) ml = s.part_ml[row_of(i0 + lane)];
+      float y[kAhead][E];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
-    to = fmaxf(M, to);
-    const float f = M == to ? 1.0f : ex2(M - to), fe = empty ? 0.0f : ml.x == to ? 1.0f : ex2(ml.x - to);
-    float sum = empty ? 0.0f : ml.y * fe;
+      for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    M = to;
-    L = L * f + sum;
-    const uint32_t there = __ballot_sync(0xffffffffu, !empty);
+        for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
+        if (u < mine) {
+          const float* from = s.part_o + (size_t)row_of(i0 + u) * D + E * lane;
+          if (E == 4) {
+            const float4 z = *reinterpret_cast<const float4*>(from);
+            y[u][0] = z.x, y[u][1] = z.y, y[u][E - 2] = z.z, y[u][E - 1] = z.w;
+          } else {
+            const float2 z = *reinterpret_cast<const float2*>(from);
+            y[u][0] = z.x, y[u][1] = z.y;
+          }
+        }
+      }
+      const bool empty = ml.x == -INFINITY && ml.y == 0.0f;   // saw nothing: its O was not written
+      float to = ml.x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) X[e] *= f;
+      for (int d = 16; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+      to = fmaxf(M, to);
+      const float f = M == to ? 1.0f : ex2(M - to), fe = empty ? 0.0f : ml.x == to ? 1.0f : ex2(ml.x - to);
+      float sum = empty ? 0.0f : ml.y * fe;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const float w = __shfl_sync(0xffffffffu, fe, u) * vs;
-      if ((there >> u) & 1u)
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      M = to;
+      L = L * f + sum;
+      const uint32_t there = __ballot_sync(0xffffffffu, !empty);
 #pragma unroll
-        for (int e = 0; e < E; ++e) X[e] = fmaf(y[u][e], w, X[e]);
+      for (int e = 0; e < E; ++e) X[e] *= f;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float w = __shfl_sync(0xffffffffu, fe, u) * vs;
+        if ((there >> u) & 1u)
+#pragma unroll
+          for (int e = 0; e < E; ++e) X[e] = fmaf(y[u][e], w, X[e]);
+      }
     }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -1028,18 +1089,19 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   const long long places = (a.window > 0 && a.window < held ? a.window : held) / chunk + 3 + kUnitCost;
   int most = 0x7fffffffll / places < n ? (int)(0x7fffffffll / places) : n;
   most = most < kPartQueries ? most : kPartQueries;
+  Cuts cuts = {};
   for (int i = 0; i < n; i += most) {
     const int m = n - i < most ? n - i : most;
     const Own own{s.hole + i, s.own_o + (size_t)i * a.n_heads * a.head_dim, s.own_ml + (size_t)i * a.n_heads, i == 0};
     e = launch_part<true>(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
                           static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, own, s.decode,
-                          status, stream);
+                          status, stream, most >= n ? &cuts : nullptr);
     if (e != cudaSuccess) return e;
   }
   const float* v_scale = low && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;
   const dim3 warps((unsigned)(((long long)n * a.n_heads + 7) / 8));
   auto join = [&](auto kernel) {
-    return launch_dependent(kernel, warps, dim3(256), 0, stream, a, n, v_scale, static_cast<uint16_t*>(o), lse, s);
+    return launch_dependent(kernel, warps, dim3(256), 0, stream, a, n, c.dtype, v_scale, static_cast<uint16_t*>(o), lse, s, cuts);
   };
   if (bf) return a.head_dim == 64 ? join(shared_join_kernel<QRE_BF16, 64>) : join(shared_join_kernel<QRE_BF16, 128>);
   return a.head_dim == 64 ? join(shared_join_kernel<QRE_FP16, 64>) : join(shared_join_kernel<QRE_FP16, 128>);
