@@ -15,8 +15,17 @@
 // two chains, each with a softmax of 128 threads, one row each: with more than 128 rows a chain has 128 of them, with
 // less both have the same rows and take the tiles in turn, so that one's products run beside the other's softmax.  K and
 // V come through a ring by TMA out of the pages; rows of 8 and 4 bits come as bytes and are widened to fp16 in shared
-// memory by four warps of their own.  No row needs a mask: a hole begins where all of the group's windows have, at a
+// memory by eight warps of their own.  No row needs a mask: a hole begins where all of the group's windows have, at a
 // whole tile, and ends with a common page, behind which the last tile's rows are zeroed.
+//
+// What it measured (calls with the common lengths found in front of them, us): 64 sequences of up to 1500 positions
+// behind 16,384, 32 heads on 8, D = 128, bf16: 84 (each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
+// 56 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 71 (265; the products take 18).  The prefixes of the first run
+// at the memory's rate, 3600 cycles a tile, once they run; 10 us of a launch are its begin (the plan, the queries, the
+// first tile's references) and 3 its end (parts).  Steps, on the first: 119 at first; queries by asynchronous copies, one
+// copy of the softmax's code, 32-bit places and a join that asks for its parts at once 97; the own positions begun beside
+// the prefixes 91; the last join for all parts 84.  No gain: a round of the softmax's code before the plan is there, for
+// the instruction cache.  In 4 bits 4 warps that widen took 2 us more than 8.
 #include <type_traits>
 
 #include "attn_decode.cuh"
@@ -264,12 +273,12 @@ struct Shape {
   static constexpr int RAW = kN * (RB + SB);         // bytes of a stored tile
   static constexpr int SLOTS = D == 128 ? (LOW ? 3 : 5) : (LOW ? 6 : 10);
   static constexpr int STAGES = !LOW ? 0 : F8 ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
-  static constexpr int THREADS = LOW ? 512 : 384;
-  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88, 512 x 128 = 256 x 160 + 256 x 96.
-  static constexpr int SOFT_REGS = LOW ? 160 : 208, OTHER_REGS = LOW ? 96 : 88;
+  static constexpr int THREADS = LOW ? 640 : 384;
+  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88; 640 x 96 = 61,440 > 256 x 152 + 384 x 56.
+  static constexpr int SOFT_REGS = LOW ? 152 : 208, OTHER_REGS = LOW ? 56 : 88;
   static constexpr int BYTES = 2 * TILE + SLOTS * TILE + STAGES * RAW + 2048;
   // warps 0-7: the two chains' softmax; then
-  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kWiden = 12;
+  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kWiden = 12, kWidenWarps = 8;
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
@@ -386,12 +395,12 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < P::SLOTS; ++s) {
-      mbar_init(&full[s], P::LOW ? 4 : 1);
+      mbar_init(&full[s], P::LOW ? P::kWidenWarps : 1);
       mbar_init(&empty[s], 2);
     }
     for (int s = 0; s < P::STAGES; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], 4);
+      mbar_init(&raw_empty[s], P::kWidenWarps);
     }
     mbar_init(q_full, 8);
     mbar_init(q_free, 8);
@@ -591,7 +600,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             if (!ok) break;
             const uint8_t* raw = sraw + st * P::RAW;
             uint8_t* to = skv + sl * P::TILE + (p / 4) * P::HALF;
-            constexpr int kRowsAt = 128 / PR, kAhead = PR;   // rows at a time; blocks of a thread: all of a tile
+            constexpr int kRowsAt = 32 * P::kWidenWarps / PR, kAhead = kN / kRowsAt;   // rows at a time; blocks of a thread: all of a tile
 #pragma unroll 1
             for (int r0 = me / PR; r0 < kN; r0 += kAhead * kRowsAt) {
               uint4 u[kAhead];       // E2M1: codes and the scale
