@@ -147,21 +147,30 @@ CASES = [
     ([2500], [[9] * 40], 8, 1, 128, 256, "bf16", "e2m1", 0, True, None),                     # 320 rows
     ([600] * 24, [[2, 3, 4]] * 24, 16, 8, 64, 16, "bf16", "bf16", 0, False, None),           # several units to a CTA
     ([250] * 70, [[1, 2]] * 70, 8, 8, 64, 16, "fp16", "e2m1", 0, False, None),
+    ([1100, 300], [[30, 900, 2], [60, 1]], 40, 2, 128, 32, "bf16", "bf16", 0, False, None),   # 20 heads per KV head
+    ([700], [[600, 3]], 24, 2, 64, 16, "fp16", "fp16", 300, False, None),                    # 12
+    ([1100], [[30, 900, 2]], 48, 3, 128, 32, "bf16", "e4m3", 0, True, None),                  # 16
+    ([1100], [[30, 900, 2]], 32, 2, 128, 32, "fp16", "e2m1", 0, True, None),                  # 16
+    ([900], [[30, 2000, 2, 5]], 36, 2, 64, 16, "bf16", "e2m1", 1500, False, None),            # 18
+    ([512], [[4000, 1]], 6, 2, 128, 64, "bf16", "e2m1", 0, True, None),                       # own positions cut over the ranges
+    ([512], [[4000, 1, 0]], 4, 1, 64, 64, "fp16", "e4m3", 0, False, None),
 ]
 
 
-@pytest.mark.parametrize("max_len", [0, -1])
+# 0: not known; -1: as it is (so short that each sequence reads for itself); 10 ** 8: a hint by which sharing always pays
+@pytest.mark.parametrize("max_len", [0, -1, 10 ** 8])
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_shared_prefixes(case, max_len):
     prompts, owns, H, Hk, D, page, kind, cache, window, scaled, order = CASES[case]
     w = Shared(prompts, owns, H, Hk, D, page, kind, cache, scaled, seed=100 * case, order=order)
     q = randn((len(w.seqs), H, D), 5 + case, kind, 1.5)
-    o, lse = run(w, q, window, max(w.lens) if max_len else 0)
+    max_len = max(w.lens) if max_len == -1 else max_len
+    o, lse = run(w, q, window, max_len)
     assert qre.qre_read_device_status() == 0
     ref, v_max = w.reference(q, window)
     check(o, lse, ref, kind, max(w.lens), v_max)
     for _ in range(3):                                       # results do not depend on timing
-        o2, lse2 = run(w, q, window, max(w.lens) if max_len else 0)
+        o2, lse2 = run(w, q, window, max_len)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
@@ -305,3 +314,22 @@ def test_most_queries_of_a_call():
     b = att.decode_shared(q, None, cu, common, lse=l1)
     assert qre.qre_read_device_status() == 0
     assert float((l0 - l1).abs().max()) < 1e-4 and float((a.float() - b.float()).abs().max()) < 2.0 ** -6
+
+
+def test_a_wait_that_gives_up():
+    """With a limit of a microsecond waits of the pipeline run out: a status, and the next call is as it was."""
+    w = Shared([5000], [[3, 7, 20]], 8, 2, 128, 64, "bf16", "e4m3", seed=4)
+    q = randn((3, 8, 128), 1, "bf16")
+    want = run(w, q)
+    assert qre.qre_read_device_status() == 0
+    try:
+        qre.qre_debug_wait_test(1000, 0)
+        run(w, q)
+        assert qre.qre_read_device_status() & ~qre.QRE_DEV_TIMEOUT == 0
+    finally:
+        qre.qre_debug_wait_test(0, 0)
+    qre.qre_clear_device_status()
+    for _ in range(2):
+        got = run(w, q)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert qre.qre_read_device_status() == 0
