@@ -333,3 +333,49 @@ def test_a_wait_that_gives_up():
         got = run(w, q)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert qre.qre_read_device_status() == 0
+
+
+@pytest.mark.parametrize("cache,pages", [("e2m1", 40000), ("bf16", 16000), ("e4m3", 24000)])
+def test_pools_beyond_32_bits(cache, pages):
+    """Pages whose bytes lie 4 GB and more behind the pool's begin, in the second layer: turned rows written and read
+    back, decode by itself and shared."""
+    H, Hk, D, page, shared = 16, 8, 128, 256, 512
+    lens = [shared + 3, shared + 90, shared + 256]
+    c = KVCache(2, pages, Hk, page, D, 3, 4, TYPE[cache], device=DEV)       # (not initialised: NaN and what not)
+    last = pages - 1
+    c.page_table[:, :2] = i32([last, last - 7])
+    c.page_table[:, 2] = i32([last - 1, last - 2, last - 3])
+    c.seq_len[:] = i32(lens)
+    seq = i32([0] * shared + [s for s, n in enumerate(lens) for _ in range(n - shared)])
+    pos = i32(list(range(shared)) + [p for n in lens for p in range(shared, n)])
+    T = seq.numel()
+    q, k, v = (randn((T, h, D), i, "bf16") for i, h in enumerate((H, Hk, Hk)))
+    from quantized_routed_expert_03_gb300.attention import Rotary
+    _, ko = c.write_rope(1, Rotary(H, Hk, D, 0, q_norm=None, k_norm=None, device=DEV), seq, pos, q, k, v)
+    assert torch.equal(ko, k)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    kr, vr = c.read(1, None, i32(cu), int(cu[-1]))
+    own = {s: (torch.cat([k[:shared], k[seq == s][shared if s == 0 else 0:]]), torch.cat([v[:shared], v[seq == s][shared if s == 0 else 0:]])) for s in range(3)}
+    for s in range(3):
+        for got, rows in ((kr, own[s][0]), (vr, own[s][1])):
+            want = npy(rows)
+            if cache == "e2m1":
+                want = oatt.e2m1_blocks(want)[2]
+            elif cache == "e4m3":
+                want = oatt.e4m3_round(want)
+            assert np.array_equal(npy(got[cu[s]:cu[s + 1]]), want)
+    qq = randn((3, H, D), 9, "bf16")
+    att = Attention(c, 1, H, 3, max_groups=1)
+    ref = [np.zeros((3, H, D)), np.zeros((3, H)), np.zeros((3, H, D)), np.zeros((3, H))]
+    for s in range(3):
+        kk, vv = npy(kr[cu[s]:cu[s + 1]]), npy(vr[cu[s]:cu[s + 1]])
+        for h in range(H):
+            for dst, x in zip(ref, oatt.attend(npy(qq)[s, h:h + 1], kk[:, h // 2], vv[:, h // 2], D ** -0.5, [0], [lens[s]])):
+                dst[s, h] = x[0]
+    lse = torch.empty((3, H), device=DEV)
+    check(att.decode(qq, None, lse=lse), lse, ref, "bf16", max(lens), float(vr.float().abs().max()))
+    groups = i32([0, 3])
+    common = c.common_len(i32([0, 1, 2]), groups)
+    assert common.tolist() == [shared]
+    check(att.decode_shared(qq, None, groups, common, lse=lse), lse, ref, "bf16", max(lens), float(vr.float().abs().max()))
+    assert qre.qre_read_device_status() == 0
