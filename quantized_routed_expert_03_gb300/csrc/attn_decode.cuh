@@ -160,10 +160,15 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ uint32_t low_half2(uint32_t a) { return h2_as_u32(__low2half2(u32_as_h2(a))); }
 __device__ __forceinline__ uint32_t high_half2(uint32_t a) { return h2_as_u32(__high2half2(u32_as_h2(a))); }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) { return h2_as_u32(__hmul2(u32_as_h2(a), u32_as_h2(b))); }
-// Two E4M3 bytes (low half of b) as an fp16 pair.
+// Two E4M3 bytes, the low or the high half of b, as an fp16 pair (the conversion takes either half of a register).
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t b) {
   uint32_t r;
-  asm("{.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(b));
+  asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_high_to_half2(uint32_t b) {
+  uint32_t r;
+  asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(b));
   return r;
 }
 
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
         uint2 ksc[K::F4 ? K::NS : 1][2];
         const uint32_t ksel = (uint32_t)(j4 >> 1) * 0x11u + 0x20u;
         auto scales_of = [&](const uint2& row, int p) {   // of pieces p and p + 1
-          return e4m3x2_to_half2(__byte_perm(p < 2 ? row.x : row.y, 0, ksel) & 0xffffu);
+          return e4m3x2_to_half2(__byte_perm(p < 2 ? row.x : row.y, 0, ksel));
         };
         if constexpr (K::F4) {
 #pragma unroll
@@ -795,10 +800,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
                 if (!K::F8) {
                   mma16816<K::BF>(s[i][nh], x[0], x[1], x[2], x[3], qb[p / 2][nh]);
                 } else {
-                  mma16816<false>(s[i][nh], e4m3x2_to_half2(x[0] & 0xffffu), e4m3x2_to_half2(x[1] & 0xffffu),
-                                  e4m3x2_to_half2(x[0] >> 16), e4m3x2_to_half2(x[1] >> 16), qb[p][nh]);
-                  mma16816<false>(s[i][nh], e4m3x2_to_half2(x[2] & 0xffffu), e4m3x2_to_half2(x[3] & 0xffffu),
-                                  e4m3x2_to_half2(x[2] >> 16), e4m3x2_to_half2(x[3] >> 16), qb[p + 1][nh]);
+                  mma16816<false>(s[i][nh], e4m3x2_to_half2(x[0]), e4m3x2_to_half2(x[1]),
+                                  e4m3x2_high_to_half2(x[0]), e4m3x2_high_to_half2(x[1]), qb[p][nh]);
+                  mma16816<false>(s[i][nh], e4m3x2_to_half2(x[2]), e4m3x2_to_half2(x[3]),
+                                  e4m3x2_high_to_half2(x[2]), e4m3x2_high_to_half2(x[3]), qb[p + 1][nh]);
                 }
               }
             }
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
           uint4 vsc[K::F4 ? 2 : 1];
           auto pair_scale = [&](const uint4& w, int p) {   // of the piece's dimensions 4 r .. 4 r + 3
             const uint32_t sel = (uint32_t)(r4 >> 2) * 0x11u + 0x40u + (p & 1 ? 0x22u : 0u);
-            return e4m3x2_to_half2(__byte_perm(p < 2 ? w.x : w.y, p < 2 ? w.z : w.w, sel) & 0xffffu);
+            return e4m3x2_to_half2(__byte_perm(p < 2 ? w.x : w.y, p < 2 ? w.z : w.w, sel));
           };
           if constexpr (K::F4) {
 #pragma unroll
@@ -949,8 +954,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const uint32_t y0 = __byte_perm(x[2 * e], 0, 0x3120), y1 = __byte_perm(x[2 * e + 1], 0, 0x3120);
-                const uint32_t a0 = e4m3x2_to_half2(y0 & 0xffffu), a1 = e4m3x2_to_half2(y0 >> 16);
-                const uint32_t a2 = e4m3x2_to_half2(y1 & 0xffffu), a3 = e4m3x2_to_half2(y1 >> 16);
+                const uint32_t a0 = e4m3x2_to_half2(y0), a1 = e4m3x2_high_to_half2(y0);
+                const uint32_t a2 = e4m3x2_to_half2(y1), a3 = e4m3x2_high_to_half2(y1);
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh) mma16816<false>(acc[d + e][nh], a0, a1, a2, a3, pb[nh]);
               }

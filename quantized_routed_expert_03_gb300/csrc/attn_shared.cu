@@ -621,9 +621,9 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
                 if constexpr (P::F8) {
                   const uint32_t b4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = e4m3x2_to_half2((b4[e / 2] >> (16 * (e & 1))) & 0xffffu);
+                  for (int e = 0; e < 8; ++e) y[e] = e & 1 ? e4m3x2_high_to_half2(b4[e / 2]) : e4m3x2_to_half2(b4[e / 2]);
                 } else {
-                  const uint32_t s2 = e4m3x2_to_half2(__byte_perm(u[k].z, 0, 0x4400) & 0xffffu);
+                  const uint32_t s2 = e4m3x2_to_half2(__byte_perm(u[k].z, 0, 0x4400));
                   e2m1x8_to_half2(u[k].x, *reinterpret_cast<uint32_t(*)[4]>(y));
                   e2m1x8_to_half2(u[k].y, *reinterpret_cast<uint32_t(*)[4]>(y + 4));
 #pragma unroll
