@@ -9,9 +9,10 @@
 // 16-bit write, a CTA has neighbouring tokens, whose pages it looks up once while the
 // first rows are on their way.
 //
-// What it measured (8 KV heads of 128, 4 bits): 131,072 rows read back 125 us, 5.0 TB/s of which three quarters are
-// written; with CTAs of 64 rows, 2 rounds of them, 131.  2227 rows of 4 heads of 64 written 4.3 us, read (17,997) 8.4;
-// with as few rows as leave a CTA a quarter full 6.8.  A search of the bounds in shared memory gains nothing.
+// What it measured (8 KV heads of 128, 4 bits): 131,072 rows read back 120 us, 5.2 TB/s of which three quarters are
+// written.  With several blocks of a thread on their way, and so fewer threads on an SM, it is slower (2: 2 us, 4: 38).
+// 2227 rows of 4 heads of 64 written 4.3 us, read (17,997) 8.4; with as few rows as leave a CTA a quarter full 6.8.  A
+// search of the bounds in shared memory gains nothing.
 #include <type_traits>
 
 #include "internal.h"
@@ -21,7 +22,7 @@ namespace qre {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 128;   // of a CTA at most: the CTAs of 150,000 rows run at once
+constexpr int kTokens = 64;    // of a CTA at most
 
 template <int RT>
 __global__ void __launch_bounds__(kThreads) kv_write4_kernel(
@@ -160,41 +161,26 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(
   const int per_head_shift = D == 64 ? 2 : 3, per_row = c.n_kv_heads << per_head_shift, per_token = 2 * per_row;
   const int blocks = mine * per_token;
   const size_t head = kv_head_bytes(c);
-  constexpr int kEach = 2;           // blocks of a thread on their way
-  for (int i0 = threadIdx.x; i0 < blocks; i0 += kEach * kThreads) {
-    uint32_t y[kEach][8];
-    uint16_t* dst[kEach];
-#pragma unroll
-    for (int u = 0; u < kEach; ++u) {
-      const int i = i0 + u * kThreads;
-      dst[u] = nullptr;
-      if (i >= blocks) continue;
-      const int t = (int)__umulhi((uint32_t)i, magic), rest = i - t * per_token;
-      const bool is_v = rest >= per_row;
-      const int x = is_v ? rest - per_row : rest, h = x >> per_head_shift, b = x & ((1 << per_head_shift) - 1);
-      const long long page = page_of[t];
-      if (page == -2) continue;
-      dst[u] = (is_v ? v + (size_t)(t0 + t) * r.v_token + (size_t)h * r.v_head
-                     : k + (size_t)(t0 + t) * r.k_token + (size_t)h * r.k_head) + kBlock4 * b;
-      if (page >= 0) {
-        const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) + page + (size_t)h * head;
-        const float* scales = is_v ? c.v_scale : c.k_scale;
-        load16<RT, CT>(base, pos_of[t] & (c.page_size - 1), b, D, c.page_size,
-                       CT != QRE_BF16 && scales ? scales[(size_t)layer * c.n_kv_heads + h] : 1.0f, y[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[u][e] = 0;
-      }
+  for (int i = threadIdx.x; i < blocks; i += kThreads) {
+    const int t = (int)__umulhi((uint32_t)i, magic), rest = i - t * per_token;
+    const bool is_v = rest >= per_row;
+    const int x = is_v ? rest - per_row : rest, h = x >> per_head_shift, b = x & ((1 << per_head_shift) - 1);
+    const long long page = page_of[t];
+    if (page == -2) continue;
+    uint32_t y[8] = {};
+    if (page >= 0) {
+      const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v : c.k) + page + (size_t)h * head;
+      const float* scales = is_v ? c.v_scale : c.k_scale;
+      load16<RT, CT>(base, pos_of[t] & (c.page_size - 1), b, D, c.page_size,
+                     CT != QRE_BF16 && scales ? scales[(size_t)layer * c.n_kv_heads + h] : 1.0f, y);
     }
-#pragma unroll
-    for (int u = 0; u < kEach; ++u) {
-      if (!dst[u]) continue;
-      if (wide) {
-        st_global_32(dst[u], y[u]);
-      } else {
-        *reinterpret_cast<uint4*>(dst[u]) = make_uint4(y[u][0], y[u][1], y[u][2], y[u][3]);
-        *reinterpret_cast<uint4*>(dst[u] + 8) = make_uint4(y[u][4], y[u][5], y[u][6], y[u][7]);
-      }
+    uint16_t* dst = (is_v ? v + (size_t)(t0 + t) * r.v_token + (size_t)h * r.v_head
+                          : k + (size_t)(t0 + t) * r.k_token + (size_t)h * r.k_head) + kBlock4 * b;
+    if (wide) {
+      st_global_32(dst, y);
+    } else {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(dst + 8) = make_uint4(y[4], y[5], y[6], y[7]);
     }
   }
 }
@@ -210,7 +196,7 @@ struct Cut {
     tokens = ctas > 0 ? (n_tokens + ctas - 1) / ctas : 1;
     const int fill = (kThreads + per_token - 1) / per_token;           // a block for every thread
     tokens = tokens < fill ? fill : tokens;
-    tokens = tokens > kTokens ? kTokens : tokens < 1 ? 1 : tokens;     // at most 2^19 blocks of a CTA: the reciprocal is good to 2^20
+    tokens = tokens > kTokens ? kTokens : tokens < 1 ? 1 : tokens;     // at most 2^18 blocks of a CTA: the reciprocal is good to 2^20
     magic = (uint32_t)((0x100000000ull + per_token - 1) / per_token);
     grid = dim3((unsigned)((n_tokens + tokens - 1) / tokens));
   }
@@ -232,7 +218,8 @@ cudaError_t launch_kv_write4(const qre_kv_cache& c, int layer, const qre_kv_rows
 cudaError_t launch_kv_read(const qre_kv_cache& c, int layer, const qre_kv_rows& r, int n, const int32_t* seqs,
                            const int32_t* first, const int32_t* cu, int total, void* k, void* v, int* status,
                            cudaStream_t stream) {
-  const Cut cut(c, total, 8);
+  // Many small CTAs: those that run write neighbouring rows (131,072 rows: 130 us with 8 per SM, 127 with 128).
+  const Cut cut(c, total, 128);
   auto fits = [](const void* p, int64_t token, int64_t head) { return reinterpret_cast<uintptr_t>(p) % 32 == 0 && token % 16 == 0 && head % 16 == 0; };
   const int wide = fits(k, r.k_token, r.k_head) && fits(v, r.v_token, r.v_head);   // whole 32-byte sectors
   auto go = [&](auto kernel) {
