@@ -605,7 +605,8 @@ QRE_API qre_status qre_qk_norm_rope(const qre_rope* rope, int32_t n_tokens, cons
  * The same on the way into the cache: q_out gets the queries, and the turned keys
  * and the values go to position token_pos[t] of sequence token_seq[t], as
  * qre_kv_write puts rows there (what a QRE_E4M3 or QRE_E2M1 cache rounds is the
- * fp32 result, and the turned keys are rounded once).  k_out (NULL: not wanted)
+ * fp32 result, and the turned keys are rounded once).  The positions of one call
+ * are distinct.  k_out (NULL: not wanted)
  * gets the turned keys too.  Padding is skipped; a token without a page at its
  * position, or with a bad id, has its queries and its row of k_out written and is
  * flagged with QRE_DEV_BAD_INDEX.

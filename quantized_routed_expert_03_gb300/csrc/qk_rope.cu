@@ -18,10 +18,11 @@
 // weights of the norm in registers; they and its angles lie in shared memory as it reads
 // them, neighbouring lanes side by side.
 //
-// What it measured: 11,278 tokens of 32 and 8 heads of 128 on their way into the pages, 300 MB: 56 us, 5.3 TB/s (a
+// What it measured: 11,278 tokens of 32 and 8 heads of 128 on their way into the pages, 300 MB: 55 us, 5.4 TB/s (a
 // copy: 6.8).  One token a CTA and its weights from memory for each row 92; with the queries, keys and values as
-// loops of their own 67 (and small calls 2 us longer).  64 tokens 5.5 us, 700 of 28 heads of 64 5.4: a launch and a
-// chain of loads.  CTAs that share a token's rows gain nothing there and cost 7 us on the large call.
+// loops of their own 67 (and small calls 2 us longer); one element an instruction 56; three CTAs an SM 62, five (51
+// registers) 71.  64 tokens 5.5 us, 700 of 28 heads of 64 5.0: a launch and a chain of loads.  CTAs that share a
+// token's rows gain nothing there and cost 7 us on the large call.
 #include <type_traits>
 
 #include "internal.h"
@@ -45,7 +46,7 @@ __device__ __forceinline__ float2 turn_by(int pos, float f) {
 enum To { kArrays = -1 };   // else the qre_dtype of the cache
 
 template <int DT, int D, int CT>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(
+__global__ void __launch_bounds__(kThreads, CT == QRE_E2M1 || CT == QRE_E4M3 ? 3 : 4) qk_rope_kernel(
     const __grid_constant__ qre_rope r, const __grid_constant__ qre_kv_cache c, int layer, int n_tokens, int tokens,
     uint32_t q_magic, uint32_t k_magic, const int32_t* __restrict__ token_seq, const int32_t* __restrict__ token_pos,
     const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, int* status) {
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
   constexpr int kRowsAt = kThreads / LR; // rows of a CTA at a time
   constexpr bool kCache = CT != kArrays;
   constexpr bool kQuant = CT == QRE_E4M3 || CT == QRE_E2M1;
-  __shared__ __align__(16) float2 turn[kTokens][D / 2];   // a lane's angles two by two, lane beside lane
+  __shared__ __align__(16) float turn[kTokens][D];   // a lane's angles two by two, lane beside lane
   __shared__ __align__(16) float weights[2][D];
   __shared__ int pos_of[kTokens];
   __shared__ long long page_of[kCache ? kTokens : 1];
@@ -116,7 +117,10 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
       of = f >> 3;
       e = f & 7;
     }
-    turn[t][2 * ((e >> 1) * step + of) + (e & 1)] = turn_by(token_pos[t0 + t], r.inv_freq[f]);
+    const float2 z = turn_by(token_pos[t0 + t], r.inv_freq[f]);
+    float* to = turn[t] + 4 * ((e >> 1) * step + of) + (e & 1);   // two cosines, two sines
+    to[0] = z.x;
+    to[2] = z.y;
   }
   // the norms' weights, a lane's 16 in a row: 1 without a norm
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
   __syncthreads();
 
   int have = -1;                     // whose weights the registers hold
-  float weight[2][8];
+  uint64_t weight[2][4];
   for (int i = i0; i < rows; i += kRowsAt) {   // (the lanes of a row go together)
     const int kind = next.kind, t = next.t, h = next.h;
     const uint4 w0 = next.x[0], w1 = next.x[1];
@@ -142,8 +146,8 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 z = *reinterpret_cast<const float4*>(&weights[kind][(e * LR + j) * 4]);
-        float* to = weight[e >> 1] + 4 * (e & 1);
-        to[0] = z.x, to[1] = z.y, to[2] = z.z, to[3] = z.w;
+        weight[e >> 1][2 * (e & 1)] = pair(z.x, z.y);
+        weight[e >> 1][2 * (e & 1) + 1] = pair(z.z, z.w);
       }
     }
     const int pos = pos_of[t];
@@ -155,17 +159,29 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
       unpack8<DT>(w1, x[1]);
     }
     if (!is_v) {
-      if (norm) {
-        float sum = 0.0f;
+      // (two elements an instruction, neighbours: the issue slots are what this kernel runs out of next to the memory)
+      uint64_t u[2][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[0][e], x[0][e], fmaf(x[1][e], x[1][e], sum));
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[b][e] = pair(x[b][2 * e], x[b][2 * e + 1]);
+      if (norm) {
+        uint64_t sums[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sums[0] = fma2(u[0][e], u[0][e], sums[0]);
+          sums[1] = fma2(u[1][e], u[1][e], sums[1]);
+        }
+        const float2 two = unpair(add2(sums[0], sums[1]));
+        float sum = two.x + two.y;
 #pragma unroll
         for (int d = LR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(mates, sum, d);
         const float inv = 1.0f / sqrtf(sum * (1.0f / D) + r.eps);
+        const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[b][e] *= inv * weight[b][e];
+          for (int e = 0; e < 4; ++e) u[b][e] = mul2(u[b][e], mul2(inv2, weight[b][e]));
       }
       if (turns) {
         const float4* cs = reinterpret_cast<const float4*>(turn[t]) + j;
@@ -173,22 +189,26 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(
         for (int e = 0; e < 4; ++e) {
           const float4 z = cs[e * step];   // angles 2 e and 2 e + 1
           if (r.interleaved) {
-            float(&u)[8] = x[e >> 1];
-            const int at = 4 * (e & 1);
-            const float a = u[at], b = u[at + 1], d = u[at + 2], f = u[at + 3];
-            u[at] = a * z.x - b * z.y;
-            u[at + 1] = b * z.x + a * z.y;
-            u[at + 2] = d * z.z - f * z.w;
-            u[at + 3] = f * z.z + d * z.w;
+            uint64_t(&w)[4] = u[e >> 1];
+            const int at = 2 * (e & 1);
+            const float2 a = unpair(w[at]), b = unpair(w[at + 1]);
+            w[at] = fma2(pair(a.y, a.x), pair(-z.z, z.z), mul2(w[at], pair(z.x, z.x)));
+            w[at + 1] = fma2(pair(b.y, b.x), pair(-z.w, z.w), mul2(w[at + 1], pair(z.y, z.y)));
           } else {
-            const float a = x[0][2 * e], b = x[1][2 * e], d = x[0][2 * e + 1], f = x[1][2 * e + 1];
-            x[0][2 * e] = a * z.x - b * z.y;
-            x[1][2 * e] = b * z.x + a * z.y;
-            x[0][2 * e + 1] = d * z.z - f * z.w;
-            x[1][2 * e + 1] = f * z.z + d * z.w;
+            const uint64_t a = u[0][e], b = u[1][e], c2 = pair(z.x, z.y);
+            u[0][e] = fma2(b, pair(-z.z, -z.w), mul2(a, c2));
+            u[1][e] = fma2(a, pair(z.z, z.w), mul2(b, c2));
           }
         }
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 z = unpair(u[b][e]);
+          x[b][2 * e] = z.x;
+          x[b][2 * e + 1] = z.y;
+        }
       y0 = pack8<DT>(x[0]);
       y1 = pack8<DT>(x[1]);
       uint16_t* dst = kind == 0 ? q_out + (size_t)(t0 + t) * r.qo_token + (size_t)h * r.qo_head
