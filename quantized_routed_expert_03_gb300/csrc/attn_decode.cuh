@@ -225,8 +225,10 @@ struct Own {
   float2* ml;         // [n][n_heads]
   // The launch before this one in the stream computes the holes' positions; this one needs nothing of it, only of the
   // ones before.  So it begins where SMs are free already, and its first CTA waits for that launch at its end: then
-  // what comes behind this launch comes behind both.
+  // what comes behind this launch comes behind both.  *ctas: how many of its CTAs have work (the SMs that the launch
+  // before leaves; NULL: all).
   int late;
+  const int* ctas;
 };
 
 template <bool SH>
@@ -366,6 +368,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   auto leave = [&]() {
     if (SH && late && blockIdx.x == 0) grid_dependency_wait();
   };
+  int grid = (int)gridDim.x;
+  if constexpr (SH) {
+    if (own.ctas && ways <= 1) grid = max(1, min(*own.ctas, grid));
+    if ((int)blockIdx.x >= grid) return;   // never the first, which waits for the launch before
+  }
 
   // ---- the plan: chunks of every query, summed up
   constexpr int kEach = 4;   // queries of a thread at a time: their loads are in flight together
@@ -426,10 +433,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   const long long total = (long long)before * units;
   const bool together = ways > 1;   // a cluster has one unit, `ways` warps share its chunks
   const long long want = ways ? (long long)n * units : (total + kMinChunks - 1) / kMinChunks;
-  const long long all = (long long)gridDim.x * kWarps;
+  const long long all = (long long)grid * kWarps;
   const int ranges = (int)(together ? all : want < all ? want : all);
   // this warp's range: few ranges spread over the SMs
-  const int me = together ? (int)blockIdx.x * kWarps + warp : warp * (int)gridDim.x + (int)blockIdx.x;
+  const int me = together ? (int)blockIdx.x * kWarps + warp : warp * grid + (int)blockIdx.x;
   // the place at which range b begins: any, or a unit's first, or one of `ways` shares of a unit
   auto begin = [&](int b) {
     if (!ways) return range_begin(b, ranges, total);
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
   };
 
   // queries that see nothing
-  for (int t = blockIdx.x; t < n; t += gridDim.x) {
+  for (int t = blockIdx.x; t < n; t += grid) {
     if (sq[t + 1].first != sq[t].first) continue;
     if constexpr (SH) {
       if (sq[t].hole.y > sq[t].hole.x) {   // what it sees is all in its hole

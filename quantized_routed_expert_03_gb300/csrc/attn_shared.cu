@@ -7,8 +7,8 @@
 // head.  The rows of a group that share a KV head, members x heads, are multiplied with a tile of keys together: at 128
 // rows a tile of 128 keys (64 KB in 16 bits at D = 128) takes the tensor cores 1024 cycles and the memory 2800.
 //
-// Steps: a plan (one CTA: what each group shares, in tiles of 128 keys); the prefixes (below); the decode kernel over
-// what lies outside the holes; the join.
+// Steps: a plan (one CTA: what each group shares, in tiles of 128 keys, and how many SMs it is worth); the prefixes
+// (below); beside them, on the other SMs, the decode kernel over what lies outside the holes; the join.
 //
 // Prefixes: units are (group, KV head, 256 rows); their tiles in a row are cut into equal ranges, one per CTA (one on an
 // SM), as the decode kernel cuts its chunks.  A CTA multiplies with tcgen05, S and P in tensor memory, O beside it, in
@@ -19,13 +19,13 @@
 // whole tile, and ends with a common page, behind which the last tile's rows are zeroed.
 //
 // What it measured (calls with the common lengths found in front of them, us): 64 sequences of up to 1500 positions
-// behind 16,384, 32 heads on 8, D = 128, bf16: 84 (each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
-// 56 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 71 (265; the products take 18).  The prefixes of the first run
-// at the memory's rate, 3600 cycles a tile, once they run; 10 us of a launch are its begin (the plan, the queries, the
-// first tile's references) and 3 its end (parts).  Steps, on the first: 119 at first; queries by asynchronous copies, one
-// copy of the softmax's code, 32-bit places and a join that asks for its parts at once 97; the own positions begun beside
-// the prefixes 91; the last join for all parts 84.  No gain: a round of the softmax's code before the plan is there, for
-// the instruction cache.  In 4 bits 4 warps that widen took 2 us more than 8.
+// behind 16,384, 32 heads on 8, D = 128, bf16: 71 (each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
+// 51 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 67 (265; the products take 18).  10 us of a launch of the
+// prefixes are its begin (the plan, the queries, the first tile's references) and 3 its end (parts).  Steps, on the
+// first: 119 at first; queries by asynchronous copies, one copy of the softmax's code, 32-bit places and a join that asks
+// for its parts at once 97; the own positions begun beside the prefixes 91; the last join for all parts 84; SMs for the
+// prefixes and others for the own positions, not all for both in turn, 71.  No gain: a round of the softmax's code before
+// the plan is there, for the instruction cache.  In 4 bits 4 warps that widen took 2 us more than 8.
 #include <type_traits>
 
 #include "attn_decode.cuh"
@@ -62,6 +62,7 @@ struct PlanHead {
   int total;             // places
   int ranges;
   int each, rest;        // total / ranges, total % ranges
+  int own_ctas;          // of the decode kernel: two (or three) on each SM that the ranges leave
   __device__ __forceinline__ int begin(int b) const { return each * b + (int)((unsigned)rest * (unsigned)b / (unsigned)ranges); }
   // the range that place i lies in
   __device__ __forceinline__ int range_of(int i) const {
@@ -130,18 +131,36 @@ Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, vo
 
 // ---------------------------------------------------------------- the plan
 
+// What the work takes, ns of an SM: a tile of a unit with more than kM rows and with less, and a position and a unit of
+// the sequences' own.  Fitted to calls that gave the prefixes 16 to 151 of the 152 SMs; with these, seven calls of all
+// types and head sizes came within 4 % of their best split (8 bits: 9 %).
+struct Costs {
+  float tile, tile_one, position, unit;
+  int ctas_sm;           // CTAs of the decode kernel on an SM
+};
+
+Costs costs_of(const qre_kv_cache& c, int ctas_sm) {
+  const bool d64 = c.head_dim == 64;
+  const float tile = c.dtype == QRE_E2M1 || c.dtype == QRE_E4M3 ? (d64 ? 1670.0f : 2100.0f) : d64 ? 1380.0f : 1750.0f;
+  const float position = c.dtype == QRE_E2M1 ? (d64 ? 3.4f : 5.0f) : c.dtype == QRE_E4M3 ? (d64 ? 3.5f : 6.1f) : d64 ? 4.5f : 7.9f;
+  // (a tile of 8 or 4 bits is widened once, for however few rows)
+  const float one = c.dtype == QRE_E2M1 || c.dtype == QRE_E4M3 ? 0.85f : 0.7f;
+  return Costs{tile, one * tile, position, 100.0f, ctas_sm};
+}
+
 // One CTA, a warp per group: the positions that it shares, [ha, hb): hb the common length in whole runs of 16 whose
 // pages are there, ha a whole tile at or behind the first position that every member sees.
 __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant__ qre_kv_cache c, int n,
                                                            const int32_t* __restrict__ seqs, int n_groups,
                                                            const int32_t* __restrict__ cu_group,
                                                            const int32_t* __restrict__ common_len, int window, int g,
-                                                           int n_kv_heads, int min_positions, int grid, Space s,
-                                                           int* status) {
+                                                           int n_kv_heads, int min_positions, int grid, Costs costs,
+                                                           Space s, int* status) {
   __shared__ long long scan[33];
   __shared__ int scan_m[33];
   __shared__ long long places_of[32];
   __shared__ int shared_of[32];
+  __shared__ float own_of[32], work_of[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -158,13 +177,14 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
   if (bad) {   // nothing is shared
     if (tid == 0) {
       set_status(status, QRE_DEV_BAD_INDEX);
-      *s.head = PlanHead{0, 0, 0, 0};
+      *s.head = PlanHead{0, 0, 0, 0, grid * costs.ctas_sm};
     }
     return;
   }
   const int ps_shift = 31 - __clz(c.page_size);
   long long total = 0;
   int before = 0;
+  float own = 0.0f, work = 0.0f;     // positions of this warp's sequences that are not shared; its groups' tiles, ns
   for (int g0 = 0; g0 < n_groups; g0 += 32) {
     const int gi = g0 + warp;
     Group x = {};
@@ -173,13 +193,17 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       x.m = cu_group[gi + 1] - x.c0;
       const int common = common_len[gi];
       int least = 0x7fffffff, most = 0, row = -1;
+      float seen = 0.0f;
       for (int i = lane; i < x.m; i += 32) {
         const int id = seqs ? seqs[x.c0 + i] : x.c0 + i;
         const int len = id >= 0 && id < c.max_seqs ? c.seq_len[id] : -1;
         if (i == 0) row = id;
         least = min(least, len);
         most = max(most, len);
+        seen += (float)(len < 0 ? 0 : window > 0 && window < len ? window : len);
       }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) seen += __shfl_xor_sync(0xffffffffu, seen, d);
       least = __reduce_min_sync(0xffffffffu, least);
       most = __reduce_max_sync(0xffffffffu, most);
       row = __shfl_sync(0xffffffffu, row, 0);
@@ -205,8 +229,13 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       if (hb - x.ha < min_positions) hb = x.ha = 0;
       x.hb = hb;
       x.tiles = (hb - x.ha + kN - 1) / kN;
+      own += seen - (float)x.m * (float)(hb - x.ha);
     }
     const int blocks = (x.m * g + kUnitRows - 1) / kUnitRows;
+    if (x.tiles) {
+      const float last = x.m * g - (blocks - 1) * kUnitRows > kM ? costs.tile : costs.tile_one;
+      work += (float)n_kv_heads * (float)(x.tiles + kTileCost) * ((float)(blocks - 1) * costs.tile + last);
+    }
     if (lane == 0) {
       places_of[warp] = x.tiles ? (long long)n_kv_heads * blocks * (x.tiles + kTileCost) : 0;
       shared_of[warp] = x.tiles ? x.m : 0;
@@ -249,13 +278,28 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       s.hole[i] = make_int2(0, 0);
       s.query[i].tiles = 0;
     }
-    if (tid == 0) *s.head = PlanHead{0, 0, 0, 0};
+    if (tid == 0) *s.head = PlanHead{0, 0, 0, 0, grid * costs.ctas_sm};
     return;
   }
+  if (lane == 0) {
+    own_of[warp] = own;
+    work_of[warp] = work;
+  }
+  __syncthreads();
   if (tid == 0) {
     s.first[n_groups] = (int)total;
-    const int most = (int)((total + kMinTiles - 1) / kMinTiles), ranges = most < grid ? most : grid;
-    *s.head = PlanHead{(int)total, ranges, ranges ? (int)total / ranges : 0, ranges ? (int)total % ranges : 0};
+    float positions = 0.0f, a = 0.0f;
+    for (int i = 0; i < 32; ++i) {
+      positions += own_of[i];
+      a += work_of[i];
+    }
+    // The prefixes and the sequences' own positions run side by side: SMs in the proportion of what they take
+    const float b = n_kv_heads * (costs.position * positions + costs.unit * (float)n);
+    int mine = (int)((float)grid * a / (a + b) + 0.5f);
+    mine = mine < 1 ? 1 : mine < grid - 1 ? mine : grid - 1;
+    const int most = (int)((total + kMinTiles - 1) / kMinTiles), ranges = most < mine ? most : mine;
+    *s.head = PlanHead{(int)total, ranges, ranges ? (int)total / ranges : 0, ranges ? (int)total % ranges : 0,
+                       (grid - ranges) * costs.ctas_sm};
   }
 }
 
@@ -943,7 +987,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   if (f1 > f0) {
     const int blocks = (g + kRows - 1) / kRows, in_kv = h - hk * g, unit = hk * blocks + in_kv / kRows, r = in_kv % kRows;
     const int nch = f1 - f0, u0 = f0 * a.n_kv_heads * blocks + unit * nch;
-    const PlanHead by{(int)cut.total, cut.ranges, (int)cut.total / cut.ranges, (int)cut.total % cut.ranges};
+    const PlanHead by{(int)cut.total, cut.ranges, (int)cut.total / cut.ranges, (int)cut.total % cut.ranges, 0};
     const int b0 = by.range_of(u0 + kUnitCost), b1 = by.range_of(u0 + nch - 1);
     if (b1 > b0) {                   // cut: what lies in own was not written
       const bool wide = g > 8;
@@ -1049,9 +1093,9 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
                                       const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream) {
   const Space s = space_of(a, c, n, n_groups, ws);
   // A prefix that is read again and again comes from L2, at some 11 TB/s; sharing costs launches, a join and the plan.  By
-  // themselves / shared, us, for one group (8 KV heads of 128, 16 bits): 64 sequences of 612 positions 25 / 31, of 2148
-  // 61 / 32; 16 of 2148 25 / 29, of 8292 63 / 43; 4 of 8292 26 / 35, of 32,868 62 / 54; 2 of 32,868 41 / 52.  In 4 bits: 16
-  // of 2148 25 / 26, of 8292 46 / 40; 64 of 612 24 / 34, of 2148 44 / 35.  So it goes by the bytes that sharing can save;
+  // themselves / shared, us, for one group (8 KV heads of 128, 16 bits): 64 sequences of 612 positions 25 / 29, of 2148
+  // 61 / 31; 16 of 2148 25 / 25, of 8292 63 / 35; 4 of 8292 27 / 32, of 32,868 62 / 50; 2 of 32,868 41 / 48.  In 4 bits: 16
+  // of 2148 24 / 27, of 8292 45 / 39; 64 of 612 24 / 34, of 2148 43 / 33.  So it goes by the bytes that sharing can save;
   // those of 4 bits take longer.
   const long long all = 2ll * c.n_kv_heads * (long long)(kv_head_bytes(c) / c.page_size) * max_len;
   const long long saved = (c.dtype == QRE_E2M1 ? all * 3 / 2 : all) * (n > n_groups ? n - n_groups : 0);
@@ -1068,8 +1112,9 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
         !make_tmap_bf16(&tk16, k, rows, c.head_dim, 16) || !make_tmap_bf16(&tv16, v, rows, c.head_dim, 16))
       return launch_attn_decode(a, c, layer, n, seqs, max_len, q, o, lse, s.decode, status, stream);
   }
+  const Costs costs = costs_of(c, ctas_per_sm(c.dtype, a.head_dim, g > 8));
   cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(1024), 0, stream, c, n, seqs, n_groups, cu_group,
-                                   common_len, a.window, g, a.n_kv_heads, kN, grid, s, status);
+                                   common_len, a.window, g, a.n_kv_heads, kN, grid, costs, s, status);
   if (e != cudaSuccess) return e;
   auto prefix = [&](auto dt, auto ct, auto d) -> cudaError_t {
     constexpr int DT = decltype(dt)::value, CT = decltype(ct)::value, D = decltype(d)::value;
@@ -1101,7 +1146,8 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   Cuts cuts = {};
   for (int i = 0; i < n; i += most) {
     const int m = n - i < most ? n - i : most;
-    const Own own{s.hole + i, s.own_o + (size_t)i * a.n_heads * a.head_dim, s.own_ml + (size_t)i * a.n_heads, i == 0};
+    const Own own{s.hole + i, s.own_o + (size_t)i * a.n_heads * a.head_dim, s.own_ml + (size_t)i * a.n_heads, i == 0,
+                  i == 0 ? &s.head->own_ctas : nullptr};
     e = launch_part<true>(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
                           static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, own, s.decode,
                           status, stream, most >= n ? &cuts : nullptr);
