@@ -950,18 +950,22 @@ __device__ __forceinline__ int part_index(int cache_type, bool wide, int r, int 
   return (((wide ? 2 * i + (r >> 3) : i) * 4 + (r & 1) + 2 * high) << 5) + 4 * row + ((r & 7) >> 1);
 }
 
-// A warp per query head: its own part (or parts, where the decode kernel's ranges cut its positions and the join is left
-// to this kernel: a launch of its own took 5 us), then those of the prefix, all in the order of the ranges.
+// `ways` warps per query head: its own part (or parts, where the decode kernel's ranges cut its positions and the join is
+// left to this kernel: a launch of its own took 5 us) and those of the prefix in the order of the ranges, 16 at a time by
+// a warp, the warps' results in their order.
+constexpr int kAhead = 16;             // parts of a warp whose O is on its way together
 template <int DT, int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ qre_attn a, int n, int cache_type,
                                                           const float* __restrict__ v_scale, uint16_t* __restrict__ o,
-                                                          float* __restrict__ lse, const __grid_constant__ Space s, Cuts cuts) {
+                                                          float* __restrict__ lse, const __grid_constant__ Space s, Cuts cuts, int ways) {
   constexpr int E = D / 32;
+  __shared__ float2 way_ml[8];
+  __shared__ float way_x[8][D];
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (id >= (long long)n * a.n_heads) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = warp & (ways - 1);
+  const long long id = ((long long)blockIdx.x * 8 + warp) / ways;
+  if (id >= (long long)n * a.n_heads) return;   // (all of a CTA's warps where they have others to wait for)
   const int t = (int)(id / a.n_heads), h = (int)(id - (long long)t * a.n_heads);
   // what does not depend on the plan's answer is on its way beside it
   const Query x = s.query[t];
@@ -980,7 +984,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   }
   const int g = a.n_heads / a.n_kv_heads, hk = h / g;
   const float vs = v_scale ? v_scale[hk] : 1.0f;
-  float M = own_ml.x, L = own_ml.y, X[E];
+  float M = way ? -INFINITY : own_ml.x, L = way ? 0.0f : own_ml.y, X[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) X[e] = M == -INFINITY ? 0.0f : own[e];
   bool joined = false;               // of parts, all of its result if it has no hole
@@ -1001,7 +1005,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < E; ++e) at[e] = part_index(cache_type, wide, r, E * lane + e);
 #pragma unroll 4
-      for (int b = b0; b <= b1; ++b) {
+      for (int b = way ? b1 + 1 : b0; b <= b1; ++b) {
         // the first part lies in its range's first place when the unit begins there too; the others begin theirs
         const float* part = cuts.parts + ((size_t)2 * b + (b == b0 && by.begin(b0) < u0 ? 1 : 0)) * floats;
         const float2 ml = reinterpret_cast<const float2*>(part + (wide ? 16 : 8) * D)[r];
@@ -1029,8 +1033,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
       const int b = b0 + i / copies, k = i - i / copies * copies;
       return base + (long long)kUnitRows * b + (long long)k * in_block;
     };
-    constexpr int kAhead = 16;         // parts whose O is on its way together
-    for (int i0 = 0; i0 < parts; i0 += kAhead) {   // a lane has a part's reference and sum
+    for (int i0 = kAhead * way; i0 < parts; i0 += kAhead * ways) {   // a lane has a part's reference and sum
       const int mine = parts - i0 < kAhead ? parts - i0 : kAhead;
       float2 ml = make_float2(-INFINITY, 0.0f);
       if (lane < mine) ml = s.part_ml[row_of(i0 + lane)];
@@ -1073,6 +1076,25 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
       }
     }
   }
+  if (ways > 1) {                      // (what is asked above is the same for all warps of a head)
+    if (way) {
+      if (lane == 0) way_ml[warp] = make_float2(M, L);
+#pragma unroll
+      for (int e = 0; e < E; ++e) way_x[warp][E * lane + e] = X[e];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / ways), "r"(32 * ways) : "memory");
+    if (way) return;
+    for (int w = warp + 1; w < warp + ways; ++w) {
+      const float2 ml = way_ml[w];
+      if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+      const float to = fmaxf(M, ml.x);
+      const float f = M == to ? 1.0f : ex2(M - to), fe = ml.x == to ? 1.0f : ex2(ml.x - to);
+      M = to;
+      L = L * f + ml.y * fe;
+#pragma unroll
+      for (int e = 0; e < E; ++e) X[e] = X[e] * f + way_x[w][E * lane + e] * fe;
+    }
+  }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   uint16_t* out = o + (size_t)t * a.o_token + (size_t)h * a.o_head + E * lane;
   if (E == 4)
@@ -1094,8 +1116,8 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   const Space s = space_of(a, c, n, n_groups, ws);
   // A prefix that is read again and again comes from L2, at some 11 TB/s; sharing costs launches, a join and the plan.  By
   // themselves / shared, us, for one group (8 KV heads of 128, 16 bits): 64 sequences of 612 positions 25 / 29, of 2148
-  // 61 / 31; 16 of 2148 25 / 25, of 8292 63 / 35; 4 of 8292 27 / 32, of 32,868 62 / 50; 2 of 32,868 41 / 48.  In 4 bits: 16
-  // of 2148 24 / 27, of 8292 45 / 39; 64 of 612 24 / 34, of 2148 43 / 33.  So it goes by the bytes that sharing can save;
+  // 61 / 31; 16 of 2148 25 / 24, of 8292 63 / 33; 4 of 8292 27 / 28, of 32,868 62 / 47; 2 of 32,868 41 / 45.  In 4 bits: 16
+  // of 2148 24 / 27, of 8292 45 / 37; 64 of 612 24 / 34, of 2148 43 / 33.  So it goes by the bytes that sharing can save;
   // those of 4 bits take longer.
   const long long all = 2ll * c.n_kv_heads * (long long)(kv_head_bytes(c) / c.page_size) * max_len;
   const long long saved = (c.dtype == QRE_E2M1 ? all * 3 / 2 : all) * (n > n_groups ? n - n_groups : 0);
@@ -1154,9 +1176,19 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
     if (e != cudaSuccess) return e;
   }
   const float* v_scale = low && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;
-  const dim3 warps((unsigned)(((long long)n * a.n_heads + 7) / 8));
+  // Few heads with many parts of the prefix each: more warps for a head, while SMs have room (two CTAs on each).  The
+  // parts of a unit are as many as its share of the ranges, two of a range where its chains take tiles in turn.  (16
+  // sequences behind 32,768, us with one warp / this: 2 KV heads of 64 50 / 32, 8 of 128 61 / 58; 64 behind 8192 with 2 of
+  // 64 29 / 27.)
+  const long long heads = (long long)n * a.n_heads, rows = (long long)n * g / n_groups;
+  const long long units = (long long)n_groups * a.n_kv_heads * ((rows + kUnitRows - 1) / kUnitRows);
+  const long long parts = (rows <= kM ? 2 : 1) * grid / (units > 0 ? units : 1);
+  int ways = 1;
+  while (ways < 8 && parts > kAhead * ways && heads * ways <= 8ll * grid) ways *= 2;
+  const dim3 ctas((unsigned)((heads * ways + 7) / 8));
   auto join = [&](auto kernel) {
-    return launch_dependent(kernel, warps, dim3(256), 0, stream, a, n, c.dtype, v_scale, static_cast<uint16_t*>(o), lse, s, cuts);
+    return launch_dependent(kernel, ctas, dim3(256), 0, stream, a, n, c.dtype, v_scale, static_cast<uint16_t*>(o), lse, s,
+                            cuts, ways);
   };
   if (bf) return a.head_dim == 64 ? join(shared_join_kernel<QRE_BF16, 64>) : join(shared_join_kernel<QRE_BF16, 128>);
   return a.head_dim == 64 ? join(shared_join_kernel<QRE_FP16, 64>) : join(shared_join_kernel<QRE_FP16, 128>);

@@ -196,6 +196,25 @@ def test_long_prefix_and_many_queries():
     assert float((d / (plain.float().abs() + 0.02)).max()) < 2.0 ** -5
 
 
+# one KV head's prefix lies in 76 ranges of CTAs, two parts of each: several warps of the join for a query head
+@pytest.mark.parametrize("prompts,owns,H,Hk,D,kind,cache,window", [
+    ([30000], [[1, 70, 9]], 3, 1, 64, "bf16", "bf16", 0),                  # 8 warps, some for two rounds
+    ([29000], [[5, 400]], 2, 2, 128, "fp16", "fp16", 0),
+    ([9000, 9100], [[1, 2, 900], [33, 4]], 5, 5, 128, "bf16", "e2m1", 0),    # 2 warps; heads that fill no CTA
+    ([30000], [[3] * 50], 4, 1, 64, "bf16", "e4m3", 0),                    # 200 rows
+    ([20000], [[3, 1000, 60]], 7, 1, 128, "fp16", "e2m1", 12000),
+    ([20000], [[3, 5000, 60]], 6, 2, 64, "bf16", "bf16", 4000),              # one sequence sees no shared position
+])
+def test_long_prefixes_of_few_heads(prompts, owns, H, Hk, D, kind, cache, window):
+    w = Shared(prompts, owns, H, Hk, D, 64, kind, cache, cache in ("e4m3", "e2m1"), 77)
+    q = randn((len(w.seqs), H, D), 78, kind, 1.5)
+    ref, v_max = w.reference(q, window)
+    o, lse = run(w, q, window)
+    check(o, lse, ref, kind, max(w.lens), v_max)
+    o2, lse2 = run(w, q, window)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_common_lengths():
     w = Shared([300, 64, 0, 130, 500], [[1, 5, 40], [1, 1], [7, 8], [3], [1] * 70], 2, 1, 64, 16, "bf16", "bf16")
     assert w.common().tolist() == [288, 64, 0, 0, 496]
