@@ -19,12 +19,13 @@
 // whole tile, and ends with a common page, behind which the last tile's rows are zeroed.
 //
 // What it measured (calls with the common lengths found in front of them, us): 64 sequences of up to 1500 positions
-// behind 16,384, 32 heads on 8, D = 128, bf16: 71 (each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
-// 51 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 67 (265; the products take 18).  10 us of a launch of the
+// behind 16,384, 32 heads on 8, D = 128, bf16: 72 (each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
+// 51 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 62 (265; the products take 18).  10 us of a launch of the
 // prefixes are its begin (the plan, the queries, the first tile's references) and 3 its end (parts).  Steps, on the
 // first: 119 at first; queries by asynchronous copies, one copy of the softmax's code, 32-bit places and a join that asks
 // for its parts at once 97; the own positions begun beside the prefixes 91; the last join for all parts 84; SMs for the
-// prefixes and others for the own positions, not all for both in turn, 71.  No gain: a round of the softmax's code before
+// prefixes and others for the own positions, not all for both in turn, 72.  The last one: 67, then 62 with the turn
+// handed over behind the scores and four widened tiles in the ring, not three (4600 -> 3950 cycles a tile).  No gain: a round of the softmax's code before
 // the plan is there, for the instruction cache.  In 4 bits 4 warps that widen took 2 us more than 8.
 #include <type_traits>
 
@@ -131,21 +132,19 @@ Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, vo
 
 // ---------------------------------------------------------------- the plan
 
-// What the work takes, ns of an SM: a tile of a unit with more than kM rows and with less, and a position and a unit of
-// the sequences' own.  Fitted to calls that gave the prefixes 16 to 151 of the 152 SMs; with these, seven calls of all
-// types and head sizes came within 4 % of their best split (8 bits: 9 %).
+// What the work takes, ns of an SM: a tile of a unit, and a position and a unit of the sequences' own.  Fitted to calls
+// that gave the prefixes 16 to 151 of the 152 SMs; with these, seven calls of all types and head sizes came within 4 % of
+// their best split.
 struct Costs {
-  float tile, tile_one, position, unit;
+  float tile, position, unit;
   int ctas_sm;           // CTAs of the decode kernel on an SM
 };
 
 Costs costs_of(const qre_kv_cache& c, int ctas_sm) {
   const bool d64 = c.head_dim == 64;
-  const float tile = c.dtype == QRE_E2M1 || c.dtype == QRE_E4M3 ? (d64 ? 1670.0f : 2100.0f) : d64 ? 1380.0f : 1750.0f;
-  const float position = c.dtype == QRE_E2M1 ? (d64 ? 3.4f : 5.0f) : c.dtype == QRE_E4M3 ? (d64 ? 3.5f : 6.1f) : d64 ? 4.5f : 7.9f;
-  // (a tile of 8 or 4 bits is widened once, for however few rows)
-  const float one = c.dtype == QRE_E2M1 || c.dtype == QRE_E4M3 ? 0.85f : 0.7f;
-  return Costs{tile, one * tile, position, 100.0f, ctas_sm};
+  if (c.dtype == QRE_E2M1) return d64 ? Costs{1650.0f, 2.7f, 500.0f, ctas_sm} : Costs{1800.0f, 3.8f, 600.0f, ctas_sm};
+  if (c.dtype == QRE_E4M3) return d64 ? Costs{1550.0f, 2.9f, 400.0f, ctas_sm} : Costs{1750.0f, 5.1f, 500.0f, ctas_sm};
+  return d64 ? Costs{1100.0f, 3.7f, 400.0f, ctas_sm} : Costs{1270.0f, 7.4f, 400.0f, ctas_sm};
 }
 
 // One CTA, a warp per group: the positions that it shares, [ha, hb): hb the common length in whole runs of 16 whose
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
   __shared__ int scan_m[33];
   __shared__ long long places_of[32];
   __shared__ int shared_of[32];
-  __shared__ float own_of[32], work_of[32];
+  __shared__ float own_of[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
   const int ps_shift = 31 - __clz(c.page_size);
   long long total = 0;
   int before = 0;
-  float own = 0.0f, work = 0.0f;     // positions of this warp's sequences that are not shared; its groups' tiles, ns
+  float own = 0.0f;                  // positions of this warp's sequences that are not shared
   for (int g0 = 0; g0 < n_groups; g0 += 32) {
     const int gi = g0 + warp;
     Group x = {};
@@ -232,10 +231,6 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       own += seen - (float)x.m * (float)(hb - x.ha);
     }
     const int blocks = (x.m * g + kUnitRows - 1) / kUnitRows;
-    if (x.tiles) {
-      const float last = x.m * g - (blocks - 1) * kUnitRows > kM ? costs.tile : costs.tile_one;
-      work += (float)n_kv_heads * (float)(x.tiles + kTileCost) * ((float)(blocks - 1) * costs.tile + last);
-    }
     if (lane == 0) {
       places_of[warp] = x.tiles ? (long long)n_kv_heads * blocks * (x.tiles + kTileCost) : 0;
       shared_of[warp] = x.tiles ? x.m : 0;
@@ -281,20 +276,14 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
     if (tid == 0) *s.head = PlanHead{0, 0, 0, 0, grid * costs.ctas_sm};
     return;
   }
-  if (lane == 0) {
-    own_of[warp] = own;
-    work_of[warp] = work;
-  }
+  if (lane == 0) own_of[warp] = own;
   __syncthreads();
   if (tid == 0) {
     s.first[n_groups] = (int)total;
-    float positions = 0.0f, a = 0.0f;
-    for (int i = 0; i < 32; ++i) {
-      positions += own_of[i];
-      a += work_of[i];
-    }
+    float positions = 0.0f;
+    for (int i = 0; i < 32; ++i) positions += own_of[i];
     // The prefixes and the sequences' own positions run side by side: SMs in the proportion of what they take
-    const float b = n_kv_heads * (costs.position * positions + costs.unit * (float)n);
+    const float a = costs.tile * (float)total, b = n_kv_heads * (costs.position * positions + costs.unit * (float)n);
     int mine = (int)((float)grid * a / (a + b) + 0.5f);
     mine = mine < 1 ? 1 : mine < grid - 1 ? mine : grid - 1;
     const int most = (int)((total + kMinTiles - 1) / kMinTiles), ranges = most < mine ? most : mine;
@@ -315,8 +304,8 @@ struct Shape {
   static constexpr int RB = F4 ? D / 2 : F8 ? D : 2 * D;   // bytes of a stored row, without scales
   static constexpr int SB = F4 ? D / kBlock4 : 0;
   static constexpr int RAW = kN * (RB + SB);         // bytes of a stored tile
-  static constexpr int SLOTS = D == 128 ? (LOW ? 3 : 5) : (LOW ? 6 : 10);
-  static constexpr int STAGES = !LOW ? 0 : F8 ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
+  static constexpr int SLOTS = D == 128 ? (LOW ? 4 : 5) : (LOW ? 8 : 10);
+  static constexpr int STAGES = !LOW ? 0 : F8 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 6);
   static constexpr int THREADS = LOW ? 640 : 384;
   // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88; 640 x 96 = 61,440 > 256 x 152 + 384 x 56.
   static constexpr int SOFT_REGS = LOW ? 152 : 208, OTHER_REGS = LOW ? 56 : 88;
@@ -575,9 +564,11 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
         };
         ok = wait_for(q_full, np);
         ++np;
-        // Steps of a chain: P V of a tile and the scores of its next one.  The chains take them in turn, 0 first: left to
-        // themselves they fall into step, both softmaxes run at once, and the tensor cores wait (3600 cycles a tile).  The
-        // turn is handed over where the other chain has a step next; it has as many as this one, or chain 1 one less.
+        // Steps of a chain: P V of a tile and the scores of its next one.  The chains take them in turn, 0 first, and hand
+        // the turn over behind the scores: if the other's P V may come between the two, the chains fall into step, both
+        // softmaxes (1200 cycles) run at once and then all products (2150): 3400 cycles a tile, 2950 so.  The turn is
+        // handed over where the other chain has a step next; it has as many as this one, or chain 1 one less.  The next
+        // scores wait for no slot that the other chain's step frees: there are four at least.
         const int first = w.first(t), step = w.step(), count = w.count(t), other = w.count(t ^ 1);
         auto pass_by = [&](int j) {      // the other chain's tile: not read here
           ok = wait_tile(i0 + 2 * j) && wait_tile(i0 + 2 * j + 1);
@@ -613,8 +604,6 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           umma_commit_lead(&o_done[t], lead);
           umma_commit_lead(&empty[slot], lead);
           ++n;
-          if (lead && (t ? k + 1 < other : k < other)) mbar_arrive(&turn[t ^ 1]);
-          __syncwarp();
           if (!both && j + 1 < w.tiles) pass_by(j + 1);
           if (ok && k + 1 < count) {     // over P: issued behind the product that reads it
             ok = wait_tile(i0 + 2 * (j + step));
@@ -622,6 +611,8 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
             tc_fence_after();
             scores(i0 + 2 * (j + step));
           }
+          if (ok && lead && (t ? k + 1 < other : k < other)) mbar_arrive(&turn[t ^ 1]);
+          __syncwarp();
         }
         i0 += 2 * w.tiles;
       }
@@ -951,9 +942,9 @@ __device__ __forceinline__ int part_index(int cache_type, bool wide, int r, int 
 }
 
 // `ways` warps per query head: its own part (or parts, where the decode kernel's ranges cut its positions and the join is
-// left to this kernel: a launch of its own took 5 us) and those of the prefix in the order of the ranges, 16 at a time by
+// left to this kernel: a launch of its own took 5 us) and those of the prefix in the order of the ranges, 20 at a time by
 // a warp, the warps' results in their order.
-constexpr int kAhead = 16;             // parts of a warp whose O is on its way together
+constexpr int kAhead = 20;             // parts of a warp whose O is on its way together
 template <int DT, int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ qre_attn a, int n, int cache_type,
                                                           const float* __restrict__ v_scale, uint16_t* __restrict__ o,
