@@ -1106,9 +1106,9 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
                                       const void* q, void* o, float* lse, void* ws, int* status, cudaStream_t stream) {
   const Space s = space_of(a, c, n, n_groups, ws);
   // A prefix that is read again and again comes from L2, at some 11 TB/s; sharing costs launches, a join and the plan.  By
-  // themselves / shared, us, for one group (8 KV heads of 128, 16 bits): 64 sequences of 612 positions 25 / 29, of 2148
-  // 61 / 31; 16 of 2148 25 / 24, of 8292 63 / 33; 4 of 8292 27 / 28, of 32,868 62 / 47; 2 of 32,868 41 / 45.  In 4 bits: 16
-  // of 2148 24 / 27, of 8292 45 / 37; 64 of 612 24 / 34, of 2148 43 / 33.  So it goes by the bytes that sharing can save;
+  // themselves / shared, us, for one group (8 KV heads of 128, 16 bits): 64 sequences of 612 positions 25 / 28, of 2148
+  // 61 / 30; 16 of 2148 25 / 24, of 8292 63 / 31; 4 of 8292 26 / 28, of 32,868 62 / 46; 2 of 32,868 41 / 45.  In 4 bits: 16
+  // of 2148 24 / 28, of 8292 45 / 30; 64 of 612 23 / 33, of 2148 43 / 32.  So it goes by the bytes that sharing can save;
   // those of 4 bits take longer.
   const long long all = 2ll * c.n_kv_heads * (long long)(kv_head_bytes(c) / c.page_size) * max_len;
   const long long saved = (c.dtype == QRE_E2M1 ? all * 3 / 2 : all) * (n > n_groups ? n - n_groups : 0);
