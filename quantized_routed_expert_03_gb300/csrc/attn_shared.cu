@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "attn_decode.cuh"
+#include "attn_split.h"
 #include "tc.cuh"
 
 namespace qre {
@@ -942,7 +943,7 @@ __device__ __forceinline__ int part_index(int cache_type, bool wide, int r, int 
 }
 
 // `ways` warps per query head: its own part (or parts, where the decode kernel's ranges cut its positions and the join is
-// left to this kernel: a launch of its own took 5 us) and those of the prefix in the order of the ranges, 20 at a time by
+// left to this kernel: a launch of its own took 5 us; their places are below 2^31 then, see attn_split.h) and those of the prefix in the order of the ranges, 20 at a time by
 // a warp, the warps' results in their order.
 constexpr int kAhead = 20;             // parts of a warp whose O is on its way together
 template <int DT, int D>
@@ -1156,6 +1157,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   const long long places = (a.window > 0 && a.window < held ? a.window : held) / chunk + 3 + kUnitCost;
   int most = 0x7fffffffll / places < n ? (int)(0x7fffffffll / places) : n;
   most = most < kPartQueries ? most : kPartQueries;
+  const bool leave = most >= n && shared_join_counts(n, places, (long long)a.n_kv_heads * ((g + kRows - 1) / kRows));
   Cuts cuts = {};
   for (int i = 0; i < n; i += most) {
     const int m = n - i < most ? n - i : most;
@@ -1163,7 +1165,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
                   i == 0 ? &s.head->own_ctas : nullptr};
     e = launch_part<true>(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
                           static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, own, s.decode,
-                          status, stream, most >= n ? &cuts : nullptr);
+                          status, stream, leave ? &cuts : nullptr);
     if (e != cudaSuccess) return e;
   }
   const float* v_scale = low && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;

@@ -1,0 +1,50 @@
+"""What the host works out of a decode call's sizes before it launches (csrc/attn_split.h), compiled by itself: no GPU
+needed."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import quantized_routed_expert_03_gb300 as qre
+
+CSRC = os.path.join(os.path.dirname(qre.__file__), "csrc")
+PROGRAM = """
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include "attn_split.h"
+int main(int argc, char** argv) {
+  long long x[16] = {};
+  for (int i = 2; i < argc; ++i) x[i - 2] = atoll(argv[i]);
+  long long r = -1;
+  if (!strcmp(argv[1], "join_counts")) r = qre::shared_join_counts(x[0], x[1], x[2]);
+  printf("%lld", r);
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def call(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    where = tmp_path_factory.mktemp("split")
+    (where / "split.cpp").write_text(PROGRAM)
+    subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror", "-I", CSRC, "-o", str(where / "split"), str(where / "split.cpp")],
+                   check=True)
+
+    def run(name, *args):
+        out = subprocess.run([str(where / "split"), name, *map(str, args)], capture_output=True, text=True)
+        assert out.returncode == 0, f"{name}{args} ended with {out.returncode}"
+        return int(out.stdout)
+    return run
+
+
+def test_the_shared_join_counts_only_what_31_bits_hold(call):
+    """The places of a call, and the first place of any unit, are at most queries * places * units."""
+    for n, places, units in ((1, 5, 1), (64, 1030, 8), (128, 65541, 256), (128, 65541, 255), (1024, 8197, 8), (1024, 8197, 255),
+                             (1024, 8197, 256), (2, 2 ** 30 - 1, 1), (1, 2 ** 31 - 1, 1), (1, 2 ** 31 - 1, 2), (15, 2 ** 27, 1),
+                             (15, 2 ** 27, 2), (1, 2 ** 27 + 5, 1024)):
+        assert call("join_counts", n, places, units) == (n * places * units <= 2 ** 31 - 1), (n, places, units)
