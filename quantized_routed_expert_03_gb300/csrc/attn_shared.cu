@@ -1169,15 +1169,8 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
     if (e != cudaSuccess) return e;
   }
   const float* v_scale = low && c.v_scale ? c.v_scale + (size_t)layer * c.n_kv_heads : nullptr;
-  // Few heads with many parts of the prefix each: more warps for a head, while SMs have room (two CTAs on each).  The
-  // parts of a unit are as many as its share of the ranges, two of a range where its chains take tiles in turn.  (16
-  // sequences behind 32,768, us with one warp / this: 2 KV heads of 64 50 / 32, 8 of 128 61 / 58; 64 behind 8192 with 2 of
-  // 64 29 / 27.)
-  const long long heads = (long long)n * a.n_heads, rows = (long long)n * g / n_groups;
-  const long long units = (long long)n_groups * a.n_kv_heads * ((rows + kUnitRows - 1) / kUnitRows);
-  const long long parts = (rows <= kM ? 2 : 1) * grid / (units > 0 ? units : 1);
-  int ways = 1;
-  while (ways < 8 && parts > kAhead * ways && heads * ways <= 8ll * grid) ways *= 2;
+  const int ways = shared_join_ways(n, a.n_heads, a.n_kv_heads, n_groups, grid, kUnitRows, kAhead);
+  const long long heads = (long long)n * a.n_heads;
   const dim3 ctas((unsigned)((heads * ways + 7) / 8));
   auto join = [&](auto kernel) {
     return launch_dependent(kernel, ctas, dim3(256), 0, stream, a, n, c.dtype, v_scale, static_cast<uint16_t*>(o), lse, s,

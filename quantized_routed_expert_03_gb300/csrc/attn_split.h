@@ -11,4 +11,19 @@ inline bool shared_join_counts(long long n, long long places, long long units) {
   return n * places <= 0x7fffffffll / units;
 }
 
+// Warps of the join for a query head.  Few heads with many parts of the prefix each get more, while SMs have room (two
+// CTAs on each); the parts of a unit of unit_rows rows are as many as its share of the `grid` ranges, two of a range where
+// its chains take tiles in turn, and a warp has `ahead` on their way.  (16 sequences behind 32,768, us with one warp /
+// this: 2 KV heads of 64 50 / 32, 8 of 128 61 / 58; 64 behind 8192 with 2 of 64 29 / 27.)  Without groups nothing is
+// shared, and a warp is enough.
+inline int shared_join_ways(long long n, int n_heads, int n_kv_heads, int n_groups, int grid, int unit_rows, int ahead) {
+  if (n_groups <= 0) return 1;
+  const long long heads = n * n_heads, rows = n * (n_heads / n_kv_heads) / n_groups;
+  const long long units = (long long)n_groups * n_kv_heads * ((rows + unit_rows - 1) / unit_rows);
+  const long long parts = (2 * rows <= unit_rows ? 2 : 1) * grid / (units > 0 ? units : 1);
+  int ways = 1;
+  while (ways < 8 && parts > (long long)ahead * ways && heads * ways <= 8ll * grid) ways *= 2;
+  return ways;
+}
+
 }  // namespace qre

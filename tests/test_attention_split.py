@@ -20,6 +20,7 @@ int main(int argc, char** argv) {
   for (int i = 2; i < argc; ++i) x[i - 2] = atoll(argv[i]);
   long long r = -1;
   if (!strcmp(argv[1], "join_counts")) r = qre::shared_join_counts(x[0], x[1], x[2]);
+  if (!strcmp(argv[1], "join_ways")) r = qre::shared_join_ways(x[0], x[1], x[2], x[3], x[4], x[5], x[6]);
   printf("%lld", r);
 }
 """
@@ -48,3 +49,14 @@ def test_the_shared_join_counts_only_what_31_bits_hold(call):
                              (1024, 8197, 256), (2, 2 ** 30 - 1, 1), (1, 2 ** 31 - 1, 1), (1, 2 ** 31 - 1, 2), (15, 2 ** 27, 1),
                              (15, 2 ** 27, 2), (1, 2 ** 27 + 5, 1024)):
         assert call("join_counts", n, places, units) == (n * places * units <= 2 ** 31 - 1), (n, places, units)
+
+
+def test_warps_of_the_shared_join_for_any_number_of_groups(call):
+    def ways(n, heads, kv_heads, groups):
+        return call("join_ways", n, heads, kv_heads, groups, 152, 256, 20)
+    assert ways(4, 4, 2, 0) == 1 and ways(4096, 64, 8, 0) == 1          # no groups: nothing to divide by
+    for n, groups in ((1, 1), (2, 4096), (4096, 4096), (4096, 1), (1, 4096)):
+        for heads, kv_heads in ((1, 1), (1024, 1), (256, 256), (64, 8)):
+            w = ways(n, heads, kv_heads, groups)
+            assert w in (1, 2, 4, 8) and (w == 1 or n * heads * w // 2 <= 8 * 152)
+    assert ways(3, 3, 1, 1) == 8 and ways(64, 32, 8, 1) == 1

@@ -39,3 +39,26 @@ def test_own_positions_whose_places_pass_31_bits():
     assert float((lse - short - math.log(2 ** 13)).abs().max()) <= 2.0 ** -7 + 1e-4
     size = float(c.v.float().abs().max())
     assert float((o.float() - want.float()).abs().max()) <= size * (2 * 2.0 ** -7 + 4 * 2.0 ** -8)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "e2m1"])
+def test_queries_without_any_group(cache):
+    """No groups are bounds that do not run from 0 to n: each query by itself, and a note."""
+    w = Shared([900, 600], [[5, 70], [3, 4]], 4, 2, 64, 16, "bf16", cache, seed=2)
+    q = randn((4, 4, 64), 1, "bf16")
+    ref, v_max = w.reference(q)
+    att = Attention(w.c, 1, 4, 4, max_groups=1)
+    lse = torch.empty((4, 4), device=DEV)
+    o = att.decode_shared(q, i32(w.seqs), i32([0]), w.c.common_len(i32(w.seqs), i32([0])), lse=lse)
+    assert qre.qre_read_device_status() == qre.QRE_DEV_BAD_INDEX
+    qre.qre_clear_device_status()
+    check(o, lse, ref, "bf16", 970, v_max)
+    # the call itself: no arrays of groups at all
+    size = qre.qre_attn_decode_shared_workspace_size(att._desc(), w.c.desc, 4, 0)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    o.fill_(float("nan"))
+    lse.fill_(float("nan"))
+    qre.qre_attn_decode_shared(att._desc(q, o=o), w.c.desc, 1, 4, i32(w.seqs), 0, None, None, 0, q, o, lse, ws)
+    assert qre.qre_read_device_status() == qre.QRE_DEV_BAD_INDEX
+    qre.qre_clear_device_status()
+    check(o, lse, ref, "bf16", 970, v_max)
