@@ -223,13 +223,27 @@ struct Own {
   const int2* hole;   // [n]
   float* o;           // [n][n_heads][D]
   float2* ml;         // [n][n_heads]
-  // The launch before this one in the stream computes the holes' positions; this one needs nothing of it, only of the
-  // ones before.  So it begins where SMs are free already, and its first CTA waits for that launch at its end: then
-  // what comes behind this launch comes behind both.  *ctas: how many of its CTAs have work (the SMs that the launch
-  // before leaves; NULL: all).
+  // The launch before this one in the stream (the prefixes) computes the holes' positions; this one needs nothing of it,
+  // only of the ones before.  So it begins where SMs are free already, and its first CTA waits for that launch at its end:
+  // then what comes behind this launch comes behind both.  What the ones before wrote (the plan, and by way of the plan all
+  // that is older) it has from the launch of the prefixes: that one waits for the plan, then releases *ready = token, then
+  // lets this one begin.  A thread that acquires the token has seen it all; one that does not waits for the prefixes to end,
+  // as any other kernel would.  The plan sets *ready to 0, and every call has another token, so that an older one is none.
+  // *ctas: how many of its CTAs have work (the SMs that the launch before leaves; NULL: all).
   int late;
+  uint32_t token;
+  const uint32_t* ready;
   const int* ctas;
 };
+
+__device__ __forceinline__ void release_token(uint32_t* p, uint32_t token) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(token) : "memory");
+}
+__device__ __forceinline__ uint32_t acquire_token(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 template <bool SH>
 struct Seq {
@@ -363,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
 
   // (late: see Own)
   const bool late = SH && own.late;
-  if (!late) grid_dependency_wait();
+  if (!late || acquire_token(own.ready) != own.token) grid_dependency_wait();
   grid_dependents_launch();
   auto leave = [&]() {
     if (SH && late && blockIdx.x == 0) grid_dependency_wait();

@@ -27,6 +27,7 @@
 // prefixes and others for the own positions, not all for both in turn, 72.  The last one: 67, then 62 with the turn
 // handed over behind the scores and four widened tiles in the ring, not three (4600 -> 3950 cycles a tile).  No gain: a round of the softmax's code before
 // the plan is there, for the instruction cache.  In 4 bits 4 warps that widen took 2 us more than 8.
+#include <atomic>
 #include <type_traits>
 
 #include "attn_decode.cuh"
@@ -84,6 +85,7 @@ struct alignas(16) Query {
 // The workspace.
 struct Space {
   PlanHead* head;
+  uint32_t* ready;       // see Own
   int32_t* first;        // [n_groups + 1] places of the groups before
   Group* groups;         // [n_groups]
   int2* hole;            // [n]
@@ -118,6 +120,7 @@ Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, vo
   // pieces of units: rows once or twice, and 256 for each range's end
   const size_t rows = 2 * heads + (size_t)kUnitRows * shared_grid();
   s.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
+  s.ready = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t)));
   s.first = reinterpret_cast<int32_t*>(take(((size_t)n_groups + 1) * sizeof(int32_t)));
   s.groups = reinterpret_cast<Group*>(take((size_t)n_groups * sizeof(Group)));
   s.hole = reinterpret_cast<int2*>(take((size_t)n * sizeof(int2)));
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_dependents_launch();
+  if (tid == 0) *s.ready = 0;
   int bad = 0;
   for (int i = tid; i < n_groups; i += 1024) {
     const int a = cu_group[i], b = cu_group[i + 1];
@@ -312,7 +316,7 @@ struct Shape {
   static constexpr int SOFT_REGS = LOW ? 152 : 208, OTHER_REGS = LOW ? 56 : 88;
   static constexpr int BYTES = 2 * TILE + SLOTS * TILE + STAGES * RAW + 2048;
   // warps 0-7: the two chains' softmax; then
-  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kWiden = 12, kWidenWarps = 8;
+  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kStart = 11, kWiden = 12, kWidenWarps = 8;
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
                          const int32_t* __restrict__ seqs, int n_groups, const uint16_t* __restrict__ q,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                          const __grid_constant__ CUtensorMap tk16, const __grid_constant__ CUtensorMap tv16, int box_rows,
-                         const __grid_constant__ Space space, uint64_t limit_ns, int* status) {
+                         const __grid_constant__ Space space, uint32_t token, uint64_t limit_ns, int* status) {
   using P = Shape<DT, CT, D>;
   extern __shared__ __align__(1024) uint8_t tiles_smem[];   // the swizzle goes by addresses; no static shared memory beside it
   uint8_t* sq = tiles_smem;                   // two query tiles
@@ -462,7 +466,6 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
   Pieces pieces(space, g, a.n_heads);
   auto begin = [&]() {
     grid_dependency_wait();
-    grid_dependents_launch();
     pieces.begin(n_groups);
   };
   const int ps_shift = 31 - __clz(c.page_size);
@@ -534,6 +537,12 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           }
         }
       }
+    } else if (warp == P::kStart) {
+      // ---- lets the next launch begin, and has the plan seen there (see Own): the only warp of a CTA that does
+      grid_dependency_wait();
+      if (blockIdx.x == 0 && lane == 0) release_token(space.ready, token);
+      __syncwarp();
+      grid_dependents_launch();
     } else if (warp == P::kMma || warp == P::kMma + 1) {
       // ---- products: the whole warp, so that the operands stay in uniform registers; a chain each
       // (what an MMA takes comes out of a shuffle from lane 0, so that the compiler knows it is the warp's: as each lane's
@@ -1126,6 +1135,9 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
         !make_tmap_bf16(&tk16, k, rows, c.head_dim, 16) || !make_tmap_bf16(&tv16, v, rows, c.head_dim, 16))
       return launch_attn_decode(a, c, layer, n, seqs, max_len, q, o, lse, s.decode, status, stream);
   }
+  static std::atomic<uint32_t> calls{0};
+  uint32_t token = ++calls;
+  if (token == 0) token = ++calls;   // what the plan sets
   const Costs costs = costs_of(c, ctas_per_sm(c.dtype, a.head_dim, g > 8));
   cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(1024), 0, stream, c, n, seqs, n_groups, cu_group,
                                    common_len, a.window, g, a.n_kv_heads, kN, grid, costs, s, status);
@@ -1137,7 +1149,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
     const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), P::BYTES);
     if (err != cudaSuccess) return err;
     return launch_dependent(kernel, dim3(grid), dim3(P::THREADS), (size_t)P::BYTES, stream, a, c, layer, seqs, n_groups,
-                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, wait_limit_ns(), status);
+                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, token, wait_limit_ns(), status);
   };
   using B = std::integral_constant<int, QRE_BF16>;
   using H = std::integral_constant<int, QRE_FP16>;
@@ -1162,7 +1174,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   for (int i = 0; i < n; i += most) {
     const int m = n - i < most ? n - i : most;
     const Own own{s.hole + i, s.own_o + (size_t)i * a.n_heads * a.head_dim, s.own_ml + (size_t)i * a.n_heads, i == 0,
-                  i == 0 ? &s.head->own_ctas : nullptr};
+                  token, s.ready, i == 0 ? &s.head->own_ctas : nullptr};
     e = launch_part<true>(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
                           static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, own, s.decode,
                           status, stream, leave ? &cuts : nullptr);

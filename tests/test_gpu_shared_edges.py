@@ -62,3 +62,53 @@ def test_queries_without_any_group(cache):
     assert qre.qre_read_device_status() == qre.QRE_DEV_BAD_INDEX
     qre.qre_clear_device_status()
     check(o, lse, ref, "bf16", 970, v_max)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e2m1"])
+def test_plans_that_change_from_call_to_call_on_one_workspace(cache):
+    """The own positions' kernel takes each call's plan (what is shared, how many CTAs it has) and no older one: calls one
+    behind the other, with nothing between them, whose holes and splits differ; then as two graphs, replayed in turn."""
+    w = Shared([6000, 900], [[700, 30, 1, 2000], [5, 70]], 8, 2, 128, 64, "bf16", cache, seed=12)
+    seqs, n, H, D = i32(w.seqs), 6, 8, 128
+    att = Attention(w.c, 1, H, n, max_groups=n)
+    att.workspace.fill_(0xFF)
+    # groups and common lengths: all, none, some, one group alone, the other alone, groups of one, the first in part
+    plans = [([0, 4, 6], [5952, 896]), ([0, 4, 6], [0, 0]), ([0, 4, 6], [2048, 896]), ([0, 4, 6], [5952, 0]),
+             ([0, 4, 6], [0, 896]), ([0, 1, 2, 3, 4, 5, 6], [0] * 6), ([0, 2, 4, 6], [5952, 5952, 896]),
+             ([0, 2, 6], [128, 0])]
+    plans = [(i32(cu), i32(common)) for cu, common in plans]
+    q = [randn((n, H, D), 20 + i, "bf16") for i in range(len(plans))]
+    want = []
+    for (cu, common), x in zip(plans, q):
+        lse = torch.empty((n, H), device=DEV)
+        want.append((att.decode_shared(x, seqs, cu, common, lse=lse).clone(), lse))
+        torch.cuda.synchronize()
+    assert qre.qre_read_device_status() == 0
+    for i in range(len(plans)):
+        ref, v_max = w.reference(q[i])
+        check(*want[i], ref, "bf16", max(w.lens), v_max)
+    order = torch.randperm(20 * len(plans), generator=torch.Generator().manual_seed(1)) % len(plans)
+    got = []
+    for i in order.tolist():
+        lse = torch.empty((n, H), device=DEV)
+        got.append((att.decode_shared(q[i], seqs, *plans[i], lse=lse), lse))
+    torch.cuda.synchronize()
+    for i, (o, lse) in zip(order.tolist(), got):
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+    out = [(torch.empty_like(q[0]), torch.empty((n, H), device=DEV)) for _ in plans]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for half, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            for i in range(half, len(plans), 2):
+                att.decode_shared(q[i], seqs, *plans[i], o=out[i][0], lse=out[i][1])
+    for step in range(20):
+        for o, lse in out:
+            o.fill_(float("nan"))
+            lse.fill_(float("nan"))
+        graphs[step & 1].replay()
+        graphs[1 - (step & 1)].replay()
+        torch.cuda.synchronize()
+        for (o, lse), (wo, wl) in zip(out, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+    assert qre.qre_read_device_status() == 0
