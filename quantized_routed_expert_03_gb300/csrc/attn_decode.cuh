@@ -64,6 +64,7 @@
 
 #include <type_traits>
 
+#include "attn_split.h"
 #include "internal.h"
 #include "kv_rows.cuh"
 
@@ -1267,20 +1268,28 @@ struct Cuts {
   const float* parts;
 };
 
+// What a CTA keeps in shared memory of n queries, and how many CTAs of a launch of n queries an SM holds.
+template <bool SH>
+size_t of_queries(int n) {
+  return (size_t)(n + 1) * sizeof(Seq<SH>);
+}
+template <bool SH>
+int fitting_ctas(const qre_attn& a, const qre_kv_cache& c, int n) {
+  return decode_ctas(ctas_per_sm(c.dtype, a.head_dim, a.n_heads / a.n_kv_heads > 8), device_max_smem_optin(),
+                     (long long)of_queries<SH>(n), 2ll * kWarps * 2 * tile_of(c));
+}
+
 // One launch (and its join; with `left` the join is left to the caller, if there is one): n queries whose places sum up below 2^31; without ids, of the rows from row0 on.
 template <bool SH>
 cudaError_t launch_part(const qre_attn& a, const qre_kv_cache& c, int layer, int n, const int32_t* seqs, int row0,
                         int max_len, const void* q, void* o, float* lse, const Own& own, void* ws, int* status,
                         cudaStream_t stream, Cuts* left = nullptr) {
   const int g = a.n_heads / a.n_kv_heads;
-  const size_t fixed = (size_t)(n + 1) * sizeof(Seq<SH>);
+  const size_t fixed = of_queries<SH>(n);
   const int tile = tile_of(c);
-  // what the CTAs of an SM share (1 KB of each is the system's, and the kernel's static arrays)
-  auto room = [&](int ctas) { return ((long long)device_max_smem_optin() + 1024) / ctas - 1024 - 256 - (long long)fixed; };
-  int ctas_sm = ctas_per_sm(c.dtype, a.head_dim, g > 8);
-  if (room(ctas_sm) < 2ll * kWarps * 2 * tile) ctas_sm = 2;   // calls of many queries
+  const int ctas_sm = fitting_ctas<SH>(a, c, n);
   const int grid = decode_grid(ctas_sm);
-  const int stages = room(ctas_sm) >= 3ll * kWarps * 2 * tile ? 3 : 2;
+  const int stages = decode_room(ctas_sm, device_max_smem_optin(), (long long)fixed) >= 3ll * kWarps * 2 * tile ? 3 : 2;
   const size_t smem = (size_t)stages * kWarps * 2 * tile + fixed;
   Header* header = static_cast<Header*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + header_bytes(n));

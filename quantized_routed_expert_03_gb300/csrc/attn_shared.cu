@@ -1135,10 +1135,16 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
         !make_tmap_bf16(&tk16, k, rows, c.head_dim, 16) || !make_tmap_bf16(&tv16, v, rows, c.head_dim, 16))
       return launch_attn_decode(a, c, layer, n, seqs, max_len, q, o, lse, s.decode, status, stream);
   }
+  // Queries of a launch of the own positions' kernel: chunks are counted in 32 bits (see launch_attn_decode; a hole makes one
+  // more)
+  const long long chunk = chunk_of(c), held = (long long)c.max_pages * c.page_size;
+  const long long places = (a.window > 0 && a.window < held ? a.window : held) / chunk + 3 + kUnitCost;
+  int most = 0x7fffffffll / places < n ? (int)(0x7fffffffll / places) : n;
+  most = most < kPartQueries ? most : kPartQueries;
   static std::atomic<uint32_t> calls{0};
   uint32_t token = ++calls;
   if (token == 0) token = ++calls;   // what the plan sets
-  const Costs costs = costs_of(c, ctas_per_sm(c.dtype, a.head_dim, g > 8));
+  const Costs costs = costs_of(c, fitting_ctas<true>(a, c, n < most ? n : most));   // (of the first: it runs beside the prefixes)
   cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(1024), 0, stream, c, n, seqs, n_groups, cu_group,
                                    common_len, a.window, g, a.n_kv_heads, kN, grid, costs, s, status);
   if (e != cudaSuccess) return e;
@@ -1164,11 +1170,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   else e = bf ? by_dim(B{}, B{}) : by_dim(H{}, H{});
   if (e != cudaSuccess) return e;
 
-  // The sequences' own positions; chunks are counted in 32 bits (see launch_attn_decode; a hole makes one more)
-  const long long chunk = chunk_of(c), held = (long long)c.max_pages * c.page_size;
-  const long long places = (a.window > 0 && a.window < held ? a.window : held) / chunk + 3 + kUnitCost;
-  int most = 0x7fffffffll / places < n ? (int)(0x7fffffffll / places) : n;
-  most = most < kPartQueries ? most : kPartQueries;
+  // The sequences' own positions
   const bool leave = most >= n && shared_join_counts(n, places, (long long)a.n_kv_heads * ((g + kRows - 1) / kRows));
   Cuts cuts = {};
   for (int i = 0; i < n; i += most) {

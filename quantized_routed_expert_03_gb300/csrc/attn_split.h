@@ -4,6 +4,18 @@
 
 namespace qre {
 
+// CTAs of the decode kernel on an SM: as many as its registers leave (`most`), fewer where two stages of the ring and what
+// a CTA keeps of each query do not fit (1 KB of each is the system's, and the kernel's static arrays).  In 4 bits at
+// head_dim 128, of three: beyond 233 queries two (with holes beyond 116), beyond 3476 one.
+inline long long decode_room(int ctas, long long max_smem, long long of_queries) {
+  return (max_smem + 1024) / ctas - 1024 - 256 - of_queries;
+}
+inline int decode_ctas(int most, long long max_smem, long long of_queries, long long two_stages) {
+  int ctas = most;
+  while (ctas > 1 && decode_room(ctas, max_smem, of_queries) < two_stages) --ctas;
+  return ctas;
+}
+
 // Whether the join of shared prefixes (attn_shared.cu), which counts the places of the sequences' own positions in 31
 // bits (64-bit divisions take long there), may join them: n queries with at most `places` each, for each of `units` head
 // blocks.  If not, the decode kernel's own join does, a launch of its own that counts in 64 bits.

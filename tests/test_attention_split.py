@@ -21,6 +21,8 @@ int main(int argc, char** argv) {
   long long r = -1;
   if (!strcmp(argv[1], "join_counts")) r = qre::shared_join_counts(x[0], x[1], x[2]);
   if (!strcmp(argv[1], "join_ways")) r = qre::shared_join_ways(x[0], x[1], x[2], x[3], x[4], x[5], x[6]);
+  if (!strcmp(argv[1], "ctas")) r = qre::decode_ctas(x[0], x[1], x[2], x[3]);
+  if (!strcmp(argv[1], "room")) r = qre::decode_room(x[0], x[1], x[2]);
   printf("%lld", r);
 }
 """
@@ -60,3 +62,15 @@ def test_warps_of_the_shared_join_for_any_number_of_groups(call):
             w = ways(n, heads, kv_heads, groups)
             assert w in (1, 2, 4, 8) and (w == 1 or n * heads * w // 2 <= 8 * 152)
     assert ways(3, 3, 1, 1) == 8 and ways(64, 32, 8, 1) == 1
+
+
+def test_ctas_of_the_decode_kernel_that_fit(call):
+    smem, low, other = 232448, 2 * 4 * 2 * 64 * 72, 2 * 4 * 2 * 4096    # two stages of four warps: 4 bits at 128, any 16 bits
+    assert [call("ctas", 3, smem, 12 * (n + 1), low) for n in (1, 233, 234, 3476, 3477, 4096)] == [3, 3, 2, 2, 1, 1]
+    assert [call("ctas", 3, smem, 24 * (n + 1), low) for n in (1, 116, 117, 1024)] == [3, 3, 2, 2]
+    assert [call("ctas", 2, smem, b * (n + 1), other) for b, n in ((12, 1), (12, 4096), (24, 1024))] == [2, 2, 2]
+    for most in (1, 2, 3):
+        for of_queries in range(0, 50000, 1100):
+            n = call("ctas", most, smem, of_queries, low)
+            assert n == 1 or call("room", n, smem, of_queries) >= low
+            assert n == most or call("room", n + 1, smem, of_queries) < low

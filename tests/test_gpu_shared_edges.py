@@ -9,7 +9,7 @@ import torch
 import quantized_routed_expert_03_gb300 as qre
 from oracle import attention as oatt
 from quantized_routed_expert_03_gb300.attention import Attention, KVCache
-from test_gpu_rows import DEV, UNIT, clean_status, i32, npy, randn   # noqa: F401
+from test_gpu_rows import DEV, TYPE, clean_status, i32, npy, randn   # noqa: F401
 from test_gpu_shared import Shared, check, run
 
 pytestmark = pytest.mark.gpu
@@ -112,3 +112,56 @@ def test_plans_that_change_from_call_to_call_on_one_workspace(cache):
         for (o, lse), (wo, wl) in zip(out, want):
             assert torch.equal(o, wo) and torch.equal(lse, wl)
     assert qre.qre_read_device_status() == 0
+
+
+def attend(c, n, H, q, o, lse, v_max, kind, only):
+    """Queries `only` of a decode of sequences 0 .. n - 1 on an unscaled cache of one layer against fp64."""
+    H, Hk, D = q.shape[1], c.n_kv_heads, c.head_dim
+    lens = c.seq_len.tolist()
+    k, v = (x.double() for x in c.read(0, i32(only), i32(np.cumsum([0] + [lens[s] for s in only])), sum(lens[s] for s in only), dtype=TYPE[kind]))
+    ref = [np.zeros((n, H, D)), np.zeros((n, H)), np.zeros((n, H, D)), np.zeros((n, H))]
+    at = 0
+    for s in only:
+        kk, vv = (x[at:at + lens[s]].cpu().numpy() for x in (k, v))
+        at += lens[s]
+        for h in range(H):
+            j = h // (H // Hk)
+            for dst, x in zip(ref, oatt.attend(npy(q)[s, h:h + 1], kk[:, j], vv[:, j], D ** -0.5, [0], [lens[s]])):
+                dst[s, h] = x[0]
+    check(o, lse, ref, kind, max(lens), v_max, set(only))
+
+
+# both sides of the numbers of queries from which an SM holds a CTA less
+@pytest.mark.parametrize("n,shared", [(232, False), (234, False), (3476, False), (3478, False), (116, True), (118, True), (1026, True)])
+def test_4_bit_calls_of_many_queries(n, shared):
+    H, Hk, D, page, prefix = 16, 2, 128, 16, 512
+    own_pages = 4
+    c = KVCache(1, prefix // page + 40 * own_pages, Hk, page, D, n, prefix // page + own_pages, TYPE["e2m1"], device=DEV)
+    T = c.k.shape[1] * page                                  # rows for every page, one sequence's after the other's
+    fill = KVCache(1, 1, Hk, page, D, 1, c.k.shape[1], TYPE["e2m1"], device=DEV)
+    fill.desc.k, fill.desc.v, fill.desc.n_pages = c.desc.k, c.desc.v, c.desc.n_pages
+    fill.page_table.copy_(torch.arange(c.k.shape[1], device=DEV)[None])
+    k, v = randn((T, Hk, D), 1, "bf16", 1.5), randn((T, Hk, D), 2, "bf16")
+    fill.write(0, torch.zeros(T, dtype=torch.int32, device=DEV), torch.arange(T, dtype=torch.int32, device=DEV), k, v)
+    rows = torch.arange(n, device=DEV)
+    c.page_table[:, :prefix // page] = torch.arange(prefix // page, dtype=torch.int32, device=DEV)
+    c.page_table[:, prefix // page:] = (prefix // page + rows[:, None] % 40 * own_pages + torch.arange(own_pages, device=DEV)).int()
+    c.seq_len[:] = (prefix + 1 + rows * 7 % (own_pages * page)).int()
+    q = randn((n, H, D), 3, "bf16")
+    lse = torch.full((n, H), float("nan"), device=DEV)
+    only = sorted({0, 1, n // 2, n - 2, n - 1})
+    v_max = float(v.abs().max()) * 1.2
+    if shared:
+        cu = i32([0, n // 2, n])
+        common = c.common_len(torch.arange(n, dtype=torch.int32, device=DEV), cu)
+        assert common.tolist() == [prefix, prefix]
+        att = Attention(c, 0, H, n, max_groups=2)
+        o = att.decode_shared(q, None, cu, common, lse=lse)
+        again = att.decode_shared(q, None, cu, common)
+    else:
+        att = Attention(c, 0, H, n)
+        o = att.decode(q, None, lse=lse)
+        again = att.decode(q, None)
+    assert qre.qre_read_device_status() == 0
+    attend(c, n, H, q, o, lse, v_max, "bf16", only)
+    assert torch.equal(o, again) and torch.isfinite(o).all()
