@@ -22,7 +22,7 @@ namespace qre {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 64;    // of a CTA at most
+constexpr int kTokens = 64;    // of a CTA at most; whole warps
 
 template <int RT>
 __global__ void __launch_bounds__(kThreads) kv_write4_kernel(
@@ -134,28 +134,51 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(
   if (blockIdx.x == 0)   // bad bounds are flagged once
     for (int i = threadIdx.x; i < n; i += kThreads)
       if (cu[i] < 0 || cu[i + 1] < cu[i] || cu[i + 1] > total) set_status(status, QRE_DEV_BAD_INDEX);
-  if ((int)threadIdx.x < mine) {
-    const int t = t0 + (int)threadIdx.x;
-    long long at = -2;
-    int pos = 0, lo = 0, hi = n - 1;   // the last sequence that begins at or before the row
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (cu[mid] <= t) lo = mid;
-      else hi = mid - 1;
+  const int t = t0 + (int)threadIdx.x;
+  auto has = [&](int i) {         // sequence i row t (its bounds are asked for together)
+    const int a = cu[i], b = cu[i + 1];
+    return (a >= 0) & (a <= t) & (t < b) & (b <= total);
+  };
+  auto look_up = [&](int i) {
+    const int s = seqs ? seqs[i] : i, from = first ? first[i] : 0;
+    const long long p = (long long)from + (t - cu[i]);
+    long long at = -1;
+    int pos = 0;
+    if (s >= 0 && s < c.max_seqs && from >= 0 && p < c.seq_len[s]) {
+      pos = (int)p;
+      at = kv_page_at(c, layer, s, pos, ps_shift);
     }
-    const int a = cu[lo], b = cu[lo + 1];
-    if (a >= 0 && a <= t && t < b && b <= total) {
-      const int s = seqs ? seqs[lo] : lo, from = first ? first[lo] : 0;
-      const long long p = (long long)from + (t - a);
-      at = -1;
-      if (s >= 0 && s < c.max_seqs && from >= 0 && p < c.seq_len[s]) {
-        pos = (int)p;
-        at = kv_page_at(c, layer, s, pos, ps_shift);
-      }
-      if (at < 0) set_status(status, QRE_DEV_BAD_INDEX);
-    }
+    if (at < 0) set_status(status, QRE_DEV_BAD_INDEX);
     page_of[threadIdx.x] = at;
     pos_of[threadIdx.x] = pos;
+  };
+  if (threadIdx.x < kTokens) {      // whole warps
+    const bool row = (int)threadIdx.x < mine;
+    bool lost = row;
+    if (row) {
+      int lo = 0, hi = n - 1;        // the last sequence that begins at or before the row
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      if (has(lo)) {
+        look_up(lo);
+        lost = false;
+      }
+    }
+    if (__any_sync(0xffffffffu, lost)) {   // nobody's row, or bounds that do not ascend have led the search astray
+      int bad = 0;
+#pragma unroll 8
+      for (int i = threadIdx.x & 31; i < n; i += 32) bad |= (cu[i] < 0) | (cu[i + 1] < cu[i]) | (cu[i + 1] > total);
+      if (__any_sync(0xffffffffu, bad))
+        for (int i = 0; lost && i < n; ++i)
+          if (has(i)) {
+            look_up(i);
+            lost = false;
+          }
+      if (lost) page_of[threadIdx.x] = -2;
+    }
   }
   __syncthreads();
   const int per_head_shift = D == 64 ? 2 : 3, per_row = c.n_kv_heads << per_head_shift, per_token = 2 * per_row;
