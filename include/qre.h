@@ -424,12 +424,13 @@ QRE_API qre_status qre_set_host_unit_cost(int32_t cost);
  * returns, so the context stays usable and the next call is unaffected.
  *   wait_limit_ns  limit of the pipeline waits of later launches (process-wide),
  *                  0 restores the default of one second; at most one second.
- *   stall_ns       when non-zero, later expert-FFN launches delay one warp of
- *                  one CTA (the decode kernels: the CTA that owns the first
- *                  unit of work; the grouped GEMM: CTA 0's token loads) by this
- *                  long before it signals its first pipeline stage (at most
- *                  100 ms), so that a wait with a shorter limit runs out; 0
- *                  turns it off.
+ *   stall_ns       when non-zero, later expert-FFN launches and reads of shared
+ *                  prefixes delay one warp of one CTA (the decode kernels: the
+ *                  CTA that owns the first unit of work; the grouped GEMM:
+ *                  CTA 0's token loads; shared prefixes: CTA 0's page loads)
+ *                  by this long before it signals its first pipeline stage (at
+ *                  most 100 ms), so that a wait with a shorter limit runs out;
+ *                  0 turns it off.
  * Results of calls made while a wait runs out are invalid.  Not for production
  * use; a CUDA graph keeps the values in force when it was captured.
  */

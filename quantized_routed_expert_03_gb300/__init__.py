@@ -356,8 +356,9 @@ def qre_validate_slots(shape, host_slots) -> None:
 
 
 def qre_debug_wait_test(wait_limit_ns: int, stall_ns: int) -> None:
-    """Test hook: lower the kernels' wait limit and delay one warp of the expert
-    FFN's first CTA, so that the give-up path runs (0, 0 restores the defaults)."""
+    """Test hook: lower the kernels' wait limit and delay one warp of the first CTA of
+    the expert FFN and of shared prefixes, so that the give-up path runs (0, 0 restores
+    the defaults)."""
     _check(load_library().qre_debug_wait_test(wait_limit_ns, stall_ns), "qre_debug_wait_test")
 
 

@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
                          const int32_t* __restrict__ seqs, int n_groups, const uint16_t* __restrict__ q,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                          const __grid_constant__ CUtensorMap tk16, const __grid_constant__ CUtensorMap tv16, int box_rows,
-                         const __grid_constant__ Space space, uint32_t token, uint64_t limit_ns, int* status) {
+                         const __grid_constant__ Space space, uint32_t token, uint64_t limit_ns, uint64_t stall_ns, int* status) {
   using P = Shape<DT, CT, D>;
   extern __shared__ __align__(1024) uint8_t tiles_smem[];   // the swizzle goes by addresses; no static shared memory beside it
   uint8_t* sq = tiles_smem;                   // two query tiles
@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
     if (warp == P::kTma) {
       // ---- fetches the tiles: a lane has one run of rows of one page
       begin();
+      if (stall_ns && blockIdx.x == 0) debug_stall_inline(stall_ns);   // test hook
       int i = 0;                       // tiles so far, K and V in turn
       bool ok = true;
       const size_t head_bytes = (size_t)c.page_size * (P::RB + P::SB);
@@ -1155,7 +1156,8 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
     const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), P::BYTES);
     if (err != cudaSuccess) return err;
     return launch_dependent(kernel, dim3(grid), dim3(P::THREADS), (size_t)P::BYTES, stream, a, c, layer, seqs, n_groups,
-                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, token, wait_limit_ns(), status);
+                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, token, wait_limit_ns(),
+                            test_stall_ns(), status);
   };
   using B = std::integral_constant<int, QRE_BF16>;
   using H = std::integral_constant<int, QRE_FP16>;

@@ -132,11 +132,13 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, 
 }
 
 // Test hook (qre_debug_wait_test): spins for ns nanoseconds of the global timer.
-static __device__ __noinline__ void debug_stall(uint64_t ns) {
+// (Inline where a register split leaves no room for a call, as mbar_wait_inline.)
+__device__ __forceinline__ void debug_stall_inline(uint64_t ns) {
   const uint64_t end = global_timer_ns() + ns;
   while (global_timer_ns() < end) {
   }
 }
+static __device__ __noinline__ void debug_stall(uint64_t ns) { debug_stall_inline(ns); }
 
 // ---------------------------------------------------------------- async copies
 

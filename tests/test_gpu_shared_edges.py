@@ -165,3 +165,28 @@ def test_4_bit_calls_of_many_queries(n, shared):
     assert qre.qre_read_device_status() == 0
     attend(c, n, H, q, o, lse, v_max, "bf16", only)
     assert torch.equal(o, again) and torch.isfinite(o).all()
+
+
+# 6 and 240 rows of a KV head: the chains take tiles in turn, or each has rows of its own
+@pytest.mark.parametrize("cache", ["bf16", "fp16", "e4m3", "e2m1"])
+@pytest.mark.parametrize("D,members", [(128, 3), (64, 3), (128, 120)])
+def test_a_wait_that_runs_out_and_the_next_call(cache, D, members):
+    """The first CTA's loads come 20 ms late: the waits for them run out after 2 ms; the loads are issued behind that all the
+    same, and the kernel waits for them, says so and ends.  The calls behind it have the same bits as the one before."""
+    kind = "fp16" if cache == "fp16" else "bf16"
+    w = Shared([9000], [[3, 7, 20] * (members // 3)], 4, 2, D, 64, kind, cache, seed=4)
+    q = randn((members, 4, D), 1, kind)
+    want = run(w, q)
+    assert qre.qre_read_device_status() == 0
+    try:
+        qre.qre_debug_wait_test(2_000_000, 20_000_000)
+        run(w, q)
+        status = qre.qre_read_device_status()
+    finally:
+        qre.qre_debug_wait_test(0, 0)
+    assert status == qre.QRE_DEV_TIMEOUT
+    qre.qre_clear_device_status()
+    for _ in range(3):                                       # (the tensor memory is free again)
+        got = run(w, q)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert qre.qre_read_device_status() == 0
