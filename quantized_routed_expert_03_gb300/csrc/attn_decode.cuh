@@ -226,23 +226,23 @@ struct Own {
   float2* ml;         // [n][n_heads]
   // The launch before this one in the stream (the prefixes) computes the holes' positions; this one needs nothing of it,
   // only of the ones before.  So it begins where SMs are free already, and its first CTA waits for that launch at its end:
-  // then what comes behind this launch comes behind both.  What the ones before wrote (the plan, and by way of the plan all
-  // that is older) it has from the launch of the prefixes: that one waits for the plan, then releases *ready = token, then
-  // lets this one begin.  A thread that acquires the token has seen it all; one that does not waits for the prefixes to end,
-  // as any other kernel would.  The plan sets *ready to 0, and every call has another token, so that an older one is none.
-  // *ctas: how many of its CTAs have work (the SMs that the launch before leaves; NULL: all).
+  // then what comes behind this launch comes behind both.  What the ones before wrote it has from the plan: that one waits
+  // for all that is older, and its last act is to release *start, the call's token above the number of this kernel's CTAs
+  // that have work (the SMs that the prefixes leave).  A thread that acquires the token has seen it all; one that does not
+  // waits for the prefixes to end, as any other kernel would.  The plan sets *start to 0 first, and every call has another
+  // token, so that an older one is none.  (Released by the prefixes, and the number of CTAs read behind it, calls took 2 us
+  // more.)
   int late;
   uint32_t token;
-  const uint32_t* ready;
-  const int* ctas;
+  const unsigned long long* start;   // (read if late)
 };
 
-__device__ __forceinline__ void release_token(uint32_t* p, uint32_t token) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(token) : "memory");
+__device__ __forceinline__ void release_start(unsigned long long* p, uint32_t token, int ctas) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"((unsigned long long)token << 32 | (uint32_t)ctas) : "memory");
 }
-__device__ __forceinline__ uint32_t acquire_token(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ unsigned long long acquire_start(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
 
@@ -378,14 +378,24 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CT, D, NH > 1))
 
   // (late: see Own)
   const bool late = SH && own.late;
-  if (!late || acquire_token(own.ready) != own.token) grid_dependency_wait();
+  int work_ctas = (int)gridDim.x;
+  if (late) {
+    unsigned long long start = acquire_start(own.start);
+    if ((uint32_t)(start >> 32) != own.token) {
+      grid_dependency_wait();
+      start = acquire_start(own.start);
+    }
+    work_ctas = (int)(uint32_t)start;
+  } else {
+    grid_dependency_wait();
+  }
   grid_dependents_launch();
   auto leave = [&]() {
     if (SH && late && blockIdx.x == 0) grid_dependency_wait();
   };
   int grid = (int)gridDim.x;
   if constexpr (SH) {
-    if (own.ctas && ways <= 1) grid = max(1, min(*own.ctas, grid));
+    if (late && ways <= 1) grid = max(1, min(work_ctas, grid));
     if ((int)blockIdx.x >= grid) return;   // never the first, which waits for the launch before
   }
 

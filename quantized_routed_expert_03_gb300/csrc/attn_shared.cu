@@ -65,7 +65,6 @@ struct PlanHead {
   int total;             // places
   int ranges;
   int each, rest;        // total / ranges, total % ranges
-  int own_ctas;          // of the decode kernel: two (or three) on each SM that the ranges leave
   __device__ __forceinline__ int begin(int b) const { return each * b + (int)((unsigned)rest * (unsigned)b / (unsigned)ranges); }
   // the range that place i lies in
   __device__ __forceinline__ int range_of(int i) const {
@@ -85,7 +84,7 @@ struct alignas(16) Query {
 // The workspace.
 struct Space {
   PlanHead* head;
-  uint32_t* ready;       // see Own
+  unsigned long long* start;   // see Own
   int32_t* first;        // [n_groups + 1] places of the groups before
   Group* groups;         // [n_groups]
   int2* hole;            // [n]
@@ -120,7 +119,7 @@ Space space_of(const qre_attn& a, const qre_kv_cache& c, int n, int n_groups, vo
   // pieces of units: rows once or twice, and 256 for each range's end
   const size_t rows = 2 * heads + (size_t)kUnitRows * shared_grid();
   s.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
-  s.ready = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t)));
+  s.start = reinterpret_cast<unsigned long long*>(take(sizeof(unsigned long long)));
   s.first = reinterpret_cast<int32_t*>(take(((size_t)n_groups + 1) * sizeof(int32_t)));
   s.groups = reinterpret_cast<Group*>(take((size_t)n_groups * sizeof(Group)));
   s.hole = reinterpret_cast<int2*>(take((size_t)n * sizeof(int2)));
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
                                                            const int32_t* __restrict__ cu_group,
                                                            const int32_t* __restrict__ common_len, int window, int g,
                                                            int n_kv_heads, int min_positions, int grid, Costs costs,
-                                                           Space s, int* status) {
+                                                           Space s, uint32_t token, int* status) {
   __shared__ long long scan[33];
   __shared__ int scan_m[33];
   __shared__ long long places_of[32];
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (tid == 0) *s.ready = 0;
+  if (tid == 0) *s.start = 0;
   int bad = 0;
   for (int i = tid; i < n_groups; i += 1024) {
     const int a = cu_group[i], b = cu_group[i + 1];
@@ -181,7 +180,8 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
   if (bad) {   // nothing is shared
     if (tid == 0) {
       set_status(status, QRE_DEV_BAD_INDEX);
-      *s.head = PlanHead{0, 0, 0, 0, grid * costs.ctas_sm};
+      *s.head = PlanHead{0, 0, 0, 0};
+      release_start(s.start, token, grid * costs.ctas_sm);
     }
     return;
   }
@@ -278,7 +278,11 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
       s.hole[i] = make_int2(0, 0);
       s.query[i].tiles = 0;
     }
-    if (tid == 0) *s.head = PlanHead{0, 0, 0, 0, grid * costs.ctas_sm};
+    __syncthreads();
+    if (tid == 0) {
+      *s.head = PlanHead{0, 0, 0, 0};
+      release_start(s.start, token, grid * costs.ctas_sm);
+    }
     return;
   }
   if (lane == 0) own_of[warp] = own;
@@ -292,8 +296,8 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const __grid_constant
     int mine = (int)((float)grid * a / (a + b) + 0.5f);
     mine = mine < 1 ? 1 : mine < grid - 1 ? mine : grid - 1;
     const int most = (int)((total + kMinTiles - 1) / kMinTiles), ranges = most < mine ? most : mine;
-    *s.head = PlanHead{(int)total, ranges, ranges ? (int)total / ranges : 0, ranges ? (int)total % ranges : 0,
-                       (grid - ranges) * costs.ctas_sm};
+    *s.head = PlanHead{(int)total, ranges, ranges ? (int)total / ranges : 0, ranges ? (int)total % ranges : 0};
+    release_start(s.start, token, (grid - ranges) * costs.ctas_sm);   // two (or three) on each SM that the ranges leave
   }
 }
 
@@ -316,7 +320,7 @@ struct Shape {
   static constexpr int SOFT_REGS = LOW ? 152 : 208, OTHER_REGS = LOW ? 56 : 88;
   static constexpr int BYTES = 2 * TILE + SLOTS * TILE + STAGES * RAW + 2048;
   // warps 0-7: the two chains' softmax; then
-  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kStart = 11, kWiden = 12, kWidenWarps = 8;
+  static constexpr int kTma = 8, kMma = 9 /* and 10 */, kWiden = 12, kWidenWarps = 8;
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
                          const int32_t* __restrict__ seqs, int n_groups, const uint16_t* __restrict__ q,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                          const __grid_constant__ CUtensorMap tk16, const __grid_constant__ CUtensorMap tv16, int box_rows,
-                         const __grid_constant__ Space space, uint32_t token, uint64_t limit_ns, uint64_t stall_ns, int* status) {
+                         const __grid_constant__ Space space, uint64_t limit_ns, uint64_t stall_ns, int* status) {
   using P = Shape<DT, CT, D>;
   extern __shared__ __align__(1024) uint8_t tiles_smem[];   // the swizzle goes by addresses; no static shared memory beside it
   uint8_t* sq = tiles_smem;                   // two query tiles
@@ -466,6 +470,7 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
   Pieces pieces(space, g, a.n_heads);
   auto begin = [&]() {
     grid_dependency_wait();
+    grid_dependents_launch();
     pieces.begin(n_groups);
   };
   const int ps_shift = 31 - __clz(c.page_size);
@@ -538,12 +543,6 @@ __global__ void __launch_bounds__(Shape<DT, CT, D>::THREADS, 1)
           }
         }
       }
-    } else if (warp == P::kStart) {
-      // ---- lets the next launch begin, and has the plan seen there (see Own): the only warp of a CTA that does
-      grid_dependency_wait();
-      if (blockIdx.x == 0 && lane == 0) release_token(space.ready, token);
-      __syncwarp();
-      grid_dependents_launch();
     } else if (warp == P::kMma || warp == P::kMma + 1) {
       // ---- products: the whole warp, so that the operands stay in uniform registers; a chain each
       // (what an MMA takes comes out of a shuffle from lane 0, so that the compiler knows it is the warp's: as each lane's
@@ -993,7 +992,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   if (f1 > f0) {
     const int blocks = (g + kRows - 1) / kRows, in_kv = h - hk * g, unit = hk * blocks + in_kv / kRows, r = in_kv % kRows;
     const int nch = f1 - f0, u0 = f0 * a.n_kv_heads * blocks + unit * nch;
-    const PlanHead by{(int)cut.total, cut.ranges, (int)cut.total / cut.ranges, (int)cut.total % cut.ranges, 0};
+    const PlanHead by{(int)cut.total, cut.ranges, (int)cut.total / cut.ranges, (int)cut.total % cut.ranges};
     const int b0 = by.range_of(u0 + kUnitCost), b1 = by.range_of(u0 + nch - 1);
     if (b1 > b0) {                   // cut: what lies in own was not written
       const bool wide = g > 8;
@@ -1147,7 +1146,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   if (token == 0) token = ++calls;   // what the plan sets
   const Costs costs = costs_of(c, fitting_ctas<true>(a, c, n < most ? n : most));   // (of the first: it runs beside the prefixes)
   cudaError_t e = launch_dependent(shared_plan_kernel, dim3(1), dim3(1024), 0, stream, c, n, seqs, n_groups, cu_group,
-                                   common_len, a.window, g, a.n_kv_heads, kN, grid, costs, s, status);
+                                   common_len, a.window, g, a.n_kv_heads, kN, grid, costs, s, token, status);
   if (e != cudaSuccess) return e;
   auto prefix = [&](auto dt, auto ct, auto d) -> cudaError_t {
     constexpr int DT = decltype(dt)::value, CT = decltype(ct)::value, D = decltype(d)::value;
@@ -1156,8 +1155,8 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
     const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), P::BYTES);
     if (err != cudaSuccess) return err;
     return launch_dependent(kernel, dim3(grid), dim3(P::THREADS), (size_t)P::BYTES, stream, a, c, layer, seqs, n_groups,
-                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, token, wait_limit_ns(),
-                            test_stall_ns(), status);
+                            static_cast<const uint16_t*>(q), tk, tv, tk16, tv16, box, s, wait_limit_ns(), test_stall_ns(),
+                            status);
   };
   using B = std::integral_constant<int, QRE_BF16>;
   using H = std::integral_constant<int, QRE_FP16>;
@@ -1178,7 +1177,7 @@ cudaError_t launch_attn_decode_shared(const qre_attn& a, const qre_kv_cache& c, 
   for (int i = 0; i < n; i += most) {
     const int m = n - i < most ? n - i : most;
     const Own own{s.hole + i, s.own_o + (size_t)i * a.n_heads * a.head_dim, s.own_ml + (size_t)i * a.n_heads, i == 0,
-                  token, s.ready, i == 0 ? &s.head->own_ctas : nullptr};
+                  token, s.start};
     e = launch_part<true>(a, c, layer, m, seqs ? seqs + i : nullptr, i, max_len, static_cast<const uint16_t*>(q) + i * a.q_token,
                           static_cast<uint16_t*>(o) + i * a.o_token, lse ? lse + (size_t)i * a.n_heads : nullptr, own, s.decode,
                           status, stream, leave ? &cuts : nullptr);

@@ -55,8 +55,8 @@ cudaError_t ensure_smem_limit(const void* kernel, int bytes);
 // excepted: the sequences' own positions of a decode call with shared prefixes
 // (attn_decode.cuh, Own) run beside their direct predecessor, the prefixes, of
 // which they need nothing.  What earlier kernels wrote they have by a token that
-// the predecessor releases between its wait and the start of its dependent, and
-// they wait for the predecessor before they end.
+// the kernel before the predecessor (the plan, which has waited) releases as its
+// last act and they acquire, and they wait for the predecessor before they end.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, size_t smem,
                                      cudaStream_t stream, Args... args) {
