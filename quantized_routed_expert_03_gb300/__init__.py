@@ -103,13 +103,26 @@ class QreError(RuntimeError):
 _STATUS_NAMES = {0: "QRE_OK", 1: "QRE_ERR_INVALID_ARG", 2: "QRE_ERR_UNSUPPORTED", 3: "QRE_ERR_MISALIGNED",
                  4: "QRE_ERR_WORKSPACE", 5: "QRE_ERR_CUDA", 6: "QRE_ERR_TIMEOUT", 7: "QRE_ERR_DEVICE_CHECK"}
 
-_lib = None
+_lib = _by_address = None
 
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _SHAPE = ctypes.POINTER(qre_layer_shape)
-# The descriptors of the cache and attention calls go by address (_at): a call of the smallest sizes is bound by what the
-# binding does, and a typed pointer costs it 0.5 us.
-_KV = _ATTN = _ROWS = _ROPE = ctypes.c_void_p
+
+
+def _descriptor(kind):
+    """Argument type of a pointer to a descriptor: one of its kind (itself, byref, a pointer), its address, or None."""
+    pointer = ctypes.POINTER(kind)
+
+    class Descriptor(ctypes.c_void_p):
+        @classmethod
+        def from_param(cls, x):
+            return ctypes.c_void_p(x) if isinstance(x, int) else pointer.from_param(x)
+    return Descriptor
+
+
+# (The binding's own calls of the cache and attention go by address, _at and _calls: a call of the smallest sizes is bound by
+# what the binding does, and a typed pointer costs it 0.5 us.)
+_KV, _ATTN, _ROWS, _ROPE = (_descriptor(kind) for kind in (qre_kv_cache, qre_attn, qre_kv_rows, qre_rope))
 _SIGS = {
     "qre_last_error": ([], ctypes.c_char_p),
     "qre_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -159,19 +172,28 @@ _SIGS = {
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Loads libqre.so (once) and declares the C signatures."""
-    global _lib
+    global _lib, _by_address
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with "
                            "`python -m quantized_routed_expert_03_gb300.build` (needs nvcc)")
-    lib = ctypes.CDLL(path)
+    lib, by_address = ctypes.CDLL(path), ctypes.CDLL(path)
     for name, (args, res) in _SIGS.items():
-        fn = getattr(lib, name)
-        fn.argtypes = args
-        fn.restype = res
+        for fn, types in ((getattr(lib, name), args),
+                          (getattr(by_address, name), [_VP if a in (_KV, _ATTN, _ROWS, _ROPE) else a for a in args])):
+            fn.argtypes = types
+            fn.restype = res
+    _by_address = by_address
     _lib = lib
     return lib
+
+
+def _calls() -> ctypes.CDLL:
+    """The library as the binding calls it: descriptors are addresses that _at has checked."""
+    if _by_address is None:
+        load_library()
+    return _by_address
 
 
 def _ptr(t):
@@ -203,7 +225,7 @@ def _stream(s):
 
 def _at(desc, kind):
     """Address of a descriptor of the cache and attention calls."""
-    if type(desc) is not kind:
+    if not isinstance(desc, kind):
         raise TypeError(f"expected a {kind.__name__}, not {type(desc).__name__}")
     return ctypes.addressof(desc)
 
@@ -405,52 +427,52 @@ def make_attn(n_heads, n_kv_heads, head_dim, dtype, scale, causal=True, window=0
 
 def qre_kv_workspace_size(cache: qre_kv_cache) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().qre_kv_workspace_size(_at(cache, qre_kv_cache), ctypes.byref(out)), "qre_kv_workspace_size")
+    _check(_calls().qre_kv_workspace_size(_at(cache, qre_kv_cache), ctypes.byref(out)), "qre_kv_workspace_size")
     return out.value
 
 
 def qre_kv_reserve(cache, n, seqs, n_new, workspace, workspace_bytes=None, stream=None) -> None:
-    _check(load_library().qre_kv_reserve(_at(cache, qre_kv_cache), n, _ptr(seqs), _ptr(n_new), _ptr(workspace),
+    _check(_calls().qre_kv_reserve(_at(cache, qre_kv_cache), n, _ptr(seqs), _ptr(n_new), _ptr(workspace),
                                          _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_kv_reserve")
 
 
 def qre_kv_write(cache, layer, rows, n_tokens, token_seq, token_pos, k, v, stream=None) -> None:
-    _check(load_library().qre_kv_write(_at(cache, qre_kv_cache), layer, _at(rows, qre_kv_rows), n_tokens, _ptr(token_seq),
+    _check(_calls().qre_kv_write(_at(cache, qre_kv_cache), layer, _at(rows, qre_kv_rows), n_tokens, _ptr(token_seq),
                                        _ptr(token_pos), _ptr(k), _ptr(v), _stream(stream)), "qre_kv_write")
 
 
 def qre_kv_fork(cache, n, src, dst, workspace, workspace_bytes=None, stream=None) -> None:
-    _check(load_library().qre_kv_fork(_at(cache, qre_kv_cache), n, _ptr(src), _ptr(dst), _ptr(workspace),
+    _check(_calls().qre_kv_fork(_at(cache, qre_kv_cache), n, _ptr(src), _ptr(dst), _ptr(workspace),
                                       _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_kv_fork")
 
 
 def qre_kv_free(cache, n, seqs, stream=None) -> None:
-    _check(load_library().qre_kv_free(_at(cache, qre_kv_cache), n, _ptr(seqs), _stream(stream)), "qre_kv_free")
+    _check(_calls().qre_kv_free(_at(cache, qre_kv_cache), n, _ptr(seqs), _stream(stream)), "qre_kv_free")
 
 
 def qre_kv_compact(cache, page_table_out, ref_count_out, n_live, workspace, workspace_bytes=None,
                    stream=None) -> None:
-    _check(load_library().qre_kv_compact(_at(cache, qre_kv_cache), _ptr(page_table_out), _ptr(ref_count_out),
+    _check(_calls().qre_kv_compact(_at(cache, qre_kv_cache), _ptr(page_table_out), _ptr(ref_count_out),
                                          _ptr(n_live), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                          _stream(stream)), "qre_kv_compact")
 
 
 def qre_attn_prefill(attn, n_seqs, total_q, total_k, cu_q, cu_k, q, k, v, o, lse=None, stream=None) -> None:
-    _check(load_library().qre_attn_prefill(_at(attn, qre_attn), n_seqs, total_q, total_k, _ptr(cu_q), _ptr(cu_k),
+    _check(_calls().qre_attn_prefill(_at(attn, qre_attn), n_seqs, total_q, total_k, _ptr(cu_q), _ptr(cu_k),
                                            _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _stream(stream)),
            "qre_attn_prefill")
 
 
 def qre_attn_decode_workspace_size(attn: qre_attn, cache: qre_kv_cache, n: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().qre_attn_decode_workspace_size(_at(attn, qre_attn), _at(cache, qre_kv_cache), n,
+    _check(_calls().qre_attn_decode_workspace_size(_at(attn, qre_attn), _at(cache, qre_kv_cache), n,
                                                          ctypes.byref(out)), "qre_attn_decode_workspace_size")
     return out.value
 
 
 def qre_attn_decode(attn, cache, layer, n, seqs, max_len, q, o, lse, workspace, workspace_bytes=None,
                     stream=None) -> None:
-    _check(load_library().qre_attn_decode(_at(attn, qre_attn), _at(cache, qre_kv_cache), layer, n, _ptr(seqs), max_len,
+    _check(_calls().qre_attn_decode(_at(attn, qre_attn), _at(cache, qre_kv_cache), layer, n, _ptr(seqs), max_len,
                                           _ptr(q), _ptr(o), _ptr(lse), _ptr(workspace),
                                           _nbytes(workspace, workspace_bytes), _stream(stream)), "qre_attn_decode")
 
@@ -469,30 +491,30 @@ def make_rope(n_heads, n_kv_heads, head_dim, dtype, inv_freq, interleaved=False,
 
 
 def qre_kv_read(cache, layer, rows, n, seqs, first, cu, total, k, v, stream=None) -> None:
-    _check(load_library().qre_kv_read(_at(cache, qre_kv_cache), layer, _at(rows, qre_kv_rows), n, _ptr(seqs), _ptr(first),
+    _check(_calls().qre_kv_read(_at(cache, qre_kv_cache), layer, _at(rows, qre_kv_rows), n, _ptr(seqs), _ptr(first),
                                       _ptr(cu), total, _ptr(k), _ptr(v), _stream(stream)), "qre_kv_read")
 
 
 def qre_qk_norm_rope(rope, n_tokens, token_pos, q, k, q_out, k_out, stream=None) -> None:
-    _check(load_library().qre_qk_norm_rope(_at(rope, qre_rope), n_tokens, _ptr(token_pos), _ptr(q), _ptr(k),
+    _check(_calls().qre_qk_norm_rope(_at(rope, qre_rope), n_tokens, _ptr(token_pos), _ptr(q), _ptr(k),
                                            _ptr(q_out), _ptr(k_out), _stream(stream)), "qre_qk_norm_rope")
 
 
 def qre_kv_write_rope(cache, layer, rope, n_tokens, token_seq, token_pos, q, k, v, q_out, k_out=None,
                       stream=None) -> None:
-    _check(load_library().qre_kv_write_rope(_at(cache, qre_kv_cache), layer, _at(rope, qre_rope), n_tokens, _ptr(token_seq),
+    _check(_calls().qre_kv_write_rope(_at(cache, qre_kv_cache), layer, _at(rope, qre_rope), n_tokens, _ptr(token_seq),
                                             _ptr(token_pos), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out),
                                             _stream(stream)), "qre_kv_write_rope")
 
 
 def qre_kv_common_len(cache, n, seqs, n_groups, cu_group, common_len, stream=None) -> None:
-    _check(load_library().qre_kv_common_len(_at(cache, qre_kv_cache), n, _ptr(seqs), n_groups, _ptr(cu_group),
+    _check(_calls().qre_kv_common_len(_at(cache, qre_kv_cache), n, _ptr(seqs), n_groups, _ptr(cu_group),
                                             _ptr(common_len), _stream(stream)), "qre_kv_common_len")
 
 
 def qre_attn_decode_shared_workspace_size(attn: qre_attn, cache: qre_kv_cache, n: int, n_groups: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().qre_attn_decode_shared_workspace_size(_at(attn, qre_attn), _at(cache, qre_kv_cache), n, n_groups,
+    _check(_calls().qre_attn_decode_shared_workspace_size(_at(attn, qre_attn), _at(cache, qre_kv_cache), n, n_groups,
                                                                 ctypes.byref(out)),
            "qre_attn_decode_shared_workspace_size")
     return out.value
@@ -500,7 +522,7 @@ def qre_attn_decode_shared_workspace_size(attn: qre_attn, cache: qre_kv_cache, n
 
 def qre_attn_decode_shared(attn, cache, layer, n, seqs, n_groups, cu_group, common_len, max_len, q, o, lse, workspace,
                            workspace_bytes=None, stream=None) -> None:
-    _check(load_library().qre_attn_decode_shared(_at(attn, qre_attn), _at(cache, qre_kv_cache), layer, n, _ptr(seqs),
+    _check(_calls().qre_attn_decode_shared(_at(attn, qre_attn), _at(cache, qre_kv_cache), layer, n, _ptr(seqs),
                                                  n_groups, _ptr(cu_group), _ptr(common_len), max_len, _ptr(q), _ptr(o),
                                                  _ptr(lse), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                                  _stream(stream)), "qre_attn_decode_shared")
