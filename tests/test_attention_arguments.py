@@ -2,8 +2,8 @@
 torch, and defaults that follow the cache (no GPU needed: nothing below is launched)."""
 
 import ctypes
-import importlib.util
-import os
+import enum
+import sys
 
 import pytest
 
@@ -44,3 +44,26 @@ def test_the_librarys_own_functions_know_their_descriptors(lib):
                             with pytest.raises(ctypes.ArgumentError):
                                 f(*[way(other) if j == i else y for j, y in enumerate(good)], *rest)
                 assert f(*[None if j == i else y for j, y in enumerate(good)], *rest) == qre.QRE_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(not hasattr(sys, "monitoring"), reason="sys.monitoring is Python 3.12's")
+def test_arguments_that_have_no_address_raise_nothing_on_the_way():
+    """None and plain addresses are common (no log-sums, sequences 0, 1, and so on): an exception for each would take most
+    of a small call's time."""
+    class Address(enum.IntEnum):
+        X = 48
+    raised, mon = [], sys.monitoring
+    mon.use_tool_id(mon.DEBUGGER_ID, "raised")
+    try:
+        mon.register_callback(mon.DEBUGGER_ID, mon.events.RAISE, lambda code, at, e: raised.append(code.co_name))
+        mon.set_events(mon.DEBUGGER_ID, mon.events.RAISE)
+        assert qre._ptr(None) is None and qre._ptr(0) == 0 and qre._ptr(A) == A
+    finally:
+        mon.set_events(mon.DEBUGGER_ID, 0)
+        mon.register_callback(mon.DEBUGGER_ID, mon.events.RAISE, None)
+        mon.free_tool_id(mon.DEBUGGER_ID)
+    assert raised == []
+    assert qre._ptr(Address.X) == 48 and qre._ptr(True) == 1
+    for other in ("x", 1.5, object()):
+        with pytest.raises(AttributeError):
+            qre._ptr(other)
