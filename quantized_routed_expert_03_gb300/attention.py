@@ -28,8 +28,9 @@ from . import (QRE_BF16, QRE_E2M1, QRE_E4M3, QRE_FP16, make_attn, make_kv_cache,
                qre_kv_free, qre_kv_read, qre_kv_reserve, qre_kv_workspace_size, qre_kv_write, qre_kv_write_rope,
                qre_qk_norm_rope)
 
-DTYPES = {torch.bfloat16: QRE_BF16, torch.float16: QRE_FP16, torch.float8_e4m3fn: QRE_E4M3,
-          torch.float4_e2m1fn_x2: QRE_E2M1}
+DTYPES = {torch.bfloat16: QRE_BF16, torch.float16: QRE_FP16, torch.float8_e4m3fn: QRE_E4M3}
+if hasattr(torch, "float4_e2m1fn_x2"):               # (older ones have no name for it, and the other caches without it)
+    DTYPES[torch.float4_e2m1fn_x2] = QRE_E2M1
 
 
 def _check_ids(device, count=None, **tensors):
@@ -79,7 +80,7 @@ class KVCache:
         self.device = torch.device(device)
         i32 = dict(dtype=torch.int32, device=self.device)
         self.n_kv_heads, self.head_dim = n_kv_heads, head_dim
-        low = dtype == torch.float4_e2m1fn_x2
+        low = DTYPES[dtype] == QRE_E2M1
         if low and head_dim % 16:
             raise ValueError(f"head_dim {head_dim} of a 4-bit cache has to be a multiple of 16")
         shape = (n_layers, n_pages, n_kv_heads, page_size, head_dim // 16 * 9 if low else head_dim)

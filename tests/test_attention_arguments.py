@@ -3,6 +3,7 @@ torch, and defaults that follow the cache (no GPU needed: nothing below is launc
 
 import ctypes
 import enum
+import importlib.util
 import sys
 
 import pytest
@@ -67,3 +68,15 @@ def test_arguments_that_have_no_address_raise_nothing_on_the_way():
     for other in ("x", 1.5, object()):
         with pytest.raises(AttributeError):
             qre._ptr(other)
+
+
+def test_a_torch_without_4_bit_types_has_the_other_caches(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    from quantized_routed_expert_03_gb300 import attention
+    monkeypatch.delattr(torch, "float4_e2m1fn_x2", raising=False)
+    spec = importlib.util.spec_from_file_location("quantized_routed_expert_03_gb300.older", attention.__file__)
+    older = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(older)
+    for dtype in (torch.bfloat16, torch.float16, torch.float8_e4m3fn):
+        assert older.KVCache(1, 4, 2, 16, 64, 2, 4, dtype, device="cpu").k.dtype == dtype
+    assert qre.QRE_E2M1 not in older.DTYPES.values()
