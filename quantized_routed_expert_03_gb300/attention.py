@@ -121,9 +121,10 @@ class KVCache:
                           q, k, v, q_out, k_out, stream)
         return q_out, k_out
 
-    def read(self, layer, seqs, cu, total, first=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    def read(self, layer, seqs, cu, total, first=None, dtype=None, k=None, v=None, stream=None):
         """The rows of sequences ``seqs`` (None: 0, 1, and so on) from positions ``first`` (None: 0) on, one sequence
-        behind the other as ``cu`` [sequences + 1] says, ``total`` in all: k, v [total, n_kv_heads, head_dim]."""
+        behind the other as ``cu`` [sequences + 1] says, ``total`` in all: k, v [total, n_kv_heads, head_dim].  dtype None:
+        that of k or v, or the cache's, bfloat16 from an E4M3 or E2M1 cache."""
         device = self.k.device
         _check_ids(device, cu=cu)
         n = cu.numel() - 1
@@ -131,7 +132,11 @@ class KVCache:
             if t is not None:
                 _check_ids(device, n, **{name: t})
         shape = (total, self.n_kv_heads, self.head_dim)
-        dtype = dtype if k is None else k.dtype
+        given = k if k is not None else v
+        if given is not None:
+            dtype = given.dtype
+        elif dtype is None:
+            dtype = self.k.dtype if self.k.dtype in (torch.bfloat16, torch.float16) else torch.bfloat16
         k = _empty(shape, dtype, device, stream) if k is None else k
         v = _empty(shape, dtype, device, stream) if v is None else v
         _check_array(k, "k", shape, dtype, device)

@@ -80,3 +80,19 @@ def test_a_torch_without_4_bit_types_has_the_other_caches(lib, monkeypatch):
     for dtype in (torch.bfloat16, torch.float16, torch.float8_e4m3fn):
         assert older.KVCache(1, 4, 2, 16, 64, 2, 4, dtype, device="cpu").k.dtype == dtype
     assert qre.QRE_E2M1 not in older.DTYPES.values()
+
+
+def test_rows_are_read_in_the_caches_own_type(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    from quantized_routed_expert_03_gb300 import attention
+    seen = []
+    monkeypatch.setattr(attention, "qre_kv_read", lambda cache, layer, rows, *rest: seen.append(rows.dtype))
+    cu = torch.tensor([0, 3], dtype=torch.int32)
+    B, H = torch.bfloat16, torch.float16
+    rows = {t: torch.zeros((3, 2, 64), dtype=t) for t in (B, H)}
+    for kind, kw, want in ((B, {}, B), (H, {}, H), (torch.float8_e4m3fn, {}, B), (torch.float8_e4m3fn, dict(dtype=H), H),
+                           (torch.float8_e4m3fn, dict(k=rows[H]), H), (torch.float8_e4m3fn, dict(v=rows[H]), H),
+                           (H, dict(k=rows[H], v=rows[H]), H)):
+        cache = attention.KVCache(1, 4, 2, 16, 64, 2, 4, kind, device="cpu")
+        k, v = cache.read(0, None, cu, 3, **kw)
+        assert k.dtype == v.dtype == want and seen.pop() == attention.DTYPES[want]
