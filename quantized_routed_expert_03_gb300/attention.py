@@ -146,12 +146,15 @@ class KVCache:
 
     def common_len(self, seqs, cu_group, out=None, stream=None):
         """[groups] int32 on the device: how many leading positions each group's sequences have in common; group i is
-        seqs[cu_group[i]:cu_group[i + 1]]."""
-        _check_ids(self.k.device, seqs=seqs, cu_group=cu_group)
+        seqs[cu_group[i]:cu_group[i + 1]] (seqs None: sequences 0, 1, and so on, up to 4096)."""
+        _check_ids(self.k.device, cu_group=cu_group)
+        if seqs is not None:
+            _check_ids(self.k.device, seqs=seqs)
+        n = seqs.numel() if seqs is not None else min(self.page_table.shape[0], 4096)
         groups = cu_group.numel() - 1
         out = _empty((groups,), torch.int32, self.k.device, stream) if out is None else out
         _check_ids(self.k.device, groups, out=out)
-        qre_kv_common_len(self.desc, seqs.numel(), seqs, groups, cu_group, out, stream)
+        qre_kv_common_len(self.desc, n, seqs, groups, cu_group, out, stream)
         return out
 
     def fork(self, src, dst, stream=None):

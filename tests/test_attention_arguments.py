@@ -96,3 +96,16 @@ def test_rows_are_read_in_the_caches_own_type(lib, monkeypatch):
         cache = attention.KVCache(1, 4, 2, 16, 64, 2, 4, kind, device="cpu")
         k, v = cache.read(0, None, cu, 3, **kw)
         assert k.dtype == v.dtype == want and seen.pop() == attention.DTYPES[want]
+
+
+def test_common_lengths_of_sequences_in_order(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    from quantized_routed_expert_03_gb300 import attention
+    seen = []
+    monkeypatch.setattr(attention, "qre_kv_common_len", lambda cache, n, seqs, groups, *rest: seen.append((n, seqs, groups)))
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32)
+    for held, n in ((7, 7), (4096, 4096), (5000, 4096)):
+        cache = attention.KVCache(1, 4, 2, 16, 64, held, 4, device="cpu")
+        assert cache.common_len(None, cu).shape == (2,) and seen.pop() == (n, None, 2)
+    with pytest.raises(ValueError, match="seqs"):
+        cache.common_len(cu.long(), cu)

@@ -190,3 +190,17 @@ def test_a_wait_that_runs_out_and_the_next_call(cache, D, members):
         got = run(w, q)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert qre.qre_read_device_status() == 0
+
+
+def test_sequences_in_order_need_no_ids():
+    """seqs None: the same common lengths and the same attention as with 0, 1, and so on."""
+    w = Shared([300, 700], [[5, 9, 1], [30, 2]], 4, 2, 64, 16, "bf16", "bf16")
+    assert w.seqs == list(range(5))
+    cu = i32(w.cu)
+    common = w.c.common_len(None, cu)
+    assert common.tolist() == [288, 688] == w.common().tolist()
+    q = randn((5, 4, 64), 1, "bf16")
+    o, lse = run(w, q)
+    att, l2 = Attention(w.c, 1, 4, 5, max_groups=2), torch.empty_like(lse)
+    assert torch.equal(att.decode_shared(q, None, cu, common, lse=l2), o) and torch.equal(l2, lse)
+    assert qre.qre_read_device_status() == 0
