@@ -190,6 +190,8 @@ class Rotary:
                 _check_array(t, name, (n,), torch.float32, t.device, contiguous=True)
 
     def _outputs(self, device, tokens, q, k, q_out, k_out, keep, stream):
+        if device.type != "cuda":
+            raise ValueError(f"heads are normed and turned on a GPU, not on {device}")
         for name, t in (("inv_freq", self.inv_freq), ("q_norm", self.q_norm), ("k_norm", self.k_norm)):
             if t is not None and t.device != device:
                 raise ValueError(f"{name} is on {t.device}, not on {device}")

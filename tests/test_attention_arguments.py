@@ -109,3 +109,21 @@ def test_common_lengths_of_sequences_in_order(lib, monkeypatch):
         assert cache.common_len(None, cu).shape == (2,) and seen.pop() == (n, None, 2)
     with pytest.raises(ValueError, match="seqs"):
         cache.common_len(cu.long(), cu)
+
+
+def test_heads_in_host_memory_are_refused(lib, monkeypatch):
+    """Everything on one device, and that is not a GPU: the kernel would be given host addresses."""
+    torch = pytest.importorskip("torch")
+    from quantized_routed_expert_03_gb300 import attention
+    ran = []
+    for name in ("qre_qk_norm_rope", "qre_kv_write_rope"):
+        monkeypatch.setattr(attention, name, lambda *a: ran.append(a))
+    q, k = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    pos = torch.arange(3, dtype=torch.int32)
+    cache = attention.KVCache(1, 4, 2, 16, 64, 2, 4, device="cpu")
+    for rotary in (attention.Rotary(4, 2, 64, device="cpu"), attention.Rotary(4, 2, 64, rot_dim=0)):
+        with pytest.raises(ValueError, match="GPU"):
+            rotary.apply(q, k, pos)
+        with pytest.raises(ValueError, match="GPU"):
+            cache.write_rope(0, rotary, pos, pos, q, k, k)
+    assert not ran
