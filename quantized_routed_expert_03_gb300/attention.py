@@ -179,6 +179,8 @@ class Rotary:
     def __init__(self, n_heads, n_kv_heads, head_dim, rot_dim=None, theta=10000.0, inv_freq=None, interleaved=False,
                  q_norm=None, k_norm=None, eps=1e-6, dtype=torch.bfloat16, device="cuda"):
         rot_dim = head_dim if rot_dim is None else rot_dim
+        if rot_dim % 2:
+            raise ValueError(f"rot_dim {rot_dim} is odd: elements turn in pairs")
         if inv_freq is None and rot_dim:
             i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
             inv_freq = (theta ** (-i / rot_dim)).float().to(device)

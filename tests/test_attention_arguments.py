@@ -127,3 +127,12 @@ def test_heads_in_host_memory_are_refused(lib, monkeypatch):
         with pytest.raises(ValueError, match="GPU"):
             cache.write_rope(0, rotary, pos, pos, q, k, k)
     assert not ran
+
+
+def test_an_odd_number_of_turned_elements_is_refused(lib):
+    """(With 16 angles of its own, 33 elements were taken for 32.)"""
+    torch = pytest.importorskip("torch")
+    from quantized_routed_expert_03_gb300.attention import Rotary
+    for kw in ({}, dict(inv_freq=torch.ones(16))):
+        with pytest.raises(ValueError, match="rot_dim 33"):
+            Rotary(4, 2, 64, rot_dim=33, device="cpu", **kw)
