@@ -204,3 +204,60 @@ def test_sequences_in_order_need_no_ids():
     att, l2 = Attention(w.c, 1, 4, 5, max_groups=2), torch.empty_like(lse)
     assert torch.equal(att.decode_shared(q, None, cu, common, lse=l2), o) and torch.equal(l2, lse)
     assert qre.qre_read_device_status() == 0
+
+
+@pytest.mark.parametrize("kind,cache,rows", [("bf16", "bf16", 6), ("fp16", "fp16", 6), ("bf16", "bf16", 160), ("bf16", "e4m3", 6),
+                                             ("fp16", "e2m1", 6), ("bf16", "e2m1", 160)])
+def test_a_nan_in_a_shared_prefix(kind, cache, rows):
+    """One in the values of KV head 0 is that dimension of its heads (in 4 bits its block's 16), one in the keys of KV head 1
+    all of its heads; KV head 2, and the other dimensions of the first, do not know."""
+    H, Hk, D, page, n = 6, 3, 64, 16, rows // 2
+    w = Shared([1000], [[1 + i % 7 for i in range(n)]], H, Hk, D, page, kind, cache, seed=5)
+    q = randn((n, H, D), 7, kind, 1.5)
+    ref, v_max = w.reference(q)
+    at, row = int(w.c.page_table[0, 500 // page]), 500 % page
+
+    def poison(pool, head, d):
+        if cache == "e4m3":
+            pool.view(torch.uint8)[1, at, head, row, d] = 0x7f
+        elif cache == "e2m1":
+            pool[1].flatten(-2)[at, head, page * D // 2 + row * (D // 16) + d // 16] = 0x7f
+        else:
+            pool[1, at, head, row, d] = float("nan")
+    poison(w.c.v, 0, 21)
+    poison(w.c.k, 1, 3)
+    o, lse = run(w, q)
+    assert qre.qre_read_device_status() == 0
+    hit = torch.zeros((n, H, D), dtype=torch.bool, device=DEV)
+    hit[:, :2, 16 if cache == "e2m1" else 21:32 if cache == "e2m1" else 22] = True
+    hit[:, 2:4] = True
+    assert torch.equal(torch.isnan(o), hit)
+    assert torch.isnan(lse[:, 2:4]).all() and not torch.isnan(lse[:, :2]).any() and not torch.isnan(lse[:, 4:]).any()
+    mask = hit.cpu().numpy()
+    clean = [x.copy() for x in ref]
+    clean[0][mask], clean[1][:, 2:4] = 0, 0
+    got, gl = torch.where(hit, torch.zeros_like(o), o), lse.clone()
+    gl[:, 2:4] = 0
+    check(got, gl, clean, kind, max(w.lens), v_max)
+
+
+@pytest.mark.parametrize("kind,rows", [("bf16", 6), ("fp16", 6), ("bf16", 160)])
+def test_an_infinite_key_in_a_shared_prefix(kind, rows):
+    """A key that scores -infinity counts nothing; one that scores +infinity leaves no softmax."""
+    H, Hk, D, page, n = 6, 3, 64, 16, rows // 2
+    w = Shared([1000], [[1 + i % 7 for i in range(n)]], H, Hk, D, page, kind, kind, seed=5)
+    q = randn((n, H, D), 7, kind, 1.5)
+    q[..., 9] = -q[..., 9].abs() - 0.125
+    q[1, 4, 9] = 0.5
+    (_, _, ra, rb), v_max = w.reference(q)
+    for pos in (0, 127, 128, 500, 991):
+        w.c.k[1, int(w.c.page_table[0, pos // page]), 2, pos % page, 9] = float("inf")
+    ref, _ = w.reference(q)
+    assert np.isnan(ref[0][1, 4]).all() and np.isnan(ref[0]).sum() == D
+    o, lse = run(w, q)
+    assert qre.qre_read_device_status() == 0
+    assert torch.isnan(o[1, 4]).all() and int(torch.isnan(o).sum()) == D
+    got = torch.nan_to_num(o, nan=0.0)
+    gl, wl = torch.where(torch.isnan(o[..., 0]), torch.zeros_like(lse), lse), np.where(np.isnan(ref[0][..., 0]), 0, ref[1])
+    # (weights that five keys leave grow by less than a part in 100, which the scores' own term covers)
+    check(got, gl, (np.nan_to_num(ref[0]), wl, np.maximum(ra, np.nan_to_num(ref[2])), rb), kind, max(w.lens), v_max)
