@@ -472,8 +472,9 @@ typedef struct {
   int32_t* page_table;  /* [max_seqs][max_pages], device                                */
   int32_t* seq_len;     /* [max_seqs], device                                           */
   int32_t* ref_count;   /* [n_pages], device                                            */
-  const float* k_scale; /* [n_layers][n_kv_heads], device; QRE_E4M3 and QRE_E2M1 only,
-                           NULL = 1; read one by one: 4-byte alignment is enough        */
+  const float* k_scale; /* [n_layers][n_kv_heads], device, positive and finite; QRE_E4M3
+                           and QRE_E2M1 only, NULL = 1; read one by one: 4-byte
+                           alignment is enough                                          */
   const float* v_scale; /* the same                                                     */
   int32_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
   int32_t max_seqs, max_pages;
@@ -573,7 +574,8 @@ QRE_API qre_status qre_kv_read(const qre_kv_cache* cache, int32_t layer, const q
  * token_pos * inv_freq[i]: a' = a cos - b sin, b' = b cos + a sin.  Pair i is the
  * elements i and i + rot_dim / 2, or with interleaved != 0 the elements 2 i and
  * 2 i + 1.  All in fp32 (the angle modulo a whole turn in 64 bits, so that far
- * positions keep theirs), rounded once.
+ * positions keep theirs), rounded once; the sum of a normed row's squares has to
+ * stay in fp32's range.
  * rot_dim is a multiple of 16, at most head_dim; 0: no rotation.
  */
 typedef struct {
@@ -711,8 +713,8 @@ QRE_API qre_status qre_attn_decode_shared_workspace_size(const qre_attn* attn, c
  * common prefix is read together is the library's choice; where max_len says that
  * all sequences are short, nothing is, and the groups are not looked at.  Else a
  * common_len that is negative or beyond a sequence's length counts as 0 for its
- * group, and with bounds that are not ascending from 0 to n each query is computed by
- * itself, both with QRE_DEV_BAD_INDEX.  A common_len that claims more than the
+ * group, and with bounds that are not ascending from 0 to n, or no groups at all, each
+ * query is computed by itself, both with QRE_DEV_BAD_INDEX.  A common_len that claims more than the
  * sequences have in common gives the attention to the first sequence's pages.
  *   max_len  host: an upper bound of the lengths, 0 if not known; a wrong one costs
  *            time and nothing else

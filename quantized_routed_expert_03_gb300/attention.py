@@ -69,8 +69,8 @@ class KVCache:
     """``n_pages`` pages of ``page_size`` positions for all layers, and up to ``max_seqs`` sequences on them.
 
     dtype: bfloat16, float16, float8_e4m3fn, or float4_e2m1fn_x2 for codes of 4 bits with a scale for every 16 elements
-    (``k`` and ``v`` are bytes then).  k_scale, v_scale: [n_layers, n_kv_heads] fp32, for an E4M3 or E2M1 cache only
-    (None: 1).
+    (``k`` and ``v`` are bytes then).  k_scale, v_scale: [n_layers, n_kv_heads] fp32, positive, for an E4M3 or E2M1
+    cache only (None: 1).
     Sequence ids, counts and positions are contiguous int32 tensors on the device that begin at a 16-byte boundary
     (clone a slice that does not); other arguments raise ValueError; nothing here synchronizes.
     """
@@ -270,7 +270,8 @@ class Attention:
         return o
 
     def decode_shared(self, q, seqs, cu_group, common_len, o=None, lse=None, max_len=0, stream=None):
-        """decode for groups of sequences with a common prefix (``KVCache.common_len``): it is read once for a group."""
+        """decode for groups of sequences with a common prefix (``KVCache.common_len``): it is read once for a group.
+        max_len, an upper bound of the lengths, lets calls that are too short to gain by it go without (0: not known)."""
         device = self._check(q, o, lse)
         if seqs is not None:
             _check_ids(device, q.shape[0], seqs=seqs)

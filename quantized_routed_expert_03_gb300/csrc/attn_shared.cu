@@ -19,8 +19,8 @@
 // whole tile, and ends with a common page, behind which the last tile's rows are zeroed.
 //
 // What it measured (calls with the common lengths found in front of them, us): 64 sequences of up to 1500 positions
-// behind 16,384, 32 heads on 8, D = 128, bf16: 72 (each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
-// 51 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 62 (265; the products take 18).  10 us of a launch of the
+// behind 16,384, 32 heads on 8, D = 128, bf16: 73 (E4M3: 64; each by itself 446; the bytes take 39); 8 groups of 8 behind up to 8192:
+// 51 (98; 24); 32 behind 32,768 in 4 bits, 64 heads on 8: 62 (E4M3: 63; 265; the products take 18).  10 us of a launch of the
 // prefixes are its begin (the plan, the queries, the first tile's references) and 3 its end (parts).  Steps, on the
 // first: 119 at first; queries by asynchronous copies, one copy of the softmax's code, 32-bit places and a join that asks
 // for its parts at once 97; the own positions begun beside the prefixes 91; the last join for all parts 84; SMs for the
@@ -316,7 +316,8 @@ struct Shape {
   static constexpr int SLOTS = D == 128 ? (LOW ? 4 : 5) : (LOW ? 8 : 10);
   static constexpr int STAGES = !LOW ? 0 : F8 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 6);
   static constexpr int THREADS = LOW ? 640 : 384;
-  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88; 640 x 96 = 61,440 > 256 x 152 + 384 x 56.
+  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88; 640 x 96 = 61,440 > 256 x 152 + 384 x 56 (the kernels that widen
+  // spill 68 to 72 bytes with these).
   static constexpr int SOFT_REGS = LOW ? 152 : 208, OTHER_REGS = LOW ? 56 : 88;
   static constexpr int BYTES = 2 * TILE + SLOTS * TILE + STAGES * RAW + 2048;
   // warps 0-7: the two chains' softmax; then

@@ -22,7 +22,8 @@
 // copy: 6.8).  One token a CTA and its weights from memory for each row 92; with the queries, keys and values as
 // loops of their own 67 (and small calls 2 us longer); one element an instruction 56; three CTAs an SM 62, five (51
 // registers) 71.  64 tokens 5.5 us, 700 of 28 heads of 64 5.0: a launch and a chain of loads.  CTAs that share a
-// token's rows gain nothing there and cost 7 us on the large call.
+// token's rows gain nothing there and cost 7 us on the large call.  Into E4M3 pages the large call takes 63 us, into 4 bits
+// 70 (three CTAs an SM, 80 registers, 4 to 8 bytes of spills: the scales and codes); 64 tokens 5.2 either way.
 #include <type_traits>
 
 #include "internal.h"
