@@ -54,12 +54,13 @@
 // What it measured in 4 bits: 4 sequences of 131,072 positions, 64 heads on 8, D = 128: 130 us, 4.6 TB/s (128 heads:
 // 163); 256 of up to 2000, window 1500, 28 on 4, D = 64: 30.8 (56 heads: 37.8).  There the conversions' latency bounds it, not
 // the memory: 64 of K and V for 16 keys, as many multiplications by scales, of some 310 instructions; 2.2 instructions a
-// cycle come from 3 warps a scheduler, the ALUs are busy for 50 % of the time.  Steps of the first: 176 as the other types, 2 CTAs per SM and the
-// halves of V's conversions exchanged; 3 CTAs and whole chunks fetched without a look at each row 159; the loader's
-// places kept 154; chunks of 64 keys, the weights spread 134.  4 CTAs (128 registers) need chunks of 32 keys: 149.
-// Registers that do not fit: 4 to 12 bytes of spills at D = 64 with more than 8 heads per KV head, with holes 20 to 28 there
-// and 12 at D = 128.  The third CTA of D = 128 needs room beside its ring
-// for what it keeps of each query: beyond 233 there are two (256 sequences of 2048: 155 us, 230: 133).
+// cycle come from 3 warps a scheduler, the ALUs are busy for 50 % of the time.  Steps of the first: 176 as the other
+// types, 2 CTAs per SM and the halves of V's conversions exchanged; 3 CTAs and whole chunks fetched without a look at
+// each row 159; the loader's places kept 154; chunks of 64 keys, the weights spread 134.  4 CTAs (128 registers) need
+// chunks of 32 keys: 149.
+// Registers that do not fit: 4 to 12 bytes of spills at D = 64 with more than 8 heads per KV head, with holes 20 to 28
+// there and 12 at D = 128.  The third CTA of D = 128 needs room beside its ring for what it keeps of each query: beyond
+// 233 there are two (256 sequences of 2048: 155 us, 230: 133).
 //
 // SH: some positions of a query are somebody else's (attn_shared.cu): its hole.
 // The result of such a query is a part in fp32, not o.
@@ -233,7 +234,7 @@ struct Own {
   // for all that is older, and its last act is to release *start, the call's token above the number of this kernel's CTAs
   // that have work (the SMs that the prefixes leave).  A thread that acquires the token has seen it all; one that does not
   // waits for the prefixes to end, as any other kernel would.  The plan sets *start to 0 first, and every call has another
-  // token, so that an older one is none.  (Released by the prefixes, and the number of CTAs read behind it, calls took 2 us
+  // token (a graph's its own again each time it is replayed, behind that 0), so that an older one is none.  (Released by the prefixes, and the number of CTAs read behind it, calls took 2 us
   // more.)
   int late;
   uint32_t token;
